@@ -76,6 +76,13 @@
  *                   scale: FP8 E4M3 bytes [E, out, in/16] (one per 16 elements);
  *                   scale2: fp32 [E];
  *                   value = e2m1(code) * e4m3(scale[o][i/16]) * scale2[e]
+ *   MOE_W_INT4_G32, MOE_W_INT4_G64, MOE_W_INT4_G128 (groups of G = 32, 64, 128)
+ *                   w: bytes [E, out, in/2], two codes 0..15 per byte, the
+ *                   element with even `in` index in the low nibble;
+ *                   scale: BF16 [E, out, in/G] (one per G elements along in);
+ *                   zero: bytes [E, out, in/G], 0..15, or NULL (every zero
+ *                   point is 8); value = (code - zero[o][i/G]) * scale[o][i/G];
+ *                   every reduction length (H, I and S) is a multiple of G
  *  idx          int32 [N, k], slots in descending selection score
  *  w            fp32  [N, k]
  *  logits       fp32  [N, E]
@@ -109,7 +116,14 @@ typedef enum {
 } moe_status_t;
 
 typedef enum { MOE_ROUTE_SOFTMAX = 0, MOE_ROUTE_SIGMOID_BIAS = 1 } moe_routing_t;
-typedef enum { MOE_W_BF16 = 0, MOE_W_FP8_B128 = 1, MOE_W_NVFP4 = 2 } moe_wfmt_t;
+typedef enum {
+    MOE_W_BF16 = 0,
+    MOE_W_FP8_B128 = 1,
+    MOE_W_NVFP4 = 2,
+    MOE_W_INT4_G32 = 3,
+    MOE_W_INT4_G64 = 4,
+    MOE_W_INT4_G128 = 5
+} moe_wfmt_t;
 /* Expert-stage algorithm.  AUTO: one token runs the single-token kernel,
  * 2-3 tokens the token-major kernels, 4 or more the expert-grouped
  * tensor-core GEMM.  The two explicit values force one (tests); TOKEN_MAJOR
@@ -176,8 +190,11 @@ typedef struct {
 /* One stacked expert matrix (device pointers; see the layouts above). */
 typedef struct {
     const void*  w;
-    const void*  scale;    /* FP8: fp32 block scales; NVFP4: E4M3 bytes; BF16: NULL */
-    const float* scale2;   /* NVFP4 only: fp32 [E]; else NULL */
+    const void*  scale;    /* FP8: fp32 block scales; NVFP4: E4M3 bytes; INT4: BF16; BF16: NULL */
+    union {
+        const float*   scale2;   /* NVFP4: fp32 [E]; BF16, FP8: NULL */
+        const uint8_t* zero;     /* INT4: zero points [E, out, in/G], or NULL (8) */
+    };
 } moe_qmat_t;
 
 /* All weights of one layer (device pointers).  The shared-expert matrices are

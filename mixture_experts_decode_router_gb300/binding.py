@@ -31,6 +31,9 @@ MOE_ROUTE_SIGMOID_BIAS = 1
 MOE_W_BF16 = 0
 MOE_W_FP8_B128 = 1
 MOE_W_NVFP4 = 2
+MOE_W_INT4_G32 = 3
+MOE_W_INT4_G64 = 4
+MOE_W_INT4_G128 = 5
 MOE_PATH_AUTO = 0
 MOE_PATH_TOKEN_MAJOR = 1
 MOE_PATH_GROUPED = 2
@@ -54,8 +57,13 @@ class moe_config_t(ctypes.Structure):
                 ("accumulate", ctypes.c_int32), ("router_fmt", ctypes.c_int32)]
 
 
+class _moe_qmat_second(ctypes.Union):
+    _fields_ = [("scale2", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
+
+
 class moe_qmat_t(ctypes.Structure):
-    _fields_ = [("w", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("scale2", ctypes.c_void_p)]
+    _anonymous_ = ("_second",)
+    _fields_ = [("w", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("_second", _moe_qmat_second)]
 
 
 class moe_weights_t(ctypes.Structure):

@@ -68,8 +68,11 @@ static moe_status_t check_config(const moe_config_t* c) {
     if (!(c->routed_scaling_factor == c->routed_scaling_factor) ||
         c->routed_scaling_factor > 3.0e38f || c->routed_scaling_factor < -3.0e38f)
         return MOE_ERR_INVALID_CONFIG;
-    if (c->expert_fmt != MOE_W_BF16 && c->expert_fmt != MOE_W_FP8_B128 && c->expert_fmt != MOE_W_NVFP4)
-        return MOE_ERR_INVALID_CONFIG;
+    if (c->expert_fmt < MOE_W_BF16 || c->expert_fmt > MOE_W_INT4_G128) return MOE_ERR_INVALID_CONFIG;
+    if (is_int4(c->expert_fmt)) {   // whole groups along every reduction
+        const int g = (1 << int4_gshift(c->expert_fmt)) - 1;
+        if ((c->hidden & g) || (c->inter & g) || (c->shared_inter & g)) return MOE_ERR_INVALID_CONFIG;
+    }
     if (c->path != MOE_PATH_AUTO && c->path != MOE_PATH_TOKEN_MAJOR && c->path != MOE_PATH_GROUPED)
         return MOE_ERR_INVALID_CONFIG;
     // Sizes that keep every index below 2^31.
@@ -101,7 +104,7 @@ static moe_status_t check_qmat(int fmt, const moe_qmat_t& q) {
     if (!q.w) return MOE_ERR_NULL;
     if (!aligned16(q.w)) return MOE_ERR_ALIGNMENT;
     // Scales are read 4 bytes at a time at most.
-    if (fmt == MOE_W_FP8_B128 || fmt == MOE_W_NVFP4) {
+    if (fmt != MOE_W_BF16) {
         if (!q.scale) return MOE_ERR_NULL;
         if (!aligned4(q.scale)) return MOE_ERR_ALIGNMENT;
     }
@@ -162,11 +165,16 @@ template <typename T> static T* at(void* ws, size_t off) {
 }
 
 // e_base: global index of the stack's first expert (0 for the shared expert).
-static QMatDev qdev(const moe_qmat_t& q, int out_dim, int in_dim, int e_base) {
-    QMatDev d;
+static QMatDev qdev(int fmt, const moe_qmat_t& q, int out_dim, int in_dim, int e_base) {
+    QMatDev d{};
     d.w = static_cast<const uint8_t*>(q.w);
     d.scale = q.scale;
-    d.scale2 = q.scale2;
+    if (is_int4(fmt)) {
+        d.zero = q.zero;
+        d.gshift = int4_gshift(fmt);
+    } else {
+        d.scale2 = q.scale2;
+    }
     d.out_dim = out_dim;
     d.in_dim = in_dim;
     d.e_base = e_base;
@@ -234,7 +242,7 @@ static moe_status_t enqueue_route(const moe_config_t* c, const moe_weights_t* w,
         e = cudaSuccess;
         if (c->router_fmt == MOE_W_NVFP4) {
             uint16_t* rq = at<uint16_t>(ws, L.rq);
-            e = launch_router_nvfp4_expand(qdev(w->router_q, c->num_experts, c->hidden, 0), c->num_experts,
+            e = launch_router_nvfp4_expand(qdev(MOE_W_NVFP4, w->router_q, c->num_experts, c->hidden, 0), c->num_experts,
                                            c->hidden, rq, early_dependents(n, sms), sms, st);
             wr = rq;
             rsc = w->router_q.scale2;
@@ -253,7 +261,7 @@ static moe_status_t enqueue_route(const moe_config_t* c, const moe_weights_t* w,
         lsum = logits;
     } else if (c->router_fmt == MOE_W_NVFP4) {
         e = launch_router_nvfp4(static_cast<const uint16_t*>(x), n, c->hidden,
-                                qdev(w->router_q, c->num_experts, c->hidden, 0), c->num_experts, lg, st);
+                                qdev(MOE_W_NVFP4, w->router_q, c->num_experts, c->hidden, 0), c->num_experts, lg, st);
         if (e == cudaSuccess && w->shared_gate_w)   // the BF16 shared-gate row on its own
             e = launch_router(static_cast<const uint16_t*>(x), n, c->hidden, nullptr, 0,
                               static_cast<const uint16_t*>(w->shared_gate_w), nullptr,
@@ -280,6 +288,18 @@ static moe_status_t enqueue_route(const moe_config_t* c, const moe_weights_t* w,
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+
+// Matrix m's second array of the grouped kernels: NVFP4 scale2, INT4 zero points.
+static void set_second(int fmt, TcParams& p, int m, const moe_qmat_t& q, const moe_qmat_t& sh) {
+    if (is_int4(fmt)) {
+        p.zero[m] = q.zero;
+        p.sh_zero[m] = sh.zero;
+        p.gshift = int4_gshift(fmt);
+    } else {
+        p.scale2[m] = q.scale2;
+        p.sh_scale2[m] = sh.scale2;
+    }
+}
 
 // The grouped tensor-core expert stage (after the grouping kernel).
 // x: the layer input; the gather applies the pre-expert RMSNorm, if any.
@@ -323,8 +343,8 @@ static moe_status_t enqueue_grouped(const moe_config_t* c, const moe_weights_t* 
     p.out_dim = I; p.in_dim = H; p.sh_out = S; p.sh_in = H;
     p.scale[0] = w->gate.scale; p.scale[1] = w->up.scale;
     p.sh_scale[0] = w->sh_gate.scale; p.sh_scale[1] = w->sh_up.scale;
-    p.scale2[0] = w->gate.scale2; p.scale2[1] = w->up.scale2;
-    p.sh_scale2[0] = w->sh_gate.scale2; p.sh_scale2[1] = w->sh_up.scale2;
+    set_second(fmt, p, 0, w->gate, w->sh_gate);
+    set_second(fmt, p, 1, w->up, w->sh_up);
     if (tiles && (e = launch_grouped_tc(fmt, true, maps, p, sms, st)) != cudaSuccess) return MOE_ERR_CUDA;
     mk.mark(st);
 
@@ -334,8 +354,8 @@ static moe_status_t enqueue_grouped(const moe_config_t* c, const moe_weights_t* 
     p.out_dim = H; p.in_dim = I; p.sh_out = S > 0 ? H : 0; p.sh_in = S;
     p.scale[0] = p.scale[1] = w->down.scale;
     p.sh_scale[0] = p.sh_scale[1] = w->sh_down.scale;
-    p.scale2[0] = p.scale2[1] = w->down.scale2;
-    p.sh_scale2[0] = p.sh_scale2[1] = w->sh_down.scale2;
+    set_second(fmt, p, 0, w->down, w->sh_down);
+    set_second(fmt, p, 1, w->down, w->sh_down);
     // The FP8 down kernel also runs the combine, after a grid barrier on its
     // persistent blocks (fp8_n64 992 -> 983 us on GB300).  The BF16 and NVFP4
     // down kernels have 192 and 480 threads a block against FP8's 736, too
@@ -406,11 +426,11 @@ static moe_status_t enqueue_experts(const moe_config_t* c, const moe_weights_t* 
     GateUpParams gu{};
     gu.x = static_cast<const uint16_t*>(xin);
     gu.n = n; gu.H = H; gu.I = I; gu.S = S; gu.k = k;
-    gu.gate = qdev(w->gate, I, H, eb);
-    gu.up = qdev(w->up, I, H, eb);
+    gu.gate = qdev(c->expert_fmt, w->gate, I, H, eb);
+    gu.up = qdev(c->expert_fmt, w->up, I, H, eb);
     if (S > 0) {
-        gu.sh_gate = qdev(w->sh_gate, S, H, 0);
-        gu.sh_up = qdev(w->sh_up, S, H, 0);
+        gu.sh_gate = qdev(c->expert_fmt, w->sh_gate, S, H, 0);
+        gu.sh_up = qdev(c->expert_fmt, w->sh_up, S, H, 0);
     }
     gu.counts = at<int32_t>(ws, L.counts);
     gu.offsets = at<int32_t>(ws, L.offsets);
@@ -424,8 +444,8 @@ static moe_status_t enqueue_experts(const moe_config_t* c, const moe_weights_t* 
     dn.n = n; dn.H = H; dn.I = I; dn.S = S; dn.k = k; dn.E = E;
     dn.e_begin = c->expert_begin; dn.e_end = c->expert_end;
     dn.accumulate = c->accumulate;
-    dn.down = qdev(w->down, H, I, eb);
-    if (S > 0) dn.sh_down = qdev(w->sh_down, H, S, 0);
+    dn.down = qdev(c->expert_fmt, w->down, H, I, eb);
+    if (S > 0) dn.sh_down = qdev(c->expert_fmt, w->sh_down, H, S, 0);
     dn.idx = idx;
     dn.w = wt;
     dn.act = gu.act;
@@ -547,13 +567,13 @@ static moe_status_t forward_impl(const moe_config_t* cfg_in, const moe_weights_t
             fp.gw = static_cast<const uint16_t*>(wts->shared_gate_w);
             fp.bias = wts->correction_bias;
             const int eb = cfg->expert_begin;
-            fp.gate = qdev(wts->gate, I, H, eb);
-            fp.up = qdev(wts->up, I, H, eb);
-            fp.down = qdev(wts->down, H, I, eb);
+            fp.gate = qdev(cfg->expert_fmt, wts->gate, I, H, eb);
+            fp.up = qdev(cfg->expert_fmt, wts->up, I, H, eb);
+            fp.down = qdev(cfg->expert_fmt, wts->down, H, I, eb);
             if (S > 0) {
-                fp.sh_gate = qdev(wts->sh_gate, S, H, 0);
-                fp.sh_up = qdev(wts->sh_up, S, H, 0);
-                fp.sh_down = qdev(wts->sh_down, H, S, 0);
+                fp.sh_gate = qdev(cfg->expert_fmt, wts->sh_gate, S, H, 0);
+                fp.sh_up = qdev(cfg->expert_fmt, wts->sh_up, S, H, 0);
+                fp.sh_down = qdev(cfg->expert_fmt, wts->sh_down, H, S, 0);
             }
             fp.logits = at<float>(ws, L.logits);
             fp.sg_logit = at<float>(ws, L.sg_logit);

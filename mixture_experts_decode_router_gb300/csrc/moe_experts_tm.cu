@@ -12,7 +12,7 @@
 //    at least one token chose (read from the device-built expert grouping, so
 //    an expert that two tokens chose is streamed once) or the shared expert.
 //    The warp streams row i of the unit's gate and up matrices once, with
-//    128-bit (BF16), 64-bit (FP8) or 32-bit (NVFP4) coalesced loads that skip
+//    128-bit (BF16), 64-bit (FP8) or 32-bit (NVFP4, INT4) coalesced loads that skip
 //    L1, dequantises in registers, and dots them with every token of the unit:
 //    act[route, i] = SiLU(g) * u in fp32.
 //  * down_blend: one warp per output column h.  For each token it sums, over
@@ -184,7 +184,7 @@ template <int FMT>
 static cudaError_t launch_gate_up_fmt(const GateUpParams& gu, int num_sms, cudaStream_t st) {
     const dim3 grid(2 * num_sms), block(256);
     // Tokens per pass over a weight row: as many as a unit can have, up to 8
-    // (BF16) or 4 (FP8 / NVFP4, whose dequantisation needs more registers).
+    // (BF16) or 4 (FP8 / NVFP4 / INT4, whose dequantisation needs more registers).
     constexpr int kMaxTB = (FMT == MOE_W_BF16) ? 8 : 4;
     const int tb = gu.n >= kMaxTB ? kMaxTB : (gu.n >= 4 ? 4 : (gu.n >= 2 ? 2 : 1));
     if (tb == 1) launch_pdl(gate_up_tm_kernel<FMT, 1>, grid, block, 0, st, gu);
@@ -195,20 +195,22 @@ static cudaError_t launch_gate_up_fmt(const GateUpParams& gu, int num_sms, cudaS
 }
 
 cudaError_t launch_gate_up_tm(int fmt, const GateUpParams& gu, int num_sms, cudaStream_t st) {
-    switch (fmt) {
+    switch (fmt_kind(fmt)) {
         case MOE_W_BF16: return launch_gate_up_fmt<MOE_W_BF16>(gu, num_sms, st);
         case MOE_W_FP8_B128: return launch_gate_up_fmt<MOE_W_FP8_B128>(gu, num_sms, st);
         case MOE_W_NVFP4: return launch_gate_up_fmt<MOE_W_NVFP4>(gu, num_sms, st);
+        case kFmtInt4: return launch_gate_up_fmt<kFmtInt4>(gu, num_sms, st);
         default: return cudaErrorInvalidValue;
     }
 }
 
 cudaError_t launch_down_blend_tm(int fmt, const DownParams& dn, int num_sms, cudaStream_t st) {
     const dim3 grid(2 * num_sms), block(256);
-    switch (fmt) {
+    switch (fmt_kind(fmt)) {
         case MOE_W_BF16: launch_pdl(down_blend_tm_kernel<MOE_W_BF16>, grid, block, 0, st, dn); break;
         case MOE_W_FP8_B128: launch_pdl(down_blend_tm_kernel<MOE_W_FP8_B128>, grid, block, 0, st, dn); break;
         case MOE_W_NVFP4: launch_pdl(down_blend_tm_kernel<MOE_W_NVFP4>, grid, block, 0, st, dn); break;
+        case kFmtInt4: launch_pdl(down_blend_tm_kernel<kFmtInt4>, grid, block, 0, st, dn); break;
         default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();

@@ -45,22 +45,21 @@ constexpr int kFComputeWarps = 15;
 constexpr int kFCompute = kFComputeWarps * 32;
 constexpr int kSeg = 8;   // row chunks per lane loaded before they are used
 
+// Chunk c of row `row` of M's expert e, whose codes are at `codes` in shared memory.
 template <int FMT>
-__device__ __forceinline__ void decode_at(const uint8_t* row, int c, float (&v)[8]) {
+__device__ __forceinline__ void decode_at(const uint8_t* codes, const QMatDev& M, int e, int row, int c,
+                                          float (&v)[8]) {
     WChunk<FMT> ch;
-    if constexpr (FMT == MOE_W_BF16) ch.raw = *reinterpret_cast<const uint4*>(row + c * 16);
-    else if constexpr (FMT == MOE_W_FP8_B128) ch.raw = *reinterpret_cast<const uint2*>(row + c * 8);
-    else ch.raw = *reinterpret_cast<const uint32_t*>(row + c * 4);
+    ch.aux(M, e, row, c);
+    if constexpr (FMT == MOE_W_BF16) ch.raw = *reinterpret_cast<const uint4*>(codes + c * 16);
+    else if constexpr (FMT == MOE_W_FP8_B128) ch.raw = *reinterpret_cast<const uint2*>(codes + c * 8);
+    else ch.raw = *reinterpret_cast<const uint32_t*>(codes + c * 4);
     ch.decode(v);
-}
-
-__device__ __forceinline__ size_t row_bytes_of(int fmt, int in_dim) {
-    return fmt == MOE_W_BF16 ? (size_t)in_dim * 2 : (fmt == MOE_W_FP8_B128 ? (size_t)in_dim : (size_t)in_dim / 2);
 }
 
 template <int FMT>
 __device__ __forceinline__ const uint8_t* row_ptr(const QMatDev& m, int e, int row) {
-    return m.w + ((size_t)(e - m.e_base) * m.out_dim + row) * row_bytes_of(FMT, m.in_dim);
+    return m.w + ((size_t)(e - m.e_base) * m.out_dim + row) * fmt_row_bytes(FMT, m.in_dim);
 }
 
 template <int FMT>
@@ -274,8 +273,8 @@ __global__ void __launch_bounds__(kFThreads, 1) fused_n1_kernel(const FusedParam
                         const int c = c0 + 32 * i;
                         if (c < C) {
                             float wg[8], wu[8], xv[8];
-                            decode_at<FMT>(grow, c, wg);
-                            decode_at<FMT>(urow, c, wu);
+                            decode_at<FMT>(grow, p.sh_gate, 0, row, c, wg);
+                            decode_at<FMT>(urow, p.sh_up, 0, row, c, wu);
                             WChunk<FMT> sch;
                             const float sg = sch.scale(p.sh_gate, 0, row, c), su = sch.scale(p.sh_up, 0, row, c);
                             bf16x8_to_float(reinterpret_cast<const uint4*>(sxe)[c], xv);
@@ -446,7 +445,7 @@ __global__ void __launch_bounds__(kFThreads, 1) fused_n1_kernel(const FusedParam
                     };
                     auto term = [&](int r, int c, const float (&av)[8], float acc) {
                         float wv[8];
-                        decode_at<FMT>(base + (size_t)r * rb, c, wv);
+                        decode_at<FMT>(base + (size_t)r * rb, M, e, h0 + r, c, wv);
                         WChunk<FMT> sch;
                         return fmaf(dot8(wv, av), sch.scale(M, e, h0 + r, c), acc);
                     };
@@ -529,9 +528,7 @@ __global__ void __launch_bounds__(kFThreads, 1) fused_n1_kernel(const FusedParam
 // Shared-memory plan of the fused kernel; returns false if it does not fit.
 bool fused_plan(const moe_config_t* c, int num_sms, FusedParams* p) {
     const int H = c->hidden, E = c->num_experts, k = c->top_k, I = c->inter, S = c->shared_inter;
-    auto rb = [&](int in_dim) -> uint32_t {
-        return c->expert_fmt == MOE_W_BF16 ? in_dim * 2 : (c->expert_fmt == MOE_W_FP8_B128 ? in_dim : in_dim / 2);
-    };
+    auto rb = [&](int in_dim) -> uint32_t { return (uint32_t)fmt_row_bytes(c->expert_fmt, in_dim); };
     p->rpc = (H + num_sms - 1) / num_sms;
     p->row_bytes = rb(H);
     p->drow_bytes = rb(I);
@@ -560,16 +557,18 @@ bool fused_plan(const moe_config_t* c, int num_sms, FusedParams* p) {
 
 cudaError_t launch_fused_n1(int fmt, const FusedParams& p, int num_sms, cudaStream_t st) {
     const void* fn = nullptr;
+    fmt = fmt_kind(fmt);
     switch (fmt) {
         case MOE_W_BF16: fn = reinterpret_cast<const void*>(fused_n1_kernel<MOE_W_BF16>); break;
         case MOE_W_FP8_B128: fn = reinterpret_cast<const void*>(fused_n1_kernel<MOE_W_FP8_B128>); break;
         case MOE_W_NVFP4: fn = reinterpret_cast<const void*>(fused_n1_kernel<MOE_W_NVFP4>); break;
+        case kFmtInt4: fn = reinterpret_cast<const void*>(fused_n1_kernel<kFmtInt4>); break;
         default: return cudaErrorInvalidValue;
     }
     // Per device and format: the largest dynamic shared memory configured so
     // far (set once, re-set only when a larger plan arrives).
     static std::mutex mu;
-    static uint32_t configured[128][3] = {};
+    static uint32_t configured[128][kFmtInt4 + 1] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
     {

@@ -21,9 +21,7 @@ __device__ __forceinline__ uint4 to_tile16(uint4 v) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float lo = __uint_as_float(w4[q] << 16), hi = __uint_as_float(w4[q] & 0xffff0000u);
-            const __half2 h = __floats2half2_rn(fminf(fmaxf(lo, -65504.f), 65504.f),
-                                                fminf(fmaxf(hi, -65504.f), 65504.f));
-            w4[q] = *reinterpret_cast<const uint32_t*>(&h);
+            w4[q] = pack_f16_sat(lo, hi);
         }
         return make_uint4(w4[0], w4[1], w4[2], w4[3]);
     }

@@ -65,7 +65,7 @@ struct TcCfg {
     // kBAtom bytes apart.
     static constexpr int kBAtom = NT * BK * 2;
     static constexpr int kBStage = (kBK / BK) * kBAtom;
-    static constexpr int kRawRow = FMT == MOE_W_FP8_B128 ? kBK : (FMT == MOE_W_NVFP4 ? kBK / 2 : 0);
+    static constexpr int kRawRow = FMT == MOE_W_FP8_B128 ? kBK : (kDeq ? kBK / 2 : 0);
     static constexpr int kRawMat = BM * kRawRow;
     static constexpr int kRawStage = kMats * kRawMat;
     // BF16 tiles: operand stages in shared memory (TMA, 128-byte swizzle).
@@ -92,7 +92,7 @@ struct TcCfg {
     // six (fp8_n64 1129 -> 1113 us against three), both down kernels pairs of
     // their six 128-K stages (FP8 triples: 1065 against 1009 us; NVFP4
     // gate/up pairs were slower, 214 -> 219 us at nvfp4_n256).
-    static constexpr int kGrp = !kDeq ? 1 : ((FMT == MOE_W_NVFP4 && GU) ? 3 : 2);
+    static constexpr int kGrp = !kDeq ? 1 : ((FMT != MOE_W_FP8_B128 && GU) ? 3 : 2);
     static constexpr int kAGroups = kAStages / kGrp;
     // Dequantised tiles: the token (B) tiles have a ring of their own, so they
     // are fetched ahead instead of after the MMA frees an A slot.  It holds
@@ -127,7 +127,8 @@ struct TcCfg {
     static constexpr int kOffB = kOffA + kASmemStages * kAStage;
     static constexpr int kOffRaw = kOffB + kBStages * kBStage;
     // Block scales of each raw stage, fetched by the producer warp with the
-    // raw codes: FP8 one fp32 per matrix; NVFP4 kBK / 16 E4M3 bytes per row per matrix.
+    // raw codes: FP8 one fp32 per matrix; NVFP4 kBK / 16 E4M3 bytes per row per matrix
+    // (INT4: the dequant warps read them from global memory, one or two per row).
     static constexpr int kScaleRow = FMT == MOE_W_NVFP4 ? kBK / 16 : 0;
     static constexpr int kScaleStage = FMT == MOE_W_FP8_B128 ? 16 : (FMT == MOE_W_NVFP4 ? kMats * BM * kScaleRow : 0);
     static constexpr int kOffScale = kOffRaw + kRawStages * kRawStage;
@@ -617,8 +618,7 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                                 const float a = gv / (1.0f + expf(-gv)) * uv;
                                 uint16_t bits;
                                 if constexpr (C::kF16) {
-                                    const __half h = __float2half_rn(fminf(fmaxf(a, -65504.f), 65504.f));
-                                    bits = *reinterpret_cast<const uint16_t*>(&h);
+                                    bits = (uint16_t)pack_f16_sat(a, 0.f);
                                 } else {
                                     const __nv_bfloat16 b = __float2bfloat16_rn(a);
                                     bits = *reinterpret_cast<const uint16_t*>(&b);
@@ -716,6 +716,38 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                                     o[8 * c + 2 * i + 1] = pack_f16(hi.x * s, hi.y * s);
                                 }
                             }
+                        }
+                    } else if constexpr (FMT == kFmtInt4) {
+                        // INT4: 32 codes (one 16-byte chunk) lie in one group.  Nibble q
+                        // becomes the f16 1024 + q (0x6400 | q), less 1024 + zero point is
+                        // exact, and the product with the scale rounds once to f16 (11
+                        // significand bits for weights of 4).
+                        static_assert(PE % 32 == 0, "INT4 dequant parts are whole 32-code chunks");
+    #pragma unroll
+                        for (int b = 0; b < PE / 32; ++b) {
+                            const int kc = k0 + pk0 + 32 * b;
+                            const uint4 v = *reinterpret_cast<const uint4*>(raw + raw_chunk<C::kRawRow>(r, pk0 / 32 + b));
+                            float s = 0.f;            // 0 outside the matrix
+                            uint32_t zp = 8u;
+                            if (mrow < t.out && kc < t.K) {
+                                const size_t gi = ((size_t)t.le * t.out + mrow) * (t.K >> p.gshift) + (kc >> p.gshift);
+                                s = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(
+                                                        sh ? p.sh_scale[pm] : p.scale[pm]) + gi) << 16);
+                                const uint8_t* zt = sh ? p.sh_zero[pm] : p.zero[pm];
+                                if (zt) zp = __ldg(zt + gi);
+                            }
+                            const __half2 zh = __float2half2_rn((float)(1024u + zp)), shh = __float2half2_rn(s);
+                            const uint32_t s2u = *reinterpret_cast<const uint32_t*>(&shh);
+                            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i)
+    #pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint32_t by = w4[i] >> (8 * j);
+                                    const uint32_t qv = ((by & 0xfu) | ((by & 0xf0u) << 12)) | 0x64006400u;
+                                    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&qv), zh);
+                                    o[16 * b + 4 * i + j] = f16x2_mul(*reinterpret_cast<const uint32_t*>(&d), s2u);
+                                }
                         }
                     } else {
                         // NVFP4: 16 codes (8 bytes) per E4M3 block scale.  A part is whole
@@ -836,7 +868,7 @@ bool weight_map(CUtensorMap* m, int fmt, const void* w, int rows_total, int in_d
                                   TcCfg<MOE_W_FP8_B128, true>::kBK, BM, CU_TENSOR_MAP_SWIZZLE_64B)
                        : make_map(m, w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in_dim, rows_total,
                                   TcCfg<MOE_W_FP8_B128, false>::kBK, BM, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (gate_up)
+    if (gate_up)   // NVFP4 and INT4: two codes per byte
         return make_map(m, w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in_dim / 2, rows_total,
                         TcCfg<MOE_W_NVFP4, true>::kBK / 2, BM, CU_TENSOR_MAP_SWIZZLE_32B);
     return make_map(m, w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in_dim / 2, rows_total,
@@ -949,16 +981,18 @@ bool build_tc_maps(int fmt, bool gate_up, const moe_weights_t* w, int E, int H, 
 cudaError_t launch_grouped_tc(int fmt, bool gate_up, const TcMaps& maps, const TcParams& p, int num_sms,
                               cudaStream_t st) {
     if (gate_up) {
-        switch (fmt) {
+        switch (fmt_kind(fmt)) {
             case MOE_W_BF16: return launch_tc<MOE_W_BF16, true>(maps, p, num_sms, st);
             case MOE_W_FP8_B128: return launch_tc<MOE_W_FP8_B128, true>(maps, p, num_sms, st);
             case MOE_W_NVFP4: return launch_tc<MOE_W_NVFP4, true>(maps, p, num_sms, st);
+            case kFmtInt4: return launch_tc<kFmtInt4, true>(maps, p, num_sms, st);
         }
     } else {
-        switch (fmt) {
+        switch (fmt_kind(fmt)) {
             case MOE_W_BF16: return launch_tc<MOE_W_BF16, false>(maps, p, num_sms, st);
             case MOE_W_FP8_B128: return launch_tc<MOE_W_FP8_B128, false>(maps, p, num_sms, st);
             case MOE_W_NVFP4: return launch_tc<MOE_W_NVFP4, false>(maps, p, num_sms, st);
+            case kFmtInt4: return launch_tc<kFmtInt4, false>(maps, p, num_sms, st);
         }
     }
     return cudaErrorInvalidValue;

@@ -129,11 +129,24 @@ inline WsLayout ws_layout(const moe_config_t& c, int64_t n) {
 // ----------------------------------------------------------------------------
 struct QMatDev {
     const uint8_t* w;       // base of the stacked matrix (bytes)
-    const void* scale;      // FP8: float blocks; NVFP4: E4M3 bytes
+    const void* scale;      // FP8: float blocks; NVFP4: E4M3 bytes; INT4: BF16 of each group
     const float* scale2;    // NVFP4 per-expert
+    const uint8_t* zero;    // INT4: each group's zero point, or NULL (8)
     int out_dim, in_dim;
     int e_base;             // global index of the stack's first expert (expert parallelism)
+    int gshift;             // INT4: log2 of the group size
 };
+
+// The INT4 formats share their kernels; the group size is a run-time shift.
+constexpr int kFmtInt4 = MOE_W_INT4_G32;
+__host__ __device__ constexpr bool is_int4(int fmt) { return fmt >= MOE_W_INT4_G32 && fmt <= MOE_W_INT4_G128; }
+__host__ __device__ constexpr int int4_gshift(int fmt) { return 5 + (fmt - MOE_W_INT4_G32); }
+// The kernel instance of a format.
+constexpr int fmt_kind(int fmt) { return is_int4(fmt) ? kFmtInt4 : fmt; }
+// Bytes of one row of `in` codes.
+__host__ __device__ constexpr size_t fmt_row_bytes(int fmt, int in) {
+    return fmt == MOE_W_BF16 ? (size_t)in * 2 : (fmt == MOE_W_FP8_B128 ? (size_t)in : (size_t)in / 2);
+}
 
 // ----------------------------------------------------------------------------
 // Programmatic dependent launch.  Every kernel of a multi-kernel sequence is
@@ -217,6 +230,14 @@ __device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t byte) {
     return __half22float2(__half2(raw));
 }
 
+// Two floats as f16x2 (lo in the low half), rounded to nearest and saturated at
+// +-65504; NaN stays NaN.
+__device__ __forceinline__ uint32_t pack_f16_sat(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // One E4M3 code -> float (exact).
 __device__ __forceinline__ float e4m3_to_float(uint32_t code) {
     return e4m3x2_to_float2(code & 0xffu).x;
@@ -226,7 +247,8 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t code) {
 // Weight chunks: 8 consecutive elements of one row (along `in`), decoded to
 // fp32, plus the multiplier that applies to the whole chunk.  Every format's
 // chunk lies inside one scale block (FP8: 128 columns; NVFP4: 16 columns),
-// because chunks start at multiples of 8.
+// because chunks start at multiples of 8.  aux() reads what decode() needs
+// beside the codes (INT4: the group's zero point); load() includes it.
 // ----------------------------------------------------------------------------
 template <int FMT> struct WChunk;
 
@@ -237,6 +259,7 @@ template <> struct WChunk<MOE_W_BF16> {
                                ((size_t)(e - m.e_base) * m.out_dim + row) * m.in_dim + (size_t)c * 8;
         raw = ld_stream_v4(base);
     }
+    __device__ __forceinline__ void aux(const QMatDev&, int, int, int) {}
     __device__ __forceinline__ float scale(const QMatDev&, int, int, int) const { return 1.0f; }
     __device__ __forceinline__ void decode(float (&v)[8]) const {
         v[0] = bf16_lo(raw.x); v[1] = bf16_hi(raw.x); v[2] = bf16_lo(raw.y); v[3] = bf16_hi(raw.y);
@@ -250,6 +273,7 @@ template <> struct WChunk<MOE_W_FP8_B128> {
         const uint8_t* base = m.w + ((size_t)(e - m.e_base) * m.out_dim + row) * m.in_dim + (size_t)c * 8;
         raw = ld_stream_v2(base);
     }
+    __device__ __forceinline__ void aux(const QMatDev&, int, int, int) {}
     __device__ __forceinline__ float scale(const QMatDev& m, int e, int row, int c) const {
         const int ob = (m.out_dim + 127) >> 7, ib = (m.in_dim + 127) >> 7;
         const float* s = reinterpret_cast<const float*>(m.scale) + (size_t)(e - m.e_base) * ob * ib;
@@ -268,6 +292,7 @@ template <> struct WChunk<MOE_W_NVFP4> {
         const uint8_t* base = m.w + ((size_t)(e - m.e_base) * m.out_dim + row) * (m.in_dim / 2) + (size_t)c * 4;
         raw = ld_stream_u32(base);
     }
+    __device__ __forceinline__ void aux(const QMatDev&, int, int, int) {}
     __device__ __forceinline__ float scale(const QMatDev& m, int e, int row, int c) const {
         const uint8_t* s = reinterpret_cast<const uint8_t*>(m.scale) +
                            ((size_t)(e - m.e_base) * m.out_dim + row) * (m.in_dim / 16);
@@ -277,6 +302,31 @@ template <> struct WChunk<MOE_W_NVFP4> {
         float2 a = e2m1x2_to_float2(raw & 0xffu), b = e2m1x2_to_float2((raw >> 8) & 0xffu);
         float2 c2 = e2m1x2_to_float2((raw >> 16) & 0xffu), d = e2m1x2_to_float2(raw >> 24);
         v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y; v[4] = c2.x; v[5] = c2.y; v[6] = d.x; v[7] = d.y;
+    }
+};
+
+// INT4: value = (code - zero point of the group) * scale of the group; decode()
+// gives the exact integer differences.
+template <> struct WChunk<kFmtInt4> {
+    uint32_t raw;
+    int zp;
+    __device__ __forceinline__ size_t group(const QMatDev& m, int e, int row, int c) const {
+        return ((size_t)(e - m.e_base) * m.out_dim + row) * (m.in_dim >> m.gshift) + ((c * 8) >> m.gshift);
+    }
+    __device__ __forceinline__ void aux(const QMatDev& m, int e, int row, int c) {
+        zp = m.zero ? (int)__ldg(m.zero + group(m, e, row, c)) : 8;
+    }
+    __device__ __forceinline__ void load(const QMatDev& m, int e, int row, int c) {
+        raw = ld_stream_u32(m.w + ((size_t)(e - m.e_base) * m.out_dim + row) * (m.in_dim / 2) + (size_t)c * 4);
+        aux(m, e, row, c);
+    }
+    __device__ __forceinline__ float scale(const QMatDev& m, int e, int row, int c) const {
+        const uint32_t b = __ldg(reinterpret_cast<const unsigned short*>(m.scale) + group(m, e, row, c));
+        return __uint_as_float(b << 16);
+    }
+    __device__ __forceinline__ void decode(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)((int)((raw >> (4 * i)) & 15u) - zp);
     }
 };
 

@@ -53,6 +53,9 @@ struct TcParams {
     const void* sh_scale[2];
     const float* scale2[2];  // NVFP4 per-expert fp32
     const float* sh_scale2[2];
+    const uint8_t* zero[2];     // INT4 zero points, or NULL
+    const uint8_t* sh_zero[2];
+    int gshift;                 // INT4: log2 of the group size
     void* act_out;           // gate_up: sorted SiLU(g)*u rows [n*k, I] (bf16 / f16)
     void* act_sh_out;        // gate_up: shared [n, S]
     float* y;                // down: weighted rows [n*k, H]

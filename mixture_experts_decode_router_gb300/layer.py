@@ -10,10 +10,11 @@ from typing import Optional
 import torch
 
 from . import binding as B
-from .synth import (FMT_BF16, FMT_FP8_B128, FMT_NVFP4, ROUTE_SIGMOID_BIAS, LayerConfig,
-                    LayerWeights, QMatT)
+from .synth import (FMT_BF16, FMT_FP8_B128, FMT_INT4_G128, FMT_INT4_G32, FMT_INT4_G64, FMT_NVFP4,
+                    ROUTE_SIGMOID_BIAS, LayerConfig, LayerWeights, QMatT)
 
-_FMT = {FMT_BF16: B.MOE_W_BF16, FMT_FP8_B128: B.MOE_W_FP8_B128, FMT_NVFP4: B.MOE_W_NVFP4}
+_FMT = {FMT_BF16: B.MOE_W_BF16, FMT_FP8_B128: B.MOE_W_FP8_B128, FMT_NVFP4: B.MOE_W_NVFP4,
+        FMT_INT4_G32: B.MOE_W_INT4_G32, FMT_INT4_G64: B.MOE_W_INT4_G64, FMT_INT4_G128: B.MOE_W_INT4_G128}
 _PATH = {"auto": B.MOE_PATH_AUTO, "token_major": B.MOE_PATH_TOKEN_MAJOR,
          "grouped": B.MOE_PATH_GROUPED}
 
@@ -46,7 +47,10 @@ def _qmat(q: Optional[QMatT]) -> B.moe_qmat_t:
         return m
     m.w = q.w.data_ptr()
     m.scale = q.scale.data_ptr() if q.scale is not None else None
-    m.scale2 = q.scale2.data_ptr() if q.scale2 is not None else None
+    if q.scale2 is not None:
+        m.scale2 = q.scale2.data_ptr()
+    elif q.zero is not None:
+        m.zero = q.zero.data_ptr()
     return m
 
 

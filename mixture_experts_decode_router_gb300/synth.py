@@ -18,6 +18,11 @@ Recipe (one layer):
         q = E2M1(w / (s16 * scale2)) rounded to the nearest magnitude of
         {0, .5, 1, 1.5, 2, 3, 4, 6} (saturating), 0 where s16 is 0; two codes
         per byte, the even element in the low nibble
+      - INT4 in groups of G along ``in`` (G = 32, 64, 128): without zero points
+        s = BF16(amax / 7) (1 when zero), q = clamp(rne(w / s), -8, 7) + 8; with
+        ``zero_points`` s = BF16((max - min) / 15), z = clamp(rne(-min / s), 0, 15),
+        q = clamp(rne(w / s) + z, 0, 15) (min <= 0 <= max); two codes per byte, the
+        even element in the low nibble
   * correction bias ~ U(-r, r) fp32 [E] (sigmoid routing only)
   * input rows ~ N(0, 1) -> BF16.  An optional ``gap_fn`` (supplied by the
     caller) returns, per row, the margin between the k-th and (k+1)-th
@@ -45,6 +50,10 @@ ROUTE_SIGMOID_BIAS = "sigmoid_bias"
 FMT_BF16 = "bf16"
 FMT_FP8_B128 = "fp8_b128"
 FMT_NVFP4 = "nvfp4"
+FMT_INT4_G32 = "int4_g32"
+FMT_INT4_G64 = "int4_g64"
+FMT_INT4_G128 = "int4_g128"
+INT4_GROUP = {FMT_INT4_G32: 32, FMT_INT4_G64: 64, FMT_INT4_G128: 128}
 
 _TID = {"router": 1, "gate": 2, "up": 3, "down": 4, "sh_gate": 5, "sh_up": 6,
         "sh_down": 7, "bias": 8, "shared_gate_w": 9, "x": 10, "dup": 11, "norm": 12}
@@ -72,6 +81,7 @@ class LayerConfig:
     router_fmt: str = FMT_BF16         # BF16 router, or NVFP4 (quantised from the same matrix)
     rms_norm_eps: float = 1e-6
     seed: int = 0
+    zero_points: bool = False          # INT4 experts: a zero point per group (else 8)
 
     def with_(self, **kw) -> "LayerConfig":
         return replace(self, **kw)
@@ -146,13 +156,32 @@ def _quant_nvfp4(w: torch.Tensor):
     return packed.contiguous(), s16.view(torch.uint8).contiguous(), float(scale2)
 
 
+def quant_int4(w: torch.Tensor, group: int, zero_points: bool = False):
+    """[out, in] fp32 -> (packed uint8 [out, in/2], BF16 scales [out, in/group],
+    uint8 zero points [out, in/group] or None)."""
+    out_d, in_d = w.shape
+    g = w.view(out_d, in_d // group, group)
+    if zero_points:
+        lo, hi = g.amin(dim=2).clamp(max=0.0), g.amax(dim=2).clamp(min=0.0)
+        s = ((hi - lo) / 15.0).to(torch.bfloat16)
+    else:
+        s = (g.abs().amax(dim=2) / 7.0).to(torch.bfloat16)
+    s = torch.where(s > 0, s, torch.ones_like(s))
+    sf = s.to(torch.float32)
+    z = torch.round(-lo / sf).clamp(0, 15) if zero_points else torch.full_like(sf, 8.0)
+    q = (torch.round(g / sf[..., None]) + z[..., None]).clamp(0, 15).to(torch.uint8).view(out_d, in_d)
+    packed = (q[:, 0::2] | (q[:, 1::2] << 4)).contiguous()
+    return packed, s.contiguous(), (z.to(torch.uint8).contiguous() if zero_points else None)
+
+
 @dataclass
 class QMatT:
     """Stacked expert matrix on a device, in the library's layout."""
     fmt: str
     w: torch.Tensor
     scale: Optional[torch.Tensor] = None
-    scale2: Optional[torch.Tensor] = None
+    scale2: Optional[torch.Tensor] = None     # NVFP4
+    zero: Optional[torch.Tensor] = None       # INT4 zero points (None = 8)
 
 
 def matrix_dims(cfg: LayerConfig, tensor: str):
@@ -163,8 +192,8 @@ def matrix_dims(cfg: LayerConfig, tensor: str):
 
 
 def expert_matrix(cfg: LayerConfig, tensor: str, e: int, device="cpu"):
-    """The stored form of expert e's `tensor` matrix alone: (w, scale, scale2)
-    -- identical to slice e of the stacked tensor make_weights builds."""
+    """The stored form of expert e's `tensor` matrix alone: (w, scale, scale2;
+    INT4: the zero points in the place of scale2) -- identical to slice e of the stacked tensor make_weights builds."""
     out_d, in_d = matrix_dims(cfg, tensor)
     m = torch.randn(out_d, in_d, generator=_gen(device, cfg.seed, tensor, e), device=device,
                     dtype=torch.float32) * cfg.weight_std
@@ -173,6 +202,8 @@ def expert_matrix(cfg: LayerConfig, tensor: str, e: int, device="cpu"):
     if cfg.expert_fmt == FMT_FP8_B128:
         q, s = _quant_fp8_b128(m)
         return q, s, None
+    if cfg.expert_fmt in INT4_GROUP:
+        return quant_int4(m, INT4_GROUP[cfg.expert_fmt], cfg.zero_points)
     q, s, s2 = _quant_nvfp4(m)
     return q, s, s2
 
@@ -190,6 +221,10 @@ def _stacked(cfg: LayerConfig, tensor: str, n_exp: int, out_d: int, in_d: int,
         w = torch.empty(n_exp, out_d, in_d // 2, dtype=torch.uint8, device=device)
         sc = torch.empty(n_exp, out_d, in_d // 16, dtype=torch.uint8, device=device)
         s2 = torch.empty(n_exp, dtype=torch.float32, device=device)
+    elif fmt in INT4_GROUP:
+        w = torch.empty(n_exp, out_d, in_d // 2, dtype=torch.uint8, device=device)
+        sc = torch.empty(n_exp, out_d, in_d // INT4_GROUP[fmt], dtype=torch.bfloat16, device=device)
+        zp = torch.empty(sc.shape, dtype=torch.uint8, device=device) if cfg.zero_points else None
     else:
         raise ValueError(fmt)
     for e in range(n_exp):
@@ -199,10 +234,14 @@ def _stacked(cfg: LayerConfig, tensor: str, n_exp: int, out_d: int, in_d: int,
             sc[e] = s
         if fmt == FMT_NVFP4:
             s2[e] = s2v
+        elif s2v is not None:
+            zp[e] = s2v
     if fmt == FMT_BF16:
         return QMatT(fmt, w)
     if fmt == FMT_FP8_B128:
         return QMatT(fmt, w, sc)
+    if fmt in INT4_GROUP:
+        return QMatT(fmt, w, sc, zero=zp)
     return QMatT(fmt, w, sc, s2)
 
 
@@ -289,7 +328,8 @@ def expert_slice(lw: LayerWeights, begin: int, end: int) -> LayerWeights:
     def part(q: QMatT) -> QMatT:
         return QMatT(q.fmt, q.w[begin:end],
                      q.scale[begin:end] if q.scale is not None else None,
-                     q.scale2[begin:end] if q.scale2 is not None else None)
+                     q.scale2[begin:end] if q.scale2 is not None else None,
+                     q.zero[begin:end] if q.zero is not None else None)
     return replace(lw, gate=part(lw.gate), up=part(lw.up), down=part(lw.down))
 
 
@@ -342,23 +382,26 @@ def make_input(cfg: LayerConfig, n: Optional[int] = None, device="cpu",
     return x
 
 
-def matrix_bytes(fmt: str, out_d: int, in_d: int) -> int:
-    """Bytes of one [out, in] matrix, scales included."""
+def matrix_bytes(fmt: str, out_d: int, in_d: int, zero_points: bool = False) -> int:
+    """Bytes of one [out, in] matrix, scales (and INT4 zero points) included."""
     if fmt == FMT_BF16:
         return out_d * in_d * 2
     if fmt == FMT_FP8_B128:
         return out_d * in_d + 4 * (-(-out_d // 128)) * (-(-in_d // 128))
     if fmt == FMT_NVFP4:
         return out_d * in_d // 2 + out_d * in_d // 16 + 4
+    if fmt in INT4_GROUP:
+        return out_d * in_d // 2 + (3 if zero_points else 2) * (out_d * in_d // INT4_GROUP[fmt])
     raise ValueError(fmt)
 
 
 def layer_bytes(cfg: LayerConfig) -> dict:
     """Byte counts of the parts of one layer, for the touched-bytes metric."""
     H, I, S, E = cfg.hidden, cfg.inter, cfg.shared_inter, cfg.num_experts
-    per_expert = 2 * matrix_bytes(cfg.expert_fmt, I, H) + matrix_bytes(cfg.expert_fmt, H, I)
-    shared = (2 * matrix_bytes(cfg.expert_fmt, S, H) + matrix_bytes(cfg.expert_fmt, H, S)
-              if S > 0 else 0)
+    def mat(out_d, in_d):
+        return matrix_bytes(cfg.expert_fmt, out_d, in_d, cfg.zero_points)
+    per_expert = 2 * mat(I, H) + mat(H, I)
+    shared = 2 * mat(S, H) + mat(H, S) if S > 0 else 0
     extra = ((4 * E if cfg.routing == ROUTE_SIGMOID_BIAS else 0) + (2 * H if cfg.shared_gate else 0)
              + (2 * H if cfg.pre_expert_norm else 0))
     router = E * H * 2 if cfg.router_fmt == FMT_BF16 else matrix_bytes(cfg.router_fmt, E, H)

@@ -37,6 +37,9 @@ Weight formats (decoded exactly, from the format definitions):
   magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6), two per byte with the even element in
   the low nibble, one E4M3 scale per 16 consecutive elements along ``in``, and
   one fp32 ``scale2`` per (expert, matrix): ``w = e2m1(q) * e4m3(s16) * scale2``.
+* INT4 in groups of G = 32, 64 or 128 along ``in``: codes 0..15, two per byte with
+  the even element in the low nibble, one BF16 scale and (optionally) one zero
+  point per group: ``w = (q - z) * s``, z = 8 without zero points.
 
 Expert matrices are decoded one expert at a time, so the largest layer (256
 experts of 3 x 7168 x 2048 FP8 weights) never has to exist in float64 at once.
@@ -59,6 +62,7 @@ ROUTE_SIGMOID_BIAS = "sigmoid_bias"
 FMT_BF16 = "bf16"
 FMT_FP8_B128 = "fp8_b128"
 FMT_NVFP4 = "nvfp4"
+INT4_GROUP = {"int4_g32": 32, "int4_g64": 64, "int4_g128": 128}
 
 FP8_BLOCK = 128      # FP8 scale tile edge (rows and columns of [out, in])
 NVFP4_BLOCK = 16     # NVFP4 elements per E4M3 scale, along `in`
@@ -132,6 +136,20 @@ def dequant_nvfp4(packed: np.ndarray, s16: np.ndarray, scale2: float) -> np.ndar
     return vals * blk * float(scale2)
 
 
+def dequant_int4(packed: np.ndarray, scale_bits: np.ndarray, zero: Optional[np.ndarray],
+                 group: int) -> np.ndarray:
+    """w[o, i] = (nibble(o, i) - z[o, i // G]) * bf16(s[o, i // G]), the element
+    with even ``i`` in the low nibble of byte ``i // 2``; z = 8 when zero is None."""
+    p = np.asarray(packed, dtype=np.uint8)
+    out_dim, half = p.shape
+    codes = np.empty((out_dim, 2 * half), dtype=np.float64)
+    codes[:, 0::2] = p & 0x0F
+    codes[:, 1::2] = p >> 4
+    of = np.arange(2 * half) // group
+    z = 8.0 if zero is None else np.asarray(zero, dtype=np.float64)[:, of]
+    return (codes - z) * bf16_decode(scale_bits)[:, of]
+
+
 # --------------------------------------------------------------------------
 # Layer description (host copies of what the C-ABI receives)
 # --------------------------------------------------------------------------
@@ -144,11 +162,14 @@ class QMat:
     fp8_b128: w uint8 [E, out, in], scale float32 [E, ceil(out/128), ceil(in/128)]
     nvfp4:    w uint8 [E, out, in/2], scale uint8 (E4M3) [E, out, in/16],
               scale2 float32 [E]
+    int4_gG:  w uint8 [E, out, in/2], scale uint16 (BF16) [E, out, in/G],
+              zero uint8 [E, out, in/G] or None
     """
     fmt: str
     w: np.ndarray
     scale: Optional[np.ndarray] = None
     scale2: Optional[np.ndarray] = None
+    zero: Optional[np.ndarray] = None
 
     def expert(self, e: int) -> np.ndarray:
         """Decoded float64 [out, in] of expert e."""
@@ -158,6 +179,9 @@ class QMat:
             return dequant_fp8_b128(self.w[e], self.scale[e])
         if self.fmt == FMT_NVFP4:
             return dequant_nvfp4(self.w[e], self.scale[e], float(self.scale2[e]))
+        if self.fmt in INT4_GROUP:
+            return dequant_int4(self.w[e], self.scale[e], None if self.zero is None else self.zero[e],
+                                INT4_GROUP[self.fmt])
         raise ValueError(f"unknown format {self.fmt}")
 
 

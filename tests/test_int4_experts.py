@@ -1,0 +1,319 @@
+"""INT4 experts with group scales: the format (CPU), refusals (CPU), and the layer on every
+path against the fp64 oracle (GPU).
+
+Output tolerance, per element: 2^-8 |ref| for the BF16 output, and 5e-3 RMS(ref) for the f16
+values inside.  At most four roundings to f16 (gate, up and down weights, and SiLU(g) u), each
+at most 2^-11 relative, enter sums of independently signed terms, so each moves an output by a
+standard deviation of at most 2^-11 / sqrt(3) of its RMS, gate and up through a SwiGLU whose
+slope stays below 1.3: sqrt(4) * 1.3 * 2^-11 / sqrt(3) = 7.4e-4, times six.
+
+With a pre-expert norm the experts' input is itself rounded to BF16, as the layer defines it and the
+oracle does not: at most 2^-8 relative for each element, which moves g and u by at most
+2^-8 / sqrt(3) of their RMS and an output by sqrt(1.3^2 + 1) times that, 3.7e-3, times six
+(2.2e-2)."""
+
+import ctypes
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_decode_router_gb300 import binding as B
+from mixture_experts_decode_router_gb300 import synth
+from mixture_experts_decode_router_gb300.layer import MoeLayer, make_config
+from oracle import moe_oracle as O
+from tests.int4_helpers import int4_oracle_layer
+from tests.moe_helpers import bf16_bits, gap_fn_for
+
+FORMATS = sorted(synth.INT4_GROUP)
+
+
+def cfg_of(fmt="int4_g32", **kw):
+    d = dict(name="int4", hidden=256, num_experts=16, top_k=2, inter=128, shared_inter=128,
+             routing=synth.ROUTE_SOFTMAX, norm_topk_prob=True, routed_scaling_factor=1.0, expert_fmt=fmt, n_tokens=1)
+    d.update(kw)
+    return synth.LayerConfig(**d)
+
+
+def close(got, ref, norm=False):
+    rms = float(np.sqrt(np.mean(ref ** 2)))
+    bad = np.abs(got - ref) - (2.0 ** -8 * np.abs(ref) + (5e-3 + (2.2e-2 if norm else 0.0)) * rms)
+    assert bad.max() <= 0, f"over by {bad.max():.3e} (RMS {rms:.3e})"
+
+
+# ---------------------------------------------------------------- the format, on the CPU
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("zero", [False, True])
+def test_decode_by_hand(fmt, zero):
+    """Every code of one row, decoded element by element in Python integers."""
+    G = synth.INT4_GROUP[fmt]
+    rng = np.random.default_rng(5)
+    packed = rng.integers(0, 256, (3, G), dtype=np.uint8)              # 2 G elements: two groups
+    scale = torch.tensor(rng.uniform(0.01, 2, (3, 2)), dtype=torch.bfloat16)
+    zp = rng.integers(0, 16, (3, 2), dtype=np.uint8) if zero else None
+    w = O.dequant_int4(packed, scale.view(torch.int16).numpy().view(np.uint16), zp, G)
+    for o in range(3):
+        for i in range(2 * G):
+            code = (int(packed[o, i // 2]) >> (4 * (i % 2))) & 15
+            z = 8 if zp is None else int(zp[o, i // G])
+            assert w[o, i] == (code - z) * float(scale[o, i // G])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("zero", [False, True])
+def test_quantiser_error(fmt, zero):
+    """Within a group every value is at most half a step off (plus the scale's own BF16
+    rounding of at most 2^-8, times the 15 steps of the range)."""
+    G = synth.INT4_GROUP[fmt]
+    w = torch.randn(8, 4 * G, generator=torch.Generator().manual_seed(3)) * 0.02
+    q, s, z = synth.quant_int4(w, G, zero)
+    back = O.dequant_int4(q.numpy(), s.view(torch.int16).numpy().view(np.uint16), None if z is None else z.numpy(), G)
+    step = s.float().numpy().repeat(G, axis=1)
+    # A rounded zero point can move an end of the range by half a step more.
+    assert np.all(np.abs(back - w.numpy()) <= step * (0.5 + 15 * 2.0 ** -8 + (0.5 if zero else 0.0)))
+
+
+def test_matrix_bytes():
+    assert synth.matrix_bytes("int4_g64", 128, 256) == 128 * 128 + 2 * 128 * 4
+    assert synth.matrix_bytes("int4_g64", 128, 256, True) == 128 * 128 + 3 * 128 * 4
+
+
+# ---------------------------------------------------------------- refusals, on the CPU
+
+FAKE = 0x7f0000000000      # never dereferenced here
+
+
+def _weights(**kw):
+    w = B.moe_weights_t()
+    w.router_w = FAKE
+    for m in ("gate", "up", "down", "sh_gate", "sh_up", "sh_down"):
+        getattr(w, m).w = FAKE
+        getattr(w, m).scale = FAKE
+    for k, v in kw.items():
+        setattr(w, k, v)
+    return w
+
+
+def test_refusals():
+    out, big = FAKE + 0x100000, 1 << 40
+
+    def call(c, w):
+        return B.moe_forward(c, w, FAKE, 1, out, None, None, FAKE, big, 0)
+
+    for fmt, g in synth.INT4_GROUP.items():
+        for field in ("hidden", "inter", "shared_inter"):
+            c = make_config(cfg_of(fmt, hidden=256, inter=256, shared_inter=256))
+            setattr(c, field, 256 + g // 2 if g > 32 else 272)      # not whole groups
+            assert call(c, _weights()) == B.MOE_ERR_INVALID_CONFIG
+            assert B.moe_workspace_bytes(c, 4) == 0
+        c = make_config(cfg_of(fmt))
+        w = _weights()
+        w.up.scale = None
+        assert call(c, w) == B.MOE_ERR_NULL
+        w = _weights()
+        w.up.scale = FAKE + 2
+        assert call(c, w) == B.MOE_ERR_ALIGNMENT
+        # Zero points are bytes (any alignment) and optional: the workspace check comes next.
+        w = _weights()
+        w.up.zero = FAKE + 1
+        assert B.moe_forward(c, w, FAKE, 1, out, None, None, FAKE, 16, 0) == B.MOE_ERR_WORKSPACE
+    c = make_config(cfg_of())
+    c.expert_fmt = 6
+    assert call(c, _weights()) == B.MOE_ERR_INVALID_CONFIG
+    c = make_config(cfg_of())
+    c.router_fmt = B.MOE_W_INT4_G32      # a router is BF16 or NVFP4
+    assert call(c, _weights()) == B.MOE_ERR_INVALID_CONFIG
+
+
+def test_zero_shares_scale2():
+    """The zero points sit where scale2 does, and the struct keeps its size."""
+    assert B.moe_qmat_t.zero.offset == B.moe_qmat_t.scale2.offset == 16
+    assert ctypes.sizeof(B.moe_qmat_t) == 24
+
+
+# ---------------------------------------------------------------- the layer, on the GPU
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    B.load()
+
+
+def check(cfg, n, path="auto", x=None, lw=None):
+    lw = synth.make_weights(cfg, "cuda") if lw is None else lw
+    L = int4_oracle_layer(lw)
+    if x is None:
+        x = synth.make_input(cfg, n, "cuda", gap_fn=gap_fn_for(L))
+    layer = MoeLayer(lw, n, path)
+    out, idx, w = layer.forward(x)
+    torch.cuda.synchronize()
+    assert layer.device_error() == 0
+    ref, ridx, rw, _ = O.moe_forward(L, bf16_bits(x))
+    assert np.array_equal(idx.cpu().numpy(), ridx)
+    assert np.max(np.abs(w.cpu().numpy() - rw)) <= 1e-5 * max(1.0, cfg.routed_scaling_factor)
+    close(out.float().cpu().numpy(), ref, cfg.pre_expert_norm)
+    return lw, x, layer, out, idx, w
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("path", ["auto", "token_major", "grouped"])
+@pytest.mark.parametrize("n", [1, 2, 5, 17])
+def test_layer(lib, fmt, zero, path, n):
+    check(cfg_of(fmt, zero_points=zero), n, path)
+
+
+@gpu
+@pytest.mark.parametrize("path", ["auto", "token_major", "grouped"])
+@pytest.mark.parametrize("H,I,S,E,k,n", [
+    (96, 32, 32, 5, 3, 1),        # the smallest widths: less than one tile, one group
+    (96, 32, 32, 5, 3, 6),
+    (160, 96, 0, 3, 3, 9),        # no shared expert, every expert chosen
+    (416, 288, 160, 40, 8, 33),   # odd tiles of 32
+    (1056, 544, 96, 7, 1, 70),    # top-1, many tokens an expert
+])
+def test_odd_sizes(lib, path, H, I, S, E, k, n):
+    check(cfg_of("int4_g32", hidden=H, inter=I, shared_inter=S, num_experts=E, top_k=k, zero_points=True,
+                 routing=synth.ROUTE_SIGMOID_BIAS, routed_scaling_factor=2.5), n, path)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 3, 24])
+def test_norm_and_shared_gate(lib, n):
+    check(cfg_of("int4_g64", shared_gate=True, pre_expert_norm=True), n)
+
+
+@gpu
+@pytest.mark.parametrize("n,path", [(2, "auto"), (24, "auto"), (24, "grouped"), (130, "auto")])
+def test_rows_do_not_depend_on_the_batch(lib, n, path):
+    """A token's output bits with other tokens in the batch, permuted, and with a duplicate."""
+    cfg = cfg_of("int4_g64", zero_points=True)
+    lw, x, layer, out, _, _ = check(cfg, n, path)
+    p = torch.randperm(n, generator=torch.Generator().manual_seed(1)).cuda()
+    out2, _, _ = MoeLayer(lw, n, path).forward(x[p].contiguous())
+    assert torch.equal(out2, out[p])
+    y = x.clone()
+    y[0] = x[n - 1]
+    out3, _, _ = MoeLayer(lw, n, path).forward(y)
+    assert torch.equal(out3[0], out[n - 1]) and torch.equal(out3[1:], out[1:])
+
+
+@gpu
+@pytest.mark.parametrize("path", ["auto", "grouped", "token_major"])
+@pytest.mark.parametrize("n", [1, 7])
+def test_given_routing(lib, n, path):
+    """moe_experts with routes the caller made: an expert twice in one token's row, indices
+    outside the layer (dropped), a zero weight, and a row whose every route is dropped."""
+    cfg = cfg_of("int4_g32", top_k=4)
+    lw = synth.make_weights(cfg, "cuda")
+    L = int4_oracle_layer(lw)
+    x = synth.make_input(cfg, n, "cuda")
+    g = torch.Generator().manual_seed(2)
+    idx = torch.randint(0, 16, (n, 4), generator=g)
+    idx[0] = torch.tensor([3, 3, 11, -1])
+    if n > 1:
+        idx[1] = torch.tensor([-5, 16, 1 << 30, -(1 << 31)])
+    w = torch.rand(n, 4, generator=g)
+    w[-1, 0] = 0
+    layer = MoeLayer(lw, n, path)
+    out = layer.experts(x, idx.to(torch.int32).cuda(), w.cuda())
+    torch.cuda.synchronize()
+    assert layer.device_error() == 0
+    xe = O.bf16_decode(bf16_bits(x))
+    sh = O.swiglu_mlp(xe, L.sh_gate.expert(0), L.sh_up.expert(0), L.sh_down.expert(0))
+    ref = sh.copy()
+    for t in range(n):
+        for j in range(4):
+            e = int(idx[t, j])
+            if 0 <= e < 16:
+                ref[t] += float(w[t, j]) * O.swiglu_mlp(xe[t], L.gate.expert(e), L.up.expert(e), L.down.expert(e))
+    close(out.float().cpu().numpy(), ref)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 6])
+def test_expert_parallel(lib, n):
+    """Two ranks' partials and the shared-expert call: slices of stacked scales and zero points."""
+    cfg = cfg_of("int4_g32", zero_points=True)
+    lw, x, _, _, _, _ = check(cfg, n)
+    L = int4_oracle_layer(lw)
+    total = np.zeros((n, cfg.hidden))
+    for r in ((0, 5), (5, 16)):
+        layer = MoeLayer(synth.expert_slice(lw, *r), n, experts=r, exclude_shared=True)
+        out, _, _ = layer.forward(x)
+        ref, _, _, _ = O.moe_forward(L, bf16_bits(x), experts=r, include_shared=False)
+        got = out.float().cpu().numpy()
+        close(got, ref) if np.any(ref) else None
+        total += got
+    layer = MoeLayer(synth.expert_slice(lw, 16, 16), n, experts=(16, 16), accumulate=True)
+    out = torch.tensor(total, dtype=torch.bfloat16, device="cuda")
+    before = out.float().cpu().numpy()
+    layer.forward(x, out=out, routing=False)
+    ref = O.moe_forward(L, bf16_bits(x), experts=(0, 0))[0]
+    close(out.float().cpu().numpy(), before + ref)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 12])
+def test_captured_and_replayed(lib, n):
+    """Two layers with workspaces of their own in one graph, replayed on new inputs."""
+    cfg = cfg_of("int4_g64")
+    lw = synth.make_weights(cfg, "cuda")
+    xs = [synth.make_input(cfg, n, "cuda", stream=s) for s in range(3)]
+    a, b = MoeLayer(lw, n), MoeLayer(lw, n)
+    want = [a.forward(x)[0].clone() for x in xs]
+    buf, oa, ob = xs[0].clone(), torch.empty_like(want[0]), torch.empty_like(want[0])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        a.forward(buf, out=oa)
+        b.forward(buf, out=ob)
+    torch.cuda.current_stream().wait_stream(st)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.forward(buf, out=oa)
+        b.forward(buf, out=ob)
+    for x, r in zip(xs, want):
+        buf.copy_(x)
+        oa.zero_(), ob.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(oa, r) and torch.equal(ob, r)
+
+
+@gpu
+def test_special_values_stay_in_their_row(lib):
+    """NaN and infinity in one token's input do not reach another token's output."""
+    cfg = cfg_of("int4_g32", n_tokens=9)
+    lw, x, layer, out, idx, w = check(cfg, 9)
+    y = x.clone()
+    y[4, 3] = float("nan")
+    y[6, 200] = float("inf")
+    got = layer.experts(y, idx, w)
+    rest = [0, 1, 2, 3, 5, 7, 8]
+    assert torch.equal(got[rest], layer.experts(x, idx, w)[rest])
+    assert torch.isnan(got[4]).all()
+
+
+@gpu
+@pytest.mark.parametrize("name,fmt,n", [("decode_n1", "int4_g128", 1), ("decode_n16", "int4_g64", 16),
+                                        ("nvfp4_n256", "int4_g32", 256)])
+def test_workload_sizes(lib, name, fmt, n):
+    cfg = dataclasses.replace(synth.WORKLOADS[name], expert_fmt=fmt, zero_points=fmt == "int4_g64", dup_frac=0.0)
+    lw = synth.make_weights(cfg, "cuda")
+    L = int4_oracle_layer(lw)
+    x = synth.make_input(cfg, n, "cuda", gap_fn=gap_fn_for(L))
+    layer = MoeLayer(lw, n)
+    out, idx, w = layer.forward(x)
+    rows = [0] if n == 1 else [0, n // 2, n - 1]
+    ref, ridx, _, _ = O.moe_forward(L, bf16_bits(x), rows=rows)
+    assert np.array_equal(idx.cpu().numpy()[rows], ridx)
+    close(out.float().cpu().numpy()[rows], ref)
+    assert layer.device_error() == 0
