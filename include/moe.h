@@ -7,6 +7,7 @@
  *   router   logits[t,e] = sum_h x[t,h] * Wr[e,h]                 (fp32)
  *   top-k    softmax: rank logits, p = softmax over all E logits;
  *            sigmoid+bias: rank sigmoid(l)+bias, p = sigmoid(l);
+ *            (also softmax+bias, sigmoid alone, and group-limited selection)
  *            w = p / sum_topk p if norm_topk_prob; w *= routed_scaling_factor
  *   experts  per (token t, slot j), e = idx[t,j]:
  *            d = Wd[e] (SiLU(Wg[e] x_t) * (Wu[e] x_t)),  SiLU(g) = g/(1+exp(-g))
@@ -115,7 +116,27 @@ typedef enum {
     MOE_ERR_HOST_MEMORY = 8      /* `x` or `out` is host memory that is not pinned (page-locked) */
 } moe_status_t;
 
-typedef enum { MOE_ROUTE_SOFTMAX = 0, MOE_ROUTE_SIGMOID_BIAS = 1 } moe_routing_t;
+/* Scores p of the experts (softmax over all E, or sigmoid, of the logits) and
+ * the selection score s that ranks them: the logit itself, or p + the correction
+ * bias in the *_BIAS modes (the bias only selects, it enters no weight). */
+typedef enum {
+    MOE_ROUTE_SOFTMAX = 0,
+    MOE_ROUTE_SIGMOID_BIAS = 1,
+    MOE_ROUTE_SOFTMAX_BIAS = 2,
+    MOE_ROUTE_SIGMOID = 3
+} moe_routing_t;
+/* Group-limited routing: the experts form `groups` groups of E / groups
+ * consecutive ones (at most 32 groups, of equal size), the `kept` groups with
+ * the best group scores stay (ties: the lower group), and the top-k is taken
+ * among their experts, of which there must be at least k.  A group's score is
+ * its best selection score, or the sum of its two best p (+ bias) (of the one,
+ * in a group of one). */
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
+/* The routing word of moe_config_t and moe_topk_config_t: a moe_routing_t
+ * alone, or one with groups. */
+#define MOE_ROUTING(mode, groups, kept, score) \
+    ((int32_t)((mode) | ((groups) << 8) | ((kept) << 16) | ((score) << 24)))
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype_t;
 typedef enum {
     MOE_W_BF16 = 0,
     MOE_W_FP8_B128 = 1,
@@ -173,7 +194,7 @@ typedef struct {
     int32_t top_k;                  /* k */
     int32_t inter;                  /* I  (routed expert intermediate size) */
     int32_t shared_inter;           /* S  (shared expert intermediate size; 0 = none) */
-    int32_t routing;                /* moe_routing_t */
+    int32_t routing;                /* moe_routing_t or MOE_ROUTING(...) */
     int32_t norm_topk_prob;         /* 0 or 1 */
     float   routed_scaling_factor;
     int32_t expert_fmt;             /* moe_wfmt_t: routed and shared experts alike */
@@ -201,7 +222,7 @@ typedef struct {
  * ignored (may be NULL) when shared_inter == 0. */
 typedef struct {
     const void*  router_w;          /* BF16 [E, H] */
-    const float* correction_bias;   /* fp32 [E]; required for SIGMOID_BIAS, must be NULL for SOFTMAX */
+    const float* correction_bias;   /* fp32 [E]; required by the *_BIAS modes, else must be NULL */
     moe_qmat_t   gate, up, down;    /* routed experts */
     moe_qmat_t   sh_gate, sh_up, sh_down;   /* shared expert (E = 1) */
     const void*  shared_gate_w;     /* BF16 [H] or NULL (then the shared gate is 1) */
@@ -336,6 +357,64 @@ moe_status_t moe_static_workspace_check(int32_t* device_error, void** workspace,
  * MOE_ERR_CUDA. */
 moe_status_t moe_workspace_check(void* ws, size_t ws_bytes, int32_t* device_error,
                                  moe_stream_t stream);
+
+/* Routing of one call, from logits the caller holds (moe_topk). */
+typedef struct {
+    int32_t num_experts;            /* E, 1..1024 */
+    int32_t top_k;                  /* k, 1..min(E, 32) */
+    int32_t routing;                /* moe_routing_t or MOE_ROUTING(...) */
+    int32_t norm_topk_prob;         /* 0 or 1 */
+    float   routed_scaling_factor;  /* finite */
+    int32_t logits_type;            /* moe_dtype_t */
+} moe_topk_config_t;
+
+/* Top-k routing of n rows of logits: the pages' topk step on its own, for a
+ * router product the caller made, and for any number of rows.  moe_route and
+ * moe_forward route through the same kernel when their routing word is not one
+ * of MOE_ROUTE_SOFTMAX and MOE_ROUTE_SIGMOID_BIAS alone.
+ *   logits      device [n, E] of logits_type, rows row_stride elements apart
+ *               (row_stride >= E; any element alignment)
+ *   bias        device fp32 [E] (*_BIAS modes; 4-byte aligned), else NULL
+ *   idx, w      device int32 / fp32 [n, k] (out), slots in descending
+ *               selection score, equal scores by ascending expert index
+ * Selection is that of the scores in 64 bits.  A NaN score ranks last.
+ * w = p, divided by the sum of the k selected p if norm_topk_prob, times
+ * routed_scaling_factor; a row whose selected logits are all -inf gets w = 0.
+ * logits may also be pinned host memory.  No workspace; n == 0 is a no-op.
+ * Errors: MOE_ERR_NULL, MOE_ERR_INVALID_CONFIG, MOE_ERR_UNSUPPORTED (more than
+ * 32 groups), MOE_ERR_ALIGNMENT (a pointer is not aligned to its element),
+ * MOE_ERR_HOST_MEMORY, MOE_ERR_CUDA. */
+moe_status_t moe_topk(const moe_topk_config_t* cfg, const void* logits, int64_t row_stride, const float* bias,
+                      int32_t n, int32_t* idx, float* w, moe_stream_t stream);
+
+/* One 4-bit weight matrix [out_features, in_features] (moe_matvec). */
+typedef struct {
+    int32_t out_features;           /* > 0 */
+    int32_t in_features;            /* > 0, a multiple of 32 and of the group size */
+    int32_t w_fmt;                  /* MOE_W_INT4_G32 / G64 / G128 or MOE_W_NVFP4 */
+    int32_t x_type;                 /* MOE_BF16 or MOE_F16 */
+    int32_t out_type;               /* moe_dtype_t */
+    int32_t accumulate;             /* 1: out = rounded(out + result) */
+} moe_matvec_config_t;
+
+/* out[t, o] = sum_i W[o, i] x[t, i] (+ bias[o]) (+ out[t, o]) for the n rows of
+ * x: the matrix-vector product of the layer's 4-bit formats for a decode batch,
+ * as the experts use it, for the dense projections around the layer.  fp32
+ * accumulation, one rounding to out_type.  A row's result does not depend on
+ * the other rows.  The weights cross HBM once for each 16 rows.
+ *   w           the matrix, in the layouts above with E = 1 (its w 16-byte
+ *               aligned, scale and scale2 4)
+ *   bias        device fp32 [out_features] (4-byte aligned), or NULL
+ *   x           device [n, in_features], rows x_stride elements apart; 16-byte
+ *               aligned, x_stride >= in_features and a multiple of 8
+ *   out         device [n, out_features], rows out_stride >= out_features
+ *               elements apart, aligned to its element; must not overlap x
+ * x and out may also be pinned host memory.  No workspace; n == 0 is a no-op.
+ * Errors: MOE_ERR_NULL, MOE_ERR_INVALID_CONFIG, MOE_ERR_UNSUPPORTED (a weight
+ * format of 8 or 16 bits), MOE_ERR_ALIGNMENT, MOE_ERR_ALIAS,
+ * MOE_ERR_HOST_MEMORY, MOE_ERR_CUDA. */
+moe_status_t moe_matvec(const moe_matvec_config_t* cfg, const moe_qmat_t* w, const float* bias, const void* x,
+                        int64_t x_stride, int32_t n, void* out, int64_t out_stride, moe_stream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* moe_status_string(moe_status_t status);

@@ -28,6 +28,13 @@ MOE_ERR_HOST_MEMORY = 8
 
 MOE_ROUTE_SOFTMAX = 0
 MOE_ROUTE_SIGMOID_BIAS = 1
+MOE_ROUTE_SOFTMAX_BIAS = 2
+MOE_ROUTE_SIGMOID = 3
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2 = 1
+MOE_F32 = 0
+MOE_BF16 = 1
+MOE_F16 = 2
 MOE_W_BF16 = 0
 MOE_W_FP8_B128 = 1
 MOE_W_NVFP4 = 2
@@ -41,7 +48,8 @@ MOE_PATH_GROUPED = 2
 # Every function include/moe.h declares.
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_experts", "moe_forward",
             "moe_forward_timed", "moe_forward_static_ws", "moe_static_workspace_check",
-            "moe_workspace_check", "moe_status_string", "moe_abi_version")
+            "moe_topk", "moe_matvec", "moe_workspace_check", "moe_status_string",
+            "moe_abi_version")
 
 MOE_STATIC_WORKSPACE_BYTES = 16 << 20
 
@@ -72,6 +80,23 @@ class moe_weights_t(ctypes.Structure):
                 ("sh_gate", moe_qmat_t), ("sh_up", moe_qmat_t), ("sh_down", moe_qmat_t),
                 ("shared_gate_w", ctypes.c_void_p), ("pre_expert_norm_w", ctypes.c_void_p),
                 ("router_q", moe_qmat_t)]
+
+
+class moe_topk_config_t(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("routing", ctypes.c_int32), ("norm_topk_prob", ctypes.c_int32),
+                ("routed_scaling_factor", ctypes.c_float), ("logits_type", ctypes.c_int32)]
+
+
+class moe_matvec_config_t(ctypes.Structure):
+    _fields_ = [("out_features", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("w_fmt", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+def MOE_ROUTING(mode: int, groups: int, kept: int, score: int) -> int:
+    """The routing word of group-limited routing (the macro of moe.h)."""
+    return mode | groups << 8 | kept << 16 | score << 24
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -112,6 +137,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.moe_static_workspace_check.restype = ctypes.c_int
     lib.moe_workspace_check.argtypes = [P, S, ctypes.POINTER(I32), P]
     lib.moe_workspace_check.restype = ctypes.c_int
+    I64 = ctypes.c_int64
+    lib.moe_topk.argtypes = [ctypes.POINTER(moe_topk_config_t), P, I64, P, I32, P, P, P]
+    lib.moe_topk.restype = ctypes.c_int
+    lib.moe_matvec.argtypes = [ctypes.POINTER(moe_matvec_config_t), ctypes.POINTER(moe_qmat_t), P, P,
+                               I64, I32, P, I64, P]
+    lib.moe_matvec.restype = ctypes.c_int
     lib.moe_status_string.argtypes = [ctypes.c_int]
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_abi_version.argtypes = []
@@ -189,6 +220,16 @@ def moe_static_workspace_check(stream=None):
     addr = ctypes.c_void_p(None)
     s = load().moe_static_workspace_check(ctypes.byref(v), ctypes.byref(addr), _stream(stream))
     return s, v.value, addr.value
+
+
+def moe_topk(cfg, logits, row_stride, bias, n, idx, w, stream=None) -> int:
+    return load().moe_topk(_ref(cfg), _ptr(logits), int(row_stride), _ptr(bias), int(n), _ptr(idx),
+                           _ptr(w), _stream(stream))
+
+
+def moe_matvec(cfg, w, bias, x, x_stride, n, out, out_stride, stream=None) -> int:
+    return load().moe_matvec(_ref(cfg), _ref(w), _ptr(bias), _ptr(x), int(x_stride), int(n), _ptr(out),
+                             int(out_stride), _stream(stream))
 
 
 def moe_workspace_check(ws, ws_bytes, stream=None):

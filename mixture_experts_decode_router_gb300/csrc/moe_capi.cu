@@ -55,6 +55,14 @@ static int residency(const void* p) {
 }
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+static moe_status_t check_routing(int32_t word, int E, int k) {
+    const Routing r = routing_of(word);
+    if (word < 0 || r.mode > MOE_ROUTE_SIGMOID || r.top2 > 1) return MOE_ERR_INVALID_CONFIG;
+    if (((word >> 8) & 0xff) == 0) return word == r.mode ? MOE_OK : MOE_ERR_INVALID_CONFIG;
+    if (E % r.groups || r.kept < 1 || r.kept > r.groups || r.kept * (E / r.groups) < k) return MOE_ERR_INVALID_CONFIG;
+    return r.groups <= 32 ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
 static moe_status_t check_config(const moe_config_t* c) {
     if (!c) return MOE_ERR_NULL;
     if (c->num_experts < 1 || c->num_experts > kMaxExperts) return MOE_ERR_INVALID_CONFIG;
@@ -62,8 +70,8 @@ static moe_status_t check_config(const moe_config_t* c) {
     if (c->hidden <= 0 || c->hidden % 32) return MOE_ERR_INVALID_CONFIG;
     if (c->inter <= 0 || c->inter % 32) return MOE_ERR_INVALID_CONFIG;
     if (c->shared_inter < 0 || c->shared_inter % 32) return MOE_ERR_INVALID_CONFIG;
-    if (c->routing != MOE_ROUTE_SOFTMAX && c->routing != MOE_ROUTE_SIGMOID_BIAS)
-        return MOE_ERR_INVALID_CONFIG;
+    const moe_status_t rs = check_routing(c->routing, c->num_experts, c->top_k);
+    if (rs != MOE_OK) return rs;
     if (c->norm_topk_prob != 0 && c->norm_topk_prob != 1) return MOE_ERR_INVALID_CONFIG;
     if (!(c->routed_scaling_factor == c->routed_scaling_factor) ||
         c->routed_scaling_factor > 3.0e38f || c->routed_scaling_factor < -3.0e38f)
@@ -124,11 +132,11 @@ static moe_status_t check_router_weights(const moe_config_t* c, const moe_weight
         if (!w->router_w) return MOE_ERR_NULL;
         if (!aligned16(w->router_w)) return MOE_ERR_ALIGNMENT;
     }
-    if (c->routing == MOE_ROUTE_SIGMOID_BIAS) {
+    if (mode_has_bias(routing_of(c->routing).mode)) {
         if (!w->correction_bias) return MOE_ERR_NULL;
         if (!aligned16(w->correction_bias)) return MOE_ERR_ALIGNMENT;
     } else if (w->correction_bias) {
-        return MOE_ERR_INVALID_CONFIG;   // a bias has no meaning under softmax routing
+        return MOE_ERR_INVALID_CONFIG;   // a bias has no meaning in this mode
     }
     return MOE_OK;
 }
@@ -250,7 +258,7 @@ static moe_status_t enqueue_route(const moe_config_t* c, const moe_weights_t* w,
         if (e == cudaSuccess)
             e = launch_router_tc(static_cast<const uint16_t*>(x), n, c->hidden, wr, c->num_experts, part,
                                  &at<Ctrl>(ws, L.ctrl)->err, rsc, early_dependents(n, sms), st);
-        if (w->shared_gate_w && with_group && topk_group_gate_fits(c->num_experts, c->hidden))
+        if (w->shared_gate_w && with_group && routing_plain(c->routing) && topk_group_gate_fits(c->num_experts, c->hidden))
             gate_in_topk = static_cast<const uint16_t*>(w->shared_gate_w);
         else if (e == cudaSuccess && w->shared_gate_w)
             e = launch_router(static_cast<const uint16_t*>(x), n, c->hidden, nullptr, 0,
@@ -274,6 +282,15 @@ static moe_status_t enqueue_route(const moe_config_t* c, const moe_weights_t* w,
     }
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     mk.mark(st);
+    if (!routing_plain(c->routing)) {
+        // Groups and the other score modes: the row kernel; the grouping, when
+        // it follows, is a launch (and ends the stage) of its own.
+        e = launch_topk_rows(lin, MOE_F32, c->num_experts, ns, (int64_t)n * c->num_experts, lsum, n, c->num_experts,
+                             c->top_k, c->routing, w->correction_bias, c->norm_topk_prob, c->routed_scaling_factor,
+                             idx, wt, sms, st);
+        if (!with_group) mk.mark(st);
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
     if (with_group)
         e = launch_topk_group(lin, ns, n, c->num_experts, c->top_k, c->routing, w->correction_bias, c->norm_topk_prob,
                               c->routed_scaling_factor, idx, wt, c->expert_begin, c->expert_end,
@@ -549,7 +566,7 @@ static moe_status_t forward_impl(const moe_config_t* cfg_in, const moe_weights_t
     int32_t* idx_p = idx ? idx : at<int32_t>(ws, L.idx);
     float* w_p = w ? w : at<float>(ws, L.w);
     mk.mark(st);
-    if (n == 1 && cfg->path != MOE_PATH_GROUPED && cfg->router_fmt == MOE_W_BF16) {
+    if (n == 1 && cfg->path != MOE_PATH_GROUPED && cfg->router_fmt == MOE_W_BF16 && routing_plain(cfg->routing)) {
         // One token: the whole layer in one cooperative launch when its
         // shared-memory plan fits (same arithmetic as the kernels below).
         const int sms = device_sm_count();
@@ -607,7 +624,7 @@ static moe_status_t forward_impl(const moe_config_t* cfg_in, const moe_weights_t
         return enqueue_experts(cfg, wts, x, n, idx_p, w_p, out, ws, L, true, false, st, mk);
     }
     if ((s = enqueue_route(cfg, wts, x, n, idx_p, w_p, nullptr, ws, L, true, true, st, mk)) != MOE_OK) return s;
-    return enqueue_experts(cfg, wts, x, n, idx_p, w_p, out, ws, L, true, true, st, mk);
+    return enqueue_experts(cfg, wts, x, n, idx_p, w_p, out, ws, L, true, routing_plain(cfg->routing), st, mk);
 }
 
 moe_status_t moe_forward(const moe_config_t* cfg, const moe_weights_t* wts, const void* x, int32_t n,
@@ -628,6 +645,70 @@ moe_status_t moe_forward_timed(const moe_config_t* cfg, const moe_weights_t* wts
     const moe_status_t s = forward_impl(cfg, wts, x, n, out, idx, w, ws, ws_bytes, stream, mk);
     if (n_marks) *n_marks = mk.next;
     return s;
+}
+
+moe_status_t moe_topk(const moe_topk_config_t* cfg, const void* logits, int64_t row_stride, const float* bias,
+                      int32_t n, int32_t* idx, float* w, moe_stream_t stream) {
+    if (!cfg) return MOE_ERR_NULL;
+    const int E = cfg->num_experts, k = cfg->top_k;
+    if (E < 1 || E > kMaxExperts || k < 1 || k > E || k > kMaxTopK) return MOE_ERR_INVALID_CONFIG;
+    const moe_status_t s = check_routing(cfg->routing, E, k);
+    if (s != MOE_OK) return s;
+    if (cfg->norm_topk_prob != 0 && cfg->norm_topk_prob != 1) return MOE_ERR_INVALID_CONFIG;
+    if (!(cfg->routed_scaling_factor >= -3.0e38f && cfg->routed_scaling_factor <= 3.0e38f))
+        return MOE_ERR_INVALID_CONFIG;
+    if (cfg->logits_type < MOE_F32 || cfg->logits_type > MOE_F16 || n < 0) return MOE_ERR_INVALID_CONFIG;
+    if (mode_has_bias(routing_of(cfg->routing).mode)) {
+        if (!bias) return MOE_ERR_NULL;
+        if (!aligned4(bias)) return MOE_ERR_ALIGNMENT;
+    } else if (bias) {
+        return MOE_ERR_INVALID_CONFIG;
+    }
+    if (n == 0) return MOE_OK;
+    if (!logits || !idx || !w) return MOE_ERR_NULL;
+    if (row_stride < E) return MOE_ERR_INVALID_CONFIG;
+    const uintptr_t esize = cfg->logits_type == MOE_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(logits) % esize || !aligned4(idx) || !aligned4(w)) return MOE_ERR_ALIGNMENT;
+    if (residency(logits) < 0) return MOE_ERR_HOST_MEMORY;
+    return launch_topk_rows(logits, cfg->logits_type, row_stride, 1, 0, nullptr, n, E, k, cfg->routing, bias,
+                            cfg->norm_topk_prob, cfg->routed_scaling_factor, idx, w, device_sm_count(),
+                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_matvec(const moe_matvec_config_t* cfg, const moe_qmat_t* w, const float* bias, const void* x,
+                        int64_t x_stride, int32_t n, void* out, int64_t out_stride, moe_stream_t stream) {
+    if (!cfg || !w) return MOE_ERR_NULL;
+    const int O = cfg->out_features, K = cfg->in_features, fmt = cfg->w_fmt;
+    if (O < 1 || K < 32 || K % 32 || fmt < MOE_W_BF16 || fmt > MOE_W_INT4_G128) return MOE_ERR_INVALID_CONFIG;
+    if (fmt != MOE_W_NVFP4 && !is_int4(fmt)) return MOE_ERR_UNSUPPORTED;
+    if (is_int4(fmt) && K % (1 << int4_gshift(fmt))) return MOE_ERR_INVALID_CONFIG;
+    if ((cfg->x_type != MOE_BF16 && cfg->x_type != MOE_F16) || cfg->out_type < MOE_F32 || cfg->out_type > MOE_F16)
+        return MOE_ERR_INVALID_CONFIG;
+    if ((cfg->accumulate != 0 && cfg->accumulate != 1) || n < 0) return MOE_ERR_INVALID_CONFIG;
+    const moe_status_t s = check_qmat(fmt, *w);
+    if (s != MOE_OK) return s;
+    if (bias && !aligned4(bias)) return MOE_ERR_ALIGNMENT;
+    if (n == 0) return MOE_OK;
+    if (!x || !out) return MOE_ERR_NULL;
+    if (x_stride < K || out_stride < O) return MOE_ERR_INVALID_CONFIG;
+    const size_t osize = cfg->out_type == MOE_F32 ? 4 : 2;
+    if (!aligned16(x) || x_stride % 8 || reinterpret_cast<uintptr_t>(out) % osize) return MOE_ERR_ALIGNMENT;
+    const size_t xb = ((size_t)(n - 1) * x_stride + K) * 2, ob = ((size_t)(n - 1) * out_stride + O) * osize;
+    const uintptr_t xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
+    if (xa < oa + ob && oa < xa + xb) return MOE_ERR_ALIAS;
+    if (residency(x) < 0 || residency(out) < 0) return MOE_ERR_HOST_MEMORY;
+    MatvecParams p{};
+    p.w = qdev(fmt, *w, O, K, 0);
+    p.bias = bias;
+    p.x = x;
+    p.x_stride = x_stride;
+    p.n = n;
+    p.out = out;
+    p.out_stride = out_stride;
+    p.out_type = cfg->out_type;
+    p.accumulate = cfg->accumulate;
+    return launch_matvec(fmt, cfg->x_type, p, device_sm_count(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status_t moe_workspace_check(void* ws, size_t ws_bytes, int32_t* device_error, moe_stream_t stream) {

@@ -137,6 +137,34 @@ struct QMatDev {
     int gshift;             // INT4: log2 of the group size
 };
 
+// A routing word taken apart (MOE_ROUTING).
+struct Routing {
+    int mode;      // moe_routing_t
+    int groups;    // 1 = no groups
+    int kept;
+    int top2;      // group score: the sum of the two best p (+ bias); else the best selection score
+};
+__host__ __device__ inline Routing routing_of(int32_t word) {
+    Routing r;
+    r.mode = word & 0xff;
+    r.groups = (word >> 8) & 0xff;
+    r.kept = (word >> 16) & 0xff;
+    r.top2 = (word >> 24) & 0xff;
+    if (r.groups == 0) r.groups = r.kept = 1;
+    return r;
+}
+// Whether the word is one the fused routing kernels (route_token_block) cover;
+// any other is routed by the row kernel of moe_topk.cu.
+__host__ __device__ inline bool routing_plain(int32_t word) {
+    return word == MOE_ROUTE_SOFTMAX || word == MOE_ROUTE_SIGMOID_BIAS;
+}
+__host__ __device__ inline bool mode_has_bias(int mode) {
+    return mode == MOE_ROUTE_SIGMOID_BIAS || mode == MOE_ROUTE_SOFTMAX_BIAS;
+}
+__host__ __device__ inline bool mode_sigmoid(int mode) {
+    return mode == MOE_ROUTE_SIGMOID_BIAS || mode == MOE_ROUTE_SIGMOID;
+}
+
 // The INT4 formats share their kernels; the group size is a run-time shift.
 constexpr int kFmtInt4 = MOE_W_INT4_G32;
 __host__ __device__ constexpr bool is_int4(int fmt) { return fmt >= MOE_W_INT4_G32 && fmt <= MOE_W_INT4_G128; }

@@ -140,6 +140,25 @@ cudaError_t launch_router_nvfp4(const uint16_t* x, int n, int H, const QMatDev& 
 // matrix), summed in order; lsum (may be null) receives the sums.
 cudaError_t launch_topk(const float* logits, int ns, float* lsum, int n, int E, int k, int routing, const float* bias,
                         int norm, float scale, int32_t* idx, float* w, cudaStream_t st);
+// Top-k routing of rows of logits (moe_topk.cu).  ns > 1 (fp32 only): a row's
+// logits are the sums, in order, of ns partial rows pstride elements apart;
+// lsum (may be null) receives them, rows E apart.
+cudaError_t launch_topk_rows(const void* logits, int dtype, int64_t row_stride, int ns, int64_t pstride, float* lsum,
+                             int n, int E, int k, int32_t routing, const float* bias, int norm, float scale,
+                             int32_t* idx, float* w, int num_sms, cudaStream_t st);
+// out[t, :] = W x[t, :] for a 4-bit W (moe_matvec.cu).
+struct MatvecParams {
+    QMatDev w;
+    const float* bias;
+    const void* x;
+    int64_t x_stride;
+    int n;
+    void* out;
+    int64_t out_stride;
+    int out_type, accumulate;
+};
+cudaError_t launch_matvec(int fmt, int x_type, const MatvecParams& p, int num_sms, cudaStream_t st);
+
 cudaError_t launch_group(const int32_t* idx, int nk, int E, int e_begin, int e_end, int32_t* counts,
                          int32_t* offsets, int32_t* perm, int32_t* inv, int32_t* active, int32_t* segs,
                          Ctrl* ctrl, cudaStream_t st);

@@ -11,12 +11,29 @@ import torch
 
 from . import binding as B
 from .synth import (FMT_BF16, FMT_FP8_B128, FMT_INT4_G128, FMT_INT4_G32, FMT_INT4_G64, FMT_NVFP4,
-                    ROUTE_SIGMOID_BIAS, LayerConfig, LayerWeights, QMatT)
+                    ROUTE_SIGMOID, ROUTE_SIGMOID_BIAS, ROUTE_SOFTMAX, ROUTE_SOFTMAX_BIAS, LayerConfig,
+                    LayerWeights, QMatT)
 
 _FMT = {FMT_BF16: B.MOE_W_BF16, FMT_FP8_B128: B.MOE_W_FP8_B128, FMT_NVFP4: B.MOE_W_NVFP4,
         FMT_INT4_G32: B.MOE_W_INT4_G32, FMT_INT4_G64: B.MOE_W_INT4_G64, FMT_INT4_G128: B.MOE_W_INT4_G128}
 _PATH = {"auto": B.MOE_PATH_AUTO, "token_major": B.MOE_PATH_TOKEN_MAJOR,
          "grouped": B.MOE_PATH_GROUPED}
+
+
+_MODE = {ROUTE_SOFTMAX: B.MOE_ROUTE_SOFTMAX, ROUTE_SIGMOID_BIAS: B.MOE_ROUTE_SIGMOID_BIAS,
+         ROUTE_SOFTMAX_BIAS: B.MOE_ROUTE_SOFTMAX_BIAS, ROUTE_SIGMOID: B.MOE_ROUTE_SIGMOID}
+_SCORE = {"max": B.MOE_GROUP_MAX, "top2": B.MOE_GROUP_TOP2}
+_TYPE = {torch.float32: B.MOE_F32, torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_F16}
+
+
+def routing_word(routing: str, num_groups: int = 1, topk_groups: int = 1, group_score: str = "top2") -> int:
+    """The C routing word of a routing name and its groups (1 = no groups)."""
+    mode = _MODE[routing]
+    if num_groups == 1:
+        return mode
+    if not (0 < num_groups < 256 and 0 < topk_groups < 256):
+        raise ValueError("num_groups and topk_groups are 1..255")
+    return B.MOE_ROUTING(mode, num_groups, topk_groups, _SCORE[group_score])
 
 
 def make_config(cfg: LayerConfig, path: str = "auto", experts=None,
@@ -27,7 +44,7 @@ def make_config(cfg: LayerConfig, path: str = "auto", experts=None,
     c = B.moe_config_t()
     c.hidden, c.num_experts, c.top_k = cfg.hidden, cfg.num_experts, cfg.top_k
     c.inter, c.shared_inter = cfg.inter, cfg.shared_inter
-    c.routing = B.MOE_ROUTE_SIGMOID_BIAS if cfg.routing == ROUTE_SIGMOID_BIAS else B.MOE_ROUTE_SOFTMAX
+    c.routing = routing_word(cfg.routing, cfg.num_groups, cfg.topk_groups, cfg.group_score)
     c.norm_topk_prob = 1 if cfg.norm_topk_prob else 0
     c.routed_scaling_factor = cfg.routed_scaling_factor
     c.expert_fmt = _FMT[cfg.expert_fmt]
@@ -131,4 +148,100 @@ class MoeLayer:
         out = torch.empty(n, self.cfg.hidden, dtype=torch.bfloat16, device=x.device)
         B.check(B.moe_experts(self.c_cfg, self.c_w, x, n, idx, w, out, self.ws, self.ws_bytes,
                               stream))
+        return out
+
+
+def _on_current_device(t: torch.Tensor) -> None:
+    if not t.is_cuda and not t.is_pinned():
+        raise ValueError("tensors are on the GPU or in pinned host memory")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+class MoeTopk:
+    """Top-k routing of logits the caller holds (``moe_topk``): ``forward(logits)``
+    returns ``(idx, w)`` of ``[n, num_experts]`` fp32, bf16 or fp16 logits, whose
+    rows may be strided.
+
+    ``routing`` is "softmax" or "sigmoid"; ``bias`` (fp32 ``[num_experts]``) is added
+    to the scores for the selection only.  ``num_groups`` > 1 limits the selection
+    to the ``topk_groups`` groups of best ``group_score`` ("max", or "top2": the sum
+    of the group's two best scores).
+    """
+
+    def __init__(self, num_experts: int, top_k: int, routing: str = "softmax",
+                 bias: Optional[torch.Tensor] = None, num_groups: int = 1, topk_groups: int = 1,
+                 group_score: str = "top2", norm_topk_prob: bool = True, routed_scaling_factor: float = 1.0):
+        if bias is not None and (bias.dtype != torch.float32 or bias.shape != (num_experts,)
+                                 or not bias.is_contiguous()):
+            raise ValueError("bias is contiguous float32 [num_experts]")
+        name = {"softmax": (ROUTE_SOFTMAX, ROUTE_SOFTMAX_BIAS),
+                "sigmoid": (ROUTE_SIGMOID, ROUTE_SIGMOID_BIAS)}[routing][bias is not None]
+        c = B.moe_topk_config_t()
+        c.num_experts, c.top_k = num_experts, top_k
+        c.routing = routing_word(name, num_groups, topk_groups, group_score)
+        c.norm_topk_prob = 1 if norm_topk_prob else 0
+        c.routed_scaling_factor = routed_scaling_factor
+        # One configuration for each logits type, so that calls change nothing here.
+        self.c_cfg, self.bias = {}, bias
+        for dtype, code in _TYPE.items():
+            self.c_cfg[dtype] = B.moe_topk_config_t.from_buffer_copy(c)
+            self.c_cfg[dtype].logits_type = code
+
+    def forward(self, logits: torch.Tensor, idx=None, w=None, stream=None):
+        c = self.c_cfg[logits.dtype]
+        if logits.dim() != 2 or logits.shape[1] != c.num_experts or (c.num_experts > 1 and logits.stride(1) != 1):
+            raise ValueError("logits are [n, num_experts] with contiguous rows")
+        _on_current_device(logits)
+        n = logits.shape[0]
+        if idx is None:
+            idx = torch.empty(n, c.top_k, dtype=torch.int32, device="cuda")
+        if w is None:
+            w = torch.empty(n, c.top_k, dtype=torch.float32, device="cuda")
+        stride = logits.stride(0) if n > 1 else c.num_experts
+        B.check(B.moe_topk(c, logits, stride, self.bias, n, idx, w, stream))
+        return idx, w
+
+
+class MoeMatvec:
+    """Products of one 4-bit matrix with a few vectors (``moe_matvec``): ``forward(x)``
+    returns ``[n, out]`` of ``out_dtype`` for bf16 or fp16 ``x`` ``[n, in]``, whose rows
+    may be strided.  ``weights``: a ``QMatT`` ``[out, in/2]`` (INT4 groups or NVFP4);
+    ``bias``: fp32 ``[out]``; ``accumulate`` adds the result into ``out`` (which must
+    then be given).
+    """
+
+    def __init__(self, weights: QMatT, bias: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                 accumulate: bool = False):
+        q = weights
+        out_f, in_f = q.w.shape[-2], 2 * q.w.shape[-1]
+        if q.w.numel() != out_f * in_f // 2 or not all(
+                t is None or t.is_contiguous() for t in (q.w, q.scale, q.scale2, q.zero, bias)):
+            raise ValueError("one contiguous matrix [out, in/2] and its scales")
+        if bias is not None and (bias.dtype != torch.float32 or bias.shape != (out_f,)):
+            raise ValueError("bias is float32 [out]")
+        c = B.moe_matvec_config_t()
+        c.out_features, c.in_features, c.w_fmt = out_f, in_f, _FMT[q.fmt]
+        c.out_type, c.accumulate = _TYPE[out_dtype], 1 if accumulate else 0
+        self.c_cfg, self.c_w = {}, _qmat(q)
+        for dtype in (torch.bfloat16, torch.float16):   # one for each type of x
+            self.c_cfg[dtype] = B.moe_matvec_config_t.from_buffer_copy(c)
+            self.c_cfg[dtype].x_type = _TYPE[dtype]
+        self.weights, self.bias, self.out_dtype = q, bias, out_dtype
+
+    def forward(self, x: torch.Tensor, out=None, stream=None):
+        c = self.c_cfg[x.dtype]
+        if x.dim() != 2 or x.shape[1] != c.in_features or x.stride(1) != 1:
+            raise ValueError("x is [n, in] with contiguous rows")
+        _on_current_device(x)
+        n = x.shape[0]
+        if out is None:
+            if c.accumulate:
+                raise ValueError("accumulate needs out")
+            out = torch.empty(n, c.out_features, dtype=self.out_dtype, device="cuda")
+        elif (out.shape != (n, c.out_features) or out.dtype != self.out_dtype
+              or (c.out_features > 1 and out.stride(1) != 1)):
+            raise ValueError("out is [n, out] of out_dtype with contiguous rows")
+        B.check(B.moe_matvec(c, self.c_w, self.bias, x, x.stride(0) if n > 1 else c.in_features, n, out,
+                             out.stride(0) if n > 1 else c.out_features, stream))
         return out

@@ -23,7 +23,7 @@ Recipe (one layer):
         ``zero_points`` s = BF16((max - min) / 15), z = clamp(rne(-min / s), 0, 15),
         q = clamp(rne(w / s) + z, 0, 15) (min <= 0 <= max); two codes per byte, the
         even element in the low nibble
-  * correction bias ~ U(-r, r) fp32 [E] (sigmoid routing only)
+  * correction bias ~ U(-r, r) fp32 [E] (the routings with a bias only)
   * input rows ~ N(0, 1) -> BF16.  An optional ``gap_fn`` (supplied by the
     caller) returns, per row, the margin between the k-th and (k+1)-th
     selection score; rows whose margin is <= ``min_gap`` are redrawn from the
@@ -47,6 +47,8 @@ import torch
 
 ROUTE_SOFTMAX = "softmax"
 ROUTE_SIGMOID_BIAS = "sigmoid_bias"
+ROUTE_SOFTMAX_BIAS = "softmax_bias"
+ROUTE_SIGMOID = "sigmoid"
 FMT_BF16 = "bf16"
 FMT_FP8_B128 = "fp8_b128"
 FMT_NVFP4 = "nvfp4"
@@ -82,6 +84,9 @@ class LayerConfig:
     rms_norm_eps: float = 1e-6
     seed: int = 0
     zero_points: bool = False          # INT4 experts: a zero point per group (else 8)
+    num_groups: int = 1                # group-limited routing: groups of experts,
+    topk_groups: int = 1               # those kept,
+    group_score: str = "top2"          # by the best score ("max") or the sum of the two best
 
     def with_(self, **kw) -> "LayerConfig":
         return replace(self, **kw)
@@ -283,7 +288,7 @@ def make_router_q(cfg: LayerConfig, device="cpu") -> Optional[QMatT]:
 
 
 def make_bias(cfg: LayerConfig, device="cpu") -> Optional[torch.Tensor]:
-    if cfg.routing != ROUTE_SIGMOID_BIAS:
+    if cfg.routing not in (ROUTE_SIGMOID_BIAS, ROUTE_SOFTMAX_BIAS):
         return None
     u = torch.rand(cfg.num_experts, generator=_gen(device, cfg.seed, "bias"), device=device)
     return ((u * 2.0 - 1.0) * cfg.bias_range).to(torch.float32)
@@ -402,7 +407,7 @@ def layer_bytes(cfg: LayerConfig) -> dict:
         return matrix_bytes(cfg.expert_fmt, out_d, in_d, cfg.zero_points)
     per_expert = 2 * mat(I, H) + mat(H, I)
     shared = 2 * mat(S, H) + mat(H, S) if S > 0 else 0
-    extra = ((4 * E if cfg.routing == ROUTE_SIGMOID_BIAS else 0) + (2 * H if cfg.shared_gate else 0)
+    extra = ((4 * E if cfg.routing in (ROUTE_SIGMOID_BIAS, ROUTE_SOFTMAX_BIAS) else 0) + (2 * H if cfg.shared_gate else 0)
              + (2 * H if cfg.pre_expert_norm else 0))
     router = E * H * 2 if cfg.router_fmt == FMT_BF16 else matrix_bytes(cfg.router_fmt, E, H)
     return {"router": router, "per_expert": per_expert, "shared": shared, "extra": extra,
