@@ -682,6 +682,7 @@ moe_status_t moe_matvec(const moe_matvec_config_t* cfg, const moe_qmat_t* w, con
     if (O < 1 || K < 32 || K % 32 || fmt < MOE_W_BF16 || fmt > MOE_W_INT4_G128) return MOE_ERR_INVALID_CONFIG;
     if (fmt != MOE_W_NVFP4 && !is_int4(fmt)) return MOE_ERR_UNSUPPORTED;
     if (is_int4(fmt) && K % (1 << int4_gshift(fmt))) return MOE_ERR_INVALID_CONFIG;
+    if (!matvec_fits(K)) return MOE_ERR_UNSUPPORTED;
     if ((cfg->x_type != MOE_BF16 && cfg->x_type != MOE_F16) || cfg->out_type < MOE_F32 || cfg->out_type > MOE_F16)
         return MOE_ERR_INVALID_CONFIG;
     if ((cfg->accumulate != 0 && cfg->accumulate != 1) || n < 0) return MOE_ERR_INVALID_CONFIG;

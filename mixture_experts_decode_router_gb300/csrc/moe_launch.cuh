@@ -157,6 +157,7 @@ struct MatvecParams {
     int64_t out_stride;
     int out_type, accumulate;
 };
+bool matvec_fits(int K);   // whether a row of x fits beside the kernel's rings
 cudaError_t launch_matvec(int fmt, int x_type, const MatvecParams& p, int num_sms, cudaStream_t st);
 
 cudaError_t launch_group(const int32_t* idx, int nk, int E, int e_begin, int e_end, int32_t* counts,
