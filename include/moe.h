@@ -390,7 +390,7 @@ moe_status_t moe_topk(const moe_topk_config_t* cfg, const void* logits, int64_t 
 /* One 4-bit weight matrix [out_features, in_features] (moe_matvec). */
 typedef struct {
     int32_t out_features;           /* > 0 */
-    int32_t in_features;            /* > 0, a multiple of 32 and of the group size, <= 62720 */
+    int32_t in_features;            /* > 0, a multiple of 32 and of the group size, <= 57344 */
     int32_t w_fmt;                  /* MOE_W_INT4_G32 / G64 / G128 or MOE_W_NVFP4 */
     int32_t x_type;                 /* MOE_BF16 or MOE_F16 */
     int32_t out_type;               /* moe_dtype_t */
@@ -411,7 +411,7 @@ typedef struct {
  *               elements apart, aligned to its element; must not overlap x
  * x and out may also be pinned host memory.  No workspace; n == 0 is a no-op.
  * Errors: MOE_ERR_NULL, MOE_ERR_INVALID_CONFIG, MOE_ERR_UNSUPPORTED (a weight
- * format of 8 or 16 bits, more than 62720 in_features), MOE_ERR_ALIGNMENT, MOE_ERR_ALIAS,
+ * format of 8 or 16 bits, more than 57344 in_features), MOE_ERR_ALIGNMENT, MOE_ERR_ALIAS,
  * MOE_ERR_HOST_MEMORY, MOE_ERR_CUDA. */
 moe_status_t moe_matvec(const moe_matvec_config_t* cfg, const moe_qmat_t* w, const float* bias, const void* x,
                         int64_t x_stride, int32_t n, void* out, int64_t out_stride, moe_stream_t stream);

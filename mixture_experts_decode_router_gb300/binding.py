@@ -165,7 +165,7 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -249,6 +249,11 @@ def moe_abi_version() -> int:
 
 class MoeError(RuntimeError):
     pass
+
+
+def entry(name: str):
+    """The library's function, for holders that call it with converted arguments."""
+    return getattr(load(), name)
 
 
 def check(status: int) -> None:

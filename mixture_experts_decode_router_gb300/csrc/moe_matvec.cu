@@ -16,7 +16,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kStages = 6;            // ring of each warp (5 stages in flight)
+constexpr int kStages = 3;            // ring of each warp (2 stages in flight)
 constexpr int kMaxSmem = 227 * 1024;
 
 __device__ __forceinline__ void store_out(const MatvecParams& p, int64_t t, int o, float v) {
@@ -34,12 +34,23 @@ __device__ __forceinline__ void store_out(const MatvecParams& p, int64_t t, int 
     }
 }
 
-// XB: x is bf16 (else f16).  INT4 multiplies in x's type.  NVFP4 multiplies in f16:
-// bf16 rows are scaled by a power of two that puts their largest value below 2^15
-// (exact for elements down to 2^-32 of it) and the results scaled back.
-template <int GSH, bool XB, int NT>
-__global__ void __launch_bounds__(32 * kWarps) matvec_kernel(const MatvecParams p, int kw, int tp) {
-    constexpr bool BF = XB && GSH != 4;
+// Shared memory of a block: the warps' rings, the results' factors, the
+// rows of x, and (kw > 1) the warps' sums.
+struct Smem {
+    uint32_t factor, x, red, total;
+};
+__host__ __device__ inline Smem smem_plan(int K, int nt, int ntok, int kw) {
+    Smem m;
+    m.factor = kWarps * kStages * q4::kStageBytes;   // of each token's result
+    m.x = m.factor + 64;
+    m.red = m.x + (uint32_t)ntok * q4::x_row_bytes(K);
+    m.total = m.red + (kw > 1 ? kWarps * nt * 512 : 0);
+    return m;
+}
+
+// XB: x is bf16 (else f16).
+template <int GSH, bool Z, bool XB, int NT>
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) matvec_kernel(const MatvecParams p, int kw, int tp) {
     extern __shared__ __align__(128) uint8_t dyn[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int K = p.w.in_dim, O = p.w.out_dim, row_bytes = K / 2;
@@ -48,66 +59,86 @@ __global__ void __launch_bounds__(32 * kWarps) matvec_kernel(const MatvecParams 
     const int n_tiles = (O + 15) / 16, step = gridDim.x * mw;
     const int64_t t0 = (int64_t)blockIdx.y * tp;
     const int ntok = (int)min((int64_t)tp, (int64_t)p.n - t0);
-    uint8_t* ring = dyn + (size_t)warp * kStages * q4::kStageBytes;
-    float* red = reinterpret_cast<float*>(dyn + (size_t)kWarps * kStages * q4::kStageBytes);   // [warp][NT][32][4]
-    float* xsc = red + kWarps * NT * 128;                                                      // [16]
-    uint8_t* sx = reinterpret_cast<uint8_t*>(xsc + 16);
-    const int xstride = q4::x_row_bytes(K);
+    const Smem sm = smem_plan(K, NT, ntok, kw);
+    const uint32_t ring = warp * kStages * q4::kStageBytes;
     pdl_wait();
 
-    // The copies run kStages - 1 stages ahead of the products, across tiles.
-    int i_tile = blockIdx.x * mw + mrow, i_s = kk, i_slot = 0;
+    // The copies run kStages - 1 stages ahead of the products, across tiles, and
+    // the scales' loads one.
+    const uint32_t dyn_a = q4::smem_addr(dyn);
+    const int full = row_bytes / 128;
+    int i_tile = kk < nst ? blockIdx.x * mw + mrow : n_tiles, i_s = kk, i_slot = 0;
+    q4::RowCopy cp;
+    cp.start(p.w.w, (int64_t)i_tile * 16, O - i_tile * 16, row_bytes, kk, lane);
     auto issue = [&]() {
-        if (i_s < nst && i_tile < n_tiles) {
-            q4::load_stage(q4::smem_addr(ring + i_slot * q4::kStageBytes), p.w.w, i_tile * 16, O, row_bytes, i_s, lane);
+        if (i_tile < n_tiles) {
+            cp.issue(dyn_a + ring + i_slot * q4::kStageBytes, i_s, kw, row_bytes, full, p.w.w, lane);
             i_s += kw;
-            if (i_s >= nst) { i_s = kk; i_tile += step; }
+            if (i_s >= nst) {
+                i_s = kk;
+                i_tile += step;
+                cp.start(p.w.w, (int64_t)i_tile * 16, O - i_tile * 16, row_bytes, kk, lane);
+            }
         }
         q4::cp_commit();
         i_slot = i_slot + 1 == kStages ? 0 : i_slot + 1;
     };
+    int n_tile = i_tile, n_s = kk;
+    q4::StageScales<GSH, Z> sc, next;
+    q4::ScaleLoad<GSH, Z> sl;
+    sl.start(p.w, (int64_t)n_tile * 16, O - n_tile * 16, kk, lane);
+    auto load_scales = [&]() {
+        if (n_tile < n_tiles) {
+            sl.load(next, n_s, kw, K, lane);
+            n_s += kw;
+            if (n_s >= nst) {
+                n_s = kk;
+                n_tile += step;
+                sl.start(p.w, (int64_t)n_tile * 16, O - n_tile * 16, kk, lane);
+            }
+        }
+    };
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue();
+    load_scales();
 
-    // x in fragment order, zero past K.
-    const int chunks = (xstride - 64) / 16;
-    for (int b = (GSH == 4 && XB) ? warp : 0; b < ntok; b += (GSH == 4 && XB) ? kWarps : 1) {
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.x) + (size_t)(t0 + b) * p.x_stride);
-        uint4* dst = reinterpret_cast<uint4*>(sx + (size_t)b * xstride);
-        if constexpr (GSH == 4 && XB) {
-            float am = 0.f;
-            for (int c = lane; c < K / 8; c += 32) {
-                float v[8];
-                bf16x8_to_float(src[c], v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(v[i]));
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-            const int sh = q4::f16_shift(am);
-            const float f = q4::exp2i(sh);
-            if (lane == 0) xsc[b] = q4::exp2i(-sh);
-            for (int c = lane; c < chunks; c += 32) {
-                float v[8] = {};
-                if (c < K / 8) bf16x8_to_float(src[c], v);
-                uint32_t h[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __half2 hv = __floats2half2_rn(v[2 * i] * f, v[2 * i + 1] * f);
-                    h[i] = *reinterpret_cast<const uint32_t*>(&hv);
-                }
-                dst[c] = q4::chunk_order<GSH>(make_uint4(h[0], h[1], h[2], h[3]));
-            }
-        } else {
-            for (int c = threadIdx.x; c < chunks; c += 32 * kWarps)
-                dst[c] = q4::chunk_order<GSH>(c < K / 8 ? src[c] : make_uint4(0u, 0u, 0u, 0u));
-            if (threadIdx.x == 0) xsc[b] = 1.f;
+    // x in fragment order, zero behind each row.
+    const int xstride = q4::x_row_bytes(K), K8 = K / 8, chunks = nst * (q4::kStageK / 8);
+    float* factor = reinterpret_cast<float*>(dyn + sm.factor);
+    auto row = [&](int b) {
+        return reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.x) + (size_t)(t0 + b) * p.x_stride);
+    };
+    if constexpr (GSH == 4 && XB) {
+        for (int b = warp; b < ntok; b += kWarps) {
+            const float f = q4::scaled_row(row(b), K8, chunks, reinterpret_cast<uint4*>(dyn + sm.x + b * xstride), lane);
+            if (lane == 0) factor[b] = f * __ldg(p.w.scale2);
         }
+    } else {
+        constexpr int kU = 4;   // loads of a thread in flight
+        for (int b = 0; b < ntok; ++b) {
+            const uint4* src = row(b);
+            uint4* dst = reinterpret_cast<uint4*>(dyn + sm.x + b * xstride);
+            for (int c0 = threadIdx.x; c0 < chunks; c0 += kU * 32 * kWarps) {
+                uint4 v[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int c = c0 + u * 32 * kWarps;
+                    v[u] = c < K8 ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int c = c0 + u * 32 * kWarps;
+                    if (c < chunks) dst[c] = q4::chunk_order<GSH>(v[u]);
+                }
+            }
+        }
+        if (threadIdx.x < 16) factor[threadIdx.x] = GSH == 4 ? __ldg(p.w.scale2) : 1.f;
     }
     __syncthreads();
+    q4::XView<NT> x;
+    x.start(sm.x, xstride, ntok, lane);
 
     const int g = lane >> 2, t = lane & 3;
-    const float ms = GSH == 4 ? __ldg(p.w.scale2) : 1.f;
     int slot = 0;
     for (int base = blockIdx.x * mw; base < n_tiles; base += step) {
         const int tile = base + mrow, row0 = tile * 16;
@@ -117,22 +148,19 @@ __global__ void __launch_bounds__(32 * kWarps) matvec_kernel(const MatvecParams 
         for (int q = 0; q < NT; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[q][i] = 0.f;
-        if (live && kk < nst) {
-            q4::StageScales<GSH> sc, next;
-            next.load(p.w, 0, row0, O, kk, lane);
+        if (live) {
             for (int s = kk; s < nst; s += kw) {
                 sc = next;
-                if (s + kw < nst) next.load(p.w, 0, row0, O, s + kw, lane);
+                load_scales();
                 q4::cp_wait<kStages - 2>();
                 __syncwarp();
                 issue();
-                q4::mma_stage<GSH, BF, NT>(ring + slot * q4::kStageBytes, sx + (size_t)g * xstride + s * 512 + t * 16,
-                                           xstride, ntok, sc, acc, lane);
+                q4::mma_stage<GSH, Z, XB && GSH != 4, NT>(dyn, ring + slot * q4::kStageBytes, x, s, sc, acc, lane);
                 slot = slot + 1 == kStages ? 0 : slot + 1;
             }
         }
         if (kw > 1) {
-            float4* mine = reinterpret_cast<float4*>(red) + (size_t)warp * NT * 32;
+            float4* mine = reinterpret_cast<float4*>(dyn + sm.red) + (size_t)warp * NT * 32;
 #pragma unroll
             for (int q = 0; q < NT; ++q) mine[q * 32 + lane] = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
             __syncthreads();
@@ -152,22 +180,22 @@ __global__ void __launch_bounds__(32 * kWarps) matvec_kernel(const MatvecParams 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = row0 + g + 8 * (i >> 1), b = 8 * q + 2 * t + (i & 1);
-                    if (row < O && b < ntok) store_out(p, t0 + b, row, acc[q][i] * (ms * xsc[b]));
+                    if (row < O && b < ntok) store_out(p, t0 + b, row, acc[q][i] * factor[b]);
                 }
         }
     }
     pdl_trigger();
 }
 
-template <int GSH, bool XB, int NT>
+template <int GSH, bool Z, bool XB, int NT>
 cudaError_t launch_nt(const MatvecParams& p, int tp, int num_sms, cudaStream_t st) {
     const int K = p.w.in_dim, n_tiles = (p.w.out_dim + 15) / 16, nst = (K + q4::kStageK - 1) / q4::kStageK;
-    // Warps that share a tile: as many as give every SM a block.
+    // Warps that share a tile: as many as give every SM about its 24 warps (a
+    // 7168 x 7168 product with one token: 12.4 us at 8 a SM, KWNEW us so).
     int kw = 1;
-    while (kw < kWarps && kw < nst && (int64_t)n_tiles * kw < (int64_t)num_sms * kWarps) kw *= 2;
-    const size_t smem = (size_t)kWarps * kStages * q4::kStageBytes + (size_t)kWarps * NT * 512 + 64 +
-                        (size_t)std::min<int64_t>(tp, p.n) * q4::x_row_bytes(K);
-    auto kern = matvec_kernel<GSH, XB, NT>;
+    while (kw < kWarps && kw < nst && (int64_t)n_tiles * kw < (int64_t)num_sms * 20) kw *= 2;
+    const size_t smem = smem_plan(K, NT, std::min(tp, p.n), kw).total;
+    auto kern = matvec_kernel<GSH, Z, XB, NT>;
     static std::mutex mu;
     static bool configured[128] = {};
     int dev = 0;
@@ -180,33 +208,39 @@ cudaError_t launch_nt(const MatvecParams& p, int tp, int num_sms, cudaStream_t s
             configured[dev] = true;
         }
     }
-    const int per_sm = 2 * smem <= (size_t)kMaxSmem ? 2 : 1;
+    const int per_sm = std::max(1, std::min(3, (int)((size_t)kMaxSmem / (smem + 1024))));
     const int mw = kWarps / kw;
     const int gx = std::min((n_tiles + mw - 1) / mw, num_sms * per_sm);
     launch_pdl(kern, dim3(gx, (unsigned)((p.n + tp - 1) / tp)), 32 * kWarps, smem, st, p, kw, tp);
     return cudaGetLastError();
 }
 
-template <int GSH, bool XB>
+template <int GSH, bool Z, bool XB>
 cudaError_t launch_fmt(const MatvecParams& p, int num_sms, cudaStream_t st) {
     // Tokens of a block: up to 16, as many as fit beside the rings.
-    const size_t room = kMaxSmem - (size_t)kWarps * (kStages * q4::kStageBytes + 2 * 512) - 64;
-    const int tp = std::min<size_t>(16, room / q4::x_row_bytes(p.w.in_dim));
-    if (tp < 1) return cudaErrorInvalidValue;   // (the caller checked matvec_fits)
+    const int64_t room = kMaxSmem - (int64_t)smem_plan(p.w.in_dim, 2, 0, kWarps).total;
+    int tp = (int)std::min<int64_t>(16, room / q4::x_row_bytes(p.w.in_dim));
+    if (tp < 1) return cudaErrorInvalidValue;   // (matvec_fits says no)
     const int tokens = std::min(tp, p.n);
-    return tokens > 8 ? launch_nt<GSH, XB, 2>(p, tp, num_sms, st) : launch_nt<GSH, XB, 1>(p, std::min(tp, 8), num_sms, st);
+    return tokens > 8 ? launch_nt<GSH, Z, XB, 2>(p, tp, num_sms, st) : launch_nt<GSH, Z, XB, 1>(p, std::min(tp, 8), num_sms, st);
 }
 
 template <int GSH>
 cudaError_t launch_x(int x_type, const MatvecParams& p, int num_sms, cudaStream_t st) {
-    return x_type == MOE_BF16 ? launch_fmt<GSH, true>(p, num_sms, st) : launch_fmt<GSH, false>(p, num_sms, st);
+    if constexpr (GSH != 4) {
+        if (p.w.zero)
+            return x_type == MOE_BF16 ? launch_fmt<GSH, true, true>(p, num_sms, st) : launch_fmt<GSH, true, false>(p, num_sms, st);
+    }
+    return x_type == MOE_BF16 ? launch_fmt<GSH, false, true>(p, num_sms, st) : launch_fmt<GSH, false, false>(p, num_sms, st);
 }
 
 }  // namespace
 
-bool matvec_fits(int K) {
-    return q4::x_row_bytes(K) <= kMaxSmem - kWarps * (kStages * q4::kStageBytes + 2 * 512) - 64;
-}
+// The longest row of x that the interface admits; one fits beside the rings.
+constexpr int kMaxIn = 57344;
+static_assert(kWarps * (kStages * q4::kStageBytes + 1024) + 64 + kMaxIn * 2 + 64 + 512 <= kMaxSmem,
+              "a row of x fits");
+bool matvec_fits(int K) { return K <= kMaxIn; }
 
 cudaError_t launch_matvec(int fmt, int x_type, const MatvecParams& p, int num_sms, cudaStream_t st) {
     switch (fmt) {

@@ -10,7 +10,7 @@
 // first have to be written, dequantised, to tensor memory.
 //
 //  * A warp owns 16 weight rows and walks its K range in stages of 256 codes
-//    (128 bytes a row, 2 KB), which it copies itself, several stages ahead, with
+//    (128 bytes a row, 2 KB), which it copies itself, some stages ahead, with
 //    16-byte cp.async (zero-filled past the matrix).  Warps share nothing but x.
 //  * 16-byte chunk c of row r sits at chunk c ^ (r & 7), so the fragment reads
 //    below touch every bank once.
@@ -19,11 +19,16 @@
 //    word of each row feeds two MMAs and all 32 codes of a step lie in one group.
 //    Its nibbles i and i + 4 form one 16-bit pair (INT4), so x is stored with
 //    the elements of every 8 in the order 0 4 1 5 2 6 3 7.
-//  * INT4 value = (q - z) s: q goes under the exponent of 128 (bf16) or 1024
-//    (f16), less 128 + z (1024 + z) is the exact difference; the MMA sums a
-//    group in fp32, and s multiplies that sum in fp32.  Nothing is rounded.
-//  * NVFP4 value = e2m1 e4m3 scale2: the product of the two small floats is exact
-//    in f16; scale2 multiplies the result.
+//  * INT4 value = (q - z) s: q goes under the exponent of 128 (bf16) or of 1024 and
+//    64 (f16), less that exponent's value + z is the exact difference; the MMA sums
+//    a group in fp32, and s multiplies that sum in fp32.  No weight is rounded, and
+//    x enters as it is.  (Measured and not kept: masked codes as f16 subnormals with
+//    -z taken away by a second MMA, or by the groups' sums of x, after scaling x
+//    into range: as many instructions, and the scaling of x on top.)
+//  * NVFP4: e2m1 times e4m3 is exact in f16; scale2 multiplies the result.  bf16
+//    rows of x are scaled by a power of two that puts their largest value below
+//    2^15 (exact for elements down to 2^-32 of it; below, they round at 2^-40 of
+//    it) and the results scaled back.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -39,38 +44,75 @@ constexpr int kStageBytes = 16 * 128;
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-// 16 bytes global -> shared; zeros when !valid (src is not read then).
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The same, with zeros when !valid (src is not read then).
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool valid) {
     const int n = valid ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Weight rows row0 .. row0 + 15 of the matrix whose code rows (`row_bytes` each)
-// start at w: the 128 bytes of stage s, into dst (swizzled).
-__device__ __forceinline__ void load_stage(uint32_t dst, const uint8_t* w, int row0, int rows, int row_bytes, int s,
-                                           int lane) {
-    const int c = lane & 7, byte = s * 128 + c * 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        const bool ok = row0 + r < rows && byte < row_bytes;
-        cp16(dst + r * 128 + ((c ^ (r & 7)) << 4), ok ? w + (size_t)(row0 + r) * row_bytes + byte : w, ok);
+// A lane's part of the copies of 16 weight rows: rows lane / 8 + 4 i, chunk lane % 8
+// of one stage after another.
+struct RowCopy {
+    const uint8_t* src;    // row lane / 8, chunk lane % 8 of the next stage
+    int rows;              // rows of the tile inside the matrix
+    uint32_t d0;           // lane's place in a stage; row r + 4's chunk is the other of bit 2
+    __device__ __forceinline__ void start(const uint8_t* w, int64_t row, int rows_left, int row_bytes, int s, int lane) {
+        const int r0 = lane >> 3;
+        src = w + (row + r0) * row_bytes + s * 128 + (lane & 7) * 16;
+        rows = rows_left;
+        d0 = r0 * 128 + (((lane & 7) ^ r0) << 4);
     }
-}
+    // The next stage, number s, into dst; `step` stages on after it.  full_stages:
+    // stages that lie inside the row.
+    __device__ __forceinline__ void issue(uint32_t dst, int s, int step, int row_bytes, int full_stages,
+                                          const uint8_t* any, int lane) {
+        const uint32_t d = dst + d0, e = dst + (d0 ^ 64u);
+        const size_t r4 = (size_t)(4 * row_bytes);
+        if (rows >= 16 && s < full_stages) {
+            cp16(d, src);
+            cp16(e + 512, src + r4);
+            cp16(d + 1024, src + 2 * r4);
+            cp16(e + 1536, src + 3 * r4);
+        } else {
+            const bool in = s * 128 + (lane & 7) * 16 < row_bytes;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool ok = in && (lane >> 3) + 4 * i < rows;
+                cp16_or_zero(((i & 1) ? e : d) + 512 * i, ok ? src + i * r4 : any, ok);
+            }
+        }
+        src += step * 128;
+    }
+};
 
-template <bool BF>
+// d += A B, or (FIRST) d = A B; 16-bit operands bf16 (BF) or f16, fp32 sums.
+template <bool BF, bool FIRST>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    if constexpr (BF)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if constexpr (FIRST) {
+        if constexpr (BF)
+            asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+        else
+            asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    } else {
+        if constexpr (BF)
+            asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        else
+            asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    }
 }
 
 __device__ __forceinline__ uint32_t lop_and_or(uint32_t a, uint32_t mask, uint32_t orv) {
@@ -80,9 +122,10 @@ __device__ __forceinline__ uint32_t lop_and_or(uint32_t a, uint32_t mask, uint32
 }
 
 // The eight codes of w less the zero point, as pairs (i, i + 4), exact.  zz: two
-// copies of 128 + z (bf16) or 1024 + z (f16).
+// copies of 128 + z (bf16) or 1024 + z (f16); z64 (f16): of 64 + z.  In f16 a
+// nibble in bits 4-7 under the exponent of 64 is 64 + q, which saves two shifts.
 template <bool BF>
-__device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t zz, uint32_t (&p)[4]) {
+__device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t zz, uint32_t z64, uint32_t (&p)[4]) {
     if constexpr (BF) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -90,34 +133,18 @@ __device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t zz, uint32_t (&p
             asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(v), "r"(zz));
         }
     } else {
-        // A nibble in bits 4-7 is 16 q under the exponent of 1024: (1024 + 16 q) / 16
-        // - (64 + z) = q - z, exact, and saves the shift.
-        const uint32_t w8 = w >> 8;
-        uint32_t zh;   // 64 + z = (1024 + z) - 960
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(zh) : "r"(zz), "r"(0x63806380u));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t v = h ? w8 : w;
-            const uint32_t lo = lop_and_or(v, 0x000f000fu, 0x64006400u);
-            const uint32_t hi = lop_and_or(v, 0x00f000f0u, 0x64006400u);
-            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[2 * h]) : "r"(lo), "r"(zz));
-            asm("{ .reg .b32 n; neg.f16x2 n, %2; fma.rn.f16x2 %0, %1, %3, n; }"
-                : "=r"(p[2 * h + 1]) : "r"(hi), "r"(zh), "r"(0x2c002c00u));
+            const uint32_t v = w >> (8 * h);
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[2 * h]) : "r"(lop_and_or(v, 0x000f000fu, 0x64006400u)), "r"(zz));
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[2 * h + 1]) : "r"(lop_and_or(v, 0x00f000f0u, 0x54005400u)), "r"(z64));
         }
     }
 }
-
-// Two copies of 128 + z (bf16) or 1024 + z (f16).
-template <bool BF>
-__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
-    if constexpr (BF) {
-        const __nv_bfloat162 v = __float2bfloat162_rn((float)(128u + z));
-        return *reinterpret_cast<const uint32_t*>(&v);
-    } else {
-        const __half2 v = __float2half2_rn((float)(1024u + z));
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
-}
+// Two copies of 128 (bf16) or 1024 (f16), to whose last places z is added.
+template <bool BF> constexpr uint32_t kZeroBase = BF ? 0x43004300u : 0x64006400u;
+// Two copies of 64 + z from those of 1024 + z.
+__device__ __forceinline__ constexpr uint32_t zero64(uint32_t zz) { return zz * 16u + (0x54005400u - 0x64006400u * 16u); }
 
 // NVFP4: the eight codes of w (pairs of neighbours) times the block scale, exact in f16.
 __device__ __forceinline__ void nvfp4_pairs(uint32_t w, uint32_t s2, uint32_t (&p)[4]) {
@@ -134,114 +161,185 @@ __device__ __forceinline__ void nvfp4_pairs(uint32_t w, uint32_t s2, uint32_t (&
 }
 
 // Scales of one stage (and INT4 zero points) as this lane holds them, loaded a
-// stage ahead.  GSH: log2 of the INT4 group, or 4 for NVFP4.
-//  INT4: lane (g, t) holds groups t, t + 4, .. of the stage for rows g, g + 8, as
-//    (bf16 scale << 16) | zero point; a group's value is shuffled from lane t.
-//  NVFP4: the blocks of the lane's own words, 2 j + t / 2: e4m3 bytes, eight a row.
-template <int GSH> struct StageScales {
+// stage ahead and left as loaded until the stage is multiplied.  GSH: log2 of the
+// INT4 group, or 4 for NVFP4; Z: zero points.
+//  INT4: lane (g, t) holds groups t, t + 4, .. of the stage for rows g, g + 8; a
+//    group's values are shuffled from lane t.
+//  NVFP4: all sixteen block scales of the two rows, four words each.
+template <int GSH, bool Z> struct StageScales {
     static constexpr int kGroups = kStageK >> GSH;            // groups of a stage
-    static constexpr int kHold = GSH == 4 ? 2 : (kGroups + 3) / 4;
-    uint32_t v[2][kHold];
+    static constexpr int kHold = GSH == 4 ? 4 : (kGroups + 3) / 4;
+    uint32_t v[2][kHold], z[2][Z ? kHold : 1];
+};
 
-    __device__ __forceinline__ void load(const QMatDev& m, size_t row_base, int row0, int rows, int s, int lane) {
-        const int g = lane >> 2, t = lane & 3, per_row = m.in_dim >> GSH;
+// A lane's part of the loads of a tile's scales, one stage after another.
+template <int GSH, bool Z> struct ScaleLoad {
+    using S = StageScales<GSH, Z>;
+    const uint8_t* sp;     // first value of the lane (INT4: group t of row g; NVFP4: block 0 of row g)
+    const uint8_t* zp;
+    int rows;              // rows of the tile inside the matrix
+    // row: the tile's first row in the stack.
+    __device__ __forceinline__ void start(const QMatDev& m, int64_t row, int rows_left, int s, int lane) {
+        const int g = lane >> 2, t = GSH == 4 ? 0 : lane & 3;
+        const size_t at = (size_t)(row + g) * (m.in_dim >> GSH) + s * S::kGroups + t;
+        sp = reinterpret_cast<const uint8_t*>(m.scale) + (GSH == 4 ? at : 2 * at);
+        if constexpr (Z) zp = m.zero + at;
+        rows = rows_left;
+    }
+    // The next stage, number s; `step` stages on after it.
+    __device__ __forceinline__ void load(S& o, int s, int step, int in_dim, int lane) {
+        const int g = lane >> 2, t = lane & 3, per_row = in_dim >> GSH;
+        const int left = per_row - s * S::kGroups;               // groups of the row from this stage on
+        if constexpr (GSH == 4) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = row0 + g + 8 * h;
-            const size_t at = (row_base + row) * per_row + (size_t)s * kGroups;
-            if constexpr (GSH == 4) {
-                const uint8_t* sp = reinterpret_cast<const uint8_t*>(m.scale) + at;
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t* q8 = sp + (size_t)(8 * h) * per_row;
+                const bool in = g + 8 * h < rows;
+                if ((in_dim & 255) == 0) {   // rows of whole stages: 4-byte aligned words
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t u = 0;
+                    for (int q = 0; q < 4; ++q) o.v[h][q] = in ? __ldg(reinterpret_cast<const uint32_t*>(q8) + q) : 0u;
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // words j = 4 q + i of the stage
-                        const int b = 2 * (4 * q + i) + (t >> 1);
-                        if (row < rows && s * kGroups + b < per_row) u |= (uint32_t)__ldg(sp + b) << (8 * i);
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t u = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (in && 4 * q + i < left) u |= (uint32_t)__ldg(q8 + 4 * q + i) << (8 * i);
+                        o.v[h][q] = u;
                     }
-                    v[h][q] = u;
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < kHold; ++q) {
-                    const int b = t + 4 * q;
-                    uint32_t u = 8u;
-                    if (b < kGroups && row < rows && s * kGroups + b < per_row) {
-                        u = (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(m.scale) + at + b) << 16;
-                        u |= m.zero ? (uint32_t)__ldg(m.zero + at + b) : 8u;
-                    }
-                    v[h][q] = u;
                 }
             }
+            sp += step * S::kGroups;
+        } else {
+            const unsigned short* s16 = reinterpret_cast<const unsigned short*>(sp);
+            if (rows >= 16 && left >= S::kGroups) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < S::kHold; ++q)
+                        if (S::kGroups >= 4 || t < S::kGroups) {
+                            o.v[h][q] = __ldg(s16 + (size_t)(8 * h) * per_row + 4 * q);
+                            if constexpr (Z) o.z[h][q] = __ldg(zp + (size_t)(8 * h) * per_row + 4 * q);
+                        }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < S::kHold; ++q) {
+                        const bool ok = g + 8 * h < rows && t + 4 * q < S::kGroups && t + 4 * q < left;
+                        o.v[h][q] = ok ? (uint32_t)__ldg(s16 + (size_t)(8 * h) * per_row + 4 * q) : 0u;
+                        if constexpr (Z) o.z[h][q] = ok ? (uint32_t)__ldg(zp + (size_t)(8 * h) * per_row + 4 * q) : 8u;
+                    }
+            }
+            sp += step * (2 * S::kGroups);
+            if constexpr (Z) zp += step * S::kGroups;
         }
     }
 };
 
-// One stage of one matrix: acc[NT] += (16 rows x 256 codes at st) x (256 elements
-// of each of 8 NT tokens).  xs: the chunk of this stage and lane, token row g (row
-// stride xstride bytes); ntok: tokens whose rows exist (the others are zero).
-template <int GSH, bool BF, int NT>
-__device__ __forceinline__ void mma_stage(const uint8_t* st, const uint8_t* xs, int xstride, int ntok,
-                                          const StageScales<GSH>& sc, float (&acc)[NT][4], int lane) {
+// What a warp's lanes read of the vectors, as offsets from the block's shared
+// memory: chunk t of tokens g (and g + 8).  Past the last token a lane reads the
+// last one's row again: its column of the result is not used.
+template <int NT> struct XView {
+    uint32_t at[NT];
+    __device__ __forceinline__ void start(uint32_t x0, int xstride, int ntok, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int q = 0; q < NT; ++q) at[q] = x0 + min(8 * q + g, ntok - 1) * xstride + t * 16;
+    }
+};
+
+// One stage of one matrix: acc[NT] += (16 rows x 256 codes at offset st) x (256
+// elements of each of 8 NT tokens, stage s of the view).
+template <int GSH, bool Z, bool BF, int NT>
+__device__ __forceinline__ void mma_stage(const uint8_t* sm, uint32_t st, const XView<NT>& x, int s,
+                                          const StageScales<GSH, Z>& sc, float (&acc)[NT][4], int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const uint8_t* wp = st + g * 128 + 4 * t;
+    const uint32_t w_at = st + g * 128 + (g << 4) + 4 * t;
+    uint32_t xa[NT];
+#pragma unroll
+    for (int q = 0; q < NT; ++q) xa[q] = x.at[q] + (uint32_t)s * (2 * kStageK);
     float d[NT][4];
-    uint32_t zz[2] = {0u, 0u};
-    float fs[2] = {0.f, 0.f};
+    uint32_t zz[2] = {kZeroBase<BF> + 0x00080008u, kZeroBase<BF> + 0x00080008u}, z64[2] = {zero64(zz[0]), zero64(zz[1])};
+    // Rows g and g + 8 of each held group in one word.
+    constexpr int kHold = StageScales<GSH, Z>::kHold;
+    uint32_t ps[kHold], pz[kHold];
+    if constexpr (GSH != 4) {
+#pragma unroll
+        for (int q = 0; q < kHold; ++q) {
+            ps[q] = __byte_perm(sc.v[0][q], sc.v[1][q], 0x5410);
+            if constexpr (Z) pz[q] = __byte_perm(sc.z[0][q], sc.z[1][q], 0x5410) + kZeroBase<BF>;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wp + ((j ^ g) << 4));
-        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wp + 1024 + ((j ^ g) << 4));
+        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(sm + (w_at ^ (uint32_t)(j << 4)));
+        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(sm + (w_at ^ (uint32_t)(j << 4)) + 1024);
         uint4 b[NT];
 #pragma unroll
-        for (int q = 0; q < NT; ++q) {
-            b[q] = make_uint4(0u, 0u, 0u, 0u);
-            if (8 * q + g < ntok) b[q] = *reinterpret_cast<const uint4*>(xs + (size_t)(8 * q) * xstride + j * 64);
-        }
+        for (int q = 0; q < NT; ++q) b[q] = *reinterpret_cast<const uint4*>(sm + xa[q] + j * 64);
         uint32_t p0[4], p1[4];
         if constexpr (GSH == 4) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t by = (sc.v[h][j >> 2] >> (8 * (j & 3))) & 0xffu;
+                // Block 2 j + t / 2: byte 2 (j & 1) + t / 2 of word j / 2, twice.
+                const uint32_t by = __byte_perm(sc.v[h][j >> 1], 0u, (2 * (j & 1) + (t >> 1)) * 0x11);
                 uint32_t s2;
-                asm("{ .reg .b16 c; cvt.u16.u32 c, %1; cvt.rn.f16x2.e4m3x2 %0, c; }" : "=r"(s2) : "r"(by * 0x101u));
+                asm("{ .reg .b16 c; cvt.u16.u32 c, %1; cvt.rn.f16x2.e4m3x2 %0, c; }" : "=r"(s2) : "r"(by));
                 if (h == 0) nvfp4_pairs(w0, s2, p0);
                 else nvfp4_pairs(w1, s2, p1);
             }
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
-                mma16816<BF>(acc[q], p0[0], p1[0], p0[1], p1[1], b[q].x, b[q].y);
-                mma16816<BF>(acc[q], p0[2], p1[2], p0[3], p1[3], b[q].z, b[q].w);
+                mma16816<BF, false>(acc[q], p0[0], p1[0], p0[1], p1[1], b[q].x, b[q].y);
+                mma16816<BF, false>(acc[q], p0[2], p1[2], p0[3], p1[3], b[q].z, b[q].w);
             }
         } else {
             constexpr int kPer = (1 << GSH) / 32;   // steps of a group
-            if (j % kPer == 0) {
-                const int grp = j / kPer;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t u = __shfl_sync(0xffffffffu, sc.v[h][grp / 4], (lane & 28) | (grp & 3));
-                    fs[h] = __uint_as_float(u & 0xffff0000u);
-                    zz[h] = zero_pair<BF>(u & 0xffu);
+            const int grp = j / kPer, from = (lane & 28) | (grp & 3);
+            if constexpr (Z) {
+                if (j % kPer == 0) {
+                    const uint32_t u = __shfl_sync(0xffffffffu, pz[grp / 4], from);
+                    zz[0] = __byte_perm(u, 0u, 0x1010);
+                    zz[1] = __byte_perm(u, 0u, 0x3232);
+                    if constexpr (!BF) {
+                        z64[0] = zero64(zz[0]);
+                        z64[1] = zero64(zz[1]);
+                    }
                 }
-#pragma unroll
-                for (int q = 0; q < NT; ++q)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) d[q][i] = 0.f;
             }
-            int4_pairs<BF>(w0, zz[0], p0);
-            int4_pairs<BF>(w1, zz[1], p1);
+            int4_pairs<BF>(w0, zz[0], z64[0], p0);
+            int4_pairs<BF>(w1, zz[1], z64[1], p1);
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
-                mma16816<BF>(d[q], p0[0], p1[0], p0[1], p1[1], b[q].x, b[q].y);
-                mma16816<BF>(d[q], p0[2], p1[2], p0[3], p1[3], b[q].z, b[q].w);
+                if (j % kPer == 0) mma16816<BF, true>(d[q], p0[0], p1[0], p0[1], p1[1], b[q].x, b[q].y);
+                else mma16816<BF, false>(d[q], p0[0], p1[0], p0[1], p1[1], b[q].x, b[q].y);
+                mma16816<BF, false>(d[q], p0[2], p1[2], p0[3], p1[3], b[q].z, b[q].w);
             }
-            if (j % kPer == kPer - 1)
+            if (j % kPer == kPer - 1) {
+                const uint32_t u = __shfl_sync(0xffffffffu, ps[grp / 4], from);
+                const float fs[2] = {__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)};
 #pragma unroll
                 for (int q = 0; q < NT; ++q)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[q][i] = fmaf(fs[i >> 1], d[q][i], acc[q][i]);
+            }
         }
     }
+}
+
+// Bytes between token rows in shared memory: whole stages of 16-bit elements, and
+// 64 bytes so that neighbouring rows' chunks fall into different banks.
+__host__ __device__ inline int x_row_bytes(int K) { return (K + kStageK - 1) / kStageK * (2 * kStageK) + 64; }
+// 2^e as a float, e in [-126, 127].
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// The exponent of the power of two that takes values of magnitude at most amax
+// below 2^15 (0 for zero, infinite or NaN amax).
+__device__ __forceinline__ int f16_shift(float amax) {
+    const int e = (int)(__float_as_uint(amax) >> 23) & 0xff;
+    if (amax == 0.f || e == 255) return 0;
+    return min(126, 14 - (e - 127));
 }
 
 // The eight 16-bit elements of a chunk in the order the fragments take them.
@@ -252,19 +350,32 @@ __device__ __forceinline__ uint4 chunk_order(uint4 u) {
                       __byte_perm(u.y, u.w, 0x7632));
 }
 
-// Bytes between token rows in shared memory: whole stages of 16-bit elements, and
-// 64 bytes so that neighbouring rows' chunks fall into different banks.
-__host__ __device__ inline int x_row_bytes(int K) { return (K + kStageK - 1) / kStageK * (2 * kStageK) + 64; }
-
-// 2^e as a float, e in [-126, 127].
-__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-// The power of two that takes values of magnitude at most amax into f16 with the
-// largest below 2^15 (1 for zero, infinite or NaN amax), as an exponent.
-__device__ __forceinline__ int f16_shift(float amax) {
-    const int e = (int)(__float_as_uint(amax) >> 23) & 0xff;
-    if (amax == 0.f || e == 255) return 0;
-    return min(126, 14 - (e - 127));
+// One bf16 row as f16, scaled by a power of two, by one warp: dst [chunks] (zero
+// past K); returns the factor that scales a result back.
+__device__ __forceinline__ float scaled_row(const uint4* src, int K8, int chunks, uint4* dst, int lane) {
+    float am = 0.f;
+    for (int c = lane; c < K8; c += 32) {
+        float v[8];
+        bf16x8_to_float(src[c], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(v[i]));   // (NaN keeps its column NaN by itself)
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+    const int sh = f16_shift(am);
+    const float f = exp2i(sh);
+    for (int c = lane; c < chunks; c += 32) {
+        float v[8] = {};
+        if (c < K8) bf16x8_to_float(src[c], v);
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 hv = __floats2half2_rn(v[2 * i] * f, v[2 * i + 1] * f);
+            h[i] = *reinterpret_cast<const uint32_t*>(&hv);
+        }
+        dst[c] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    return exp2i(-sh);
 }
 
 }  // namespace q4

@@ -151,11 +151,15 @@ class MoeLayer:
         return out
 
 
-def _on_current_device(t: torch.Tensor) -> None:
-    if not t.is_cuda and not t.is_pinned():
+def _device_of(t: torch.Tensor) -> torch.device:
+    """The current GPU, on which ``t`` is, or to which ``t`` is pinned host memory."""
+    if t.is_cuda:
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+        return t.device
+    if not t.is_pinned():
         raise ValueError("tensors are on the GPU or in pinned host memory")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return torch.device("cuda", torch.cuda.current_device())
 
 
 class MoeTopk:
@@ -183,23 +187,27 @@ class MoeTopk:
         c.norm_topk_prob = 1 if norm_topk_prob else 0
         c.routed_scaling_factor = routed_scaling_factor
         # One configuration for each logits type, so that calls change nothing here.
-        self.c_cfg, self.bias = {}, bias
+        self.num_experts, self.top_k, self.bias = num_experts, top_k, bias
+        self.c_cfg = {}
         for dtype, code in _TYPE.items():
             self.c_cfg[dtype] = B.moe_topk_config_t.from_buffer_copy(c)
             self.c_cfg[dtype].logits_type = code
+        self._bias = None if bias is None else bias.data_ptr()
+        self._topk = B.entry("moe_topk")
 
     def forward(self, logits: torch.Tensor, idx=None, w=None, stream=None):
-        c = self.c_cfg[logits.dtype]
-        if logits.dim() != 2 or logits.shape[1] != c.num_experts or (c.num_experts > 1 and logits.stride(1) != 1):
+        cfg = self.c_cfg[logits.dtype]
+        E, k = self.num_experts, self.top_k
+        if logits.dim() != 2 or logits.size(1) != E or (E > 1 and logits.stride(1) != 1):
             raise ValueError("logits are [n, num_experts] with contiguous rows")
-        _on_current_device(logits)
-        n = logits.shape[0]
+        dev = _device_of(logits)
+        n = logits.size(0)
         if idx is None:
-            idx = torch.empty(n, c.top_k, dtype=torch.int32, device="cuda")
+            idx = torch.empty((n, k), dtype=torch.int32, device=dev)
         if w is None:
-            w = torch.empty(n, c.top_k, dtype=torch.float32, device="cuda")
-        stride = logits.stride(0) if n > 1 else c.num_experts
-        B.check(B.moe_topk(c, logits, stride, self.bias, n, idx, w, stream))
+            w = torch.empty((n, k), dtype=torch.float32, device=dev)
+        B.check(self._topk(cfg, logits.data_ptr(), logits.stride(0) if n > 1 else E, self._bias, n,
+                           idx.data_ptr(), w.data_ptr(), B._stream(stream)))
         return idx, w
 
 
@@ -228,20 +236,26 @@ class MoeMatvec:
             self.c_cfg[dtype] = B.moe_matvec_config_t.from_buffer_copy(c)
             self.c_cfg[dtype].x_type = _TYPE[dtype]
         self.weights, self.bias, self.out_dtype = q, bias, out_dtype
+        self.in_features, self.out_features, self.accumulate = in_f, out_f, accumulate
+        self._bias = None if bias is None else bias.data_ptr()
+        self._matvec = B.entry("moe_matvec")
 
     def forward(self, x: torch.Tensor, out=None, stream=None):
-        c = self.c_cfg[x.dtype]
-        if x.dim() != 2 or x.shape[1] != c.in_features or x.stride(1) != 1:
+        cfg = self.c_cfg[x.dtype]
+        K, O = self.in_features, self.out_features
+        if x.dim() != 2 or x.size(1) != K or x.stride(1) != 1:
             raise ValueError("x is [n, in] with contiguous rows")
-        _on_current_device(x)
-        n = x.shape[0]
+        dev = _device_of(x)
+        n = x.size(0)
         if out is None:
-            if c.accumulate:
+            if self.accumulate:
                 raise ValueError("accumulate needs out")
-            out = torch.empty(n, c.out_features, dtype=self.out_dtype, device="cuda")
-        elif (out.shape != (n, c.out_features) or out.dtype != self.out_dtype
-              or (c.out_features > 1 and out.stride(1) != 1)):
-            raise ValueError("out is [n, out] of out_dtype with contiguous rows")
-        B.check(B.moe_matvec(c, self.c_w, self.bias, x, x.stride(0) if n > 1 else c.in_features, n, out,
-                             out.stride(0) if n > 1 else c.out_features, stream))
+            out = torch.empty((n, O), dtype=self.out_dtype, device=dev)
+            ostride = O
+        else:
+            if out.shape != (n, O) or out.dtype != self.out_dtype or (O > 1 and out.stride(1) != 1):
+                raise ValueError("out is [n, out] of out_dtype with contiguous rows")
+            ostride = out.stride(0) if n > 1 else O
+        B.check(self._matvec(cfg, self.c_w, self._bias, x.data_ptr(), x.stride(0) if n > 1 else K, n,
+                             out.data_ptr(), ostride, B._stream(stream)))
         return out
