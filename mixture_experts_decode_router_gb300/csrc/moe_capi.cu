@@ -214,9 +214,28 @@ constexpr int kTokenMajorMaxN = 3;
 // and a router CTA still on an SM leaves room for one.
 static bool early_dependents(int32_t n, int sms) { return n <= sms; }
 
+// INT4 under AUTO: the streaming kernels while the experts have at most
+// kStreamMaxAvg tokens on average, the grouped tensor-core path above.
+constexpr int kStreamMaxAvg = 16;
+constexpr int kPathStream = 3;
+
 // The multi-kernel path a call of n tokens takes.
 static int effective_path(const moe_config_t* c, int32_t n) {
+    if (c->path == MOE_PATH_AUTO && is_int4(c->expert_fmt) && (int64_t)n * c->top_k <= (int64_t)kStreamMaxAvg * c->num_experts &&
+        (n > 1 || q4_n1_fits(c->hidden, c->top_k, c->inter, c->shared_inter)))
+        return kPathStream;
     return c->path == MOE_PATH_AUTO ? (n <= kTokenMajorMaxN ? MOE_PATH_TOKEN_MAJOR : MOE_PATH_GROUPED) : c->path;
+}
+
+// Whether a call of n tokens takes the tensor-core router.
+static bool tc_router_path(const moe_config_t* c, int32_t n) {
+    const int path = effective_path(c, n);
+    return path == MOE_PATH_GROUPED || (path == kPathStream && n > kTokenMajorMaxN);
+}
+
+// Routes of a segment (launch_group).
+static int seg_tile(const moe_config_t* c, int32_t n) {
+    return effective_path(c, n) == kPathStream ? q4_tile(n, c->top_k, c->num_experts) : kTcTokensPerTile;
 }
 
 // Enqueue router + top-k.  Arguments already validated.  `with_group`: the
@@ -241,7 +260,7 @@ static moe_status_t enqueue_route(const moe_config_t* c, const moe_weights_t* w,
     // grouping kernel when it runs and has room, else launched on its own.
     const uint16_t* gate_in_topk = nullptr;
     if ((c->router_fmt == MOE_W_BF16 || c->router_fmt == MOE_W_NVFP4) && x_dev &&
-        effective_path(c, n) == MOE_PATH_GROUPED && router_tc_fits(n, c->num_experts, c->hidden)) {
+        tc_router_path(c, n) && router_tc_fits(n, c->num_experts, c->hidden)) {
         // An NVFP4 router is first expanded to BF16 (exactly); its scale2
         // multiplies the partials.
         float* part = at<float>(ws, L.lgp);
@@ -293,7 +312,7 @@ static moe_status_t enqueue_route(const moe_config_t* c, const moe_weights_t* w,
     }
     if (with_group)
         e = launch_topk_group(lin, ns, n, c->num_experts, c->top_k, c->routing, w->correction_bias, c->norm_topk_prob,
-                              c->routed_scaling_factor, idx, wt, c->expert_begin, c->expert_end,
+                              c->routed_scaling_factor, idx, wt, seg_tile(c, n), c->expert_begin, c->expert_end,
                               at<int32_t>(ws, L.counts), at<int32_t>(ws, L.offsets), at<int32_t>(ws, L.perm),
                               at<int32_t>(ws, L.inv), at<int32_t>(ws, L.active), at<int32_t>(ws, L.segs),
                               at<Ctrl>(ws, L.ctrl), static_cast<const uint16_t*>(x), gate_in_topk,
@@ -398,6 +417,53 @@ static moe_status_t enqueue_grouped(const moe_config_t* c, const moe_weights_t* 
     return MOE_OK;
 }
 
+// The INT4 streaming expert stage (after the grouping kernel; one token: on its own).
+static moe_status_t enqueue_stream(const moe_config_t* c, const moe_weights_t* w, const void* x, int32_t n,
+                                   const int32_t* idx, const float* wt, void* out, void* ws, const WsLayout& L,
+                                   const float* sg_logit, cudaStream_t st, Marks& mk) {
+    const int sms = device_sm_count();
+    const int fmt = c->expert_fmt, H = c->hidden, I = c->inter, S = c->shared_inter, k = c->top_k, eb = c->expert_begin;
+    Q4Params p{};
+    p.x = static_cast<const uint16_t*>(x);
+    p.n = n; p.H = H; p.I = I; p.S = S; p.k = k;
+    p.gate = qdev(fmt, w->gate, I, H, eb);
+    p.up = qdev(fmt, w->up, I, H, eb);
+    p.down = qdev(fmt, w->down, H, I, eb);
+    p.zero = w->gate.zero || w->up.zero || w->down.zero;
+    if (S > 0) {
+        p.sh_gate = qdev(fmt, w->sh_gate, S, H, 0);
+        p.sh_up = qdev(fmt, w->sh_up, S, H, 0);
+        p.sh_down = qdev(fmt, w->sh_down, H, S, 0);
+        p.zero = p.zero || w->sh_gate.zero || w->sh_up.zero || w->sh_down.zero;
+    }
+    p.e_begin = c->expert_begin;
+    p.e_end = c->expert_end;
+    p.segs = at<int32_t>(ws, L.segs);
+    p.perm = at<int32_t>(ws, L.perm);
+    p.ctrl = at<Ctrl>(ws, L.ctrl);
+    p.idx = idx;
+    p.route_w = wt;
+    p.sg_logit = w->shared_gate_w ? sg_logit : nullptr;
+    p.act = at<float>(ws, L.act);
+    p.act_sh = at<float>(ws, L.act_sh);
+    p.y = at<float>(ws, L.y);
+    p.y_sh = at<float>(ws, L.ysh);
+    p.out = static_cast<uint16_t*>(out);
+    p.accumulate = c->accumulate;
+    const int tile = q4_tile(n, k, c->num_experts);
+    if (launch_experts_q4(fmt, p, true, tile, sms, st) != cudaSuccess) return MOE_ERR_CUDA;
+    mk.mark(st);
+    if (launch_experts_q4(fmt, p, false, tile, sms, st) != cudaSuccess) return MOE_ERR_CUDA;
+    mk.mark(st);
+    if (n > 1) {
+        if (launch_combine(p.y, p.y_sh, at<int32_t>(ws, L.inv), n, H, k, S > 0 ? 1 : 0, c->accumulate, p.out,
+                           early_dependents(n, sms), sms, st) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        mk.mark(st);
+    }
+    return MOE_OK;
+}
+
 // Enqueue grouping + experts + blend.  `sg_from_ws`: the shared-gate logit was
 // written to the workspace by enqueue_route of the same call.  `grouped`: so
 // were the routes' grouping by expert (enqueue_route with_group).
@@ -428,8 +494,9 @@ static moe_status_t enqueue_experts(const moe_config_t* c, const moe_weights_t* 
         if (e != cudaSuccess) return MOE_ERR_CUDA;
         xin = xe;
     }
-    if (!grouped) {
-        e = launch_group(idx, n * k, E, c->expert_begin, c->expert_end, at<int32_t>(ws, L.counts),
+    // (One token on the streaming path takes its routes as they are.)
+    if (!grouped && !(path == kPathStream && n == 1)) {
+        e = launch_group(idx, n * k, E, seg_tile(c, n), c->expert_begin, c->expert_end, at<int32_t>(ws, L.counts),
                          at<int32_t>(ws, L.offsets), at<int32_t>(ws, L.perm), at<int32_t>(ws, L.inv),
                          at<int32_t>(ws, L.active), at<int32_t>(ws, L.segs), at<Ctrl>(ws, L.ctrl), st);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
@@ -438,6 +505,8 @@ static moe_status_t enqueue_experts(const moe_config_t* c, const moe_weights_t* 
 
     if (path == MOE_PATH_GROUPED)
         return enqueue_grouped(c, w, x, n, wt, out, ws, L, sg_logit, st, mk);
+
+    if (path == kPathStream) return enqueue_stream(c, w, xin, n, idx, wt, out, ws, L, sg_logit, st, mk);
 
     const int eb = c->expert_begin;
     GateUpParams gu{};
@@ -538,7 +607,8 @@ moe_status_t moe_experts(const moe_config_t* cfg_in, const moe_weights_t* wts, c
     const int x_res = residency(x);
     if (x_res < 0 || residency(out) < 0) return MOE_ERR_HOST_MEMORY;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (x_res == 1 && n > 1 && (s = stage_x(cfg, x, n, ws, L, st)) != MOE_OK) return s;
+    if (x_res == 1 && (n > 1 || effective_path(cfg, n) == kPathStream) && (s = stage_x(cfg, x, n, ws, L, st)) != MOE_OK)
+        return s;
     Marks mk;
     return enqueue_experts(cfg, wts, x, n, idx, w, out, ws, L, false, false, st, mk);
 }
@@ -566,7 +636,8 @@ static moe_status_t forward_impl(const moe_config_t* cfg_in, const moe_weights_t
     int32_t* idx_p = idx ? idx : at<int32_t>(ws, L.idx);
     float* w_p = w ? w : at<float>(ws, L.w);
     mk.mark(st);
-    if (n == 1 && cfg->path != MOE_PATH_GROUPED && cfg->router_fmt == MOE_W_BF16 && routing_plain(cfg->routing)) {
+    if (n == 1 && cfg->path != MOE_PATH_GROUPED && cfg->router_fmt == MOE_W_BF16 && routing_plain(cfg->routing) &&
+        effective_path(cfg, n) != kPathStream) {
         // One token: the whole layer in one cooperative launch when its
         // shared-memory plan fits (same arithmetic as the kernels below).
         const int sms = device_sm_count();

@@ -15,7 +15,7 @@
 //   inv[r]      sorted position of route r (-1 for a dropped route)
 //   active[u]   experts with counts > 0, ascending; ctrl->n_active of them
 //   segs[s]     (expert, first sorted position, routes) for runs of at most
-//               kTcTokensPerTile routes of one expert, ascending expert;
+//               `tile` routes of one expert, ascending expert;
 //               ctrl->n_rsegs of them (the tiles of the grouped path)
 #include <algorithm>
 #include <mutex>
@@ -41,7 +41,7 @@ inline int seg_warps(int E, int nk) {
 // active, segs and the control block's totals; tot[e] becomes the first sorted
 // position of expert e.  Called by every thread of the block; ends with a
 // barrier.
-__device__ __forceinline__ void group_scan_experts(int32_t* tot, int E, int32_t* __restrict__ counts,
+__device__ __forceinline__ void group_scan_experts(int32_t* tot, int E, int tile, int32_t* __restrict__ counts,
                                                    int32_t* __restrict__ offsets, int32_t* __restrict__ active,
                                                    int32_t* __restrict__ segs, Ctrl* __restrict__ ctrl) {
     __shared__ int32_t warp_sums[3][32];
@@ -51,7 +51,7 @@ __device__ __forceinline__ void group_scan_experts(int32_t* tot, int E, int32_t*
     // (of ceil(counts / kTcTokensPerTile)).
     const int c = (tid < E) ? tot[tid] : 0;
     const int a = (tid < E && c > 0) ? 1 : 0;
-    const int g = (c + kTcTokensPerTile - 1) / kTcTokensPerTile;
+    const int g = (c + tile - 1) / tile;
     int sc = c, sa = a, sg = g;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -90,8 +90,8 @@ __device__ __forceinline__ void group_scan_experts(int32_t* tot, int E, int32_t*
         for (int b = 0; b < g; ++b) {
             int32_t* sgp = segs + 3 * (excl_g + b);
             sgp[0] = tid;
-            sgp[1] = excl_c + b * kTcTokensPerTile;
-            sgp[2] = min(kTcTokensPerTile, c - b * kTcTokensPerTile);
+            sgp[1] = excl_c + b * tile;
+            sgp[2] = min(tile, c - b * tile);
         }
     }
     if (tid == 0) {
@@ -104,7 +104,7 @@ __device__ __forceinline__ void group_scan_experts(int32_t* tot, int E, int32_t*
 
 // The grouping of all n*k routes by one block of kGroupThreads threads, sw of
 // whose warps own route segments.  sm: (sw + 1) * E ints of shared memory.
-__device__ __forceinline__ void group_block(const int32_t* __restrict__ idx, int nk, int E, int e_begin, int e_end,
+__device__ __forceinline__ void group_block(const int32_t* __restrict__ idx, int nk, int E, int tile, int e_begin, int e_end,
                                             int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                             int32_t* __restrict__ perm, int32_t* __restrict__ inv,
                                             int32_t* __restrict__ active, int32_t* __restrict__ segs,
@@ -146,7 +146,7 @@ __device__ __forceinline__ void group_block(const int32_t* __restrict__ idx, int
     }
     __syncthreads();
 
-    group_scan_experts(tot, E, counts, offsets, active, segs, ctrl);
+    group_scan_experts(tot, E, tile, counts, offsets, active, segs, ctrl);
 
     // Stable scatter: each segment warp walks its routes in order (loaded
     // kIdxBatch rounds of 32 at a time).
@@ -195,8 +195,8 @@ __device__ __forceinline__ void group_block(const int32_t* __restrict__ idx, int
 constexpr int kBitsRoutes = 8 * kGroupThreads;   // routes a thread holds in registers: 8
 constexpr int kBitsWords = 8192;                 // E * W words of bitmap at most (32 KB)
 
-__device__ __forceinline__ void group_block_bits(const int32_t* __restrict__ idx, int n, int k, int E, int e_begin,
-                                                 int e_end, int32_t* __restrict__ counts,
+__device__ __forceinline__ void group_block_bits(const int32_t* __restrict__ idx, int n, int k, int E, int tile,
+                                                 int e_begin, int e_end, int32_t* __restrict__ counts,
                                                  int32_t* __restrict__ offsets, int32_t* __restrict__ perm,
                                                  int32_t* __restrict__ inv, int32_t* __restrict__ active,
                                                  int32_t* __restrict__ segs, Ctrl* __restrict__ ctrl, int32_t* sm) {
@@ -232,7 +232,7 @@ __device__ __forceinline__ void group_block_bits(const int32_t* __restrict__ idx
         tot[e] = run;
     }
     __syncthreads();
-    group_scan_experts(tot, E, counts, offsets, active, segs, ctrl);
+    group_scan_experts(tot, E, tile, counts, offsets, active, segs, ctrl);
 #pragma unroll
     for (int u = 0; u < kBitsRoutes / kGroupThreads; ++u) {
         const int r = tid + nt * u;
@@ -254,13 +254,13 @@ inline bool group_bits_fits(int n, int k, int E) {
 }
 
 __global__ void __launch_bounds__(kGroupThreads)
-group_kernel(const int32_t* __restrict__ idx, int nk, int E, int e_begin, int e_end,
+group_kernel(const int32_t* __restrict__ idx, int nk, int E, int tile, int e_begin, int e_end,
              int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
              int32_t* __restrict__ perm, int32_t* __restrict__ inv, int32_t* __restrict__ active,
              int32_t* __restrict__ segs, Ctrl* __restrict__ ctrl, int sw) {
     extern __shared__ int32_t sm[];
     pdl_wait();
-    group_block(idx, nk, E, e_begin, e_end, counts, offsets, perm, inv, active, segs, ctrl, sm, sw);
+    group_block(idx, nk, E, tile, e_begin, e_end, counts, offsets, perm, inv, active, segs, ctrl, sm, sw);
     pdl_trigger();
 }
 
@@ -276,7 +276,7 @@ template <int kMinBlocks>
 __global__ void __launch_bounds__(kGroupThreads, kMinBlocks)
 topk_group_kernel(const float* __restrict__ logits, int ns, int n, int E, int k, int routing,
                   const float* __restrict__ bias, int norm, float scale, int32_t* idx_out,
-                  float* __restrict__ w_out, int e_begin, int e_end, int32_t* __restrict__ counts,
+                  float* __restrict__ w_out, int tile, int e_begin, int e_end, int32_t* __restrict__ counts,
                   int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ inv,
                   int32_t* __restrict__ active, int32_t* __restrict__ segs, Ctrl* __restrict__ ctrl, int sw,
                   int bits, const uint16_t* __restrict__ x, const uint16_t* __restrict__ gw,
@@ -355,21 +355,21 @@ topk_group_kernel(const float* __restrict__ logits, int ns, int n, int E, int k,
     __syncthreads();
     if (s_last) {
         if (bits)
-            group_block_bits(idx_out, n, k, E, e_begin, e_end, counts, offsets, perm, inv, active, segs, ctrl, gsm);
+            group_block_bits(idx_out, n, k, E, tile, e_begin, e_end, counts, offsets, perm, inv, active, segs, ctrl, gsm);
         else
-            group_block(idx_out, n * k, E, e_begin, e_end, counts, offsets, perm, inv, active, segs, ctrl, gsm, sw);
+            group_block(idx_out, n * k, E, tile, e_begin, e_end, counts, offsets, perm, inv, active, segs, ctrl, gsm, sw);
         if (tid == 0) ctrl->routed = 0;
     }
     pdl_trigger();
 }
 
-cudaError_t launch_group(const int32_t* idx, int nk, int E, int e_begin, int e_end, int32_t* counts,
+cudaError_t launch_group(const int32_t* idx, int nk, int E, int tile, int e_begin, int e_end, int32_t* counts,
                          int32_t* offsets, int32_t* perm, int32_t* inv, int32_t* active, int32_t* segs,
                          Ctrl* ctrl, cudaStream_t st) {
     const int sw = seg_warps(E, nk);
     const size_t smem = sizeof(int32_t) * (size_t)(sw + 1) * E;
     // (sw + 1) * E ints <= 36 KB for E <= 1024: under the 48 KB default.
-    launch_pdl(group_kernel, 1, kGroupThreads, smem, st, idx, nk, E, e_begin, e_end, counts, offsets, perm, inv,
+    launch_pdl(group_kernel, 1, kGroupThreads, smem, st, idx, nk, E, tile, e_begin, e_end, counts, offsets, perm, inv,
                active, segs, ctrl, sw);
     return cudaGetLastError();
 }
@@ -382,7 +382,7 @@ bool topk_group_gate_fits(int E, int H) {
 }
 
 cudaError_t launch_topk_group(const float* logits, int ns, int n, int E, int k, int routing, const float* bias, int norm,
-                              float scale, int32_t* idx, float* w, int e_begin, int e_end, int32_t* counts,
+                              float scale, int32_t* idx, float* w, int tile, int e_begin, int e_end, int32_t* counts,
                               int32_t* offsets, int32_t* perm, int32_t* inv, int32_t* active, int32_t* segs,
                               Ctrl* ctrl, const uint16_t* x, const uint16_t* gw, float* sg_logit, int H, bool early,
                               int num_sms, cudaStream_t st) {
@@ -411,7 +411,7 @@ cudaError_t launch_topk_group(const float* logits, int ns, int n, int E, int k, 
         }
     }
     launch_pdl(kern, n, kGroupThreads, smem, st, logits, ns, n, E, k, routing, bias, norm, scale, idx, w,
-               e_begin, e_end, counts, offsets, perm, inv, active, segs, ctrl, sw, bits ? 1 : 0, x, gw, sg_logit, H,
+               tile, e_begin, e_end, counts, offsets, perm, inv, active, segs, ctrl, sw, bits ? 1 : 0, x, gw, sg_logit, H,
                sgx_off, early ? 1 : 0);
     return cudaGetLastError();
 }

@@ -16,6 +16,17 @@ constexpr int kWarp = 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 
+// The INT4 formats share their kernels; the group size is a run-time shift.
+constexpr int kFmtInt4 = MOE_W_INT4_G32;
+__host__ __device__ constexpr bool is_int4(int fmt) { return fmt >= MOE_W_INT4_G32 && fmt <= MOE_W_INT4_G128; }
+__host__ __device__ constexpr int int4_gshift(int fmt) { return 5 + (fmt - MOE_W_INT4_G32); }
+// The kernel instance of a format.
+constexpr int fmt_kind(int fmt) { return is_int4(fmt) ? kFmtInt4 : fmt; }
+// Bytes of one row of `in` codes.
+__host__ __device__ constexpr size_t fmt_row_bytes(int fmt, int in) {
+    return fmt == MOE_W_BF16 ? (size_t)in * 2 : (fmt == MOE_W_FP8_B128 ? (size_t)in : (size_t)in / 2);
+}
+
 // ----------------------------------------------------------------------------
 // Workspace layout.  The control block sits at offset 0 for every n; the other
 // regions follow, each 256-byte aligned, sized for the call's n.
@@ -84,11 +95,17 @@ struct WsLayout {
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// Upper bound of the routed segments (<= kTcTokensPerTile routes of one expert):
-// sum_e ceil(c_e / T) <= (n*k)/T + min(E, n*k).
-inline int64_t grouped_segs_bound(int64_t n, int64_t k, int64_t E) {
+// Routes of a segment on the INT4 streaming path (moe_experts_q4.cu): 8 while the
+// experts have few tokens on average, else 16.  A segment of up to 8 runs with three
+// blocks an SM, one of up to 16 with two, and a longer one reads its expert's
+// matrices again.
+inline int q4_tile(int64_t n, int64_t k, int64_t E) { return n * k <= 4 * E ? 8 : 16; }
+
+// Upper bound of the routed segments (<= T routes of one expert, T the fewest that
+// the format's kernels take): sum_e ceil(c_e / T) <= (n*k)/T + min(E, n*k).
+inline int64_t grouped_segs_bound(int64_t n, int64_t k, int64_t E, int fmt) {
     const int64_t nk = n * k;
-    return nk / kTcTokensPerTile + (nk < E ? nk : E) + 1;
+    return nk / (is_int4(fmt) ? 8 : kTcTokensPerTile) + (nk < E ? nk : E) + 1;
 }
 
 inline WsLayout ws_layout(const moe_config_t& c, int64_t n) {
@@ -109,7 +126,7 @@ inline WsLayout ws_layout(const moe_config_t& c, int64_t n) {
     L.act_sh = take(sizeof(float) * n * (S > 0 ? S : 1));
     // Grouped tensor-core path.
     L.inv = take(sizeof(int32_t) * n * k);                       // route -> sorted position
-    L.segs = take(sizeof(int32_t) * 3 * grouped_segs_bound(n, k, E));
+    L.segs = take(sizeof(int32_t) * 3 * grouped_segs_bound(n, k, E, c.expert_fmt));
     L.xs = take(sizeof(uint16_t) * n * k * H);                   // expert-sorted activations
     L.xh = take(sizeof(uint16_t) * n * H);                       // copy of x for the shared expert (f16 / bf16)
     L.as = take(sizeof(uint16_t) * n * k * I);                   // SiLU(g)*u, sorted rows
@@ -163,17 +180,6 @@ __host__ __device__ inline bool mode_has_bias(int mode) {
 }
 __host__ __device__ inline bool mode_sigmoid(int mode) {
     return mode == MOE_ROUTE_SIGMOID_BIAS || mode == MOE_ROUTE_SIGMOID;
-}
-
-// The INT4 formats share their kernels; the group size is a run-time shift.
-constexpr int kFmtInt4 = MOE_W_INT4_G32;
-__host__ __device__ constexpr bool is_int4(int fmt) { return fmt >= MOE_W_INT4_G32 && fmt <= MOE_W_INT4_G128; }
-__host__ __device__ constexpr int int4_gshift(int fmt) { return 5 + (fmt - MOE_W_INT4_G32); }
-// The kernel instance of a format.
-constexpr int fmt_kind(int fmt) { return is_int4(fmt) ? kFmtInt4 : fmt; }
-// Bytes of one row of `in` codes.
-__host__ __device__ constexpr size_t fmt_row_bytes(int fmt, int in) {
-    return fmt == MOE_W_BF16 ? (size_t)in * 2 : (fmt == MOE_W_FP8_B128 ? (size_t)in : (size_t)in / 2);
 }
 
 // ----------------------------------------------------------------------------

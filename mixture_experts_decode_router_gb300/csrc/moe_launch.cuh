@@ -34,6 +34,29 @@ struct DownParams {
     uint16_t* out;
 };
 
+// INT4 streaming path (moe_experts_q4.cu).
+struct Q4Params {
+    const uint16_t* x;       // [n, H] the experts' input
+    int n, H, I, S, k;
+    QMatDev gate, up, down, sh_gate, sh_up, sh_down;
+    bool zero;               // any matrix has zero points
+    int e_begin, e_end;      // experts held here
+    const int32_t* segs;     // [n_rsegs][3] (n > 1)
+    const int32_t* perm;     // sorted position -> route id (n > 1)
+    const Ctrl* ctrl;
+    const int32_t* idx;      // [k] (one token)
+    const float* route_w;    // [n*k]
+    const float* sg_logit;   // shared gate logits or NULL
+    float* act;              // [n*k, I] by sorted position (one token: by slot)
+    float* act_sh;           // [n, S]
+    float* y;                // [n*k, H] weighted rows (n > 1)
+    float* y_sh;             // [n, H]
+    uint16_t* out;           // [H] (one token)
+    int accumulate;
+};
+bool q4_n1_fits(int H, int k, int I, int S);   // whether the one-token kernels' shared memory suffices
+cudaError_t launch_experts_q4(int fmt, const Q4Params& p, bool gate_up, int tile, int num_sms, cudaStream_t st);
+
 // Grouped tensor-core path (moe_grouped_tc.cu).
 struct TcMaps {
     CUtensorMap w[2];    // routed weights: (gate, up) or (down)
@@ -160,11 +183,12 @@ struct MatvecParams {
 bool matvec_fits(int K);   // whether a row of x fits beside the kernel's rings
 cudaError_t launch_matvec(int fmt, int x_type, const MatvecParams& p, int num_sms, cudaStream_t st);
 
-cudaError_t launch_group(const int32_t* idx, int nk, int E, int e_begin, int e_end, int32_t* counts,
+// tile: routes of a segment at most.
+cudaError_t launch_group(const int32_t* idx, int nk, int E, int tile, int e_begin, int e_end, int32_t* counts,
                          int32_t* offsets, int32_t* perm, int32_t* inv, int32_t* active, int32_t* segs,
                          Ctrl* ctrl, cudaStream_t st);
 cudaError_t launch_topk_group(const float* logits, int ns, int n, int E, int k, int routing, const float* bias,
-                              int norm, float scale, int32_t* idx, float* w, int e_begin, int e_end, int32_t* counts,
+                              int norm, float scale, int32_t* idx, float* w, int tile, int e_begin, int e_end, int32_t* counts,
                               int32_t* offsets, int32_t* perm, int32_t* inv, int32_t* active, int32_t* segs,
                               Ctrl* ctrl, const uint16_t* x, const uint16_t* gw, float* sg_logit, int H, bool early,
                               int num_sms, cudaStream_t st);

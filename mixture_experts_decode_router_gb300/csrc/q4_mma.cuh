@@ -177,13 +177,17 @@ template <int GSH, bool Z> struct ScaleLoad {
     using S = StageScales<GSH, Z>;
     const uint8_t* sp;     // first value of the lane (INT4: group t of row g; NVFP4: block 0 of row g)
     const uint8_t* zp;
+    bool has_zero;         // (Z kernels take matrices without zero points too)
     int rows;              // rows of the tile inside the matrix
     // row: the tile's first row in the stack.
     __device__ __forceinline__ void start(const QMatDev& m, int64_t row, int rows_left, int s, int lane) {
         const int g = lane >> 2, t = GSH == 4 ? 0 : lane & 3;
         const size_t at = (size_t)(row + g) * (m.in_dim >> GSH) + s * S::kGroups + t;
         sp = reinterpret_cast<const uint8_t*>(m.scale) + (GSH == 4 ? at : 2 * at);
-        if constexpr (Z) zp = m.zero + at;
+        if constexpr (Z) {
+            has_zero = m.zero != nullptr;
+            zp = m.zero + (has_zero ? at : 0);
+        }
         rows = rows_left;
     }
     // The next stage, number s; `step` stages on after it.
@@ -219,7 +223,7 @@ template <int GSH, bool Z> struct ScaleLoad {
                     for (int q = 0; q < S::kHold; ++q)
                         if (S::kGroups >= 4 || t < S::kGroups) {
                             o.v[h][q] = __ldg(s16 + (size_t)(8 * h) * per_row + 4 * q);
-                            if constexpr (Z) o.z[h][q] = __ldg(zp + (size_t)(8 * h) * per_row + 4 * q);
+                            if constexpr (Z) o.z[h][q] = has_zero ? __ldg(zp + (size_t)(8 * h) * per_row + 4 * q) : 8;
                         }
             } else {
 #pragma unroll
@@ -228,11 +232,11 @@ template <int GSH, bool Z> struct ScaleLoad {
                     for (int q = 0; q < S::kHold; ++q) {
                         const bool ok = g + 8 * h < rows && t + 4 * q < S::kGroups && t + 4 * q < left;
                         o.v[h][q] = ok ? (uint32_t)__ldg(s16 + (size_t)(8 * h) * per_row + 4 * q) : 0u;
-                        if constexpr (Z) o.z[h][q] = ok ? (uint32_t)__ldg(zp + (size_t)(8 * h) * per_row + 4 * q) : 8u;
+                        if constexpr (Z) o.z[h][q] = ok && has_zero ? (uint32_t)__ldg(zp + (size_t)(8 * h) * per_row + 4 * q) : 8u;
                     }
             }
             sp += step * (2 * S::kGroups);
-            if constexpr (Z) zp += step * S::kGroups;
+            if constexpr (Z) if (has_zero) zp += step * S::kGroups;
         }
     }
 };
