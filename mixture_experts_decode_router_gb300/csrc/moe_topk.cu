@@ -18,6 +18,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <climits>
 #include <mutex>
 
 #include "moe_launch.cuh"
@@ -27,6 +28,7 @@ namespace moe {
 namespace {
 
 constexpr int kRowWarps = 4;   // rows per block
+constexpr int kMinBlocks = 6;  // blocks of an SM (256 experts and fewer)
 
 struct TopkParams {
     const void* logits;
@@ -55,65 +57,84 @@ __device__ __forceinline__ float load_logit(const TopkParams& p, int64_t t, int 
     return v;
 }
 
-// The k selected experts of a row from its logits sl [E]: lane j < k returns the
-// expert of slot j.  sc: E doubles of scratch.  Group g's score by lane g.
+// A double as a signed integer of the same order (-0 as +0); NaN as the lowest.
+__device__ __forceinline__ long long ordered64(double v) {
+    const long long q = __double_as_longlong(v + 0.0);
+    return v != v ? LLONG_MIN : q ^ (long long)((unsigned long long)(q >> 63) >> 1);
+}
+
+// The k selected experts of a row from its logits sl [E], every score in 64 bits:
+// lane j < k returns the expert of slot j.  sc: E 64-bit words of scratch.
 __device__ __noinline__ int select_exact(const TopkParams& p, const float* sl, double* sc, int lane) {
     const bool biased = mode_has_bias(p.r.mode), sig = mode_sigmoid(p.r.mode);
+    long long* key = reinterpret_cast<long long*>(sc);   // the scores, as integers of their order
     double m = 0., z = 1.;
-    if (!sig && (biased || p.r.top2)) {
-        m = -INFINITY;
-        for (int e = lane; e < p.E; e += 32) m = fmax(m, (double)sl[e]);
-        for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (!sig && (biased || (p.r.groups > 1 && p.r.top2))) {
+        float mf = -INFINITY;
+        for (int e = lane; e < p.E; e += 32) mf = fmaxf(mf, sl[e]);
+        for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xffffffffu, mf, o));
+        m = mf;
         z = 0.;
         for (int e = lane; e < p.E; e += 32) z += exp((double)sl[e] - m);
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     }
     auto prob = [&](float l) { return sig ? 1. / (1. + exp(-(double)l)) : exp((double)l - m) / z; };
-    auto clean = [](double s) { return s != s ? -(double)INFINITY : s; };   // NaN ranks last
-    for (int e = lane; e < p.E; e += 32) sc[e] = clean(biased ? prob(sl[e]) + p.bias[e] : (double)sl[e]);
-    __syncwarp();
-    uint32_t alive = 0xffffffffu;
     const int size = p.E / p.r.groups;
+    const bool by_p = biased || (p.r.groups > 1 && p.r.top2);
+    uint32_t alive = 0xffffffffu;
     if (p.r.groups > 1) {
+        // Group scores by p (+ bias), or by the logits.
+        for (int e = lane; e < p.E; e += 32) {
+            const double v = by_p ? prob(sl[e]) + (biased ? (double)__ldg(p.bias + e) : 0.) : (double)sl[e];
+            sc[e] = v != v ? -(double)INFINITY : v;
+        }
+        __syncwarp();
         double a = -INFINITY, b = -INFINITY;
         if (lane < p.r.groups) {
             for (int i = 0; i < size; ++i) {
-                const int e = lane * size + i;
-                const double s = p.r.top2 && !biased ? clean(prob(sl[e])) : sc[e];
+                const double s = sc[lane * size + i];
                 if (s > a) { b = a; a = s; }
                 else if (s > b) b = s;
             }
             if (p.r.top2 && size > 1) a += b;
         }
+        __syncwarp();
+        const long long mine = ordered64(a);
         int ahead = 0;
         for (int g = 0; g < p.r.groups; ++g) {
-            const double o = __shfl_sync(0xffffffffu, a, g);
-            ahead += (o > a || (o == a && g < lane)) ? 1 : 0;
+            const long long o = __shfl_sync(0xffffffffu, mine, g);
+            ahead += (o > mine || (o == mine && g < lane)) ? 1 : 0;
         }
         alive = __ballot_sync(0xffffffffu, lane < p.r.groups && ahead < p.r.kept);
     }
+    for (int e = lane; e < p.E; e += 32) {
+        if (p.r.groups > 1 && biased) key[e] = ordered64(sc[e]);
+        else key[e] = ordered64(biased ? prob(sl[e]) + (double)__ldg(p.bias + e) : (double)sl[e]);
+        if (key[e] == LLONG_MIN) key[e] = ordered64(-(double)INFINITY);   // NaN ranks with -inf
+    }
+    __syncwarp();
     // Round j takes the best (score, lower index) behind round j - 1's.
-    double last = INFINITY;
-    int last_e = -1, mine = 0;
+    long long last = LLONG_MAX;
+    int last_e = -1, mine_e = 0;
     for (int j = 0; j < p.k; ++j) {
-        double best = -INFINITY;
+        long long best = LLONG_MIN;
         int best_e = 1 << 30;
         for (int e = lane; e < p.E; e += 32) {
-            const double s = sc[e];
-            if (!((alive >> (e / size)) & 1u) && p.r.groups > 1) continue;
+            const long long s = key[e];
+            if (p.r.groups > 1 && !((alive >> (e / size)) & 1u)) continue;
             if (!(s < last || (s == last && e > last_e))) continue;
-            if (s > best || (s == best && e < best_e)) { best = s; best_e = e; }
+            if (s > best) { best = s; best_e = e; }
         }
         for (int o = 16; o > 0; o >>= 1) {
-            const double s = __shfl_xor_sync(0xffffffffu, best, o);
+            const long long s = __shfl_xor_sync(0xffffffffu, best, o);
             const int e = __shfl_xor_sync(0xffffffffu, best_e, o);
             if (s > best || (s == best && e < best_e)) { best = s; best_e = e; }
         }
         last = best;
         last_e = best_e;
-        if (lane == j) mine = best_e;
+        if (lane == j) mine_e = best_e;
     }
-    return mine;
+    return mine_e;
 }
 
 // The weights of the selected logits (lane j < k holds slot j's logit l):
@@ -123,32 +144,53 @@ __device__ __noinline__ int select_exact(const TopkParams& p, const float* sl, d
 // renormalising takes the row's largest logit m and sum z of exp(l - m).
 __device__ __forceinline__ float row_weight(const TopkParams& p, float l, float m, float z, int lane) {
     const bool in = lane < p.k, sig = mode_sigmoid(p.r.mode);
-    float v;
-    if (p.norm) {
+    float v = sig ? __fdividef(1.f, 1.f + __expf(-l)) : __fdividef(__expf(l - m), z);
+    if (!p.norm) return (m == -INFINITY && !sig && !(l != l) ? 0.f : v) * p.scale;
+    // Softmax ratios, and sigmoids that are all small, from the largest selected logit.
+    if (!sig || !__any_sync(0xffffffffu, in && l > -60.f)) {
         float M = in ? l : -INFINITY;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        if (sig) {
-            M = fminf(M, 0.f);
-            v = l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - M) / (1.f + expf(l));
-        } else {
-            v = expf(l - M);
-        }
+        for (int o = 1; o < p.k; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        M = __shfl_sync(0xffffffffu, M, 0);
+        v = __expf(l - M);   // (a small sigmoid is exp(l) to within its rounding)
         if (M == -INFINITY && !(l != l)) v = 0.f;
-        if (!in) v = 0.f;
-        const float tot = warp_sum(v);
-        v = tot == 0.f ? 0.f : v / tot;
-    } else if (sig) {
-        v = 1.f / (1.f + expf(-l));
-    } else {
-        v = m == -INFINITY && !(l != l) ? 0.f : expf(l - m) / z;
     }
-    return v * p.scale;
+    if (!in) v = 0.f;
+    float tot = v;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    if (p.k > 8) {
+        tot += __shfl_xor_sync(0xffffffffu, tot, 8);
+        tot += __shfl_xor_sync(0xffffffffu, tot, 16);
+    }
+    return tot == 0.f ? 0.f : __fdividef(v, tot) * p.scale;
 }
 
-// fp32 as an unsigned integer of the same order (-0 as +0).
+// V floats of a lane to and from shared memory (16-byte aligned when V is a multiple of 4).
+template <int V> __device__ __forceinline__ void put(float* d, const float (&v)[V]) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = v[i];
+    }
+}
+template <int V> __device__ __forceinline__ void get(const float* d, float (&v)[V]) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(d + i);
+            v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = d[i];
+    }
+}
+
+// fp32 as an unsigned integer of the same order.
 __device__ __forceinline__ uint32_t ordered(float v) {
-    const uint32_t b = __float_as_uint(v + 0.0f);
+    const uint32_t b = __float_as_uint(v);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t k) {
@@ -209,24 +251,64 @@ template <int N> __device__ __forceinline__ void sort_desc(uint32_t (&v)[N]) {  
                     }
 }
 
+// The experts e0 + i (i < V) of all lanes that `in` picks, in index order, to list (the
+// first 32); returns how many there are.
+template <int V, typename In>
+__device__ __forceinline__ int compact(In in, int e0, int lane, int* list) {
+    uint32_t cand = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (in(i)) cand |= 1u << i;
+    int before = __popc(cand);
+    const int own = before;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, before, 31);
+    int at = before - own;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if ((cand >> i) & 1u) {
+            if (at < 32) list[at] = e0 + i;
+            ++at;
+        }
+    __syncwarp();
+    return total;
+}
+
 // TYPE: of the logits.  V: experts of a lane (32 V >= E).
 template <int TYPE, int V>
-__global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? 6 : 1) topk_rows_kernel(const TopkParams p, int vec) {
+__global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? kMinBlocks : 1) topk_rows_kernel(const TopkParams p, int vec) {
     constexpr int W = V < 8 ? V : 8, L = V / W;      // lists of W
     extern __shared__ __align__(16) uint8_t dyn[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.E, k = p.k, e0 = lane * V;
-    // Per warp: logits and selection scores [32 V], 64-bit scratch [E] (256 bytes at least).
-    float* sl = reinterpret_cast<float*>(dyn) + (size_t)warp * (64 * V);
+    // The bias [32 V]; per warp: logits and selection scores [32 V], 64-bit scratch [E]
+    // (256 bytes at least).
+    float* sb = reinterpret_cast<float*>(dyn);
+    float* sl = sb + 32 * V + (size_t)warp * (64 * V);
     float* ss = sl + 32 * V;
-    double* sc = reinterpret_cast<double*>(dyn + (size_t)kRowWarps * 256 * V) + (size_t)warp * max(E, 32);
+    double* sc = reinterpret_cast<double*>(dyn + (size_t)(1 + 2 * kRowWarps) * 128 * V) + (size_t)warp * max(E, 32);
+    // Bit i: expert e0 + i exists.
+    const uint32_t valid = E - e0 >= V ? 0xffffffffu : (E > e0 ? (1u << (E - e0)) - 1u : 0u);
     const bool biased = mode_has_bias(p.r.mode), sig = mode_sigmoid(p.r.mode);
     const int size = E / p.r.groups;                 // experts of a group
     const bool need_p = biased || (p.r.groups > 1 && p.r.top2);
     const bool need_z = !sig && (need_p || !p.norm);
     const uint32_t ibits = E <= 256 ? 8 : (E <= 512 ? 9 : 10), imask = (1u << ibits) - 1u;
     const float bucket = exp2f((float)ibits - 22.f);
+    // Groups of 2^j whole lanes: every lane of a group holds its scores; other sizes: lane
+    // g those of group g.
+    const bool lanes = size % V == 0 && ((size / V) & (size / V - 1)) == 0;
+    const int per = lanes ? size / V : 1, grp = lane / per, e_grp = e0 / size;
+    const bool in = grp < p.r.groups;
     pdl_wait();
+    if (biased) {
+        for (int i = threadIdx.x; i < 32 * V; i += 32 * kRowWarps) sb[i] = i < E ? __ldg(p.bias + i) : 0.f;
+        __syncthreads();
+    }
 
     for (int64_t t = (int64_t)blockIdx.x * kRowWarps + warp; t < p.n; t += (int64_t)gridDim.x * kRowWarps) {
         float l[V];
@@ -236,8 +318,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? 6 : 1) topk_rows_kern
             for (int i = 0; i < V; ++i)
                 if (e0 + i < E) p.lsum[(size_t)t * E + e0 + i] = l[i];
         __syncwarp();   // the row before is done with shared memory
-#pragma unroll
-        for (int i = 0; i < V; ++i) sl[e0 + i] = l[i];
+        put<V>(sl + e0, l);
 
         // Softmax over the row: the largest logit and the sum of exp(l - m).
         float m = -INFINITY, z = 1.f;
@@ -255,46 +336,43 @@ __global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? 6 : 1) topk_rows_kern
         // (the argument's rounding, the sum); of the sum with the bias half an ulp.
         float s[V];
         float perr = 0.f;                                // error of a p
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = l[i];
         if (need_p) {
             const float rz = 1.f / z;
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 s[i] = sig ? __fdividef(1.f, 1.f + __expf(-l[i])) : expf(l[i] - m) * rz;
-            if (biased)
+            if (biased) {
+                float b[V];
+                get<V>(sb + e0, b);
 #pragma unroll
-                for (int i = 0; i < V; ++i) s[i] += e0 + i < E ? __ldg(p.bias + e0 + i) : 0.f;
+                for (int i = 0; i < V; ++i) s[i] += b[i];
+            }
             perr = sig ? 0x1p-21f : 0x1p-18f * rz;
         }
         bool clear = true, gclear = true;
-        uint32_t alive = 0xffffffffu;                    // bit i: expert e0 + i may be chosen
+        uint32_t alive = valid;                          // bit i: expert e0 + i may be chosen
         if (p.r.groups > 1) {
             // Group scores: the sum of the two best p (+ bias), or the best selection score.
-            const bool by_p = p.r.top2 || biased;
-            const bool lanes = size % V == 0 && ((size / V) & (size / V - 1)) == 0;   // groups are 2^j whole lanes
+            const bool by_p = need_p;
             float a = -INFINITY, b = -INFINITY;
-            int grp;
             if (lanes) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float v = by_p ? s[i] : l[i];
-                    b = fmaxf(b, fminf(a, v));
-                    a = fmaxf(a, v);
+                    b = fmaxf(b, fminf(a, s[i]));
+                    a = fmaxf(a, s[i]);
                 }
-                for (int o = 1; o < size / V; o <<= 1) {
+                for (int o = 1; o < per; o <<= 1) {
                     const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
                     b = fmaxf(fminf(a, a2), fmaxf(b, b2));
                     a = fmaxf(a, a2);
                 }
-                grp = lane / (size / V);
             } else {
-                if (by_p) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) ss[e0 + i] = s[i];
-                }
+                put<V>(ss + e0, s);
                 __syncwarp();
-                grp = lane;
                 if (lane < p.r.groups) {
-                    const float* src = (by_p ? ss : sl) + lane * size;
+                    const float* src = ss + lane * size;
                     for (int i = 0; i < size; ++i) {
                         b = fmaxf(b, fminf(a, src[i]));
                         a = fmaxf(a, src[i]);
@@ -302,26 +380,76 @@ __global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? 6 : 1) topk_rows_kern
                 }
                 __syncwarp();
             }
-            const float gs = p.r.top2 ? (size > 1 ? a + b : a) : a;
-            const int per = lanes ? size / V : 1;        // lanes of a group
+            const float gs = (p.r.top2 ? (size > 1 ? a + b : a) : a) + 0.f;
+            // Ranks by integers of the scores' order with the group in the low bits.
+            const uint32_t gk = in ? (ordered(gs) & ~31u) | (31u - grp) : 0u;
             int ahead = 0;
-            for (int g = 0; g < p.r.groups; ++g) {
-                const float o = __shfl_sync(0xffffffffu, gs, g * per);
-                ahead += (o > gs || (o == gs && g < grp)) ? 1 : 0;
+            for (int g = 0; g < p.r.groups; ++g) ahead += __shfl_sync(0xffffffffu, gk, g * per) > gk ? 1 : 0;
+            bool keep = in && ahead < p.r.kept;
+            if (p.r.kept < p.r.groups) {
+                // Whether the last kept group is clear of the best left by `tol` of the larger, and `add`.
+                auto apart = [&](float tol, float add) {
+                    const float worst = unordered(__reduce_min_sync(0xffffffffu, keep ? ordered(gs) : 0xffffffffu));
+                    const float best = unordered(__reduce_max_sync(0xffffffffu, in && !keep ? ordered(gs) : 0u));
+                    return tol == 0.f ? worst >= best : worst - best > add + tol * fmaxf(fabsf(worst), fabsf(best));
+                };
+                const float err = by_p ? 4.f * perr : 1e-38f;
+                // (The index hides 32 ulps of a score in fp32, nothing of 16-bit logits.)
+                clear = apart(TYPE == MOE_F32 || by_p ? 0x1p-17f : 0.f, err);
+                if (!clear) {                             // the whole scores
+                    ahead = 0;
+                    for (int g = 0; g < p.r.groups; ++g) {
+                        const float o = __shfl_sync(0xffffffffu, gs, g * per);
+                        ahead += (o > gs || (o == gs && g < grp)) ? 1 : 0;
+                    }
+                    keep = in && ahead < p.r.kept;
+                    clear = apart(by_p ? 0x1p-21f : 0.f, err);
+                    if (by_p && !__all_sync(0xffffffffu, clear) && (sig || !biased)) {
+                        // The experts that can be a group's two best (or best) in 64 bits, one lane
+                        // each; without a bias the softmax's common factor is left out.
+                        const float low = (p.r.top2 ? b : a) - 4.f * perr - 0x1p-21f * fabsf(b);
+                        int* list = reinterpret_cast<int*>(sc);
+                        const int total = compact<V>([&](int i) {
+                            const int ge = lanes ? grp * per : min((e0 + i) / size, 31);   // the lane that holds the group's scores
+                            const float lo = __shfl_sync(0xffffffffu, low, ge);
+                            return ((valid >> i) & 1u) && s[i] >= lo;
+                        }, e0, lane, list);
+                        if (total <= 32) {
+                            const int ce = lane < total ? list[lane] : 0;
+                            double v = sig ? 1. / (1. + exp(-(double)sl[ce])) : exp((double)sl[ce] - (double)m);
+                            if (biased) v += (double)sb[ce];
+                            const int cg = lane < total ? ce / size : 64;
+                            double va = -INFINITY, vb = -INFINITY;
+                            for (int i = 0; i < total; ++i) {
+                                const double o = __shfl_sync(0xffffffffu, v, i);
+                                if (__shfl_sync(0xffffffffu, cg, i) != grp) continue;
+                                if (ordered64(o) > ordered64(va)) { vb = va; va = o; }
+                                else if (ordered64(o) > ordered64(vb)) vb = o;
+                            }
+                            const long long q = ordered64(p.r.top2 && size > 1 ? va + vb : va);
+                            ahead = 0;
+                            for (int g = 0; g < p.r.groups; ++g) {
+                                const long long o = __shfl_sync(0xffffffffu, q, g * per);
+                                ahead += (o > q || (o == q && g < grp)) ? 1 : 0;
+                            }
+                            keep = in && ahead < p.r.kept;
+                            clear = true;
+                        }
+                        __syncwarp();
+                    }
+                }
             }
-            const bool in = grp < p.r.groups, keep = in && ahead < p.r.kept;
-            const float worst = unordered(__reduce_min_sync(0xffffffffu, keep ? ordered(gs) : 0xffffffffu));
-            const float best = unordered(__reduce_max_sync(0xffffffffu, in && !keep ? ordered(gs) : ordered(-INFINITY)));
-            if (by_p && p.r.kept < p.r.groups)
-                clear = worst - best > 4.f * perr + 0x1p-21f * fmaxf(fabsf(worst), fabsf(best));
-            // (The best logits decide exactly, but a NaN is for the 64-bit path.)
-            else if (!(worst >= best)) clear = false;
             gclear = __all_sync(0xffffffffu, clear);
             const uint32_t kept = lanes ? 0u : __ballot_sync(0xffffffffu, keep);
+            if (lanes) {
+                if (!keep) alive = 0u;
+            } else {
+                int gi = e_grp, r = e0 - gi * size;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const bool on = lanes ? keep : ((kept >> ((e0 + i) / size)) & 1u) != 0u;
-                if (!on) alive &= ~(1u << i);
+                for (int i = 0; i < V; ++i) {
+                    if (!((kept >> (gi & 31)) & 1u)) alive &= ~(1u << i);
+                    if (++r == size) { r = 0; ++gi; }
+                }
             }
         }
         if (!biased)
@@ -329,14 +457,18 @@ __global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? 6 : 1) topk_rows_kern
             for (int i = 0; i < V; ++i) s[i] = l[i];
         const float serr = biased ? perr : 0.f;
 
+        if (biased) put<V>(ss + e0, s);
         uint32_t key[L][W];
+        bool nan = false;
+        const uint32_t c0 = imask - (uint32_t)e0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float v = s[i] == s[i] ? s[i] : -INFINITY;   // NaN ranks last
-            if (biased) ss[e0 + i] = s[i];
-            const bool on = e0 + i < E && ((alive >> i) & 1u);
-            key[i / W][i % W] = on ? (ordered(v) & ~imask) | (imask - (uint32_t)(e0 + i)) : 0u;
+            nan = nan || s[i] != s[i];
+            const uint32_t o = ordered(biased ? s[i] : s[i] + 0.0f);   // (-0 ties with +0)
+            key[i / W][i % W] = (alive & (1u << i)) ? (o & ~imask) | (c0 - i) : 0u;
         }
+        // A NaN ranks last: by the 64-bit path.  (Past E the logits are -inf.)
+        if (nan && valid) clear = false;
 #pragma unroll
         for (int q = 0; q < L; ++q) sort_desc(key[q]);
         uint32_t mine = 0u;
@@ -347,12 +479,12 @@ __global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? 6 : 1) topk_rows_kern
             const uint32_t w = __reduce_max_sync(0xffffffffu, h);
             if (lane == j) mine = w;                      // (k = 32: the last is dropped and not needed, see below)
 #pragma unroll
-            for (int q = 0; q < L; ++q)
-                if (key[q][0] == w) {
+            for (int q = 0; q < L; ++q) {
+                const bool won = key[q][0] == w;
 #pragma unroll
-                    for (int i = 0; i + 1 < W; ++i) key[q][i] = key[q][i + 1];
-                    key[q][W - 1] = 0u;
-                }
+                for (int i = 0; i + 1 < W; ++i) key[q][i] = won ? key[q][i + 1] : key[q][i];
+                key[q][W - 1] = won ? 0u : key[q][W - 1];
+            }
         }
         __syncwarp();
         int e = (int)(imask - (mine & imask));
@@ -380,37 +512,28 @@ __global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? 6 : 1) topk_rows_kern
             // errors hide: one lane each, if they are at most 32.
             const float at_k = __shfl_sync(0xffffffffu, sj, k - 1);
             const float thr = at_k - (fabsf(at_k) * (2.f * bucket) + 2.f * serr + 0x1p-21f * fabsf(at_k) + 1e-38f);
-            uint32_t cand = 0u;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (e0 + i < E && s[i] >= thr) cand |= 1u << i;
-            cand &= alive;
-            int before = __popc(cand);
-            const int own = before;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, before, o);
-                if (lane >= o) before += y;
-            }
-            const int total = __shfl_sync(0xffffffffu, before, 31);
+            int* list = reinterpret_cast<int*>(sc);
+            const int total = compact<V>([&](int i) { return ((alive >> i) & 1u) && s[i] >= thr; }, e0, lane, list);
             // (-inf or NaN at the k-th, a softmax with a bias, unclear groups: every score in 64 bits.)
-            if (gclear && at_k > -3.0e38f && total <= 32 && !(biased && !sig)) {
-                int* list = reinterpret_cast<int*>(sc);
-                int at = before - own;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if ((cand >> i) & 1u) list[at++] = e0 + i;
-                __syncwarp();
+            if (gclear && !__any_sync(0xffffffffu, nan) && at_k > -3.0e38f && total <= 32 && !(biased && !sig)) {
                 const int ce = lane < total ? list[lane] : 0;
-                double v = (double)sl[ce];
-                if (biased) v = 1. / (1. + exp(-v)) + (double)__ldg(p.bias + ce);
-                // As integers of the same order.
-                long long q = __double_as_longlong(v + 0.0);
-                q ^= (long long)((unsigned long long)(q >> 63) >> 1);
+                // By their whole 32-bit scores, if these are clear; else in 64 bits.
+                const float v32 = lane < total ? (biased ? ss : sl)[ce] : -INFINITY;
                 int ahead = 0;
+                bool close = false;
+                const float near = 2.f * serr + 0x1p-22f * fabsf(v32);
                 for (int i = 0; i < total; ++i) {
-                    const long long o = __shfl_sync(0xffffffffu, q, i);
-                    ahead += (o > q || (o == q && i < lane)) ? 1 : 0;   // (the list is in index order)
+                    const float o = __shfl_sync(0xffffffffu, v32, i);
+                    ahead += (o > v32 || (o == v32 && i < lane)) ? 1 : 0;   // (the list is in index order)
+                    close = close || (i != lane && fabsf(o - v32) <= near);
+                }
+                if (biased && __any_sync(0xffffffffu, lane < total && close)) {
+                    const long long q = ordered64(1. / (1. + exp(-(double)sl[ce])) + (double)sb[ce]);
+                    ahead = 0;
+                    for (int i = 0; i < total; ++i) {
+                        const long long o = __shfl_sync(0xffffffffu, q, i);
+                        ahead += (o > q || (o == q && i < lane)) ? 1 : 0;
+                    }
                 }
                 __syncwarp();
                 if (lane < total && ahead < k) list[32 + ahead] = ce;
@@ -436,7 +559,7 @@ cudaError_t launch_rows(const TopkParams& p, int num_sms, cudaStream_t st) {
     const size_t esize = TYPE == MOE_F32 ? 4 : 2;
     const int vec = p.ns == 1 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.row_stride * esize % 16 == 0 && p.E % kPer == 0;
     const int64_t blocks = ((int64_t)p.n + kRowWarps - 1) / kRowWarps;
-    const size_t smem = (size_t)kRowWarps * (256 * V + std::max(8 * p.E, 256));   // <= 64 KB
+    const size_t smem = (size_t)128 * V + (size_t)kRowWarps * (256 * V + std::max(8 * p.E, 256));   // <= 68 KB
     static std::mutex mu;
     static bool configured[128] = {};
     int dev = 0;
@@ -445,12 +568,12 @@ cudaError_t launch_rows(const TopkParams& p, int num_sms, cudaStream_t st) {
     if (V == 32) {
         std::lock_guard<std::mutex> lock(mu);
         if (!configured[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 68 * 1024);
             if (e != cudaSuccess) return e;
             configured[dev] = true;
         }
     }
-    const int grid = (int)std::min<int64_t>(blocks, (int64_t)num_sms * 8);
+    const int grid = (int)std::min<int64_t>(blocks, (int64_t)num_sms * (V <= 8 ? kMinBlocks : 2));   // one wave
     launch_pdl(kern, grid, 32 * kRowWarps, smem, st, p, vec);
     return cudaGetLastError();
 }
