@@ -162,10 +162,18 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def raw_stream(device: int) -> int:
+    """torch's current stream of a device, as a cudaStream_t."""
+    global raw_stream
+    import torch
+    raw_stream = torch._C._cuda_getCurrentRawStream
+    return raw_stream(device)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

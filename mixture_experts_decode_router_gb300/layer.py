@@ -110,6 +110,7 @@ class MoeLayer:
         # The control block (first 256 bytes) must start at zero; calls keep it zero.
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
         self.max_tokens = max_tokens
+        self._ws_ptr, self._experts = self.ws.data_ptr(), B.entry("moe_experts")
 
     def forward(self, x: torch.Tensor, out=None, idx=None, w=None, stream=None,
                 routing: bool = True):
@@ -145,21 +146,23 @@ class MoeLayer:
 
     def experts(self, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, stream=None):
         n = x.shape[0]
-        out = torch.empty(n, self.cfg.hidden, dtype=torch.bfloat16, device=x.device)
-        B.check(B.moe_experts(self.c_cfg, self.c_w, x, n, idx, w, out, self.ws, self.ws_bytes,
-                              stream))
+        out = torch.empty((n, self.cfg.hidden), dtype=torch.bfloat16, device=x.device)
+        s = self._experts(self.c_cfg, self.c_w, x.data_ptr(), n, idx.data_ptr(), w.data_ptr(), out.data_ptr(),
+                          self._ws_ptr, self.ws_bytes, B._stream(stream))
+        if s:
+            B.check(s)
         return out
 
 
-def _device_of(t: torch.Tensor) -> torch.device:
-    """The current GPU, on which ``t`` is, or to which ``t`` is pinned host memory."""
-    if t.is_cuda:
-        if t.get_device() != torch.cuda.current_device():
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-        return t.device
-    if not t.is_pinned():
+def _device_of(t: torch.Tensor) -> int:
+    """The current GPU's index: ``t`` is on it, or in pinned host memory."""
+    at = t.get_device()
+    if at < 0 and not t.is_pinned():
         raise ValueError("tensors are on the GPU or in pinned host memory")
-    return torch.device("cuda", torch.cuda.current_device())
+    dev = torch.cuda.current_device()
+    if at >= 0 and at != dev:
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    return dev
 
 
 class MoeTopk:
@@ -197,17 +200,18 @@ class MoeTopk:
 
     def forward(self, logits: torch.Tensor, idx=None, w=None, stream=None):
         cfg = self.c_cfg[logits.dtype]
-        E, k = self.num_experts, self.top_k
-        if logits.dim() != 2 or logits.size(1) != E or (E > 1 and logits.stride(1) != 1):
+        E, k, shape, strides = self.num_experts, self.top_k, logits.shape, logits.stride()
+        if len(shape) != 2 or shape[1] != E or (E > 1 and strides[1] != 1):
             raise ValueError("logits are [n, num_experts] with contiguous rows")
-        dev = _device_of(logits)
-        n = logits.size(0)
+        n, dev = shape[0], _device_of(logits)
         if idx is None:
             idx = torch.empty((n, k), dtype=torch.int32, device=dev)
         if w is None:
             w = torch.empty((n, k), dtype=torch.float32, device=dev)
-        B.check(self._topk(cfg, logits.data_ptr(), logits.stride(0) if n > 1 else E, self._bias, n,
-                           idx.data_ptr(), w.data_ptr(), B._stream(stream)))
+        s = self._topk(cfg, logits.data_ptr(), strides[0] if n > 1 else E, self._bias, n, idx.data_ptr(),
+                       w.data_ptr(), B.raw_stream(dev) if stream is None else B._stream(stream))
+        if s:
+            B.check(s)
         return idx, w
 
 
@@ -242,20 +246,22 @@ class MoeMatvec:
 
     def forward(self, x: torch.Tensor, out=None, stream=None):
         cfg = self.c_cfg[x.dtype]
-        K, O = self.in_features, self.out_features
-        if x.dim() != 2 or x.size(1) != K or x.stride(1) != 1:
+        K, O, shape, strides = self.in_features, self.out_features, x.shape, x.stride()
+        if len(shape) != 2 or shape[1] != K or strides[1] != 1:
             raise ValueError("x is [n, in] with contiguous rows")
-        dev = _device_of(x)
-        n = x.size(0)
+        n, dev = shape[0], _device_of(x)
+        ostride = O
         if out is None:
             if self.accumulate:
                 raise ValueError("accumulate needs out")
             out = torch.empty((n, O), dtype=self.out_dtype, device=dev)
-            ostride = O
         else:
             if out.shape != (n, O) or out.dtype != self.out_dtype or (O > 1 and out.stride(1) != 1):
                 raise ValueError("out is [n, out] of out_dtype with contiguous rows")
-            ostride = out.stride(0) if n > 1 else O
-        B.check(self._matvec(cfg, self.c_w, self._bias, x.data_ptr(), x.stride(0) if n > 1 else K, n,
-                             out.data_ptr(), ostride, B._stream(stream)))
+            if n > 1:
+                ostride = out.stride(0)
+        s = self._matvec(cfg, self.c_w, self._bias, x.data_ptr(), strides[0] if n > 1 else K, n, out.data_ptr(),
+                         ostride, B.raw_stream(dev) if stream is None else B._stream(stream))
+        if s:
+            B.check(s)
         return out
