@@ -30,17 +30,10 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;                 // ring of each warp, in 2 KB stages (gate_up: two stages of two)
+constexpr int kStages = 3;                 // ring of each warp
 constexpr int kRing = kWarps * kStages * q4::kStageBytes;
-constexpr int kRingGU = kWarps * 4 * q4::kStageBytes;
 constexpr int kActStages = 3;              // stages of a chunk of act
-#ifndef XGU
-#define XGU 10240
-#endif
-// Rows of act (a chunk for 16 tokens in groups of 32) or of x, and their group sums,
-// in shared memory: three blocks an SM.
-constexpr int kActBytes = 16 * (kActStages * 512 + 64) + kActStages * q4::sum_bytes(5, 2);
-constexpr int kXBytes = XGU;
+constexpr int kXBytes = 16 * (kActStages * 512 + 64);   // rows of x or act in shared memory (25.6 KB: three blocks an SM)
 constexpr int kMaxSmem = 227 * 1024;
 
 // 768 fp32 values of one act row (zero past `left`) as f16 chunks for the fragments,
@@ -89,54 +82,57 @@ struct Item {
 
 template <int GSH, bool Z, bool GU, int NT>
 __device__ __forceinline__ void run_item(const Q4Params& p, const Item& it, uint8_t* dyn) {
-    constexpr int kMats = GU ? 2 : 1, kSt = GU ? 2 : kStages, kRingB = GU ? kRingGU : kRing;
+    constexpr int kMats = GU ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int out = GU ? (it.sh ? p.S : p.I) : p.H, K = GU ? p.H : (it.sh ? p.S : p.I);
     const int nst = (K + q4::kStageK - 1) / q4::kStageK, row_bytes = K / 2, full = row_bytes / 128;
     const int row0 = (it.tile0 + warp) * 16, rows = out - row0;
     const int64_t srow = (int64_t)it.le * out + row0;        // the tile's first row in the stack
     const bool live = rows > 0;
-    const uint32_t ring = warp * (kRingB / kWarps), ring_a = q4::smem_addr(dyn) + ring;
-    float* factor = reinterpret_cast<float*>(dyn + kRingB);   // [16] of the chunk (down)
+    const uint32_t ring = warp * kStages * q4::kStageBytes, ring_a = q4::smem_addr(dyn) + ring;
+    float* factor = reinterpret_cast<float*>(dyn + kRing);   // [16] of the chunk (down)
     float* weight = factor + 16;                             // [16] of the token (down)
-    const uint32_t x0 = kRingB + 128;
+    const uint32_t x0 = kRing + 128;
     const QMatDev& m0 = GU ? (it.sh ? p.sh_gate : p.gate) : (it.sh ? p.sh_down : p.down);
     const QMatDev& m1 = it.sh ? p.sh_up : p.up;
-    // Stages of a chunk; a token's row of a chunk in shared memory; the chunk's sums.
-    const int cs = GU ? min(nst, (kXBytes - 64 * it.ntok) / (512 * it.ntok + q4::sum_bytes(GSH, NT))) : min(nst, kActStages);
+    // Stages of a chunk; a token's row of a chunk in shared memory.
+    const int cs = GU ? min(nst, (kXBytes / it.ntok - 64) / 512) : min(nst, kActStages);
     const int xstride = (GU ? cs : kActStages) * 512 + 64;
-    const uint32_t sums = x0 + it.ntok * xstride;
 
-    // The copies (gate and up of a stage together) run kStages - 1 stages ahead, the
-    // scales' loads one.
-    int i_s = 0, n_s = 0, i_slot = 0;
-    q4::RowCopy cp[kMats];
-    q4::ScaleLoad<GSH, Z> sl[kMats];
-    q4::StageScales<GSH, Z> sc[kMats], nx[kMats];
+    // Stages in the order chunk, matrix, stage; the copies run kStages - 1 ahead and
+    // the scales' loads one.
+    struct Walk {
+        int s, m, c0;
+        __device__ __forceinline__ bool next(int cs, int nst) {   // whether the matrix or the chunk changes
+            if (++s < min(c0 + cs, nst)) return false;
+            if (++m == kMats) { m = 0; c0 += cs; }
+            s = c0;
+            return true;
+        }
+    };
+    Walk wi{0, 0, 0}, wn{0, 0, 0};
+    int i_slot = 0;
+    q4::RowCopy cp;
+    q4::ScaleLoad<GSH, Z> sl;
+    q4::StageScales<GSH, Z> sc, nx;
     auto issue = [&]() {
-        if (live && i_s < nst) {
-#pragma unroll
-            for (int m = 0; m < kMats; ++m)
-                cp[m].issue(ring_a + (i_slot * kMats + m) * q4::kStageBytes, i_s, 1, row_bytes, full, m0.w, lane);
-            ++i_s;
+        if (live && wi.s < nst) {
+            cp.issue(ring_a + i_slot * q4::kStageBytes, wi.s, 1, row_bytes, full, m0.w, lane);
+            if (wi.next(cs, nst)) cp.start(wi.m ? m1.w : m0.w, srow, rows, row_bytes, wi.s, lane);
         }
         q4::cp_commit();
-        i_slot = i_slot + 1 == kSt ? 0 : i_slot + 1;
+        i_slot = i_slot + 1 == kStages ? 0 : i_slot + 1;
     };
     auto load_scales = [&]() {
-        if (live && n_s < nst) {
-#pragma unroll
-            for (int m = 0; m < kMats; ++m) sl[m].load(nx[m], n_s, 1, K, lane);
-            ++n_s;
+        if (live && wn.s < nst) {
+            sl.load(nx, wn.s, 1, K, lane);
+            if (wn.next(cs, nst)) sl.start(wn.m ? m1 : m0, srow, rows, wn.s, lane);
         }
     };
+    cp.start(m0.w, srow, rows, row_bytes, 0, lane);
+    sl.start(m0, srow, rows, 0, lane);
 #pragma unroll
-    for (int m = 0; m < kMats; ++m) {
-        cp[m].start((m ? m1 : m0).w, srow, rows, row_bytes, 0, lane);
-        sl[m].start(m ? m1 : m0, srow, rows, 0, lane);
-    }
-#pragma unroll
-    for (int s = 0; s < kSt - 1; ++s) issue();
+    for (int s = 0; s < kStages - 1; ++s) issue();
     load_scales();
     if (!GU && threadIdx.x < it.ntok) {
         const int b = it.pos0 + threadIdx.x;
@@ -179,22 +175,18 @@ __device__ __forceinline__ void run_item(const Q4Params& p, const Item& it, uint
             }
         }
         __syncthreads();
-        q4::group_sums<GSH, GU, NT>(dyn, x, sums, min(cs, nst - c0), warp, kWarps, lane);
-        __syncthreads();
         if (live) {
-            for (int s = c0; s < min(c0 + cs, nst); ++s) {
 #pragma unroll
-                for (int m = 0; m < kMats; ++m) sc[m] = nx[m];
-                load_scales();
-                q4::cp_wait<kSt - 2>();
-                __syncwarp();
-                issue();
-                uint32_t st[kMats];
-#pragma unroll
-                for (int m = 0; m < kMats; ++m) st[m] = ring + (slot * kMats + m) * q4::kStageBytes;
-                q4::mma_stage_sums<GSH, Z, GU, NT, kMats>(dyn, st, x, sums, s - c0, sc, acc, lane);
-                slot = slot + 1 == kSt ? 0 : slot + 1;
-            }
+            for (int m = 0; m < kMats; ++m)
+                for (int s = c0; s < min(c0 + cs, nst); ++s) {
+                    sc = nx;
+                    load_scales();
+                    q4::cp_wait<kStages - 2>();
+                    __syncwarp();
+                    issue();
+                    q4::mma_stage<GSH, Z, GU, NT>(dyn, ring + slot * q4::kStageBytes, x, s - c0, sc, acc[m], lane);
+                    slot = slot + 1 == kStages ? 0 : slot + 1;
+                }
             if constexpr (!GU) {
 #pragma unroll
                 for (int q = 0; q < NT; ++q)
@@ -481,7 +473,7 @@ cudaError_t launch_smem(Kern kern, int slot, size_t smem, dim3 grid, cudaStream_
 // Blocks of the general kernels: every SM's share of the items there can be.
 template <int GSH, bool Z, int SLOT>
 cudaError_t launch_fmt(const Q4Params& p, bool gate_up, int tile, int num_sms, cudaStream_t st) {
-    const size_t smem = gate_up ? kRingGU + 128 + kXBytes : kRing + 128 + kActBytes;
+    const size_t smem = kRing + 128 + kXBytes;
     const int per_sm = tile == 8 ? 3 : 2;
     const dim3 grid(num_sms * per_sm);
     if (p.n == 1) {

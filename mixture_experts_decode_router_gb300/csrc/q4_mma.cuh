@@ -55,36 +55,36 @@ __device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// A lane's part of the copies of 16 weight rows, one stage after another: rows
-// lane / 4 and lane / 4 + 8, chunks lane % 4 and lane % 4 + 4.
+// A lane's part of the copies of 16 weight rows: rows lane / 8 + 4 i, chunk lane % 8
+// of one stage after another.
 struct RowCopy {
-    const uint8_t* src;    // row lane / 4, chunk lane % 4 of the next stage
+    const uint8_t* src;    // row lane / 8, chunk lane % 8 of the next stage
     int rows;              // rows of the tile inside the matrix
-    uint32_t d0;           // lane's place in a stage
+    uint32_t d0;           // lane's place in a stage; row r + 4's chunk is the other of bit 2
     __device__ __forceinline__ void start(const uint8_t* w, int64_t row, int rows_left, int row_bytes, int s, int lane) {
-        const int r = lane >> 2;
-        src = w + (row + r) * row_bytes + s * 128 + (lane & 3) * 16;
+        const int r0 = lane >> 3;
+        src = w + (row + r0) * row_bytes + s * 128 + (lane & 7) * 16;
         rows = rows_left;
-        d0 = r * 128 + (((lane & 3) ^ r) << 4);
+        d0 = r0 * 128 + (((lane & 7) ^ r0) << 4);
     }
     // The next stage, number s, into dst; `step` stages on after it.  full_stages:
     // stages that lie inside the row.
     __device__ __forceinline__ void issue(uint32_t dst, int s, int step, int row_bytes, int full_stages,
                                           const uint8_t* any, int lane) {
         const uint32_t d = dst + d0, e = dst + (d0 ^ 64u);
-        const uint8_t* src8 = src + (size_t)(8 * row_bytes);
+        const size_t r4 = (size_t)(4 * row_bytes);
         if (rows >= 16 && s < full_stages) {
             cp16(d, src);
-            cp16(e, src + 64);
-            cp16(d + 1024, src8);
-            cp16(e + 1024, src8 + 64);
+            cp16(e + 512, src + r4);
+            cp16(d + 1024, src + 2 * r4);
+            cp16(e + 1536, src + 3 * r4);
         } else {
-            const int left = row_bytes - s * 128 - (lane & 3) * 16, r = lane >> 2;
-            const bool in0 = left > 0, in1 = left > 64, lo = r < rows, hi = r + 8 < rows;
-            cp16_or_zero(d, in0 && lo ? src : any, in0 && lo);
-            cp16_or_zero(e, in1 && lo ? src + 64 : any, in1 && lo);
-            cp16_or_zero(d + 1024, in0 && hi ? src8 : any, in0 && hi);
-            cp16_or_zero(e + 1024, in1 && hi ? src8 + 64 : any, in1 && hi);
+            const bool in = s * 128 + (lane & 7) * 16 < row_bytes;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool ok = in && (lane >> 3) + 4 * i < rows;
+                cp16_or_zero(((i & 1) ? e : d) + 512 * i, ok ? src + i * r4 : any, ok);
+            }
         }
         src += step * 128;
     }
@@ -328,117 +328,6 @@ __device__ __forceinline__ void mma_stage(const uint8_t* sm, uint32_t st, const 
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[q][i] = fmaf(fs[i >> 1], d[q][i], acc[q][i]);
             }
-        }
-    }
-}
-
-// The eight codes of w above 128 (bf16) or 64 (f16), as pairs (i, i + 4).
-template <bool BF>
-__device__ __forceinline__ void int4_raw_pairs(uint32_t w, uint32_t (&p)[4]) {
-    if constexpr (BF) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = lop_and_or(w >> (4 * i), 0x000f000fu, 0x43004300u);
-    } else {
-        p[0] = lop_and_or(w << 4, 0x00f000f0u, 0x54005400u);
-        p[1] = lop_and_or(w, 0x00f000f0u, 0x54005400u);
-        p[2] = lop_and_or(w >> 4, 0x00f000f0u, 0x54005400u);
-        p[3] = lop_and_or(w >> 8, 0x00f000f0u, 0x54005400u);
-    }
-}
-
-// One stage of M matrices with the same tokens, the codes used as they stand above
-// 128 (or 64): a group's sum is d - (128 + z) X with X the group's sum of x, which
-// costs four fewer instructions for eight codes than the exact differences and four
-// more for a group.  d is up to 30 times (f16: 14 times) the result, so the fp32
-// sums keep 2^-19 of it: for results that are rounded to 16 bits.
-// sums: X of the chunk's groups and tokens (group_sums).
-template <int GSH, bool Z, bool BF, int NT, int M>
-__device__ __forceinline__ void mma_stage_sums(const uint8_t* sm, const uint32_t (&st)[M], const XView<NT>& x,
-                                               uint32_t sums, int s, const StageScales<GSH, Z> (&sc)[M],
-                                               float (&acc)[M][NT][4], int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    constexpr int kHold = StageScales<GSH, Z>::kHold, kPer = (1 << GSH) / 32, kGroups = kStageK >> GSH;
-    constexpr float kBase = BF ? 128.f : 64.f;
-    const uint32_t w_at = g * 128 + (g << 4) + 4 * t, sum_at = sums + (uint32_t)(s * kGroups) * (32 * NT) + 8 * t;
-    uint32_t xa[NT];
-#pragma unroll
-    for (int q = 0; q < NT; ++q) xa[q] = x.at[q] + (uint32_t)s * (2 * kStageK);
-    // Rows g and g + 8 of each held group in one word; 128 + z in bf16.
-    uint32_t ps[M][kHold], pz[M][kHold];
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-        for (int q = 0; q < kHold; ++q) {
-            ps[m][q] = __byte_perm(sc[m].v[0][q], sc[m].v[1][q], 0x5410);
-            if constexpr (Z)
-                pz[m][q] = __byte_perm(__float_as_uint(kBase + (float)sc[m].z[0][q]),
-                                       __float_as_uint(kBase + (float)sc[m].z[1][q]), 0x7632);
-        }
-    float d[M][NT][4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint4 b[NT];
-#pragma unroll
-        for (int q = 0; q < NT; ++q) b[q] = *reinterpret_cast<const uint4*>(sm + xa[q] + j * 64);
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            const uint32_t at = st[m] + (w_at ^ (uint32_t)(j << 4));
-            uint32_t p0[4], p1[4];
-            int4_raw_pairs<BF>(*reinterpret_cast<const uint32_t*>(sm + at), p0);
-            int4_raw_pairs<BF>(*reinterpret_cast<const uint32_t*>(sm + at + 1024), p1);
-#pragma unroll
-            for (int q = 0; q < NT; ++q) {
-                if (j % kPer == 0) mma16816<BF, true>(d[m][q], p0[0], p1[0], p0[1], p1[1], b[q].x, b[q].y);
-                else mma16816<BF, false>(d[m][q], p0[0], p1[0], p0[1], p1[1], b[q].x, b[q].y);
-                mma16816<BF, false>(d[m][q], p0[2], p1[2], p0[3], p1[3], b[q].z, b[q].w);
-            }
-        }
-        if (j % kPer == kPer - 1) {
-            const int grp = j / kPer, from = (lane & 28) | (grp & 3);
-            float2 xs[NT];
-#pragma unroll
-            for (int q = 0; q < NT; ++q) xs[q] = *reinterpret_cast<const float2*>(sm + sum_at + grp * (32 * NT) + 32 * q);
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const uint32_t u = __shfl_sync(0xffffffffu, ps[m][grp / 4], from);
-                const float fs[2] = {__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)};
-                float fz[2] = {kBase + 8.f, kBase + 8.f};
-                if constexpr (Z) {
-                    const uint32_t uz = __shfl_sync(0xffffffffu, pz[m][grp / 4], from);
-                    fz[0] = __uint_as_float(uz << 16);
-                    fz[1] = __uint_as_float(uz & 0xffff0000u);
-                }
-#pragma unroll
-                for (int q = 0; q < NT; ++q)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[m][q][i] = fmaf(fs[i >> 1], fmaf(-fz[i >> 1], (i & 1) ? xs[q].y : xs[q].x, d[m][q][i]), acc[m][q][i]);
-            }
-        }
-    }
-}
-// Bytes of the sums of a stage.
-__host__ __device__ constexpr int sum_bytes(int gsh, int nt) { return (kStageK >> gsh) * 32 * nt; }
-
-// X of `stages` staged stages: products with ones, by the block's warps in turn.
-template <int GSH, bool BF, int NT>
-__device__ __forceinline__ void group_sums(uint8_t* sm, const XView<NT>& x, uint32_t sums, int stages, int warp, int warps,
-                                           int lane) {
-    constexpr int kGroups = kStageK >> GSH, kPer = (1 << GSH) / 32;
-    constexpr uint32_t one = BF ? 0x3f803f80u : 0x3c003c00u;
-    for (int i = warp; i < stages * kGroups; i += warps) {
-        const int s = i / kGroups, j0 = (i % kGroups) * kPer;
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const uint4 b = *reinterpret_cast<const uint4*>(sm + x.at[q] + (uint32_t)s * (2 * kStageK) + (j0 + j) * 64);
-                mma16816<BF, false>(d, one, one, one, one, b.x, b.y);
-                mma16816<BF, false>(d, one, one, one, one, b.z, b.w);
-            }
-            if (lane < 4)
-                *reinterpret_cast<float2*>(sm + sums + (uint32_t)i * (32 * NT) + 32 * q + 8 * lane) = make_float2(d[0], d[1]);
         }
     }
 }
