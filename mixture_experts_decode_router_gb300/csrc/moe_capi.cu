@@ -215,8 +215,12 @@ constexpr int kTokenMajorMaxN = 3;
 static bool early_dependents(int32_t n, int sms) { return n <= sms; }
 
 // INT4 under AUTO: the streaming kernels while the experts have at most
-// kStreamMaxAvg tokens on average, the grouped tensor-core path above.
-constexpr int kStreamMaxAvg = 16;
+// kStreamMaxAvg tokens on average, the grouped tensor-core path above.  Measured on
+// GB300, the experts in groups of 128, streaming against grouped: hidden 2048, 256
+// experts, top-8, 512 tokens (16 on average) 267 against 327 us, 768 tokens 363
+// against 343; hidden 7168, 64 experts, 128 tokens (16) 762 against 984 us, 192
+// tokens (24) 1067 against 1014.
+constexpr int kStreamMaxAvg = 20;
 constexpr int kPathStream = 3;
 
 // The multi-kernel path a call of n tokens takes.
