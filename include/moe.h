@@ -147,7 +147,9 @@ typedef enum {
 } moe_wfmt_t;
 /* Expert-stage algorithm.  AUTO: one token runs the single-token kernel,
  * 2-3 tokens the token-major kernels, 4 or more the expert-grouped
- * tensor-core GEMM.  The two explicit values force one (tests); TOKEN_MAJOR
+ * tensor-core GEMM; INT4 experts run streaming kernels of their own while an
+ * expert has at most 20 tokens on average (n k <= 20 E), the expert-grouped
+ * GEMM above.  The two explicit values force one (tests); TOKEN_MAJOR
  * with one token still runs the single-token kernel (same arithmetic). */
 typedef enum { MOE_PATH_AUTO = 0, MOE_PATH_TOKEN_MAJOR = 1, MOE_PATH_GROUPED = 2 } moe_path_t;
 
@@ -286,6 +288,8 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_weights_t* wts,
  * Markers: 0 before the first kernel, then one after each stage, in launch
  * order.  One token on the single-token kernel: 2 markers (before, after).
  * Token-major kernels: 5 (router, top-k + grouping, gate+up, down+blend).
+ * INT4 streaming kernels: 6 (router, top-k + grouping, gate+up, down, combine),
+ * one token 5 (router, top-k, gate+up, down+blend).
  * Grouped tensor-core path: 7 (router, top-k + grouping, gather, gate+up, down,
  * combine).  The pre-expert RMSNorm, when present, runs at the start of the
  * stage after top-k + grouping.
@@ -389,7 +393,7 @@ moe_status_t moe_topk(const moe_topk_config_t* cfg, const void* logits, int64_t 
 
 /* One 4-bit weight matrix [out_features, in_features] (moe_matvec). */
 typedef struct {
-    int32_t out_features;           /* > 0 */
+    int32_t out_features;           /* 1..2^28 */
     int32_t in_features;            /* > 0, a multiple of 32 and of the group size, <= 57344 */
     int32_t w_fmt;                  /* MOE_W_INT4_G32 / G64 / G128 or MOE_W_NVFP4 */
     int32_t x_type;                 /* MOE_BF16 or MOE_F16 */
@@ -411,7 +415,7 @@ typedef struct {
  *               elements apart, aligned to its element; must not overlap x
  * x and out may also be pinned host memory.  No workspace; n == 0 is a no-op.
  * Errors: MOE_ERR_NULL, MOE_ERR_INVALID_CONFIG, MOE_ERR_UNSUPPORTED (a weight
- * format of 8 or 16 bits, more than 57344 in_features), MOE_ERR_ALIGNMENT, MOE_ERR_ALIAS,
+ * format of 8 or 16 bits, more than 57344 in_features or 2^28 out_features), MOE_ERR_ALIGNMENT, MOE_ERR_ALIAS,
  * MOE_ERR_HOST_MEMORY, MOE_ERR_CUDA. */
 moe_status_t moe_matvec(const moe_matvec_config_t* cfg, const moe_qmat_t* w, const float* bias, const void* x,
                         int64_t x_stride, int32_t n, void* out, int64_t out_stride, moe_stream_t stream);

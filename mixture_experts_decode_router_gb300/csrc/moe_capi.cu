@@ -698,7 +698,9 @@ static moe_status_t forward_impl(const moe_config_t* cfg_in, const moe_weights_t
         mk.mark(st);
         return enqueue_experts(cfg, wts, x, n, idx_p, w_p, out, ws, L, true, false, st, mk);
     }
-    if ((s = enqueue_route(cfg, wts, x, n, idx_p, w_p, nullptr, ws, L, true, true, st, mk)) != MOE_OK) return s;
+    // (One token on the streaming path takes its routes ungrouped.)
+    const bool group = !(n == 1 && effective_path(cfg, n) == kPathStream);
+    if ((s = enqueue_route(cfg, wts, x, n, idx_p, w_p, nullptr, ws, L, group, true, st, mk)) != MOE_OK) return s;
     return enqueue_experts(cfg, wts, x, n, idx_p, w_p, out, ws, L, true, routing_plain(cfg->routing), st, mk);
 }
 
@@ -757,7 +759,7 @@ moe_status_t moe_matvec(const moe_matvec_config_t* cfg, const moe_qmat_t* w, con
     if (O < 1 || K < 32 || K % 32 || fmt < MOE_W_BF16 || fmt > MOE_W_INT4_G128) return MOE_ERR_INVALID_CONFIG;
     if (fmt != MOE_W_NVFP4 && !is_int4(fmt)) return MOE_ERR_UNSUPPORTED;
     if (is_int4(fmt) && K % (1 << int4_gshift(fmt))) return MOE_ERR_INVALID_CONFIG;
-    if (!matvec_fits(K)) return MOE_ERR_UNSUPPORTED;
+    if (!matvec_fits(K) || O > 1 << 28) return MOE_ERR_UNSUPPORTED;
     if ((cfg->x_type != MOE_BF16 && cfg->x_type != MOE_F16) || cfg->out_type < MOE_F32 || cfg->out_type > MOE_F16)
         return MOE_ERR_INVALID_CONFIG;
     if ((cfg->accumulate != 0 && cfg->accumulate != 1) || n < 0) return MOE_ERR_INVALID_CONFIG;

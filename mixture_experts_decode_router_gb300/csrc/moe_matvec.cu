@@ -191,7 +191,7 @@ template <int GSH, bool Z, bool XB, int NT>
 cudaError_t launch_nt(const MatvecParams& p, int tp, int num_sms, cudaStream_t st) {
     const int K = p.w.in_dim, n_tiles = (p.w.out_dim + 15) / 16, nst = (K + q4::kStageK - 1) / q4::kStageK;
     // Warps that share a tile: as many as give every SM about its 24 warps (a
-    // 7168 x 7168 product with one token: 12.4 us at 8 a SM, KWNEW us so).
+    // 7168 x 7168 product with one token: 12.4 us with 8, 11.7 us so).
     int kw = 1;
     while (kw < kWarps && kw < nst && (int64_t)n_tiles * kw < (int64_t)num_sms * 20) kw *= 2;
     const size_t smem = smem_plan(K, NT, std::min(tp, p.n), kw).total;
@@ -211,7 +211,15 @@ cudaError_t launch_nt(const MatvecParams& p, int tp, int num_sms, cudaStream_t s
     const int per_sm = std::max(1, std::min(3, (int)((size_t)kMaxSmem / (smem + 1024))));
     const int mw = kWarps / kw;
     const int gx = std::min((n_tiles + mw - 1) / mw, num_sms * per_sm);
-    launch_pdl(kern, dim3(gx, (unsigned)((p.n + tp - 1) / tp)), 32 * kWarps, smem, st, p, kw, tp);
+    // (A grid has at most 65535 rows of blocks.)
+    constexpr int64_t kMaxY = 65535;
+    MatvecParams q = p;
+    for (int64_t n0 = 0; n0 < p.n; n0 += kMaxY * tp) {
+        q.n = (int)std::min<int64_t>(p.n - n0, kMaxY * tp);
+        q.x = static_cast<const uint16_t*>(p.x) + n0 * p.x_stride;
+        q.out = static_cast<uint8_t*>(p.out) + n0 * p.out_stride * (p.out_type == MOE_F32 ? 4 : 2);
+        launch_pdl(kern, dim3(gx, (unsigned)((q.n + tp - 1) / tp)), 32 * kWarps, smem, st, q, kw, tp);
+    }
     return cudaGetLastError();
 }
 

@@ -514,8 +514,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? kMinBlocks : 1) topk_
             const float thr = at_k - (fabsf(at_k) * (2.f * bucket) + 2.f * serr + 0x1p-21f * fabsf(at_k) + 1e-38f);
             int* list = reinterpret_cast<int*>(sc);
             const int total = compact<V>([&](int i) { return ((alive >> i) & 1u) && s[i] >= thr; }, e0, lane, list);
-            // (-inf or NaN at the k-th, a softmax with a bias, unclear groups: every score in 64 bits.)
-            if (gclear && !__any_sync(0xffffffffu, nan) && at_k > -3.0e38f && total <= 32 && !(biased && !sig)) {
+            // (Infinite scores, NaN, a softmax with a bias, unclear groups: every score in 64 bits.)
+            if (gclear && !__any_sync(0xffffffffu, nan) && fabsf(at_k) < 3.0e38f && total >= k && total <= 32 && !(biased && !sig)) {
                 const int ce = lane < total ? list[lane] : 0;
                 // By their whole 32-bit scores, if these are clear; else in 64 bits.
                 const float v32 = lane < total ? (biased ? ss : sl)[ce] : -INFINITY;

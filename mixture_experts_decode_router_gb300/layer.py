@@ -165,6 +165,12 @@ def _device_of(t: torch.Tensor) -> int:
     return dev
 
 
+def _check_routes(t: torch.Tensor, dtype, n: int, k: int, dev: int) -> None:
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] < n or t.shape[1] != k or not t.is_contiguous() \
+            or t.get_device() != dev:
+        raise ValueError(f"idx is int32 and w float32, contiguous [>= {n}, {k}] on cuda:{dev}")
+
+
 class MoeTopk:
     """Top-k routing of logits the caller holds (``moe_topk``): ``forward(logits)``
     returns ``(idx, w)`` of ``[n, num_experts]`` fp32, bf16 or fp16 logits, whose
@@ -204,10 +210,16 @@ class MoeTopk:
         if len(shape) != 2 or shape[1] != E or (E > 1 and strides[1] != 1):
             raise ValueError("logits are [n, num_experts] with contiguous rows")
         n, dev = shape[0], _device_of(logits)
+        if self.bias is not None and self.bias.get_device() != dev:
+            raise ValueError(f"bias on {self.bias.device}, but the current device is cuda:{dev}")
         if idx is None:
             idx = torch.empty((n, k), dtype=torch.int32, device=dev)
+        else:
+            _check_routes(idx, torch.int32, n, k, dev)
         if w is None:
             w = torch.empty((n, k), dtype=torch.float32, device=dev)
+        else:
+            _check_routes(w, torch.float32, n, k, dev)
         s = self._topk(cfg, logits.data_ptr(), strides[0] if n > 1 else E, self._bias, n, idx.data_ptr(),
                        w.data_ptr(), B.raw_stream(dev) if stream is None else B._stream(stream))
         if s:
@@ -242,6 +254,9 @@ class MoeMatvec:
         self.weights, self.bias, self.out_dtype = q, bias, out_dtype
         self.in_features, self.out_features, self.accumulate = in_f, out_f, accumulate
         self._bias = None if bias is None else bias.data_ptr()
+        self._dev = q.w.get_device()
+        if any(t is not None and t.get_device() != self._dev for t in (q.scale, q.scale2, q.zero, bias)):
+            raise ValueError("weights and bias on one device")
         self._matvec = B.entry("moe_matvec")
 
     def forward(self, x: torch.Tensor, out=None, stream=None):
@@ -250,12 +265,15 @@ class MoeMatvec:
         if len(shape) != 2 or shape[1] != K or strides[1] != 1:
             raise ValueError("x is [n, in] with contiguous rows")
         n, dev = shape[0], _device_of(x)
+        if self._dev != dev:
+            raise ValueError(f"weights on {self.weights.w.device}, but the current device is cuda:{dev}")
         ostride = O
         if out is None:
             if self.accumulate:
                 raise ValueError("accumulate needs out")
             out = torch.empty((n, O), dtype=self.out_dtype, device=dev)
         else:
+            _device_of(out)
             if out.shape != (n, O) or out.dtype != self.out_dtype or (O > 1 and out.stride(1) != 1):
                 raise ValueError("out is [n, out] of out_dtype with contiguous rows")
             if n > 1:

@@ -289,6 +289,83 @@ def test_captured_and_replayed(lib, n):
 
 
 @gpu
+@pytest.mark.parametrize("n", [1, 5, 40])
+def test_pinned_input_and_output(lib, n):
+    cfg = cfg_of("int4_g32")
+    lw, x, layer, out, idx, w = check(cfg, n)
+    xh, oh = x.cpu().pin_memory(), torch.empty(n, cfg.hidden, dtype=torch.bfloat16).pin_memory()
+    layer.forward(xh, out=oh, idx=torch.empty_like(idx), w=torch.empty_like(w))
+    torch.cuda.synchronize()
+    assert torch.equal(oh, out.cpu())
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 2, 6, 30])
+def test_route_then_experts_is_forward(lib, n):
+    cfg = cfg_of("int4_g64", zero_points=True, shared_gate=True)
+    lw, x, layer, out, idx, w = check(cfg, n)
+    i2, w2, _ = layer.route(x)
+    assert torch.equal(i2, idx) and torch.equal(w2, w)
+    assert torch.equal(layer.experts(x, i2, w2), out)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 20])
+def test_zero_points_in_some_matrices(lib, n):
+    """Zero points for up and the shared down alone, and at an odd address."""
+    cfg = cfg_of("int4_g32", zero_points=True)
+    lw = synth.make_weights(cfg, "cuda")
+    for m in ("gate", "down", "sh_gate", "sh_up"):
+        setattr(lw, m, dataclasses.replace(getattr(lw, m), zero=None))
+    buf = torch.zeros(lw.up.zero.numel() + 1, dtype=torch.uint8, device="cuda")
+    odd = buf[1:].view(lw.up.zero.shape)
+    odd.copy_(lw.up.zero)
+    lw.up = dataclasses.replace(lw.up, zero=odd)
+    for path in ("auto", "token_major", "grouped"):
+        check(cfg, n, path, lw=lw)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 2, 9])
+def test_magnitudes(lib, n):
+    """Inputs far from 1: activations that f16 would hold as zero or infinity."""
+    cfg = cfg_of("int4_g64", shared_inter=0)
+    lw = synth.make_weights(cfg, "cuda")
+    L = int4_oracle_layer(lw)
+    for scale in (2.0 ** -14, 2.0 ** 14):
+        x = synth.make_input(cfg, n, "cuda") * scale
+        g = torch.Generator().manual_seed(n)
+        idx = torch.randint(0, 16, (n, 2), generator=g).to(torch.int32).cuda()
+        w = torch.rand(n, 2, generator=g).cuda()
+        out = MoeLayer(lw, n).experts(x, idx, w)
+        xe = O.bf16_decode(bf16_bits(x))
+        ref = np.zeros((n, cfg.hidden))
+        for t in range(n):
+            for j in range(2):
+                e = int(idx[t, j])
+                ref[t] += float(w[t, j]) * O.swiglu_mlp(xe[t], L.gate.expert(e), L.up.expert(e), L.down.expert(e))
+        close(out.float().cpu().numpy(), ref)
+
+
+@gpu
+def test_many_tokens_of_one_expert(lib):
+    """Every token on the same two experts: segments of every length up to the tile, and past it."""
+    cfg = cfg_of("int4_g32", zero_points=True)
+    lw = synth.make_weights(cfg, "cuda")
+    L = int4_oracle_layer(lw)
+    for n in (7, 8, 9, 15, 16, 17, 33):
+        x = synth.make_input(cfg, n, "cuda")
+        idx = torch.tensor([[3, 9]] * n, dtype=torch.int32, device="cuda")
+        w = torch.full((n, 2), 0.5, device="cuda")
+        out = MoeLayer(lw, n).experts(x, idx, w)
+        xe = O.bf16_decode(bf16_bits(x))
+        ref = O.swiglu_mlp(xe, L.sh_gate.expert(0), L.sh_up.expert(0), L.sh_down.expert(0))
+        for e in (3, 9):
+            ref = ref + 0.5 * O.swiglu_mlp(xe, L.gate.expert(e), L.up.expert(e), L.down.expert(e))
+        close(out.float().cpu().numpy(), ref)
+
+
+@gpu
 def test_special_values_stay_in_their_row(lib):
     """NaN and infinity in one token's input do not reach another token's output."""
     cfg = cfg_of("int4_g32", n_tokens=9)

@@ -34,6 +34,8 @@ def test_refusals():
     q = B.moe_qmat_t()
     assert B.moe_matvec(None, q, None, FAKE, 32, 1, FAKE, 32, 0) == B.MOE_ERR_NULL
     assert B.moe_matvec(B.moe_matvec_config_t(), None, None, FAKE, 32, 1, FAKE, 32, 0) == B.MOE_ERR_NULL
+    assert _call(out=(1 << 28) + 1, ys=(1 << 28) + 1) == B.MOE_ERR_UNSUPPORTED
+    assert _call(inp=57344 + 64, xs=57344 + 64) == B.MOE_ERR_UNSUPPORTED
     for kw in (dict(out=0), dict(inp=0), dict(inp=48, xs=48), dict(inp=96, xs=96), dict(fmt=6), dict(fmt=-1),
                dict(x_type=B.MOE_F32), dict(x_type=3), dict(out_type=3), dict(acc=2), dict(n=-1), dict(xs=255),
                dict(xs=248), dict(ys=63)):
@@ -215,6 +217,57 @@ def test_special_values_stay_in_their_row(lib, fmt):
     assert torch.equal(got[keep], want[keep])
     assert torch.isnan(got[3]).all()
     assert not torch.isfinite(got[5][torch.tensor(w[:, 200] != 0)]).any()
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["int4_g128", "nvfp4"])
+@pytest.mark.parametrize("n", [1, 3, 12])
+def test_the_longest_rows(lib, fmt, n):
+    """Rows of x of which few fit in shared memory beside the kernel's rings."""
+    for K in (16384, 57344):
+        q, w = matrix(19, K, fmt)
+        x = rows(n, K, seed=n)
+        y = MoeMatvec(q, out_dtype=torch.float32).forward(x)
+        close(y, x, w)
+        assert torch.equal(MoeMatvec(q, out_dtype=torch.float32).forward(x[n - 1:]), y[n - 1:])
+
+
+@gpu
+def test_more_rows_than_a_grid_has(lib):
+    """More rows of x than 65535 rows of blocks of eight or sixteen."""
+    q, w = matrix(3, 32, "int4_g32")
+    n = 65535 * 16 + 5
+    x = rows(n, 32)
+    y = MoeMatvec(q, out_dtype=torch.float32).forward(x)
+    close(y, x, w)
+
+
+@gpu
+def test_two_streams_at_once(lib):
+    qs = [matrix(300, 1024, f, seed=i)[0] for i, f in enumerate(("int4_g64", "nvfp4"))]
+    ops, x = [MoeMatvec(q) for q in qs], rows(7, 1024)
+    want = [op.forward(x).clone() for op in ops]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for st, op in zip(streams, ops):
+            with torch.cuda.stream(st):
+                got.append([op.forward(x) for _ in range(3)])
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, r) for ys, r in zip(got, want) for y in ys)
+
+
+@gpu
+def test_weights_elsewhere(lib):
+    w, s, _ = synth.quant_int4(torch.randn(16, 64), 32)
+    x = rows(2, 64)
+    with pytest.raises(ValueError):
+        MoeMatvec(synth.QMatT("int4_g32", w, s)).forward(x)              # weights on the CPU
+    with pytest.raises(ValueError):
+        MoeMatvec(synth.QMatT("int4_g32", w.cuda(), s))
+    with pytest.raises(ValueError):
+        MoeMatvec(synth.QMatT("int4_g32", w.cuda(), s.cuda())).forward(x, out=torch.empty(2, 16, dtype=torch.bfloat16))
 
 
 @gpu

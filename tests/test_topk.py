@@ -321,6 +321,66 @@ def test_nan_ranks_last(lib):
 
 
 @gpu
+@pytest.mark.parametrize("groups,kept", [(1, 1), (8, 2)])
+@pytest.mark.parametrize("score", ["max", "top2"])
+def test_infinite_logits(lib, groups, kept, score):
+    """+inf in one, a few, and all places: a sigmoid of 1, and the first by its logit."""
+    lg = draw(9, 64, seed=12).clone()
+    lg[0, 7] = lg[1, 3] = lg[1, 50] = float("inf")
+    lg[2, 10:30] = float("inf")
+    lg[3] = float("inf")
+    lg[4, 5], lg[4, 6:] = float("inf"), -float("inf")
+    for b in (None, bias_of(64)):
+        idx, w = check(lg, 4, "sigmoid", b, groups, kept, score)
+        assert torch.isfinite(w).all()
+    idx, _ = MoeTopk(64, 4).forward(lg)
+    order = lg.sort(dim=1, descending=True, stable=True).indices[:, :4]
+    assert torch.equal(idx.long(), order)
+
+
+@gpu
+def test_infinite_bias(lib):
+    """A bias of -inf keeps an expert out while others are left; +inf takes it first."""
+    lg, b = draw(20, 64, seed=13), bias_of(64)
+    b[::2] = -float("inf")
+    b[5] = float("inf")
+    idx, _ = check(lg, 4, "sigmoid", b)
+    assert (idx[:, 0] == 5).all() and (idx % 2 == 1).all()
+
+
+@gpu
+def test_two_streams_at_once(lib):
+    lg = [draw(500, 256, seed=s) for s in (20, 21)]
+    ops = [MoeTopk(256, 8, "sigmoid", bias_of(256), 8, 4), MoeTopk(256, 6)]
+    want = [[tuple(t.clone() for t in op.forward(l)) for l in lg] for op in ops]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for st, op in zip(streams, ops):
+            with torch.cuda.stream(st):
+                got.append([op.forward(l) for l in lg])
+        torch.cuda.synchronize()
+        for g2, w2 in zip(got, want):
+            for (i, w), (ri, rw) in zip(g2, w2):
+                assert torch.equal(i, ri) and torch.equal(w, rw)
+
+
+@gpu
+def test_given_outputs_are_checked(lib):
+    lg = draw(4, 64)
+    op = MoeTopk(64, 4)
+    good = torch.empty(4, 4, dtype=torch.int32, device="cuda")
+    for bad in (good.long(), good[:3], good[:, :3], good.cpu(), torch.empty(4, 8, dtype=torch.int32, device="cuda")[:, ::2]):
+        with pytest.raises(ValueError):
+            op.forward(lg, idx=bad)
+    with pytest.raises(ValueError):
+        op.forward(lg, w=good)
+    with pytest.raises(ValueError):
+        MoeTopk(64, 4, "sigmoid", torch.zeros(64)).forward(lg)      # a bias on the CPU
+
+
+@gpu
 def test_many_rows_past_32_bit_offsets(lib):
     """Rows whose offset in elements passes 2^31: the last rows are those of a small call."""
     stride = 1 << 20
