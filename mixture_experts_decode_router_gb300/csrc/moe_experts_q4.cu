@@ -14,7 +14,7 @@
 //   One token: gate_up_n1 and down_n1 take the routes as they are (no grouping),
 //   split K over a block's warps, and down_n1 adds the slots and writes the output.
 //
-// act enters the down product as f16, each token's chunk of 768 scaled by a power of
+// act enters the down product as f16, each token's chunk of 768 (one token: 256) scaled by a power of
 // two that puts its largest value below 2^15: one rounding to 11 significand bits
 // down to 2^-29 of that value, at any magnitude.  Chunks and order of every sum
 // depend on the layer's sizes alone, so a token's bits do not depend on its batch.
@@ -32,15 +32,17 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;                 // ring of each warp
 constexpr int kRing = kWarps * kStages * q4::kStageBytes;
+constexpr int kStages2 = 2;                // of one token's gate and up together
+constexpr int kRing2 = kWarps * kStages2 * 2 * q4::kStageBytes;
 constexpr int kActStages = 3;              // stages of a chunk of act
 constexpr int kXBytes = 16 * (kActStages * 512 + 64);   // rows of x or act in shared memory (25.6 KB: three blocks an SM)
 constexpr int kMaxSmem = 227 * 1024;
 
-// 768 fp32 values of one act row (zero past `left`) as f16 chunks for the fragments,
+// 256 kN fp32 values of one act row (zero past `left`) as f16 chunks for the fragments,
 // by one warp; returns the factor that scales results back.
+template <int kN>
 __device__ __forceinline__ float stage_act(const float* src, int left, uint8_t* dst, int lane) {
-    constexpr int kN = kActStages * q4::kStageK / 256;   // chunks of 8 a lane
-    float v[kN][8];
+    float v[kN][8];   // chunks of 8
     float am = 0.f;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
@@ -169,7 +171,7 @@ __device__ __forceinline__ void run_item(const Q4Params& p, const Item& it, uint
         } else {
             const float* a = it.sh ? p.act_sh : p.act;
             for (int b = warp; b < it.ntok; b += kWarps) {
-                const float f = stage_act(a + (size_t)(it.pos0 + b) * K + c0 * q4::kStageK, K - c0 * q4::kStageK,
+                const float f = stage_act<kActStages>(a + (size_t)(it.pos0 + b) * K + c0 * q4::kStageK, K - c0 * q4::kStageK,
                                           dyn + x0 + b * xstride, lane);
                 if (lane == 0) factor[b] = f;
             }
@@ -249,7 +251,9 @@ __global__ void __launch_bounds__(kThreads, TILE == 8 ? 3 : 2) experts_q4_kernel
 // ---------------------------------------------------------------- one token
 
 // One block per (slot, 16 rows of I) and (shared expert, 16 rows of S): its warps take
-// every eighth stage of gate and up, their sums added in warp order.
+// every eighth stage of gate and up together, their sums added in warp order.  (One
+// matrix after the other, and act staged in chunks of 768: the two kernels took 12.8 us
+// at hidden 2048, intermediate 512, eight experts and a shared one, and take 9.9 us.)
 template <int GSH, bool Z>
 __global__ void __launch_bounds__(kThreads, 3) gate_up_n1_kernel(const Q4Params p) {
     extern __shared__ __align__(128) uint8_t dyn[];
@@ -266,39 +270,38 @@ __global__ void __launch_bounds__(kThreads, 3) gate_up_n1_kernel(const Q4Params 
     const int64_t srow = (int64_t)(sh ? 0 : e - p.e_begin) * out + row0;
     const QMatDev& m0 = sh ? p.sh_gate : p.gate;
     const QMatDev& m1 = sh ? p.sh_up : p.up;
-    const uint32_t ring = warp * kStages * q4::kStageBytes, ring_a = q4::smem_addr(dyn) + ring;
-    float* red = reinterpret_cast<float*>(dyn + kRing);        // [2][kWarps][16]
-    const uint32_t x0 = kRing + 2 * kWarps * 16 * 4;
-    int wi = warp, mi = 0, wn = warp, mn = 0, i_slot = 0, slot_s = 0;
-    q4::RowCopy cp;
-    q4::ScaleLoad<GSH, Z> sl;
-    q4::StageScales<GSH, Z> sc, nx;
-    cp.start(m0.w, srow, out - row0, row_bytes, wi, lane);
-    sl.start(m0, srow, out - row0, wn, lane);
+    constexpr uint32_t kSlot = 2 * q4::kStageBytes;            // of gate and of up
+    const uint32_t ring = warp * kStages2 * kSlot, ring_a = q4::smem_addr(dyn) + ring;
+    float* red = reinterpret_cast<float*>(dyn + kRing2);       // [2][kWarps][16]
+    const uint32_t x0 = kRing2 + 2 * kWarps * 16 * 4;
+    int i_s = warp, n_s = warp, i_slot = 0, slot_s = 0;
+    q4::RowCopy cp[2];
+    q4::ScaleLoad<GSH, Z> sl[2];
+    q4::StageScales<GSH, Z> sc[2], nx[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        cp[m].start(m ? m1.w : m0.w, srow, out - row0, row_bytes, i_s, lane);
+        sl[m].start(m ? m1 : m0, srow, out - row0, n_s, lane);
+    }
     auto issue = [&]() {
-        if (mi < 2 && wi < nst) {
-            cp.issue(ring_a + i_slot * q4::kStageBytes, wi, kWarps, row_bytes, full, m0.w, lane);
-            wi += kWarps;
-            if (wi >= nst && ++mi < 2) {
-                wi = warp;
-                cp.start(m1.w, srow, out - row0, row_bytes, wi, lane);
-            }
+        if (i_s < nst) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                cp[m].issue(ring_a + i_slot * kSlot + m * q4::kStageBytes, i_s, kWarps, row_bytes, full, m0.w, lane);
+            i_s += kWarps;
         }
         q4::cp_commit();
-        i_slot = i_slot + 1 == kStages ? 0 : i_slot + 1;
+        i_slot = i_slot + 1 == kStages2 ? 0 : i_slot + 1;
     };
     auto load_scales = [&]() {
-        if (mn < 2 && wn < nst) {
-            sl.load(nx, wn, kWarps, K, lane);
-            wn += kWarps;
-            if (wn >= nst && ++mn < 2) {
-                wn = warp;
-                sl.start(m1, srow, out - row0, wn, lane);
-            }
+        if (n_s < nst) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) sl[m].load(nx[m], n_s, kWarps, K, lane);
+            n_s += kWarps;
         }
     };
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) issue();
+    for (int s = 0; s < kStages2 - 1; ++s) issue();
     load_scales();
     for (int c = threadIdx.x; c < nst * 32; c += kThreads)
         *reinterpret_cast<uint4*>(dyn + x0 + c * 16) =
@@ -307,17 +310,18 @@ __global__ void __launch_bounds__(kThreads, 3) gate_up_n1_kernel(const Q4Params 
     q4::XView<1> x;
     x.start(x0, 0, 1, lane);
     float acc[2][1][4] = {};
+    for (int s = warp; s < nst; s += kWarps) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-        for (int s = warp; s < nst; s += kWarps) {
-            sc = nx;
-            load_scales();
-            q4::cp_wait<kStages - 2>();
-            __syncwarp();
-            issue();
-            q4::mma_stage<GSH, Z, true, 1>(dyn, ring + slot_s * q4::kStageBytes, x, s, sc, acc[m], lane);
-            slot_s = slot_s + 1 == kStages ? 0 : slot_s + 1;
-        }
+        for (int m = 0; m < 2; ++m) sc[m] = nx[m];
+        load_scales();
+        q4::cp_wait<kStages2 - 2>();
+        __syncwarp();
+        issue();
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            q4::mma_stage<GSH, Z, true, 1>(dyn, ring + slot_s * kSlot + m * q4::kStageBytes, x, s, sc[m], acc[m], lane);
+        slot_s = slot_s + 1 == kStages2 ? 0 : slot_s + 1;
+    }
     if ((lane & 3) == 0) {   // column 0: rows g and g + 8
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
@@ -345,12 +349,11 @@ __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row0 = blockIdx.x * 16, rows = p.H - row0;
     const int nr = (p.I + q4::kStageK - 1) / q4::kStageK, ns = (p.S + q4::kStageK - 1) / q4::kStageK;
-    const int ca = (nr + kActStages - 1) / kActStages, cb = (ns + kActStages - 1) / kActStages;   // chunks of a row
-    const int units = p.k * nr + ns, chunks = p.k * ca + cb;
+    const int units = p.k * nr + ns;
     const uint32_t ring = warp * kStages * q4::kStageBytes, ring_a = q4::smem_addr(dyn) + ring;
     float* red = reinterpret_cast<float*>(dyn + kRing);             // [kWarps][16]
-    float* cf = red + kWarps * 16;                                  // weight and factor of each chunk
-    const uint32_t x0 = kRing + kWarps * 64 + ((chunks * 4 + 15) & ~15);
+    float* cf = red + kWarps * 16;                                  // weight and factor of each unit
+    const uint32_t x0 = kRing + kWarps * 64 + ((units * 4 + 15) & ~15);
     pdl_wait();
     pdl_trigger();
     // Unit u: stage u % nr of slot u / nr, then the shared expert's stages.
@@ -399,15 +402,13 @@ __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) 
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue();
     load_scales();
-    // Every slot's act in chunks of kActStages stages.
-    for (int c = warp; c < chunks; c += kWarps) {
-        const bool sh = c >= p.k * ca;
-        const int slot = sh ? p.k : c / ca, i = sh ? c - p.k * ca : c - slot * ca, K = sh ? p.S : p.I;
-        const int e = sh ? 0 : __ldg(p.idx + slot);
-        if (!sh && (e < p.e_begin || e >= p.e_end)) continue;
-        const float* a = (sh ? p.act_sh : p.act + (size_t)slot * p.I) + i * kActStages * q4::kStageK;
-        const float f = stage_act(a, K - i * kActStages * q4::kStageK, dyn + x0 + c * (kActStages * 512), lane);
-        if (lane == 0) cf[c] = f * (sh ? shared_gate(p.sg_logit, 0) : __ldg(p.route_w + slot));
+    // Every slot's act, a warp a stage.
+    for (int u = warp; u < units; u += kWarps) {
+        const Unit a = unit(u);
+        if (!a.held) continue;
+        const float* src = (a.slot == p.k ? p.act_sh : p.act + (size_t)a.slot * p.I) + a.s * q4::kStageK;
+        const float f = stage_act<1>(src, a.K - a.s * q4::kStageK, dyn + x0 + u * 512, lane);
+        if (lane == 0) cf[u] = f * (a.slot == p.k ? shared_gate(p.sg_logit, 0) : __ldg(p.route_w + a.slot));
     }
     __syncthreads();
     float total[4] = {0.f, 0.f, 0.f, 0.f};
@@ -419,12 +420,11 @@ __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) 
         __syncwarp();
         issue();
         if (a.held) {
-            const int c = (a.slot == p.k ? p.k * ca : a.slot * ca) + a.s / kActStages;
             q4::XView<1> x;
-            x.start(x0 + c * (kActStages * 512), 0, 1, lane);
+            x.start(x0 + u * 512, 0, 1, lane);
             float acc[1][4] = {};
-            q4::mma_stage<GSH, Z, false, 1>(dyn, ring + slot_s * q4::kStageBytes, x, a.s % kActStages, sc, acc, lane);
-            const float w = cf[c];
+            q4::mma_stage<GSH, Z, false, 1>(dyn, ring + slot_s * q4::kStageBytes, x, 0, sc, acc, lane);
+            const float w = cf[u];
 #pragma unroll
             for (int i = 0; i < 4; ++i) total[i] = fmaf(acc[0][i], w, total[i]);
         }
@@ -445,11 +445,10 @@ __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) 
     }
 }
 
-size_t gate_up_n1_smem(int H) { return kRing + 2 * kWarps * 64 + (size_t)q4::x_row_bytes(H); }
+size_t gate_up_n1_smem(int H) { return kRing2 + 2 * kWarps * 64 + (size_t)q4::x_row_bytes(H); }
 size_t down_n1_smem(int k, int I, int S) {
-    const int chunk = kActStages * q4::kStageK;
-    const size_t chunks = (size_t)k * ((I + chunk - 1) / chunk) + (S + chunk - 1) / chunk;
-    return kRing + kWarps * 64 + ((chunks * 4 + 15) & ~size_t(15)) + chunks * kActStages * 512;
+    const size_t units = (size_t)k * ((I + q4::kStageK - 1) / q4::kStageK) + (S + q4::kStageK - 1) / q4::kStageK;
+    return kRing + kWarps * 64 + ((units * 4 + 15) & ~size_t(15)) + units * 512;
 }
 
 template <typename Kern>
