@@ -18,6 +18,16 @@
 // two that puts its largest value below 2^15: one rounding to 11 significand bits
 // down to 2^-29 of that value, at any magnitude.  Chunks and order of every sum
 // depend on the layer's sizes alone, so a token's bits do not depend on its batch.
+//
+// On GB300 (hidden 2048, intermediate 512, 8 of 256 experts and a shared one): one token
+// 9.9 us (1.5 TB/s), 16 tokens with groups of 64 and zero points 65 us (2.7 TB/s), 256
+// rows with groups of 32 212 us (2.1 TB/s); hidden 7168, intermediate 2048, 8 of 64
+// experts, 64 tokens 486 us (3.0 TB/s).  The copies and the staging alone take 41, 125
+// and 306 us of the last three; the rest is what the warps' instructions do not overlap.
+// (Measured and not kept: the rows of x prepared once by a kernel of their own and read
+// through L1 by warps that share nothing, 70, 273 and 547 us; two row tiles a warp for
+// each staging, 67, 226 and 511 us; four blocks an SM with rings of two stages, 85, 229
+// and 586 us.)
 #include <algorithm>
 #include <mutex>
 

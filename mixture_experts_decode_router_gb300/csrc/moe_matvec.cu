@@ -1,7 +1,14 @@
 // moe_matvec.cu -- products of 4-bit group-scaled matrices with a few vectors
 // (sm_103a): out[t, o] = sum_i W[o, i] x[t, i] (+ bias[o]) (+ out[t, o]).
 //
-// Bound by the weight stream.  Blocks of 8 warps; a warp multiplies 16 rows
+// Bound by the instructions on the weight stream (q4_mma.cuh).  On GB300: 100003 x 2048,
+// groups of 32, six tokens 33.4 us (3.5 TB/s); 7168 x 7168 with zero points, one token
+// 9.1 us (3.1 TB/s); 2048 x 2048 2.8 us, launch and latency.  Without the products the
+// first takes 21 us.  (Stretches of stages that split the tiles of a part evenly over a
+// block's warps, which balances the rounds, took 35 us: the copies of a block's warps
+// then lie apart in K.)
+//
+// Blocks of 8 warps; a warp multiplies 16 rows
 // (q4_mma.cuh) and kw warps share a tile of rows, each with every kw-th stage of
 // K, their sums added in warp order through shared memory.  Blocks are
 // persistent over the row tiles, the warps' copies running ahead across tiles.
@@ -191,7 +198,7 @@ template <int GSH, bool Z, bool XB, int NT>
 cudaError_t launch_nt(const MatvecParams& p, int tp, int num_sms, cudaStream_t st) {
     const int K = p.w.in_dim, n_tiles = (p.w.out_dim + 15) / 16, nst = (K + q4::kStageK - 1) / q4::kStageK;
     // Warps that share a tile: as many as give every SM about its 24 warps (a
-    // 7168 x 7168 product with one token: 12.4 us with 8, 11.7 us so).
+    // 7168 x 7168 product with one token: 10.6 us with 8, 9.1 us so).
     int kw = 1;
     while (kw < kWarps && kw < nst && (int64_t)n_tiles * kw < (int64_t)num_sms * 20) kw *= 2;
     const size_t smem = smem_plan(K, NT, std::min(tp, p.n), kw).total;
