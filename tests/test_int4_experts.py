@@ -366,6 +366,87 @@ def test_many_tokens_of_one_expert(lib):
 
 
 @gpu
+@pytest.mark.parametrize("n,marks", [(1, 5), (2, 6), (9, 6)])
+def test_timed_markers(lib, n, marks):
+    """The markers that moe.h counts for the streaming kernels, in stream order, and the same bits."""
+    cfg = cfg_of("int4_g64")
+    lw, x, layer, out, idx, w = check(cfg, n)
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(8)]
+    for e in ev:
+        e.record()
+    got = torch.empty_like(out)
+    s, nm = B.moe_forward_timed(layer.c_cfg, layer.c_w, x, n, got, torch.empty_like(idx), torch.empty_like(w), layer.ws,
+                                layer.ws_bytes, None, [e.cuda_event for e in ev])
+    torch.cuda.synchronize()
+    assert s == B.MOE_OK and nm == marks
+    assert torch.equal(got, out)
+    assert all(ev[i].elapsed_time(ev[i + 1]) >= 0 for i in range(nm - 1))
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_accumulate_adds_to_the_output(lib, n):
+    cfg = cfg_of("int4_g32", zero_points=True)
+    lw, x, _, out, idx, w = check(cfg, n)
+    was = torch.randn(n, cfg.hidden, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16).cuda()
+    got = MoeLayer(lw, n, accumulate=True).forward(x, out=was.clone())[0]
+    L = int4_oracle_layer(lw)
+    ref = O.moe_forward(L, bf16_bits(x))[0] + was.double().cpu().numpy()
+    close(got.float().cpu().numpy(), ref)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 10])
+def test_two_streams_at_once(lib, n):
+    """Two layers, a workspace each, on two streams; then two streams sharing the weights."""
+    cfg = cfg_of("int4_g64")
+    lw = synth.make_weights(cfg, "cuda")
+    xs = [synth.make_input(cfg, n, "cuda", stream=s) for s in range(2)]
+    layers = [MoeLayer(lw, n) for _ in range(2)]
+    want = [l.forward(x)[0].clone() for l, x in zip(layers, xs)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for st, l, x in zip(streams, layers, xs):
+            with torch.cuda.stream(st):
+                got.append([l.forward(x)[0] for _ in range(3)])
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, r) for ys, r in zip(got, want) for y in ys)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 6])
+def test_static_workspace(lib, n):
+    cfg = cfg_of("int4_g128")
+    lw, x, layer, out, idx, w = check(cfg, n)
+    got, i2, w2 = torch.empty_like(out), torch.empty_like(idx), torch.empty_like(w)
+    assert B.moe_forward_static_ws(layer.c_cfg, layer.c_w, x, n, got, i2, w2) == B.MOE_OK
+    torch.cuda.synchronize()
+    assert torch.equal(got, out) and torch.equal(i2, idx) and torch.equal(w2, w)
+    assert B.moe_static_workspace_check()[:2] == (B.MOE_OK, 0)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 2, 9, 40])
+def test_a_workspace_as_large_as_it_says(lib, n):
+    """A workspace of exactly moe_workspace_bytes in front of a guard: nothing past its end is
+    written, and one byte less is refused."""
+    cfg = cfg_of("int4_g32", inter=160, shared_inter=96)
+    lw, x, layer, out, idx, w = check(cfg, n)
+    size = B.moe_workspace_bytes(layer.c_cfg, n)
+    buf = torch.zeros(size + 4096, dtype=torch.uint8, device="cuda")
+    buf[size:] = 0xA5
+    got = torch.empty(n * cfg.hidden + 512, dtype=torch.bfloat16, device="cuda").fill_(3.0)
+    s = B.moe_forward(layer.c_cfg, layer.c_w, x, n, got, torch.empty_like(idx), torch.empty_like(w), buf, size)
+    torch.cuda.synchronize()
+    assert s == B.MOE_OK
+    assert torch.equal(got[:n * cfg.hidden].view(n, -1), out) and (got[n * cfg.hidden:] == 3.0).all()
+    assert (buf[size:] == 0xA5).all()
+    assert B.moe_forward(layer.c_cfg, layer.c_w, x, n, got, idx, w, buf, size - 1) == B.MOE_ERR_WORKSPACE
+
+
+@gpu
 def test_special_values_stay_in_their_row(lib):
     """NaN and infinity in one token's input do not reach another token's output."""
     cfg = cfg_of("int4_g32", n_tokens=9)
