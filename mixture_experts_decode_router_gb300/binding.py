@@ -259,9 +259,26 @@ class MoeError(RuntimeError):
     pass
 
 
-def entry(name: str):
-    """The library's function, for holders that call it with converted arguments."""
-    return getattr(load(), name)
+_ext = None
+
+
+def tensor_calls():
+    """The extension module whose topk, matvec and experts take torch tensors."""
+    global _ext
+    if _ext is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (the extension links to its libraries)
+        lib = load()
+        spec = importlib.util.spec_from_file_location(
+            "_moe_torch", _build.EXT, loader=importlib.machinery.ExtensionFileLoader("_moe_torch", _build.EXT))
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+        addr = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in ("moe_topk", "moe_matvec", "moe_experts")]
+        ext.bind(*addr, check)
+        _ext = ext
+    return _ext
 
 
 def check(status: int) -> None:

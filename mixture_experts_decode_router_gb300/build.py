@@ -13,11 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmoe_gb300.so")
+EXT = os.path.join(BUILD, "_moe_torch.so")       # the holders' calls on torch tensors
+EXT_SRC = os.path.join(CSRC, "moe_torch.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]
@@ -45,8 +48,22 @@ def _compile(nvcc, src, verbose_ptxas=False):
     return obj, r.stderr
 
 
+def _build_ext() -> None:
+    import torch
+    home, cuda = os.path.dirname(torch.__file__), os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           EXT_SRC, "-o", EXT + ".tmp", *("-I" + i for i in inc), "-L" + os.path.join(home, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(EXT + ".tmp", EXT)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT) or os.path.getmtime(EXT_SRC) > os.path.getmtime(EXT):
         return True
     t = os.path.getmtime(LIB)
     deps = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")]
@@ -61,8 +78,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        ext = ex.submit(_build_ext)
         results = list(ex.map(lambda s: _compile(nvcc, s, verbose_ptxas), srcs))
+        ext.result()
     objs = [o for o, _ in results]
     if verbose_ptxas:
         for _, log in results:

@@ -1,0 +1,234 @@
+// moe_torch.cpp -- the holders' calls on torch tensors, as a CPython extension.
+//
+// A small operator's call from Python costs more on the host than on the GPU: 2-3 us
+// on the GPU against 14 us for the checks, the output tensors, the converted arguments
+// and the launch, each a Python call of its own.  Here they are one, which takes
+// 4-5 us.  Argument checks, output tensors and streams only: the library's C
+// functions are called by the addresses that bind() was given.
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/moe.h"
+
+namespace {
+
+decltype(&moe_topk) g_topk;
+decltype(&moe_matvec) g_matvec;
+decltype(&moe_experts) g_experts;
+PyObject* g_check;   // raises a status's error
+
+struct Raised {};    // a Python exception is set
+[[noreturn]] void raise(PyObject* type, const char* what) {
+    PyErr_SetString(type, what);
+    throw Raised{};
+}
+
+// A tensor argument, or null for None.
+const at::Tensor* tensor(PyObject* o) {
+    if (o == Py_None) return nullptr;
+    if (!THPVariable_Check(o)) raise(PyExc_TypeError, "a tensor is expected");
+    return &THPVariable_Unpack(o);
+}
+const at::Tensor& some_tensor(PyObject* o) {
+    const at::Tensor* t = tensor(o);
+    if (!t) raise(PyExc_TypeError, "a tensor is expected");
+    return *t;
+}
+long long integer(PyObject* o) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Raised{};
+    return v;
+}
+template <typename T> T* address(PyObject* o) {
+    void* p = PyLong_AsVoidPtr(o);
+    if (!p && PyErr_Occurred()) throw Raised{};
+    return static_cast<T*>(p);
+}
+template <typename T> T* data(const at::Tensor& t) { return static_cast<T*>(t.data_ptr()); }
+
+// The current GPU: t is on it, or in pinned host memory.
+int current_gpu(const at::Tensor& t) {
+    if (!t.is_cuda() && !t.is_pinned()) raise(PyExc_ValueError, "tensors are on the GPU or in pinned host memory");
+    const int dev = c10::cuda::current_device();
+    if (t.is_cuda() && t.get_device() != dev) raise(PyExc_ValueError, "a tensor is on another device than the current one");
+    return dev;
+}
+moe_stream_t stream_of(PyObject* o, int dev) {
+    return o == Py_None ? (moe_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream()
+                        : address<std::remove_pointer_t<moe_stream_t>>(o);
+}
+at::Tensor matrix(int64_t rows, int64_t cols, at::ScalarType type, c10::Device dev) {
+    return at::empty({rows, cols}, at::TensorOptions().dtype(type).device(dev));
+}
+int type_code(const at::Tensor& t) {
+    switch (t.scalar_type()) {
+        case at::kFloat: return MOE_F32;
+        case at::kBFloat16: return MOE_BF16;
+        case at::kHalf: return MOE_F16;
+        default: return -1;
+    }
+}
+void check(moe_status_t s) {
+    if (s == MOE_OK) return;
+    PyObject* r = PyObject_CallFunction(g_check, "i", (int)s);
+    if (r) {
+        Py_DECREF(r);
+        PyErr_SetString(PyExc_RuntimeError, "a call failed");
+    }
+    throw Raised{};
+}
+PyObject* wrap(at::Tensor t) { return THPVariable_Wrap(std::move(t)); }
+
+void need(Py_ssize_t got, Py_ssize_t want) {
+    if (got != want) raise(PyExc_TypeError, "wrong number of arguments");
+}
+
+// bind(moe_topk, moe_matvec, moe_experts, check): the functions' addresses.
+PyObject* bind(PyObject* const* a, Py_ssize_t n) {
+    need(n, 4);
+    g_topk = reinterpret_cast<decltype(g_topk)>(address<void>(a[0]));
+    g_matvec = reinterpret_cast<decltype(g_matvec)>(address<void>(a[1]));
+    g_experts = reinterpret_cast<decltype(g_experts)>(address<void>(a[2]));
+    Py_INCREF(a[3]);
+    Py_XDECREF(g_check);
+    g_check = a[3];
+    Py_RETURN_NONE;
+}
+
+void check_routes(const at::Tensor& t, at::ScalarType type, int64_t n, int64_t k, int dev) {
+    if (t.scalar_type() != type || t.dim() != 2 || t.size(0) < n || t.size(1) != k || !t.is_contiguous() ||
+        !t.is_cuda() || t.get_device() != dev)
+        raise(PyExc_ValueError, "idx is int32 and w float32, contiguous [>= n, k] on the current device");
+}
+
+// topk(config address, bias or None, logits, idx or None, w or None, stream or None) -> (idx, w)
+PyObject* topk(PyObject* const* a, Py_ssize_t na) {
+    need(na, 6);
+    moe_topk_config_t c = *address<const moe_topk_config_t>(a[0]);
+    const at::Tensor* bias = tensor(a[1]);
+    const at::Tensor& l = some_tensor(a[2]);
+    const at::Tensor *gi = tensor(a[3]), *gw = tensor(a[4]);
+    const int64_t E = c.num_experts, k = c.top_k;
+    c.logits_type = type_code(l);
+    if (c.logits_type < 0) raise(PyExc_KeyError, "logits are float32, bfloat16 or float16");
+    if (l.dim() != 2 || l.size(1) != E || (E > 1 && l.stride(1) != 1))
+        raise(PyExc_ValueError, "logits are [n, num_experts] with contiguous rows");
+    const int dev = current_gpu(l);
+    if (bias && (!bias->is_cuda() || bias->get_device() != dev)) raise(PyExc_ValueError, "bias is not on the current device");
+    const int64_t n = l.size(0);
+    const c10::Device on(c10::kCUDA, (c10::DeviceIndex)dev);
+    if (gi) check_routes(*gi, at::kInt, n, k, dev);
+    if (gw) check_routes(*gw, at::kFloat, n, k, dev);
+    at::Tensor idx = gi ? *gi : matrix(n, k, at::kInt, on), w = gw ? *gw : matrix(n, k, at::kFloat, on);
+    if (n > INT32_MAX) raise(PyExc_ValueError, "too many rows");
+    const void* lp = l.data_ptr();
+    const float* bp = bias ? data<const float>(*bias) : nullptr;
+    int32_t* ip = data<int32_t>(idx);
+    float* wp = data<float>(w);
+    const int64_t stride = n > 1 ? l.stride(0) : E;
+    const moe_stream_t st = stream_of(a[5], dev);
+    moe_status_t s;
+    Py_BEGIN_ALLOW_THREADS;
+    s = g_topk(&c, lp, stride, bp, (int32_t)n, ip, wp, st);
+    Py_END_ALLOW_THREADS;
+    check(s);
+    return Py_BuildValue("(NN)", wrap(std::move(idx)), wrap(std::move(w)));
+}
+
+// matvec(config address, matrix address, bias address, the weights' device, x, out or None, stream or None) -> out
+PyObject* matvec(PyObject* const* a, Py_ssize_t na) {
+    need(na, 7);
+    moe_matvec_config_t c = *address<const moe_matvec_config_t>(a[0]);
+    const moe_qmat_t* q = address<const moe_qmat_t>(a[1]);
+    const float* bias = address<const float>(a[2]);
+    const long long wdev = integer(a[3]);
+    const at::Tensor& x = some_tensor(a[4]);
+    const at::Tensor* given = tensor(a[5]);
+    const int64_t K = c.in_features, O = c.out_features;
+    c.x_type = type_code(x);
+    if (c.x_type != MOE_BF16 && c.x_type != MOE_F16) raise(PyExc_KeyError, "x is bfloat16 or float16");
+    if (x.dim() != 2 || x.size(1) != K || x.stride(1) != 1) raise(PyExc_ValueError, "x is [n, in] with contiguous rows");
+    const int dev = current_gpu(x);
+    if (wdev != dev) raise(PyExc_ValueError, "the weights are not on the current device");
+    const int64_t n = x.size(0);
+    if (n > INT32_MAX) raise(PyExc_ValueError, "too many rows");
+    int64_t ostride = O;
+    at::Tensor out;
+    if (given) {
+        current_gpu(*given);
+        if (given->dim() != 2 || given->size(0) != n || given->size(1) != O || type_code(*given) != c.out_type ||
+            (O > 1 && given->stride(1) != 1))
+            raise(PyExc_ValueError, "out is [n, out] of out_dtype with contiguous rows");
+        out = *given;
+        if (n > 1) ostride = out.stride(0);
+    } else {
+        if (c.accumulate) raise(PyExc_ValueError, "accumulate needs out");
+        const at::ScalarType type = c.out_type == MOE_F32 ? at::kFloat : c.out_type == MOE_BF16 ? at::kBFloat16 : at::kHalf;
+        out = matrix(n, O, type, c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+    }
+    const void* xp = x.data_ptr();
+    void* op = out.data_ptr();
+    const int64_t stride = n > 1 ? x.stride(0) : K;
+    const moe_stream_t st = stream_of(a[6], dev);
+    moe_status_t s;
+    Py_BEGIN_ALLOW_THREADS;
+    s = g_matvec(&c, q, bias, xp, stride, (int32_t)n, op, ostride, st);
+    Py_END_ALLOW_THREADS;
+    check(s);
+    return wrap(std::move(out));
+}
+
+// experts(config address, weights address, workspace address, its bytes, x, idx, w, stream or None) -> out
+PyObject* experts(PyObject* const* a, Py_ssize_t na) {
+    need(na, 8);
+    const moe_config_t* c = address<const moe_config_t>(a[0]);
+    const moe_weights_t* wts = address<const moe_weights_t>(a[1]);
+    void* ws = address<void>(a[2]);
+    const size_t ws_bytes = (size_t)integer(a[3]);
+    const at::Tensor &x = some_tensor(a[4]), &idx = some_tensor(a[5]), &w = some_tensor(a[6]);
+    if (x.dim() < 1 || x.size(0) > INT32_MAX) raise(PyExc_ValueError, "x is [n, hidden]");
+    const int64_t n = x.size(0);
+    at::Tensor out = matrix(n, c->hidden, at::kBFloat16, x.device());
+    const void* xp = x.data_ptr();
+    const int32_t* ip = static_cast<const int32_t*>(idx.data_ptr());
+    const float* wp = static_cast<const float*>(w.data_ptr());
+    void* op = out.data_ptr();
+    const moe_stream_t st = stream_of(a[7], c10::cuda::current_device());
+    moe_status_t s;
+    Py_BEGIN_ALLOW_THREADS;
+    s = g_experts(c, wts, xp, (int32_t)n, ip, wp, op, ws, ws_bytes, st);
+    Py_END_ALLOW_THREADS;
+    check(s);
+    return wrap(std::move(out));
+}
+
+// No C++ exception leaves a Python call.
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    try {
+        return F(args, n);
+    } catch (const Raised&) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+PyMethodDef methods[] = {
+    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<bind>)), METH_FASTCALL, nullptr},
+    {"topk", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<topk>)), METH_FASTCALL, nullptr},
+    {"matvec", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<matvec>)), METH_FASTCALL, nullptr},
+    {"experts", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<experts>)), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__moe_torch() { return PyModule_Create(&module); }

@@ -5,6 +5,7 @@ the layer happens here.
 
 from __future__ import annotations
 
+from ctypes import addressof
 from typing import Optional
 
 import torch
@@ -110,7 +111,8 @@ class MoeLayer:
         # The control block (first 256 bytes) must start at zero; calls keep it zero.
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
         self.max_tokens = max_tokens
-        self._ws_ptr, self._experts = self.ws.data_ptr(), B.entry("moe_experts")
+        self._experts = B.tensor_calls().experts
+        self._args = (addressof(self.c_cfg), addressof(self.c_w), self.ws.data_ptr(), self.ws_bytes)
 
     def forward(self, x: torch.Tensor, out=None, idx=None, w=None, stream=None,
                 routing: bool = True):
@@ -145,30 +147,7 @@ class MoeLayer:
         return idx, w, lg
 
     def experts(self, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, stream=None):
-        n = x.shape[0]
-        out = torch.empty((n, self.cfg.hidden), dtype=torch.bfloat16, device=x.device)
-        s = self._experts(self.c_cfg, self.c_w, x.data_ptr(), n, idx.data_ptr(), w.data_ptr(), out.data_ptr(),
-                          self._ws_ptr, self.ws_bytes, B._stream(stream))
-        if s:
-            B.check(s)
-        return out
-
-
-def _device_of(t: torch.Tensor) -> int:
-    """The current GPU's index: ``t`` is on it, or in pinned host memory."""
-    at = t.get_device()
-    if at < 0 and not t.is_pinned():
-        raise ValueError("tensors are on the GPU or in pinned host memory")
-    dev = torch.cuda.current_device()
-    if at >= 0 and at != dev:
-        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
-    return dev
-
-
-def _check_routes(t: torch.Tensor, dtype, n: int, k: int, dev: int) -> None:
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] < n or t.shape[1] != k or not t.is_contiguous() \
-            or t.get_device() != dev:
-        raise ValueError(f"idx is int32 and w float32, contiguous [>= {n}, {k}] on cuda:{dev}")
+        return self._experts(*self._args, x, idx, w, stream if stream is None else B._stream(stream))
 
 
 class MoeTopk:
@@ -195,36 +174,11 @@ class MoeTopk:
         c.routing = routing_word(name, num_groups, topk_groups, group_score)
         c.norm_topk_prob = 1 if norm_topk_prob else 0
         c.routed_scaling_factor = routed_scaling_factor
-        # One configuration for each logits type, so that calls change nothing here.
-        self.num_experts, self.top_k, self.bias = num_experts, top_k, bias
-        self.c_cfg = {}
-        for dtype, code in _TYPE.items():
-            self.c_cfg[dtype] = B.moe_topk_config_t.from_buffer_copy(c)
-            self.c_cfg[dtype].logits_type = code
-        self._bias = None if bias is None else bias.data_ptr()
-        self._topk = B.entry("moe_topk")
+        self.num_experts, self.top_k, self.bias, self.c_cfg = num_experts, top_k, bias, c
+        self._topk, self._cfg = B.tensor_calls().topk, addressof(c)
 
     def forward(self, logits: torch.Tensor, idx=None, w=None, stream=None):
-        cfg = self.c_cfg[logits.dtype]
-        E, k, shape, strides = self.num_experts, self.top_k, logits.shape, logits.stride()
-        if len(shape) != 2 or shape[1] != E or (E > 1 and strides[1] != 1):
-            raise ValueError("logits are [n, num_experts] with contiguous rows")
-        n, dev = shape[0], _device_of(logits)
-        if self.bias is not None and self.bias.get_device() != dev:
-            raise ValueError(f"bias on {self.bias.device}, but the current device is cuda:{dev}")
-        if idx is None:
-            idx = torch.empty((n, k), dtype=torch.int32, device=dev)
-        else:
-            _check_routes(idx, torch.int32, n, k, dev)
-        if w is None:
-            w = torch.empty((n, k), dtype=torch.float32, device=dev)
-        else:
-            _check_routes(w, torch.float32, n, k, dev)
-        s = self._topk(cfg, logits.data_ptr(), strides[0] if n > 1 else E, self._bias, n, idx.data_ptr(),
-                       w.data_ptr(), B.raw_stream(dev) if stream is None else B._stream(stream))
-        if s:
-            B.check(s)
-        return idx, w
+        return self._topk(self._cfg, self.bias, logits, idx, w, stream if stream is None else B._stream(stream))
 
 
 class MoeMatvec:
@@ -247,39 +201,14 @@ class MoeMatvec:
         c = B.moe_matvec_config_t()
         c.out_features, c.in_features, c.w_fmt = out_f, in_f, _FMT[q.fmt]
         c.out_type, c.accumulate = _TYPE[out_dtype], 1 if accumulate else 0
-        self.c_cfg, self.c_w = {}, _qmat(q)
-        for dtype in (torch.bfloat16, torch.float16):   # one for each type of x
-            self.c_cfg[dtype] = B.moe_matvec_config_t.from_buffer_copy(c)
-            self.c_cfg[dtype].x_type = _TYPE[dtype]
+        self.c_cfg, self.c_w = c, _qmat(q)
         self.weights, self.bias, self.out_dtype = q, bias, out_dtype
         self.in_features, self.out_features, self.accumulate = in_f, out_f, accumulate
-        self._bias = None if bias is None else bias.data_ptr()
-        self._dev = q.w.get_device()
-        if any(t is not None and t.get_device() != self._dev for t in (q.scale, q.scale2, q.zero, bias)):
+        dev = q.w.get_device()
+        if any(t is not None and t.get_device() != dev for t in (q.scale, q.scale2, q.zero, bias)):
             raise ValueError("weights and bias on one device")
-        self._matvec = B.entry("moe_matvec")
+        self._matvec = B.tensor_calls().matvec
+        self._args = (addressof(c), addressof(self.c_w), 0 if bias is None else bias.data_ptr(), dev)
 
     def forward(self, x: torch.Tensor, out=None, stream=None):
-        cfg = self.c_cfg[x.dtype]
-        K, O, shape, strides = self.in_features, self.out_features, x.shape, x.stride()
-        if len(shape) != 2 or shape[1] != K or strides[1] != 1:
-            raise ValueError("x is [n, in] with contiguous rows")
-        n, dev = shape[0], _device_of(x)
-        if self._dev != dev:
-            raise ValueError(f"weights on {self.weights.w.device}, but the current device is cuda:{dev}")
-        ostride = O
-        if out is None:
-            if self.accumulate:
-                raise ValueError("accumulate needs out")
-            out = torch.empty((n, O), dtype=self.out_dtype, device=dev)
-        else:
-            _device_of(out)
-            if out.shape != (n, O) or out.dtype != self.out_dtype or (O > 1 and out.stride(1) != 1):
-                raise ValueError("out is [n, out] of out_dtype with contiguous rows")
-            if n > 1:
-                ostride = out.stride(0)
-        s = self._matvec(cfg, self.c_w, self._bias, x.data_ptr(), strides[0] if n > 1 else K, n, out.data_ptr(),
-                         ostride, B.raw_stream(dev) if stream is None else B._stream(stream))
-        if s:
-            B.check(s)
-        return out
+        return self._matvec(*self._args, x, out, stream if stream is None else B._stream(stream))
