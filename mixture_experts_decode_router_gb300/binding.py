@@ -263,7 +263,7 @@ _ext = None
 
 
 def tensor_calls():
-    """The extension module whose topk, matvec and experts take torch tensors."""
+    """The extension module whose topk, matvec, experts and forward take torch tensors."""
     global _ext
     if _ext is None:
         import importlib.machinery
@@ -275,7 +275,7 @@ def tensor_calls():
             "_moe_torch", _build.EXT, loader=importlib.machinery.ExtensionFileLoader("_moe_torch", _build.EXT))
         ext = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ext)
-        addr = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in ("moe_topk", "moe_matvec", "moe_experts")]
+        addr = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in ("moe_topk", "moe_matvec", "moe_experts", "moe_forward")]
         ext.bind(*addr, check)
         _ext = ext
     return _ext

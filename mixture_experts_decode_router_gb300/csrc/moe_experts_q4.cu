@@ -93,7 +93,7 @@ struct Item {
 };
 
 template <int GSH, bool Z, bool GU, int NT>
-__device__ __forceinline__ void run_item(const Q4Params& p, const Item& it, uint8_t* dyn) {
+__device__ __forceinline__ void run_item(const Q4Params& p, const Item& it, uint8_t* dyn, bool& waited) {
     constexpr int kMats = GU ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int out = GU ? (it.sh ? p.S : p.I) : p.H, K = GU ? p.H : (it.sh ? p.S : p.I);
@@ -146,6 +146,11 @@ __device__ __forceinline__ void run_item(const Q4Params& p, const Item& it, uint
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue();
     load_scales();
+    if (!GU && !waited) {
+        pdl_wait();
+        pdl_trigger();
+        waited = true;
+    }
     if (!GU && threadIdx.x < it.ntok) {
         const int b = it.pos0 + threadIdx.x;
         weight[threadIdx.x] = it.sh ? shared_gate(p.sg_logit, b) : __ldg(p.route_w + __ldg(p.perm + b));
@@ -230,9 +235,14 @@ __device__ __forceinline__ void run_item(const Q4Params& p, const Item& it, uint
 template <int GSH, bool Z, bool GU, int TILE>
 __global__ void __launch_bounds__(kThreads, TILE == 8 ? 3 : 2) experts_q4_kernel(const Q4Params p) {
     extern __shared__ __align__(128) uint8_t dyn[];
-    pdl_wait();
-    pdl_trigger();
-    const int n_rsegs = p.ctrl->n_rsegs;
+    // The down kernel's first item starts its weights before it waits for gate_up, whose
+    // own wait, before it let this kernel start, covered the grouping.
+    bool waited = GU;
+    if (GU) {
+        pdl_wait();
+        pdl_trigger();
+    }
+    const int n_rsegs = __ldcg(&p.ctrl->n_rsegs);
     const int n_ssegs = p.S > 0 ? (p.n + TILE - 1) / TILE : 0;
     const int gr = ((GU ? p.I : p.H) + 16 * kWarps - 1) / (16 * kWarps), gs = ((GU ? p.S : p.H) + 16 * kWarps - 1) / (16 * kWarps);
     const int items = n_ssegs * gs + n_rsegs * gr;
@@ -247,15 +257,16 @@ __global__ void __launch_bounds__(kThreads, TILE == 8 ? 3 : 2) experts_q4_kernel
             it.tile0 = (i - s * gs) * kWarps;
         } else {
             const int j = i - n_ssegs * gs, s = j / gr;
-            it.le = __ldg(p.segs + 3 * s) - p.e_begin;
-            it.pos0 = __ldg(p.segs + 3 * s + 1);
-            it.ntok = __ldg(p.segs + 3 * s + 2);
+            it.le = __ldcg(p.segs + 3 * s) - p.e_begin;
+            it.pos0 = __ldcg(p.segs + 3 * s + 1);
+            it.ntok = __ldcg(p.segs + 3 * s + 2);
             it.tile0 = (j - s * gr) * kWarps;
         }
         if (i != (int)blockIdx.x) __syncthreads();   // the item before is done with shared memory
-        if (TILE == 8 || it.ntok <= 8) run_item<GSH, Z, GU, 1>(p, it, dyn);
-        else if constexpr (TILE > 8) run_item<GSH, Z, GU, 2>(p, it, dyn);
+        if (TILE == 8 || it.ntok <= 8) run_item<GSH, Z, GU, 1>(p, it, dyn, waited);
+        else if constexpr (TILE > 8) run_item<GSH, Z, GU, 2>(p, it, dyn, waited);
     }
+    if (!waited) pdl_wait();   // (a block without items)
 }
 
 // ---------------------------------------------------------------- one token
@@ -364,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) 
     float* red = reinterpret_cast<float*>(dyn + kRing);             // [kWarps][16]
     float* cf = red + kWarps * 16;                                  // weight and factor of each unit
     const uint32_t x0 = kRing + kWarps * 64 + ((units * 4 + 15) & ~15);
-    pdl_wait();
-    pdl_trigger();
+    // (What comes before the wait does not depend on gate_up, whose own wait, before it
+    // let this kernel start, covered the routing.)
     // Unit u: stage u % nr of slot u / nr, then the shared expert's stages.
     struct Unit {
         int slot, s, e, K;
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) 
         a.slot = sh ? p.k : u / nr;
         a.s = sh ? u - p.k * nr : u - a.slot * nr;
         a.K = sh ? p.S : p.I;
-        const int e = sh ? 0 : __ldg(p.idx + a.slot);
+        const int e = sh ? 0 : __ldcg(p.idx + a.slot);
         a.held = sh || (e >= p.e_begin && e < p.e_end);
         a.e = sh ? 0 : e - p.e_begin;
         return a;
@@ -412,6 +423,8 @@ __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) 
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue();
     load_scales();
+    pdl_wait();
+    pdl_trigger();
     // Every slot's act, a warp a stage.
     for (int u = warp; u < units; u += kWarps) {
         const Unit a = unit(u);

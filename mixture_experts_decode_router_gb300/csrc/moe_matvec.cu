@@ -8,7 +8,7 @@
 // block's warps, which balances the rounds, took 35 us: the copies of a block's warps
 // then lie apart in K.)
 //
-// Blocks of 8 warps; a warp multiplies 16 rows
+// Blocks of 8 or 16 warps; a warp multiplies 16 rows
 // (q4_mma.cuh) and kw warps share a tile of rows, each with every kw-th stage of
 // K, their sums added in warp order through shared memory.  Blocks are
 // persistent over the row tiles, the warps' copies running ahead across tiles.
@@ -22,7 +22,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kMaxKw = 8;             // warps that share a tile at most
 constexpr int kStages = 3;            // ring of each warp (2 stages in flight)
 constexpr int kMaxSmem = 227 * 1024;
 
@@ -46,18 +46,18 @@ __device__ __forceinline__ void store_out(const MatvecParams& p, int64_t t, int 
 struct Smem {
     uint32_t factor, x, red, total;
 };
-__host__ __device__ inline Smem smem_plan(int K, int nt, int ntok, int kw) {
+__host__ __device__ inline Smem smem_plan(int warps, int K, int nt, int ntok, int kw) {
     Smem m;
-    m.factor = kWarps * kStages * q4::kStageBytes;   // of each token's result
+    m.factor = warps * kStages * q4::kStageBytes;   // of each token's result
     m.x = m.factor + 64;
     m.red = m.x + (uint32_t)ntok * q4::x_row_bytes(K);
-    m.total = m.red + (kw > 1 ? kWarps * nt * 512 : 0);
+    m.total = m.red + (kw > 1 ? warps * nt * 512 : 0);
     return m;
 }
 
 // XB: x is bf16 (else f16).
-template <int GSH, bool Z, bool XB, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) matvec_kernel(const MatvecParams p, int kw, int tp) {
+template <int GSH, bool Z, bool XB, int NT, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps > 8 ? 1 : NT == 1 ? 3 : 2) matvec_kernel(const MatvecParams p, int kw, int tp) {
     extern __shared__ __align__(128) uint8_t dyn[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int K = p.w.in_dim, O = p.w.out_dim, row_bytes = K / 2;
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) matvec_kernel(co
     const int n_tiles = (O + 15) / 16, step = gridDim.x * mw;
     const int64_t t0 = (int64_t)blockIdx.y * tp;
     const int ntok = (int)min((int64_t)tp, (int64_t)p.n - t0);
-    const Smem sm = smem_plan(K, NT, ntok, kw);
+    const Smem sm = smem_plan(kWarps, K, NT, ntok, kw);
     const uint32_t ring = warp * kStages * q4::kStageBytes;
     pdl_wait();
 
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) matvec_kernel(co
     };
     if constexpr (GSH == 4 && XB) {
         for (int b = warp; b < ntok; b += kWarps) {
-            const float f = q4::scaled_row(row(b), K8, chunks, reinterpret_cast<uint4*>(dyn + sm.x + b * xstride), lane);
+            const float f = q4::scaled_row<NT == 1 && kWarps == 8 ? 4 : 8>(row(b), K8, chunks, reinterpret_cast<uint4*>(dyn + sm.x + b * xstride), lane);
             if (lane == 0) factor[b] = f * __ldg(p.w.scale2);
         }
     } else {
@@ -194,15 +194,11 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) matvec_kernel(co
     pdl_trigger();
 }
 
-template <int GSH, bool Z, bool XB, int NT>
-cudaError_t launch_nt(const MatvecParams& p, int tp, int num_sms, cudaStream_t st) {
-    const int K = p.w.in_dim, n_tiles = (p.w.out_dim + 15) / 16, nst = (K + q4::kStageK - 1) / q4::kStageK;
-    // Warps that share a tile: as many as give every SM about its 24 warps (a
-    // 7168 x 7168 product with one token: 10.6 us with 8, 9.1 us so).
-    int kw = 1;
-    while (kw < kWarps && kw < nst && (int64_t)n_tiles * kw < (int64_t)num_sms * 20) kw *= 2;
-    const size_t smem = smem_plan(K, NT, std::min(tp, p.n), kw).total;
-    auto kern = matvec_kernel<GSH, Z, XB, NT>;
+template <int GSH, bool Z, bool XB, int NT, int kWarps>
+cudaError_t launch_warps(const MatvecParams& p, int tp, int kw, int num_sms, cudaStream_t st) {
+    const int n_tiles = (p.w.out_dim + 15) / 16;
+    const size_t smem = smem_plan(kWarps, p.w.in_dim, NT, std::min(tp, p.n), kw).total;
+    auto kern = matvec_kernel<GSH, Z, XB, NT, kWarps>;
     static std::mutex mu;
     static bool configured[128] = {};
     int dev = 0;
@@ -215,7 +211,7 @@ cudaError_t launch_nt(const MatvecParams& p, int tp, int num_sms, cudaStream_t s
             configured[dev] = true;
         }
     }
-    const int per_sm = std::max(1, std::min(3, (int)((size_t)kMaxSmem / (smem + 1024))));
+    const int per_sm = kWarps > 8 ? 1 : std::max(1, std::min(3, (int)((size_t)kMaxSmem / (smem + 1024))));
     const int mw = kWarps / kw;
     const int gx = std::min((n_tiles + mw - 1) / mw, num_sms * per_sm);
     // (A grid has at most 65535 rows of blocks.)
@@ -230,10 +226,26 @@ cudaError_t launch_nt(const MatvecParams& p, int tp, int num_sms, cudaStream_t s
     return cudaGetLastError();
 }
 
+template <int GSH, bool Z, bool XB, int NT>
+cudaError_t launch_nt(const MatvecParams& p, int tp, int num_sms, cudaStream_t st) {
+    const int K = p.w.in_dim, n_tiles = (p.w.out_dim + 15) / 16, nst = (K + q4::kStageK - 1) / q4::kStageK;
+    // Warps that share a tile: as many as give every SM about its 24 warps (a
+    // 7168 x 7168 product with one token: 10.6 us with 8, 9.1 us so).
+    int kw = 1;
+    while (kw < kMaxKw && kw < nst && (int64_t)n_tiles * kw < (int64_t)num_sms * 20) kw *= 2;
+    // Rows of x so long that an SM has room for one block of 8 warps: 16 warps, if their
+    // rings fit (7168 x 2048 NVFP4, 16 tokens: 9.1 us with 8, 8.2 us with 16).
+    const int tokens = std::min(tp, p.n);
+    if (2 * (smem_plan(8, K, NT, tokens, kw).total + 1024) > (uint32_t)kMaxSmem &&
+        smem_plan(16, K, NT, tokens, kw).total <= (uint32_t)kMaxSmem)
+        return launch_warps<GSH, Z, XB, NT, 16>(p, tp, kw, num_sms, st);
+    return launch_warps<GSH, Z, XB, NT, 8>(p, tp, kw, num_sms, st);
+}
+
 template <int GSH, bool Z, bool XB>
 cudaError_t launch_fmt(const MatvecParams& p, int num_sms, cudaStream_t st) {
     // Tokens of a block: up to 16, as many as fit beside the rings.
-    const int64_t room = kMaxSmem - (int64_t)smem_plan(p.w.in_dim, 2, 0, kWarps).total;
+    const int64_t room = kMaxSmem - (int64_t)smem_plan(8, p.w.in_dim, 2, 0, kMaxKw).total;
     int tp = (int)std::min<int64_t>(16, room / q4::x_row_bytes(p.w.in_dim));
     if (tp < 1) return cudaErrorInvalidValue;   // (matvec_fits says no)
     const int tokens = std::min(tp, p.n);
@@ -253,7 +265,7 @@ cudaError_t launch_x(int x_type, const MatvecParams& p, int num_sms, cudaStream_
 
 // The longest row of x that the interface admits; one fits beside the rings.
 constexpr int kMaxIn = 57344;
-static_assert(kWarps * (kStages * q4::kStageBytes + 1024) + 64 + kMaxIn * 2 + 64 + 512 <= kMaxSmem,
+static_assert(8 * (kStages * q4::kStageBytes + 1024) + 64 + kMaxIn * 2 + 64 + 512 <= kMaxSmem,
               "a row of x fits");
 bool matvec_fits(int K) { return K <= kMaxIn; }
 

@@ -21,6 +21,7 @@ namespace {
 decltype(&moe_topk) g_topk;
 decltype(&moe_matvec) g_matvec;
 decltype(&moe_experts) g_experts;
+decltype(&moe_forward) g_forward;
 PyObject* g_check;   // raises a status's error
 
 struct Raised {};    // a Python exception is set
@@ -89,15 +90,16 @@ void need(Py_ssize_t got, Py_ssize_t want) {
     if (got != want) raise(PyExc_TypeError, "wrong number of arguments");
 }
 
-// bind(moe_topk, moe_matvec, moe_experts, check): the functions' addresses.
+// bind(moe_topk, moe_matvec, moe_experts, moe_forward, check): the functions' addresses.
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-    need(n, 4);
+    need(n, 5);
     g_topk = reinterpret_cast<decltype(g_topk)>(address<void>(a[0]));
     g_matvec = reinterpret_cast<decltype(g_matvec)>(address<void>(a[1]));
     g_experts = reinterpret_cast<decltype(g_experts)>(address<void>(a[2]));
-    Py_INCREF(a[3]);
+    g_forward = reinterpret_cast<decltype(g_forward)>(address<void>(a[3]));
+    Py_INCREF(a[4]);
     Py_XDECREF(g_check);
-    g_check = a[3];
+    g_check = a[4];
     Py_RETURN_NONE;
 }
 
@@ -208,6 +210,41 @@ PyObject* experts(PyObject* const* a, Py_ssize_t na) {
     return wrap(std::move(out));
 }
 
+// forward(config address, weights address, workspace address, its bytes, x, out or None, idx or None, w or None,
+// whether idx and w are wanted, stream or None) -> (out, idx, w)
+PyObject* forward(PyObject* const* a, Py_ssize_t na) {
+    need(na, 10);
+    const moe_config_t* c = address<const moe_config_t>(a[0]);
+    const moe_weights_t* wts = address<const moe_weights_t>(a[1]);
+    void* ws = address<void>(a[2]);
+    const size_t ws_bytes = (size_t)integer(a[3]);
+    const at::Tensor& x = some_tensor(a[4]);
+    const at::Tensor *go = tensor(a[5]), *gi = tensor(a[6]), *gw = tensor(a[7]);
+    const int routing = PyObject_IsTrue(a[8]);
+    if (routing < 0) throw Raised{};
+    if (x.dim() < 1 || x.size(0) > INT32_MAX) raise(PyExc_ValueError, "x is [n, hidden]");
+    if (!go && c->accumulate) raise(PyExc_ValueError, "accumulate needs out");
+    const int64_t n = x.size(0);
+    at::Tensor out = go ? *go : matrix(n, c->hidden, at::kBFloat16, x.device()), idx, w;
+    if (gi) idx = *gi;
+    else if (routing) idx = matrix(n, c->top_k, at::kInt, x.device());
+    if (gw) w = *gw;
+    else if (routing) w = matrix(n, c->top_k, at::kFloat, x.device());
+    const void* xp = x.data_ptr();
+    void* op = out.data_ptr();
+    int32_t* ip = idx.defined() ? static_cast<int32_t*>(idx.data_ptr()) : nullptr;
+    float* wp = w.defined() ? static_cast<float*>(w.data_ptr()) : nullptr;
+    const moe_stream_t st = stream_of(a[9], c10::cuda::current_device());
+    moe_status_t s;
+    Py_BEGIN_ALLOW_THREADS;
+    s = g_forward(c, wts, xp, (int32_t)n, op, ip, wp, ws, ws_bytes, st);
+    Py_END_ALLOW_THREADS;
+    check(s);
+    PyObject* none = Py_None;
+    return Py_BuildValue("(NNN)", wrap(std::move(out)), idx.defined() ? wrap(std::move(idx)) : Py_NewRef(none),
+                         w.defined() ? wrap(std::move(w)) : Py_NewRef(none));
+}
+
 // No C++ exception leaves a Python call.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -225,6 +262,7 @@ PyMethodDef methods[] = {
     {"topk", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<topk>)), METH_FASTCALL, nullptr},
     {"matvec", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<matvec>)), METH_FASTCALL, nullptr},
     {"experts", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<experts>)), METH_FASTCALL, nullptr},
+    {"forward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<forward>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -361,29 +361,48 @@ __device__ __forceinline__ uint4 chunk_order(uint4 u) {
 }
 
 // One bf16 row as f16, scaled by a power of two, by one warp: dst [chunks] (zero
-// past K); returns the factor that scales a result back.
+// past K); returns the factor that scales a result back.  kU: loads of a lane in
+// flight; a row of at most 32 kU chunks is read once.
+template <int kU>
 __device__ __forceinline__ float scaled_row(const uint4* src, int K8, int chunks, uint4* dst, int lane) {
-    float am = 0.f;
-    for (int c = lane; c < K8; c += 32) {
-        float v[8];
-        bf16x8_to_float(src[c], v);
+    uint4 u[kU];
+    auto load = [&](int c0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(v[i]));   // (NaN keeps its column NaN by itself)
+        for (int i = 0; i < kU; ++i) {
+            const int c = c0 + 32 * i + lane;
+            u[i] = c < K8 ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    float am = 0.f;
+    for (int c0 = 0; c0 < K8; c0 += 32 * kU) {
+        load(c0);
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+            float v[8];
+            bf16x8_to_float(u[i], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(v[e]));   // (NaN keeps its column NaN by itself)
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
     const int sh = f16_shift(am);
     const float f = exp2i(sh);
-    for (int c = lane; c < chunks; c += 32) {
-        float v[8] = {};
-        if (c < K8) bf16x8_to_float(src[c], v);
-        uint32_t h[4];
+    for (int c0 = 0; c0 < chunks; c0 += 32 * kU) {
+        if (K8 > 32 * kU) load(c0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 hv = __floats2half2_rn(v[2 * i] * f, v[2 * i + 1] * f);
-            h[i] = *reinterpret_cast<const uint32_t*>(&hv);
+        for (int i = 0; i < kU; ++i) {
+            const int c = c0 + 32 * i + lane;
+            float v[8];
+            bf16x8_to_float(u[i], v);
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __half2 hv = __floats2half2_rn(v[2 * e] * f, v[2 * e + 1] * f);
+                h[e] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            if (c < chunks) dst[c] = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        dst[c] = make_uint4(h[0], h[1], h[2], h[3]);
     }
     return exp2i(-sh);
 }

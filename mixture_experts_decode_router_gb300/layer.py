@@ -111,26 +111,15 @@ class MoeLayer:
         # The control block (first 256 bytes) must start at zero; calls keep it zero.
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
         self.max_tokens = max_tokens
-        self._experts = B.tensor_calls().experts
+        calls = B.tensor_calls()
+        self._experts, self._forward = calls.experts, calls.forward
         self._args = (addressof(self.c_cfg), addressof(self.c_w), self.ws.data_ptr(), self.ws_bytes)
 
     def forward(self, x: torch.Tensor, out=None, idx=None, w=None, stream=None,
                 routing: bool = True):
         """``routing=False``: do not return the routing (idx and w are None), so
         a call that holds no routed expert can skip it."""
-        n = x.shape[0]
-        k = self.cfg.top_k
-        dev = x.device
-        if out is None:
-            if self.accumulate:
-                raise ValueError("accumulate needs out")
-            out = torch.empty(n, self.cfg.hidden, dtype=torch.bfloat16, device=dev)
-        if routing:
-            idx = torch.empty(n, k, dtype=torch.int32, device=dev) if idx is None else idx
-            w = torch.empty(n, k, dtype=torch.float32, device=dev) if w is None else w
-        B.check(B.moe_forward(self.c_cfg, self.c_w, x, n, out, idx, w, self.ws, self.ws_bytes,
-                              stream))
-        return out, idx, w
+        return self._forward(*self._args, x, out, idx, w, routing, stream if stream is None else B._stream(stream))
 
     def device_error(self, stream=None) -> int:
         """Reads and clears the workspace's device error word (syncs the stream)."""
