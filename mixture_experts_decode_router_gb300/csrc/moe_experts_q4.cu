@@ -20,9 +20,9 @@
 // depend on the layer's sizes alone, so a token's bits do not depend on its batch.
 //
 // On GB300 (hidden 2048, intermediate 512, 8 of 256 experts and a shared one): one token
-// 9.9 us (1.5 TB/s), 16 tokens with groups of 64 and zero points 65 us (2.7 TB/s), 256
-// rows with groups of 32 212 us (2.1 TB/s); hidden 7168, intermediate 2048, 8 of 64
-// experts, 64 tokens 486 us (3.0 TB/s).  The copies and the staging alone take 41, 125
+// 9.7 us (1.5 TB/s), 16 tokens with groups of 64 and zero points 64 us (2.8 TB/s), 256
+// rows with groups of 32 213 us (2.1 TB/s); hidden 7168, intermediate 2048, 8 of 64
+// experts, 64 tokens 487 us (3.0 TB/s).  The copies and the staging alone take 41, 125
 // and 306 us of the last three; the rest is what the warps' instructions do not overlap.
 // (Measured and not kept: the rows of x prepared once by a kernel of their own and read
 // through L1 by warps that share nothing, 70, 273 and 547 us; two row tiles a warp for
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, TILE == 8 ? 3 : 2) experts_q4_kernel
 // One block per (slot, 16 rows of I) and (shared expert, 16 rows of S): its warps take
 // every eighth stage of gate and up together, their sums added in warp order.  (One
 // matrix after the other, and act staged in chunks of 768: the two kernels took 12.8 us
-// at hidden 2048, intermediate 512, eight experts and a shared one, and take 9.9 us.)
+// at hidden 2048, intermediate 512, eight experts and a shared one, and take 9.7 us.)
 template <int GSH, bool Z>
 __global__ void __launch_bounds__(kThreads, 3) gate_up_n1_kernel(const Q4Params p) {
     extern __shared__ __align__(128) uint8_t dyn[];

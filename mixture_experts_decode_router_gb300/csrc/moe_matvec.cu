@@ -3,7 +3,8 @@
 //
 // Bound by the instructions on the weight stream (q4_mma.cuh).  On GB300: 100003 x 2048,
 // groups of 32, six tokens 33.4 us (3.5 TB/s); 7168 x 7168 with zero points, one token
-// 9.1 us (3.1 TB/s); 2048 x 2048 2.8 us, launch and latency.  Without the products the
+// 9.2 us (3.1 TB/s); 2048 x 2048 2.9 us, launch and latency; 7168 x 2048 NVFP4, 16
+// tokens 8.2 us, the staging of x in every block.  Without the products the
 // first takes 21 us.  (Stretches of stages that split the tiles of a part evenly over a
 // block's warps, which balances the rounds, took 35 us: the copies of a block's warps
 // then lie apart in K.)
