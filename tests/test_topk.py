@@ -366,6 +366,22 @@ def test_two_streams_at_once(lib):
                 assert torch.equal(i, ri) and torch.equal(w, rw)
 
 
+def test_arguments_that_are_no_tensors():
+    """On the CPU: what is no tensor, or of no type that the operators take, is refused before anything runs."""
+    op = MoeTopk(64, 4)
+    for bad in (None, 3, [[0.0] * 64]):
+        with pytest.raises(TypeError):
+            op.forward(bad)
+    with pytest.raises(TypeError):
+        op.forward(torch.zeros(2, 64), idx=1)
+    for bad in (torch.zeros(2, 64, dtype=torch.float64), torch.zeros(2, 64, dtype=torch.int32)):
+        with pytest.raises(KeyError):
+            op.forward(bad)
+    for bad in (torch.zeros(64), torch.zeros(2, 63), torch.zeros(2, 128)[:, ::2], torch.zeros(1, 2, 64), torch.zeros(2, 64)):
+        with pytest.raises(ValueError):
+            op.forward(bad)                # (the last is not on the GPU)
+
+
 @gpu
 def test_given_outputs_are_checked(lib):
     lg = draw(4, 64)
