@@ -92,7 +92,7 @@ struct Item {
     int le, pos0, ntok, tile0;   // expert in its stack, first sorted row, tokens, first 16-row tile
 };
 
-template <int GSH, bool Z, bool GU, int NT>
+template <int GSH, bool Z, bool GU, int TILE, int NT>
 __device__ __forceinline__ void run_item(const Q4Params& p, const Item& it, uint8_t* dyn, bool& waited) {
     constexpr int kMats = GU ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -146,6 +146,8 @@ __device__ __forceinline__ void run_item(const Q4Params& p, const Item& it, uint
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue();
     load_scales();
+    [[maybe_unused]] int token = 0;   // lane b's token
+    if (GU && TILE > 8 && lane < it.ntok) token = it.sh ? it.pos0 + lane : __ldg(p.perm + it.pos0 + lane) / p.k;
     if (!GU && !waited) {
         pdl_wait();
         pdl_trigger();
@@ -172,16 +174,39 @@ __device__ __forceinline__ void run_item(const Q4Params& p, const Item& it, uint
     for (int c0 = 0; c0 < nst; c0 += cs) {
         if (c0 > 0) __syncthreads();   // every warp is done with the chunk before
         if constexpr (GU) {
-            // Elements [c0, c0 + cs) stages of each token's row, zero past K.
+            // Elements [c0, c0 + cs) stages of each token's row, zero past K.  Segments of
+            // up to 16 tokens: a warp a stage of a row, kU of them loaded before any is
+            // stored (256 rows of 8 of 256 experts: 214 us by single chunks, 208 us so);
+            // shorter ones by single chunks (16 tokens: 64 us, 66 us the other way).
             const int k8 = K / 8, chunks = cs * 32;
-            for (int i = threadIdx.x; i < it.ntok * chunks; i += kThreads) {
-                const int b = i / chunks, c = i - b * chunks, cc = c0 * 32 + c;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (cc < k8) {
-                    const int tok = it.sh ? it.pos0 + b : __ldg(p.perm + it.pos0 + b) / p.k;
-                    v = __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)tok * K) + cc);
+            if constexpr (TILE > 8) {
+                constexpr int kU = 4;
+                const int units = it.ntok * cs;
+                for (int u0 = warp; u0 < units; u0 += kU * kWarps) {
+                    uint4 v[kU];
+#pragma unroll
+                    for (int i = 0; i < kU; ++i) {
+                        const int u = u0 + i * kWarps, b = u / cs, cc = (c0 + u - b * cs) * 32 + lane;
+                        const int tok = __shfl_sync(0xffffffffu, token, min(b, it.ntok - 1));
+                        v[i] = u < units && cc < k8 ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)tok * K) + cc)
+                                                    : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kU; ++i) {
+                        const int u = u0 + i * kWarps, b = u / cs, c = (u - b * cs) * 32 + lane;
+                        if (u < units) *reinterpret_cast<uint4*>(dyn + x0 + b * xstride + c * 16) = q4::chunk_order<GSH>(v[i]);
+                    }
                 }
-                *reinterpret_cast<uint4*>(dyn + x0 + b * xstride + c * 16) = q4::chunk_order<GSH>(v);
+            } else {
+                for (int i = threadIdx.x; i < it.ntok * chunks; i += kThreads) {
+                    const int b = i / chunks, c = i - b * chunks, cc = c0 * 32 + c;
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (cc < k8) {
+                        const int tok = it.sh ? it.pos0 + b : __ldg(p.perm + it.pos0 + b) / p.k;
+                        v = __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)tok * K) + cc);
+                    }
+                    *reinterpret_cast<uint4*>(dyn + x0 + b * xstride + c * 16) = q4::chunk_order<GSH>(v);
+                }
             }
         } else {
             const float* a = it.sh ? p.act_sh : p.act;
@@ -263,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, TILE == 8 ? 3 : 2) experts_q4_kernel
             it.tile0 = (j - s * gr) * kWarps;
         }
         if (i != (int)blockIdx.x) __syncthreads();   // the item before is done with shared memory
-        if (TILE == 8 || it.ntok <= 8) run_item<GSH, Z, GU, 1>(p, it, dyn, waited);
-        else if constexpr (TILE > 8) run_item<GSH, Z, GU, 2>(p, it, dyn, waited);
+        if (TILE == 8 || it.ntok <= 8) run_item<GSH, Z, GU, TILE, 1>(p, it, dyn, waited);
+        else if constexpr (TILE > 8) run_item<GSH, Z, GU, TILE, 2>(p, it, dyn, waited);
     }
     if (!waited) pdl_wait();   // (a block without items)
 }
