@@ -21,8 +21,8 @@
 //
 // On GB300 (hidden 2048, intermediate 512, 8 of 256 experts and a shared one): one token
 // 9.7 us (1.5 TB/s), 16 tokens with groups of 64 and zero points 64 us (2.8 TB/s), 256
-// rows with groups of 32 213 us (2.1 TB/s); hidden 7168, intermediate 2048, 8 of 64
-// experts, 64 tokens 487 us (3.0 TB/s).  The copies and the staging alone take 41, 125
+// rows with groups of 32 208 us (2.2 TB/s); hidden 7168, intermediate 2048, 8 of 64
+// experts, 64 tokens 483 us (3.1 TB/s).  The copies and the staging alone take 41, 125
 // and 306 us of the last three; the rest is what the warps' instructions do not overlap.
 // (Measured and not kept: the rows of x prepared once by a kernel of their own and read
 // through L1 by warps that share nothing, 70, 273 and 547 us; two row tiles a warp for

@@ -2,12 +2,12 @@
 // (sm_103a): out[t, o] = sum_i W[o, i] x[t, i] (+ bias[o]) (+ out[t, o]).
 //
 // Bound by the instructions on the weight stream (q4_mma.cuh).  On GB300: 100003 x 2048,
-// groups of 32, six tokens 33.4 us (3.5 TB/s); 7168 x 7168 with zero points, one token
+// groups of 32, six tokens 32.3 us (3.6 TB/s); 7168 x 7168 with zero points, one token
 // 9.2 us (3.1 TB/s); 2048 x 2048 2.9 us, launch and latency; 7168 x 2048 NVFP4, 16
 // tokens 8.2 us, the staging of x in every block.  Without the products the
 // first takes 21 us.  (Stretches of stages that split the tiles of a part evenly over a
-// block's warps, which balances the rounds, took 35 us: the copies of a block's warps
-// then lie apart in K.)
+// block's warps, which balances the rounds, took 35 us where this took 33.4: the copies
+// of a block's warps then lie apart in K.)
 //
 // Blocks of 8 or 16 warps; a warp multiplies 16 rows
 // (q4_mma.cuh) and kw warps share a tile of rows, each with every kw-th stage of
