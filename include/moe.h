@@ -288,8 +288,9 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_weights_t* wts,
  * Markers: 0 before the first kernel, then one after each stage, in launch
  * order.  One token on the single-token kernel: 2 markers (before, after).
  * Token-major kernels: 5 (router, top-k + grouping, gate+up, down+blend).
- * INT4 streaming kernels: 6 (router, top-k + grouping, gate+up, down, combine),
- * one token 5 (router, top-k, gate+up, down+blend).
+ * INT4 streaming kernels: 6 (router, top-k + grouping, gate+up, down, combine);
+ * where the tokens take their routes one by one (one token, or up to four whose
+ * experts take at most 64 MB together) 5 (router, top-k, gate+up, down+blend).
  * Grouped tensor-core path: 7 (router, top-k + grouping, gather, gate+up, down,
  * combine).  The pre-expert RMSNorm, when present, runs at the start of the
  * stage after top-k + grouping.

@@ -231,6 +231,23 @@ static int effective_path(const moe_config_t* c, int32_t n) {
     return c->path == MOE_PATH_AUTO ? (n <= kTokenMajorMaxN ? MOE_PATH_TOKEN_MAJOR : MOE_PATH_GROUPED) : c->path;
 }
 
+// A few tokens on the streaming path take their routes as they are, in kernels of one
+// token that the grid repeats: no grouping, no combining, but an expert's weights once
+// for each token that chose it.  Measured on GB300, 8 experts of each token and a
+// shared one, groups of 128, per token against grouped: hidden 2048, intermediate 512,
+// 256 experts (14 MB a token) 2 tokens 15.2 against 24.4 us, 4 tokens 24.8 against
+// 33.4, 8 tokens 44.2 against 35.7; hidden 1024, intermediate 512, 32 experts (7 MB) 4
+// tokens 17.1 against 19.3, 6 tokens 20.3 against 20.0; hidden 2048, intermediate 1024,
+// 64 experts (27 MB) 2 tokens 26.1 against 32.4, 4 tokens 48.1 against 35.1; hidden
+// 4096, intermediate 1536 (81 MB) 2 tokens 65.3 against 59.6.
+constexpr int kPerTokenMax = 4;
+constexpr int64_t kPerTokenBytes = (int64_t)64 << 20;
+static bool per_token(const moe_config_t* c, int32_t n) {
+    if (effective_path(c, n) != kPathStream || n > kPerTokenMax) return false;
+    const int64_t bytes = (int64_t)c->hidden * ((int64_t)c->top_k * c->inter + c->shared_inter) * 3 / 2;
+    return n == 1 || (n * bytes <= kPerTokenBytes && q4_n1_fits(c->hidden, c->top_k, c->inter, c->shared_inter));
+}
+
 // Whether a call of n tokens takes the tensor-core router.
 static bool tc_router_path(const moe_config_t* c, int32_t n) {
     const int path = effective_path(c, n);
@@ -445,6 +462,7 @@ static moe_status_t enqueue_stream(const moe_config_t* c, const moe_weights_t* w
     p.segs = at<int32_t>(ws, L.segs);
     p.perm = at<int32_t>(ws, L.perm);
     p.ctrl = at<Ctrl>(ws, L.ctrl);
+    p.per_token = per_token(c, n);
     p.idx = idx;
     p.route_w = wt;
     p.sg_logit = w->shared_gate_w ? sg_logit : nullptr;
@@ -459,7 +477,7 @@ static moe_status_t enqueue_stream(const moe_config_t* c, const moe_weights_t* w
     mk.mark(st);
     if (launch_experts_q4(fmt, p, false, tile, sms, st) != cudaSuccess) return MOE_ERR_CUDA;
     mk.mark(st);
-    if (n > 1) {
+    if (!p.per_token) {
         if (launch_combine(p.y, p.y_sh, at<int32_t>(ws, L.inv), n, H, k, S > 0 ? 1 : 0, c->accumulate, p.out,
                            early_dependents(n, sms), sms, st) != cudaSuccess)
             return MOE_ERR_CUDA;
@@ -498,8 +516,7 @@ static moe_status_t enqueue_experts(const moe_config_t* c, const moe_weights_t* 
         if (e != cudaSuccess) return MOE_ERR_CUDA;
         xin = xe;
     }
-    // (One token on the streaming path takes its routes as they are.)
-    if (!grouped && !(path == kPathStream && n == 1)) {
+    if (!grouped && !per_token(c, n)) {
         e = launch_group(idx, n * k, E, seg_tile(c, n), c->expert_begin, c->expert_end, at<int32_t>(ws, L.counts),
                          at<int32_t>(ws, L.offsets), at<int32_t>(ws, L.perm), at<int32_t>(ws, L.inv),
                          at<int32_t>(ws, L.active), at<int32_t>(ws, L.segs), at<Ctrl>(ws, L.ctrl), st);
@@ -698,8 +715,7 @@ static moe_status_t forward_impl(const moe_config_t* cfg_in, const moe_weights_t
         mk.mark(st);
         return enqueue_experts(cfg, wts, x, n, idx_p, w_p, out, ws, L, true, false, st, mk);
     }
-    // (One token on the streaming path takes its routes ungrouped.)
-    const bool group = !(n == 1 && effective_path(cfg, n) == kPathStream);
+    const bool group = !per_token(cfg, n);
     if ((s = enqueue_route(cfg, wts, x, n, idx_p, w_p, nullptr, ws, L, group, true, st, mk)) != MOE_OK) return s;
     return enqueue_experts(cfg, wts, x, n, idx_p, w_p, out, ws, L, true, routing_plain(cfg->routing), st, mk);
 }

@@ -11,8 +11,9 @@
 //   down      item = (the same tokens, 8 tiles of 16 rows of H):
 //             y[p, h] = weight (route p) Wd a (fp32); the combine kernel adds a
 //             token's rows in slot order
-//   One token: gate_up_n1 and down_n1 take the routes as they are (no grouping),
-//   split K over a block's warps, and down_n1 adds the slots and writes the output.
+//   One token, or a few: gate_up_n1 and down_n1 take a token's routes as they are (no
+//   grouping), split K over a block's warps, and down_n1 adds the slots and writes the
+//   output.
 //
 // act enters the down product as f16, each token's chunk of 768 (one token: 256) scaled by a power of
 // two that puts its largest value below 2^15: one rounding to 11 significand bits
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, TILE == 8 ? 3 : 2) experts_q4_kernel
     if (!waited) pdl_wait();   // (a block without items)
 }
 
-// ---------------------------------------------------------------- one token
+// ---------------------------------------------------------------- one token a block
 
 // One block per (slot, 16 rows of I) and (shared expert, 16 rows of S): its warps take
 // every eighth stage of gate and up together, their sums added in warp order.  (One
@@ -304,14 +305,14 @@ template <int GSH, bool Z>
 __global__ void __launch_bounds__(kThreads, 3) gate_up_n1_kernel(const Q4Params p) {
     extern __shared__ __align__(128) uint8_t dyn[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tr = (p.I + 15) / 16, tile = blockIdx.x;
+    const int tr = (p.I + 15) / 16, tile = blockIdx.x, tok = blockIdx.y;
     const bool sh = tile >= p.k * tr;
     const int slot = sh ? p.k : tile / tr, row0 = (sh ? tile - p.k * tr : tile % tr) * 16;
     const int out = sh ? p.S : p.I, K = p.H, row_bytes = K / 2, full = row_bytes / 128;
     const int nst = (K + q4::kStageK - 1) / q4::kStageK;
     pdl_wait();
     pdl_trigger();
-    const int e = sh ? 0 : __ldg(p.idx + slot);
+    const int e = sh ? 0 : __ldg(p.idx + tok * p.k + slot);
     if (!sh && (e < p.e_begin || e >= p.e_end)) return;   // not held here: down skips it too
     const int64_t srow = (int64_t)(sh ? 0 : e - p.e_begin) * out + row0;
     const QMatDev& m0 = sh ? p.sh_gate : p.gate;
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 3) gate_up_n1_kernel(const Q4Params 
     load_scales();
     for (int c = threadIdx.x; c < nst * 32; c += kThreads)
         *reinterpret_cast<uint4*>(dyn + x0 + c * 16) =
-            q4::chunk_order<GSH>(c < K / 8 ? __ldg(reinterpret_cast<const uint4*>(p.x) + c) : make_uint4(0u, 0u, 0u, 0u));
+            q4::chunk_order<GSH>(c < K / 8 ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)tok * K) + c) : make_uint4(0u, 0u, 0u, 0u));
     __syncthreads();
     q4::XView<1> x;
     x.start(x0, 0, 1, lane);
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 3) gate_up_n1_kernel(const Q4Params 
             gu[m] = red[m * kWarps * 16 + threadIdx.x];
             for (int w = 1; w < kWarps; ++w) gu[m] += red[(m * kWarps + w) * 16 + threadIdx.x];
         }
-        (sh ? p.act_sh : p.act + (size_t)slot * p.I)[row0 + threadIdx.x] = silu(gu[0]) * gu[1];
+        (sh ? p.act_sh + (size_t)tok * p.S : p.act + (size_t)(tok * p.k + slot) * p.I)[row0 + threadIdx.x] = silu(gu[0]) * gu[1];
     }
 }
 
@@ -393,7 +394,8 @@ template <int GSH, bool Z>
 __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) {
     extern __shared__ __align__(128) uint8_t dyn[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row0 = blockIdx.x * 16, rows = p.H - row0;
+    const int row0 = blockIdx.x * 16, rows = p.H - row0, tok = blockIdx.y;
+    const int32_t* idx = p.idx + tok * p.k;
     const int nr = (p.I + q4::kStageK - 1) / q4::kStageK, ns = (p.S + q4::kStageK - 1) / q4::kStageK;
     const int units = p.k * nr + ns;
     const uint32_t ring = warp * kStages * q4::kStageBytes, ring_a = q4::smem_addr(dyn) + ring;
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) 
         a.slot = sh ? p.k : u / nr;
         a.s = sh ? u - p.k * nr : u - a.slot * nr;
         a.K = sh ? p.S : p.I;
-        const int e = sh ? 0 : __ldcg(p.idx + a.slot);
+        const int e = sh ? 0 : __ldcg(idx + a.slot);
         a.held = sh || (e >= p.e_begin && e < p.e_end);
         a.e = sh ? 0 : e - p.e_begin;
         return a;
@@ -454,9 +456,9 @@ __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) 
     for (int u = warp; u < units; u += kWarps) {
         const Unit a = unit(u);
         if (!a.held) continue;
-        const float* src = (a.slot == p.k ? p.act_sh : p.act + (size_t)a.slot * p.I) + a.s * q4::kStageK;
+        const float* src = (a.slot == p.k ? p.act_sh + (size_t)tok * p.S : p.act + (size_t)(tok * p.k + a.slot) * p.I) + a.s * q4::kStageK;
         const float f = stage_act<1>(src, a.K - a.s * q4::kStageK, dyn + x0 + u * 512, lane);
-        if (lane == 0) cf[u] = f * (a.slot == p.k ? shared_gate(p.sg_logit, 0) : __ldg(p.route_w + a.slot));
+        if (lane == 0) cf[u] = f * (a.slot == p.k ? shared_gate(p.sg_logit, tok) : __ldg(p.route_w + tok * p.k + a.slot));
     }
     __syncthreads();
     float total[4] = {0.f, 0.f, 0.f, 0.f};
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 3) down_n1_kernel(const Q4Params p) 
     if (threadIdx.x < 16 && (int)threadIdx.x < rows) {
         float v = red[threadIdx.x];
         for (int w = 1; w < kWarps; ++w) v += red[w * 16 + threadIdx.x];
-        uint16_t* o = p.out + row0 + threadIdx.x;
+        uint16_t* o = p.out + (size_t)tok * p.H + row0 + threadIdx.x;
         if (p.accumulate) v += __uint_as_float((uint32_t)*o << 16);
         const __nv_bfloat16 b = __float2bfloat16_rn(v);
         *o = *reinterpret_cast<const uint16_t*>(&b);
@@ -523,11 +525,11 @@ cudaError_t launch_fmt(const Q4Params& p, bool gate_up, int tile, int num_sms, c
     const size_t smem = kRing + 128 + kXBytes;
     const int per_sm = tile == 8 ? 3 : 2;
     const dim3 grid(num_sms * per_sm);
-    if (p.n == 1) {
+    if (p.per_token) {
         if (gate_up)
             return launch_smem(gate_up_n1_kernel<GSH, Z>, SLOT * 6, gate_up_n1_smem(p.H),
-                               dim3(p.k * ((p.I + 15) / 16) + (p.S + 15) / 16), st, p);
-        return launch_smem(down_n1_kernel<GSH, Z>, SLOT * 6 + 1, down_n1_smem(p.k, p.I, p.S), dim3((p.H + 15) / 16), st, p);
+                               dim3(p.k * ((p.I + 15) / 16) + (p.S + 15) / 16, p.n), st, p);
+        return launch_smem(down_n1_kernel<GSH, Z>, SLOT * 6 + 1, down_n1_smem(p.k, p.I, p.S), dim3((p.H + 15) / 16, p.n), st, p);
     }
     if (tile == 8)
         return gate_up ? launch_smem(experts_q4_kernel<GSH, Z, true, 8>, SLOT * 6 + 2, smem, grid, st, p)

@@ -44,17 +44,18 @@ struct Q4Params {
     const int32_t* segs;     // [n_rsegs][3] (n > 1)
     const int32_t* perm;     // sorted position -> route id (n > 1)
     const Ctrl* ctrl;
-    const int32_t* idx;      // [k] (one token)
+    bool per_token;          // each token's routes as they are (a few tokens)
+    const int32_t* idx;      // [n, k] (per token)
     const float* route_w;    // [n*k]
     const float* sg_logit;   // shared gate logits or NULL
-    float* act;              // [n*k, I] by sorted position (one token: by slot)
+    float* act;              // [n*k, I] by sorted position (per token: by route)
     float* act_sh;           // [n, S]
     float* y;                // [n*k, H] weighted rows (n > 1)
     float* y_sh;             // [n, H]
-    uint16_t* out;           // [H] (one token)
+    uint16_t* out;           // [n, H] (per token)
     int accumulate;
 };
-bool q4_n1_fits(int H, int k, int I, int S);   // whether the one-token kernels' shared memory suffices
+bool q4_n1_fits(int H, int k, int I, int S);   // whether the per-token kernels' shared memory suffices
 cudaError_t launch_experts_q4(int fmt, const Q4Params& p, bool gate_up, int tile, int num_sms, cudaStream_t st);
 
 // Grouped tensor-core path (moe_grouped_tc.cu).

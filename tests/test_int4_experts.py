@@ -366,7 +366,7 @@ def test_many_tokens_of_one_expert(lib):
 
 
 @gpu
-@pytest.mark.parametrize("n,marks", [(1, 5), (2, 6), (9, 6)])
+@pytest.mark.parametrize("n,marks", [(1, 5), (4, 5), (5, 6), (9, 6)])
 def test_timed_markers(lib, n, marks):
     """The markers that moe.h counts for the streaming kernels, in stream order, and the same bits."""
     cfg = cfg_of("int4_g64")
@@ -381,6 +381,26 @@ def test_timed_markers(lib, n, marks):
     assert s == B.MOE_OK and nm == marks
     assert torch.equal(got, out)
     assert all(ev[i].elapsed_time(ev[i + 1]) >= 0 for i in range(nm - 1))
+
+
+@gpu
+@pytest.mark.parametrize("n", [2, 3, 4])
+@pytest.mark.parametrize("held", [(0, 16), (5, 11)])
+def test_a_few_tokens_as_each_alone(lib, n, held):
+    """Up to four tokens of small experts: the bits of every token alone, with an expert twice in
+    a row, indices outside the layer, experts held elsewhere, and the shared expert's gate."""
+    cfg = cfg_of("int4_g32", top_k=4, zero_points=True, shared_gate=True)
+    lw = synth.expert_slice(synth.make_weights(cfg, "cuda"), *held)
+    x = synth.make_input(cfg, n, "cuda")
+    g = torch.Generator().manual_seed(n)
+    idx = torch.randint(0, 16, (n, 4), generator=g).to(torch.int32)
+    idx[0] = torch.tensor([7, 7, -1, 99])
+    idx, w = idx.cuda(), torch.rand(n, 4, generator=g).cuda()
+    layer, one = MoeLayer(lw, n, experts=held), MoeLayer(lw, 1, experts=held)
+    out = layer.experts(x, idx, w)
+    for t in range(n):
+        assert torch.equal(out[t], one.experts(x[t:t + 1], idx[t:t + 1], w[t:t + 1])[0])
+    assert layer.device_error() == 0
 
 
 @gpu
