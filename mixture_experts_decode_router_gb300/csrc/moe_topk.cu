@@ -383,22 +383,32 @@ __global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? kMinBlocks : 1) topk_
                 }
                 __syncwarp();
             }
-            const float gs = (p.r.top2 ? (size > 1 ? a + b : a) : a) + 0.f;
+            const bool two = p.r.top2 && size > 1;
+            const float gs = (two ? a + b : a) + 0.f;
             // Ranks by integers of the scores' order with the group in the low bits.
             const uint32_t gk = in ? (ordered(gs) & ~31u) | (31u - grp) : 0u;
             int ahead = 0;
             for (int g = 0; g < p.r.groups; ++g) ahead += __shfl_sync(0xffffffffu, gk, g * per) > gk ? 1 : 0;
             bool keep = in && ahead < p.r.kept;
             if (p.r.kept < p.r.groups) {
-                // Whether the last kept group is clear of the best left by `tol` of the larger, and `add`.
-                auto apart = [&](float tol, float add) {
-                    const float worst = unordered(__reduce_min_sync(0xffffffffu, keep ? ordered(gs) : 0xffffffffu));
-                    const float best = unordered(__reduce_max_sync(0xffffffffu, in && !keep ? ordered(gs) : 0u));
-                    return tol == 0.f ? worst >= best : worst - best > add + tol * fmaxf(fabsf(worst), fabsf(best));
+                // Whether every kept group is clear of every other: the lowest that the scores of
+                // the kept can be against the highest of the rest.  A score is off by `tol` of
+                // itself, and, of p (+ bias), by the errors of its p and the roundings of its
+                // terms.  These go with the terms: a sum of two large biases of opposite sign has
+                // them whole.  (tol 0 of logits: the scores are exact.  An infinite score is exact,
+                // its terms' roundings do not reach it; a NaN is clear of none.)
+                const float terms = two ? fabsf(a) + fabsf(b) : fabsf(a);
+                const float fix = by_p ? (two ? 2.f : 1.f) * perr + 0x1p-22f * terms : 1e-38f;
+                auto apart = [&](float tol) {
+                    const bool exact = tol == 0.f && !by_p;
+                    const float err = exact || fabsf(gs) == INFINITY ? 0.f : fix + tol * fabsf(gs);
+                    const float lo = gs == gs ? gs - err : -INFINITY, hi = gs == gs ? gs + err : INFINITY;
+                    const float worst = unordered(__reduce_min_sync(0xffffffffu, keep ? ordered(lo) : 0xffffffffu));
+                    const float best = unordered(__reduce_max_sync(0xffffffffu, in && !keep ? ordered(hi) : 0u));
+                    return exact ? worst >= best : worst > best;
                 };
-                const float err = by_p ? 4.f * perr : 1e-38f;
                 // (The index hides 32 ulps of a score in fp32, nothing of 16-bit logits.)
-                clear = apart(TYPE == MOE_F32 || by_p ? 0x1p-17f : 0.f, err);
+                clear = apart(TYPE == MOE_F32 || by_p ? 0x1p-17f : 0.f);
                 if (!clear) {                             // the whole scores
                     ahead = 0;
                     for (int g = 0; g < p.r.groups; ++g) {
@@ -406,7 +416,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? kMinBlocks : 1) topk_
                         ahead += (o > gs || (o == gs && g < grp)) ? 1 : 0;
                     }
                     keep = in && ahead < p.r.kept;
-                    clear = apart(by_p ? 0x1p-21f : 0.f, err);
+                    clear = apart(0.f);
                     if (by_p && !__all_sync(0xffffffffu, clear) && (sig || !biased)) {
                         // The experts that can be a group's two best (or best) in 64 bits, one lane
                         // each; without a bias the softmax's common factor is left out.

@@ -498,3 +498,17 @@ def test_logits_to_experts(lib):
             ref[t] += float(w[t, j]) * O.swiglu_mlp(xe[t], L.gate.expert(e), L.up.expert(e), L.down.expert(e))
     from tests.test_int4_experts import close
     close(out.float().cpu().numpy(), ref)
+
+
+@gpu
+@pytest.mark.parametrize("size,scale", [(2, 100.0), (4, 1024.0), (4, 1e4), (8, 1e6), (32, 4096.0)])
+@pytest.mark.parametrize("kept", [1, 4])
+@pytest.mark.parametrize("routing", ["softmax", "sigmoid"])
+def test_group_sums_that_cancel(lib, size, scale, kept, routing):
+    """Biases of opposite sign in each group's two best: the rounding of p + bias goes with the terms,
+    and what is left of their sum orders the groups."""
+    E = 8 * size
+    lg = draw(4000, E, seed=size)
+    b = torch.full((E,), -scale, device="cuda")
+    b[torch.arange(8, device="cuda") * size + torch.arange(8, device="cuda") % size] = scale
+    check(lg, min(4, kept * size), routing, b, 8, kept, "top2")
