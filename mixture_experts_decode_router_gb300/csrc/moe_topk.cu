@@ -420,7 +420,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, V <= 8 ? kMinBlocks : 1) topk_
                     if (by_p && !__all_sync(0xffffffffu, clear) && (sig || !biased)) {
                         // The experts that can be a group's two best (or best) in 64 bits, one lane
                         // each; without a bias the softmax's common factor is left out.
-                        const float low = (p.r.top2 ? b : a) - 4.f * perr - 0x1p-21f * fabsf(b);
+                        // (An infinite score is exact: less an error that goes with it, it would be NaN.)
+                        const float from = p.r.top2 ? b : a;
+                        const float low = fabsf(from) == INFINITY ? from : from - 4.f * perr - 0x1p-21f * fabsf(from);
                         int* list = reinterpret_cast<int*>(sc);
                         const int total = compact<V>([&](int i) {
                             const int ge = lanes ? grp * per : min((e0 + i) / size, 31);   // the lane that holds the group's scores

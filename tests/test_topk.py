@@ -512,3 +512,23 @@ def test_group_sums_that_cancel(lib, size, scale, kept, routing):
     b = torch.full((E,), -scale, device="cuda")
     b[torch.arange(8, device="cuda") * size + torch.arange(8, device="cuda") % size] = scale
     check(lg, min(4, kept * size), routing, b, 8, kept, "top2")
+
+
+@gpu
+@pytest.mark.parametrize("score", ["max", "top2"])
+@pytest.mark.parametrize("routing", ["softmax", "sigmoid"])
+def test_infinite_biases_in_groups(lib, score, routing):
+    """+inf twice in a group (of 2, 4 and 32 experts), in two groups, next to -inf, and groups of -inf alone."""
+    inf = float("inf")
+    for size in (2, 4, 32):
+        E = 8 * size
+        lg, base = draw(300, E, seed=30 + size), bias_of(E)
+        for at in ({5: (inf, inf)}, {5: (inf, inf), 2: (inf, inf)}, {6: (inf, -inf)}, {3: (-inf, -inf), 1: (inf, inf)}):
+            b = base.clone()
+            for g, v in at.items():
+                b[g * size:g * size + 2] = torch.tensor(v, device="cuda")
+            for kept in (1, 4):
+                check(lg, 2, routing, b, 8, kept, score)
+        b = base.clone()
+        b[:5 * size] = -inf                        # three groups are left
+        check(lg, 2, routing, b, 8, 4, score)
