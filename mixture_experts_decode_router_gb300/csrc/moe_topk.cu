@@ -144,17 +144,19 @@ __device__ __noinline__ int select_exact(const TopkParams& p, const float* sl, d
 // p, renormalised over the k when norm, times scale.  Renormalised weights are
 // ratios, formed from exp(l - M) with M the largest selected logit (sigmoid: at
 // most 0), so that they neither overflow nor vanish together.  Softmax without
-// renormalising takes the row's largest logit m and sum z of exp(l - m).
+// renormalising takes the row's largest logit m and sum z of exp(l - m).  (expf and whole
+// quotients: __expf is off by an ulp for each unit of its argument, 60 ulps of a sigmoid's
+// weight at a logit of -60; it saves nothing that 32768 rows show.)
 __device__ __forceinline__ float row_weight(const TopkParams& p, float l, float m, float z, int lane) {
     const bool in = lane < p.k, sig = mode_sigmoid(p.r.mode);
-    float v = sig ? __fdividef(1.f, 1.f + __expf(-l)) : __fdividef(__expf(l - m), z);
+    float v = sig ? 1.f / (1.f + expf(-l)) : expf(l - m) / z;
     if (!p.norm) return (m == -INFINITY && !sig && !(l != l) ? 0.f : v) * p.scale;
     // Softmax ratios, and sigmoids that are all small, from the largest selected logit.
     if (!sig || !__any_sync(0xffffffffu, in && l > -60.f)) {
         float M = in ? l : -INFINITY;
         for (int o = 1; o < p.k; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         M = __shfl_sync(0xffffffffu, M, 0);
-        v = __expf(l - M);   // (a small sigmoid is exp(l) to within its rounding)
+        v = expf(l - M);   // (a small sigmoid is exp(l) to within its rounding)
         if (M == -INFINITY && !(l != l)) v = 0.f;
     }
     if (!in) v = 0.f;
@@ -165,7 +167,7 @@ __device__ __forceinline__ float row_weight(const TopkParams& p, float l, float 
         tot += __shfl_xor_sync(0xffffffffu, tot, 8);
         tot += __shfl_xor_sync(0xffffffffu, tot, 16);
     }
-    return tot == 0.f ? 0.f : __fdividef(v, tot) * p.scale;
+    return tot == 0.f ? 0.f : v / tot * p.scale;
 }
 
 // V floats of a lane to and from shared memory (16-byte aligned when V is a multiple of 4).

@@ -532,3 +532,20 @@ def test_infinite_biases_in_groups(lib, score, routing):
         b = base.clone()
         b[:5 * size] = -inf                        # three groups are left
         check(lg, 2, routing, b, 8, 4, score)
+
+
+@gpu
+@pytest.mark.parametrize("norm", [False, True])
+def test_weights_of_far_logits(lib, norm):
+    """Small sigmoids and softmax terms keep their relative accuracy.  Logits are whole numbers, so l - m is
+    exact: exp (2 ulp, 4 * 2^-24), 1 + exp (2^-24), a quotient (2^-24), the row's sum (its terms, and 7 additions
+    at 64 experts: 11 * 2^-24), the factor (2^-24), and with norm the k chosen and their quotient (6 * 2^-24):
+    24 * 2^-24 at most."""
+    d = torch.arange(64, device="cuda", dtype=torch.float32)
+    lg = torch.stack([-d, -1.25 * d, 20.0 - d, -17.0 - d])
+    for routing in ("sigmoid", "softmax"):
+        op = MoeTopk(64, 32, routing, norm_topk_prob=norm, routed_scaling_factor=2.5)
+        idx, w = op.forward(lg)
+        ri, rw = plain(lg.double().cpu().numpy(), 32, routing, norm=norm, factor=2.5)
+        assert np.array_equal(idx.cpu().numpy(), ri)
+        assert np.max(np.abs(w.double().cpu().numpy() / rw - 1)) <= 24 * 2.0 ** -24
