@@ -186,6 +186,25 @@ PyObject* matvec(PyObject* const* a, Py_ssize_t na) {
     return wrap(std::move(out));
 }
 
+// What moe_experts and moe_forward read and write, as the library takes it.
+int64_t layer_rows(const moe_config_t& c, const at::Tensor& x) {
+    if (x.dim() < 1 || x.size(0) > INT32_MAX) raise(PyExc_ValueError, "x is [n, hidden]");
+    const int64_t n = x.size(0);
+    if (x.scalar_type() != at::kBFloat16 || x.numel() != n * c.hidden || !x.is_contiguous())
+        raise(PyExc_ValueError, "x is contiguous bfloat16 [n, hidden]");
+    return n;
+}
+void check_layer_routes(const at::Tensor& t, at::ScalarType type, int64_t n, int64_t k, int dev) {
+    if (t.scalar_type() != type || t.numel() < n * k || (t.dim() != 1 && (t.dim() != 2 || t.size(1) != k)) ||
+        !t.is_contiguous() || !t.is_cuda() || t.get_device() != dev)
+        raise(PyExc_ValueError, "idx is int32 and w float32, contiguous [>= n, k] on the current device");
+}
+void check_layer_out(const moe_config_t& c, const at::Tensor& t, int64_t n) {
+    current_gpu(t);
+    if (t.scalar_type() != at::kBFloat16 || t.numel() < n * c.hidden || !t.is_contiguous())
+        raise(PyExc_ValueError, "out is contiguous bfloat16 [>= n, hidden]");
+}
+
 // experts(config address, weights address, workspace address, its bytes, x, idx, w, stream or None) -> out
 PyObject* experts(PyObject* const* a, Py_ssize_t na) {
     need(na, 8);
@@ -194,14 +213,16 @@ PyObject* experts(PyObject* const* a, Py_ssize_t na) {
     void* ws = address<void>(a[2]);
     const size_t ws_bytes = (size_t)integer(a[3]);
     const at::Tensor &x = some_tensor(a[4]), &idx = some_tensor(a[5]), &w = some_tensor(a[6]);
-    if (x.dim() < 1 || x.size(0) > INT32_MAX) raise(PyExc_ValueError, "x is [n, hidden]");
-    const int64_t n = x.size(0);
+    const int64_t n = layer_rows(*c, x);
+    const int dev = current_gpu(x);
+    check_layer_routes(idx, at::kInt, n, c->top_k, dev);
+    check_layer_routes(w, at::kFloat, n, c->top_k, dev);
     at::Tensor out = matrix(n, c->hidden, at::kBFloat16, x.device());
     const void* xp = x.data_ptr();
     const int32_t* ip = static_cast<const int32_t*>(idx.data_ptr());
     const float* wp = static_cast<const float*>(w.data_ptr());
     void* op = out.data_ptr();
-    const moe_stream_t st = stream_of(a[7], c10::cuda::current_device());
+    const moe_stream_t st = stream_of(a[7], dev);
     moe_status_t s;
     Py_BEGIN_ALLOW_THREADS;
     s = g_experts(c, wts, xp, (int32_t)n, ip, wp, op, ws, ws_bytes, st);
@@ -222,9 +243,12 @@ PyObject* forward(PyObject* const* a, Py_ssize_t na) {
     const at::Tensor *go = tensor(a[5]), *gi = tensor(a[6]), *gw = tensor(a[7]);
     const int routing = PyObject_IsTrue(a[8]);
     if (routing < 0) throw Raised{};
-    if (x.dim() < 1 || x.size(0) > INT32_MAX) raise(PyExc_ValueError, "x is [n, hidden]");
     if (!go && c->accumulate) raise(PyExc_ValueError, "accumulate needs out");
-    const int64_t n = x.size(0);
+    const int64_t n = layer_rows(*c, x);
+    const int dev = current_gpu(x);
+    if (go) check_layer_out(*c, *go, n);
+    if (gi) check_layer_routes(*gi, at::kInt, n, c->top_k, dev);
+    if (gw) check_layer_routes(*gw, at::kFloat, n, c->top_k, dev);
     at::Tensor out = go ? *go : matrix(n, c->hidden, at::kBFloat16, x.device()), idx, w;
     if (gi) idx = *gi;
     else if (routing) idx = matrix(n, c->top_k, at::kInt, x.device());
@@ -234,7 +258,7 @@ PyObject* forward(PyObject* const* a, Py_ssize_t na) {
     void* op = out.data_ptr();
     int32_t* ip = idx.defined() ? static_cast<int32_t*>(idx.data_ptr()) : nullptr;
     float* wp = w.defined() ? static_cast<float*>(w.data_ptr()) : nullptr;
-    const moe_stream_t st = stream_of(a[9], c10::cuda::current_device());
+    const moe_stream_t st = stream_of(a[9], dev);
     moe_status_t s;
     Py_BEGIN_ALLOW_THREADS;
     s = g_forward(c, wts, xp, (int32_t)n, op, ip, wp, ws, ws_bytes, st);

@@ -1,0 +1,104 @@
+"""The Python holders' calls: what they take, what they refuse, the memory and the streams they use."""
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_decode_router_gb300 import binding as B
+from mixture_experts_decode_router_gb300 import synth
+from mixture_experts_decode_router_gb300.layer import MoeLayer
+
+gpu = pytest.mark.gpu
+
+
+def cfg_of(fmt="int4_g32", **kw):
+    d = dict(name="holders", hidden=128, num_experts=8, top_k=2, inter=64, shared_inter=64,
+             routing=synth.ROUTE_SOFTMAX, norm_topk_prob=True, routed_scaling_factor=1.0, expert_fmt=fmt, n_tokens=3)
+    d.update(kw)
+    return synth.LayerConfig(**d)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    B.load()
+
+
+# ---------------------------------------------------------------- the layer's tensors
+
+def refusals_of_a_layer(dev):
+    """Every tensor that moe_experts or moe_forward would read or write as something else."""
+    layer = MoeLayer(synth.make_weights(cfg_of(), dev), 3)
+    def t(shape, dtype):
+        return torch.zeros(shape, dtype=dtype, device=dev)
+    x, idx, w = t((3, 128), torch.bfloat16), t((3, 2), torch.int32), t((3, 2), torch.float32)
+    xs = [x.half(), x.float(), x[:, :64], x[:, :64].contiguous(), t((3, 256), torch.bfloat16)[:, ::2], x[0],
+          t((128, 3), torch.bfloat16).T, torch.zeros((), dtype=torch.bfloat16, device=dev)]
+    routes = [idx.long(), w, idx[:2], idx[:, :1], t((3, 1), torch.int32), t((3, 4), torch.int32)[:, ::2], t((2, 3), torch.int32),
+              t((3, 3), torch.int32), t((5,), torch.int32)]
+    weights = [w.double(), idx, w.half(), w[:2], w[:, :1], t((3, 4), torch.float32)[:, ::2], t((3, 3), torch.float32)]
+    outs = [x.float(), x[:2], t((3, 256), torch.bfloat16)[:, ::2], x[:, :64].contiguous()]
+    for bad in xs:
+        with pytest.raises(ValueError):
+            layer.experts(bad, idx, w)
+        with pytest.raises(ValueError):
+            layer.forward(bad)
+    for bad in routes:
+        with pytest.raises(ValueError):
+            layer.experts(x, bad, w)
+        with pytest.raises(ValueError):
+            layer.forward(x, idx=bad)
+    for bad in weights:
+        with pytest.raises(ValueError):
+            layer.experts(x, idx, bad)
+        with pytest.raises(ValueError):
+            layer.forward(x, w=bad)
+    for bad in outs:
+        with pytest.raises(ValueError):
+            layer.forward(x, out=bad)
+    for bad in (None, 3, [[0.0] * 128]):
+        with pytest.raises(TypeError):
+            layer.forward(bad)
+    return layer, x, idx, w
+
+
+def test_layer_refusals():
+    """On the CPU, where nothing can run: a ValueError of the call, before the library is called."""
+    layer, x, idx, w = refusals_of_a_layer("cpu")
+    with pytest.raises(ValueError):
+        layer.experts(x, idx, w)               # nothing of this is on a GPU
+    with pytest.raises(ValueError):
+        layer.forward(x)
+
+
+@gpu
+def test_layer_refusals_on_the_gpu(lib):
+    layer, x, idx, w = refusals_of_a_layer("cuda")
+    for kw in (dict(idx=idx.cpu()), dict(w=w.cpu()), dict(out=x.cpu()), dict(idx=idx.cpu().pin_memory())):
+        with pytest.raises(ValueError):
+            layer.forward(x, **kw)
+    with pytest.raises(ValueError):
+        layer.experts(x, idx.cpu(), w)
+    assert layer.device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8_b128", "nvfp4", "int4_g32"])
+def test_forms_that_hold_the_same_elements(lib, fmt):
+    """Larger buffers, flat routes, and x of more than two dimensions are taken as before."""
+    cfg = cfg_of(fmt)
+    lw = synth.make_weights(cfg, "cuda")
+    layer, x = MoeLayer(lw, 3), synth.make_input(cfg, 3, "cuda")
+    out, idx, w = layer.forward(x)
+    assert torch.equal(layer.experts(x.view(3, 1, 128), idx.view(-1), w.view(-1)), layer.experts(x, idx, w))
+    big = torch.zeros(5, 128, dtype=torch.bfloat16, device="cuda")
+    bi, bw = torch.zeros(5, 2, dtype=torch.int32, device="cuda"), torch.zeros(5, 2, device="cuda")
+    layer.forward(x, out=big, idx=bi, w=bw)
+    assert torch.equal(big[:3], out) and torch.equal(bi[:3], idx) and torch.equal(bw[:3], w)
+    assert not big[3:].any() and not bi[3:].any() and not bw[3:].any()
+    # One row of a wider matrix is contiguous.
+    wide = torch.zeros(1, 200, dtype=torch.bfloat16, device="cuda")
+    wide[:, :128] = x[:1]
+    assert torch.equal(layer.forward(wide[:, :128])[0], layer.forward(x[:1])[0])
+    assert layer.forward(x[:0])[0].shape == (0, 128)
