@@ -187,6 +187,8 @@ PyObject* matvec(PyObject* const* a, Py_ssize_t na) {
 }
 
 // What moe_experts and moe_forward read and write, as the library takes it.
+// Outputs and routes may be device addresses, which the caller answers for.
+bool is_address(PyObject* o) { return PyLong_Check(o) && !PyBool_Check(o); }
 int64_t layer_rows(const moe_config_t& c, const at::Tensor& x) {
     if (x.dim() < 1 || x.size(0) > INT32_MAX) raise(PyExc_ValueError, "x is [n, hidden]");
     const int64_t n = x.size(0);
@@ -194,15 +196,22 @@ int64_t layer_rows(const moe_config_t& c, const at::Tensor& x) {
         raise(PyExc_ValueError, "x is contiguous bfloat16 [n, hidden]");
     return n;
 }
-void check_layer_routes(const at::Tensor& t, at::ScalarType type, int64_t n, int64_t k, int dev) {
+template <typename T>
+T* layer_routes(PyObject* o, at::ScalarType type, int64_t n, int64_t k, int dev) {
+    if (is_address(o)) return address<T>(o);
+    const at::Tensor& t = some_tensor(o);
     if (t.scalar_type() != type || t.numel() < n * k || (t.dim() != 1 && (t.dim() != 2 || t.size(1) != k)) ||
         !t.is_contiguous() || !t.is_cuda() || t.get_device() != dev)
         raise(PyExc_ValueError, "idx is int32 and w float32, contiguous [>= n, k] on the current device");
+    return data<T>(t);
 }
-void check_layer_out(const moe_config_t& c, const at::Tensor& t, int64_t n) {
+void* layer_out(const moe_config_t& c, PyObject* o, int64_t n) {
+    if (is_address(o)) return address<void>(o);
+    const at::Tensor& t = some_tensor(o);
     current_gpu(t);
     if (t.scalar_type() != at::kBFloat16 || t.numel() < n * c.hidden || !t.is_contiguous())
         raise(PyExc_ValueError, "out is contiguous bfloat16 [>= n, hidden]");
+    return t.data_ptr();
 }
 
 // experts(config address, weights address, workspace address, its bytes, x, idx, w, stream or None) -> out
@@ -212,15 +221,13 @@ PyObject* experts(PyObject* const* a, Py_ssize_t na) {
     const moe_weights_t* wts = address<const moe_weights_t>(a[1]);
     void* ws = address<void>(a[2]);
     const size_t ws_bytes = (size_t)integer(a[3]);
-    const at::Tensor &x = some_tensor(a[4]), &idx = some_tensor(a[5]), &w = some_tensor(a[6]);
+    const at::Tensor& x = some_tensor(a[4]);
     const int64_t n = layer_rows(*c, x);
     const int dev = current_gpu(x);
-    check_layer_routes(idx, at::kInt, n, c->top_k, dev);
-    check_layer_routes(w, at::kFloat, n, c->top_k, dev);
+    const int32_t* ip = layer_routes<int32_t>(a[5], at::kInt, n, c->top_k, dev);
+    const float* wp = layer_routes<float>(a[6], at::kFloat, n, c->top_k, dev);
     at::Tensor out = matrix(n, c->hidden, at::kBFloat16, x.device());
     const void* xp = x.data_ptr();
-    const int32_t* ip = static_cast<const int32_t*>(idx.data_ptr());
-    const float* wp = static_cast<const float*>(w.data_ptr());
     void* op = out.data_ptr();
     const moe_stream_t st = stream_of(a[7], dev);
     moe_status_t s;
@@ -240,33 +247,31 @@ PyObject* forward(PyObject* const* a, Py_ssize_t na) {
     void* ws = address<void>(a[2]);
     const size_t ws_bytes = (size_t)integer(a[3]);
     const at::Tensor& x = some_tensor(a[4]);
-    const at::Tensor *go = tensor(a[5]), *gi = tensor(a[6]), *gw = tensor(a[7]);
     const int routing = PyObject_IsTrue(a[8]);
     if (routing < 0) throw Raised{};
-    if (!go && c->accumulate) raise(PyExc_ValueError, "accumulate needs out");
+    if (a[5] == Py_None && c->accumulate) raise(PyExc_ValueError, "accumulate needs out");
     const int64_t n = layer_rows(*c, x);
     const int dev = current_gpu(x);
-    if (go) check_layer_out(*c, *go, n);
-    if (gi) check_layer_routes(*gi, at::kInt, n, c->top_k, dev);
-    if (gw) check_layer_routes(*gw, at::kFloat, n, c->top_k, dev);
-    at::Tensor out = go ? *go : matrix(n, c->hidden, at::kBFloat16, x.device()), idx, w;
-    if (gi) idx = *gi;
-    else if (routing) idx = matrix(n, c->top_k, at::kInt, x.device());
-    if (gw) w = *gw;
-    else if (routing) w = matrix(n, c->top_k, at::kFloat, x.device());
+    // What is not given is made here, and returned; what is given is returned as it is.
+    at::Tensor out, idx, w;
+    void* op;
+    int32_t* ip = nullptr;
+    float* wp = nullptr;
+    if (a[5] != Py_None) op = layer_out(*c, a[5], n);
+    if (a[6] != Py_None) ip = layer_routes<int32_t>(a[6], at::kInt, n, c->top_k, dev);
+    if (a[7] != Py_None) wp = layer_routes<float>(a[7], at::kFloat, n, c->top_k, dev);
+    if (a[5] == Py_None) op = (out = matrix(n, c->hidden, at::kBFloat16, x.device())).data_ptr();
+    if (a[6] == Py_None && routing) ip = data<int32_t>(idx = matrix(n, c->top_k, at::kInt, x.device()));
+    if (a[7] == Py_None && routing) wp = data<float>(w = matrix(n, c->top_k, at::kFloat, x.device()));
     const void* xp = x.data_ptr();
-    void* op = out.data_ptr();
-    int32_t* ip = idx.defined() ? static_cast<int32_t*>(idx.data_ptr()) : nullptr;
-    float* wp = w.defined() ? static_cast<float*>(w.data_ptr()) : nullptr;
     const moe_stream_t st = stream_of(a[9], dev);
     moe_status_t s;
     Py_BEGIN_ALLOW_THREADS;
     s = g_forward(c, wts, xp, (int32_t)n, op, ip, wp, ws, ws_bytes, st);
     Py_END_ALLOW_THREADS;
     check(s);
-    PyObject* none = Py_None;
-    return Py_BuildValue("(NNN)", wrap(std::move(out)), idx.defined() ? wrap(std::move(idx)) : Py_NewRef(none),
-                         w.defined() ? wrap(std::move(w)) : Py_NewRef(none));
+    auto give = [](at::Tensor& made, PyObject* given) { return made.defined() ? wrap(std::move(made)) : Py_NewRef(given); };
+    return Py_BuildValue("(NNN)", give(out, a[5]), give(idx, a[6]), give(w, a[7]));
 }
 
 // No C++ exception leaves a Python call.

@@ -102,3 +102,28 @@ def test_forms_that_hold_the_same_elements(lib, fmt):
     wide[:, :128] = x[:1]
     assert torch.equal(layer.forward(wide[:, :128])[0], layer.forward(x[:1])[0])
     assert layer.forward(x[:0])[0].shape == (0, 128)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "int4_g32"])
+def test_addresses_of_outputs_and_routes(lib, fmt):
+    """out, idx and w may be device addresses, as the C functions take them; they come back as they were given."""
+    cfg = cfg_of(fmt)
+    layer = MoeLayer(synth.make_weights(cfg, "cuda"), 3)
+    x = synth.make_input(cfg, 3, "cuda")
+    out, idx, w = layer.forward(x)
+    o2, i2, w2 = torch.zeros_like(out), torch.zeros_like(idx), torch.zeros_like(w)
+    got = layer.forward(x, out=o2.data_ptr(), idx=i2.data_ptr(), w=w2.data_ptr())
+    assert got == (o2.data_ptr(), i2.data_ptr(), w2.data_ptr())
+    assert torch.equal(o2, out) and torch.equal(i2, idx) and torch.equal(w2, w)
+    assert torch.equal(layer.experts(x, idx.data_ptr(), w.data_ptr()), layer.experts(x, idx, w))
+
+
+def test_what_is_neither_a_tensor_nor_an_address():
+    layer = MoeLayer(synth.make_weights(cfg_of(), "cpu"), 3)
+    x = torch.zeros(3, 128, dtype=torch.bfloat16)
+    for bad in ("idx", 1.5, [0], True):
+        with pytest.raises((TypeError, ValueError)):
+            layer.forward(x, idx=bad)
+        with pytest.raises((TypeError, ValueError)):
+            layer.experts(x, bad, bad)
