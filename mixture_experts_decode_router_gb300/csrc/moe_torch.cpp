@@ -64,6 +64,7 @@ moe_stream_t stream_of(PyObject* o, int dev) {
     return o == Py_None ? (moe_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream()
                         : address<std::remove_pointer_t<moe_stream_t>>(o);
 }
+c10::Device gpu(int dev) { return c10::Device(c10::kCUDA, (c10::DeviceIndex)dev); }
 at::Tensor matrix(int64_t rows, int64_t cols, at::ScalarType type, c10::Device dev) {
     return at::empty({rows, cols}, at::TensorOptions().dtype(type).device(dev));
 }
@@ -124,10 +125,9 @@ PyObject* topk(PyObject* const* a, Py_ssize_t na) {
     const int dev = current_gpu(l);
     if (bias && (!bias->is_cuda() || bias->get_device() != dev)) raise(PyExc_ValueError, "bias is not on the current device");
     const int64_t n = l.size(0);
-    const c10::Device on(c10::kCUDA, (c10::DeviceIndex)dev);
     if (gi) check_routes(*gi, at::kInt, n, k, dev);
     if (gw) check_routes(*gw, at::kFloat, n, k, dev);
-    at::Tensor idx = gi ? *gi : matrix(n, k, at::kInt, on), w = gw ? *gw : matrix(n, k, at::kFloat, on);
+    at::Tensor idx = gi ? *gi : matrix(n, k, at::kInt, gpu(dev)), w = gw ? *gw : matrix(n, k, at::kFloat, gpu(dev));
     if (n > INT32_MAX) raise(PyExc_ValueError, "too many rows");
     const void* lp = l.data_ptr();
     const float* bp = bias ? data<const float>(*bias) : nullptr;
@@ -172,7 +172,7 @@ PyObject* matvec(PyObject* const* a, Py_ssize_t na) {
     } else {
         if (c.accumulate) raise(PyExc_ValueError, "accumulate needs out");
         const at::ScalarType type = c.out_type == MOE_F32 ? at::kFloat : c.out_type == MOE_BF16 ? at::kBFloat16 : at::kHalf;
-        out = matrix(n, O, type, c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+        out = matrix(n, O, type, gpu(dev));
     }
     const void* xp = x.data_ptr();
     void* op = out.data_ptr();
@@ -226,7 +226,7 @@ PyObject* experts(PyObject* const* a, Py_ssize_t na) {
     const int dev = current_gpu(x);
     const int32_t* ip = layer_routes<int32_t>(a[5], at::kInt, n, c->top_k, dev);
     const float* wp = layer_routes<float>(a[6], at::kFloat, n, c->top_k, dev);
-    at::Tensor out = matrix(n, c->hidden, at::kBFloat16, x.device());
+    at::Tensor out = matrix(n, c->hidden, at::kBFloat16, gpu(dev));
     const void* xp = x.data_ptr();
     void* op = out.data_ptr();
     const moe_stream_t st = stream_of(a[7], dev);
@@ -260,9 +260,9 @@ PyObject* forward(PyObject* const* a, Py_ssize_t na) {
     if (a[5] != Py_None) op = layer_out(*c, a[5], n);
     if (a[6] != Py_None) ip = layer_routes<int32_t>(a[6], at::kInt, n, c->top_k, dev);
     if (a[7] != Py_None) wp = layer_routes<float>(a[7], at::kFloat, n, c->top_k, dev);
-    if (a[5] == Py_None) op = (out = matrix(n, c->hidden, at::kBFloat16, x.device())).data_ptr();
-    if (a[6] == Py_None && routing) ip = data<int32_t>(idx = matrix(n, c->top_k, at::kInt, x.device()));
-    if (a[7] == Py_None && routing) wp = data<float>(w = matrix(n, c->top_k, at::kFloat, x.device()));
+    if (a[5] == Py_None) op = (out = matrix(n, c->hidden, at::kBFloat16, gpu(dev))).data_ptr();
+    if (a[6] == Py_None && routing) ip = data<int32_t>(idx = matrix(n, c->top_k, at::kInt, gpu(dev)));
+    if (a[7] == Py_None && routing) wp = data<float>(w = matrix(n, c->top_k, at::kFloat, gpu(dev)));
     const void* xp = x.data_ptr();
     const moe_stream_t st = stream_of(a[9], dev);
     moe_status_t s;

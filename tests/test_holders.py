@@ -127,3 +127,19 @@ def test_what_is_neither_a_tensor_nor_an_address():
             layer.forward(x, idx=bad)
         with pytest.raises((TypeError, ValueError)):
             layer.experts(x, bad, bad)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "int4_g32"])
+@pytest.mark.parametrize("n", [1, 3])
+def test_pinned_x_without_outputs(lib, fmt, n):
+    """What a call with x in pinned memory returns is on the current GPU."""
+    cfg = cfg_of(fmt)
+    layer = MoeLayer(synth.make_weights(cfg, "cuda"), n)
+    x = synth.make_input(cfg, n, "cuda")
+    want = layer.forward(x)
+    host = x.cpu().pin_memory()
+    for got, ref in zip(layer.forward(host), want):
+        assert got.is_cuda and torch.equal(got, ref)
+    assert torch.equal(layer.experts(host, *want[1:]), layer.experts(x, *want[1:]))
+    torch.cuda.synchronize()
