@@ -222,6 +222,7 @@ PyObject* experts(PyObject* const* a, Py_ssize_t na) {
     void* ws = address<void>(a[2]);
     const size_t ws_bytes = (size_t)integer(a[3]);
     const at::Tensor& x = some_tensor(a[4]);
+    if (c->accumulate) raise(PyExc_ValueError, "experts() makes its output: accumulate into the out of forward()");
     const int64_t n = layer_rows(*c, x);
     const int dev = current_gpu(x);
     const int32_t* ip = layer_routes<int32_t>(a[5], at::kInt, n, c->top_k, dev);

@@ -143,3 +143,13 @@ def test_pinned_x_without_outputs(lib, fmt, n):
         assert got.is_cuda and torch.equal(got, ref)
     assert torch.equal(layer.experts(host, *want[1:]), layer.experts(x, *want[1:]))
     torch.cuda.synchronize()
+
+
+def test_experts_of_an_accumulating_layer():
+    """There is nothing to add to: refused (the output would be added to what its memory held)."""
+    layer = MoeLayer(synth.make_weights(cfg_of(), "cpu"), 3, accumulate=True)
+    x, idx, w = torch.zeros(3, 128, dtype=torch.bfloat16), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2)
+    with pytest.raises(ValueError, match="accumulate"):
+        layer.experts(x, idx, w)
+    with pytest.raises(ValueError, match="accumulate"):
+        layer.forward(x)
