@@ -214,17 +214,25 @@ void* layer_out(const moe_config_t& c, PyObject* o, int64_t n) {
     return t.data_ptr();
 }
 
-// experts(config address, weights address, workspace address, its bytes, x, idx, w, stream or None) -> out
+void* workspace(PyObject* o, size_t bytes, int dev) {
+    if (is_address(o)) return address<void>(o);
+    const at::Tensor& t = some_tensor(o);
+    if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous() || t.nbytes() < bytes)
+        raise(PyExc_ValueError, "the workspace is ws_bytes of contiguous memory on the current device");
+    return t.data_ptr();
+}
+
+// experts(config address, weights address, workspace or its address, its bytes, x, idx, w, stream or None) -> out
 PyObject* experts(PyObject* const* a, Py_ssize_t na) {
     need(na, 8);
     const moe_config_t* c = address<const moe_config_t>(a[0]);
     const moe_weights_t* wts = address<const moe_weights_t>(a[1]);
-    void* ws = address<void>(a[2]);
     const size_t ws_bytes = (size_t)integer(a[3]);
     const at::Tensor& x = some_tensor(a[4]);
     if (c->accumulate) raise(PyExc_ValueError, "experts() makes its output: accumulate into the out of forward()");
     const int64_t n = layer_rows(*c, x);
     const int dev = current_gpu(x);
+    void* ws = workspace(a[2], ws_bytes, dev);
     const int32_t* ip = layer_routes<int32_t>(a[5], at::kInt, n, c->top_k, dev);
     const float* wp = layer_routes<float>(a[6], at::kFloat, n, c->top_k, dev);
     at::Tensor out = matrix(n, c->hidden, at::kBFloat16, gpu(dev));
@@ -239,13 +247,12 @@ PyObject* experts(PyObject* const* a, Py_ssize_t na) {
     return wrap(std::move(out));
 }
 
-// forward(config address, weights address, workspace address, its bytes, x, out or None, idx or None, w or None,
+// forward(config address, weights address, workspace or its address, its bytes, x, out or None, idx or None, w or None,
 // whether idx and w are wanted, stream or None) -> (out, idx, w)
 PyObject* forward(PyObject* const* a, Py_ssize_t na) {
     need(na, 10);
     const moe_config_t* c = address<const moe_config_t>(a[0]);
     const moe_weights_t* wts = address<const moe_weights_t>(a[1]);
-    void* ws = address<void>(a[2]);
     const size_t ws_bytes = (size_t)integer(a[3]);
     const at::Tensor& x = some_tensor(a[4]);
     const int routing = PyObject_IsTrue(a[8]);
@@ -253,6 +260,7 @@ PyObject* forward(PyObject* const* a, Py_ssize_t na) {
     if (a[5] == Py_None && c->accumulate) raise(PyExc_ValueError, "accumulate needs out");
     const int64_t n = layer_rows(*c, x);
     const int dev = current_gpu(x);
+    void* ws = workspace(a[2], ws_bytes, dev);
     // What is not given is made here, and returned; what is given is returned as it is.
     at::Tensor out, idx, w;
     void* op;

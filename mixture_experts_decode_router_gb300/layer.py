@@ -113,13 +113,13 @@ class MoeLayer:
         self.max_tokens = max_tokens
         calls = B.tensor_calls()
         self._experts, self._forward = calls.experts, calls.forward
-        self._args = (addressof(self.c_cfg), addressof(self.c_w), self.ws.data_ptr(), self.ws_bytes)
 
     def forward(self, x: torch.Tensor, out=None, idx=None, w=None, stream=None,
                 routing: bool = True):
         """``routing=False``: do not return the routing (idx and w are None), so
         a call that holds no routed expert can skip it."""
-        return self._forward(*self._args, x, out, idx, w, routing, stream if stream is None else B._stream(stream))
+        return self._forward(addressof(self.c_cfg), addressof(self.c_w), self.ws, self.ws_bytes, x, out, idx, w, routing,
+                             stream if stream is None else B._stream(stream))
 
     def device_error(self, stream=None) -> int:
         """Reads and clears the workspace's device error word (syncs the stream)."""
@@ -136,7 +136,8 @@ class MoeLayer:
         return idx, w, lg
 
     def experts(self, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, stream=None):
-        return self._experts(*self._args, x, idx, w, stream if stream is None else B._stream(stream))
+        return self._experts(addressof(self.c_cfg), addressof(self.c_w), self.ws, self.ws_bytes, x, idx, w,
+                             stream if stream is None else B._stream(stream))
 
 
 class MoeTopk:
@@ -164,10 +165,10 @@ class MoeTopk:
         c.norm_topk_prob = 1 if norm_topk_prob else 0
         c.routed_scaling_factor = routed_scaling_factor
         self.num_experts, self.top_k, self.bias, self.c_cfg = num_experts, top_k, bias, c
-        self._topk, self._cfg = B.tensor_calls().topk, addressof(c)
+        self._topk = B.tensor_calls().topk
 
     def forward(self, logits: torch.Tensor, idx=None, w=None, stream=None):
-        return self._topk(self._cfg, self.bias, logits, idx, w, stream if stream is None else B._stream(stream))
+        return self._topk(addressof(self.c_cfg), self.bias, logits, idx, w, stream if stream is None else B._stream(stream))
 
 
 class MoeMatvec:
@@ -191,13 +192,22 @@ class MoeMatvec:
         c.out_features, c.in_features, c.w_fmt = out_f, in_f, _FMT[q.fmt]
         c.out_type, c.accumulate = _TYPE[out_dtype], 1 if accumulate else 0
         self.c_cfg, self.c_w = c, _qmat(q)
-        self.weights, self.bias, self.out_dtype = q, bias, out_dtype
+        self._held = q, bias, (q.w, q.scale, q.scale2, q.zero)   # the memory that c_w and the bias point to
+        self.out_dtype = out_dtype
         self.in_features, self.out_features, self.accumulate = in_f, out_f, accumulate
         dev = q.w.get_device()
         if any(t is not None and t.get_device() != dev for t in (q.scale, q.scale2, q.zero, bias)):
             raise ValueError("weights and bias on one device")
         self._matvec = B.tensor_calls().matvec
-        self._args = (addressof(c), addressof(self.c_w), 0 if bias is None else bias.data_ptr(), dev)
+        self._bias, self._device = 0 if bias is None else bias.data_ptr(), dev
+
+    @property
+    def weights(self) -> QMatT:
+        return self._held[0]
+
+    @property
+    def bias(self) -> Optional[torch.Tensor]:
+        return self._held[1]
 
     def forward(self, x: torch.Tensor, out=None, stream=None):
-        return self._matvec(*self._args, x, out, stream if stream is None else B._stream(stream))
+        return self._matvec(addressof(self.c_cfg), addressof(self.c_w), self._bias, self._device, x, out, stream if stream is None else B._stream(stream))

@@ -6,7 +6,7 @@ import torch
 
 from mixture_experts_decode_router_gb300 import binding as B
 from mixture_experts_decode_router_gb300 import synth
-from mixture_experts_decode_router_gb300.layer import MoeLayer
+from mixture_experts_decode_router_gb300.layer import MoeLayer, MoeMatvec
 
 gpu = pytest.mark.gpu
 
@@ -153,3 +153,57 @@ def test_experts_of_an_accumulating_layer():
         layer.experts(x, idx, w)
     with pytest.raises(ValueError, match="accumulate"):
         layer.forward(x)
+
+
+# ---------------------------------------------------------------- what the holders hold
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "int4_g32"])
+@pytest.mark.parametrize("n", [1, 3])
+def test_a_new_workspace_config_or_weights(lib, fmt, n):
+    """A workspace, config or weight struct assigned after construction is the one that the next call uses."""
+    cfg = cfg_of(fmt)
+    a, b = (synth.make_weights(cfg.with_(seed=s), "cuda") for s in (1, 2))
+    layer, other, x = MoeLayer(a, n), MoeLayer(b, n), synth.make_input(cfg, n, "cuda")
+    want = layer.forward(x)
+    old = layer.ws
+    layer.ws = torch.zeros_like(old)
+    old.zero_()
+    assert torch.equal(layer.forward(x)[0], want[0])
+    assert not old.any() and layer.ws.any()
+    was = layer.c_cfg, layer.c_w                            # (held: the calls before could read them still)
+    layer.c_cfg = type(was[0]).from_buffer_copy(was[0])
+    layer.c_cfg.routed_scaling_factor = 2.0
+    assert torch.equal(layer.forward(x)[2], 2 * want[2])
+    layer.c_cfg, layer.c_w = was[0], other.c_w
+    assert torch.equal(layer.forward(x)[0], other.forward(x)[0])
+    layer.c_w = was[1]
+    assert torch.equal(layer.forward(x)[0], want[0])
+
+
+@gpu
+def test_a_new_workspace_of_another_size(lib):
+    cfg = cfg_of()
+    layer, x = MoeLayer(synth.make_weights(cfg, "cuda"), 3), synth.make_input(cfg, 3, "cuda")
+    for bad in (torch.zeros(16, dtype=torch.uint8, device="cuda"), layer.ws.cpu(), torch.zeros(2 * layer.ws_bytes, dtype=torch.uint8, device="cuda")[::2]):
+        good, layer.ws = layer.ws, bad
+        with pytest.raises(ValueError):
+            layer.forward(x)
+        layer.ws = good
+    layer.forward(x)
+    assert layer.device_error() == 0
+
+
+def test_a_matrix_keeps_what_it_points_to():
+    """The weights and the bias are those of construction: assigning others would leave the struct's addresses behind."""
+    w, s, _ = synth.quant_int4(torch.randn(16, 64), 32)
+    q = synth.QMatT("int4_g32", w, s)
+    op = MoeMatvec(q, bias=torch.zeros(16))
+    assert op.weights is q and op.bias.shape == (16,)
+    for name in ("weights", "bias"):
+        with pytest.raises(AttributeError):
+            setattr(op, name, None)
+    at, held = op.c_w.scale, s.data_ptr()
+    q.scale = torch.zeros_like(s)          # the tensors that the struct points to live on
+    del s
+    assert at == held and any(t is not None and t.data_ptr() == at for t in op._held[2])
