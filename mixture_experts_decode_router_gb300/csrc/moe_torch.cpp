@@ -122,6 +122,8 @@ PyObject* topk(PyObject* const* a, Py_ssize_t na) {
     if (c.logits_type < 0) raise(PyExc_KeyError, "logits are float32, bfloat16 or float16");
     if (l.dim() != 2 || l.size(1) != E || (E > 1 && l.stride(1) != 1))
         raise(PyExc_ValueError, "logits are [n, num_experts] with contiguous rows");
+    if (bias && (bias->scalar_type() != at::kFloat || bias->dim() != 1 || bias->size(0) != E || !bias->is_contiguous()))
+        raise(PyExc_ValueError, "bias is contiguous float32 [num_experts]");
     const int dev = current_gpu(l);
     if (bias && (!bias->is_cuda() || bias->get_device() != dev)) raise(PyExc_ValueError, "bias is not on the current device");
     const int64_t n = l.size(0);

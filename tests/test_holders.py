@@ -6,7 +6,7 @@ import torch
 
 from mixture_experts_decode_router_gb300 import binding as B
 from mixture_experts_decode_router_gb300 import synth
-from mixture_experts_decode_router_gb300.layer import MoeLayer, MoeMatvec
+from mixture_experts_decode_router_gb300.layer import MoeLayer, MoeMatvec, MoeTopk
 
 gpu = pytest.mark.gpu
 
@@ -207,3 +207,11 @@ def test_a_matrix_keeps_what_it_points_to():
     q.scale = torch.zeros_like(s)          # the tensors that the struct points to live on
     del s
     assert at == held and any(t is not None and t.data_ptr() == at for t in op._held[2])
+
+
+def test_a_bias_assigned_later_is_checked():
+    op = MoeTopk(8, 2, "sigmoid", torch.zeros(8))
+    for bad in (torch.zeros(7), torch.zeros(8, dtype=torch.float64), torch.zeros(16)[::2], torch.zeros(8, 1)):
+        op.bias = bad
+        with pytest.raises(ValueError, match="bias is contiguous"):
+            op.forward(torch.zeros(3, 8))      # (before what says that the logits are on no GPU)
