@@ -9,7 +9,9 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -64,9 +66,16 @@ moe_stream_t stream_of(PyObject* o, int dev) {
     return o == Py_None ? (moe_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream()
                         : address<std::remove_pointer_t<moe_stream_t>>(o);
 }
-c10::Device gpu(int dev) { return c10::Device(c10::kCUDA, (c10::DeviceIndex)dev); }
-at::Tensor matrix(int64_t rows, int64_t cols, at::ScalarType type, c10::Device dev) {
-    return at::empty({rows, cols}, at::TensorOptions().dtype(type).device(dev));
+// An output on GPU dev for a call on stream st: its memory is that stream's, so that it is not
+// handed out again while the call runs, and in use on the current one, where the caller reads it.
+at::Tensor matrix(int64_t rows, int64_t cols, at::ScalarType type, int dev, moe_stream_t st) {
+    const at::TensorOptions how = at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev);
+    if (current.stream() == st) return at::empty({rows, cols}, how);
+    const c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(st, (c10::DeviceIndex)dev));
+    at::Tensor t = at::empty({rows, cols}, how);
+    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current);
+    return t;
 }
 int type_code(const at::Tensor& t) {
     switch (t.scalar_type()) {
@@ -129,14 +138,14 @@ PyObject* topk(PyObject* const* a, Py_ssize_t na) {
     const int64_t n = l.size(0);
     if (gi) check_routes(*gi, at::kInt, n, k, dev);
     if (gw) check_routes(*gw, at::kFloat, n, k, dev);
-    at::Tensor idx = gi ? *gi : matrix(n, k, at::kInt, gpu(dev)), w = gw ? *gw : matrix(n, k, at::kFloat, gpu(dev));
+    const moe_stream_t st = stream_of(a[5], dev);
+    at::Tensor idx = gi ? *gi : matrix(n, k, at::kInt, dev, st), w = gw ? *gw : matrix(n, k, at::kFloat, dev, st);
     if (n > INT32_MAX) raise(PyExc_ValueError, "too many rows");
     const void* lp = l.data_ptr();
     const float* bp = bias ? data<const float>(*bias) : nullptr;
     int32_t* ip = data<int32_t>(idx);
     float* wp = data<float>(w);
     const int64_t stride = n > 1 ? l.stride(0) : E;
-    const moe_stream_t st = stream_of(a[5], dev);
     moe_status_t s;
     Py_BEGIN_ALLOW_THREADS;
     s = g_topk(&c, lp, stride, bp, (int32_t)n, ip, wp, st);
@@ -162,6 +171,7 @@ PyObject* matvec(PyObject* const* a, Py_ssize_t na) {
     if (wdev != dev) raise(PyExc_ValueError, "the weights are not on the current device");
     const int64_t n = x.size(0);
     if (n > INT32_MAX) raise(PyExc_ValueError, "too many rows");
+    const moe_stream_t st = stream_of(a[6], dev);
     int64_t ostride = O;
     at::Tensor out;
     if (given) {
@@ -174,12 +184,11 @@ PyObject* matvec(PyObject* const* a, Py_ssize_t na) {
     } else {
         if (c.accumulate) raise(PyExc_ValueError, "accumulate needs out");
         const at::ScalarType type = c.out_type == MOE_F32 ? at::kFloat : c.out_type == MOE_BF16 ? at::kBFloat16 : at::kHalf;
-        out = matrix(n, O, type, gpu(dev));
+        out = matrix(n, O, type, dev, st);
     }
     const void* xp = x.data_ptr();
     void* op = out.data_ptr();
     const int64_t stride = n > 1 ? x.stride(0) : K;
-    const moe_stream_t st = stream_of(a[6], dev);
     moe_status_t s;
     Py_BEGIN_ALLOW_THREADS;
     s = g_matvec(&c, q, bias, xp, stride, (int32_t)n, op, ostride, st);
@@ -237,10 +246,10 @@ PyObject* experts(PyObject* const* a, Py_ssize_t na) {
     void* ws = workspace(a[2], ws_bytes, dev);
     const int32_t* ip = layer_routes<int32_t>(a[5], at::kInt, n, c->top_k, dev);
     const float* wp = layer_routes<float>(a[6], at::kFloat, n, c->top_k, dev);
-    at::Tensor out = matrix(n, c->hidden, at::kBFloat16, gpu(dev));
+    const moe_stream_t st = stream_of(a[7], dev);
+    at::Tensor out = matrix(n, c->hidden, at::kBFloat16, dev, st);
     const void* xp = x.data_ptr();
     void* op = out.data_ptr();
-    const moe_stream_t st = stream_of(a[7], dev);
     moe_status_t s;
     Py_BEGIN_ALLOW_THREADS;
     s = g_experts(c, wts, xp, (int32_t)n, ip, wp, op, ws, ws_bytes, st);
@@ -263,6 +272,7 @@ PyObject* forward(PyObject* const* a, Py_ssize_t na) {
     const int64_t n = layer_rows(*c, x);
     const int dev = current_gpu(x);
     void* ws = workspace(a[2], ws_bytes, dev);
+    const moe_stream_t st = stream_of(a[9], dev);
     // What is not given is made here, and returned; what is given is returned as it is.
     at::Tensor out, idx, w;
     void* op;
@@ -271,11 +281,10 @@ PyObject* forward(PyObject* const* a, Py_ssize_t na) {
     if (a[5] != Py_None) op = layer_out(*c, a[5], n);
     if (a[6] != Py_None) ip = layer_routes<int32_t>(a[6], at::kInt, n, c->top_k, dev);
     if (a[7] != Py_None) wp = layer_routes<float>(a[7], at::kFloat, n, c->top_k, dev);
-    if (a[5] == Py_None) op = (out = matrix(n, c->hidden, at::kBFloat16, gpu(dev))).data_ptr();
-    if (a[6] == Py_None && routing) ip = data<int32_t>(idx = matrix(n, c->top_k, at::kInt, gpu(dev)));
-    if (a[7] == Py_None && routing) wp = data<float>(w = matrix(n, c->top_k, at::kFloat, gpu(dev)));
+    if (a[5] == Py_None) op = (out = matrix(n, c->hidden, at::kBFloat16, dev, st)).data_ptr();
+    if (a[6] == Py_None && routing) ip = data<int32_t>(idx = matrix(n, c->top_k, at::kInt, dev, st));
+    if (a[7] == Py_None && routing) wp = data<float>(w = matrix(n, c->top_k, at::kFloat, dev, st));
     const void* xp = x.data_ptr();
-    const moe_stream_t st = stream_of(a[9], dev);
     moe_status_t s;
     Py_BEGIN_ALLOW_THREADS;
     s = g_forward(c, wts, xp, (int32_t)n, op, ip, wp, ws, ws_bytes, st);

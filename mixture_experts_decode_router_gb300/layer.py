@@ -85,6 +85,17 @@ def make_weights(lw: LayerWeights) -> B.moe_weights_t:
     return w
 
 
+def _made(stream, *shape, **kw) -> torch.Tensor:
+    """An output of a call on `stream`: that stream's memory, in use on the current one."""
+    current = None if stream is None or kw["device"].type != "cuda" else torch.cuda.current_stream(kw["device"])
+    if current is None or B._stream(stream) == current.cuda_stream:
+        return torch.empty(*shape, **kw)
+    with torch.cuda.stream(torch.cuda.ExternalStream(B._stream(stream), kw["device"])):
+        t = torch.empty(*shape, **kw)
+    t.record_stream(current)
+    return t
+
+
 class MoeLayer:
     """One MoE layer on the current CUDA device.
 
@@ -129,9 +140,9 @@ class MoeLayer:
 
     def route(self, x: torch.Tensor, logits: bool = True, stream=None):
         n, k, E = x.shape[0], self.cfg.top_k, self.cfg.num_experts
-        idx = torch.empty(n, k, dtype=torch.int32, device=x.device)
-        w = torch.empty(n, k, dtype=torch.float32, device=x.device)
-        lg = torch.empty(n, E, dtype=torch.float32, device=x.device) if logits else None
+        idx = _made(stream, n, k, dtype=torch.int32, device=x.device)
+        w = _made(stream, n, k, dtype=torch.float32, device=x.device)
+        lg = _made(stream, n, E, dtype=torch.float32, device=x.device) if logits else None
         B.check(B.moe_route(self.c_cfg, self.c_w, x, n, idx, w, lg, self.ws, self.ws_bytes, stream))
         return idx, w, lg
 

@@ -215,3 +215,54 @@ def test_a_bias_assigned_later_is_checked():
         op.bias = bad
         with pytest.raises(ValueError, match="bias is contiguous"):
             op.forward(torch.zeros(3, 8))      # (before what says that the logits are on no GPU)
+
+
+# ---------------------------------------------------------------- a stream given by argument
+
+def calls_on_a_stream():
+    """name -> (call of a stream or None, its first output's shape and type)."""
+    cfg = cfg_of(hidden=1024, n_tokens=64)
+    layer = MoeLayer(synth.make_weights(cfg, "cuda"), 64)
+    x = synth.make_input(cfg, 64, "cuda")
+    _, idx, w = layer.forward(x)
+    q, s, _ = synth.quant_int4(torch.randn(1024, 1024, device="cuda"), 32)
+    lg = torch.randn(64, 8, device="cuda")
+    mv, tk = MoeMatvec(synth.QMatT("int4_g32", q, s)), MoeTopk(8, 2)
+    out, pair = ((64, 1024), torch.bfloat16), ((64, 2), torch.int32)
+    return {"forward": (lambda st: layer.forward(x, stream=st), out), "experts": (lambda st: (layer.experts(x, idx, w, stream=st),), out),
+            "route": (lambda st: layer.route(x, stream=st), pair), "topk": (lambda st: tk.forward(lg, stream=st), pair),
+            "matvec": (lambda st: (mv.forward(x, stream=st),), out)}
+
+
+CALLS = ["forward", "experts", "route", "topk", "matvec"]
+
+
+@gpu
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_of_another_stream(lib, name, raw):
+    """Outputs of a call on another stream are that stream's memory: dropped while it runs, they are not handed out on
+    the current stream; dropped while the current stream reads them, not on the other."""
+    call, (shape, dtype) = calls_on_a_stream()[name]
+    want = call(None)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    given = st.cuda_stream if raw else st
+    got = call(given)
+    torch.cuda.current_stream().wait_stream(st)
+    assert all(torch.equal(g, r) for g, r in zip(got, want))
+    at = {t.data_ptr() for t in call(given)}                # dropped at once
+    assert not at & {torch.empty(shape, dtype=dtype, device="cuda").data_ptr() for _ in range(3)}
+    torch.cuda.synchronize()
+    got = call(given)
+    torch.cuda.current_stream().wait_stream(st)
+    torch.cuda._sleep(40_000_000)                           # 20 ms
+    kept = got[0].clone()
+    at = got[0].data_ptr()
+    del got
+    with torch.cuda.stream(st):
+        assert torch.empty(shape, dtype=dtype, device="cuda").data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(kept, want[0])
+    # The current stream, given by name, is no other stream.
+    assert all(torch.equal(g, r) for g, r in zip(call(torch.cuda.current_stream()), want))
