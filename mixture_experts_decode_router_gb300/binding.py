@@ -270,9 +270,9 @@ def tensor_calls():
         import importlib.util
 
         import torch  # noqa: F401  (the extension links to its libraries)
-        lib = load()
+        lib, path = load(), _build.build_ext()
         spec = importlib.util.spec_from_file_location(
-            "_moe_torch", _build.EXT, loader=importlib.machinery.ExtensionFileLoader("_moe_torch", _build.EXT))
+            "_moe_torch", path, loader=importlib.machinery.ExtensionFileLoader("_moe_torch", path))
         ext = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ext)
         addr = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in ("moe_topk", "moe_matvec", "moe_experts", "moe_forward")]
