@@ -11,7 +11,7 @@ from typing import Optional
 import torch
 
 from . import binding as B
-from .synth import (FMT_BF16, FMT_FP8_B128, FMT_INT4_G128, FMT_INT4_G32, FMT_INT4_G64, FMT_NVFP4,
+from .synth import (FMT_BF16, FMT_FP8_B128, FMT_INT4_G128, FMT_INT4_G32, FMT_INT4_G64, FMT_NVFP4, INT4_GROUP,
                     ROUTE_SIGMOID, ROUTE_SIGMOID_BIAS, ROUTE_SOFTMAX, ROUTE_SOFTMAX_BIAS, LayerConfig,
                     LayerWeights, QMatT)
 
@@ -57,6 +57,31 @@ def make_config(cfg: LayerConfig, path: str = "auto", experts=None,
     c.accumulate = 1 if accumulate else 0
     c.router_fmt = _FMT[cfg.router_fmt]
     return c
+
+
+_BYTES = {torch.uint8, torch.int8}
+_E4M3 = _BYTES | {torch.float8_e4m3fn}
+_E2M1 = _BYTES | {t for t in (getattr(torch, "float4_e2m1fn_x2", None),) if t is not None}
+
+
+def _check_4bit(q: QMatT, n: int, out: int, inp: int) -> None:
+    """The arrays of n 4-bit matrices [out, inp] are those of their format: the kernels see only
+    addresses, and read them by these sizes and types."""
+    def is_a(t, cols, types):
+        return (t is not None and t.dtype in types and t.dim() > 0 and t.shape[-1] == cols
+                and t.numel() == n * out * cols and t.is_contiguous())
+    if q.fmt == FMT_NVFP4:
+        if not (is_a(q.w, inp // 2, _E2M1) and is_a(q.scale, inp // 16, _E4M3)):
+            raise ValueError("NVFP4 is E2M1 pairs [out, in/2] and E4M3 scales [out, in/16], in bytes")
+        if q.zero is not None or q.scale2 is None or q.scale2.dtype != torch.float32 or q.scale2.numel() != n \
+                or not q.scale2.is_contiguous():
+            raise ValueError("NVFP4 has one float32 scale2 a matrix and no zero points")
+    else:
+        G = INT4_GROUP[q.fmt]
+        if inp % G or not (is_a(q.w, inp // 2, _BYTES) and is_a(q.scale, inp // G, {torch.bfloat16})):
+            raise ValueError(f"{q.fmt} is pairs of codes [out, in/2], in bytes, and bfloat16 scales [out, in/{G}]")
+        if q.scale2 is not None or not (q.zero is None or is_a(q.zero, inp // G, _BYTES)):
+            raise ValueError(f"{q.fmt} has zero points [out, in/{G}], in bytes, or none, and no scale2")
 
 
 def _qmat(q: Optional[QMatT]) -> B.moe_qmat_t:
@@ -197,6 +222,8 @@ class MoeMatvec:
         if q.w.numel() != out_f * in_f // 2 or not all(
                 t is None or t.is_contiguous() for t in (q.w, q.scale, q.scale2, q.zero, bias)):
             raise ValueError("one contiguous matrix [out, in/2] and its scales")
+        if q.fmt == FMT_NVFP4 or q.fmt in INT4_GROUP:
+            _check_4bit(q, 1, out_f, in_f)
         if bias is not None and (bias.dtype != torch.float32 or bias.shape != (out_f,)):
             raise ValueError("bias is float32 [out]")
         c = B.moe_matvec_config_t()

@@ -1,6 +1,7 @@
 """The Python holders' calls: what they take, what they refuse, the memory and the streams they use."""
 
-import numpy as np
+import dataclasses
+
 import pytest
 import torch
 
@@ -266,3 +267,35 @@ def test_outputs_of_another_stream(lib, name, raw):
     assert torch.equal(kept, want[0])
     # The current stream, given by name, is no other stream.
     assert all(torch.equal(g, r) for g, r in zip(call(torch.cuda.current_stream()), want))
+
+
+# ---------------------------------------------------------------- weights
+
+def bad_int4(q):
+    """Arrays that the int4_g32 kernels would read past, or as something else."""
+    s, z = q.scale, torch.zeros(q.scale.shape, dtype=torch.uint8)
+    return [dict(scale=s[..., :1].contiguous()), dict(scale=s.half()), dict(scale=s.float()), dict(scale=None),
+            dict(scale=s[..., :1, :].contiguous()), dict(scale=s.transpose(-1, -2).contiguous().transpose(-1, -2)),
+            dict(zero=z[..., :1].contiguous()), dict(zero=z.to(torch.int32)), dict(zero=z.to(torch.bfloat16)),
+            dict(scale2=torch.ones(1)), dict(w=q.w.view(torch.int32)), dict(w=q.w.to(torch.int16)), dict(fmt="int4_g64"),
+            dict(fmt="int4_g128")]
+
+
+def test_a_matrix_of_other_arrays():
+    w, s, z = synth.quant_int4(torch.randn(16, 128), 32, True)
+    good = synth.QMatT("int4_g32", w, s, zero=z)
+    for q in (good, dataclasses.replace(good, zero=None), dataclasses.replace(good, w=w.view(torch.int8), zero=z.view(torch.int8)),
+              synth.QMatT("int4_g32", w[None], s[None], zero=z[None])):
+        MoeMatvec(q)
+    for bad in bad_int4(good):
+        with pytest.raises(ValueError):
+            MoeMatvec(dataclasses.replace(good, **bad))
+    b, f = torch.zeros(16, 64, dtype=torch.uint8), torch.zeros(16, 8, dtype=torch.uint8)
+    nv = synth.QMatT("nvfp4", b, f, torch.ones(1))
+    for q in (nv, dataclasses.replace(nv, scale=f.view(torch.float8_e4m3fn)), dataclasses.replace(nv, scale2=torch.tensor(1.0))):
+        MoeMatvec(q)
+    for bad in (dict(scale=f[:, :4].contiguous()), dict(scale=f.to(torch.bfloat16)), dict(scale2=None), dict(scale2=torch.ones(16)),
+                dict(scale2=torch.ones(1, dtype=torch.float64)), dict(zero=f), dict(scale=None), dict(w=b.to(torch.int32)),
+                dict(scale=torch.zeros(16, 8, dtype=torch.float8_e5m2))):
+        with pytest.raises(ValueError):
+            MoeMatvec(dataclasses.replace(nv, **bad))
