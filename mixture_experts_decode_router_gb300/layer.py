@@ -143,12 +143,31 @@ class MoeLayer:
         self.ws_bytes = B.moe_workspace_bytes(self.c_cfg, max_tokens)
         if self.ws_bytes == 0:
             raise B.MoeError("invalid layer configuration")
+        if self.cfg.expert_fmt in INT4_GROUP:
+            self._check_int4()
         dev = weights.router_w.device
         # The control block (first 256 bytes) must start at zero; calls keep it zero.
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
         self.max_tokens = max_tokens
         calls = B.tensor_calls()
         self._experts, self._forward = calls.experts, calls.forward
+
+    def _check_int4(self) -> None:
+        """The arrays of the matrices that this layer's calls read."""
+        c, lw = self.c_cfg, self.weights
+        held = c.num_experts if c.expert_begin == c.expert_end == 0 else c.expert_end - c.expert_begin
+        stacks = [("gate", held, c.inter, c.hidden), ("up", held, c.inter, c.hidden), ("down", held, c.hidden, c.inter)]
+        shared = 0 if c.exclude_shared else c.shared_inter
+        stacks += [("sh_gate", 1, shared, c.hidden), ("sh_up", 1, shared, c.hidden), ("sh_down", 1, c.hidden, shared)]
+        for name, n, out, inp in stacks:
+            q = getattr(lw, name)
+            if n * out * inp == 0:
+                continue
+            if q is None or q.fmt != self.cfg.expert_fmt:
+                raise ValueError(f"{name} is an {self.cfg.expert_fmt} matrix")
+            _check_4bit(q, n, out, inp)
+            if any(t is not None and t.device != lw.router_w.device for t in (q.w, q.scale, q.zero)):
+                raise ValueError("weights on one device")
 
     def forward(self, x: torch.Tensor, out=None, idx=None, w=None, stream=None,
                 routing: bool = True):

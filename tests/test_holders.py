@@ -299,3 +299,35 @@ def test_a_matrix_of_other_arrays():
                 dict(scale=torch.zeros(16, 8, dtype=torch.float8_e5m2))):
         with pytest.raises(ValueError):
             MoeMatvec(dataclasses.replace(nv, **bad))
+
+
+@pytest.mark.parametrize("name", ["gate", "down", "sh_up", "sh_down"])
+def test_a_layer_of_other_arrays(name):
+    """INT4 stacks whose arrays are not those of the layer's sizes, experts and format."""
+    lw = synth.make_weights(cfg_of(zero_points=True), "cpu")
+    good = getattr(lw, name)
+    MoeLayer(lw, 3)
+    fewer = [] if name.startswith("sh_") else [dict(w=good.w[:7], scale=good.scale[:7], zero=good.zero[:7])]
+    for bad in bad_int4(good) + fewer:
+        setattr(lw, name, dataclasses.replace(good, **bad))
+        with pytest.raises(ValueError):
+            MoeLayer(lw, 3)
+    setattr(lw, name, None)
+    with pytest.raises(ValueError):
+        MoeLayer(lw, 3)
+
+
+def test_a_layer_without_some_of_its_arrays():
+    """What a call does not read is not asked for: no shared expert, none of the experts, one rank's slice."""
+    lw = synth.make_weights(cfg_of(zero_points=True), "cpu")
+    for held in ((0, 8), (2, 5), (8, 8)):
+        MoeLayer(synth.expert_slice(lw, *held), 3, experts=held)
+    with pytest.raises(ValueError):
+        MoeLayer(synth.expert_slice(lw, 2, 5), 3, experts=(2, 6))
+    none = synth.expert_slice(lw, 8, 8)
+    none.gate = none.up = none.down = None
+    MoeLayer(none, 3, experts=(8, 8))
+    lw.sh_gate = lw.sh_up = lw.sh_down = None
+    MoeLayer(lw, 3, exclude_shared=True)
+    with pytest.raises(ValueError):
+        MoeLayer(lw, 3)
