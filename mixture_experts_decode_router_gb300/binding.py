@@ -73,6 +73,11 @@ class moe_qmat_t(ctypes.Structure):
     _anonymous_ = ("_second",)
     _fields_ = [("w", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("_second", _moe_qmat_second)]
 
+    def __init__(self, w=None, scale=None, scale2=None, **kw):
+        if scale2 is not None:
+            kw["scale2"] = scale2
+        super().__init__(w, scale, **kw)
+
 
 class moe_weights_t(ctypes.Structure):
     _fields_ = [("router_w", ctypes.c_void_p), ("correction_bias", ctypes.c_void_p),

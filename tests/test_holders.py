@@ -331,3 +331,16 @@ def test_a_layer_without_some_of_its_arrays():
     MoeLayer(lw, 3, exclude_shared=True)
     with pytest.raises(ValueError):
         MoeLayer(lw, 3)
+
+
+def test_a_matrix_struct_by_position():
+    """moe_qmat_t takes its addresses in order, as the C struct does, and by name."""
+    q = B.moe_qmat_t(1 << 40, 2, 3)
+    assert (q.w, q.scale, q.scale2, q.zero) == (1 << 40, 2, 3, 3)
+    q = B.moe_qmat_t(w=1, zero=4)
+    assert (q.w, q.scale, q.scale2, q.zero) == (1, None, 4, 4)
+    q = B.moe_qmat_t()
+    assert (q.w, q.scale, q.scale2, q.zero) == (None,) * 4
+    w = B.moe_weights_t()
+    w.gate = B.moe_qmat_t(5, 6, 7)
+    assert (w.gate.w, w.gate.scale, w.gate.scale2) == (5, 6, 7)
