@@ -210,14 +210,24 @@ typedef struct {
     int32_t router_fmt;             /* MOE_W_BF16 (router_w) or MOE_W_NVFP4 (router_q) */
 } moe_config_t;
 
+/* (An unnamed union is C11; GNU compilers take it in any mode.) */
+#ifdef __GNUC__
+#define MOE_EXTENSION __extension__
+#else
+#define MOE_EXTENSION
+#endif
 /* One stacked expert matrix (device pointers; see the layouts above). */
 typedef struct {
     const void*  w;
     const void*  scale;    /* FP8: fp32 block scales; NVFP4: E4M3 bytes; INT4: BF16; BF16: NULL */
-    union {
+#if defined(__cplusplus) || defined(__GNUC__) || (defined(__STDC_VERSION__) && __STDC_VERSION__ >= 201112L)
+    MOE_EXTENSION union {
         const float*   scale2;   /* NVFP4: fp32 [E]; BF16, FP8: NULL */
         const uint8_t* zero;     /* INT4: zero points [E, out, in/G], or NULL (8) */
     };
+#else   /* C without unnamed unions: INT4 zero points are cast into scale2 */
+    const float* scale2;
+#endif
 } moe_qmat_t;
 
 /* All weights of one layer (device pointers).  The shared-expert matrices are

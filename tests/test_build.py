@@ -55,3 +55,21 @@ def test_the_library_loads_without_torch(tmp_path):
             "assert B.moe_abi_version() == 2 and 'success' in B.moe_status_string(0)\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("lang,std", [("c", "c99"), ("c", "c11"), ("c", "gnu99"), ("c++", "c++11"), ("c++", "c++17")])
+def test_the_header_in_strict_compilers(lang, std, tmp_path):
+    """Strict C99 and C++ take the header, with its matrices' second array under both names."""
+    src = tmp_path / "use.c"
+    src.write_text('#include "moe.h"\n'
+                   "int main(void) {\n"
+                   "    moe_qmat_t q = {0};\n"
+                   "    const uint8_t z = 0;\n"
+                   "    q.zero = &z;\n"
+                   "    return (const void*)q.scale2 != (const void*)q.zero || sizeof(q) != 3 * sizeof(void*);\n"
+                   "}\n")
+    exe = tmp_path / "use"
+    flags = ["-Wall", "-Wextra", "-Werror", "-pedantic-errors"] + (["-Wno-missing-field-initializers"] if lang == "c++" else [])
+    subprocess.run(["gcc", "-x", lang, f"-std={std}", *flags, "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)],
+                   check=True, capture_output=True)
+    assert subprocess.run([str(exe)]).returncode == 0
