@@ -54,7 +54,6 @@ constexpr int kMaxSmem = 227 * 1024;
 template <int kN>
 __device__ __forceinline__ float stage_act(const float* src, int left, uint8_t* dst, int lane) {
     float v[kN][8];   // chunks of 8
-    float am = 0.f;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
         const int c = lane + 32 * i;
@@ -65,11 +64,22 @@ __device__ __forceinline__ float stage_act(const float* src, int left, uint8_t* 
         }
         v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
         v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(v[i][e]));
     }
+    auto largest = [&](bool finite) {
+        float am = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        for (int i = 0; i < kN; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float a = fabsf(v[i][e]);
+                am = fmaxf(am, finite && a == INFINITY ? 0.f : a);
+            }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        return am;
+    };
+    float am = largest(false);
+    if (am == INFINITY) am = largest(true);   // an infinity stays one at any scale; the rest has to stay finite
     const int sh = q4::f16_shift(am);
     const float f = q4::exp2i(sh);
 #pragma unroll

@@ -345,10 +345,10 @@ __host__ __device__ inline int x_row_bytes(int K) { return (K + kStageK - 1) / k
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // The exponent of the power of two that takes values of magnitude at most amax
-// below 2^15 (0 for zero, infinite or NaN amax).
+// below 2^15 (0 for zero).
 __device__ __forceinline__ int f16_shift(float amax) {
     const int e = (int)(__float_as_uint(amax) >> 23) & 0xff;
-    if (amax == 0.f || e == 255) return 0;
+    if (amax == 0.f) return 0;
     return min(126, 14 - (e - 127));
 }
 
@@ -373,19 +373,27 @@ __device__ __forceinline__ float scaled_row(const uint4* src, int K8, int chunks
             u[i] = c < K8 ? src[c] : make_uint4(0u, 0u, 0u, 0u);
         }
     };
-    float am = 0.f;
-    for (int c0 = 0; c0 < K8; c0 += 32 * kU) {
-        load(c0);
+    auto largest = [&](bool finite) {
+        float am = 0.f;
+        for (int c0 = 0; c0 < K8; c0 += 32 * kU) {
+            load(c0);
 #pragma unroll
-        for (int i = 0; i < kU; ++i) {
-            float v[8];
-            bf16x8_to_float(u[i], v);
+            for (int i = 0; i < kU; ++i) {
+                float v[8];
+                bf16x8_to_float(u[i], v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(v[e]));   // (NaN keeps its column NaN by itself)
+                for (int e = 0; e < 8; ++e) {   // (NaN keeps its column NaN by itself)
+                    const float a = fabsf(v[e]);
+                    am = fmaxf(am, finite && a == INFINITY ? 0.f : a);
+                }
+            }
         }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        return am;
+    };
+    float am = largest(false);
+    if (am == INFINITY) am = largest(true);   // an infinity stays one at any scale; the rest has to stay finite
     const int sh = f16_shift(am);
     const float f = exp2i(sh);
     for (int c0 = 0; c0 < chunks; c0 += 32 * kU) {

@@ -495,3 +495,34 @@ def test_workload_sizes(lib, name, fmt, n):
     assert np.array_equal(idx.cpu().numpy()[rows], ridx)
     close(out.float().cpu().numpy()[rows], ref)
     assert layer.device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 9])
+def test_infinite_act_beside_large_ones(lib, n):
+    """SiLU(g) u past fp32's range, of finite g and u, beside values past fp16's: an output is an infinity of its
+    weight's sign and the product's, or NaN where the weight is 0."""
+    cfg = cfg_of("int4_g32", shared_inter=0, top_k=1)
+    lw = synth.make_weights(cfg, "cuda")
+    x = synth.make_input(cfg, n, "cuda") * 2.0 ** 13
+    xe = O.bf16_decode(bf16_bits(x))
+    L = int4_oracle_layer(lw)
+    gs, us = lw.gate.scale.float(), lw.up.scale.float()
+    for t in range(n):                                    # row 5 of the token's expert: g about 1e29 and positive
+        gs[t, 5] *= 2.0 ** 85 * float(np.sign(L.gate.expert(t)[5] @ xe[t]))
+        us[t, 5] *= 2.0 ** 85
+    lw.gate = dataclasses.replace(lw.gate, scale=gs.to(torch.bfloat16))
+    lw.up = dataclasses.replace(lw.up, scale=us.to(torch.bfloat16))
+    L = int4_oracle_layer(lw)
+    idx, w = torch.arange(n, dtype=torch.int32, device="cuda")[:, None], torch.ones(n, 1, device="cuda")
+    got = MoeLayer(lw, n).experts(x, idx, w).float().cpu().numpy()
+    for t in range(n):
+        g, u = L.gate.expert(t) @ xe[t], L.up.expert(t) @ xe[t]
+        # No fp32 sum of g or u overflows, and only act 5 does.
+        assert max(np.abs(L.gate.expert(t)[5]) @ np.abs(xe[t]), np.abs(L.up.expert(t)[5]) @ np.abs(xe[t])) < 1e37
+        rest = np.delete(g * u, 5)
+        assert g[5] > 0 and abs(g[5] * u[5]) > 1e40 and 1e5 < np.max(np.abs(rest)) < 1e30
+        d = L.down.expert(t)[:, 5]
+        want = np.full(len(d), np.nan, np.float32)
+        want[d != 0] = np.inf * np.sign(d[d != 0]) * np.sign(u[5])
+        assert np.array_equal(got[t], want, equal_nan=True)

@@ -338,3 +338,19 @@ def test_projection_before_the_layer(lib):
     ref, ridx, _, _ = O.moe_forward(L, bf16_bits(h))
     assert np.array_equal(idx.cpu().numpy(), ridx)
     close_layer(out.float().cpu().numpy(), ref)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n", [1, 5])
+def test_infinity_beside_large_values(lib, fmt, n):
+    """A row with an infinity and values past fp16's range: the infinity's sign, or NaN where its weight is 0."""
+    q, w = matrix(70, 4096, fmt, seed=3)
+    x = rows(n, 4096, spread=1e6)
+    x[n - 1, 300] = float("inf")
+    y = MoeMatvec(q, out_dtype=torch.float32).forward(x)
+    at = w[:, 300]
+    want = torch.tensor(np.where(at == 0, np.nan, np.sign(at) * np.inf), dtype=torch.float32, device="cuda")
+    assert torch.equal(torch.isnan(y[n - 1]), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(y[n - 1]), torch.nan_to_num(want))
+    close(y[:n - 1], x[:n - 1], w)
