@@ -214,18 +214,11 @@ constexpr int kTokenMajorMaxN = 3;
 // and a router CTA still on an SM leaves room for one.
 static bool early_dependents(int32_t n, int sms) { return n <= sms; }
 
-// INT4 under AUTO: the streaming kernels while the experts have at most
-// kStreamMaxAvg tokens on average, the grouped tensor-core path above.  Measured on
-// GB300, the experts in groups of 128, streaming against grouped: hidden 2048, 256
-// experts, top-8, 512 tokens (16 on average) 267 against 327 us, 768 tokens 363
-// against 343; hidden 7168, 64 experts, 128 tokens (16) 762 against 984 us, 192
-// tokens (24) 1067 against 1014.
-constexpr int kStreamMaxAvg = 20;
-constexpr int kPathStream = 3;
+constexpr int kPathStream = 3;   // INT4, below kStreamMaxAvg tokens an expert
 
 // The multi-kernel path a call of n tokens takes.
 static int effective_path(const moe_config_t* c, int32_t n) {
-    if (c->path == MOE_PATH_AUTO && is_int4(c->expert_fmt) && (int64_t)n * c->top_k <= (int64_t)kStreamMaxAvg * c->num_experts &&
+    if (c->path == MOE_PATH_AUTO && is_int4(c->expert_fmt) && !int4_grouped(*c, n) &&
         (n > 1 || q4_n1_fits(c->hidden, c->top_k, c->inter, c->shared_inter)))
         return kPathStream;
     return c->path == MOE_PATH_AUTO ? (n <= kTokenMajorMaxN ? MOE_PATH_TOKEN_MAJOR : MOE_PATH_GROUPED) : c->path;
@@ -387,8 +380,9 @@ static moe_status_t enqueue_grouped(const moe_config_t* c, const moe_weights_t* 
     p.perm = at<int32_t>(ws, L.perm);
     p.route_w = wt;
     p.sg_logit = w->shared_gate_w ? sg_logit : nullptr;
-    p.act_out = at<uint16_t>(ws, L.as);
-    p.act_sh_out = at<uint16_t>(ws, L.ash);
+    uint16_t *as = at<uint16_t>(ws, L.as), *ash = at<uint16_t>(ws, L.ash);
+    p.act_out = is_int4(fmt) ? static_cast<void*>(at<float>(ws, L.act)) : as;
+    p.act_sh_out = is_int4(fmt) ? static_cast<void*>(at<float>(ws, L.act_sh)) : ash;
     p.y = at<float>(ws, L.y);
     p.y_sh = at<float>(ws, L.ysh);
 
@@ -403,10 +397,18 @@ static moe_status_t enqueue_grouped(const moe_config_t* c, const moe_weights_t* 
     set_second(fmt, p, 0, w->gate, w->sh_gate);
     set_second(fmt, p, 1, w->up, w->sh_up);
     if (tiles && (e = launch_grouped_tc(fmt, true, maps, p, sms, st)) != cudaSuccess) return MOE_ERR_CUDA;
+    if (tiles && is_int4(fmt)) {
+        p.row_exp = at<int32_t>(ws, L.aexp);
+        p.row_exp_sh = p.row_exp + (size_t)n * k;
+        e = launch_act_rows(static_cast<const float*>(p.act_out), static_cast<const float*>(p.act_sh_out), n, I, S,
+                            at<int32_t>(ws, L.offsets), E, as, ash, at<int32_t>(ws, L.aexp), n * k,
+                            early_dependents(n, sms), sms, st);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
+    }
     mk.mark(st);
 
     // down (+ routing weight / shared gate)
-    if (tiles && !build_tc_maps(fmt, false, w, E_loc, H, I, S, n, n * k, p.act_out, p.act_sh_out, &maps))
+    if (tiles && !build_tc_maps(fmt, false, w, E_loc, H, I, S, n, n * k, as, ash, &maps))
         return MOE_ERR_CUDA;
     p.out_dim = H; p.in_dim = I; p.sh_out = S > 0 ? H : 0; p.sh_in = S;
     p.scale[0] = p.scale[1] = w->down.scale;

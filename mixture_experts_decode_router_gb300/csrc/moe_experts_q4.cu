@@ -80,8 +80,8 @@ __device__ __forceinline__ float stage_act(const float* src, int left, uint8_t* 
     };
     float am = largest(false);
     if (am == INFINITY) am = largest(true);   // an infinity stays one at any scale; the rest has to stay finite
-    const int sh = q4::f16_shift(am);
-    const float f = q4::exp2i(sh);
+    const int sh = f16_shift(am);
+    const float f = exp2i(sh);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
         auto pair = [&](int x, int y) {
@@ -90,7 +90,7 @@ __device__ __forceinline__ float stage_act(const float* src, int left, uint8_t* 
         };
         reinterpret_cast<uint4*>(dst)[lane + 32 * i] = make_uint4(pair(0, 4), pair(1, 5), pair(2, 6), pair(3, 7));
     }
-    return q4::exp2i(-sh);
+    return exp2i(-sh);
 }
 
 __device__ __forceinline__ float shared_gate(const float* sg_logit, int t) {

@@ -143,6 +143,65 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
     pdl_trigger();
 }
 
+// SiLU(g) u of the INT4 experts as the f16 rows of the down product: each row times the power
+// of two that puts its largest finite value below 2^15, its exponent to exps.  One rounding to
+// 11 significand bits, down to 2^-29 of that value, at any magnitude; an infinity stays one.
+// One warp a row; a row of up to 32 kU chunks of 8 is read once.
+__global__ void __launch_bounds__(256) act_rows_kernel(const float* __restrict__ act, const float* __restrict__ act_sh,
+                                                       int n, int I, int S, const int32_t* __restrict__ offsets, int E,
+                                                       uint16_t* __restrict__ as, uint16_t* __restrict__ ash,
+                                                       int32_t* __restrict__ exps, int n_routes_max, int early) {
+    constexpr int kU = 4;
+    pdl_wait();
+    if (early) pdl_trigger();
+    const int n_routes = offsets[E], rows = n_routes + (S > 0 ? n : 0);
+    const int lane = threadIdx.x & 31, nwarps = gridDim.x * (blockDim.x >> 5);
+    for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += nwarps) {
+        const bool routed = r < n_routes;
+        const int rr = routed ? r : r - n_routes, width = routed ? I : S, C8 = width >> 3;
+        const float4* src = reinterpret_cast<const float4*>((routed ? act : act_sh) + (size_t)rr * width);
+        uint4* dst = reinterpret_cast<uint4*>((routed ? as : ash) + (size_t)rr * width);
+        float4 v[kU][2];
+        auto load = [&](int c0) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int c = c0 + 32 * u;
+                v[u][0] = c < C8 ? src[2 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[u][1] = c < C8 ? src[2 * c + 1] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        };
+        float am = 0.f;
+        for (int c0 = lane; c0 < C8 + lane; c0 += 32 * kU) {
+            load(c0);
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    am = fmaxf(am, fmaxf(fmaxf(finite_abs(v[u][h].x), finite_abs(v[u][h].y)),
+                                         fmaxf(finite_abs(v[u][h].z), finite_abs(v[u][h].w))));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        const int sh = f16_shift(am);
+        const float f = exp2i(sh);
+        for (int c0 = lane; c0 < C8; c0 += 32 * kU) {
+            if (C8 > 32 * kU) load(c0);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                auto pair = [&](float x, float y) {
+                    const __half2 h = __floats2half2_rn(x * f, y * f);
+                    return *reinterpret_cast<const uint32_t*>(&h);
+                };
+                if (c0 + 32 * u < C8)
+                    dst[c0 + 32 * u] = make_uint4(pair(v[u][0].x, v[u][0].y), pair(v[u][0].z, v[u][0].w),
+                                                  pair(v[u][1].x, v[u][1].y), pair(v[u][1].z, v[u][1].w));
+            }
+        }
+        if (lane == 0) exps[routed ? rr : n_routes_max + rr] = sh;
+    }
+    pdl_trigger();
+}
+
 // dst = src, n16 16-byte words (x staged from pinned host memory).
 __global__ void __launch_bounds__(256) copy16_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst,
                                                      size_t n16) {
@@ -169,6 +228,14 @@ cudaError_t launch_gather(int fmt, const uint16_t* x, int n, int H, int k, const
     auto kern = fmt != MOE_W_BF16 ? (norm_w ? gather_kernel<true, true> : gather_kernel<true, false>)
                                   : (norm_w ? gather_kernel<false, true> : gather_kernel<false, false>);
     launch_pdl(kern, grid, 256, 0, st, x, n, H, k, perm, offsets, E, xs, xh, norm_w, eps, early ? 1 : 0);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_act_rows(const float* act, const float* act_sh, int n, int I, int S, const int32_t* offsets, int E,
+                            uint16_t* as, uint16_t* ash, int32_t* exps, int n_routes_max, bool early, int num_sms,
+                            cudaStream_t st) {
+    launch_pdl(act_rows_kernel, 2 * num_sms, 256, 0, st, act, act_sh, n, I, S, offsets, E, as, ash, exps, n_routes_max,
+               early ? 1 : 0);
     return cudaGetLastError();
 }
 

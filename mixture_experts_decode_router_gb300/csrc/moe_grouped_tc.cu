@@ -584,6 +584,7 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                 if constexpr (GU) s2u = sh ? p.sh_scale2[1][0] : p.scale2[1][t.le];
             }
             float tw[2] = {0.f, 0.f};   // down: weight of token lane, lane + 32 (times scale2)
+            [[maybe_unused]] int te[2] = {0, 0};   // INT4 down: exponent of that token's row
             if constexpr (!GU) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -593,6 +594,7 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                         if (sh) wgt = p.sg_logit ? 1.0f / (1.0f + expf(-p.sg_logit[t.pos0 + j])) : 1.0f;
                         else wgt = p.route_w[p.perm[t.pos0 + j]];
                         tw[h] = wgt * s2g;
+                        if constexpr (FMT == kFmtInt4) te[h] = (sh ? p.row_exp_sh : p.row_exp)[t.pos0 + j];
                     }
                 }
             }
@@ -616,6 +618,10 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                             if (j < t.ntok) {
                                 const float gv = g[jj] * s2g, uv = u[jj] * s2u;
                                 const float a = gv / (1.0f + expf(-gv)) * uv;
+                                if constexpr (FMT == kFmtInt4) {   // fp32: act_rows_kernel makes it f16
+                                    reinterpret_cast<float*>(dst)[(size_t)(t.pos0 + j) * t.out + m] = a;
+                                    continue;
+                                }
                                 uint16_t bits;
                                 if constexpr (C::kF16) {
                                     bits = (uint16_t)pack_f16_sat(a, 0.f);
@@ -638,6 +644,8 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                     for (int jj = 0; jj < 16; ++jj) {
                         const int j = j0 + jj;
                         wj[jj] = __shfl_sync(0xffffffffu, j < 32 ? tw[0] : tw[1], j & 31);
+                        if constexpr (FMT == kFmtInt4)
+                            d[jj] = times_exp2(d[jj], -__shfl_sync(0xffffffffu, j < 32 ? te[0] : te[1], j & 31));
                     }
                     if (valid) {
 #pragma unroll

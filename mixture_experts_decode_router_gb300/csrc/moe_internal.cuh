@@ -88,9 +88,23 @@ inline bool router_tc_fits(int64_t n, int64_t E, int H) {
     return n >= 1 && E >= 1 && H % 8 == 0 && b <= kRouterTcMaxPartialBytes && router_tc_smem(H, n) <= 232448;
 }
 
+// INT4 under AUTO: the streaming kernels while the experts have at most
+// kStreamMaxAvg tokens on average, the grouped tensor-core path above.  Measured on
+// GB300, the experts in groups of 128, streaming against grouped: hidden 2048, 256
+// experts, top-8, 512 tokens (16 on average) 267 against 327 us, 768 tokens 363
+// against 343; hidden 7168, 64 experts, 128 tokens (16) 762 against 984 us, 192
+// tokens (24) 1067 against 1014.
+constexpr int kStreamMaxAvg = 20;
+
+// Whether a call of n tokens runs INT4 experts on the grouped path (monotone in n).
+inline bool int4_grouped(const moe_config_t& c, int64_t n) {
+    if (!is_int4(c.expert_fmt)) return false;
+    return c.path == MOE_PATH_GROUPED || (c.path == MOE_PATH_AUTO && n * c.top_k > (int64_t)kStreamMaxAvg * c.num_experts);
+}
+
 struct WsLayout {
     size_t ctrl, logits, sg_logit, idx, w, counts, offsets, perm, active, act, act_sh,
-        inv, segs, xs, xh, as, ash, y, ysh, xe, xd, lgp, rq, total;
+        inv, segs, xs, xh, as, ash, y, ysh, xe, xd, lgp, rq, aexp, total;
 };
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -139,6 +153,7 @@ inline WsLayout ws_layout(const moe_config_t& c, int64_t n) {
     L.xd = take(sizeof(uint16_t) * n * H);                       // x staged from pinned host memory
     L.lgp = take(router_tc_partials_bytes(n, E, (int)H));        // tensor-core router partials
     L.rq = take(c.router_fmt == MOE_W_NVFP4 ? sizeof(uint16_t) * E * H : 0);   // an NVFP4 router as BF16
+    L.aexp = take(int4_grouped(c, n) ? sizeof(int32_t) * (n * k + n) : 0);   // exponents of the rows of as, then of ash
     L.total = off;
     return L;
 }
@@ -272,6 +287,27 @@ __device__ __forceinline__ uint32_t pack_f16_sat(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// 2^e as a float, e in [-126, 127].
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// The exponent of the power of two that takes values of magnitude at most amax
+// below 2^15 (0 for zero).
+__device__ __forceinline__ int f16_shift(float amax) {
+    const int e = (int)(__float_as_uint(amax) >> 23) & 0xff;
+    if (amax == 0.f) return 0;
+    return min(126, 14 - (e - 127));
+}
+// v 2^e for e in [-252, 254], in two steps of one direction.
+__device__ __forceinline__ float times_exp2(float v, int e) {
+    const int h = e >> 1;
+    return v * exp2i(h) * exp2i(e - h);
+}
+// |v|, or 0 for an infinity or NaN.
+__device__ __forceinline__ float finite_abs(float v) {
+    const float a = fabsf(v);
+    return a < INFINITY ? a : 0.f;
 }
 
 // One E4M3 code -> float (exact).

@@ -80,7 +80,9 @@ struct TcParams {
     const uint8_t* zero[2];     // INT4 zero points, or NULL
     const uint8_t* sh_zero[2];
     int gshift;                 // INT4: log2 of the group size
-    void* act_out;           // gate_up: sorted SiLU(g)*u rows [n*k, I] (bf16 / f16)
+    const int32_t* row_exp;     // INT4 down: the power of two by which each row of act was multiplied
+    const int32_t* row_exp_sh;
+    void* act_out;           // gate_up: sorted SiLU(g)*u rows [n*k, I] (bf16 / f16; INT4: fp32)
     void* act_sh_out;        // gate_up: shared [n, S]
     float* y;                // down: weighted rows [n*k, H]
     float* y_sh;             // down: gated shared rows [n, H]
@@ -109,6 +111,11 @@ cudaError_t launch_copy16(const void* src, void* dst, size_t bytes, int num_sms,
 cudaError_t launch_gather(int fmt, const uint16_t* x, int n, int H, int k, const int32_t* perm,
                           const int32_t* offsets, int E, uint16_t* xs, uint16_t* xh, const uint16_t* norm_w,
                           float eps, bool early, int num_sms, cudaStream_t st);
+// INT4: the rows of SiLU(g) u (fp32) as f16 times a power of two each, whose exponents go to
+// exps (n_routes_max rows of as, then those of ash).
+cudaError_t launch_act_rows(const float* act, const float* act_sh, int n, int I, int S, const int32_t* offsets, int E,
+                            uint16_t* as, uint16_t* ash, int32_t* exps, int n_routes_max, bool early, int num_sms,
+                            cudaStream_t st);
 cudaError_t launch_combine(const float* y, const float* ysh, const int32_t* inv, int n, int H, int k,
                            int has_shared, int accumulate, uint16_t* out, bool early, int num_sms, cudaStream_t st);
 

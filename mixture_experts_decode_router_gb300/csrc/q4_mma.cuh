@@ -341,17 +341,6 @@ __device__ __forceinline__ void mma_stage(const uint8_t* sm, uint32_t st, const 
 // Bytes between token rows in shared memory: whole stages of 16-bit elements, and
 // 64 bytes so that neighbouring rows' chunks fall into different banks.
 __host__ __device__ inline int x_row_bytes(int K) { return (K + kStageK - 1) / kStageK * (2 * kStageK) + 64; }
-// 2^e as a float, e in [-126, 127].
-__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-// The exponent of the power of two that takes values of magnitude at most amax
-// below 2^15 (0 for zero).
-__device__ __forceinline__ int f16_shift(float amax) {
-    const int e = (int)(__float_as_uint(amax) >> 23) & 0xff;
-    if (amax == 0.f) return 0;
-    return min(126, 14 - (e - 127));
-}
-
 // The eight 16-bit elements of a chunk in the order the fragments take them.
 template <int GSH>
 __device__ __forceinline__ uint4 chunk_order(uint4 u) {

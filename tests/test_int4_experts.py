@@ -526,3 +526,61 @@ def test_infinite_act_beside_large_ones(lib, n):
         want = np.full(len(d), np.nan, np.float32)
         want[d != 0] = np.inf * np.sign(d[d != 0]) * np.sign(u[5])
         assert np.array_equal(got[t], want, equal_nan=True)
+
+
+def experts_ref(lw, x, idx, w):
+    """The routed experts' (and an ungated shared one's) output in 64 bits for given routes."""
+    L, xe = int4_oracle_layer(lw), O.bf16_decode(bf16_bits(x))
+    ref = np.zeros((len(xe), lw.cfg.hidden))
+    if lw.sh_gate is not None:
+        ref += O.swiglu_mlp(xe, L.sh_gate.expert(0), L.sh_up.expert(0), L.sh_down.expert(0))
+    for t in range(len(xe)):
+        for j in range(idx.shape[1]):
+            e = int(idx[t, j])
+            ref[t] += float(w[t, j]) * O.swiglu_mlp(xe[t], L.gate.expert(e), L.up.expert(e), L.down.expert(e))
+    return ref
+
+
+def routes(n, k=2, E=16):
+    g = torch.Generator().manual_seed(n)
+    return torch.randint(0, E, (n, k), generator=g).to(torch.int32).cuda(), torch.rand(n, k, generator=g).cuda()
+
+
+@gpu
+@pytest.mark.parametrize("path,n", [("grouped", 1), ("grouped", 9), ("auto", 170)])
+@pytest.mark.parametrize("shared", [0, 128])
+def test_act_past_f16_on_the_grouped_path(lib, path, n, shared):
+    """SiLU(g) u that f16 would hold as zero or infinity, with x and the scales inside its range."""
+    cfg = cfg_of("int4_g64", shared_inter=shared, zero_points=True)
+    lw = synth.make_weights(cfg, "cuda")
+    for scale in (2.0 ** -10, 2.0 ** 13):
+        x = synth.make_input(cfg, n, "cuda") * scale
+        idx, w = routes(n)
+        layer = MoeLayer(lw, n, path)
+        got, ref = layer.experts(x, idx, w).float().cpu().numpy(), experts_ref(lw, x, idx, w)
+        for t in range(n):
+            close(got[t], ref[t])
+        assert layer.device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("n,path", [(1, "grouped"), (2, "grouped"), (40, "grouped"), (170, "auto")])
+def test_a_workspace_of_the_grouped_path(lib, n, path):
+    """A workspace of exactly moe_workspace_bytes in front of a guard: nothing past its end is written; one made for
+    more tokens serves fewer, on whichever path they run."""
+    cfg = cfg_of("int4_g32", inter=160, shared_inter=96, zero_points=True)
+    lw, x, layer, out, idx, w = check(cfg, n, path)
+    size = B.moe_workspace_bytes(layer.c_cfg, n)
+    buf = torch.zeros(size + 4096, dtype=torch.uint8, device="cuda")
+    buf[size:] = 0xA5
+    got = torch.empty_like(out)
+    assert B.moe_forward(layer.c_cfg, layer.c_w, x, n, got, torch.empty_like(idx), torch.empty_like(w), buf, size) == B.MOE_OK
+    torch.cuda.synchronize()
+    assert torch.equal(got, out) and (buf[size:] == 0xA5).all()
+    for m in range(1, n, max(1, n // 7)):
+        assert B.moe_workspace_bytes(layer.c_cfg, m) <= size
+        assert B.moe_forward(layer.c_cfg, layer.c_w, x, m, got, None, None, buf, size) == B.MOE_OK
+        torch.cuda.synchronize()
+        if path == "grouped":
+            assert torch.equal(got[:m], out[:m])
+    assert (buf[size:] == 0xA5).all() and B.moe_workspace_check(buf, size) == (B.MOE_OK, 0)
