@@ -365,7 +365,7 @@ static moe_status_t enqueue_grouped(const moe_config_t* c, const moe_weights_t* 
     cudaError_t e = launch_gather(fmt, static_cast<const uint16_t*>(x), n, H, k, at<int32_t>(ws, L.perm),
                                   at<int32_t>(ws, L.offsets), E, xs, xh,
                                   static_cast<const uint16_t*>(w->pre_expert_norm_w), c->rms_norm_eps,
-                                  early_dependents(n, sms), sms, st);
+                                  is_int4(fmt) ? at<int32_t>(ws, L.xexp) : nullptr, early_dependents(n, sms), sms, st);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     mk.mark(st);
 
@@ -386,6 +386,10 @@ static moe_status_t enqueue_grouped(const moe_config_t* c, const moe_weights_t* 
     p.y = at<float>(ws, L.y);
     p.y_sh = at<float>(ws, L.ysh);
 
+    if (is_int4(fmt)) {
+        p.row_exp = at<int32_t>(ws, L.xexp);
+        p.row_exp_sh = p.row_exp + (size_t)n * k;
+    }
     const bool tiles = E_loc > 0 || S > 0;   // otherwise the output is zero: combine alone
     // gate + up
     TcMaps maps;

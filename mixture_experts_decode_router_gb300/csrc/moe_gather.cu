@@ -130,6 +130,80 @@ __global__ void __launch_bounds__(256) gather_kernel(const uint16_t* __restrict_
     pdl_trigger();
 }
 
+// The same rows for the INT4 tiles: f16 under a power of two each, which puts the row's largest
+// finite value below 2^15 and whose exponent goes to exps.  Exact for values down to 2^-29 of it
+// (a BF16 value has 8 significand bits), at any magnitude; an infinity stays one.
+template <bool NORM>
+__global__ void __launch_bounds__(256) gather_scaled_kernel(const uint16_t* __restrict__ x, int n, int H, int k,
+                                                            const int32_t* __restrict__ perm,
+                                                            const int32_t* __restrict__ offsets, int E,
+                                                            uint16_t* __restrict__ xs, uint16_t* __restrict__ xh,
+                                                            const uint16_t* __restrict__ nw, float eps,
+                                                            int32_t* __restrict__ exps, int early) {
+    constexpr int kU = 8;
+    pdl_wait();
+    if (early) pdl_trigger();
+    const int n_routes = offsets[E], rows = n_routes + n, C8 = H >> 3;
+    const int lane = threadIdx.x & 31, nwarps = gridDim.x * (blockDim.x >> 5);
+    for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += nwarps) {
+        const bool routed = r < n_routes;
+        const int t = routed ? perm[r] / k : r - n_routes;
+        const uint4* src = reinterpret_cast<const uint4*>(x + (size_t)t * H);
+        uint4* dst = reinterpret_cast<uint4*>(routed ? xs + (size_t)r * H : xh + (size_t)(r - n_routes) * H);
+        const float inv = NORM ? rms_inv_warp(reinterpret_cast<const uint16_t*>(src), H, eps, lane) : 0.f;
+        uint4 v[kU];
+        auto load = [&](int c0) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int c = c0 + 32 * u;
+                v[u] = c < C8 ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            if constexpr (NORM) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int c = c0 + 32 * u;
+                    if (c < C8) v[u] = rms_apply8(v[u], __ldg(reinterpret_cast<const uint4*>(nw) + c), inv);
+                }
+            }
+        };
+        // The largest finite magnitude, of BF16 bits: those of an infinity or NaN count as 0.
+        uint32_t am = 0u;
+        for (int c0 = lane; c0 < C8 + lane; c0 += 32 * kU) {
+            load(c0);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const uint32_t w4[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t lo = w4[q] & 0x7fffu, hi = (w4[q] >> 16) & 0x7fffu;
+                    am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                }
+            }
+        }
+        am = __reduce_max_sync(0xffffffffu, am);
+        const int sh = f16_shift(__uint_as_float(am << 16));
+        const float f = exp2i(sh);
+        for (int c0 = lane; c0 < C8; c0 += 32 * kU) {
+            if (C8 > 32 * kU) load(c0);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                if (c0 + 32 * u >= C8) continue;
+                float e[8];
+                bf16x8_to_float(v[u], e);
+                uint32_t o[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const __half2 h = __floats2half2_rn(e[2 * q] * f, e[2 * q + 1] * f);
+                    o[q] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                dst[c0 + 32 * u] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        if (lane == 0) exps[routed ? r : n * k + (r - n_routes)] = sh;
+    }
+    pdl_trigger();
+}
+
 // out[t, h] = bf16( sum_j y[inv[t*k + j], h] (slot order) + y_sh[t, h] ), for
 // calls whose down kernel does not run the combine itself.
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ y, const float* __restrict__ ysh,
@@ -223,8 +297,13 @@ cudaError_t launch_copy16(const void* src, void* dst, size_t bytes, int num_sms,
 
 cudaError_t launch_gather(int fmt, const uint16_t* x, int n, int H, int k, const int32_t* perm,
                           const int32_t* offsets, int E, uint16_t* xs, uint16_t* xh, const uint16_t* norm_w,
-                          float eps, bool early, int num_sms, cudaStream_t st) {
+                          float eps, int32_t* exps, bool early, int num_sms, cudaStream_t st) {
     const int grid = 2 * num_sms;
+    if (exps) {
+        launch_pdl(norm_w ? gather_scaled_kernel<true> : gather_scaled_kernel<false>, grid, 256, 0, st, x, n, H, k, perm,
+                   offsets, E, xs, xh, norm_w, eps, exps, early ? 1 : 0);
+        return cudaGetLastError();
+    }
     auto kern = fmt != MOE_W_BF16 ? (norm_w ? gather_kernel<true, true> : gather_kernel<true, false>)
                                   : (norm_w ? gather_kernel<false, true> : gather_kernel<false, false>);
     launch_pdl(kern, grid, 256, 0, st, x, n, H, k, perm, offsets, E, xs, xh, norm_w, eps, early ? 1 : 0);

@@ -584,7 +584,12 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                 if constexpr (GU) s2u = sh ? p.sh_scale2[1][0] : p.scale2[1][t.le];
             }
             float tw[2] = {0.f, 0.f};   // down: weight of token lane, lane + 32 (times scale2)
-            [[maybe_unused]] int te[2] = {0, 0};   // INT4 down: exponent of that token's row
+            [[maybe_unused]] int te[2] = {0, 0};   // INT4: exponent of that token's row
+            if constexpr (FMT == kFmtInt4) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (lane + 32 * h < t.ntok) te[h] = (sh ? p.row_exp_sh : p.row_exp)[t.pos0 + lane + 32 * h];
+            }
             if constexpr (!GU) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -594,7 +599,6 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                         if (sh) wgt = p.sg_logit ? 1.0f / (1.0f + expf(-p.sg_logit[t.pos0 + j])) : 1.0f;
                         else wgt = p.route_w[p.perm[t.pos0 + j]];
                         tw[h] = wgt * s2g;
-                        if constexpr (FMT == kFmtInt4) te[h] = (sh ? p.row_exp_sh : p.row_exp)[t.pos0 + j];
                     }
                 }
             }
@@ -611,6 +615,14 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                     float g[16], u[16];
                     ptx::tmem_ld16(tb + j0, g);
                     ptx::tmem_ld16(tb + NT + j0, u);
+                    if constexpr (FMT == kFmtInt4) {
+#pragma unroll
+                        for (int jj = 0; jj < 16; ++jj) {
+                            const int ex = __shfl_sync(0xffffffffu, j0 + jj < 32 ? te[0] : te[1], (j0 + jj) & 31);
+                            g[jj] = times_exp2(g[jj], -ex);
+                            u[jj] = times_exp2(u[jj], -ex);
+                        }
+                    }
                     if (valid) {
 #pragma unroll
                         for (int jj = 0; jj < 16; ++jj) {

@@ -104,7 +104,7 @@ inline bool int4_grouped(const moe_config_t& c, int64_t n) {
 
 struct WsLayout {
     size_t ctrl, logits, sg_logit, idx, w, counts, offsets, perm, active, act, act_sh,
-        inv, segs, xs, xh, as, ash, y, ysh, xe, xd, lgp, rq, aexp, total;
+        inv, segs, xs, xh, as, ash, y, ysh, xe, xd, lgp, rq, aexp, xexp, total;
 };
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -154,6 +154,7 @@ inline WsLayout ws_layout(const moe_config_t& c, int64_t n) {
     L.lgp = take(router_tc_partials_bytes(n, E, (int)H));        // tensor-core router partials
     L.rq = take(c.router_fmt == MOE_W_NVFP4 ? sizeof(uint16_t) * E * H : 0);   // an NVFP4 router as BF16
     L.aexp = take(int4_grouped(c, n) ? sizeof(int32_t) * (n * k + n) : 0);   // exponents of the rows of as, then of ash
+    L.xexp = take(int4_grouped(c, n) ? sizeof(int32_t) * (n * k + n) : 0);   // of the rows of xs, then of xh
     L.total = off;
     return L;
 }

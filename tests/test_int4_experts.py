@@ -584,3 +584,45 @@ def test_a_workspace_of_the_grouped_path(lib, n, path):
         if path == "grouped":
             assert torch.equal(got[:m], out[:m])
     assert (buf[size:] == 0xA5).all() and B.moe_workspace_check(buf, size) == (B.MOE_OK, 0)
+
+
+@gpu
+@pytest.mark.parametrize("path,n", [("grouped", 1), ("grouped", 9), ("auto", 170)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_inputs_past_f16_on_the_grouped_path(lib, path, n, norm):
+    """Rows of x that f16 would hold as zero or infinity, beside ordinary ones."""
+    cfg = cfg_of("int4_g64", pre_expert_norm=norm)
+    for scale in (2.0 ** -40, 2.0 ** -14, 2.0 ** 14, 2.0 ** 40):
+        lw = synth.make_weights(cfg, "cuda")
+        x = synth.make_input(cfg, n, "cuda")
+        if norm:
+            lw.pre_expert_norm_w = (lw.pre_expert_norm_w.float() * scale).to(torch.bfloat16)
+            xe = x.float() * torch.rsqrt((x.float() ** 2).mean(1, keepdim=True) + cfg.rms_norm_eps)
+            xr = (xe * lw.pre_expert_norm_w.float()).to(torch.bfloat16)
+        else:
+            x[::2] *= scale
+            xr = x
+        idx, w = routes(n)
+        layer = MoeLayer(lw, n, path)
+        got, ref = layer.experts(x, idx, w).float().cpu().numpy(), experts_ref(lw, xr, idx, w)
+        for t in range(n):
+            close(got[t], ref[t], norm)
+        assert layer.device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("path", ["auto", "grouped"])
+def test_infinite_and_nan_inputs(lib, path):
+    """An infinity stays one, and reaches only its own token, on either path."""
+    cfg = cfg_of("int4_g32", shared_inter=0)
+    lw = synth.make_weights(cfg, "cuda")
+    x = synth.make_input(cfg, 9, "cuda")
+    idx, w = routes(9)
+    layer = MoeLayer(lw, 9, path)
+    want = layer.experts(x, idx, w)
+    y = x.clone()
+    y[4, 3], y[6, 200] = float("nan"), float("inf")
+    got = layer.experts(y, idx, w)
+    rest = [0, 1, 2, 3, 5, 7, 8]
+    assert torch.equal(got[rest], want[rest])
+    assert torch.isnan(got[4]).all() and not torch.isfinite(got[6]).any()
