@@ -362,10 +362,21 @@ static moe_status_t enqueue_grouped(const moe_config_t* c, const moe_weights_t* 
     const int E_loc = local_experts(c);
     uint16_t* xs = at<uint16_t>(ws, L.xs);
     uint16_t* xh = at<uint16_t>(ws, L.xh);
+    WeightRows wr{};
+    if (is_int4(fmt)) {
+        const moe_qmat_t* q[] = {&w->gate, &w->up, &w->down, &w->sh_gate, &w->sh_up, &w->sh_down};
+        for (int m = 0; m < 3; ++m) {
+            wr.scale[m] = static_cast<const uint16_t*>(q[m]->scale);
+            wr.sh_scale[m] = static_cast<const uint16_t*>(q[3 + m]->scale);
+        }
+        wr.exps = at<int8_t>(ws, L.wexp);
+        wr.held = E_loc; wr.e_begin = c->expert_begin; wr.H = H; wr.I = I; wr.S = S; wr.gshift = int4_gshift(fmt);
+    }
     cudaError_t e = launch_gather(fmt, static_cast<const uint16_t*>(x), n, H, k, at<int32_t>(ws, L.perm),
                                   at<int32_t>(ws, L.offsets), E, xs, xh,
                                   static_cast<const uint16_t*>(w->pre_expert_norm_w), c->rms_norm_eps,
-                                  is_int4(fmt) ? at<int32_t>(ws, L.xexp) : nullptr, early_dependents(n, sms), sms, st);
+                                  is_int4(fmt) ? at<int32_t>(ws, L.xexp) : nullptr, wr,
+                                  at<int32_t>(ws, L.active), at<Ctrl>(ws, L.ctrl), early_dependents(n, sms), sms, st);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     mk.mark(st);
 
@@ -389,6 +400,10 @@ static moe_status_t enqueue_grouped(const moe_config_t* c, const moe_weights_t* 
     if (is_int4(fmt)) {
         p.row_exp = at<int32_t>(ws, L.xexp);
         p.row_exp_sh = p.row_exp + (size_t)n * k;
+        for (int m = 0; m < 2; ++m) {
+            p.wexp[m] = wr.exps + wr.routed(m);
+            p.sh_wexp[m] = wr.exps + wr.shared(m);
+        }
     }
     const bool tiles = E_loc > 0 || S > 0;   // otherwise the output is zero: combine alone
     // gate + up
@@ -408,6 +423,10 @@ static moe_status_t enqueue_grouped(const moe_config_t* c, const moe_weights_t* 
                             at<int32_t>(ws, L.offsets), E, as, ash, at<int32_t>(ws, L.aexp), n * k,
                             early_dependents(n, sms), sms, st);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
+        for (int m = 0; m < 2; ++m) {
+            p.wexp[m] = wr.exps + wr.routed(2);
+            p.sh_wexp[m] = wr.exps + wr.shared(2);
+        }
     }
     mk.mark(st);
 

@@ -133,14 +133,73 @@ __global__ void __launch_bounds__(256) gather_kernel(const uint16_t* __restrict_
 // The same rows for the INT4 tiles: f16 under a power of two each, which puts the row's largest
 // finite value below 2^15 and whose exponent goes to exps.  Exact for values down to 2^-29 of it
 // (a BF16 value has 8 significand bits), at any magnitude; an infinity stays one.
+//
+// Beside them, the weight rows' exponents: f16 holds (code - zero point) times a scale, so each
+// row's scales are multiplied by the power of two that puts the largest below 2^9 (127 of which
+// f16 holds), which the epilogue undoes.  (Scales below 2^-22 of their row's largest lose bits,
+// as they would in any one row of f16 operands.)  A warp takes 32 rows of one matrix, of the
+// experts that have tokens, as many lanes a row as it has loads of 16 bytes (8 scales; 4 bytes
+// where rows are no multiple of 16), four loads of a lane in flight.  768 tokens of hidden 2048,
+// 256 experts, groups of 32: the kernel 31 us, the call 411 (4-byte loads: 58 and 436).
+__device__ __forceinline__ void weight_row_exps(const WeightRows& wr, const int32_t* __restrict__ active, int n_active) {
+    const int lane = threadIdx.x & 31, wpb = blockDim.x >> 5;
+    const int per = (2 * wr.I + wr.H) / 32, routed = n_active * per, units = routed + (wr.S > 0 ? (2 * wr.S + wr.H) / 32 : 0);
+    for (int unit = blockIdx.x * wpb + (threadIdx.x >> 5); unit < units; unit += gridDim.x * wpb) {
+        const bool sh = unit >= routed;
+        const int a = sh ? 0 : unit / per, r = (sh ? unit - routed : unit - a * per) * 32, W = sh ? wr.S : wr.I;
+        const int m = r < W ? 0 : (r < 2 * W ? 1 : 2);
+        // The first row in its matrix's stack.
+        const int64_t row0 = (r - m * W) + (sh ? 0 : (int64_t)(__ldg(active + a) - wr.e_begin) * (m < 2 ? W : wr.H));
+        const int ng = (m < 2 ? wr.H : W) >> wr.gshift;
+        const uint16_t* s = (m == 0 ? (sh ? wr.sh_scale[0] : wr.scale[0]) : m == 1 ? (sh ? wr.sh_scale[1] : wr.scale[1])
+                                                                           : (sh ? wr.sh_scale[2] : wr.scale[2])) + row0 * ng;
+        int8_t* out = wr.exps + (sh ? wr.shared(m) : wr.routed(m)) + row0;
+        const bool vec = ng % 8 == 0 && reinterpret_cast<uintptr_t>(s) % 16 == 0;
+        const int words = vec ? ng / 8 : (ng + 1) / 2;   // loads of a row
+        const int lg = words >= 32 ? 5 : 32 - __clz(words - 1), lanes = 1 << lg, l = lane & (lanes - 1);   // (words >= 1)
+        for (int q0 = 0; q0 < lanes; q0 += 4) {
+            uint32_t am[4] = {0u, 0u, 0u, 0u};   // magnitude bits; those of an infinity or NaN count as 0
+            for (int w = l; w < words; w += lanes) {
+                uint4 b[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint16_t* p = s + (size_t)(((q0 + v) << (5 - lg)) + (lane >> lg)) * ng + (vec ? 8 : 2) * w;
+                    b[v] = make_uint4(0u, 0u, 0u, 0u);
+                    if (q0 + v >= lanes) continue;
+                    if (vec) b[v] = __ldg(reinterpret_cast<const uint4*>(p));
+                    else if (ng % 2 == 0) b[v].x = __ldg(reinterpret_cast<const uint32_t*>(p));   // (4-byte aligned arrays)
+                    else b[v].x = __ldg(p) | (2 * w + 1 < ng ? (uint32_t)__ldg(p + 1) << 16 : 0u);
+                }
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint32_t b4[4] = {b[v].x, b[v].y, b[v].z, b[v].w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t lo = b4[q] & 0x7fffu, hi = (b4[q] >> 16) & 0x7fffu;
+                        am[v] = max(am[v], max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                    }
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                for (int o = 1; o < lanes; o <<= 1) am[v] = max(am[v], __shfl_xor_sync(0xffffffffu, am[v], o));
+                if (l == 0 && q0 + v < lanes)
+                    out[((q0 + v) << (5 - lg)) + (lane >> lg)] = am[v] == 0u ? 0 : (int8_t)min(126, 8 - ((int)(am[v] >> 7) - 127));
+            }
+        }
+    }
+}
+
 template <bool NORM>
 __global__ void __launch_bounds__(256) gather_scaled_kernel(const uint16_t* __restrict__ x, int n, int H, int k,
                                                             const int32_t* __restrict__ perm,
                                                             const int32_t* __restrict__ offsets, int E,
                                                             uint16_t* __restrict__ xs, uint16_t* __restrict__ xh,
                                                             const uint16_t* __restrict__ nw, float eps,
-                                                            int32_t* __restrict__ exps, int early) {
-    constexpr int kU = 8;
+                                                            int32_t* __restrict__ exps, const WeightRows wr,
+                                                            const int32_t* __restrict__ active,
+                                                            const Ctrl* __restrict__ ctrl, int early) {
+    constexpr int kU = NORM ? 4 : 8;
     pdl_wait();
     if (early) pdl_trigger();
     const int n_routes = offsets[E], rows = n_routes + n, C8 = H >> 3;
@@ -201,6 +260,7 @@ __global__ void __launch_bounds__(256) gather_scaled_kernel(const uint16_t* __re
         }
         if (lane == 0) exps[routed ? r : n * k + (r - n_routes)] = sh;
     }
+    weight_row_exps(wr, active, ctrl->n_active);
     pdl_trigger();
 }
 
@@ -297,11 +357,11 @@ cudaError_t launch_copy16(const void* src, void* dst, size_t bytes, int num_sms,
 
 cudaError_t launch_gather(int fmt, const uint16_t* x, int n, int H, int k, const int32_t* perm,
                           const int32_t* offsets, int E, uint16_t* xs, uint16_t* xh, const uint16_t* norm_w,
-                          float eps, int32_t* exps, bool early, int num_sms, cudaStream_t st) {
+                          float eps, int32_t* exps, const WeightRows& wr, const int32_t* active, const Ctrl* ctrl, bool early, int num_sms, cudaStream_t st) {
     const int grid = 2 * num_sms;
     if (exps) {
-        launch_pdl(norm_w ? gather_scaled_kernel<true> : gather_scaled_kernel<false>, grid, 256, 0, st, x, n, H, k, perm,
-                   offsets, E, xs, xh, norm_w, eps, exps, early ? 1 : 0);
+        launch_pdl(norm_w ? gather_scaled_kernel<true> : gather_scaled_kernel<false>, 4 * num_sms, 256, 0, st, x, n, H, k, perm,
+                   offsets, E, xs, xh, norm_w, eps, exps, wr, active, ctrl, early ? 1 : 0);
         return cudaGetLastError();
     }
     auto kern = fmt != MOE_W_BF16 ? (norm_w ? gather_kernel<true, true> : gather_kernel<true, false>)

@@ -27,7 +27,10 @@
 // scale), one rounding with an 11-bit significand; NVFP4: e2m1 * e4m3 scale,
 // exact in f16, with the fp32 scale2 applied to the accumulator).  Those tiles
 // run the f16 MMA with f16 activations (exact for BF16 inputs in f16's normal
-// range, saturated at +-65504).  A pipeline stage covers 64 K (128 K in the
+// range, saturated at +-65504).  INT4: (code - zero point) times the group's
+// scale, rounded once to f16, each weight row's scales and each row of x and of
+// act under a power of two that brings the largest into f16's range and that the
+// epilogue undoes (moe_gather.cu), so the formats' range is fp32's.  A pipeline stage covers 64 K (128 K in the
 // FP8 and NVFP4 down kernels).  Warp roles: 0 TMA producer of the weight
 // codes (and FP8/NVFP4 block scales), 1 MMA issuer (one thread) and TMEM
 // owner, 2-5 epilogue (TMEM -> registers -> global), then the dequant warps,
@@ -585,7 +588,11 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
             }
             float tw[2] = {0.f, 0.f};   // down: weight of token lane, lane + 32 (times scale2)
             [[maybe_unused]] int te[2] = {0, 0};   // INT4: exponent of that token's row
+            [[maybe_unused]] int we[2] = {0, 0};   // and of this weight row (gate, up; down)
             if constexpr (FMT == kFmtInt4) {
+#pragma unroll
+                for (int q2 = 0; q2 < C::kMats; ++q2)
+                    if (valid) we[q2] = (sh ? p.sh_wexp[q2] : p.wexp[q2])[(size_t)t.le * t.out + m];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if (lane + 32 * h < t.ntok) te[h] = (sh ? p.row_exp_sh : p.row_exp)[t.pos0 + lane + 32 * h];
@@ -619,8 +626,8 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
 #pragma unroll
                         for (int jj = 0; jj < 16; ++jj) {
                             const int ex = __shfl_sync(0xffffffffu, j0 + jj < 32 ? te[0] : te[1], (j0 + jj) & 31);
-                            g[jj] = times_exp2(g[jj], -ex);
-                            u[jj] = times_exp2(u[jj], -ex);
+                            g[jj] = times_exp2(g[jj], -(ex + we[0]));
+                            u[jj] = times_exp2(u[jj], -(ex + we[1]));
                         }
                     }
                     if (valid) {
@@ -657,7 +664,7 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                         const int j = j0 + jj;
                         wj[jj] = __shfl_sync(0xffffffffu, j < 32 ? tw[0] : tw[1], j & 31);
                         if constexpr (FMT == kFmtInt4)
-                            d[jj] = times_exp2(d[jj], -__shfl_sync(0xffffffffu, j < 32 ? te[0] : te[1], j & 31));
+                            d[jj] = times_exp2(d[jj], -(we[0] + __shfl_sync(0xffffffffu, j < 32 ? te[0] : te[1], j & 31)));
                     }
                     if (valid) {
 #pragma unroll
@@ -692,6 +699,9 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
             const bool sh = t.e < 0;
             const int KB = (t.K + C::kBK - 1) / C::kBK;
             const int mrow = t.m0 + r;
+            [[maybe_unused]] int wx = 0;   // INT4: the exponent of this row's scales (first used behind the raw stage's wait)
+            if constexpr (FMT == kFmtInt4)
+                if (mrow < t.out) wx = (sh ? p.sh_wexp[pm] : p.wexp[pm])[(size_t)t.le * t.out + mrow];
             bool ok = true;
             for (int kb = 0; kb < KB && ok; ++git) {
                 // A group of kGrp operand stages (fewer at the end of the tile).
@@ -740,8 +750,9 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                     } else if constexpr (FMT == kFmtInt4) {
                         // INT4: 32 codes (one 16-byte chunk) lie in one group.  Nibble q
                         // becomes the f16 1024 + q (0x6400 | q), less 1024 + zero point is
-                        // exact, and the product with the scale rounds once to f16 (11
-                        // significand bits for weights of 4).
+                        // exact, and the product with the scale, which the row's power of two
+                        // brings into f16's range, rounds once to f16 (11 significand bits for
+                        // weights of 4).
                         static_assert(PE % 32 == 0, "INT4 dequant parts are whole 32-code chunks");
     #pragma unroll
                         for (int b = 0; b < PE / 32; ++b) {
@@ -756,7 +767,7 @@ grouped_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
                                 const uint8_t* zt = sh ? p.sh_zero[pm] : p.zero[pm];
                                 if (zt) zp = __ldg(zt + gi);
                             }
-                            const __half2 zh = __float2half2_rn((float)(1024u + zp)), shh = __float2half2_rn(s);
+                            const __half2 zh = __float2half2_rn((float)(1024u + zp)), shh = __float2half2_rn(s * exp2i(wx));
                             const uint32_t s2u = *reinterpret_cast<const uint32_t*>(&shh);
                             const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
     #pragma unroll

@@ -90,10 +90,12 @@ inline bool router_tc_fits(int64_t n, int64_t E, int H) {
 
 // INT4 under AUTO: the streaming kernels while the experts have at most
 // kStreamMaxAvg tokens on average, the grouped tensor-core path above.  Measured on
-// GB300, the experts in groups of 128, streaming against grouped: hidden 2048, 256
-// experts, top-8, 512 tokens (16 on average) 267 against 327 us, 768 tokens 363
-// against 343; hidden 7168, 64 experts, 128 tokens (16) 762 against 984 us, 192
-// tokens (24) 1067 against 1014.
+// GB300, the experts alone, streaming against grouped.  Hidden 2048, 256 experts, top-8,
+// 512 tokens (16 on average) and 640 (20): groups of 128 276 against 368 and 333 against
+// 380 us, of 32 306 against 388 and 378 against 400, of 32 with zero points 364 against
+// 403 and 444 against 415.  Hidden 7168, 64 experts, 128 tokens (16) and 160 (20): groups
+// of 128 751 against 1044 and 913 against 1052, of 32 853 against 1173 and 1107 against
+// 1183, of 32 with zero points 1033 against 1402 and 1328 against 1410.
 constexpr int kStreamMaxAvg = 20;
 
 // Whether a call of n tokens runs INT4 experts on the grouped path (monotone in n).
@@ -102,9 +104,22 @@ inline bool int4_grouped(const moe_config_t& c, int64_t n) {
     return c.path == MOE_PATH_GROUPED || (c.path == MOE_PATH_AUTO && n * c.top_k > (int64_t)kStreamMaxAvg * c.num_experts);
 }
 
+// INT4 on the grouped path: the exponents of the weight rows' powers of two (int8), gate, up and
+// down of the experts held here, then of the shared expert.
+struct WeightRows {
+    static int64_t count(int64_t held, int64_t H, int64_t I, int64_t S) { return held * (2 * I + H) + (S > 0 ? 2 * S + H : 0); }
+    const uint16_t* scale[3];      // gate, up, down
+    const uint16_t* sh_scale[3];
+    int8_t* exps;
+    int held, e_begin, H, I, S, gshift;
+    // First exponent of a matrix's rows (m: 0 gate, 1 up, 2 down).
+    __host__ __device__ int64_t routed(int m) const { return (int64_t)held * I * m; }
+    __host__ __device__ int64_t shared(int m) const { return (int64_t)held * (2 * I + H) + (int64_t)S * m; }
+};
+
 struct WsLayout {
     size_t ctrl, logits, sg_logit, idx, w, counts, offsets, perm, active, act, act_sh,
-        inv, segs, xs, xh, as, ash, y, ysh, xe, xd, lgp, rq, aexp, xexp, total;
+        inv, segs, xs, xh, as, ash, y, ysh, xe, xd, lgp, rq, aexp, xexp, wexp, total;
 };
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -155,6 +170,7 @@ inline WsLayout ws_layout(const moe_config_t& c, int64_t n) {
     L.rq = take(c.router_fmt == MOE_W_NVFP4 ? sizeof(uint16_t) * E * H : 0);   // an NVFP4 router as BF16
     L.aexp = take(int4_grouped(c, n) ? sizeof(int32_t) * (n * k + n) : 0);   // exponents of the rows of as, then of ash
     L.xexp = take(int4_grouped(c, n) ? sizeof(int32_t) * (n * k + n) : 0);   // of the rows of xs, then of xh
+    L.wexp = take(int4_grouped(c, n) ? (size_t)WeightRows::count(c.expert_end - c.expert_begin, H, I, S) : 0);
     L.total = off;
     return L;
 }

@@ -82,6 +82,8 @@ struct TcParams {
     int gshift;                 // INT4: log2 of the group size
     const int32_t* row_exp;     // INT4: the power of two by which each row of x (down: of act) was multiplied
     const int32_t* row_exp_sh;
+    const int8_t* wexp[2];      // INT4: the power of two by which each weight row's scales are multiplied
+    const int8_t* sh_wexp[2];
     void* act_out;           // gate_up: sorted SiLU(g)*u rows [n*k, I] (bf16 / f16; INT4: fp32)
     void* act_sh_out;        // gate_up: shared [n, S]
     float* y;                // down: weighted rows [n*k, H]
@@ -108,10 +110,11 @@ cudaError_t launch_grouped_tc(int fmt, bool gate_up, const TcMaps& maps, const T
 cudaError_t launch_copy16(const void* src, void* dst, size_t bytes, int num_sms, cudaStream_t st);
 // norm_w (may be null): the pre-expert RMSNorm weight; the rows gathered are
 // then the normalised ones (the norm kernel's values).  exps (INT4): each row enters as f16
-// times the power of two whose exponent goes there (n k rows of xs, then those of xh).
+// times the power of two whose exponent goes there (n k rows of xs, then those of xh), and wr's
+// exponents of the weight rows of the active experts and the shared one are formed.
 cudaError_t launch_gather(int fmt, const uint16_t* x, int n, int H, int k, const int32_t* perm,
                           const int32_t* offsets, int E, uint16_t* xs, uint16_t* xh, const uint16_t* norm_w,
-                          float eps, int32_t* exps, bool early, int num_sms, cudaStream_t st);
+                          float eps, int32_t* exps, const WeightRows& wr, const int32_t* active, const Ctrl* ctrl, bool early, int num_sms, cudaStream_t st);
 // INT4: the rows of SiLU(g) u (fp32) as f16 times a power of two each, whose exponents go to
 // exps (n_routes_max rows of as, then those of ash).
 cudaError_t launch_act_rows(const float* act, const float* act_sh, int n, int I, int S, const int32_t* offsets, int E,

@@ -626,3 +626,45 @@ def test_infinite_and_nan_inputs(lib, path):
     rest = [0, 1, 2, 3, 5, 7, 8]
     assert torch.equal(got[rest], want[rest])
     assert torch.isnan(got[4]).all() and not torch.isfinite(got[6]).any()
+
+
+def scaled(q, factor):
+    return dataclasses.replace(q, scale=(q.scale.float() * factor).to(torch.bfloat16))
+
+
+@gpu
+@pytest.mark.parametrize("path,n", [("grouped", 1), ("grouped", 9), ("auto", 170)])
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("gate,up,down", [
+    (1.0, 2.0 ** -24, 1.0), (1.0, 2.0 ** 30, 2.0 ** -30), (1.0, 2.0 ** -40, 2.0 ** 40), (1.0, 1.0, 2.0 ** 24),
+    (2.0 ** -30, 2.0 ** 30, 1.0)])
+def test_scales_far_from_one(lib, path, n, zero, gate, up, down):
+    """Group scales that f16 would hold as zero or infinity, on the grouped path (past 160 tokens of this layer AUTO's)."""
+    cfg = cfg_of("int4_g32", zero_points=zero)
+    lw = synth.make_weights(cfg, "cuda")
+    for m, f in (("gate", gate), ("up", up), ("down", down)):
+        setattr(lw, m, scaled(getattr(lw, m), f))
+        setattr(lw, "sh_" + m, scaled(getattr(lw, "sh_" + m), f))
+    x = synth.make_input(cfg, n, "cuda")
+    idx, w = routes(n)
+    layer = MoeLayer(lw, n, path)
+    out = layer.experts(x, idx, w)
+    close(out.float().cpu().numpy(), experts_ref(lw, x, idx, w))
+    assert layer.device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("path", ["auto", "grouped"])
+def test_scales_apart_in_a_row(lib, path):
+    """Groups of one row whose scales are 2^16 apart: the small ones count where x is small beside the large."""
+    cfg = cfg_of("int4_g32", shared_inter=0)
+    lw = synth.make_weights(cfg, "cuda")
+    s = lw.up.scale.float()
+    s[..., 1::2] *= 2.0 ** -16
+    lw.up = dataclasses.replace(lw.up, scale=s.to(torch.bfloat16))
+    x = synth.make_input(cfg, 12, "cuda").view(12, -1, 2, 32).clone()
+    x[:, :, 0] *= 2.0 ** -10
+    x[:, :, 1] *= 2.0 ** 6
+    x = x.view(12, -1)
+    idx, w = routes(12)
+    close(MoeLayer(lw, 12, path).experts(x, idx, w).float().cpu().numpy(), experts_ref(lw, x, idx, w))
