@@ -668,3 +668,111 @@ def test_scales_apart_in_a_row(lib, path):
     x = x.view(12, -1)
     idx, w = routes(12)
     close(MoeLayer(lw, 12, path).experts(x, idx, w).float().cpu().numpy(), experts_ref(lw, x, idx, w))
+
+
+@gpu
+@pytest.mark.parametrize("zero", [False, True])
+def test_expert_parallel_on_the_grouped_path(lib, zero):
+    """Ranks that hold some experts, none, or all but the shared one, with scales far from one."""
+    n, cfg = 9, cfg_of("int4_g32", zero_points=zero, shared_gate=True)
+    lw = synth.make_weights(cfg, "cuda")
+    for m in ("up", "sh_up"):
+        setattr(lw, m, scaled(getattr(lw, m), 2.0 ** 30))
+    L = int4_oracle_layer(lw)
+    x = synth.make_input(cfg, n, "cuda", gap_fn=gap_fn_for(L))
+    for r in ((0, 5), (5, 16), (7, 8)):
+        layer = MoeLayer(synth.expert_slice(lw, *r), n, "grouped", experts=r, exclude_shared=True)
+        out, _, _ = layer.forward(x)
+        ref, _, _, _ = O.moe_forward(L, bf16_bits(x), experts=r, include_shared=False)
+        got = out.float().cpu().numpy()
+        close(got, ref) if np.any(ref) else np.testing.assert_array_equal(got, 0)
+        assert layer.device_error() == 0
+    layer = MoeLayer(synth.expert_slice(lw, 16, 16), n, "grouped", experts=(16, 16), accumulate=True)
+    out = torch.zeros(n, cfg.hidden, dtype=torch.bfloat16, device="cuda")
+    layer.forward(x, out=out, routing=False)
+    close(out.float().cpu().numpy(), O.moe_forward(L, bf16_bits(x), experts=(0, 0))[0])
+    assert layer.device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("path,n", [("auto", 3), ("auto", 20), ("grouped", 20), ("token_major", 2)])
+@pytest.mark.parametrize("hidden,inter", [(256, 128), (512, 256), (96, 160)])
+def test_scales_at_a_4_byte_offset(lib, path, n, hidden, inter):
+    """Scale arrays that are aligned to 4 bytes alone: the same bits."""
+    cfg = cfg_of("int4_g32", hidden=hidden, inter=inter, shared_inter=inter)
+    lw = synth.make_weights(cfg, "cuda")
+    x = synth.make_input(cfg, n, "cuda")
+    idx, w = routes(n)
+    want = MoeLayer(lw, n, path).experts(x, idx, w)
+    for m in ("gate", "up", "down", "sh_gate", "sh_up", "sh_down"):
+        q = getattr(lw, m)
+        buf = torch.empty(q.scale.numel() + 2, dtype=torch.bfloat16, device="cuda")
+        moved = buf[2:].view(q.scale.shape)
+        moved.copy_(q.scale)
+        assert moved.data_ptr() % 16 == 4
+        setattr(lw, m, dataclasses.replace(q, scale=moved))
+    assert torch.equal(MoeLayer(lw, n, path).experts(x, idx, w), want)
+
+
+@gpu
+def test_experts_without_tokens_on_the_grouped_path(lib):
+    """NaN and infinite scales of experts that no token chose reach nothing, and those of one that some chose, those."""
+    cfg = cfg_of("int4_g32", shared_inter=0)
+    lw = synth.make_weights(cfg, "cuda")
+    x = synth.make_input(cfg, 9, "cuda")
+    idx, w = torch.tensor([[1, 4]] * 8 + [[4, 9]], dtype=torch.int32, device="cuda"), torch.ones(9, 2, device="cuda")
+    want = MoeLayer(lw, 9, "grouped").experts(x, idx, w)
+    s = lw.up.scale.clone()
+    s[[0, 2, 3, 5]] = float("nan")
+    s[9, :, 0] = float("inf")
+    lw.up = dataclasses.replace(lw.up, scale=s)
+    got = MoeLayer(lw, 9, "grouped").experts(x, idx, w)
+    assert torch.equal(got[:8], want[:8]) and not torch.isfinite(got[8]).any()
+
+
+@gpu
+def test_infinite_act_on_the_grouped_path(lib):
+    """One value of SiLU(g) u past fp32's range beside values past fp16's, one expert and one row of down's each: the
+    infinity's sign, or NaN where its weight is 0."""
+    cfg = cfg_of("int4_g32", shared_inter=0, top_k=1)
+    lw = synth.make_weights(cfg, "cuda")
+    n = 9
+    x = synth.make_input(cfg, n, "cuda") * 2.0 ** 13
+    xe = O.bf16_decode(bf16_bits(x))
+    L = int4_oracle_layer(lw)
+    gs, us = lw.gate.scale.float(), lw.up.scale.float()
+    for t in range(n):
+        gs[t, 5] *= 2.0 ** 85 * float(np.sign(L.gate.expert(t)[5] @ xe[t]))
+        us[t, 5] *= 2.0 ** 85
+    lw.gate = dataclasses.replace(lw.gate, scale=gs.to(torch.bfloat16))
+    lw.up = dataclasses.replace(lw.up, scale=us.to(torch.bfloat16))
+    L = int4_oracle_layer(lw)
+    idx, w = torch.arange(n, dtype=torch.int32, device="cuda")[:, None], torch.ones(n, 1, device="cuda")
+    got = MoeLayer(lw, n, "grouped").experts(x, idx, w).float().cpu().numpy()
+    for t in range(n):
+        d, u5 = L.down.expert(t)[:, 5], float(L.up.expert(t)[5] @ xe[t])
+        want = np.full(len(d), np.nan, np.float32)
+        want[d != 0] = np.inf * np.sign(d[d != 0]) * np.sign(u5)
+        assert np.array_equal(got[t], want, equal_nan=True)
+
+
+@gpu
+@pytest.mark.parametrize("n", [9, 170])
+def test_the_grouped_path_captured_and_replayed(lib, n):
+    """In a graph, replayed on inputs of other magnitudes, between layers that share the weights."""
+    cfg = cfg_of("int4_g64", zero_points=True)
+    lw = synth.make_weights(cfg, "cuda")
+    xs = [synth.make_input(cfg, n, "cuda", stream=s) * f for s, f in ((0, 1.0), (1, 2.0 ** 20), (2, 2.0 ** -20))]
+    a, b = MoeLayer(lw, n, "grouped"), MoeLayer(lw, n, "grouped")
+    want = [a.forward(x)[0].clone() for x in xs]
+    buf, oa, ob = xs[0].clone(), torch.empty_like(want[0]), torch.empty_like(want[0])
+    b.forward(buf, out=ob)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.forward(buf, out=oa)
+        b.forward(buf, out=ob)
+    for x, r in zip(xs, want):
+        buf.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(oa, r) and torch.equal(ob, r)
