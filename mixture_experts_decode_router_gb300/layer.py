@@ -115,7 +115,8 @@ def _made(stream, *shape, **kw) -> torch.Tensor:
     current = None if stream is None or kw["device"].type != "cuda" else torch.cuda.current_stream(kw["device"])
     if current is None or B._stream(stream) == current.cuda_stream:
         return torch.empty(*shape, **kw)
-    with torch.cuda.stream(torch.cuda.ExternalStream(B._stream(stream), kw["device"])):
+    raw, dev = B._stream(stream), kw["device"]   # (ExternalStream(0) would be a new stream)
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, dev) if raw else torch.cuda.default_stream(dev)):
         t = torch.empty(*shape, **kw)
     t.record_stream(current)
     return t

@@ -344,3 +344,21 @@ def test_a_matrix_struct_by_position():
     w = B.moe_weights_t()
     w.gate = B.moe_qmat_t(5, 6, 7)
     assert (w.gate.w, w.gate.scale, w.gate.scale2) == (5, 6, 7)
+
+
+@gpu
+@pytest.mark.parametrize("name", CALLS)
+def test_outputs_of_the_default_stream_from_another(lib, name):
+    """stream=0 is the default stream: called from another, the outputs are the default stream's memory."""
+    call, (shape, dtype) = calls_on_a_stream()[name]
+    want = call(None)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        got = call(0)
+        at = got[0].data_ptr()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, r) for g, r in zip(got, want))
+    del got
+    torch.cuda.synchronize()
+    assert at in {t.data_ptr() for t in [torch.empty(shape, dtype=dtype, device="cuda") for _ in range(64)]}
