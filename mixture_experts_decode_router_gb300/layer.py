@@ -112,7 +112,7 @@ def make_weights(lw: LayerWeights) -> B.moe_weights_t:
 
 def _made(stream, *shape, **kw) -> torch.Tensor:
     """An output of a call on `stream`: that stream's memory, in use on the current one."""
-    current = None if stream is None or kw["device"].type != "cuda" else torch.cuda.current_stream(kw["device"])
+    current = None if stream is None else torch.cuda.current_stream(kw["device"])
     if current is None or B._stream(stream) == current.cuda_stream:
         return torch.empty(*shape, **kw)
     raw, dev = B._stream(stream), kw["device"]   # (ExternalStream(0) would be a new stream)
@@ -184,10 +184,15 @@ class MoeLayer:
         return v
 
     def route(self, x: torch.Tensor, logits: bool = True, stream=None):
+        dev, H = self.weights.router_w.device, self.cfg.hidden
+        if x.dtype != torch.bfloat16 or x.dim() < 1 or x.numel() != x.shape[0] * H or not x.is_contiguous():
+            raise ValueError("x is contiguous bfloat16 [n, hidden]")
+        if dev.type != "cuda" or dev.index != torch.cuda.current_device() or not (x.device == dev or x.is_pinned()):
+            raise ValueError("x is on the current device, which is the layer's, or in pinned host memory")
         n, k, E = x.shape[0], self.cfg.top_k, self.cfg.num_experts
-        idx = _made(stream, n, k, dtype=torch.int32, device=x.device)
-        w = _made(stream, n, k, dtype=torch.float32, device=x.device)
-        lg = _made(stream, n, E, dtype=torch.float32, device=x.device) if logits else None
+        idx = _made(stream, n, k, dtype=torch.int32, device=dev)
+        w = _made(stream, n, k, dtype=torch.float32, device=dev)
+        lg = _made(stream, n, E, dtype=torch.float32, device=dev) if logits else None
         B.check(B.moe_route(self.c_cfg, self.c_w, x, n, idx, w, lg, self.ws, self.ws_bytes, stream))
         return idx, w, lg
 

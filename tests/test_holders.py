@@ -362,3 +362,30 @@ def test_outputs_of_the_default_stream_from_another(lib, name):
     del got
     torch.cuda.synchronize()
     assert at in {t.data_ptr() for t in [torch.empty(shape, dtype=dtype, device="cuda") for _ in range(64)]}
+
+
+# ---------------------------------------------------------------- moe_route
+
+def test_route_refusals():
+    """On the CPU: what moe_route would read as something else, or past its end, is refused before the library is called."""
+    layer = MoeLayer(synth.make_weights(cfg_of(), "cpu"), 3)
+    x = torch.zeros(3, 128, dtype=torch.bfloat16)
+    for bad in (x.half(), x.float(), x[:, :64].contiguous(), torch.zeros(3, 256, dtype=torch.bfloat16)[:, ::2], x[0]):
+        with pytest.raises(ValueError, match="contiguous bfloat16"):
+            layer.route(bad)
+    with pytest.raises(ValueError, match="on the current device"):
+        layer.route(x)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 3])
+def test_route_of_pinned_x(lib, n):
+    """Its outputs are on the layer's GPU, wherever x is."""
+    cfg = cfg_of()
+    layer = MoeLayer(synth.make_weights(cfg, "cuda"), n)
+    x = synth.make_input(cfg, n, "cuda")
+    for got, want in zip(layer.route(x.cpu().pin_memory()), layer.route(x)):
+        assert got.is_cuda and torch.equal(got, want)
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError):
+        layer.route(x.cpu())
