@@ -83,7 +83,13 @@
  *                   scale: BF16 [E, out, in/G] (one per G elements along in);
  *                   zero: bytes [E, out, in/G], 0..15, or NULL (every zero
  *                   point is 8); value = (code - zero[o][i/G]) * scale[o][i/G];
- *                   every reduction length (H, I and S) is a multiple of G
+ *                   every reduction length (H, I and S) is a multiple of G.
+ *                   INT4 experts have fp32's range at any number of tokens:
+ *                   SiLU(g) u (and, on the expert-grouped path, x and the
+ *                   scales) enter the products as f16 under a power of two for
+ *                   each row, or for each 256 or 768 elements of a row.  Values
+ *                   below 2^-29 (scales: 2^-22) of the largest that shares their
+ *                   power of two lose bits there.
  *  idx          int32 [N, k], slots in descending selection score
  *  w            fp32  [N, k]
  *  logits       fp32  [N, E]
@@ -253,6 +259,10 @@ size_t moe_workspace_bytes(const moe_config_t* cfg, int32_t max_tokens);
  * tensor cores (fp32 accumulation per K range, the ranges summed in a fixed
  * order), otherwise on the CUDA cores; so moe_route + moe_experts is
  * moe_forward bit for bit.
+ * The routing words MOE_ROUTE_SOFTMAX and MOE_ROUTE_SIGMOID_BIAS alone rank
+ * scores computed in fp32 (sigmoid(l) + bias of two experts can tie or change
+ * places there within their fp32 errors); every other word ranks them in 64
+ * bits, as moe_topk does with any word.
  *   x       device BF16 [n, H]
  *   idx     device int32 [n, k]   (out) selected experts, descending score
  *   w       device fp32  [n, k]   (out) routing weights
@@ -392,7 +402,8 @@ typedef struct {
  *   bias        device fp32 [E] (*_BIAS modes; 4-byte aligned), else NULL
  *   idx, w      device int32 / fp32 [n, k] (out), slots in descending
  *               selection score, equal scores by ascending expert index
- * Selection is that of the scores in 64 bits.  A NaN score ranks last.
+ * Selection is that of the scores in 64 bits, for any finite or infinite bias.
+ * A NaN score ranks as -inf does; a group score of inf - inf ranks last.
  * w = p, divided by the sum of the k selected p if norm_topk_prob, times
  * routed_scaling_factor; a row whose selected logits are all -inf gets w = 0.
  * logits may also be pinned host memory.  No workspace; n == 0 is a no-op.
@@ -416,7 +427,9 @@ typedef struct {
  * x: the matrix-vector product of the layer's 4-bit formats for a decode batch,
  * as the experts use it, for the dense projections around the layer.  fp32
  * accumulation, one rounding to out_type.  A row's result does not depend on
- * the other rows.  The weights cross HBM once for each 16 rows.
+ * the other rows.  The weights cross HBM once for each 16 rows of x while
+ * in_features <= 5376, for each 8 up to 10752, and for as many as 175040 bytes
+ * hold at 2 in_features + 64 each beyond (5 at 16384, 1 at 57344).
  *   w           the matrix, in the layouts above with E = 1 (its w 16-byte
  *               aligned, scale and scale2 4)
  *   bias        device fp32 [out_features] (4-byte aligned), or NULL

@@ -228,11 +228,11 @@ static int effective_path(const moe_config_t* c, int32_t n) {
 // token that the grid repeats: no grouping, no combining, but an expert's weights once
 // for each token that chose it.  Measured on GB300, 8 experts of each token and a
 // shared one, groups of 128, per token against grouped: hidden 2048, intermediate 512,
-// 256 experts (14 MB a token) 2 tokens 15.2 against 24.4 us, 4 tokens 24.8 against
-// 33.4, 8 tokens 44.2 against 35.7; hidden 1024, intermediate 512, 32 experts (7 MB) 4
-// tokens 17.1 against 19.3, 6 tokens 20.3 against 20.0; hidden 2048, intermediate 1024,
-// 64 experts (27 MB) 2 tokens 26.1 against 32.4, 4 tokens 48.1 against 35.1; hidden
-// 4096, intermediate 1536 (81 MB) 2 tokens 65.3 against 59.6.
+// 256 experts (14 MB a token) 2 tokens 14.2 against 24.2 us, 4 tokens 24.8 against
+// 33.2, 8 tokens 43.3 against 35.7; hidden 1024, intermediate 512, 32 experts (7 MB) 4
+// tokens 16.5 against 18.9, 6 tokens 19.7 against 19.2; hidden 2048, intermediate 1024,
+// 64 experts (27 MB) 2 tokens 25.6 against 32.6, 4 tokens 47.1 against 34.0; hidden
+// 4096, intermediate 1536 (81 MB) 2 tokens 64.3 against 60.6.
 constexpr int kPerTokenMax = 4;
 constexpr int64_t kPerTokenBytes = (int64_t)64 << 20;
 static bool per_token(const moe_config_t* c, int32_t n) {

@@ -16,14 +16,16 @@
 //   output.
 //
 // act enters the down product as f16, each token's chunk of 768 (one token: 256) scaled by a power of
-// two that puts its largest value below 2^15: one rounding to 11 significand bits
+// two that puts its largest finite value below 2^15: one rounding to 11 significand bits
 // down to 2^-29 of that value, at any magnitude.  Chunks and order of every sum
-// depend on the layer's sizes alone, so a token's bits do not depend on its batch.
+// depend on the layer's sizes alone within each of the two forms: a token's bits do not
+// depend on the other tokens of its batch, and do differ between the batches that take
+// their routes one by one (one token, or a few) and the larger ones.
 //
 // On GB300 (hidden 2048, intermediate 512, 8 of 256 experts and a shared one): one token
 // 9.7 us (1.5 TB/s), 16 tokens with groups of 64 and zero points 64 us (2.8 TB/s), 256
-// rows with groups of 32 208 us (2.2 TB/s); hidden 7168, intermediate 2048, 8 of 64
-// experts, 64 tokens 483 us (3.1 TB/s).  The copies and the staging alone take 41, 125
+// rows with groups of 32 205 us (2.2 TB/s); hidden 7168, intermediate 2048, 8 of 64
+// experts, 64 tokens 473 us (3.1 TB/s).  The copies and the staging alone take 41, 125
 // and 306 us of the last three; the rest is what the warps' instructions do not overlap.
 // (Measured and not kept: the rows of x prepared once by a kernel of their own and read
 // through L1 by warps that share nothing, 70, 273 and 547 us; two row tiles a warp for

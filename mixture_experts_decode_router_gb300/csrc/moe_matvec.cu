@@ -2,9 +2,9 @@
 // (sm_103a): out[t, o] = sum_i W[o, i] x[t, i] (+ bias[o]) (+ out[t, o]).
 //
 // Bound by the instructions on the weight stream (q4_mma.cuh).  On GB300: 100003 x 2048,
-// groups of 32, six tokens 32.3 us (3.6 TB/s); 7168 x 7168 with zero points, one token
-// 9.2 us (3.1 TB/s); 2048 x 2048 2.9 us, launch and latency; 7168 x 2048 NVFP4, 16
-// tokens 8.2 us, the staging of x in every block.  Without the products the
+// groups of 32, six tokens 31.0 us (3.8 TB/s); 7168 x 7168 with zero points, one token
+// 8.9 us (3.2 TB/s); 2048 x 2048 3.0 us, launch and latency; 7168 x 2048 NVFP4, 16
+// tokens 8.0 us, the staging of x in every block.  Without the products the
 // first takes 21 us.  (Stretches of stages that split the tiles of a part evenly over a
 // block's warps, which balances the rounds, took 35 us where this took 33.4: the copies
 // of a block's warps then lie apart in K.)

@@ -14,10 +14,10 @@
 // chosen come out of k + 1 rounds of one redux each: a lane's scores are order-
 // preserving integers with the expert's index in the low bits (so equal scores go to
 // the lower index), sorted in lists of 8, and the lane whose head wins shifts its
-// list.  Bound by instruction issue: about 820 of a warp for a row of 256 sigmoid scores
-// with a bias, 8 groups and 8 chosen (the rounds 230, the groups 200, the weights 100):
-// 32768 such rows take 38 us on GB300, 0.93 TB/s of fp32 logits; one row 3 us, most of
-// it launch and latency.  (Every score in 64 bits: 1116 us and 28 us.)
+// list.  Bound by instruction issue: about 850 of a warp for a row of 256 sigmoid scores
+// with a bias, 8 groups and 8 chosen, at 0.59 a scheduler and cycle: 32768 such rows take
+// 37 us on GB300, 0.91 TB/s of fp32 logits; one row 3.2 us, most of it launch and
+// latency.  (Every score in 64 bits: 1116 us and 28 us.)
 #include <cuda_fp16.h>
 
 #include <algorithm>

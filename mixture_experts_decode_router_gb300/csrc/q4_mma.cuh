@@ -20,7 +20,8 @@
 //    Its nibbles i and i + 4 form one 16-bit pair (INT4), so x is stored with
 //    the elements of every 8 in the order 0 4 1 5 2 6 3 7.
 //  * INT4 value = (q - z) s: q goes under the exponent of 128 (bf16) or of 1024 and
-//    64 (f16), less that exponent's value + z is the exact difference; the MMA sums
+//    64 (f16), the well-known way from small integers to floats without a conversion;
+//    less that exponent's value + z is the exact difference; the MMA sums
 //    a group in fp32, and s multiplies that sum in fp32.  No weight is rounded, and
 //    x enters as it is.  (Measured and not kept: masked codes as f16 subnormals with
 //    -z taken away by a second MMA, or by the groups' sums of x, after scaling x
