@@ -389,3 +389,26 @@ def test_route_of_pinned_x(lib, n):
     torch.cuda.synchronize()
     with pytest.raises(ValueError):
         layer.route(x.cpu())
+
+
+@gpu
+@pytest.mark.parametrize("name", ["forward", "experts", "topk", "matvec"])
+def test_a_forked_stream_in_a_capture(lib, name):
+    """A call on a stream that joins the capture, its outputs made and some dropped there, replayed."""
+    call, _ = calls_on_a_stream()[name]
+    want = [t.clone() for t in call(None)]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        st.wait_stream(torch.cuda.current_stream())
+        call(st)
+        got = call(st)
+        torch.cuda.current_stream().wait_stream(st)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
