@@ -403,7 +403,8 @@ typedef struct {
  *   idx, w      device int32 / fp32 [n, k] (out), slots in descending
  *               selection score, equal scores by ascending expert index
  * Selection is that of the scores in 64 bits, for any finite or infinite bias.
- * A NaN score ranks as -inf does; a group score of inf - inf ranks last.
+ * A NaN score ranks as -inf does (a softmax of -inf alone is NaN: such a row
+ * takes experts by index); a group score of inf - inf ranks last.
  * w = p, divided by the sum of the k selected p if norm_topk_prob, times
  * routed_scaling_factor; a row whose selected logits are all -inf gets w = 0.
  * logits may also be pinned host memory.  No workspace; n == 0 is a no-op.
