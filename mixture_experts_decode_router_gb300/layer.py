@@ -6,6 +6,7 @@ the layer happens here.
 from __future__ import annotations
 
 from ctypes import addressof
+from dataclasses import fields, is_dataclass
 from typing import Optional
 
 import torch
@@ -110,6 +111,13 @@ def make_weights(lw: LayerWeights) -> B.moe_weights_t:
     return w
 
 
+def _tensors(o) -> list:
+    """The tensors of a weights dataclass, those of its matrices included."""
+    if isinstance(o, torch.Tensor):
+        return [o]
+    return [t for f in fields(o) for t in _tensors(getattr(o, f.name))] if is_dataclass(o) else []
+
+
 def _made(stream, *shape, **kw) -> torch.Tensor:
     """An output of a call on `stream`: that stream's memory, in use on the current one."""
     current = None if stream is None else torch.cuda.current_stream(kw["device"])
@@ -141,12 +149,13 @@ class MoeLayer:
         self.accumulate = accumulate
         self.c_cfg = make_config(self.cfg, path, experts, exclude_shared, accumulate)
         self.c_w = make_weights(weights)
+        self._held = _tensors(weights)   # the memory that c_w points to
         self.ws_bytes = B.moe_workspace_bytes(self.c_cfg, max_tokens)
         if self.ws_bytes == 0:
             raise B.MoeError("invalid layer configuration")
         if self.cfg.expert_fmt in INT4_GROUP:
             self._check_int4()
-        dev = weights.router_w.device
+        dev = self._device = weights.router_w.device
         # The control block (first 256 bytes) must start at zero; calls keep it zero.
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
         self.max_tokens = max_tokens
@@ -184,7 +193,7 @@ class MoeLayer:
         return v
 
     def route(self, x: torch.Tensor, logits: bool = True, stream=None):
-        dev, H = self.weights.router_w.device, self.cfg.hidden
+        dev, H = self._device, self.cfg.hidden
         if x.dtype != torch.bfloat16 or x.dim() < 1 or x.numel() != x.shape[0] * H or not x.is_contiguous():
             raise ValueError("x is contiguous bfloat16 [n, hidden]")
         if dev.type != "cuda" or dev.index != torch.cuda.current_device() or not (x.device == dev or x.is_pinned()):

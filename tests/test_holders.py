@@ -1,6 +1,8 @@
 """The Python holders' calls: what they take, what they refuse, the memory and the streams they use."""
 
 import dataclasses
+import gc
+import weakref
 
 import pytest
 import torch
@@ -412,3 +414,17 @@ def test_a_forked_stream_in_a_capture(lib, name):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4_g32"])
+def test_a_layer_keeps_what_it_points_to(fmt):
+    """Matrices replaced in the weights after construction: the ones that the struct points to live on."""
+    lw = synth.make_weights(cfg_of(fmt, shared_gate=True, pre_expert_norm=True), "cpu")
+    layer = MoeLayer(lw, 3)
+    refs = [weakref.ref(t) for t in (lw.up.w, lw.sh_down.w, lw.router_w, lw.shared_gate_w, lw.pre_expert_norm_w)]
+    lw.up = lw.sh_down = lw.router_w = lw.shared_gate_w = lw.pre_expert_norm_w = None
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del layer
+    gc.collect()
+    assert all(r() is None for r in refs)
