@@ -445,6 +445,95 @@ typedef struct {
 moe_status_t moe_matvec(const moe_matvec_config_t* cfg, const moe_qmat_t* w, const float* bias, const void* x,
                         int64_t x_stride, int32_t n, void* out, int64_t out_stride, moe_stream_t stream);
 
+/* Residual addition and RMSNorm of rows (moe_norm). */
+typedef struct {
+    int32_t hidden;                 /* H, 1..32768 */
+    int32_t x_type;                 /* moe_dtype_t */
+    int32_t residual_type;          /* of residual and residual_out: x_type or MOE_F32 */
+    int32_t weight_type;            /* moe_dtype_t */
+    int32_t out_type;               /* moe_dtype_t */
+    int32_t scale_group;            /* elements of a row that share a scale of out8: 128, or 0 for the whole row */
+    float   eps;                    /* >= 0 */
+    float   weight_offset;          /* added to the weight: 0, or 1 where weights are stored about 0 */
+} moe_norm_config_t;
+
+/* The norm between two layers, for any number of rows: a layer's output x is
+ * added to the residual stream, and the sum, normalised, is the next input --
+ * in 16 or 32 bits, in 8 bits with scales (the FP8 experts' E4M3 and their
+ * blocks of 128 along a reduction), or both.  (The layer's own pre-expert norm
+ * has neither a residual nor an 8-bit output.)
+ *   h = x + residual in fp32, rounded to the residual's type; x without one
+ *   y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset)      (fp32)
+ *   residual_out = h;  out = y, rounded to out_type;
+ *   scale8[g] = max(max |y| / 448, 2^-126) over the group g;  out8 = E4M3(y / scale8[g])
+ *   x, residual     device [n, H]; residual may be NULL
+ *   weight          device [H], or NULL (1)
+ *   residual_out    device [n, H] (out), or NULL; may be residual itself
+ *   out             device [n, H] (out), or NULL; may be x itself (of one type)
+ *   out8, scale8    device E4M3 bytes [n, H] and fp32 [n, ceil(H / 128)] or [n] (out),
+ *                   or NULL; one of out and out8 is given
+ * Rows are *_stride >= H elements apart; every pointer is aligned to its
+ * element.  Where all of them (and the strides) are multiples of 16 bytes (8 for
+ * out8) and H of 8, rows are read and written 16 bytes at a time.
+ * Outputs overlap nothing else, from their first row to their last.
+ * h^2 may leave fp32's range: such a row is normalised all the same.  A row of
+ * zeros with eps = 0 gives zeros.  An infinity in h makes NaN of itself and
+ * zeros of the rest, a NaN the whole row; the scale of a group with an infinity
+ * or a NaN in y is that, and the values it stands for are NaN.
+ * All of these but weight may also be pinned host memory.  No workspace;
+ * n == 0 is a no-op.
+ * Errors: MOE_ERR_NULL, MOE_ERR_INVALID_CONFIG, MOE_ERR_UNSUPPORTED (more than
+ * 32768 elements), MOE_ERR_ALIGNMENT, MOE_ERR_ALIAS, MOE_ERR_HOST_MEMORY,
+ * MOE_ERR_CUDA. */
+moe_status_t moe_norm(const moe_norm_config_t* cfg, const void* x, int64_t x_stride, const void* residual,
+                      int64_t residual_stride, const void* weight, int32_t n, void* residual_out,
+                      int64_t residual_out_stride, void* out, int64_t out_stride, void* out8, int64_t out8_stride,
+                      float* scale8, moe_stream_t stream);
+
+/* Low-rank adapters of one projection (moe_lora). */
+typedef struct {
+    int32_t in_features;            /* a multiple of 8, at most 2^20 */
+    int32_t out_features;           /* 1..2^28 */
+    int32_t rank;                   /* a multiple of 8, at most 128 (an adapter of less is filled with zeros) */
+    int32_t num_adapters;           /* 1..1024 */
+    int32_t x_type;                 /* of x and of both matrices: MOE_BF16 or MOE_F16 */
+    int32_t out_type;               /* of base and out: moe_dtype_t */
+} moe_lora_config_t;
+
+/* Bytes of workspace a call with up to `max_rows` rows needs (a multiple of
+ * 256).  Returns 0 if `cfg` is NULL or invalid, or max_rows < 0. */
+size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows);
+
+/* out[t] = base[t] + scale[e] B_e (A_e x[t]),  e = idx[t]: the adapters of many
+ * requests at once beside a projection that they share (moe_matvec's, or any
+ * other), whose result is `base`.  A row whose e is outside [0, num_adapters)
+ * has no adapter: out[t] = base[t].
+ *   a           device [num_adapters, rank, in_features] (16-byte aligned)
+ *   b           device [num_adapters, out_features, rank] (16-byte aligned)
+ *   scale       device fp32 [num_adapters], or NULL (1)
+ *   x           device [n, in_features], rows x_stride elements apart; 16-byte
+ *               aligned, x_stride >= in_features and a multiple of 8
+ *   idx         device int32 [n], in any order
+ *   base        device [n, out_features], rows base_stride elements apart, or
+ *               NULL (zeros); may be out itself
+ *   out         device [n, out_features] (out), rows out_stride elements apart;
+ *               overlaps neither x nor (unless it is base) base, from the first
+ *               row to the last
+ *   ws          device workspace (16-byte aligned) of at least
+ *               moe_lora_workspace_bytes(cfg, n) bytes; it need not be cleared,
+ *               and keeps nothing between calls
+ * base and out are aligned to their element.  fp32 sums; A_e x[t] enters the
+ * second product in 16 bits of precision for outputs of 16 bits, in 24 for
+ * fp32 outputs; one rounding to out_type, after the addition of base.
+ * x, base and out may also be pinned host memory; n == 0 is a no-op.
+ * Errors: MOE_ERR_NULL, MOE_ERR_INVALID_CONFIG, MOE_ERR_UNSUPPORTED (a rank
+ * over 128, more than 1024 adapters, 2^20 in_features or 2^28 out_features),
+ * MOE_ERR_WORKSPACE, MOE_ERR_ALIGNMENT, MOE_ERR_ALIAS, MOE_ERR_HOST_MEMORY,
+ * MOE_ERR_CUDA. */
+moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b, const float* scale, const void* x,
+                      int64_t x_stride, const int32_t* idx, int32_t n, const void* base, int64_t base_stride, void* out,
+                      int64_t out_stride, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char* moe_status_string(moe_status_t status);
 

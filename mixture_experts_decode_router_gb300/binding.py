@@ -48,7 +48,7 @@ MOE_PATH_GROUPED = 2
 # Every function include/moe.h declares.
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_experts", "moe_forward",
             "moe_forward_timed", "moe_forward_static_ws", "moe_static_workspace_check",
-            "moe_topk", "moe_matvec", "moe_workspace_check", "moe_status_string",
+            "moe_topk", "moe_matvec", "moe_norm", "moe_lora_workspace_bytes", "moe_lora", "moe_workspace_check", "moe_status_string",
             "moe_abi_version")
 
 MOE_STATIC_WORKSPACE_BYTES = 16 << 20
@@ -97,6 +97,19 @@ class moe_matvec_config_t(ctypes.Structure):
     _fields_ = [("out_features", ctypes.c_int32), ("in_features", ctypes.c_int32),
                 ("w_fmt", ctypes.c_int32), ("x_type", ctypes.c_int32),
                 ("out_type", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class moe_norm_config_t(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("residual_type", ctypes.c_int32), ("weight_type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("scale_group", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class moe_lora_config_t(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("num_adapters", ctypes.c_int32),
+                ("x_type", ctypes.c_int32), ("out_type", ctypes.c_int32)]
 
 
 def MOE_ROUTING(mode: int, groups: int, kept: int, score: int) -> int:
@@ -148,6 +161,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.moe_matvec.argtypes = [ctypes.POINTER(moe_matvec_config_t), ctypes.POINTER(moe_qmat_t), P, P,
                                I64, I32, P, I64, P]
     lib.moe_matvec.restype = ctypes.c_int
+    lib.moe_norm.argtypes = [ctypes.POINTER(moe_norm_config_t), P, I64, P, I64, P, I32, P, I64, P, I64, P, I64, P, P]
+    lib.moe_norm.restype = ctypes.c_int
+    lib.moe_lora_workspace_bytes.argtypes = [ctypes.POINTER(moe_lora_config_t), I32]
+    lib.moe_lora_workspace_bytes.restype = S
+    lib.moe_lora.argtypes = [ctypes.POINTER(moe_lora_config_t), P, P, P, P, I64, P, I32, P, I64, P, I64, P, S, P]
+    lib.moe_lora.restype = ctypes.c_int
     lib.moe_status_string.argtypes = [ctypes.c_int]
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_abi_version.argtypes = []
@@ -245,6 +264,22 @@ def moe_matvec(cfg, w, bias, x, x_stride, n, out, out_stride, stream=None) -> in
                              int(out_stride), _stream(stream))
 
 
+def moe_norm(cfg, x, x_stride, residual, residual_stride, weight, n, residual_out, residual_out_stride, out, out_stride,
+             out8, out8_stride, scale8, stream=None) -> int:
+    return load().moe_norm(_ref(cfg), _ptr(x), int(x_stride), _ptr(residual), int(residual_stride), _ptr(weight), int(n),
+                           _ptr(residual_out), int(residual_out_stride), _ptr(out), int(out_stride), _ptr(out8),
+                           int(out8_stride), _ptr(scale8), _stream(stream))
+
+
+def moe_lora_workspace_bytes(cfg: moe_lora_config_t, max_rows: int) -> int:
+    return load().moe_lora_workspace_bytes(_ref(cfg), int(max_rows))
+
+
+def moe_lora(cfg, a, b, scale, x, x_stride, idx, n, base, base_stride, out, out_stride, ws, ws_bytes, stream=None) -> int:
+    return load().moe_lora(_ref(cfg), _ptr(a), _ptr(b), _ptr(scale), _ptr(x), int(x_stride), _ptr(idx), int(n), _ptr(base),
+                           int(base_stride), _ptr(out), int(out_stride), _ptr(ws), int(ws_bytes), _stream(stream))
+
+
 def moe_workspace_check(ws, ws_bytes, stream=None):
     """(status, device error word); reads and clears the word, syncing the stream."""
     v = ctypes.c_int32(0)
@@ -268,7 +303,7 @@ _ext = None
 
 
 def tensor_calls():
-    """The extension module whose topk, matvec, experts and forward take torch tensors."""
+    """The extension module whose topk, matvec, experts, forward, norm and lora take torch tensors."""
     global _ext
     if _ext is None:
         import importlib.machinery
@@ -280,7 +315,8 @@ def tensor_calls():
             "_moe_torch", path, loader=importlib.machinery.ExtensionFileLoader("_moe_torch", path))
         ext = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ext)
-        addr = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in ("moe_topk", "moe_matvec", "moe_experts", "moe_forward")]
+        addr = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                for f in ("moe_topk", "moe_matvec", "moe_experts", "moe_forward", "moe_norm", "moe_lora_workspace_bytes", "moe_lora")]
         ext.bind(*addr, check)
         _ext = ext
     return _ext

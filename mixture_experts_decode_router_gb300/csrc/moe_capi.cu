@@ -830,6 +830,131 @@ moe_status_t moe_matvec(const moe_matvec_config_t* cfg, const moe_qmat_t* w, con
                ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// Rows of a caller's matrix: n of `cols` elements of `size` bytes, `stride` elements apart.
+struct RowsArg {
+    const void* p;
+    int64_t stride;
+    int64_t n, cols;
+    size_t size;
+};
+static constexpr int64_t kMaxStride = (int64_t)1 << 40;
+static uintptr_t begin_of(const RowsArg& a) { return reinterpret_cast<uintptr_t>(a.p); }
+static uintptr_t end_of(const RowsArg& a) { return begin_of(a) + ((size_t)(a.n - 1) * a.stride + a.cols) * a.size; }
+static bool overlap(const RowsArg& a, const RowsArg& b) {
+    return a.p && b.p && begin_of(a) < end_of(b) && begin_of(b) < end_of(a);
+}
+static bool same_rows(const RowsArg& a, const RowsArg& b) {
+    return a.p == b.p && a.size == b.size && (a.stride == b.stride || a.n == 1);
+}
+
+static bool finite_f(float v) { return v >= -3.0e38f && v <= 3.0e38f; }
+
+moe_status_t moe_norm(const moe_norm_config_t* cfg, const void* x, int64_t x_stride, const void* residual,
+                      int64_t residual_stride, const void* weight, int32_t n, void* residual_out,
+                      int64_t residual_out_stride, void* out, int64_t out_stride, void* out8, int64_t out8_stride,
+                      float* scale8, moe_stream_t stream) {
+    if (!cfg) return MOE_ERR_NULL;
+    const int H = cfg->hidden;
+    auto type_ok = [](int t) { return t >= MOE_F32 && t <= MOE_F16; };
+    if (H < 1 || n < 0 || !type_ok(cfg->x_type)) return MOE_ERR_INVALID_CONFIG;
+    if (residual && (!type_ok(cfg->residual_type) || (cfg->residual_type != cfg->x_type && cfg->residual_type != MOE_F32)))
+        return MOE_ERR_INVALID_CONFIG;
+    if ((weight && !type_ok(cfg->weight_type)) || (out && !type_ok(cfg->out_type))) return MOE_ERR_INVALID_CONFIG;
+    if (out8 && cfg->scale_group != 0 && cfg->scale_group != 128) return MOE_ERR_INVALID_CONFIG;
+    if (!(cfg->eps >= 0.f && cfg->eps <= 3.0e38f) || !finite_f(cfg->weight_offset)) return MOE_ERR_INVALID_CONFIG;
+    if (H > kNormMaxHidden) return MOE_ERR_UNSUPPORTED;
+    if (residual_out && !residual) return MOE_ERR_INVALID_CONFIG;
+    if (n == 0) return MOE_OK;
+    if (!x || (!out && !out8) || (out8 && !scale8)) return MOE_ERR_NULL;
+    auto bytes = [](int t) { return (size_t)(t == MOE_F32 ? 4 : 2); };
+    const RowsArg X{x, x_stride, n, H, bytes(cfg->x_type)}, R{residual, residual_stride, n, H, bytes(cfg->residual_type)},
+        W{weight, H, 1, H, bytes(cfg->weight_type)}, RO{residual_out, residual_out_stride, n, H, bytes(cfg->residual_type)},
+        Y{out, out_stride, n, H, bytes(cfg->out_type)}, Q{out8, out8_stride, n, H, 1};
+    const int64_t n_scales = cfg->scale_group ? (H + 127) / 128 : 1;
+    const RowsArg S{out8 ? scale8 : nullptr, n_scales, n, n_scales, sizeof(float)};
+    const RowsArg* all[] = {&X, &R, &W, &RO, &Y, &Q, &S};
+    for (const RowsArg* a : all) {
+        if (!a->p) continue;
+        if (a->stride < a->cols || a->stride > kMaxStride) return MOE_ERR_INVALID_CONFIG;
+        if (begin_of(*a) % a->size) return MOE_ERR_ALIGNMENT;
+    }
+    // Each output on its own, but for an output in place: residual_out over residual, out over x.
+    const RowsArg *outs[] = {&RO, &Y, &Q, &S}, *ins[] = {&X, &R, &W};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 3; ++j)
+            if (overlap(*outs[i], *ins[j]) &&
+                !(((i == 0 && j == 1) || (i == 1 && j == 0 && cfg->out_type == cfg->x_type)) && same_rows(*outs[i], *ins[j])))
+                return MOE_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(*outs[i], *outs[j])) return MOE_ERR_ALIAS;
+    }
+    for (const RowsArg* a : all)
+        if (a->p && a != &W && residency(a->p) < 0) return MOE_ERR_HOST_MEMORY;
+    NormParams p{};
+    p.x = x; p.res = residual; p.w = weight;
+    p.x_type = cfg->x_type; p.res_type = cfg->residual_type; p.w_type = cfg->weight_type; p.out_type = cfg->out_type;
+    p.x_stride = x_stride; p.res_stride = residual_stride; p.res_out_stride = residual_out_stride;
+    p.out_stride = out_stride; p.out8_stride = out8_stride;
+    p.res_out = residual_out; p.out = out;
+    p.out8 = static_cast<uint8_t*>(out8);
+    p.scale8 = scale8;
+    p.n = n; p.H = H; p.n_scales = (int)n_scales;
+    p.group = cfg->scale_group != 0;
+    p.eps = cfg->eps; p.w_offset = cfg->weight_offset;
+    return launch_norm(p, device_sm_count(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+static moe_status_t check_lora(const moe_lora_config_t* c) {
+    if (!c) return MOE_ERR_NULL;
+    if (c->in_features < 8 || c->in_features % 8 || c->out_features < 1 || c->rank < 8 || c->rank % 8 || c->num_adapters < 1)
+        return MOE_ERR_INVALID_CONFIG;
+    if ((c->x_type != MOE_BF16 && c->x_type != MOE_F16) || c->out_type < MOE_F32 || c->out_type > MOE_F16)
+        return MOE_ERR_INVALID_CONFIG;
+    if (c->rank > 128 || c->num_adapters > kMaxExperts || c->in_features > 1 << 20 || c->out_features > 1 << 28)
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows) {
+    if (check_lora(cfg) != MOE_OK || max_rows < 0) return 0;
+    return lora_workspace(max_rows, cfg->num_adapters);
+}
+
+moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b, const float* scale, const void* x,
+                      int64_t x_stride, const int32_t* idx, int32_t n, const void* base, int64_t base_stride, void* out,
+                      int64_t out_stride, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    const moe_status_t s = check_lora(cfg);
+    if (s != MOE_OK) return s;
+    const int K = cfg->in_features, O = cfg->out_features;
+    if (n < 0) return MOE_ERR_INVALID_CONFIG;
+    if (!a || !b) return MOE_ERR_NULL;
+    if (!aligned16(a) || !aligned16(b) || !aligned4(scale)) return MOE_ERR_ALIGNMENT;
+    if (n == 0) return MOE_OK;
+    if (!x || !idx || !out || !ws) return MOE_ERR_NULL;
+    const size_t osize = cfg->out_type == MOE_F32 ? 4 : 2;
+    const RowsArg X{x, x_stride, n, K, 2}, Y0{base, base_stride, n, O, osize}, Y{out, out_stride, n, O, osize};
+    for (const RowsArg* r : {&X, &Y0, &Y})
+        if (r->p && (r->stride < r->cols || r->stride > kMaxStride)) return MOE_ERR_INVALID_CONFIG;
+    if (!aligned16(x) || x_stride % 8 || begin_of(Y0) % osize || begin_of(Y) % osize || !aligned4(idx) || !aligned16(ws))
+        return MOE_ERR_ALIGNMENT;
+    if (overlap(X, Y) || (overlap(Y0, Y) && !same_rows(Y0, Y))) return MOE_ERR_ALIAS;
+    if (ws_bytes < lora_workspace(n, cfg->num_adapters)) return MOE_ERR_WORKSPACE;
+    for (const RowsArg* r : {&X, &Y0, &Y})
+        if (r->p && residency(r->p) < 0) return MOE_ERR_HOST_MEMORY;
+    LoraParams p{};
+    p.a = static_cast<const uint16_t*>(a);
+    p.b = static_cast<const uint16_t*>(b);
+    p.scale = scale;
+    p.x = static_cast<const uint16_t*>(x);
+    p.idx = idx;
+    p.base = base;
+    p.out = out;
+    p.x_stride = x_stride; p.base_stride = base_stride; p.out_stride = out_stride;
+    p.n = n; p.K = K; p.O = O; p.r = cfg->rank; p.L = cfg->num_adapters; p.out_type = cfg->out_type;
+    return launch_lora(p, cfg->x_type, ws, device_sm_count(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK : MOE_ERR_CUDA;
+}
+
 moe_status_t moe_workspace_check(void* ws, size_t ws_bytes, int32_t* device_error, moe_stream_t stream) {
     if (!ws || !device_error) return MOE_ERR_NULL;
     if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;

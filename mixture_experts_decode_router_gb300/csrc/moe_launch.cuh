@@ -195,6 +195,40 @@ struct MatvecParams {
 bool matvec_fits(int K);   // whether a row of x fits beside the kernel's rings
 cudaError_t launch_matvec(int fmt, int x_type, const MatvecParams& p, int num_sms, cudaStream_t st);
 
+// Residual addition and RMSNorm of rows (moe_norm.cu).  Strides in elements.
+constexpr int kNormMaxHidden = 32768;
+struct NormParams {
+    const void *x, *res, *w;   // res, w may be null
+    int x_type, res_type, w_type, out_type;
+    int64_t x_stride, res_stride, res_out_stride, out_stride, out8_stride;
+    void *res_out, *out;       // may be null
+    uint8_t* out8;             // may be null
+    float* scale8;             // [n, n_scales]
+    int n, H, n_scales;
+    int group;                 // a scale for each 128 elements (else for the row)
+    float eps, w_offset;
+};
+cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t st);
+
+// Low-rank adapters of rows (moe_lora.cu).  Strides in elements.
+struct LoraParams {
+    const uint16_t *a, *b;     // [L, r, K], [L, O, r]
+    const float* scale;        // [L] or null
+    const uint16_t* x;
+    const int32_t* idx;        // [n]
+    const void* base;          // or null
+    void* out;
+    int64_t x_stride, base_stride, out_stride;
+    int n, K, O, r, L, out_type;
+    // Set by launch_lora.
+    bool vec;                  // rows of base and out start at multiples of four elements
+    bool copy;                 // rows without an adapter are to be written
+    const int32_t *segs, *perm;   // the rows sorted by adapter, or null
+    const Ctrl* ctrl;
+};
+size_t lora_workspace(int64_t n, int L);
+cudaError_t launch_lora(const LoraParams& p, int x_type, void* ws, int num_sms, cudaStream_t st);
+
 // tile: routes of a segment at most.
 cudaError_t launch_group(const int32_t* idx, int nk, int E, int tile, int e_begin, int e_end, int32_t* counts,
                          int32_t* offsets, int32_t* perm, int32_t* inv, int32_t* active, int32_t* segs,

@@ -1,0 +1,436 @@
+// moe_lora.cu -- low-rank adapters of many requests beside a shared projection (sm_103a):
+//   out[t] = base[t] + scale[a] B_a (A_a x[t]),  a = idx[t];  out[t] = base[t] where a is no adapter
+//
+// Few rows: bound by the bytes of the adapters that occur and by latency.  One cluster takes up
+// to eight rows that share an adapter, so that the adapter's matrices are read once for them:
+// its blocks split K for v = A x (each warp's products m16n8k16 with A as the rows and the
+// eight x as the columns, 16-byte loads straight into the fragments), add their partial v over
+// distributed shared memory, and split the outputs for B v.  No workspace and one launch.
+//
+// Exactness: products of 16-bit elements are exact in fp32 and summed there.  v enters the
+// second product as a sum of 16-bit parts: two for outputs of 16 bits (16 bits of v, below the
+// output's own rounding), three for fp32 outputs (24 bits of v).  fp16 parts are those of v
+// times a power of two for each row, which takes its largest element to [2^14, 2^15).
+#include <algorithm>
+#include <mutex>
+
+#include "moe_launch.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kRows = 8;           // rows of a cluster (the n of the products)
+constexpr int kScanRows = 512;     // rows whose adapters a block can go through by itself
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// A float of block `rank`'s shared memory, at this block's address p.
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), b;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(b) : "memory");
+    return v;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (kBf16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// v as a sum of `kParts` 16-bit numbers; an infinity (or what rounds to one) and a NaN have one part.
+template <bool kBf16, int kParts> __device__ __forceinline__ void split(float v, uint16_t (&part)[kParts]) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        float f;
+        if constexpr (kBf16) {
+            const __nv_bfloat16 b = __float2bfloat16_rn(v);
+            part[i] = __bfloat16_as_ushort(b);
+            f = __bfloat162float(b);
+        } else {
+            const __half b = __float2half_rn(v);
+            part[i] = __half_as_ushort(b);
+            f = __half2float(b);
+        }
+        v = fabsf(f) < INFINITY ? v - f : 0.f;
+    }
+}
+
+// Four consecutive elements of a row of base or out.
+__device__ __forceinline__ void load4(int type, const void* p, int64_t at, int left, bool vec, float (&v)[4]) {
+    if (type == MOE_F32) {
+        const float* f = reinterpret_cast<const float*>(p) + at;
+        if (vec) {
+            const float4 q = *reinterpret_cast<const float4*>(f);
+            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = i < left ? f[i] : 0.f;
+        }
+        return;
+    }
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p) + at;
+    uint32_t u[2];
+    if (vec) {
+        const uint2 q = *reinterpret_cast<const uint2*>(h);
+        u[0] = q.x; u[1] = q.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) u[i] = (2 * i < left ? h[2 * i] : 0u) | ((2 * i + 1 < left ? (uint32_t)h[2 * i + 1] : 0u) << 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (type == MOE_BF16) {
+            v[2 * i] = bf16_lo(u[i]);
+            v[2 * i + 1] = bf16_hi(u[i]);
+        } else {
+            const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+            v[2 * i] = q.x;
+            v[2 * i + 1] = q.y;
+        }
+    }
+}
+__device__ __forceinline__ void store4(int type, void* p, int64_t at, int left, bool vec, const float (&v)[4]) {
+    if (type == MOE_F32) {
+        float* f = reinterpret_cast<float*>(p) + at;
+        if (vec) {
+            *reinterpret_cast<float4*>(f) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) f[i] = v[i];
+        }
+        return;
+    }
+    uint32_t u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (type == MOE_BF16) {
+            const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&q);
+        } else {
+            const __half2 q = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+    }
+    uint16_t* h = reinterpret_cast<uint16_t*>(p) + at;
+    if (vec) {
+        *reinterpret_cast<uint2*>(h) = make_uint2(u[0], u[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) h[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+// out[row] = base[row] (zeros without a base), the block's part `part` of `parts`.
+__device__ __forceinline__ void copy_row(const LoraParams& p, int64_t row, int part, int parts) {
+    const int quads = (p.O + 3) / 4;
+    for (int q = part * kThreads + threadIdx.x; q < quads; q += parts * kThreads) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        const int left = p.O - 4 * q;
+        const bool vec = p.vec && left >= 4;
+        if (p.base) load4(p.out_type, p.base, row * p.base_stride + 4 * q, left, vec, v);
+        store4(p.out_type, p.out, row * p.out_stride + 4 * q, left, vec, v);
+    }
+}
+
+// kRT: tiles of 16 of the rank.  kParts: parts of v.
+template <bool kBf16, int kRT, int kParts>
+__global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p) {
+    constexpr int kR = kRT * 16;
+    __shared__ float s_part[kWarps][kR][kRows];   // then v, [row][rank]
+    __shared__ float s_mine[kR * kRows];
+    __shared__ int32_t s_idx[kScanRows];
+    __shared__ int s_rows[kRows], s_count;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int C = (int)cluster_size(), c = (int)cluster_rank(), group = blockIdx.x / C;
+    pdl_wait();
+
+    // The cluster's rows: row `group`, if an adapter's rows before it fill whole clusters, and
+    // the next ones of its adapter; or a run of the rows sorted by adapter.
+    int adapter, count;
+    if (p.segs) {
+        if (group >= p.ctrl->n_rsegs) return;
+        adapter = p.segs[3 * group];
+        count = p.segs[3 * group + 2];
+        if (tid < count) s_rows[tid] = p.perm[p.segs[3 * group + 1] + tid];
+    } else {
+        for (int i = tid; i < p.n; i += kThreads) s_idx[i] = p.idx[i];
+        __syncthreads();
+        adapter = s_idx[group];
+        if (adapter < 0 || adapter >= p.L) {
+            if (p.copy) copy_row(p, group, c, C);
+            return;
+        }
+        int before = 0;
+        for (int i0 = 0; i0 < group; i0 += kThreads)
+            before += __syncthreads_count(i0 + tid < group && s_idx[i0 + tid] == adapter);
+        if (before % kRows) return;
+        if (warp == 0) {
+            int found = 0;
+            for (int i0 = group; i0 < p.n && found < kRows; i0 += 32) {
+                const bool same = i0 + lane < p.n && s_idx[i0 + lane] == adapter;
+                const uint32_t all = __ballot_sync(0xffffffffu, same);
+                const int at = found + __popc(all & ((1u << lane) - 1));
+                if (same && at < kRows) s_rows[at] = i0 + lane;
+                found += __popc(all);
+            }
+            if (lane == 0) s_count = min(found, kRows);
+        }
+        __syncthreads();
+        count = s_count;
+    }
+    __syncthreads();
+
+    // v = A x: lane (g, t) holds elements 8 t .. 8 t + 7 of a step of 32 along K, of the rows g and
+    // g + 8 of each tile and of x's row g.  (The products' order of k is any, the same for both.)
+    const int K = p.K, r = p.r;
+    const uint16_t* A = p.a + (int64_t)adapter * r * K;
+    const uint16_t* x = g < count ? p.x + (int64_t)s_rows[g] * p.x_stride : nullptr;
+    const int steps = (K + 31) / 32, per = (steps + C - 1) / C, s1 = min(steps, (c + 1) * per);
+    float acc[kRT][4];
+#pragma unroll
+    for (int j = 0; j < kRT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    constexpr int kU = kRT >= 4 ? 1 : 4 / kRT;   // steps in flight
+    for (int s = c * per + warp; s < s1; s += kU * kWarps) {
+        uint4 xv[kU], av[kU][kRT][2];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int su = s + u * kWarps, k = su * 32 + t * 8;
+            const bool in = su < s1 && k < K;
+            xv[u] = in && x ? __ldg(reinterpret_cast<const uint4*>(x + k)) : zero;
+#pragma unroll
+            for (int j = 0; j < kRT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = j * 16 + i * 8 + g;
+                    av[u][j][i] = in && row < r ? ld_stream_v4(A + (int64_t)row * K + k) : zero;
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int j = 0; j < kRT; ++j) {
+                mma<kBf16>(acc[j], av[u][j][0].x, av[u][j][1].x, av[u][j][0].y, av[u][j][1].y, xv[u].x, xv[u].y);
+                mma<kBf16>(acc[j], av[u][j][0].z, av[u][j][1].z, av[u][j][0].w, av[u][j][1].w, xv[u].z, xv[u].w);
+            }
+    }
+#pragma unroll
+    for (int j = 0; j < kRT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float2*>(&s_part[warp][j * 16 + i * 8 + g][2 * t]) = make_float2(acc[j][2 * i], acc[j][2 * i + 1]);
+    __syncthreads();
+    for (int e = tid; e < kR * kRows; e += kThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s += (&s_part[w][0][0])[e];
+        s_mine[e] = s;
+    }
+    cluster_arrive();
+    cluster_wait();
+    float* s_v = &s_part[0][0][0];   // [kRows][kR]
+    const float scale = p.scale ? __ldg(p.scale + adapter) : 1.f;
+    for (int e = tid; e < kR * kRows; e += kThreads) {
+        float s = 0.f;
+        for (int b = 0; b < C; ++b) s += ld_cluster(&s_mine[e], b);
+        // (Rows behind the rank are 0, not what a 0 weight makes of an infinity.)
+        s_v[(e % kRows) * kR + e / kRows] = e / kRows < r ? s * scale : 0.f;
+    }
+    cluster_arrive();   // (the others' sums are read; waited for before the block ends)
+    __syncthreads();
+
+    // out = base + B v: v is the columns' operand, its parts in registers; lane (g, t) holds
+    // elements 4 t .. 4 t + 3 of a step of 16 along the rank.
+    uint32_t vb[kRT][kParts][2];
+    int e = 0;
+    if constexpr (!kBf16) {
+        float most = 0.f;
+        for (int k = t; k < kR; k += 4) most = fmaxf(most, finite_abs(s_v[g * kR + k]));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        e = f16_shift(most);
+    }
+#pragma unroll
+    for (int j = 0; j < kRT; ++j) {
+        uint16_t q[4][kParts];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float v = s_v[g * kR + j * 16 + 4 * t + i];
+            split<kBf16, kParts>(kBf16 ? v : times_exp2(v, e), q[i]);
+        }
+#pragma unroll
+        for (int m = 0; m < kParts; ++m) {
+            vb[j][m][0] = q[0][m] | ((uint32_t)q[1][m] << 16);
+            vb[j][m][1] = q[2][m] | ((uint32_t)q[3][m] << 16);
+        }
+    }
+    // This lane's results are those of rows 2 t and 2 t + 1.
+    const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
+    int64_t orow[2];
+    bool has[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        has[m] = 2 * t + m < count;
+        orow[m] = has[m] ? s_rows[2 * t + m] : 0;
+    }
+    const int O = p.O, units = (O + 31) / 32, uper = (units + C - 1) / C, u1 = min(units, (c + 1) * uper);
+    const uint16_t* Bm = p.b + (int64_t)adapter * O * r;
+    for (int u = c * uper + warp; u < u1; u += kWarps) {
+        // Outputs o .. o + 3 of this lane: rows g and g + 8 of two tiles.
+        const int o = u * 32 + 4 * g, left = O - o;
+        const bool vec = p.vec && left >= 4;
+        uint2 bv[kRT][2][2];
+#pragma unroll
+        for (int j = 0; j < kRT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool in = i < left && j * 16 + 4 * t < r;
+                bv[j][i >> 1][i & 1] = in ? ld_stream_v2(Bm + (int64_t)(o + i) * r + j * 16 + 4 * t) : make_uint2(0u, 0u);
+            }
+        float was[2][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) was[m][i] = 0.f;
+            if (p.base && has[m] && left > 0) load4(p.out_type, p.base, orow[m] * p.base_stride + o, left, vec, was[m]);
+        }
+        float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int j = 0; j < kRT; ++j)
+#pragma unroll
+            for (int m = kParts - 1; m >= 0; --m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    mma<kBf16>(d[h], bv[j][h][0].x, bv[j][h][1].x, bv[j][h][0].y, bv[j][h][1].y, vb[j][m][0], vb[j][m][1]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (!has[m] || left <= 0) continue;
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v = d[i >> 1][2 * (i & 1) + m];
+                if constexpr (!kBf16) v = times_exp2(v, -(m ? e1 : e0));
+                y[i] = was[m][i] + v;
+            }
+            store4(p.out_type, p.out, orow[m] * p.out_stride + o, left, vec, y);
+        }
+    }
+    pdl_trigger();
+    cluster_wait();
+}
+
+// Rows without an adapter, when the rows go by the sorted order.
+__global__ void __launch_bounds__(kThreads) lora_copy_kernel(const LoraParams p) {
+    pdl_wait();
+    for (int64_t row = blockIdx.x; row < p.n; row += gridDim.x) {
+        const int a = p.idx[row];
+        if (a < 0 || a >= p.L) copy_row(p, row, 0, 1);
+    }
+    pdl_trigger();
+}
+
+template <bool kBf16, int kRT, int kParts>
+cudaError_t launch_rows(const LoraParams& p, int groups, int cluster, cudaStream_t st) {
+    auto kern = lora_rows_kernel<kBf16, kRT, kParts>;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)groups * cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <bool kBf16, int kParts>
+cudaError_t launch_rank(const LoraParams& p, int groups, int cluster, cudaStream_t st) {
+    if (p.r <= 16) return launch_rows<kBf16, 1, kParts>(p, groups, cluster, st);
+    if (p.r <= 32) return launch_rows<kBf16, 2, kParts>(p, groups, cluster, st);
+    if (p.r <= 64) return launch_rows<kBf16, 4, kParts>(p, groups, cluster, st);
+    return launch_rows<kBf16, 8, kParts>(p, groups, cluster, st);
+}
+
+cudaError_t launch_all(const LoraParams& p, int x_type, int groups, int cluster, cudaStream_t st) {
+    const bool three = p.out_type == MOE_F32;
+    if (x_type == MOE_BF16) return three ? launch_rank<true, 3>(p, groups, cluster, st) : launch_rank<true, 2>(p, groups, cluster, st);
+    return three ? launch_rank<false, 3>(p, groups, cluster, st) : launch_rank<false, 2>(p, groups, cluster, st);
+}
+
+struct Layout {
+    size_t counts, offsets, perm, inv, active, segs, total;
+    int64_t max_segs;
+};
+Layout layout(int64_t n, int L) {
+    Layout l{};
+    size_t off = sizeof(Ctrl);
+    auto take = [&](size_t bytes) { const size_t o = off; off = align_up(off + bytes, 256); return o; };
+    if (n > kScanRows) {
+        l.max_segs = n / kRows + std::min<int64_t>(n, L) + 1;
+        l.counts = take(sizeof(int32_t) * L);
+        l.offsets = take(sizeof(int32_t) * (L + 1));
+        l.perm = take(sizeof(int32_t) * n);
+        l.inv = take(sizeof(int32_t) * n);
+        l.active = take(sizeof(int32_t) * L);
+        l.segs = take(sizeof(int32_t) * 3 * l.max_segs);
+    }
+    l.total = off;
+    return l;
+}
+
+}  // namespace
+
+size_t lora_workspace(int64_t n, int L) { return layout(n, L).total; }
+
+cudaError_t launch_lora(const LoraParams& given, int x_type, void* ws, int num_sms, cudaStream_t st) {
+    LoraParams p = given;
+    const int size = p.out_type == MOE_F32 ? 4 : 2;
+    auto rows4 = [&](const void* a, int64_t stride) { return reinterpret_cast<uintptr_t>(a) % (4 * size) == 0 && (p.n == 1 || stride % 4 == 0); };
+    p.vec = rows4(p.out, p.out_stride) && (!p.base || rows4(p.base, p.base_stride));
+    p.copy = p.base != p.out;
+    int groups = p.n, cluster = 8;
+    if (p.n > kScanRows) {
+        const Layout l = layout(p.n, p.L);
+        uint8_t* w = static_cast<uint8_t*>(ws);
+        auto at = [&](size_t o) { return reinterpret_cast<int32_t*>(w + o); };
+        p.ctrl = reinterpret_cast<Ctrl*>(w);
+        p.segs = at(l.segs);
+        p.perm = at(l.perm);
+        cudaError_t e = launch_group(p.idx, p.n, p.L, kRows, 0, p.L, at(l.counts), at(l.offsets), at(l.perm), at(l.inv), at(l.active),
+                                     at(l.segs), reinterpret_cast<Ctrl*>(w), st);
+        if (e != cudaSuccess) return e;
+        if (p.copy && (e = launch_pdl(lora_copy_kernel, dim3(std::min(p.n, num_sms * 8)), dim3(kThreads), 0, st, p)) != cudaSuccess) return e;
+        groups = (int)l.max_segs;
+        cluster = 4;
+    }
+    const cudaError_t e = launch_all(p, x_type, groups, cluster, st);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace moe

@@ -24,6 +24,9 @@ decltype(&moe_topk) g_topk;
 decltype(&moe_matvec) g_matvec;
 decltype(&moe_experts) g_experts;
 decltype(&moe_forward) g_forward;
+decltype(&moe_norm) g_norm;
+decltype(&moe_lora_workspace_bytes) g_lora_workspace_bytes;
+decltype(&moe_lora) g_lora;
 PyObject* g_check;   // raises a status's error
 
 struct Raised {};    // a Python exception is set
@@ -100,16 +103,20 @@ void need(Py_ssize_t got, Py_ssize_t want) {
     if (got != want) raise(PyExc_TypeError, "wrong number of arguments");
 }
 
-// bind(moe_topk, moe_matvec, moe_experts, moe_forward, check): the functions' addresses.
+// bind(moe_topk, moe_matvec, moe_experts, moe_forward, moe_norm, moe_lora_workspace_bytes, moe_lora, check): the
+// functions' addresses.
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-    need(n, 5);
+    need(n, 8);
     g_topk = reinterpret_cast<decltype(g_topk)>(address<void>(a[0]));
     g_matvec = reinterpret_cast<decltype(g_matvec)>(address<void>(a[1]));
     g_experts = reinterpret_cast<decltype(g_experts)>(address<void>(a[2]));
     g_forward = reinterpret_cast<decltype(g_forward)>(address<void>(a[3]));
-    Py_INCREF(a[4]);
+    g_norm = reinterpret_cast<decltype(g_norm)>(address<void>(a[4]));
+    g_lora_workspace_bytes = reinterpret_cast<decltype(g_lora_workspace_bytes)>(address<void>(a[5]));
+    g_lora = reinterpret_cast<decltype(g_lora)>(address<void>(a[6]));
+    Py_INCREF(a[7]);
     Py_XDECREF(g_check);
-    g_check = a[4];
+    g_check = a[7];
     Py_RETURN_NONE;
 }
 
@@ -294,6 +301,130 @@ PyObject* forward(PyObject* const* a, Py_ssize_t na) {
     return Py_BuildValue("(NNN)", give(out, a[5]), give(idx, a[6]), give(w, a[7]));
 }
 
+// A matrix [n, cols] of contiguous rows and its stride; `what` is said of any other.
+struct Rows {
+    void* p = nullptr;
+    int64_t stride = 0;
+};
+Rows rows_of(const at::Tensor& t, int64_t n, int64_t cols, at::ScalarType type, const char* what) {
+    if (t.dim() != 2 || t.size(0) != n || t.size(1) != cols || t.scalar_type() != type || (cols > 1 && t.stride(1) != 1))
+        raise(PyExc_ValueError, what);
+    return {t.data_ptr(), n > 1 ? t.stride(0) : cols};
+}
+at::ScalarType torch_type(int code) { return code == MOE_F32 ? at::kFloat : code == MOE_BF16 ? at::kBFloat16 : at::kHalf; }
+
+// norm(config address, weight, whether an 8-bit output is wanted, x, residual, residual_out, out, out8, scale, stream; the last
+// six may be None) -> (out, residual_out, out8, scale)
+PyObject* norm(PyObject* const* a, Py_ssize_t na) {
+    need(na, 10);
+    moe_norm_config_t c = *address<const moe_norm_config_t>(a[0]);
+    const at::Tensor& w = some_tensor(a[1]);
+    const int want8 = PyObject_IsTrue(a[2]);
+    if (want8 < 0) throw Raised{};
+    const at::Tensor &x = some_tensor(a[3]), *res = tensor(a[4]), *gro = tensor(a[5]), *gy = tensor(a[6]), *gq = tensor(a[7]),
+                     *gs = tensor(a[8]);
+    const int64_t H = c.hidden;
+    const bool want = c.out_type >= 0;
+    c.x_type = type_code(x);
+    if (c.x_type < 0) raise(PyExc_KeyError, "x is float32, bfloat16 or float16");
+    if (x.dim() != 2 || x.size(1) != H || (H > 1 && x.stride(1) != 1)) raise(PyExc_ValueError, "x is [n, hidden] with contiguous rows");
+    const int64_t n = x.size(0);
+    if (n > INT32_MAX) raise(PyExc_ValueError, "too many rows");
+    if ((gy && !want) || ((gq || gs) && !want8) || (gro && !res)) raise(PyExc_ValueError, "an output is given that is not asked for");
+    c.residual_type = res ? type_code(*res) : c.x_type;
+    if (res && c.residual_type != c.x_type && c.residual_type != MOE_F32)
+        raise(PyExc_ValueError, "residual is of x's type or float32");
+    const int64_t groups = c.scale_group ? (H + c.scale_group - 1) / c.scale_group : 1;
+    Rows R, RO, Y, Q;
+    const Rows X{x.data_ptr(), n > 1 ? x.stride(0) : H};
+    if (res) R = rows_of(*res, n, H, torch_type(c.residual_type), "residual is [n, hidden] with contiguous rows");
+    if (gro) RO = rows_of(*gro, n, H, torch_type(c.residual_type), "residual_out is [n, hidden] of the residual's type with contiguous rows");
+    if (gy) Y = rows_of(*gy, n, H, torch_type(c.out_type), "out is [n, hidden] of out_dtype with contiguous rows");
+    if (gq) Q = rows_of(*gq, n, H, at::kFloat8_e4m3fn, "out8 is float8_e4m3fn [n, hidden] with contiguous rows");
+    if (gs && (gs->dim() != 2 || gs->size(0) != n || gs->size(1) != groups || gs->scalar_type() != at::kFloat || !gs->is_contiguous()))
+        raise(PyExc_ValueError, "scale is contiguous float32 [n, groups]");
+    const int dev = current_gpu(x);
+    if (type_code(w) != c.weight_type || w.numel() != H || !w.is_contiguous())
+        raise(PyExc_ValueError, "the weight is no longer what the operator was made with");
+    if (!w.is_cuda() || w.get_device() != dev) raise(PyExc_ValueError, "the weight is not on the current device");
+    for (const at::Tensor* t : {res, gro, gy, gq, gs})
+        if (t) current_gpu(*t);
+    const moe_stream_t st = stream_of(a[9], dev);
+    at::Tensor ro, y, q, s;
+    auto make = [&](int64_t cols, at::ScalarType type, at::Tensor& t) {
+        t = matrix(n, cols, type, dev, st);
+        return Rows{t.data_ptr(), cols};
+    };
+    if (res && !gro) RO = make(H, torch_type(c.residual_type), ro);
+    if (want && !gy) Y = make(H, torch_type(c.out_type), y);
+    if (want8 && !gq) Q = make(H, at::kFloat8_e4m3fn, q);
+    float* sp = gs ? data<float>(*gs) : nullptr;
+    if (want8 && !gs) sp = static_cast<float*>(make(groups, at::kFloat, s).p);
+    const void* wp = w.data_ptr();
+    moe_status_t status;
+    Py_BEGIN_ALLOW_THREADS;
+    status = g_norm(&c, X.p, X.stride, R.p, R.stride, wp, (int32_t)n, RO.p, RO.stride, Y.p, Y.stride, Q.p, Q.stride, sp, st);
+    Py_END_ALLOW_THREADS;
+    check(status);
+    auto give = [](at::Tensor& made, PyObject* given) { return made.defined() ? wrap(std::move(made)) : Py_NewRef(given); };
+    return Py_BuildValue("(NNNN)", give(y, a[6]), give(ro, a[5]), give(q, a[7]), give(s, a[8]));
+}
+
+// lora(config address, (a, b, scale or None), the adapters' device, x, idx, base or None, out or None, stream or None) -> out
+PyObject* lora(PyObject* const* a, Py_ssize_t na) {
+    need(na, 8);
+    const moe_lora_config_t* c = address<const moe_lora_config_t>(a[0]);
+    if (!PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[1]) != 3) raise(PyExc_TypeError, "three matrices are expected");
+    const at::Tensor &wa = some_tensor(PyTuple_GET_ITEM(a[1], 0)), &wb = some_tensor(PyTuple_GET_ITEM(a[1], 1)),
+                     *scale = tensor(PyTuple_GET_ITEM(a[1], 2));
+    const long long wdev = integer(a[2]);
+    const at::Tensor &x = some_tensor(a[3]), &idx = some_tensor(a[4]), *base = tensor(a[5]), *given = tensor(a[6]);
+    const int64_t K = c->in_features, O = c->out_features;
+    if (x.dim() != 2 || x.size(1) != K || x.stride(1) != 1 || type_code(x) != c->x_type)
+        raise(PyExc_ValueError, "x is [n, in] of the adapters' type with contiguous rows");
+    const int64_t n = x.size(0);
+    if (n > INT32_MAX) raise(PyExc_ValueError, "too many rows");
+    const at::ScalarType type = torch_type(c->out_type);
+    Rows Y0, Y;
+    if (base) Y0 = rows_of(*base, n, O, type, "base is [n, out] of out_dtype with contiguous rows");
+    if (given) Y = rows_of(*given, n, O, type, "out is [n, out] of out_dtype with contiguous rows");
+    const int dev = current_gpu(x);
+    const int64_t L = c->num_adapters, r = c->rank;
+    if (type_code(wa) != c->x_type || type_code(wb) != c->x_type || wa.numel() != L * r * K || wb.numel() != L * r * O ||
+        !wa.is_contiguous() || !wb.is_contiguous() ||
+        (scale && (scale->scalar_type() != at::kFloat || scale->numel() != L || !scale->is_contiguous())))
+        raise(PyExc_ValueError, "the adapters are no longer what the operator was made with");
+    if (wdev != dev || wa.get_device() != dev || wb.get_device() != dev || (scale && scale->get_device() != dev))
+        raise(PyExc_ValueError, "the adapters are not on the current device");
+    if (idx.scalar_type() != at::kInt || idx.dim() != 1 || idx.size(0) != n || !idx.is_contiguous() || !idx.is_cuda() ||
+        idx.get_device() != dev)
+        raise(PyExc_ValueError, "idx is contiguous int32 [n] on the current device");
+    for (const at::Tensor* t : {base, given})
+        if (t) current_gpu(*t);
+    const moe_stream_t st = stream_of(a[7], dev);
+    at::Tensor out;
+    if (given) {
+        out = *given;
+    } else {
+        out = matrix(n, O, type, dev, st);
+        Y = {out.data_ptr(), O};
+    }
+    // The call's own workspace, of its stream's memory: calls on several streams share none.
+    const size_t ws_bytes = g_lora_workspace_bytes(c, (int32_t)n);
+    at::Tensor ws = matrix(1, (int64_t)ws_bytes, at::kByte, dev, st);
+    void* wp = ws.data_ptr();
+    const void *ap = wa.data_ptr(), *bp = wb.data_ptr(), *xp = x.data_ptr();
+    const float* sp = scale ? data<const float>(*scale) : nullptr;
+    const int32_t* ip = data<const int32_t>(idx);
+    const int64_t stride = n > 1 ? x.stride(0) : K;
+    moe_status_t s;
+    Py_BEGIN_ALLOW_THREADS;
+    s = g_lora(c, ap, bp, sp, xp, stride, ip, (int32_t)n, Y0.p, Y0.stride, Y.p, Y.stride, wp, ws_bytes, st);
+    Py_END_ALLOW_THREADS;
+    check(s);
+    return wrap(std::move(out));
+}
+
 // No C++ exception leaves a Python call.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -312,6 +443,8 @@ PyMethodDef methods[] = {
     {"matvec", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<matvec>)), METH_FASTCALL, nullptr},
     {"experts", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<experts>)), METH_FASTCALL, nullptr},
     {"forward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<forward>)), METH_FASTCALL, nullptr},
+    {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<norm>)), METH_FASTCALL, nullptr},
+    {"lora", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<lora>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -283,3 +283,86 @@ class MoeMatvec:
 
     def forward(self, x: torch.Tensor, out=None, stream=None):
         return self._matvec(addressof(self.c_cfg), addressof(self.c_w), self._bias, self._device, x, out, stream if stream is None else B._stream(stream))
+
+
+class MoeNorm:
+    """Residual addition and RMSNorm of rows (``moe_norm``): ``forward(x, residual)``
+    returns ``(out, residual_out, out8, scale)`` of ``x`` ``[n, hidden]`` (fp32, bf16 or
+    fp16), None for what is not asked for.
+
+    ``residual`` (optional) is of x's type or fp32: ``residual_out`` is their sum, which is
+    normalised; ``residual_out=residual`` adds in place.  ``weight`` is ``[hidden]`` (fp32,
+    bf16 or fp16), ``weight_offset`` is added to it.  ``out`` is of ``out_dtype`` (None: no
+    such output); ``out8`` is ``"group"`` (E4M3 with an fp32 scale for each 128 elements of
+    a row, ``[n, ceil(hidden / 128)]``), ``"row"`` (one scale a row, ``[n, 1]``) or None.
+    Rows may be strided.
+    """
+
+    def __init__(self, weight: torch.Tensor, eps: float = 1e-6, out_dtype: Optional[torch.dtype] = torch.bfloat16,
+                 out8: Optional[str] = None, weight_offset: float = 0.0):
+        if not isinstance(weight, torch.Tensor) or weight.dtype not in _TYPE or weight.dim() != 1 or not weight.is_contiguous():
+            raise ValueError("weight is contiguous float32, bfloat16 or float16 [hidden]")
+        if out8 not in (None, "group", "row") or (out8 is None and out_dtype is None):
+            raise ValueError('out8 is "group", "row" or None, and None only with an out_dtype')
+        c = B.moe_norm_config_t()
+        c.hidden, c.weight_type = weight.shape[0], _TYPE[weight.dtype]
+        c.out_type = -1 if out_dtype is None else _TYPE[out_dtype]
+        c.scale_group = 128 if out8 == "group" else 0
+        c.eps, c.weight_offset = eps, weight_offset
+        self.c_cfg, self._weight, self.out_dtype, self.out8 = c, weight, out_dtype, out8
+        self.hidden = weight.shape[0]
+        self._norm = B.tensor_calls().norm
+
+    @property
+    def weight(self) -> torch.Tensor:
+        return self._weight
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, residual_out=None, out=None, out8=None,
+                scale=None, stream=None):
+        return self._norm(addressof(self.c_cfg), self._weight, self.out8 is not None, x, residual, residual_out, out, out8, scale,
+                          stream if stream is None else B._stream(stream))
+
+
+class MoeLora:
+    """Low-rank adapters of many requests beside a shared projection (``moe_lora``):
+    ``forward(x, idx, base)`` returns ``base[t] + scale[e] b[e] (a[e] x[t])`` with
+    ``e = idx[t]``, and ``base[t]`` where e is no adapter (for example -1).
+
+    ``a`` ``[adapters, rank, in]`` and ``b`` ``[adapters, out, rank]`` are bf16 or fp16, as
+    ``x`` ``[n, in]`` is; ``scale`` is fp32 ``[adapters]`` or None (1).  ``idx`` is int32
+    ``[n]``.  ``base`` is the projection's ``[n, out]`` of ``out_dtype`` or None (0);
+    ``out=base`` adds in place.  Rows may be strided.
+    """
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16):
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2] or a.dtype != b.dtype \
+                or a.dtype not in (torch.bfloat16, torch.float16) or not (a.is_contiguous() and b.is_contiguous()):
+            raise ValueError("a [adapters, rank, in] and b [adapters, out, rank] are contiguous, both bfloat16 or both float16")
+        if scale is not None and (scale.dtype != torch.float32 or scale.shape != (a.shape[0],) or not scale.is_contiguous()):
+            raise ValueError("scale is contiguous float32 [adapters]")
+        dev = a.get_device()
+        if any(t is not None and t.get_device() != dev for t in (b, scale)):
+            raise ValueError("adapters and scales on one device")
+        c = B.moe_lora_config_t()
+        c.num_adapters, c.rank, c.in_features = a.shape
+        c.out_features, c.x_type, c.out_type = b.shape[1], _TYPE[a.dtype], _TYPE[out_dtype]
+        if B.moe_lora_workspace_bytes(c, 0) == 0:
+            raise B.MoeError("invalid adapters: the rank is a multiple of 8 up to 128, in of 8, and there are at most 1024")
+        self.c_cfg, self._held, self.out_dtype, self._device = c, (a, b, scale), out_dtype, dev
+        self._lora = B.tensor_calls().lora
+
+    @property
+    def a(self) -> torch.Tensor:
+        return self._held[0]
+
+    @property
+    def b(self) -> torch.Tensor:
+        return self._held[1]
+
+    @property
+    def scale(self) -> Optional[torch.Tensor]:
+        return self._held[2]
+
+    def forward(self, x: torch.Tensor, idx: torch.Tensor, base: Optional[torch.Tensor] = None, out=None, stream=None):
+        return self._lora(addressof(self.c_cfg), self._held, self._device, x, idx, base, out,
+                          stream if stream is None else B._stream(stream))
