@@ -951,13 +951,14 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// 2-D map over a row-major [rows, cols] matrix of `esize`-byte elements.
+// 2-D map over a row-major [rows, cols] matrix of `esize`-byte elements, rows `stride` elements apart
+// (0: cols).
 bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t cols,
-              uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+              uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle, uint64_t stride) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {cols * esize};
+    const cuuint64_t strides[1] = {(stride ? stride : cols) * esize};
     const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

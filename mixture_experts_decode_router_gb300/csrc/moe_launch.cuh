@@ -4,6 +4,8 @@
 
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -166,9 +168,10 @@ cudaError_t launch_router_tc(const uint16_t* x, int n, int H, const uint16_t* wr
 // for the tensor-core router, which multiplies its partials by scale2.
 cudaError_t launch_router_nvfp4_expand(const QMatDev& wq, int E, int H, uint16_t* out, bool early, int num_sms,
                                        cudaStream_t st);
-// 2-D TMA map over a row-major [rows, cols] matrix of `esize`-byte elements (moe_grouped_tc.cu).
+// 2-D TMA map over a row-major [rows, cols] matrix of `esize`-byte elements, rows `stride` elements
+// apart (0: cols) (moe_grouped_tc.cu).
 bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t cols,
-              uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
+              uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle, uint64_t stride = 0);
 cudaError_t launch_router_nvfp4(const uint16_t* x, int n, int H, const QMatDev& wq, int E, float* logits,
                                 cudaStream_t st);
 // logits: ns partial rows per token ([ns][n][E], ns = 1 for a plain logit
@@ -210,7 +213,7 @@ struct NormParams {
 };
 cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t st);
 
-// Low-rank adapters of rows (moe_lora.cu).  Strides in elements.
+// Low-rank adapters of rows (moe_lora.cu; many rows: moe_lora_tc.cu).  Strides in elements.
 struct LoraParams {
     const uint16_t *a, *b;     // [L, r, K], [L, O, r]
     const float* scale;        // [L] or null
@@ -220,14 +223,28 @@ struct LoraParams {
     void* out;
     int64_t x_stride, base_stride, out_stride;
     int n, K, O, r, L, out_type;
+    bool x_host;               // x is pinned host memory
     // Set by launch_lora.
-    bool vec;                  // rows of base and out start at multiples of four elements
+    int vec;                   // elements of base's and out's rows that can be read at once: 8, 4 or 1
     bool copy;                 // rows without an adapter are to be written
-    const int32_t *segs, *perm;   // the rows sorted by adapter, or null
+    // The rows sorted by adapter, or null: runs (adapter, or -1 for none; first position; rows), the
+    // runs of adapters before those of none.  ctrl->n_active runs of adapters, n_rsegs in all.
+    const int32_t *segs, *perm;
     const Ctrl* ctrl;
 };
-size_t lora_workspace(int64_t n, int L);
+size_t lora_workspace(int64_t n, int L, int r);
 cudaError_t launch_lora(const LoraParams& p, int x_type, void* ws, int num_sms, cudaStream_t st);
+// Runs of at most 128 rows through the tensor cores' kernels, v's partial sums [splits][n][r] in part.
+constexpr int kLoraTile = 128;
+constexpr int kLoraBlocks = 304;      // blocks that a call aims at
+constexpr int kLoraMaxSplits = 8;
+inline int64_t lora_part_rows(int64_t n) {   // of splits * n, and of every smaller n's
+    return std::min<int64_t>(kLoraMaxSplits * n, (int64_t)kLoraBlocks * kLoraTile + 2 * n);
+}
+// Whether the tensor maps of a call can be made; `maps` receives them (x, A, B).
+bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[3]);
+cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[3], float* part, int32_t* err, int max_segs,
+                           cudaStream_t st);
 
 // tile: routes of a segment at most.
 cudaError_t launch_group(const int32_t* idx, int nk, int E, int tile, int e_begin, int e_end, int32_t* counts,

@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "moe_launch.cuh"
+#include "moe_lora.cuh"
 
 namespace moe {
 
@@ -55,98 +56,13 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// v as a sum of `kParts` 16-bit numbers; an infinity (or what rounds to one) and a NaN have one part.
-template <bool kBf16, int kParts> __device__ __forceinline__ void split(float v, uint16_t (&part)[kParts]) {
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) {
-        float f;
-        if constexpr (kBf16) {
-            const __nv_bfloat16 b = __float2bfloat16_rn(v);
-            part[i] = __bfloat16_as_ushort(b);
-            f = __bfloat162float(b);
-        } else {
-            const __half b = __float2half_rn(v);
-            part[i] = __half_as_ushort(b);
-            f = __half2float(b);
-        }
-        v = fabsf(f) < INFINITY ? v - f : 0.f;
-    }
-}
-
-// Four consecutive elements of a row of base or out.
-__device__ __forceinline__ void load4(int type, const void* p, int64_t at, int left, bool vec, float (&v)[4]) {
-    if (type == MOE_F32) {
-        const float* f = reinterpret_cast<const float*>(p) + at;
-        if (vec) {
-            const float4 q = *reinterpret_cast<const float4*>(f);
-            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = i < left ? f[i] : 0.f;
-        }
-        return;
-    }
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(p) + at;
-    uint32_t u[2];
-    if (vec) {
-        const uint2 q = *reinterpret_cast<const uint2*>(h);
-        u[0] = q.x; u[1] = q.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) u[i] = (2 * i < left ? h[2 * i] : 0u) | ((2 * i + 1 < left ? (uint32_t)h[2 * i + 1] : 0u) << 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (type == MOE_BF16) {
-            v[2 * i] = bf16_lo(u[i]);
-            v[2 * i + 1] = bf16_hi(u[i]);
-        } else {
-            const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-            v[2 * i] = q.x;
-            v[2 * i + 1] = q.y;
-        }
-    }
-}
-__device__ __forceinline__ void store4(int type, void* p, int64_t at, int left, bool vec, const float (&v)[4]) {
-    if (type == MOE_F32) {
-        float* f = reinterpret_cast<float*>(p) + at;
-        if (vec) {
-            *reinterpret_cast<float4*>(f) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < left) f[i] = v[i];
-        }
-        return;
-    }
-    uint32_t u[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (type == MOE_BF16) {
-            const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&q);
-        } else {
-            const __half2 q = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&q);
-        }
-    }
-    uint16_t* h = reinterpret_cast<uint16_t*>(p) + at;
-    if (vec) {
-        *reinterpret_cast<uint2*>(h) = make_uint2(u[0], u[1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < left) h[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
-    }
-}
-
 // out[row] = base[row] (zeros without a base), the block's part `part` of `parts`.
 __device__ __forceinline__ void copy_row(const LoraParams& p, int64_t row, int part, int parts) {
     const int quads = (p.O + 3) / 4;
     for (int q = part * kThreads + threadIdx.x; q < quads; q += parts * kThreads) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         const int left = p.O - 4 * q;
-        const bool vec = p.vec && left >= 4;
+        const bool vec = p.vec >= 4 && left >= 4;
         if (p.base) load4(p.out_type, p.base, row * p.base_stride + 4 * q, left, vec, v);
         store4(p.out_type, p.out, row * p.out_stride + 4 * q, left, vec, v);
     }
@@ -169,9 +85,14 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     int adapter, count;
     if (p.segs) {
         if (group >= p.ctrl->n_rsegs) return;
+        const int first = p.segs[3 * group + 1];
         adapter = p.segs[3 * group];
         count = p.segs[3 * group + 2];
-        if (tid < count) s_rows[tid] = p.perm[p.segs[3 * group + 1] + tid];
+        if (adapter < 0) {
+            for (int i = 0; p.copy && i < count; ++i) copy_row(p, p.perm[first + i], c, C);
+            return;
+        }
+        if (tid < count) s_rows[tid] = p.perm[first + tid];
     } else {
         for (int i = tid; i < p.n; i += kThreads) s_idx[i] = p.idx[i];
         __syncthreads();
@@ -300,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     for (int u = c * uper + warp; u < u1; u += kWarps) {
         // Outputs o .. o + 3 of this lane: rows g and g + 8 of two tiles.
         const int o = u * 32 + 4 * g, left = O - o;
-        const bool vec = p.vec && left >= 4;
+        const bool vec = p.vec >= 4 && left >= 4;
         uint2 bv[kRT][2][2];
 #pragma unroll
         for (int j = 0; j < kRT; ++j)
@@ -341,12 +262,112 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     cluster_wait();
 }
 
-// Rows without an adapter, when the rows go by the sorted order.
-__global__ void __launch_bounds__(kThreads) lora_copy_kernel(const LoraParams p) {
+// The rows sorted by adapter (stable), those of no adapter last, by one block: each warp counts and
+// then places a stretch of the rows, 32 at a time, the equal ones among them found by a match.
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kBatch = 8;
+__global__ void __launch_bounds__(kSortThreads)
+lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_t* __restrict__ perm, int32_t* __restrict__ segs, Ctrl* ctrl) {
+    // cnt[e][w]: adapter e's rows (e = L: no adapter's) in warp w's stretch, then those before them;
+    // total[e]: e's rows; first[e]: their first position.
+    extern __shared__ int32_t cnt[];
+    int32_t *total = cnt + (L + 1) * kSortWarps, *first = total + L + 1;
+    __shared__ int32_t s_sum[2][32], s_all[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < (L + 1) * kSortWarps; i += kSortThreads) cnt[i] = 0;
+    __syncthreads();
     pdl_wait();
-    for (int64_t row = blockIdx.x; row < p.n; row += gridDim.x) {
-        const int a = p.idx[row];
-        if (a < 0 || a >= p.L) copy_row(p, row, 0, 1);
+    const int per = (int)(((int64_t)n + kSortThreads - 1) / kSortThreads) * 32;
+    const int64_t begin = (int64_t)warp * per, end = min((int64_t)n, begin + per);
+    int ev[kBatch];
+    auto fetch = [&](int64_t r0) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t r = r0 + 32 * u + lane;
+            ev[u] = r < end ? idx[r] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) ev[u] = r0 + 32 * u + lane < end ? (ev[u] >= 0 && ev[u] < L ? ev[u] : L) : -1;
+    };
+    for (int64_t r0 = begin; r0 < end; r0 += 32 * kBatch) {
+        fetch(r0);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const uint32_t peers = __match_any_sync(0xffffffffu, ev[u]);
+            if (ev[u] >= 0 && lane == __ffs(peers) - 1) cnt[ev[u] * kSortWarps + warp] += __popc(peers);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    for (int e = warp; e <= L; e += kSortWarps) {
+        const int c = cnt[e * kSortWarps + lane];
+        int s = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        cnt[e * kSortWarps + lane] = s - c;
+        if (lane == 31) total[e] = s;
+    }
+    __syncthreads();
+    // First position and first run of each adapter (L <= 1024, one a thread).
+    const int c = tid < L ? total[tid] : 0, g = (c + tile - 1) / tile;
+    int sc = c, sg = g;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int yc = __shfl_up_sync(0xffffffffu, sc, o), yg = __shfl_up_sync(0xffffffffu, sg, o);
+        if (lane >= o) { sc += yc; sg += yg; }
+    }
+    if (lane == 31) { s_sum[0][warp] = sc; s_sum[1][warp] = sg; }
+    __syncthreads();
+    if (warp == 0) {
+        const int c0 = s_sum[0][lane], g0 = s_sum[1][lane];
+        int vc = c0, vg = g0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int yc = __shfl_up_sync(0xffffffffu, vc, o), yg = __shfl_up_sync(0xffffffffu, vg, o);
+            if (lane >= o) { vc += yc; vg += yg; }
+        }
+        s_sum[0][lane] = vc - c0;
+        s_sum[1][lane] = vg - g0;
+        if (lane == 31) { s_all[0] = vc; s_all[1] = vg; }
+    }
+    __syncthreads();
+    auto write_run = [&](int run, int e, int at, int count) {
+        int32_t* s = segs + 3 * (int64_t)run;
+        s[0] = e;
+        s[1] = at;
+        s[2] = min(tile, count);
+    };
+    if (tid < L) {
+        const int at = s_sum[0][warp] + sc - c, run = s_sum[1][warp] + sg - g;
+        first[tid] = at;
+        for (int i = 0; i < g; ++i) write_run(run + i, tid, at + i * tile, c - i * tile);
+    }
+    const int none = total[L], runs = (int)(((int64_t)none + tile - 1) / tile);
+    for (int i = tid; i < runs; i += kSortThreads) write_run(s_all[1] + i, -1, s_all[0] + i * tile, none - i * tile);
+    if (tid == 0) {
+        first[L] = s_all[0];
+        ctrl->n_active = s_all[1];
+        ctrl->n_rsegs = s_all[1] + runs;
+        ctrl->err = 0;
+    }
+    __syncthreads();
+    for (int64_t r0 = begin; r0 < end; r0 += 32 * kBatch) {
+        if (per > 32 * kBatch) fetch(r0);   // (else they are still there)
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const uint32_t peers = __match_any_sync(0xffffffffu, ev[u]);
+            const int before = __popc(peers & ((1u << lane) - 1));
+            int* mine = &cnt[max(ev[u], 0) * kSortWarps + warp];
+            const int at = ev[u] >= 0 ? *mine + before : 0;
+            __syncwarp();
+            if (ev[u] >= 0) {
+                perm[first[ev[u]] + at] = (int32_t)(r0 + 32 * u + lane);
+                if (before == 0) *mine = at + __popc(peers);
+            }
+            __syncwarp();
+        }
     }
     pdl_trigger();
 }
@@ -384,52 +405,73 @@ cudaError_t launch_all(const LoraParams& p, int x_type, int groups, int cluster,
 }
 
 struct Layout {
-    size_t counts, offsets, perm, inv, active, segs, total;
-    int64_t max_segs;
+    size_t perm, segs, part, total;
+    int64_t max_segs;   // of kLoraTile rows
 };
-Layout layout(int64_t n, int L) {
+Layout layout(int64_t n, int L, int r) {
     Layout l{};
     size_t off = sizeof(Ctrl);
     auto take = [&](size_t bytes) { const size_t o = off; off = align_up(off + bytes, 256); return o; };
     if (n > kScanRows) {
-        l.max_segs = n / kRows + std::min<int64_t>(n, L) + 1;
-        l.counts = take(sizeof(int32_t) * L);
-        l.offsets = take(sizeof(int32_t) * (L + 1));
         l.perm = take(sizeof(int32_t) * n);
-        l.inv = take(sizeof(int32_t) * n);
-        l.active = take(sizeof(int32_t) * L);
-        l.segs = take(sizeof(int32_t) * 3 * l.max_segs);
+        l.segs = take(sizeof(int32_t) * 3 * (n / kRows + std::min<int64_t>(n, L + 1) + 1));
+        l.part = take(sizeof(float) * lora_part_rows(n) * r);
     }
     l.total = off;
     return l;
 }
 
+cudaError_t launch_sort(const LoraParams& p, int tile, int32_t* perm, int32_t* segs, Ctrl* ctrl, cudaStream_t st) {
+    const size_t smem = sizeof(int32_t) * (p.L + 1) * (kSortWarps + 2);
+    static std::mutex mu;
+    static bool configured[128] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!configured[dev]) {
+            const cudaError_t e = cudaFuncSetAttribute(lora_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (int)sizeof(int32_t) * (kMaxExperts + 1) * (kSortWarps + 2));
+            if (e != cudaSuccess) return e;
+            configured[dev] = true;
+        }
+    }
+    return launch_pdl(lora_sort_kernel, dim3(1), dim3(kSortThreads), smem, st, p.idx, p.n, p.L, tile, perm, segs, ctrl);
+}
+
 }  // namespace
 
-size_t lora_workspace(int64_t n, int L) { return layout(n, L).total; }
+size_t lora_workspace(int64_t n, int L, int r) { return layout(n, L, r).total; }
 
 cudaError_t launch_lora(const LoraParams& given, int x_type, void* ws, int num_sms, cudaStream_t st) {
     LoraParams p = given;
     const int size = p.out_type == MOE_F32 ? 4 : 2;
-    auto rows4 = [&](const void* a, int64_t stride) { return reinterpret_cast<uintptr_t>(a) % (4 * size) == 0 && (p.n == 1 || stride % 4 == 0); };
-    p.vec = rows4(p.out, p.out_stride) && (!p.base || rows4(p.base, p.base_stride));
+    auto rows_of = [&](int v, const void* a, int64_t stride) {
+        return !a || (reinterpret_cast<uintptr_t>(a) % (v * size) == 0 && (p.n == 1 || stride % v == 0));
+    };
+    p.vec = 1;
+    for (int v : {4, 8})
+        if (rows_of(v, p.out, p.out_stride) && rows_of(v, p.base, p.base_stride)) p.vec = v;
     p.copy = p.base != p.out;
-    int groups = p.n, cluster = 8;
-    if (p.n > kScanRows) {
-        const Layout l = layout(p.n, p.L);
-        uint8_t* w = static_cast<uint8_t*>(ws);
-        auto at = [&](size_t o) { return reinterpret_cast<int32_t*>(w + o); };
-        p.ctrl = reinterpret_cast<Ctrl*>(w);
-        p.segs = at(l.segs);
-        p.perm = at(l.perm);
-        cudaError_t e = launch_group(p.idx, p.n, p.L, kRows, 0, p.L, at(l.counts), at(l.offsets), at(l.perm), at(l.inv), at(l.active),
-                                     at(l.segs), reinterpret_cast<Ctrl*>(w), st);
-        if (e != cudaSuccess) return e;
-        if (p.copy && (e = launch_pdl(lora_copy_kernel, dim3(std::min(p.n, num_sms * 8)), dim3(kThreads), 0, st, p)) != cudaSuccess) return e;
-        groups = (int)l.max_segs;
-        cluster = 4;
+    cudaError_t e;
+    if (p.n <= kScanRows) {
+        e = launch_all(p, x_type, p.n, 8, st);
+        return e != cudaSuccess ? e : cudaGetLastError();
     }
-    const cudaError_t e = launch_all(p, x_type, groups, cluster, st);
+    const Layout l = layout(p.n, p.L, p.r);
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(w);
+    p.ctrl = ctrl;
+    p.segs = reinterpret_cast<int32_t*>(w + l.segs);
+    p.perm = reinterpret_cast<int32_t*>(w + l.perm);
+    CUtensorMap maps[3];
+    const bool tc = !p.x_host && lora_maps(p, x_type, maps);
+    const int tile = tc ? kLoraTile : kRows;
+    if ((e = launch_sort(p, tile, reinterpret_cast<int32_t*>(w + l.perm), reinterpret_cast<int32_t*>(w + l.segs), ctrl, st)) != cudaSuccess)
+        return e;
+    const int max_segs = (int)(p.n / tile + std::min(p.n, p.L + 1) + 1);
+    e = tc ? launch_lora_tc(p, x_type, maps, reinterpret_cast<float*>(w + l.part), &ctrl->err, max_segs, st)
+           : launch_all(p, x_type, max_segs, 4, st);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -1,0 +1,139 @@
+// moe_lora.cuh -- what the adapters' kernels (moe_lora.cu, moe_lora_tc.cu) share: v's parts, and
+// elements of base and out.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+// v as a sum of `kParts` 16-bit numbers; an infinity (or what rounds to one) and a NaN have one part.
+template <bool kBf16, int kParts> __device__ __forceinline__ void split(float v, uint16_t (&part)[kParts]) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        float f;
+        if constexpr (kBf16) {
+            const __nv_bfloat16 b = __float2bfloat16_rn(v);
+            part[i] = __bfloat16_as_ushort(b);
+            f = __bfloat162float(b);
+        } else {
+            const __half b = __float2half_rn(v);
+            part[i] = __half_as_ushort(b);
+            f = __half2float(b);
+        }
+        v = fabsf(f) < INFINITY ? v - f : 0.f;
+    }
+}
+
+// Four consecutive elements of a row of base or out.
+__device__ __forceinline__ void load4(int type, const void* p, int64_t at, int left, bool vec, float (&v)[4]) {
+    if (type == MOE_F32) {
+        const float* f = reinterpret_cast<const float*>(p) + at;
+        if (vec) {
+            const float4 q = *reinterpret_cast<const float4*>(f);
+            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = i < left ? f[i] : 0.f;
+        }
+        return;
+    }
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p) + at;
+    uint32_t u[2];
+    if (vec) {
+        const uint2 q = *reinterpret_cast<const uint2*>(h);
+        u[0] = q.x; u[1] = q.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) u[i] = (2 * i < left ? h[2 * i] : 0u) | ((2 * i + 1 < left ? (uint32_t)h[2 * i + 1] : 0u) << 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (type == MOE_BF16) {
+            v[2 * i] = bf16_lo(u[i]);
+            v[2 * i + 1] = bf16_hi(u[i]);
+        } else {
+            const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+            v[2 * i] = q.x;
+            v[2 * i + 1] = q.y;
+        }
+    }
+}
+__device__ __forceinline__ void store4(int type, void* p, int64_t at, int left, bool vec, const float (&v)[4]) {
+    if (type == MOE_F32) {
+        float* f = reinterpret_cast<float*>(p) + at;
+        if (vec) {
+            *reinterpret_cast<float4*>(f) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) f[i] = v[i];
+        }
+        return;
+    }
+    uint32_t u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (type == MOE_BF16) {
+            const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&q);
+        } else {
+            const __half2 q = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+    }
+    uint16_t* h = reinterpret_cast<uint16_t*>(p) + at;
+    if (vec) {
+        *reinterpret_cast<uint2*>(h) = make_uint2(u[0], u[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) h[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+// Single elements, and the 16 bytes of four (kF32) or eight.
+template <bool kF32> __device__ __forceinline__ float load_one(int type, const void* p, int64_t at) {
+    if constexpr (kF32) return reinterpret_cast<const float*>(p)[at];
+    const uint16_t u = reinterpret_cast<const uint16_t*>(p)[at];
+    return type == MOE_BF16 ? bf16_lo(u) : __half2float(__ushort_as_half(u));
+}
+template <bool kF32> __device__ __forceinline__ void store_one(int type, void* p, int64_t at, float v) {
+    if constexpr (kF32) reinterpret_cast<float*>(p)[at] = v;
+    else reinterpret_cast<uint16_t*>(p)[at] = type == MOE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+template <bool kF32> __device__ __forceinline__ void add_raw(int type, const uint4& was, float* y) {
+    const uint32_t u[4] = {was.x, was.y, was.z, was.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (kF32) {
+            y[i] += __uint_as_float(u[i]);
+        } else if (type == MOE_BF16) {
+            y[2 * i] += bf16_lo(u[i]);
+            y[2 * i + 1] += bf16_hi(u[i]);
+        } else {
+            const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+            y[2 * i] += q.x;
+            y[2 * i + 1] += q.y;
+        }
+    }
+}
+template <bool kF32> __device__ __forceinline__ void store_raw(int type, void* p, int64_t at, const float* y) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (kF32) {
+            u[i] = __float_as_uint(y[i]);
+        } else if (type == MOE_BF16) {
+            const __nv_bfloat162 q = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&q);
+        } else {
+            const __half2 q = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+    }
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p) + at * (kF32 ? 4 : 2)) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+}  // namespace moe

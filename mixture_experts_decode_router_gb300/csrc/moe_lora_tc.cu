@@ -1,0 +1,489 @@
+// moe_lora_tc.cu -- low-rank adapters of many rows on the tensor cores (sm_103a): the rows sorted by
+// adapter, in tiles of up to 128 rows of one adapter (moe_lora.cu).
+//
+// Bound by HBM: x once, base and out once; the adapters' matrices come from L2, and the products
+// are 4 n r (in + out) / 2 operations, a tenth of the tensor cores' rate at rank 64.
+//
+// v = A x (lora_shrink_kernel): a block takes a tile of rows and a stretch of K.  Rows of x are
+// gathered where they lie by TMA (four rows an instruction, 64 elements of each), beside the adapter's
+// rows; M = 128 rows, N = the rank; the fp32 sums in tensor memory are written as that stretch's part.
+//
+// out = base + B v (lora_expand_kernel): a block takes a tile of rows and a stretch of the outputs,
+// 128 at a time.  v, summed over the stretches in their order, scaled and split into 16-bit parts
+// (moe_lora.cu), stays in shared memory as the products' M = 128 rows; B's rows come by TMA.  Eight
+// warps add the base: results go through shared memory, so that base and out are read and written
+// along their rows, 16 bytes a thread where they are aligned and by neighbouring elements where they
+// are not, base's loads in flight while the products run.
+#include <mutex>
+
+#include "moe_launch.cuh"
+#include "moe_lora.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kM = kLoraTile;
+constexpr int kBox = 64;                       // elements along a reduction: 128 bytes
+constexpr int kBoxBytes = kM * kBox * 2;       // of 128 rows
+
+struct TcArgs {
+    LoraParams p;
+    int N;            // rank, a multiple of 16
+    int splits, kc;   // stretches of K, 64-element boxes of each
+    int stages;       // shrink: ring
+    int per;          // expand: tiles of 128 outputs of a block
+    int tmem_cols;    // shrink
+    float* part;      // [splits][n][r]
+    int32_t* err;
+};
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+    return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+// Rows y of a [rows, K] map (box 64 x 1), 64 elements from x on, four times 128 bytes.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int32_t x, int4 y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+
+constexpr int kShrinkThreads = 128;
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kShrinkThreads)
+lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap, const TcArgs g) {
+    extern __shared__ __align__(1024) uint8_t raw[];
+    uint8_t* smem = align1024(raw);
+    const LoraParams& p = g.p;
+    const int stage_bytes = kBoxBytes + g.N * kBox * 2;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + g.stages * stage_bytes);
+    uint64_t *empty = full + g.stages, *done = empty + g.stages;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < g.stages; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        ptx::mbar_init(done, 1);
+        *s_abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) ptx::tmem_alloc(s_tmem, g.tmem_cols);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    pdl_wait();
+
+    const int tile = blockIdx.x, split = blockIdx.y;
+    if (tile < p.ctrl->n_active) {
+        const int adapter = p.segs[3 * tile], first = p.segs[3 * tile + 1], count = p.segs[3 * tile + 2];
+        const int j0 = split * g.kc, nj = min((p.K + kBox - 1) / kBox - j0, g.kc);
+        if (warp == 0) {
+            // Lane i gathers rows 4 i .. 4 i + 3 (the last row again behind it).
+            const int groups = (count + 3) / 4;
+            int4 rows = make_int4(0, 0, 0, 0);
+            if (lane < groups) {
+                const int32_t* q = p.perm + first;
+                rows.x = q[4 * lane];
+                rows.y = q[min(4 * lane + 1, count - 1)];
+                rows.z = q[min(4 * lane + 2, count - 1)];
+                rows.w = q[min(4 * lane + 3, count - 1)];
+            }
+            int sent = 0;
+            for (int j = 0; j < nj; ++j) {
+                const int s = j % g.stages;
+                if (j >= g.stages && !ptx::mbar_wait_warp(&empty[s], (j / g.stages - 1) & 1, s_abort, g.err, 31)) break;
+                uint8_t* at = smem + s * stage_bytes;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], groups * 512 + g.N * kBox * 2);
+                __syncwarp();
+                const int k = (j0 + j) * kBox;
+                if (lane < groups) tma_gather4(at + 512 * lane, &xmap, k, rows, &full[s]);
+                if (lane == 0) ptx::tma_load_2d(at + kBoxBytes, &amap, k, adapter * p.r, &full[s]);
+                sent = j + 1;
+            }
+            // (After a wait that gave up: the copies in flight end before the block does.)
+            if (ptx::aborted_warp(s_abort) && lane == 0)
+                for (int j = max(0, sent - g.stages); j < sent; ++j) ptx::mbar_wait_quiet(&full[j % g.stages], (j / g.stages) & 1, ptx::kWaitLimitNs);
+        } else if (warp == 1) {
+            const uint32_t idesc = ptx::idesc_f16(kM, g.N, kBf16);
+            for (int j = 0; j < nj; ++j) {
+                const int s = j % g.stages;
+                if (!ptx::mbar_wait_warp(&full[s], (j / g.stages) & 1, s_abort, g.err, 32)) break;
+                ptx::tc_fence_after();
+                if (ptx::elect_one()) {
+                    const uint64_t a = ptx::sw128_desc(ptx::smem_u32(smem + s * stage_bytes));
+                    const uint64_t b = ptx::sw128_desc(ptx::smem_u32(smem + s * stage_bytes + kBoxBytes));
+#pragma unroll
+                    for (int k = 0; k < kBox / 16; ++k) ptx::mma_f16(tmem, a + 2 * k, b + 2 * k, idesc, j > 0 || k > 0);
+                    ptx::mma_commit(&empty[s]);
+                    if (j == nj - 1) ptx::mma_commit(done);
+                }
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+        if (ptx::mbar_wait_warp(done, 0, s_abort, g.err, 33)) {
+            ptx::tc_fence_after();
+            const int row = 32 * warp + lane;
+            float* to = g.part + ((int64_t)split * p.n + first + row) * p.r;
+            const uint32_t tb = tmem + ((uint32_t)(32 * warp) << 16);
+            if (32 * warp < count)
+                for (int c = 0; c < g.N; c += 16) {
+                    float d[16];
+                    ptx::tmem_ld16(tb + c, d);
+                    if (row < count) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (c + 4 * i < p.r) *reinterpret_cast<float4*>(to + c + 4 * i) = make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+                    }
+                }
+        }
+    }
+    pdl_trigger();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, g.tmem_cols);
+    }
+}
+
+constexpr int kNT = 128;                 // outputs of a tile
+constexpr int kEpiWarps = 8;
+constexpr int kExpandThreads = 32 * (kEpiWarps + 2);
+constexpr int kRing = 2;                 // tiles of B in flight
+constexpr int kStageRow = 36;            // floats of a row of a warp's staging (32 and 4: no bank conflicts)
+constexpr int kStageBytes = 32 * kStageRow * 4;
+
+__host__ __device__ constexpr int expand_parts(bool f32) { return f32 ? 3 : 2; }
+inline size_t expand_smem(int rank16, bool f32) {
+    const int boxes = (rank16 + kBox - 1) / kBox;
+    return 1024 + (size_t)(expand_parts(f32) + kRing) * boxes * kBoxBytes + kEpiWarps * kStageBytes + 256;
+}
+
+template <bool kBf16, bool kF32>
+__global__ void __launch_bounds__(kExpandThreads, kF32 ? 1 : 2)
+lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
+    constexpr int kParts = expand_parts(kF32);
+    extern __shared__ __align__(1024) uint8_t raw[];
+    __shared__ int32_t s_rows[kM], s_exp[kM];
+    const LoraParams& p = g.p;
+    const int boxes = (g.N + kBox - 1) / kBox, vbytes = boxes * kBoxBytes;
+    uint8_t* sV = align1024(raw);                       // [part][box][128 rows x 128 bytes]
+    uint8_t* sB = sV + kParts * vbytes;                 // [stage][box][128 outputs x 128 bytes]
+    uint8_t* sStage = sB + kRing * vbytes;
+    uint64_t* bfull = reinterpret_cast<uint64_t*>(sStage + kEpiWarps * kStageBytes);
+    uint64_t *bempty = bfull + kRing, *tfull = bempty + kRing, *tempty = tfull + 2;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            ptx::mbar_init(&bfull[i], 1);
+            ptx::mbar_init(&bempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&tfull[i], 1);
+            ptx::mbar_init(&tempty[i], kEpiWarps);
+        }
+        *s_abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kEpiWarps) ptx::tmem_alloc(s_tmem, 2 * kNT);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    pdl_wait();
+
+    const int tile = blockIdx.x, O = p.O;
+    const int n_tiles = (O + kNT - 1) / kNT, t0 = blockIdx.y * g.per, nt = min(n_tiles - t0, g.per);
+    const int runs = p.ctrl->n_rsegs;
+    const int adapter = tile < runs ? p.segs[3 * tile] : -1;
+    const int first = tile < runs ? p.segs[3 * tile + 1] : 0, count = tile < runs ? p.segs[3 * tile + 2] : 0;
+    if (adapter < 0 && p.copy && nt > 0) {
+        // Rows without an adapter (or none): base's elements as they are.
+        const int o0 = t0 * kNT, o1 = min(O, (t0 + nt) * kNT);
+        for (int i = warp; i < count; i += kEpiWarps + 2) {
+            const int64_t row = p.perm[first + i];
+            const int v = p.vec >= 4 ? 4 : 1;
+            for (int o = o0 + v * lane; o < o1; o += v * 32) {
+                float f[4] = {0.f, 0.f, 0.f, 0.f};
+                const int left = v == 1 ? 1 : o1 - o;
+                if (p.base) load4(p.out_type, p.base, row * p.base_stride + o, left, v == 4 && left >= 4, f);
+                store4(p.out_type, p.out, row * p.out_stride + o, left, v == 4 && left >= 4, f);
+            }
+        }
+    } else if (adapter >= 0 && nt > 0) {
+        // v of the tile's rows, split, in the products' layout: lanes of a row hold eight elements each.
+        if (tid < kM) s_rows[tid] = tid < count ? p.perm[first + tid] : 0;
+        const int chunks = g.N / 8;
+        int lanes = 2;
+        while (lanes < chunks) lanes *= 2;
+        const float scale = p.scale ? __ldg(p.scale + adapter) : 1.f;
+        const int per_warp = 32 / lanes, c8 = lane % lanes;
+        for (int i0 = warp * per_warp; i0 < count; i0 += (kEpiWarps + 2) * per_warp) {
+            const int row = i0 + lane / lanes;
+            const bool in = row < count && c8 * 8 < p.r;
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (in) {
+                const float* from = g.part + (int64_t)(first + row) * p.r + c8 * 8;
+                for (int s = 0; s < g.splits; ++s) {
+                    const float4 a = *reinterpret_cast<const float4*>(from + (int64_t)s * p.n * p.r);
+                    const float4 b = *reinterpret_cast<const float4*>(from + (int64_t)s * p.n * p.r + 4);
+                    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+                    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= scale;
+            }
+            int e = 0;
+            if constexpr (!kBf16) {
+                float most = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) most = fmaxf(most, finite_abs(v[i]));
+                for (int o = 1; o < lanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                e = f16_shift(most);
+                if (row < count && c8 == 0) s_exp[row] = e;
+            }
+            uint16_t q[8][kParts];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) split<kBf16, kParts>(kBf16 ? v[i] : times_exp2(v[i], e), q[i]);
+            if (row < count && c8 < chunks) {
+                uint8_t* at = sV + (c8 >> 3) * kBoxBytes + row * 128 + (((c8 & 7) ^ (row & 7)) << 4);
+#pragma unroll
+                for (int m = 0; m < kParts; ++m)
+                    *reinterpret_cast<uint4*>(at + m * vbytes) =
+                        make_uint4(q[0][m] | (uint32_t)q[1][m] << 16, q[2][m] | (uint32_t)q[3][m] << 16, q[4][m] | (uint32_t)q[5][m] << 16,
+                                   q[6][m] | (uint32_t)q[7][m] << 16);
+            }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncthreads();
+
+        if (warp == kEpiWarps + 1) {
+            int sent = 0;
+            for (int i = 0; i < nt; ++i) {
+                const int s = i % kRing;
+                if (i >= kRing && !ptx::mbar_wait_warp(&bempty[s], (i / kRing - 1) & 1, s_abort, g.err, 34)) break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&bfull[s], vbytes);
+                    for (int b = 0; b < boxes; ++b)
+                        ptx::tma_load_2d(sB + s * vbytes + b * kBoxBytes, &bmap, b * kBox, adapter * O + (t0 + i) * kNT, &bfull[s]);
+                }
+                __syncwarp();
+                sent = i + 1;
+            }
+            if (ptx::aborted_warp(s_abort) && lane == 0)
+                for (int i = max(0, sent - kRing); i < sent; ++i) ptx::mbar_wait_quiet(&bfull[i % kRing], (i / kRing) & 1, ptx::kWaitLimitNs);
+        } else if (warp == kEpiWarps) {
+            const uint32_t idesc = ptx::idesc_f16(kM, kNT, kBf16);
+            const int steps = g.N / 16;
+            for (int i = 0; i < nt; ++i) {
+                const int s = i % kRing, buf = i & 1;
+                if (!ptx::mbar_wait_warp(&bfull[s], (i / kRing) & 1, s_abort, g.err, 35)) break;
+                if (i >= 2 && !ptx::mbar_wait_warp(&tempty[buf], (i / 2 - 1) & 1, s_abort, g.err, 36)) break;
+                ptx::tc_fence_after();
+                if (ptx::elect_one()) {
+                    uint32_t more = 0;
+                    for (int m = kParts - 1; m >= 0; --m)     // the smallest part first
+                        for (int k = 0; k < steps; ++k) {
+                            ptx::mma_f16(tmem + buf * kNT, ptx::sw128_desc(ptx::smem_u32(sV + m * vbytes + (k / 4) * kBoxBytes)) + 2 * (k % 4),
+                                         ptx::sw128_desc(ptx::smem_u32(sB + s * vbytes + (k / 4) * kBoxBytes)) + 2 * (k % 4), idesc, more);
+                            more = 1;
+                        }
+                    ptx::mma_commit(&bempty[s]);
+                    ptx::mma_commit(&tfull[buf]);
+                }
+                __syncwarp();
+            }
+        } else {
+            // Rows 32 q .. 32 q + 31 of the tile, 64 of the 128 outputs in two passes of 32.
+            const int q = warp & 3, half = warp >> 2;
+            float* stage = reinterpret_cast<float*>(sStage + warp * kStageBytes);
+            const bool some = 32 * q < count;
+            constexpr int kV = kF32 ? 4 : 8;                  // elements of 16 bytes
+            constexpr int kCol = 32 / kV, kIts = kCol;        // threads of a row; rows of a thread (32 / (32 / kCol))
+            const int c = (lane % kCol) * kV, r0 = 32 * q + lane / kCol;
+            int rows[kIts];
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int r = r0 + it * (32 / kCol);
+                rows[it] = r < count ? s_rows[r] : -1;
+            }
+            const uint8_t* base = reinterpret_cast<const uint8_t*>(p.base);
+            constexpr int kSize = kF32 ? 4 : 2;
+            const bool wide = p.vec * kSize >= 16;
+            uint4 was[2][kIts];
+            // Base's elements of pass `pass` (two a tile) of this block.
+            auto fetch = [&](int pass, uint4 (&to)[kIts]) {
+                const int o = (t0 + (pass >> 1)) * kNT + half * 64 + (pass & 1) * 32 + c;
+#pragma unroll
+                for (int it = 0; it < kIts; ++it)
+                    if (rows[it] >= 0 && o + kV <= O)
+                        to[it] = *reinterpret_cast<const uint4*>(base + ((int64_t)rows[it] * p.base_stride + o) * kSize);
+            };
+            const bool early = wide && base != nullptr;
+            if (early) fetch(0, was[0]);
+            for (int i = 0; i < nt; ++i) {
+                const int buf = i & 1;
+                if (!ptx::mbar_wait_warp(&tfull[buf], (i >> 1) & 1, s_abort, g.err, 37)) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int pass = 2 * i + h;
+                    if (early && pass + 1 < 2 * nt) fetch(pass + 1, was[(h + 1) & 1]);
+                    if (some) {
+                        const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * kNT + half * 64 + h * 32;
+                        float d[16];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            ptx::tmem_ld16(tb + 16 * u, d);
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                *reinterpret_cast<float4*>(stage + lane * kStageRow + 16 * u + 4 * w) =
+                                    make_float4(d[4 * w], d[4 * w + 1], d[4 * w + 2], d[4 * w + 3]);
+                        }
+                    }
+                    if (h == 1) {                             // the accumulator is read
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        ptx::mbar_arrive_elect(&tempty[buf]);
+                    }
+                    __syncwarp();
+                    if (some) {
+                        const int o_pass = (t0 + i) * kNT + half * 64 + h * 32;
+                        if (wide) {
+                            const int o = o_pass + c;
+#pragma unroll
+                            for (int it = 0; it < kIts; ++it) {
+                                if (rows[it] < 0 || o >= O) continue;
+                                const int r = lane / kCol + it * (32 / kCol);
+                                float y[kV];
+#pragma unroll
+                                for (int w = 0; w < kV / 4; ++w) {
+                                    const float4 f = *reinterpret_cast<const float4*>(stage + r * kStageRow + c + 4 * w);
+                                    y[4 * w] = f.x; y[4 * w + 1] = f.y; y[4 * w + 2] = f.z; y[4 * w + 3] = f.w;
+                                }
+                                if constexpr (!kBf16) {
+                                    const int e = -s_exp[32 * q + r];
+#pragma unroll
+                                    for (int w = 0; w < kV; ++w) y[w] = times_exp2(y[w], e);
+                                }
+                                const int64_t at = (int64_t)rows[it] * p.out_stride + o;
+                                if (o + kV <= O) {
+                                    if (base) add_raw<kF32>(p.out_type, was[h & 1][it], y);
+                                    store_raw<kF32>(p.out_type, p.out, at, y);
+                                } else {
+#pragma unroll
+                                    for (int w = 0; w < kV; ++w)
+                                        if (o + w < O) {
+                                            if (base) y[w] += load_one<kF32>(p.out_type, base, (int64_t)rows[it] * p.base_stride + o + w);
+                                            store_one<kF32>(p.out_type, p.out, at + w, y[w]);
+                                        }
+                                }
+                            }
+                        } else {
+                            // Neighbouring lanes at neighbouring elements, eight rows in flight.
+                            const int o = o_pass + lane;
+                            for (int b0 = 0; b0 < 32 && 32 * q + b0 < count; b0 += 8) {
+                                float y[8];
+#pragma unroll
+                                for (int w = 0; w < 8; ++w) {
+                                    const int r = 32 * q + b0 + w;
+                                    if (base && r < count && o < O) y[w] = load_one<kF32>(p.out_type, p.base, (int64_t)s_rows[r] * p.base_stride + o);
+                                    else y[w] = 0.f;
+                                }
+#pragma unroll
+                                for (int w = 0; w < 8; ++w) {
+                                    const int r = 32 * q + b0 + w;
+                                    if (r < count && o < O) {
+                                        float v = stage[(b0 + w) * kStageRow + lane];
+                                        if constexpr (!kBf16) v = times_exp2(v, -s_exp[r]);
+                                        store_one<kF32>(p.out_type, p.out, (int64_t)s_rows[r] * p.out_stride + o, base ? y[w] + v : v);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                    __syncwarp();                             // the staging is read
+                }
+            }
+        }
+    }
+    pdl_trigger();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kEpiWarps) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 2 * kNT);
+    }
+}
+
+template <typename Kern>
+cudaError_t configure(Kern kern, int slot) {
+    static std::mutex mu;
+    static bool configured[128][8] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (configured[dev][slot]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+    if (e == cudaSuccess) configured[dev][slot] = true;
+    return e;
+}
+
+}  // namespace
+
+bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[3]) {
+    // (Coordinates are 32-bit; strides fit 40 bits.)
+    if ((int64_t)p.L * p.O > INT32_MAX || p.x_stride * 2 >= (int64_t)1 << 40) return false;
+    const CUtensorMapDataType t = x_type == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const uint32_t N = (p.r + 15) / 16 * 16;
+    return make_map(&maps[0], p.x, t, 2, p.K, p.n, kBox, 1, CU_TENSOR_MAP_SWIZZLE_128B, p.x_stride) &&
+           make_map(&maps[1], p.a, t, 2, p.K, (uint64_t)p.L * p.r, kBox, N, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           make_map(&maps[2], p.b, t, 2, p.r, (uint64_t)p.L * p.O, kBox, kNT, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[3], float* part, int32_t* err, int max_segs,
+                           cudaStream_t st) {
+    TcArgs g{};
+    g.p = p;
+    g.N = (p.r + 15) / 16 * 16;
+    g.part = part;
+    g.err = err;
+    // Stretches of K and of the outputs: about kLoraBlocks blocks, two an SM.
+    const int tiles = (p.n + kM - 1) / kM, boxes = (p.K + kBox - 1) / kBox;
+    const int want = (kLoraBlocks + tiles - 1) / tiles;
+    g.kc = (boxes + std::min(want, kLoraMaxSplits) - 1) / std::min(want, kLoraMaxSplits);
+    g.splits = (boxes + g.kc - 1) / g.kc;
+    const int stage = kBoxBytes + g.N * kBox * 2;
+    g.stages = std::min(g.kc, 100 * 1024 / stage);
+    g.tmem_cols = 32;
+    while (g.tmem_cols < g.N) g.tmem_cols *= 2;
+    const size_t smem = 1024 + (size_t)g.stages * stage + 256;
+    auto shrink = x_type == MOE_BF16 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>;
+    cudaError_t e = configure(shrink, x_type == MOE_BF16 ? 0 : 1);
+    if (e != cudaSuccess) return e;
+    if ((e = launch_pdl(shrink, dim3(max_segs, g.splits), dim3(kShrinkThreads), smem, st, maps[0], maps[1], g)) != cudaSuccess) return e;
+
+    const bool f32 = p.out_type == MOE_F32, bf = x_type == MOE_BF16;
+    const int n_tiles = (p.O + kNT - 1) / kNT;
+    const int parts = std::min({want, n_tiles, 65535});
+    g.per = (n_tiles + parts - 1) / parts;
+    const dim3 grid(max_segs, (n_tiles + g.per - 1) / g.per);
+    auto expand = bf ? (f32 ? lora_expand_kernel<true, true> : lora_expand_kernel<true, false>)
+                     : (f32 ? lora_expand_kernel<false, true> : lora_expand_kernel<false, false>);
+    if ((e = configure(expand, 2 + (bf ? 0 : 2) + (f32 ? 1 : 0))) != cudaSuccess) return e;
+    return launch_pdl(expand, grid, dim3(kExpandThreads), expand_smem(g.N, f32), st, maps[2], g);
+}
+
+}  // namespace moe

@@ -366,7 +366,7 @@ def test_another_stream_replay_and_pinned(lib, n):
     host = torch.empty(n, 104, dtype=BF).pin_memory()
     op.forward(xs[2].cpu().pin_memory(), ids[2], base.cpu().pin_memory(), out=host)
     torch.cuda.synchronize()
-    assert torch.equal(host.cuda(), want[2])
+    check(op, xs[2], ids[2], base, host.cuda())             # (many rows: not by the same kernels)
 
 
 @gpu
