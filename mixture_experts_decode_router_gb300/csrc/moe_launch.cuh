@@ -241,9 +241,10 @@ constexpr int kLoraMaxSplits = 8;
 inline int64_t lora_part_rows(int64_t n) {   // of splits * n, and of every smaller n's
     return std::min<int64_t>(kLoraMaxSplits * n, (int64_t)kLoraBlocks * kLoraTile + 2 * n);
 }
-// Whether the tensor maps of a call can be made; `maps` receives them (x, A, B).
-bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[3]);
-cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[3], float* part, int32_t* err, int max_segs,
+// Whether the tensor maps of a call can be made; `maps` receives them (x by
+// single rows, A, B, x by 32 rows).
+bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[4]);
+cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[4], float* part, int32_t* err, int max_segs,
                            cudaStream_t st);
 
 // tile: routes of a segment at most.

@@ -31,9 +31,8 @@ constexpr int kBoxBytes = kM * kBox * 2;       // of 128 rows
 struct TcArgs {
     LoraParams p;
     int N;            // rank, a multiple of 16
-    int splits, kc;   // stretches of K, 64-element boxes of each
+    int max_splits;   // of K: as many as part holds
     int stages;       // shrink: ring
-    int per;          // expand: tiles of 128 outputs of a block
     int tmem_cols;    // shrink
     float* part;      // [splits][n][r]
     int32_t* err;
@@ -52,11 +51,77 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
-constexpr int kShrinkThreads = 128;
+// A wait of the whole warp that tries for some microseconds before it begins to count the time (the
+// timer's first reading alone takes a microsecond, which every wait of a ring would pay).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* err, int32_t code) {
+    for (int i = 0; i < 256; ++i)
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    return ptx::mbar_wait_warp(bar, parity, abort, err, code);
+}
+
+// Into how many pieces of `size` (boxes of K, tiles of outputs) each of `runs` tiles is cut, at most
+// `most`: that for which the blocks' rounds are over soonest, where a piece costs 2% of a tile more
+// than its part.  (Both kernels form the same from ctrl->n_active.)
+struct Pieces {
+    int n, size;
+};
+__device__ __forceinline__ Pieces pieces(int runs, int size, int most) {
+    int best = 1;
+    float cost = 1e30f;
+    for (int c = 1; c <= min(most, size); ++c) {
+        const int per = (size + c - 1) / c;
+        const float t = (float)((runs * c + kLoraBlocks - 1) / kLoraBlocks) * ((float)per / size + 0.02f);
+        if (t < cost) {
+            cost = t;
+            best = c;
+        }
+    }
+    const int per = (size + best - 1) / best;
+    return {(size + per - 1) / per, per};
+}
+
+// A warp's 32 rows of a tile, from its row r0 on: how TMA is to fetch them.  Rows that follow one
+// another in memory come as one box of 32 rows (rows behind the last come along, and are not used);
+// others, four at a time (the last row again behind the last).  One lane issues: an instruction of
+// many lanes is issued lane by lane, 64 cycles each.
+struct RowFetch {
+    int4 rows[8];
+    int groups;       // of four; 0 where there are no rows
+    bool together;
+    __device__ __forceinline__ void start(const int32_t* perm, int first, int r0, int count) {
+        const int here = min(32, count - r0);
+        const int32_t* q = perm + first + r0;
+        groups = here > 0 ? (here + 3) / 4 : 0;
+        together = here > 0 && q[here - 1] - q[0] == here - 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < groups) {
+                rows[i].x = q[4 * i];
+                rows[i].y = q[min(4 * i + 1, here - 1)];
+                rows[i].z = q[min(4 * i + 2, here - 1)];
+                rows[i].w = q[min(4 * i + 3, here - 1)];
+            }
+    }
+    __device__ __forceinline__ uint32_t bytes() const { return groups == 0 ? 0 : together ? 32 * 128 : groups * 512; }
+    // 128 bytes of each row, from element x on.
+    __device__ __forceinline__ void issue(uint8_t* dst, const CUtensorMap* one, const CUtensorMap* box, int x, uint64_t* bar) const {
+        if (together) {
+            ptx::tma_load_2d(dst, box, x, rows[0].x, bar);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < groups) tma_gather4(dst + 512 * i, one, x, rows[i], bar);
+        }
+    }
+};
+
+// Warp 0 fetches the adapter's rows, warp 1 issues the products, warps 2 to 5 fetch 32 rows of x each.
+constexpr int kShrinkThreads = 192;
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kShrinkThreads)
-lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap, const TcArgs g) {
+lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xbox,
+                   const __grid_constant__ CUtensorMap amap, const TcArgs g) {
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t* smem = align1024(raw);
     const LoraParams& p = g.p;
@@ -68,7 +133,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < g.stages; ++i) {
-            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&full[i], 5);
             ptx::mbar_init(&empty[i], 1);
         }
         ptx::mbar_init(done, 1);
@@ -82,60 +147,60 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
     const uint32_t tmem = *s_tmem;
     pdl_wait();
 
-    const int tile = blockIdx.x, split = blockIdx.y;
-    if (tile < p.ctrl->n_active) {
+    const int runs = p.ctrl->n_active, boxes = (p.K + kBox - 1) / kBox;
+    const Pieces ks = pieces(runs, boxes, g.max_splits);
+    int slot = 0, unit_no = 0;
+    uint32_t phase = 0;               // of the ring: the slot's use counted from 0, modulo 2
+    bool used = false;                // the ring has been round
+    for (int64_t unit = blockIdx.x; unit < (int64_t)runs * ks.n; unit += gridDim.x, ++unit_no) {
+        const int tile = (int)(unit / ks.n), piece = (int)(unit % ks.n);
         const int adapter = p.segs[3 * tile], first = p.segs[3 * tile + 1], count = p.segs[3 * tile + 2];
-        const int j0 = split * g.kc, nj = min((p.K + kBox - 1) / kBox - j0, g.kc);
-        if (warp == 0) {
-            // Lane i gathers rows 4 i .. 4 i + 3 (the last row again behind it).
-            const int groups = (count + 3) / 4;
-            int4 rows = make_int4(0, 0, 0, 0);
-            if (lane < groups) {
-                const int32_t* q = p.perm + first;
-                rows.x = q[4 * lane];
-                rows.y = q[min(4 * lane + 1, count - 1)];
-                rows.z = q[min(4 * lane + 2, count - 1)];
-                rows.w = q[min(4 * lane + 3, count - 1)];
+        const int j0 = piece * ks.size, nj = min(boxes - j0, ks.size);
+        auto next = [&]() {
+            if (++slot == g.stages) {
+                slot = 0;
+                phase ^= 1;
+                used = true;
             }
-            int sent = 0;
-            for (int j = 0; j < nj; ++j) {
-                const int s = j % g.stages;
-                if (j >= g.stages && !ptx::mbar_wait_warp(&empty[s], (j / g.stages - 1) & 1, s_abort, g.err, 31)) break;
-                uint8_t* at = smem + s * stage_bytes;
-                if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], groups * 512 + g.N * kBox * 2);
-                __syncwarp();
-                const int k = (j0 + j) * kBox;
-                if (lane < groups) tma_gather4(at + 512 * lane, &xmap, k, rows, &full[s]);
-                if (lane == 0) ptx::tma_load_2d(at + kBoxBytes, &amap, k, adapter * p.r, &full[s]);
-                sent = j + 1;
-            }
-            // (After a wait that gave up: the copies in flight end before the block does.)
-            if (ptx::aborted_warp(s_abort) && lane == 0)
-                for (int j = max(0, sent - g.stages); j < sent; ++j) ptx::mbar_wait_quiet(&full[j % g.stages], (j / g.stages) & 1, ptx::kWaitLimitNs);
-        } else if (warp == 1) {
+        };
+        if (warp == 1) {
             const uint32_t idesc = ptx::idesc_f16(kM, g.N, kBf16);
-            for (int j = 0; j < nj; ++j) {
-                const int s = j % g.stages;
-                if (!ptx::mbar_wait_warp(&full[s], (j / g.stages) & 1, s_abort, g.err, 32)) break;
+            for (int j = 0; j < nj; ++j, next()) {
+                if (!wait_warp(&full[slot], phase, s_abort, g.err, 32)) break;
                 ptx::tc_fence_after();
                 if (ptx::elect_one()) {
-                    const uint64_t a = ptx::sw128_desc(ptx::smem_u32(smem + s * stage_bytes));
-                    const uint64_t b = ptx::sw128_desc(ptx::smem_u32(smem + s * stage_bytes + kBoxBytes));
+                    const uint64_t a = ptx::sw128_desc(ptx::smem_u32(smem + slot * stage_bytes));
+                    const uint64_t b = ptx::sw128_desc(ptx::smem_u32(smem + slot * stage_bytes + kBoxBytes));
 #pragma unroll
                     for (int k = 0; k < kBox / 16; ++k) ptx::mma_f16(tmem, a + 2 * k, b + 2 * k, idesc, j > 0 || k > 0);
-                    ptx::mma_commit(&empty[s]);
+                    ptx::mma_commit(&empty[slot]);
                     if (j == nj - 1) ptx::mma_commit(done);
+                }
+                __syncwarp();
+            }
+        } else {
+            RowFetch f;
+            if (warp > 1) f.start(p.perm, first, 32 * (warp - 2), count);
+            const uint32_t bytes = warp == 0 ? g.N * kBox * 2 : f.bytes();
+            for (int j = 0; j < nj; ++j, next()) {
+                if (used && !wait_warp(&empty[slot], phase ^ 1, s_abort, g.err, 31)) break;
+                uint8_t* at = smem + slot * stage_bytes;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&full[slot], bytes);
+                    const int k = (j0 + j) * kBox;
+                    if (warp == 0) ptx::tma_load_2d(at + kBoxBytes, &amap, k, adapter * p.r, &full[slot]);
+                    else if (bytes) f.issue(at + 4096 * (warp - 2), &xmap, &xbox, k, &full[slot]);
                 }
                 __syncwarp();
             }
         }
         __syncwarp();
-        if (ptx::mbar_wait_warp(done, 0, s_abort, g.err, 33)) {
+        if (wait_warp(done, unit_no & 1, s_abort, g.err, 33)) {
             ptx::tc_fence_after();
-            const int row = 32 * warp + lane;
-            float* to = g.part + ((int64_t)split * p.n + first + row) * p.r;
-            const uint32_t tb = tmem + ((uint32_t)(32 * warp) << 16);
-            if (32 * warp < count)
+            const int q = warp & 3, row = 32 * q + lane;     // (the quarter of tensor memory that the warp can read)
+            float* to = g.part + ((int64_t)piece * p.n + first + row) * p.r;
+            const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16);
+            if (warp > 1 && 32 * q < count)
                 for (int c = 0; c < g.N; c += 16) {
                     float d[16];
                     ptx::tmem_ld16(tb + c, d);
@@ -146,7 +211,13 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
                     }
                 }
         }
+        ptx::tc_fence_before();
+        if (__syncthreads_or(*s_abort)) break;   // (and the accumulator is read)
+        ptx::tc_fence_after();
     }
+    // After a wait that gave up, copies may be in flight: they end before the block does.
+    if (*s_abort && threadIdx.x == 0)
+        for (int s = 0; s < g.stages; ++s) ptx::mbar_wait_quiet(&full[s], phase, ptx::kWaitLimitNs / 8);
     pdl_trigger();
     ptx::tc_fence_before();
     __syncthreads();
@@ -204,220 +275,224 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
     const uint32_t tmem = *s_tmem;
     pdl_wait();
 
-    const int tile = blockIdx.x, O = p.O;
-    const int n_tiles = (O + kNT - 1) / kNT, t0 = blockIdx.y * g.per, nt = min(n_tiles - t0, g.per);
-    const int runs = p.ctrl->n_rsegs;
-    const int adapter = tile < runs ? p.segs[3 * tile] : -1;
-    const int first = tile < runs ? p.segs[3 * tile + 1] : 0, count = tile < runs ? p.segs[3 * tile + 2] : 0;
-    if (adapter < 0 && p.copy && nt > 0) {
-        // Rows without an adapter (or none): base's elements as they are.
-        const int o0 = t0 * kNT, o1 = min(O, (t0 + nt) * kNT);
-        for (int i = warp; i < count; i += kEpiWarps + 2) {
-            const int64_t row = p.perm[first + i];
-            const int v = p.vec >= 4 ? 4 : 1;
-            for (int o = o0 + v * lane; o < o1; o += v * 32) {
-                float f[4] = {0.f, 0.f, 0.f, 0.f};
-                const int left = v == 1 ? 1 : o1 - o;
-                if (p.base) load4(p.out_type, p.base, row * p.base_stride + o, left, v == 4 && left >= 4, f);
-                store4(p.out_type, p.out, row * p.out_stride + o, left, v == 4 && left >= 4, f);
-            }
-        }
-    } else if (adapter >= 0 && nt > 0) {
-        // v of the tile's rows, split, in the products' layout: lanes of a row hold eight elements each.
-        if (tid < kM) s_rows[tid] = tid < count ? p.perm[first + tid] : 0;
-        const int chunks = g.N / 8;
-        int lanes = 2;
-        while (lanes < chunks) lanes *= 2;
-        const float scale = p.scale ? __ldg(p.scale + adapter) : 1.f;
-        const int per_warp = 32 / lanes, c8 = lane % lanes;
-        for (int i0 = warp * per_warp; i0 < count; i0 += (kEpiWarps + 2) * per_warp) {
-            const int row = i0 + lane / lanes;
-            const bool in = row < count && c8 * 8 < p.r;
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (in) {
-                const float* from = g.part + (int64_t)(first + row) * p.r + c8 * 8;
-                for (int s = 0; s < g.splits; ++s) {
-                    const float4 a = *reinterpret_cast<const float4*>(from + (int64_t)s * p.n * p.r);
-                    const float4 b = *reinterpret_cast<const float4*>(from + (int64_t)s * p.n * p.r + 4);
-                    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-                    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    const int O = p.O, n_tiles = (O + kNT - 1) / kNT, runs = p.ctrl->n_rsegs;
+    const Pieces ks = pieces(p.ctrl->n_active, (p.K + kBox - 1) / kBox, g.max_splits);
+    const Pieces os = pieces(runs, n_tiles, 64);
+    int done_tiles = 0;      // of this block, before this unit
+    for (int64_t unit = blockIdx.x; unit < (int64_t)runs * os.n; unit += gridDim.x) {
+        const int tile = (int)(unit / os.n), t0 = (int)(unit % os.n) * os.size, nt = min(n_tiles - t0, os.size);
+        const int adapter = p.segs[3 * tile], first = p.segs[3 * tile + 1], count = p.segs[3 * tile + 2];
+        if (adapter < 0 && p.copy) {
+            // Rows without an adapter: base's elements as they are.
+            const int o0 = t0 * kNT, o1 = min(O, (t0 + nt) * kNT);
+            for (int i = warp; i < count; i += kEpiWarps + 2) {
+                const int64_t row = p.perm[first + i];
+                const int v = p.vec >= 4 ? 4 : 1;
+                for (int o = o0 + v * lane; o < o1; o += v * 32) {
+                    float f[4] = {0.f, 0.f, 0.f, 0.f};
+                    const int left = v == 1 ? 1 : o1 - o;
+                    if (p.base) load4(p.out_type, p.base, row * p.base_stride + o, left, v == 4 && left >= 4, f);
+                    store4(p.out_type, p.out, row * p.out_stride + o, left, v == 4 && left >= 4, f);
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= scale;
             }
-            int e = 0;
-            if constexpr (!kBf16) {
-                float most = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) most = fmaxf(most, finite_abs(v[i]));
-                for (int o = 1; o < lanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                e = f16_shift(most);
-                if (row < count && c8 == 0) s_exp[row] = e;
-            }
-            uint16_t q[8][kParts];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) split<kBf16, kParts>(kBf16 ? v[i] : times_exp2(v[i], e), q[i]);
-            if (row < count && c8 < chunks) {
-                uint8_t* at = sV + (c8 >> 3) * kBoxBytes + row * 128 + (((c8 & 7) ^ (row & 7)) << 4);
-#pragma unroll
-                for (int m = 0; m < kParts; ++m)
-                    *reinterpret_cast<uint4*>(at + m * vbytes) =
-                        make_uint4(q[0][m] | (uint32_t)q[1][m] << 16, q[2][m] | (uint32_t)q[3][m] << 16, q[4][m] | (uint32_t)q[5][m] << 16,
-                                   q[6][m] | (uint32_t)q[7][m] << 16);
-            }
-        }
-        ptx::fence_proxy_async_smem();
-        __syncthreads();
-
-        if (warp == kEpiWarps + 1) {
-            int sent = 0;
-            for (int i = 0; i < nt; ++i) {
-                const int s = i % kRing;
-                if (i >= kRing && !ptx::mbar_wait_warp(&bempty[s], (i / kRing - 1) & 1, s_abort, g.err, 34)) break;
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(&bfull[s], vbytes);
-                    for (int b = 0; b < boxes; ++b)
-                        ptx::tma_load_2d(sB + s * vbytes + b * kBoxBytes, &bmap, b * kBox, adapter * O + (t0 + i) * kNT, &bfull[s]);
-                }
-                __syncwarp();
-                sent = i + 1;
-            }
-            if (ptx::aborted_warp(s_abort) && lane == 0)
-                for (int i = max(0, sent - kRing); i < sent; ++i) ptx::mbar_wait_quiet(&bfull[i % kRing], (i / kRing) & 1, ptx::kWaitLimitNs);
-        } else if (warp == kEpiWarps) {
-            const uint32_t idesc = ptx::idesc_f16(kM, kNT, kBf16);
-            const int steps = g.N / 16;
-            for (int i = 0; i < nt; ++i) {
-                const int s = i % kRing, buf = i & 1;
-                if (!ptx::mbar_wait_warp(&bfull[s], (i / kRing) & 1, s_abort, g.err, 35)) break;
-                if (i >= 2 && !ptx::mbar_wait_warp(&tempty[buf], (i / 2 - 1) & 1, s_abort, g.err, 36)) break;
-                ptx::tc_fence_after();
-                if (ptx::elect_one()) {
-                    uint32_t more = 0;
-                    for (int m = kParts - 1; m >= 0; --m)     // the smallest part first
-                        for (int k = 0; k < steps; ++k) {
-                            ptx::mma_f16(tmem + buf * kNT, ptx::sw128_desc(ptx::smem_u32(sV + m * vbytes + (k / 4) * kBoxBytes)) + 2 * (k % 4),
-                                         ptx::sw128_desc(ptx::smem_u32(sB + s * vbytes + (k / 4) * kBoxBytes)) + 2 * (k % 4), idesc, more);
-                            more = 1;
-                        }
-                    ptx::mma_commit(&bempty[s]);
-                    ptx::mma_commit(&tfull[buf]);
-                }
-                __syncwarp();
-            }
-        } else {
-            // Rows 32 q .. 32 q + 31 of the tile, 64 of the 128 outputs in two passes of 32.
-            const int q = warp & 3, half = warp >> 2;
-            float* stage = reinterpret_cast<float*>(sStage + warp * kStageBytes);
-            const bool some = 32 * q < count;
-            constexpr int kV = kF32 ? 4 : 8;                  // elements of 16 bytes
-            constexpr int kCol = 32 / kV, kIts = kCol;        // threads of a row; rows of a thread (32 / (32 / kCol))
-            const int c = (lane % kCol) * kV, r0 = 32 * q + lane / kCol;
-            int rows[kIts];
-#pragma unroll
-            for (int it = 0; it < kIts; ++it) {
-                const int r = r0 + it * (32 / kCol);
-                rows[it] = r < count ? s_rows[r] : -1;
-            }
-            const uint8_t* base = reinterpret_cast<const uint8_t*>(p.base);
-            constexpr int kSize = kF32 ? 4 : 2;
-            const bool wide = p.vec * kSize >= 16;
-            uint4 was[2][kIts];
-            // Base's elements of pass `pass` (two a tile) of this block.
-            auto fetch = [&](int pass, uint4 (&to)[kIts]) {
-                const int o = (t0 + (pass >> 1)) * kNT + half * 64 + (pass & 1) * 32 + c;
-#pragma unroll
-                for (int it = 0; it < kIts; ++it)
-                    if (rows[it] >= 0 && o + kV <= O)
-                        to[it] = *reinterpret_cast<const uint4*>(base + ((int64_t)rows[it] * p.base_stride + o) * kSize);
-            };
-            const bool early = wide && base != nullptr;
-            if (early) fetch(0, was[0]);
-            for (int i = 0; i < nt; ++i) {
-                const int buf = i & 1;
-                if (!ptx::mbar_wait_warp(&tfull[buf], (i >> 1) & 1, s_abort, g.err, 37)) break;
-                ptx::tc_fence_after();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int pass = 2 * i + h;
-                    if (early && pass + 1 < 2 * nt) fetch(pass + 1, was[(h + 1) & 1]);
-                    if (some) {
-                        const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * kNT + half * 64 + h * 32;
-                        float d[16];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            ptx::tmem_ld16(tb + 16 * u, d);
-#pragma unroll
-                            for (int w = 0; w < 4; ++w)
-                                *reinterpret_cast<float4*>(stage + lane * kStageRow + 16 * u + 4 * w) =
-                                    make_float4(d[4 * w], d[4 * w + 1], d[4 * w + 2], d[4 * w + 3]);
-                        }
+        } else if (adapter >= 0) {
+            // v of the tile's rows, split, in the products' layout: lanes of a row hold eight elements each.
+            if (tid < kM) s_rows[tid] = tid < count ? p.perm[first + tid] : 0;
+            const int chunks = g.N / 8;
+            int lanes = 2;
+            while (lanes < chunks) lanes *= 2;
+            const float scale = p.scale ? __ldg(p.scale + adapter) : 1.f;
+            const int per_warp = 32 / lanes, c8 = lane % lanes;
+            for (int i0 = warp * per_warp; i0 < count; i0 += (kEpiWarps + 2) * per_warp) {
+                const int row = i0 + lane / lanes;
+                const bool in = row < count && c8 * 8 < p.r;
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (in) {
+                    const float* from = g.part + (int64_t)(first + row) * p.r + c8 * 8;
+                    for (int s = 0; s < ks.n; ++s) {
+                        const float4 a = *reinterpret_cast<const float4*>(from + (int64_t)s * p.n * p.r);
+                        const float4 b = *reinterpret_cast<const float4*>(from + (int64_t)s * p.n * p.r + 4);
+                        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+                        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
                     }
-                    if (h == 1) {                             // the accumulator is read
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        ptx::mbar_arrive_elect(&tempty[buf]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] *= scale;
+                }
+                int e = 0;
+                if constexpr (!kBf16) {
+                    float most = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) most = fmaxf(most, finite_abs(v[i]));
+                    for (int o = 1; o < lanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    e = f16_shift(most);
+                    if (row < count && c8 == 0) s_exp[row] = e;
+                }
+                uint16_t q[8][kParts];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split<kBf16, kParts>(kBf16 ? v[i] : times_exp2(v[i], e), q[i]);
+                if (row < count && c8 < chunks) {
+                    uint8_t* at = sV + (c8 >> 3) * kBoxBytes + row * 128 + (((c8 & 7) ^ (row & 7)) << 4);
+#pragma unroll
+                    for (int m = 0; m < kParts; ++m)
+                        *reinterpret_cast<uint4*>(at + m * vbytes) =
+                            make_uint4(q[0][m] | (uint32_t)q[1][m] << 16, q[2][m] | (uint32_t)q[3][m] << 16, q[4][m] | (uint32_t)q[5][m] << 16,
+                                       q[6][m] | (uint32_t)q[7][m] << 16);
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            __syncthreads();
+
+            if (warp == kEpiWarps + 1) {
+                int sent = done_tiles;
+                for (int i = 0; i < nt; ++i, ++sent) {
+                    const int s = sent % kRing;
+                    if (sent >= kRing && !wait_warp(&bempty[s], (sent / kRing - 1) & 1, s_abort, g.err, 34)) break;
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(&bfull[s], vbytes);
+                        for (int b = 0; b < boxes; ++b)
+                            ptx::tma_load_2d(sB + s * vbytes + b * kBoxBytes, &bmap, b * kBox, adapter * O + (t0 + i) * kNT, &bfull[s]);
                     }
                     __syncwarp();
-                    if (some) {
-                        const int o_pass = (t0 + i) * kNT + half * 64 + h * 32;
-                        if (wide) {
-                            const int o = o_pass + c;
-#pragma unroll
-                            for (int it = 0; it < kIts; ++it) {
-                                if (rows[it] < 0 || o >= O) continue;
-                                const int r = lane / kCol + it * (32 / kCol);
-                                float y[kV];
-#pragma unroll
-                                for (int w = 0; w < kV / 4; ++w) {
-                                    const float4 f = *reinterpret_cast<const float4*>(stage + r * kStageRow + c + 4 * w);
-                                    y[4 * w] = f.x; y[4 * w + 1] = f.y; y[4 * w + 2] = f.z; y[4 * w + 3] = f.w;
-                                }
-                                if constexpr (!kBf16) {
-                                    const int e = -s_exp[32 * q + r];
-#pragma unroll
-                                    for (int w = 0; w < kV; ++w) y[w] = times_exp2(y[w], e);
-                                }
-                                const int64_t at = (int64_t)rows[it] * p.out_stride + o;
-                                if (o + kV <= O) {
-                                    if (base) add_raw<kF32>(p.out_type, was[h & 1][it], y);
-                                    store_raw<kF32>(p.out_type, p.out, at, y);
-                                } else {
-#pragma unroll
-                                    for (int w = 0; w < kV; ++w)
-                                        if (o + w < O) {
-                                            if (base) y[w] += load_one<kF32>(p.out_type, base, (int64_t)rows[it] * p.base_stride + o + w);
-                                            store_one<kF32>(p.out_type, p.out, at + w, y[w]);
-                                        }
-                                }
+                }
+                if (ptx::aborted_warp(s_abort) && lane == 0)
+                    for (int i = max(0, sent - kRing); i < sent; ++i) ptx::mbar_wait_quiet(&bfull[i % kRing], (i / kRing) & 1, ptx::kWaitLimitNs);
+            } else if (warp == kEpiWarps) {
+                const uint32_t idesc = ptx::idesc_f16(kM, kNT, kBf16);
+                const int steps = g.N / 16;
+                for (int i = 0; i < nt; ++i) {
+                    const int at = done_tiles + i, s = at % kRing, buf = at & 1;
+                    if (!wait_warp(&bfull[s], (at / kRing) & 1, s_abort, g.err, 35)) break;
+                    if (at >= 2 && !wait_warp(&tempty[buf], (at / 2 - 1) & 1, s_abort, g.err, 36)) break;
+                    ptx::tc_fence_after();
+                    if (ptx::elect_one()) {
+                        uint32_t more = 0;
+                        for (int m = kParts - 1; m >= 0; --m)     // the smallest part first
+                            for (int k = 0; k < steps; ++k) {
+                                ptx::mma_f16(tmem + buf * kNT, ptx::sw128_desc(ptx::smem_u32(sV + m * vbytes + (k / 4) * kBoxBytes)) + 2 * (k % 4),
+                                             ptx::sw128_desc(ptx::smem_u32(sB + s * vbytes + (k / 4) * kBoxBytes)) + 2 * (k % 4), idesc, more);
+                                more = 1;
                             }
-                        } else {
-                            // Neighbouring lanes at neighbouring elements, eight rows in flight.
-                            const int o = o_pass + lane;
-                            for (int b0 = 0; b0 < 32 && 32 * q + b0 < count; b0 += 8) {
-                                float y[8];
+                        ptx::mma_commit(&bempty[s]);
+                        ptx::mma_commit(&tfull[buf]);
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // Rows 32 q .. 32 q + 31 of the tile, 64 of the 128 outputs in two passes of 32.
+                const int q = warp & 3, half = warp >> 2;
+                float* stage = reinterpret_cast<float*>(sStage + warp * kStageBytes);
+                const bool some = 32 * q < count;
+                constexpr int kV = kF32 ? 4 : 8;                  // elements of 16 bytes
+                constexpr int kCol = 32 / kV, kIts = kCol;        // threads of a row; rows of a thread (32 / (32 / kCol))
+                const int c = (lane % kCol) * kV, r0 = 32 * q + lane / kCol;
+                int rows[kIts];
 #pragma unroll
-                                for (int w = 0; w < 8; ++w) {
-                                    const int r = 32 * q + b0 + w;
-                                    if (base && r < count && o < O) y[w] = load_one<kF32>(p.out_type, p.base, (int64_t)s_rows[r] * p.base_stride + o);
-                                    else y[w] = 0.f;
+                for (int it = 0; it < kIts; ++it) {
+                    const int r = r0 + it * (32 / kCol);
+                    rows[it] = r < count ? s_rows[r] : -1;
+                }
+                const uint8_t* base = reinterpret_cast<const uint8_t*>(p.base);
+                constexpr int kSize = kF32 ? 4 : 2;
+                const bool wide = p.vec * kSize >= 16;
+                uint4 was[2][kIts];
+                // Base's elements of pass `pass` (two a tile) of this block.
+                auto fetch = [&](int pass, uint4 (&to)[kIts]) {
+                    const int o = (t0 + (pass >> 1)) * kNT + half * 64 + (pass & 1) * 32 + c;
+#pragma unroll
+                    for (int it = 0; it < kIts; ++it)
+                        if (rows[it] >= 0 && o + kV <= O)
+                            to[it] = *reinterpret_cast<const uint4*>(base + ((int64_t)rows[it] * p.base_stride + o) * kSize);
+                };
+                const bool early = wide && base != nullptr;
+                if (early) fetch(0, was[0]);
+                for (int i = 0; i < nt; ++i) {
+                    const int buf = (done_tiles + i) & 1;
+                    if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) break;
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int pass = 2 * i + h;
+                        if (early && pass + 1 < 2 * nt) fetch(pass + 1, was[(h + 1) & 1]);
+                        if (some) {
+                            const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * kNT + half * 64 + h * 32;
+                            float d[16];
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                ptx::tmem_ld16(tb + 16 * u, d);
+#pragma unroll
+                                for (int w = 0; w < 4; ++w)
+                                    *reinterpret_cast<float4*>(stage + lane * kStageRow + 16 * u + 4 * w) =
+                                        make_float4(d[4 * w], d[4 * w + 1], d[4 * w + 2], d[4 * w + 3]);
+                            }
+                        }
+                        if (h == 1) {                             // the accumulator is read
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            ptx::mbar_arrive_elect(&tempty[buf]);
+                        }
+                        __syncwarp();
+                        if (some) {
+                            const int o_pass = (t0 + i) * kNT + half * 64 + h * 32;
+                            if (wide) {
+                                const int o = o_pass + c;
+#pragma unroll
+                                for (int it = 0; it < kIts; ++it) {
+                                    if (rows[it] < 0 || o >= O) continue;
+                                    const int r = lane / kCol + it * (32 / kCol);
+                                    float y[kV];
+#pragma unroll
+                                    for (int w = 0; w < kV / 4; ++w) {
+                                        const float4 f = *reinterpret_cast<const float4*>(stage + r * kStageRow + c + 4 * w);
+                                        y[4 * w] = f.x; y[4 * w + 1] = f.y; y[4 * w + 2] = f.z; y[4 * w + 3] = f.w;
+                                    }
+                                    if constexpr (!kBf16) {
+                                        const int e = -s_exp[32 * q + r];
+#pragma unroll
+                                        for (int w = 0; w < kV; ++w) y[w] = times_exp2(y[w], e);
+                                    }
+                                    const int64_t at = (int64_t)rows[it] * p.out_stride + o;
+                                    if (o + kV <= O) {
+                                        if (base) add_raw<kF32>(p.out_type, was[h & 1][it], y);
+                                        store_raw<kF32>(p.out_type, p.out, at, y);
+                                    } else {
+#pragma unroll
+                                        for (int w = 0; w < kV; ++w)
+                                            if (o + w < O) {
+                                                if (base) y[w] += load_one<kF32>(p.out_type, base, (int64_t)rows[it] * p.base_stride + o + w);
+                                                store_one<kF32>(p.out_type, p.out, at + w, y[w]);
+                                            }
+                                    }
                                 }
+                            } else {
+                                // Neighbouring lanes at neighbouring elements, eight rows in flight.
+                                const int o = o_pass + lane;
+                                for (int b0 = 0; b0 < 32 && 32 * q + b0 < count; b0 += 8) {
+                                    float y[8];
 #pragma unroll
-                                for (int w = 0; w < 8; ++w) {
-                                    const int r = 32 * q + b0 + w;
-                                    if (r < count && o < O) {
-                                        float v = stage[(b0 + w) * kStageRow + lane];
-                                        if constexpr (!kBf16) v = times_exp2(v, -s_exp[r]);
-                                        store_one<kF32>(p.out_type, p.out, (int64_t)s_rows[r] * p.out_stride + o, base ? y[w] + v : v);
+                                    for (int w = 0; w < 8; ++w) {
+                                        const int r = 32 * q + b0 + w;
+                                        if (base && r < count && o < O) y[w] = load_one<kF32>(p.out_type, p.base, (int64_t)s_rows[r] * p.base_stride + o);
+                                        else y[w] = 0.f;
+                                    }
+#pragma unroll
+                                    for (int w = 0; w < 8; ++w) {
+                                        const int r = 32 * q + b0 + w;
+                                        if (r < count && o < O) {
+                                            float v = stage[(b0 + w) * kStageRow + lane];
+                                            if constexpr (!kBf16) v = times_exp2(v, -s_exp[r]);
+                                            store_one<kF32>(p.out_type, p.out, (int64_t)s_rows[r] * p.out_stride + o, base ? y[w] + v : v);
+                                        }
                                     }
                                 }
                             }
                         }
+                        __syncwarp();                             // the staging is read
                     }
-                    __syncwarp();                             // the staging is read
                 }
             }
+            done_tiles += nt;
         }
+        if (__syncthreads_or(*s_abort)) break;   // (and v and the rows' numbers are read)
     }
     pdl_trigger();
     ptx::tc_fence_before();
@@ -443,43 +518,37 @@ cudaError_t configure(Kern kern, int slot) {
 
 }  // namespace
 
-bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[3]) {
+bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[4]) {
     // (Coordinates are 32-bit; strides fit 40 bits.)
     if ((int64_t)p.L * p.O > INT32_MAX || p.x_stride * 2 >= (int64_t)1 << 40) return false;
     const CUtensorMapDataType t = x_type == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const uint32_t N = (p.r + 15) / 16 * 16;
     return make_map(&maps[0], p.x, t, 2, p.K, p.n, kBox, 1, CU_TENSOR_MAP_SWIZZLE_128B, p.x_stride) &&
            make_map(&maps[1], p.a, t, 2, p.K, (uint64_t)p.L * p.r, kBox, N, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           make_map(&maps[3], p.x, t, 2, p.K, p.n, kBox, 32, CU_TENSOR_MAP_SWIZZLE_128B, p.x_stride) &&
            make_map(&maps[2], p.b, t, 2, p.r, (uint64_t)p.L * p.O, kBox, kNT, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[3], float* part, int32_t* err, int max_segs,
+cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[4], float* part, int32_t* err, int max_segs,
                            cudaStream_t st) {
     TcArgs g{};
     g.p = p;
     g.N = (p.r + 15) / 16 * 16;
     g.part = part;
+    g.max_splits = (int)std::min<int64_t>(kLoraMaxSplits, lora_part_rows(p.n) / p.n);
     g.err = err;
-    // Stretches of K and of the outputs: about kLoraBlocks blocks, two an SM.
-    const int tiles = (p.n + kM - 1) / kM, boxes = (p.K + kBox - 1) / kBox;
-    const int want = (kLoraBlocks + tiles - 1) / tiles;
-    g.kc = (boxes + std::min(want, kLoraMaxSplits) - 1) / std::min(want, kLoraMaxSplits);
-    g.splits = (boxes + g.kc - 1) / g.kc;
     const int stage = kBoxBytes + g.N * kBox * 2;
-    g.stages = std::min(g.kc, 100 * 1024 / stage);
+    g.stages = std::min((p.K + kBox - 1) / kBox, 100 * 1024 / stage);
     g.tmem_cols = 32;
     while (g.tmem_cols < g.N) g.tmem_cols *= 2;
     const size_t smem = 1024 + (size_t)g.stages * stage + 256;
     auto shrink = x_type == MOE_BF16 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>;
     cudaError_t e = configure(shrink, x_type == MOE_BF16 ? 0 : 1);
     if (e != cudaSuccess) return e;
-    if ((e = launch_pdl(shrink, dim3(max_segs, g.splits), dim3(kShrinkThreads), smem, st, maps[0], maps[1], g)) != cudaSuccess) return e;
+    if ((e = launch_pdl(shrink, dim3((unsigned)std::min<int64_t>(kLoraBlocks, (int64_t)max_segs * g.max_splits)), dim3(kShrinkThreads), smem, st, maps[0], maps[3], maps[1], g)) != cudaSuccess) return e;
 
     const bool f32 = p.out_type == MOE_F32, bf = x_type == MOE_BF16;
-    const int n_tiles = (p.O + kNT - 1) / kNT;
-    const int parts = std::min({want, n_tiles, 65535});
-    g.per = (n_tiles + parts - 1) / parts;
-    const dim3 grid(max_segs, (n_tiles + g.per - 1) / g.per);
+    const dim3 grid((unsigned)std::min<int64_t>(kLoraBlocks, (int64_t)max_segs * ((p.O + kNT - 1) / kNT)));
     auto expand = bf ? (f32 ? lora_expand_kernel<true, true> : lora_expand_kernel<true, false>)
                      : (f32 ? lora_expand_kernel<false, true> : lora_expand_kernel<false, false>);
     if ((e = configure(expand, 2 + (bf ? 0 : 2) + (f32 ? 1 : 0))) != cudaSuccess) return e;
