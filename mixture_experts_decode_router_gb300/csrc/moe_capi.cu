@@ -939,14 +939,15 @@ moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b
         return MOE_ERR_ALIGNMENT;
     if (overlap(X, Y) || (overlap(Y0, Y) && !same_rows(Y0, Y))) return MOE_ERR_ALIAS;
     if (ws_bytes < lora_workspace(n, cfg->num_adapters, cfg->rank)) return MOE_ERR_WORKSPACE;
-    const int where = residency(x);
-    if (where < 0 || residency(out) < 0 || (base && residency(base) < 0)) return MOE_ERR_HOST_MEMORY;
+    const int at_x = residency(x), at_out = residency(out), at_base = base ? residency(base) : 0;
+    if (at_x < 0 || at_out < 0 || at_base < 0) return MOE_ERR_HOST_MEMORY;
     LoraParams p{};
     p.a = static_cast<const uint16_t*>(a);
     p.b = static_cast<const uint16_t*>(b);
     p.scale = scale;
     p.x = static_cast<const uint16_t*>(x);
-    p.x_host = where == 1;
+    p.x_host = at_x == 1;
+    p.out_host = at_out == 1 || at_base == 1;
     p.idx = idx;
     p.base = base;
     p.out = out;

@@ -223,7 +223,7 @@ struct LoraParams {
     void* out;
     int64_t x_stride, base_stride, out_stride;
     int n, K, O, r, L, out_type;
-    bool x_host;               // x is pinned host memory
+    bool x_host, out_host;     // x; base or out: it is pinned host memory
     // Set by launch_lora.
     int vec;                   // elements of base's and out's rows that can be read at once: 8, 4 or 1
     bool copy;                 // rows without an adapter are to be written

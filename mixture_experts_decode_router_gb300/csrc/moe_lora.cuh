@@ -93,23 +93,23 @@ __device__ __forceinline__ void store4(int type, void* p, int64_t at, int left, 
     }
 }
 
-// Single elements, and the 16 bytes of four (kF32) or eight.
-template <bool kF32> __device__ __forceinline__ float load_one(int type, const void* p, int64_t at) {
-    if constexpr (kF32) return reinterpret_cast<const float*>(p)[at];
+// Single elements, and the 16 bytes of four (fp32) or eight.
+template <int kType> __device__ __forceinline__ float load_one(const void* p, int64_t at) {
+    if constexpr (kType == MOE_F32) return reinterpret_cast<const float*>(p)[at];
     const uint16_t u = reinterpret_cast<const uint16_t*>(p)[at];
-    return type == MOE_BF16 ? bf16_lo(u) : __half2float(__ushort_as_half(u));
+    return kType == MOE_BF16 ? bf16_lo(u) : __half2float(__ushort_as_half(u));
 }
-template <bool kF32> __device__ __forceinline__ void store_one(int type, void* p, int64_t at, float v) {
-    if constexpr (kF32) reinterpret_cast<float*>(p)[at] = v;
-    else reinterpret_cast<uint16_t*>(p)[at] = type == MOE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+template <int kType> __device__ __forceinline__ void store_one(void* p, int64_t at, float v) {
+    if constexpr (kType == MOE_F32) reinterpret_cast<float*>(p)[at] = v;
+    else reinterpret_cast<uint16_t*>(p)[at] = kType == MOE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
-template <bool kF32> __device__ __forceinline__ void add_raw(int type, const uint4& was, float* y) {
+template <int kType> __device__ __forceinline__ void add_raw(const uint4& was, float* y) {
     const uint32_t u[4] = {was.x, was.y, was.z, was.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (kF32) {
+        if constexpr (kType == MOE_F32) {
             y[i] += __uint_as_float(u[i]);
-        } else if (type == MOE_BF16) {
+        } else if constexpr (kType == MOE_BF16) {
             y[2 * i] += bf16_lo(u[i]);
             y[2 * i + 1] += bf16_hi(u[i]);
         } else {
@@ -119,13 +119,13 @@ template <bool kF32> __device__ __forceinline__ void add_raw(int type, const uin
         }
     }
 }
-template <bool kF32> __device__ __forceinline__ void store_raw(int type, void* p, int64_t at, const float* y) {
+template <int kType> __device__ __forceinline__ uint4 pack_raw(const float* y) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (kF32) {
+        if constexpr (kType == MOE_F32) {
             u[i] = __float_as_uint(y[i]);
-        } else if (type == MOE_BF16) {
+        } else if constexpr (kType == MOE_BF16) {
             const __nv_bfloat162 q = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
             u[i] = *reinterpret_cast<const uint32_t*>(&q);
         } else {
@@ -133,7 +133,7 @@ template <bool kF32> __device__ __forceinline__ void store_raw(int type, void* p
             u[i] = *reinterpret_cast<const uint32_t*>(&q);
         }
     }
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p) + at * (kF32 ? 4 : 2)) = make_uint4(u[0], u[1], u[2], u[3]);
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 }  // namespace moe

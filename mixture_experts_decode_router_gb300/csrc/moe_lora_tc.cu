@@ -15,6 +15,7 @@
 // along their rows, 16 bytes a thread where they are aligned and by neighbouring elements where they
 // are not, base's loads in flight while the products run.
 #include <mutex>
+#include <type_traits>
 
 #include "moe_launch.cuh"
 #include "moe_lora.cuh"
@@ -34,6 +35,8 @@ struct TcArgs {
     int max_splits;   // of K: as many as part holds
     int stages;       // shrink: ring
     int tmem_cols;    // shrink
+    int slots;        // expand: passes of a warp in shared memory (0: results alone)
+    int expand_blocks;
     float* part;      // [splits][n][r]
     int32_t* err;
 };
@@ -51,6 +54,31 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// 16 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// 64 columns of 32 lanes of tensor memory: the thread's lane's.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+        "%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,"
+        "%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+          "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]),
+          "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]),
+          "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+}
+
 // A wait of the whole warp that tries for some microseconds before it begins to count the time (the
 // timer's first reading alone takes a microsecond, which every wait of a ring would pay).
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* err, int32_t code) {
@@ -65,17 +93,20 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 struct Pieces {
     int n, size;
 };
-__device__ __forceinline__ Pieces pieces(int runs, int size, int most) {
-    int best = 1;
-    float cost = 1e30f;
-    for (int c = 1; c <= min(most, size); ++c) {
-        const int per = (size + c - 1) / c;
-        const float t = (float)((runs * c + kLoraBlocks - 1) / kLoraBlocks) * ((float)per / size + 0.02f);
-        if (t < cost) {
-            cost = t;
-            best = c;
+__device__ __forceinline__ Pieces pieces(int runs, int size, int most, int blocks) {
+    // Lane i weighs i + 1 and i + 33 pieces; the costs, in whole warps' agreement, by their upper bits.
+    const int lane = threadIdx.x & 31;
+    uint32_t key = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = lane + 1 + 32 * i;
+        if (c <= min(most, size)) {
+            const int per = (size + c - 1) / c;
+            const float cost = (float)((runs * c + blocks - 1) / blocks) * ((float)per / size + 0.02f);
+            key = min(key, (__float_as_uint(cost) & ~63u) | (uint32_t)(c - 1));
         }
     }
+    const int best = (int)(__reduce_min_sync(0xffffffffu, key) & 63u) + 1;
     const int per = (size + best - 1) / best;
     return {(size + per - 1) / per, per};
 }
@@ -148,7 +179,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
     pdl_wait();
 
     const int runs = p.ctrl->n_active, boxes = (p.K + kBox - 1) / kBox;
-    const Pieces ks = pieces(runs, boxes, g.max_splits);
+    const Pieces ks = pieces(runs, boxes, g.max_splits, kLoraBlocks);
     int slot = 0, unit_no = 0;
     uint32_t phase = 0;               // of the ring: the slot's use counted from 0, modulo 2
     bool used = false;                // the ring has been round
@@ -235,14 +266,27 @@ constexpr int kStageRow = 36;            // floats of a row of a warp's staging 
 constexpr int kStageBytes = 32 * kStageRow * 4;
 
 __host__ __device__ constexpr int expand_parts(bool f32) { return f32 ? 3 : 2; }
-inline size_t expand_smem(int rank16, bool f32) {
+constexpr int kPassBytes = 32 * 128;     // base's or out's 128 bytes of 32 rows
+constexpr size_t kMaxSmem = 226 * 1024;  // (beside 1 KB of static arrays)
+inline size_t expand_smem(int rank16, bool f32, int slots) {
     const int boxes = (rank16 + kBox - 1) / kBox;
-    return 1024 + (size_t)(expand_parts(f32) + kRing) * boxes * kBoxBytes + kEpiWarps * kStageBytes + 256;
+    return 1024 + (size_t)(expand_parts(f32) + kRing) * boxes * kBoxBytes + kEpiWarps * (slots ? slots * kPassBytes : kStageBytes) + 512;
 }
 
-template <bool kBf16, bool kF32>
-__global__ void __launch_bounds__(kExpandThreads, kF32 ? 1 : 2)
+// The first `count` elements of 16 bytes, one by one (rows that end inside them).
+template <int kSize> __device__ __noinline__ void copy_elements(uint8_t* to, const uint8_t* from, int count) {
+    for (int i = 0; i < count; ++i) {
+        if constexpr (kSize == 4) reinterpret_cast<uint32_t*>(to)[i] = reinterpret_cast<const uint32_t*>(from)[i];
+        else reinterpret_cast<uint16_t*>(to)[i] = reinterpret_cast<const uint16_t*>(from)[i];
+    }
+}
+
+// kWide: rows of base and out that are aligned to 16 bytes (a ring of g.slots passes of each warp in
+// shared memory).
+template <bool kBf16, int kOut, bool kWide>
+__global__ void __launch_bounds__(kExpandThreads, kWide || kOut == MOE_F32 ? 1 : 2)
 lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
+    constexpr bool kF32 = kOut == MOE_F32;
     constexpr int kParts = expand_parts(kF32);
     extern __shared__ __align__(1024) uint8_t raw[];
     __shared__ int32_t s_rows[kM], s_exp[kM];
@@ -251,7 +295,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
     uint8_t* sV = align1024(raw);                       // [part][box][128 rows x 128 bytes]
     uint8_t* sB = sV + kParts * vbytes;                 // [stage][box][128 outputs x 128 bytes]
     uint8_t* sStage = sB + kRing * vbytes;
-    uint64_t* bfull = reinterpret_cast<uint64_t*>(sStage + kEpiWarps * kStageBytes);
+    uint64_t* bfull = reinterpret_cast<uint64_t*>(sStage + kEpiWarps * (kWide ? g.slots * kPassBytes : kStageBytes));
     uint64_t *bempty = bfull + kRing, *tfull = bempty + kRing, *tempty = tfull + 2;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
@@ -276,72 +320,206 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
     pdl_wait();
 
     const int O = p.O, n_tiles = (O + kNT - 1) / kNT, runs = p.ctrl->n_rsegs;
-    const Pieces ks = pieces(p.ctrl->n_active, (p.K + kBox - 1) / kBox, g.max_splits);
-    const Pieces os = pieces(runs, n_tiles, 64);
+    const Pieces ks = pieces(p.ctrl->n_active, (p.K + kBox - 1) / kBox, g.max_splits, kLoraBlocks);
+    const Pieces os = pieces(runs, n_tiles, 64, g.expand_blocks);
     int done_tiles = 0;      // of this block, before this unit
+    constexpr int kSize = kF32 ? 4 : 2, kV = 16 / kSize;        // elements of 16 bytes
+    constexpr int kCols = 128 / kSize, kPasses = 64 / kCols;    // a pass: 128 bytes of the warp's 32 rows
     for (int64_t unit = blockIdx.x; unit < (int64_t)runs * os.n; unit += gridDim.x) {
         const int tile = (int)(unit / os.n), t0 = (int)(unit % os.n) * os.size, nt = min(n_tiles - t0, os.size);
         const int adapter = p.segs[3 * tile], first = p.segs[3 * tile + 1], count = p.segs[3 * tile + 2];
         if (adapter < 0 && p.copy) {
             // Rows without an adapter: base's elements as they are.
             const int o0 = t0 * kNT, o1 = min(O, (t0 + nt) * kNT);
+            constexpr int kU = 4;
             for (int i = warp; i < count; i += kEpiWarps + 2) {
                 const int64_t row = p.perm[first + i];
-                const int v = p.vec >= 4 ? 4 : 1;
-                for (int o = o0 + v * lane; o < o1; o += v * 32) {
-                    float f[4] = {0.f, 0.f, 0.f, 0.f};
-                    const int left = v == 1 ? 1 : o1 - o;
-                    if (p.base) load4(p.out_type, p.base, row * p.base_stride + o, left, v == 4 && left >= 4, f);
-                    store4(p.out_type, p.out, row * p.out_stride + o, left, v == 4 && left >= 4, f);
+                const uint8_t* from = reinterpret_cast<const uint8_t*>(p.base) + row * p.base_stride * kSize;
+                uint8_t* to = reinterpret_cast<uint8_t*>(p.out) + row * p.out_stride * kSize;
+                int o = o0;
+                if (p.vec >= kV) {
+                    for (; o + kV * 32 <= o1; o += kU * kV * 32) {
+                        uint4 v[kU];
+#pragma unroll
+                        for (int u = 0; u < kU; ++u) {
+                            const int at = o + (u * 32 + lane) * kV;
+                            v[u] = p.base && at + kV <= o1 ? *reinterpret_cast<const uint4*>(from + (size_t)at * kSize) : make_uint4(0u, 0u, 0u, 0u);
+                        }
+#pragma unroll
+                        for (int u = 0; u < kU; ++u) {
+                            const int at = o + (u * 32 + lane) * kV;
+                            if (at + kV <= o1) *reinterpret_cast<uint4*>(to + (size_t)at * kSize) = v[u];
+                        }
+                    }
+                    o = min(o, o0 + (o1 - o0) / kV * kV);
                 }
+                for (o += lane; o < o1; o += 32)
+                    store_one<kOut>(p.out, row * p.out_stride + o, p.base ? load_one<kOut>(p.base, row * p.base_stride + o) : 0.f);
             }
         } else if (adapter >= 0) {
+            const int q = warp & 3, half = warp >> 2, here = warp < kEpiWarps ? min(32, count - 32 * q) : 0;
+            if (warp < kEpiWarps && half == 0 && lane < here) s_rows[32 * q + lane] = p.perm[first + 32 * q + lane];
+            // kWide: lane i takes 16 bytes (i % 8) of the warp's rows i / 8, i / 8 + 4, ... (the last row again behind
+            // it, which is not written); base's of the first passes are on their way while v is formed.
+            const int chunk = lane & 7, r8 = lane >> 3, valid = here > r8 ? (here - r8 + 3) / 4 : 0;
+            const uint8_t* from[8];
+            uint8_t* to[8];
+            uint8_t* mine = sStage + warp * g.slots * kPassBytes;
+            uint8_t* across[2] = {mine + r8 * 128 + ((chunk ^ r8) << 4), mine + r8 * 128 + ((chunk ^ (r8 + 4)) << 4)};   // rows 4 it + r8
+            const int last = nt * kPasses;
+            auto column = [&](int pass) { return (t0 + pass / kPasses) * kNT + half * 64 + pass % kPasses * kCols; };
+            auto fetch = [&](int pass, int slot) {
+                if (p.base && pass < last) {
+                    const int o = column(pass) + chunk * kV;
+                    const size_t at = (size_t)column(pass) * kSize;
+                    if (o + kV <= O) {
+#pragma unroll
+                        for (int it = 0; it < 8; ++it) cp_async16(across[it & 1] + slot * kPassBytes + it * 512, from[it] + at);
+                    } else if (o < O) {
+#pragma unroll
+                        for (int it = 0; it < 8; ++it)
+                            if (it < valid) copy_elements<kSize>(across[it & 1] + slot * kPassBytes + it * 512, from[it] + at, O - o);
+                    }
+                }
+                cp_commit();
+            };
+            if constexpr (kWide) {
+                if (here > 0) {
+#pragma unroll
+                    for (int it = 0; it < 8; ++it) {
+                        const int64_t row = p.perm[first + 32 * q + min(4 * it + r8, here - 1)];
+                        from[it] = reinterpret_cast<const uint8_t*>(p.base) + row * p.base_stride * kSize + chunk * 16;
+                        to[it] = reinterpret_cast<uint8_t*>(p.out) + row * p.out_stride * kSize + chunk * 16;
+                    }
+                    for (int i = 0; i < g.slots - 1; ++i) fetch(i, i);
+                }
+            }
             // v of the tile's rows, split, in the products' layout: lanes of a row hold eight elements each.
-            if (tid < kM) s_rows[tid] = tid < count ? p.perm[first + tid] : 0;
             const int chunks = g.N / 8;
             int lanes = 2;
             while (lanes < chunks) lanes *= 2;
             const float scale = p.scale ? __ldg(p.scale + adapter) : 1.f;
             const int per_warp = 32 / lanes, c8 = lane % lanes;
-            for (int i0 = warp * per_warp; i0 < count; i0 += (kEpiWarps + 2) * per_warp) {
-                const int row = i0 + lane / lanes;
-                const bool in = row < count && c8 * 8 < p.r;
-                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (in) {
-                    const float* from = g.part + (int64_t)(first + row) * p.r + c8 * 8;
-                    for (int s = 0; s < ks.n; ++s) {
-                        const float4 a = *reinterpret_cast<const float4*>(from + (int64_t)s * p.n * p.r);
-                        const float4 b = *reinterpret_cast<const float4*>(from + (int64_t)s * p.n * p.r + 4);
-                        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-                        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+            constexpr int kGroups = 2;       // of rows whose loads are in flight together
+            for (int i0 = warp * per_warp; warp < kEpiWarps && i0 < count; i0 += kGroups * kEpiWarps * per_warp) {
+                float v[kGroups][8];
+#pragma unroll
+                for (int u = 0; u < kGroups; ++u) {
+                    const int row = i0 + u * kEpiWarps * per_warp + lane / lanes;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+                    if (row < count && c8 * 8 < p.r) {
+                        const float* part = g.part + (int64_t)(first + row) * p.r + c8 * 8;
+#pragma unroll 4
+                        for (int s = 0; s < ks.n; ++s, part += (int64_t)p.n * p.r) {
+                            const float4 a = *reinterpret_cast<const float4*>(part), b = *reinterpret_cast<const float4*>(part + 4);
+                            v[u][0] += a.x; v[u][1] += a.y; v[u][2] += a.z; v[u][3] += a.w;
+                            v[u][4] += b.x; v[u][5] += b.y; v[u][6] += b.z; v[u][7] += b.w;
+                        }
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] *= scale;
                 }
-                int e = 0;
-                if constexpr (!kBf16) {
-                    float most = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) most = fmaxf(most, finite_abs(v[i]));
-                    for (int o = 1; o < lanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                    e = f16_shift(most);
-                    if (row < count && c8 == 0) s_exp[row] = e;
-                }
-                uint16_t q[8][kParts];
+                for (int u = 0; u < kGroups; ++u) {
+                    const int row = i0 + u * kEpiWarps * per_warp + lane / lanes;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) split<kBf16, kParts>(kBf16 ? v[i] : times_exp2(v[i], e), q[i]);
-                if (row < count && c8 < chunks) {
-                    uint8_t* at = sV + (c8 >> 3) * kBoxBytes + row * 128 + (((c8 & 7) ^ (row & 7)) << 4);
+                    for (int i = 0; i < 8; ++i) v[u][i] *= scale;
+                    int e = 0;
+                    if constexpr (!kBf16) {
+                        float most = 0.f;
 #pragma unroll
-                    for (int m = 0; m < kParts; ++m)
-                        *reinterpret_cast<uint4*>(at + m * vbytes) =
-                            make_uint4(q[0][m] | (uint32_t)q[1][m] << 16, q[2][m] | (uint32_t)q[3][m] << 16, q[4][m] | (uint32_t)q[5][m] << 16,
-                                       q[6][m] | (uint32_t)q[7][m] << 16);
+                        for (int i = 0; i < 8; ++i) most = fmaxf(most, finite_abs(v[u][i]));
+                        for (int o = 1; o < lanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                        e = f16_shift(most);
+                        if (row < count && c8 == 0) s_exp[row] = e;
+                    }
+                    uint16_t part[8][kParts];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split<kBf16, kParts>(kBf16 ? v[u][i] : times_exp2(v[u][i], e), part[i]);
+                    if (row < count && c8 < chunks) {
+                        uint8_t* at = sV + (c8 >> 3) * kBoxBytes + row * 128 + (((c8 & 7) ^ (row & 7)) << 4);
+#pragma unroll
+                        for (int m = 0; m < kParts; ++m)
+                            *reinterpret_cast<uint4*>(at + m * vbytes) =
+                                make_uint4(part[0][m] | (uint32_t)part[1][m] << 16, part[2][m] | (uint32_t)part[3][m] << 16,
+                                           part[4][m] | (uint32_t)part[5][m] << 16, part[6][m] | (uint32_t)part[7][m] << 16);
+                    }
                 }
             }
-            ptx::fence_proxy_async_smem();
-            __syncthreads();
+            if (warp <= kEpiWarps) {      // (the warp that fetches B has begun)
+                ptx::fence_proxy_async_smem();
+                ptx::named_bar(1, 32 * (kEpiWarps + 1));
+            }
 
+            // kWide.  A thread has a row: its results from tensor memory, base's elements from shared memory and their
+            // sums back into their place, 16 bytes at a time (the swizzle keeps eight rows of a column apart); then
+            // eight lanes write each row's 128 bytes.
+            auto epilogue = [&]() {
+                float m0 = 1.f, m1 = 1.f;
+                if (!kBf16 && lane < here) {
+                    const int e = -s_exp[32 * q + lane];
+                    m0 = exp2i(e >> 1);
+                    m1 = exp2i(e - (e >> 1));
+                }
+                auto own = [&](int slot, int c) { return mine + slot * kPassBytes + lane * 128 + ((c ^ (lane & 7)) << 4); };
+                int slot = 0;
+                for (int i = 0; i < nt; ++i) {
+                    const int buf = (done_tiles + i) & 1;
+                    if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) return;
+                    ptx::tc_fence_after();
+                    float d[64];
+                    if (here > 0) tmem_ld64(tmem + ((uint32_t)(32 * q) << 16) + buf * kNT + half * 64, d);
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    ptx::mbar_arrive_elect(&tempty[buf]);
+                    if (here <= 0) continue;
+                    if constexpr (!kBf16) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) d[c] = d[c] * m0 * m1;
+                    }
+#pragma unroll
+                    for (int h = 0; h < kPasses; ++h) {
+                        const int pass = i * kPasses + h, into = slot == 0 ? g.slots - 1 : slot - 1;
+                        fetch(pass + g.slots - 1, into);     // (where the pass before this one was)
+                        if (g.slots == 4) cp_wait<3>();
+                        else if (g.slots == 3) cp_wait<2>();
+                        else cp_wait<1>();
+                        __syncwarp();
+#pragma unroll
+                        for (int c0 = 0; c0 < 8; c0 += 4) {
+                            uint4 was[4];
+                            if (p.base) {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) was[c] = *reinterpret_cast<const uint4*>(own(slot, c0 + c));
+                            }
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                float y[kV];
+#pragma unroll
+                                for (int w = 0; w < kV; ++w) y[w] = d[h * kCols + (c0 + c) * kV + w];
+                                if (p.base) add_raw<kOut>(was[c], y);
+                                *reinterpret_cast<uint4*>(own(slot, c0 + c)) = pack_raw<kOut>(y);
+                            }
+                        }
+                        __syncwarp();
+                        const int o = column(pass) + chunk * kV;
+                        const size_t at = (size_t)column(pass) * kSize;
+                        if (o + kV <= O) {
+                            uint4 sum[8];
+#pragma unroll
+                            for (int it = 0; it < 8; ++it) sum[it] = *reinterpret_cast<const uint4*>(across[it & 1] + slot * kPassBytes + it * 512);
+#pragma unroll
+                            for (int it = 0; it < 8; ++it)
+                                if (it < valid) *reinterpret_cast<uint4*>(to[it] + at) = sum[it];
+                        } else if (o < O) {
+#pragma unroll
+                            for (int it = 0; it < 8; ++it)
+                                if (it < valid) copy_elements<kSize>(to[it] + at, across[it & 1] + slot * kPassBytes + it * 512, O - o);
+                        }
+                        __syncwarp();
+                        slot = slot + 1 == g.slots ? 0 : slot + 1;
+                    }
+                }
+            };
             if (warp == kEpiWarps + 1) {
                 int sent = done_tiles;
                 for (int i = 0; i < nt; ++i, ++sent) {
@@ -378,115 +556,53 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                     __syncwarp();
                 }
             } else {
-                // Rows 32 q .. 32 q + 31 of the tile, 64 of the 128 outputs in two passes of 32.
-                const int q = warp & 3, half = warp >> 2;
-                float* stage = reinterpret_cast<float*>(sStage + warp * kStageBytes);
-                const bool some = 32 * q < count;
-                constexpr int kV = kF32 ? 4 : 8;                  // elements of 16 bytes
-                constexpr int kCol = 32 / kV, kIts = kCol;        // threads of a row; rows of a thread (32 / (32 / kCol))
-                const int c = (lane % kCol) * kV, r0 = 32 * q + lane / kCol;
-                int rows[kIts];
+                if constexpr (kWide) {
+                    epilogue();
+                } else {
+                    // Any rows: 64 of the 128 outputs in two passes of 32, through the warp's staging; neighbouring lanes
+                    // at neighbouring elements, eight rows in flight.
+                    float* stage = reinterpret_cast<float*>(sStage + warp * kStageBytes);
+                    for (int i = 0; i < nt; ++i) {
+                        const int buf = (done_tiles + i) & 1;
+                        if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) break;
+                        ptx::tc_fence_after();
 #pragma unroll
-                for (int it = 0; it < kIts; ++it) {
-                    const int r = r0 + it * (32 / kCol);
-                    rows[it] = r < count ? s_rows[r] : -1;
-                }
-                const uint8_t* base = reinterpret_cast<const uint8_t*>(p.base);
-                constexpr int kSize = kF32 ? 4 : 2;
-                const bool wide = p.vec * kSize >= 16;
-                uint4 was[2][kIts];
-                // Base's elements of pass `pass` (two a tile) of this block.
-                auto fetch = [&](int pass, uint4 (&to)[kIts]) {
-                    const int o = (t0 + (pass >> 1)) * kNT + half * 64 + (pass & 1) * 32 + c;
+                        for (int h = 0; h < 2; ++h) {
+                            if (here > 0) {
+                                const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * kNT + half * 64 + h * 32;
+                                float d[16];
 #pragma unroll
-                    for (int it = 0; it < kIts; ++it)
-                        if (rows[it] >= 0 && o + kV <= O)
-                            to[it] = *reinterpret_cast<const uint4*>(base + ((int64_t)rows[it] * p.base_stride + o) * kSize);
-                };
-                const bool early = wide && base != nullptr;
-                if (early) fetch(0, was[0]);
-                for (int i = 0; i < nt; ++i) {
-                    const int buf = (done_tiles + i) & 1;
-                    if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) break;
-                    ptx::tc_fence_after();
+                                for (int u = 0; u < 2; ++u) {
+                                    ptx::tmem_ld16(tb + 16 * u, d);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int pass = 2 * i + h;
-                        if (early && pass + 1 < 2 * nt) fetch(pass + 1, was[(h + 1) & 1]);
-                        if (some) {
-                            const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * kNT + half * 64 + h * 32;
-                            float d[16];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                ptx::tmem_ld16(tb + 16 * u, d);
-#pragma unroll
-                                for (int w = 0; w < 4; ++w)
-                                    *reinterpret_cast<float4*>(stage + lane * kStageRow + 16 * u + 4 * w) =
-                                        make_float4(d[4 * w], d[4 * w + 1], d[4 * w + 2], d[4 * w + 3]);
+                                    for (int w = 0; w < 4; ++w)
+                                        *reinterpret_cast<float4*>(stage + lane * kStageRow + 16 * u + 4 * w) =
+                                            make_float4(d[4 * w], d[4 * w + 1], d[4 * w + 2], d[4 * w + 3]);
+                                }
                             }
-                        }
-                        if (h == 1) {                             // the accumulator is read
-                            ptx::tc_fence_before();
+                            if (h == 1) ptx::tc_fence_before();       // the accumulator is read
                             __syncwarp();
-                            ptx::mbar_arrive_elect(&tempty[buf]);
-                        }
-                        __syncwarp();
-                        if (some) {
-                            const int o_pass = (t0 + i) * kNT + half * 64 + h * 32;
-                            if (wide) {
-                                const int o = o_pass + c;
+                            if (h == 1) ptx::mbar_arrive_elect(&tempty[buf]);
+                            const int o = (t0 + i) * kNT + half * 64 + h * 32 + lane;
+                            for (int b0 = 0; b0 < here; b0 += 8) {
+                                float y[8];
 #pragma unroll
-                                for (int it = 0; it < kIts; ++it) {
-                                    if (rows[it] < 0 || o >= O) continue;
-                                    const int r = lane / kCol + it * (32 / kCol);
-                                    float y[kV];
+                                for (int w = 0; w < 8; ++w)
+                                    y[w] = p.base && b0 + w < here && o < O
+                                               ? load_one<kOut>(p.base, (int64_t)s_rows[32 * q + b0 + w] * p.base_stride + o)
+                                               : 0.f;
 #pragma unroll
-                                    for (int w = 0; w < kV / 4; ++w) {
-                                        const float4 f = *reinterpret_cast<const float4*>(stage + r * kStageRow + c + 4 * w);
-                                        y[4 * w] = f.x; y[4 * w + 1] = f.y; y[4 * w + 2] = f.z; y[4 * w + 3] = f.w;
-                                    }
-                                    if constexpr (!kBf16) {
-                                        const int e = -s_exp[32 * q + r];
-#pragma unroll
-                                        for (int w = 0; w < kV; ++w) y[w] = times_exp2(y[w], e);
-                                    }
-                                    const int64_t at = (int64_t)rows[it] * p.out_stride + o;
-                                    if (o + kV <= O) {
-                                        if (base) add_raw<kF32>(p.out_type, was[h & 1][it], y);
-                                        store_raw<kF32>(p.out_type, p.out, at, y);
-                                    } else {
-#pragma unroll
-                                        for (int w = 0; w < kV; ++w)
-                                            if (o + w < O) {
-                                                if (base) y[w] += load_one<kF32>(p.out_type, base, (int64_t)rows[it] * p.base_stride + o + w);
-                                                store_one<kF32>(p.out_type, p.out, at + w, y[w]);
-                                            }
-                                    }
-                                }
-                            } else {
-                                // Neighbouring lanes at neighbouring elements, eight rows in flight.
-                                const int o = o_pass + lane;
-                                for (int b0 = 0; b0 < 32 && 32 * q + b0 < count; b0 += 8) {
-                                    float y[8];
-#pragma unroll
-                                    for (int w = 0; w < 8; ++w) {
-                                        const int r = 32 * q + b0 + w;
-                                        if (base && r < count && o < O) y[w] = load_one<kF32>(p.out_type, p.base, (int64_t)s_rows[r] * p.base_stride + o);
-                                        else y[w] = 0.f;
-                                    }
-#pragma unroll
-                                    for (int w = 0; w < 8; ++w) {
-                                        const int r = 32 * q + b0 + w;
-                                        if (r < count && o < O) {
-                                            float v = stage[(b0 + w) * kStageRow + lane];
-                                            if constexpr (!kBf16) v = times_exp2(v, -s_exp[r]);
-                                            store_one<kF32>(p.out_type, p.out, (int64_t)s_rows[r] * p.out_stride + o, base ? y[w] + v : v);
-                                        }
+                                for (int w = 0; w < 8; ++w) {
+                                    const int r = 32 * q + b0 + w;
+                                    if (b0 + w < here && o < O) {
+                                        float v = stage[(b0 + w) * kStageRow + lane];
+                                        if constexpr (!kBf16) v = times_exp2(v, -s_exp[r]);
+                                        store_one<kOut>(p.out, (int64_t)s_rows[r] * p.out_stride + o, p.base ? y[w] + v : v);
                                     }
                                 }
                             }
+                            __syncwarp();                             // the staging is read
                         }
-                        __syncwarp();                             // the staging is read
                     }
                 }
             }
@@ -494,6 +610,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
         }
         if (__syncthreads_or(*s_abort)) break;   // (and v and the rows' numbers are read)
     }
+    if (kWide) cp_wait<0>();
     pdl_trigger();
     ptx::tc_fence_before();
     __syncthreads();
@@ -506,12 +623,12 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
 template <typename Kern>
 cudaError_t configure(Kern kern, int slot) {
     static std::mutex mu;
-    static bool configured[128][8] = {};
+    static bool configured[128][14] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (configured[dev][slot]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
     if (e == cudaSuccess) configured[dev][slot] = true;
     return e;
 }
@@ -545,14 +662,29 @@ cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&
     auto shrink = x_type == MOE_BF16 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>;
     cudaError_t e = configure(shrink, x_type == MOE_BF16 ? 0 : 1);
     if (e != cudaSuccess) return e;
-    if ((e = launch_pdl(shrink, dim3((unsigned)std::min<int64_t>(kLoraBlocks, (int64_t)max_segs * g.max_splits)), dim3(kShrinkThreads), smem, st, maps[0], maps[3], maps[1], g)) != cudaSuccess) return e;
+    if ((e = launch_pdl(shrink, dim3((unsigned)std::min<int64_t>(kLoraBlocks, (int64_t)max_segs * g.max_splits)), dim3(kShrinkThreads), smem, st,
+                        maps[0], maps[3], maps[1], g)) != cudaSuccess)
+        return e;
 
+    // Rows of base and out that are aligned to 16 bytes, in device memory: one block an SM, whose warps
+    // have as many passes in shared memory as fit, up to four.
     const bool f32 = p.out_type == MOE_F32, bf = x_type == MOE_BF16;
-    const dim3 grid((unsigned)std::min<int64_t>(kLoraBlocks, (int64_t)max_segs * ((p.O + kNT - 1) / kNT)));
-    auto expand = bf ? (f32 ? lora_expand_kernel<true, true> : lora_expand_kernel<true, false>)
-                     : (f32 ? lora_expand_kernel<false, true> : lora_expand_kernel<false, false>);
-    if ((e = configure(expand, 2 + (bf ? 0 : 2) + (f32 ? 1 : 0))) != cudaSuccess) return e;
-    return launch_pdl(expand, grid, dim3(kExpandThreads), expand_smem(g.N, f32), st, maps[2], g);
+    const bool wide = !p.out_host && p.vec * (f32 ? 4 : 2) >= 16;
+    g.slots = 0;
+    if (wide)
+        for (g.slots = 4; g.slots > 2 && expand_smem(g.N, f32, g.slots) > kMaxSmem; --g.slots) {}
+    g.expand_blocks = wide ? kLoraBlocks / 2 : kLoraBlocks;
+    const dim3 grid((unsigned)std::min<int64_t>(g.expand_blocks, (int64_t)max_segs * ((p.O + kNT - 1) / kNT)));
+    auto of_out = [&](auto bf16, auto is_wide) {
+        constexpr bool kB = decltype(bf16)::value, kW = decltype(is_wide)::value;
+        return p.out_type == MOE_F32 ? lora_expand_kernel<kB, MOE_F32, kW> : p.out_type == MOE_BF16 ? lora_expand_kernel<kB, MOE_BF16, kW>
+                                                                                                    : lora_expand_kernel<kB, MOE_F16, kW>;
+    };
+    using yes = std::true_type;
+    using no = std::false_type;
+    auto expand = bf ? (wide ? of_out(yes{}, yes{}) : of_out(yes{}, no{})) : (wide ? of_out(no{}, yes{}) : of_out(no{}, no{}));
+    if ((e = configure(expand, 2 + (wide ? 6 : 0) + (bf ? 0 : 3) + p.out_type)) != cudaSuccess) return e;
+    return launch_pdl(expand, grid, dim3(kExpandThreads), expand_smem(g.N, f32, g.slots), st, maps[2], g);
 }
 
 }  // namespace moe
