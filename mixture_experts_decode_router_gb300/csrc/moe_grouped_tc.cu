@@ -966,6 +966,19 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esiz
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D map over the rows of a [rows, cols] matrix of 16-bit elements (the second coordinate), and those
+// `apart`, 2 apart and 3 apart behind each (the third): boxes of 64 elements of two rows and their six others.
+bool make_map_pairs(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows, int apart) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cols, rows, 4};
+    const cuuint64_t strides[2] = {cols * 2, cols * 2 * apart};
+    const cuuint32_t box[3] = {64, 2, 4};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool build_tc_maps(int fmt, bool gate_up, const moe_weights_t* w, int E, int H, int I, int S, int n,
                    int n_routes_max, const void* act_routed, const void* act_shared, TcMaps* maps) {
     // gate_up: routed weights [E*I, H], shared [S, H], B = xs [rows, H] / x(or xh) [n, H]

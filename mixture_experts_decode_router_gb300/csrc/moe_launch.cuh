@@ -172,6 +172,7 @@ cudaError_t launch_router_nvfp4_expand(const QMatDev& wq, int E, int H, uint16_t
 // apart (0: cols) (moe_grouped_tc.cu).
 bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, uint64_t cols,
               uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle, uint64_t stride = 0);
+bool make_map_pairs(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows, int apart);
 cudaError_t launch_router_nvfp4(const uint16_t* x, int n, int H, const QMatDev& wq, int E, float* logits,
                                 cudaStream_t st);
 // logits: ns partial rows per token ([ns][n][E], ns = 1 for a plain logit
@@ -242,9 +243,9 @@ inline int64_t lora_part_rows(int64_t n) {   // of splits * n, and of every smal
     return std::min<int64_t>(kLoraMaxSplits * n, (int64_t)kLoraBlocks * kLoraTile + 2 * n);
 }
 // Whether the tensor maps of a call can be made; `maps` receives them (x by
-// single rows, A, B, x by 32 rows).
-bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[4]);
-cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[4], float* part, int32_t* err, int max_segs,
+// single rows, A, B, x by 32 rows, B by pairs of rows).
+bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[5]);
+cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[5], float* part, int32_t* err, int max_segs,
                            cudaStream_t st);
 
 // tile: routes of a segment at most.

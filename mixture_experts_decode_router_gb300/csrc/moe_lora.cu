@@ -464,7 +464,7 @@ cudaError_t launch_lora(const LoraParams& given, int x_type, void* ws, int num_s
     p.ctrl = ctrl;
     p.segs = reinterpret_cast<int32_t*>(w + l.segs);
     p.perm = reinterpret_cast<int32_t*>(w + l.perm);
-    CUtensorMap maps[4];
+    CUtensorMap maps[5];
     const bool tc = !p.x_host && lora_maps(p, x_type, maps);
     const int tile = tc ? kLoraTile : kRows;
     if ((e = launch_sort(p, tile, reinterpret_cast<int32_t*>(w + l.perm), reinterpret_cast<int32_t*>(w + l.segs), ctrl, st)) != cudaSuccess)

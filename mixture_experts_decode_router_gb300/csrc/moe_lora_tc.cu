@@ -11,9 +11,14 @@
 // out = base + B v (lora_expand_kernel): a block takes a tile of rows and a stretch of the outputs,
 // 128 at a time.  v, summed over the stretches in their order, scaled and split into 16-bit parts
 // (moe_lora.cu), stays in shared memory as the products' M = 128 rows; B's rows come by TMA.  Eight
-// warps add the base: results go through shared memory, so that base and out are read and written
-// along their rows, 16 bytes a thread where they are aligned and by neighbouring elements where they
-// are not, base's loads in flight while the products run.
+// warps add the base to what they read of tensor memory.  They read it by fragments, of which a lane
+// has column pairs 8 apart; B's rows are put into shared memory so that these are pieces of 16 bytes
+// of neighbouring outputs, four lanes' side by side.  base comes by asynchronous copies, a tile ahead,
+// to where the lane that wants it reads it, and out is written from the registers.  (base loaded into
+// registers a tile ahead: 74 us against XX for 8192 rows of 7168 outputs, since waits for anything
+// else waited for those loads too; results through shared memory, 128 bytes along a row: 61 us, bound
+// by its traffic and steps.)  Rows that are not of whole aligned pieces go through shared memory, by
+// neighbouring elements.
 #include <mutex>
 #include <type_traits>
 
@@ -35,7 +40,6 @@ struct TcArgs {
     int max_splits;   // of K: as many as part holds
     int stages;       // shrink: ring
     int tmem_cols;    // shrink
-    int slots;        // expand: passes of a warp in shared memory (0: results alone)
     int expand_blocks;
     float* part;      // [splits][n][r]
     int32_t* err;
@@ -54,6 +58,20 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// 64 columns of 16 lanes of tensor memory by fragments: of lane (g, t) = (lane / 4, lane % 4), values
+// 4 j .. 4 j + 3 are columns 8 j + 2 t and the next of row g, and of row g + 8.
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float (&v)[32]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+        "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
 // 16 bytes from global to shared memory, asynchronously.
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
@@ -61,21 +79,12 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// 64 columns of 32 lanes of tensor memory: the thread's lane's.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+// A box of a 3-D map.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-        "%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,"
-        "%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
-          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
-          "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]),
-          "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]),
-          "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-        : "r"(taddr)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(ptx::smem_u32(bar))
         : "memory");
 }
 
@@ -259,32 +268,24 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
 }
 
 constexpr int kNT = 128;                 // outputs of a tile
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 8;             // 32 rows and 64 outputs of a tile each
 constexpr int kExpandThreads = 32 * (kEpiWarps + 2);
 constexpr int kRing = 2;                 // tiles of B in flight
 constexpr int kStageRow = 36;            // floats of a row of a warp's staging (32 and 4: no bank conflicts)
 constexpr int kStageBytes = 32 * kStageRow * 4;
 
 __host__ __device__ constexpr int expand_parts(bool f32) { return f32 ? 3 : 2; }
-constexpr int kPassBytes = 32 * 128;     // base's or out's 128 bytes of 32 rows
 constexpr size_t kMaxSmem = 226 * 1024;  // (beside 1 KB of static arrays)
-inline size_t expand_smem(int rank16, bool f32, int slots) {
+// A warp's 32 rows and 64 outputs of base.
+__host__ __device__ constexpr int ahead_bytes(bool f32) { return 32 * 64 * (f32 ? 4 : 2); }
+inline size_t expand_smem(int rank16, bool f32, bool wide) {
     const int boxes = (rank16 + kBox - 1) / kBox;
-    return 1024 + (size_t)(expand_parts(f32) + kRing) * boxes * kBoxBytes + kEpiWarps * (slots ? slots * kPassBytes : kStageBytes) + 512;
+    return 1024 + (size_t)(expand_parts(f32) + kRing) * boxes * kBoxBytes + kEpiWarps * (wide ? ahead_bytes(f32) : kStageBytes) + 256;
 }
 
-// The first `count` elements of 16 bytes, one by one (rows that end inside them).
-template <int kSize> __device__ __noinline__ void copy_elements(uint8_t* to, const uint8_t* from, int count) {
-    for (int i = 0; i < count; ++i) {
-        if constexpr (kSize == 4) reinterpret_cast<uint32_t*>(to)[i] = reinterpret_cast<const uint32_t*>(from)[i];
-        else reinterpret_cast<uint16_t*>(to)[i] = reinterpret_cast<const uint16_t*>(from)[i];
-    }
-}
-
-// kWide: rows of base and out that are aligned to 16 bytes (a ring of g.slots passes of each warp in
-// shared memory).
+// kWide: rows of base and out that are aligned to 16 bytes, of a multiple of 32 (fp32: 16) outputs.
 template <bool kBf16, int kOut, bool kWide>
-__global__ void __launch_bounds__(kExpandThreads, kWide || kOut == MOE_F32 ? 1 : 2)
+__global__ void __launch_bounds__(kExpandThreads, kOut == MOE_F32 ? 1 : 2)
 lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
     constexpr bool kF32 = kOut == MOE_F32;
     constexpr int kParts = expand_parts(kF32);
@@ -295,7 +296,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
     uint8_t* sV = align1024(raw);                       // [part][box][128 rows x 128 bytes]
     uint8_t* sB = sV + kParts * vbytes;                 // [stage][box][128 outputs x 128 bytes]
     uint8_t* sStage = sB + kRing * vbytes;
-    uint64_t* bfull = reinterpret_cast<uint64_t*>(sStage + kEpiWarps * (kWide ? g.slots * kPassBytes : kStageBytes));
+    uint64_t* bfull = reinterpret_cast<uint64_t*>(sStage + kEpiWarps * (kWide ? ahead_bytes(kF32) : kStageBytes));
     uint64_t *bempty = bfull + kRing, *tfull = bempty + kRing, *tempty = tfull + 2;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
@@ -324,7 +325,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
     const Pieces os = pieces(runs, n_tiles, 64, g.expand_blocks);
     int done_tiles = 0;      // of this block, before this unit
     constexpr int kSize = kF32 ? 4 : 2, kV = 16 / kSize;        // elements of 16 bytes
-    constexpr int kCols = 128 / kSize, kPasses = 64 / kCols;    // a pass: 128 bytes of the warp's 32 rows
+    constexpr int kPieces = 16 / kV;                            // of a lane's 16 outputs of a row
     for (int64_t unit = blockIdx.x; unit < (int64_t)runs * os.n; unit += gridDim.x) {
         const int tile = (int)(unit / os.n), t0 = (int)(unit % os.n) * os.size, nt = min(n_tiles - t0, os.size);
         const int adapter = p.segs[3 * tile], first = p.segs[3 * tile + 1], count = p.segs[3 * tile + 2];
@@ -358,40 +359,32 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
             }
         } else if (adapter >= 0) {
             const int q = warp & 3, half = warp >> 2, here = warp < kEpiWarps ? min(32, count - 32 * q) : 0;
-            if (warp < kEpiWarps && half == 0 && lane < here) s_rows[32 * q + lane] = p.perm[first + 32 * q + lane];
-            // kWide: lane i takes 16 bytes (i % 8) of the warp's rows i / 8, i / 8 + 4, ... (the last row again behind
-            // it, which is not written); base's of the first passes are on their way while v is formed.
-            const int chunk = lane & 7, r8 = lane >> 3, valid = here > r8 ? (here - r8 + 3) / 4 : 0;
-            const uint8_t* from[8];
-            uint8_t* to[8];
-            uint8_t* mine = sStage + warp * g.slots * kPassBytes;
-            uint8_t* across[2] = {mine + r8 * 128 + ((chunk ^ r8) << 4), mine + r8 * 128 + ((chunk ^ (r8 + 4)) << 4)};   // rows 4 it + r8
-            const int last = nt * kPasses;
-            auto column = [&](int pass) { return (t0 + pass / kPasses) * kNT + half * 64 + pass % kPasses * kCols; };
-            auto fetch = [&](int pass, int slot) {
-                if (p.base && pass < last) {
-                    const int o = column(pass) + chunk * kV;
-                    const size_t at = (size_t)column(pass) * kSize;
-                    if (o + kV <= O) {
+            if (warp < 4 && lane < here) s_rows[32 * q + lane] = p.perm[first + 32 * q + lane];
+            // kWide: rows 8 i + lane / 4 of the warp's (the last again behind it, which is not written), of each 4 kV
+            // outputs kV from kV (lane % 4) on; base's of the first tile are on their way while v is formed.
+            const uint8_t* from[4];
+            uint8_t* to[4];
+            const int left = O - (t0 * kNT + half * 64 + kV * (lane & 3));      // outputs from the lane's first one on
+            uint8_t* mine = sStage + warp * ahead_bytes(kF32) + lane * 16;      // [row][piece][lane]
+            auto fetch = [&](int i, int r) {
+                if (p.base && i < nt) {
 #pragma unroll
-                        for (int it = 0; it < 8; ++it) cp_async16(across[it & 1] + slot * kPassBytes + it * 512, from[it] + at);
-                    } else if (o < O) {
-#pragma unroll
-                        for (int it = 0; it < 8; ++it)
-                            if (it < valid) copy_elements<kSize>(across[it & 1] + slot * kPassBytes + it * 512, from[it] + at, O - o);
-                    }
+                    for (int w = 0; w < kPieces; ++w)
+                        if (i * kNT + 4 * kV * w < left) cp_async16(mine + (r * kPieces + w) * 512, from[r] + (size_t)i * (kNT * kSize) + 64 * w);
                 }
                 cp_commit();
             };
             if constexpr (kWide) {
                 if (here > 0) {
 #pragma unroll
-                    for (int it = 0; it < 8; ++it) {
-                        const int64_t row = p.perm[first + 32 * q + min(4 * it + r8, here - 1)];
-                        from[it] = reinterpret_cast<const uint8_t*>(p.base) + row * p.base_stride * kSize + chunk * 16;
-                        to[it] = reinterpret_cast<uint8_t*>(p.out) + row * p.out_stride * kSize + chunk * 16;
+                    for (int r = 0; r < 4; ++r) {
+                        const int64_t row = p.perm[first + 32 * q + min(8 * r + (lane >> 2), here - 1)];
+                        const int64_t o = t0 * kNT + half * 64 + kV * (lane & 3);
+                        from[r] = reinterpret_cast<const uint8_t*>(p.base) + (row * p.base_stride + o) * kSize;
+                        to[r] = reinterpret_cast<uint8_t*>(p.out) + (row * p.out_stride + o) * kSize;
                     }
-                    for (int i = 0; i < g.slots - 1; ++i) fetch(i, i);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) fetch(0, r);
                 }
             }
             // v of the tile's rows, split, in the products' layout: lanes of a row hold eight elements each.
@@ -400,17 +393,17 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
             while (lanes < chunks) lanes *= 2;
             const float scale = p.scale ? __ldg(p.scale + adapter) : 1.f;
             const int per_warp = 32 / lanes, c8 = lane % lanes;
-            constexpr int kGroups = 2;       // of rows whose loads are in flight together
-            for (int i0 = warp * per_warp; warp < kEpiWarps && i0 < count; i0 += kGroups * kEpiWarps * per_warp) {
+            constexpr int kGroups = kWide ? 1 : 2;   // of rows whose loads are in flight together
+            for (int g0 = warp * per_warp; warp < kEpiWarps && g0 < count; g0 += kGroups * kEpiWarps * per_warp) {
                 float v[kGroups][8];
 #pragma unroll
                 for (int u = 0; u < kGroups; ++u) {
-                    const int row = i0 + u * kEpiWarps * per_warp + lane / lanes;
+                    const int row = g0 + u * kEpiWarps * per_warp + lane / lanes;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
                     if (row < count && c8 * 8 < p.r) {
                         const float* part = g.part + (int64_t)(first + row) * p.r + c8 * 8;
-#pragma unroll 4
+#pragma unroll 2
                         for (int s = 0; s < ks.n; ++s, part += (int64_t)p.n * p.r) {
                             const float4 a = *reinterpret_cast<const float4*>(part), b = *reinterpret_cast<const float4*>(part + 4);
                             v[u][0] += a.x; v[u][1] += a.y; v[u][2] += a.z; v[u][3] += a.w;
@@ -420,7 +413,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                 }
 #pragma unroll
                 for (int u = 0; u < kGroups; ++u) {
-                    const int row = i0 + u * kEpiWarps * per_warp + lane / lanes;
+                    const int row = g0 + u * kEpiWarps * per_warp + lane / lanes;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[u][i] *= scale;
                     int e = 0;
@@ -450,73 +443,54 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                 ptx::named_bar(1, 32 * (kEpiWarps + 1));
             }
 
-            // kWide.  A thread has a row: its results from tensor memory, base's elements from shared memory and their
-            // sums back into their place, 16 bytes at a time (the swizzle keeps eight rows of a column apart); then
-            // eight lanes write each row's 128 bytes.
+            // kWide: two fragments of 16 rows.
             auto epilogue = [&]() {
-                float m0 = 1.f, m1 = 1.f;
-                if (!kBf16 && lane < here) {
-                    const int e = -s_exp[32 * q + lane];
-                    m0 = exp2i(e >> 1);
-                    m1 = exp2i(e - (e >> 1));
+                float m0[4], m1[4];
+                if (!kBf16) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 8 * r + (lane >> 2), e = row < here ? -s_exp[32 * q + row] : 0;
+                        m0[r] = exp2i(e >> 1);
+                        m1[r] = exp2i(e - (e >> 1));
+                    }
                 }
-                auto own = [&](int slot, int c) { return mine + slot * kPassBytes + lane * 128 + ((c ^ (lane & 7)) << 4); };
-                int slot = 0;
                 for (int i = 0; i < nt; ++i) {
                     const int buf = (done_tiles + i) & 1;
                     if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) return;
                     ptx::tc_fence_after();
-                    float d[64];
-                    if (here > 0) tmem_ld64(tmem + ((uint32_t)(32 * q) << 16) + buf * kNT + half * 64, d);
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    ptx::mbar_arrive_elect(&tempty[buf]);
-                    if (here <= 0) continue;
-                    if constexpr (!kBf16) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) d[c] = d[c] * m0 * m1;
-                    }
+                    for (int u = 0; u < 2; ++u) {
+                        float d[32];
+                        if (here > 16 * u) tmem_ld_fragments(tmem + ((uint32_t)(32 * q + 16 * u) << 16) + buf * kNT + half * 64, d);
+                        if (u == 1) {                            // the accumulator is read
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            ptx::mbar_arrive_elect(&tempty[buf]);
+                        }
+                        if (here <= 16 * u) continue;
 #pragma unroll
-                    for (int h = 0; h < kPasses; ++h) {
-                        const int pass = i * kPasses + h, into = slot == 0 ? g.slots - 1 : slot - 1;
-                        fetch(pass + g.slots - 1, into);     // (where the pass before this one was)
-                        if (g.slots == 4) cp_wait<3>();
-                        else if (g.slots == 3) cp_wait<2>();
-                        else cp_wait<1>();
-                        __syncwarp();
+                        for (int s = 0; s < 2; ++s) {
+                            const int r = 2 * u + s;
+                            cp_wait<3>();                        // (a group a row: this one's is the oldest of four)
 #pragma unroll
-                        for (int c0 = 0; c0 < 8; c0 += 4) {
-                            uint4 was[4];
-                            if (p.base) {
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) was[c] = *reinterpret_cast<const uint4*>(own(slot, c0 + c));
-                            }
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
+                            for (int w = 0; w < kPieces; ++w) {
                                 float y[kV];
 #pragma unroll
-                                for (int w = 0; w < kV; ++w) y[w] = d[h * kCols + (c0 + c) * kV + w];
-                                if (p.base) add_raw<kOut>(was[c], y);
-                                *reinterpret_cast<uint4*>(own(slot, c0 + c)) = pack_raw<kOut>(y);
+                                for (int j = 0; j < kV / 2; ++j) {
+                                    y[2 * j] = d[4 * (kV / 2 * w + j) + 2 * s];
+                                    y[2 * j + 1] = d[4 * (kV / 2 * w + j) + 2 * s + 1];
+                                }
+                                if constexpr (!kBf16) {
+#pragma unroll
+                                    for (int j = 0; j < kV; ++j) y[j] = y[j] * m0[r] * m1[r];
+                                }
+                                if (i * kNT + 4 * kV * w < left && 8 * r + (lane >> 2) < here) {
+                                    if (p.base) add_raw<kOut>(*reinterpret_cast<const uint4*>(mine + (r * kPieces + w) * 512), y);
+                                    *reinterpret_cast<uint4*>(to[r] + (size_t)i * (kNT * kSize) + 64 * w) = pack_raw<kOut>(y);
+                                }
                             }
+                            fetch(i + 1, r);                     // (to where this one was)
                         }
-                        __syncwarp();
-                        const int o = column(pass) + chunk * kV;
-                        const size_t at = (size_t)column(pass) * kSize;
-                        if (o + kV <= O) {
-                            uint4 sum[8];
-#pragma unroll
-                            for (int it = 0; it < 8; ++it) sum[it] = *reinterpret_cast<const uint4*>(across[it & 1] + slot * kPassBytes + it * 512);
-#pragma unroll
-                            for (int it = 0; it < 8; ++it)
-                                if (it < valid) *reinterpret_cast<uint4*>(to[it] + at) = sum[it];
-                        } else if (o < O) {
-#pragma unroll
-                            for (int it = 0; it < 8; ++it)
-                                if (it < valid) copy_elements<kSize>(to[it] + at, across[it & 1] + slot * kPassBytes + it * 512, O - o);
-                        }
-                        __syncwarp();
-                        slot = slot + 1 == g.slots ? 0 : slot + 1;
                     }
                 }
             };
@@ -527,8 +501,18 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                     if (sent >= kRing && !wait_warp(&bempty[s], (sent / kRing - 1) & 1, s_abort, g.err, 34)) break;
                     if (lane == 0) {
                         ptx::mbar_arrive_expect_tx(&bfull[s], vbytes);
-                        for (int b = 0; b < boxes; ++b)
-                            ptx::tma_load_2d(sB + s * vbytes + b * kBoxBytes, &bmap, b * kBox, adapter * O + (t0 + i) * kNT, &bfull[s]);
+                        const int row = adapter * O + (t0 + i) * kNT;
+                        for (int b = 0; b < boxes; ++b) {
+                            uint8_t* at = sB + s * vbytes + b * kBoxBytes;
+                            if constexpr (kWide) {
+                                // Column 8 j + 2 t + e of a half is output 4 kV (j / (kV / 2)) + kV t + 2 (j % (kV / 2)) + e:
+                                // a box of e and t for each j.
+                                for (int c = 0; c < 16; ++c)
+                                    tma_load_3d(at + c * 1024, &bmap, b * kBox, row + 64 * (c / 8) + 4 * kV * (c % 8 / (kV / 2)) + 2 * (c % (kV / 2)), 0, &bfull[s]);
+                            } else {
+                                ptx::tma_load_2d(at, &bmap, b * kBox, row, &bfull[s]);
+                            }
+                        }
                     }
                     __syncwarp();
                 }
@@ -635,7 +619,7 @@ cudaError_t configure(Kern kern, int slot) {
 
 }  // namespace
 
-bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[4]) {
+bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[5]) {
     // (Coordinates are 32-bit; strides fit 40 bits.)
     if ((int64_t)p.L * p.O > INT32_MAX || p.x_stride * 2 >= (int64_t)1 << 40) return false;
     const CUtensorMapDataType t = x_type == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -643,10 +627,11 @@ bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[4]) {
     return make_map(&maps[0], p.x, t, 2, p.K, p.n, kBox, 1, CU_TENSOR_MAP_SWIZZLE_128B, p.x_stride) &&
            make_map(&maps[1], p.a, t, 2, p.K, (uint64_t)p.L * p.r, kBox, N, CU_TENSOR_MAP_SWIZZLE_128B) &&
            make_map(&maps[3], p.x, t, 2, p.K, p.n, kBox, 32, CU_TENSOR_MAP_SWIZZLE_128B, p.x_stride) &&
-           make_map(&maps[2], p.b, t, 2, p.r, (uint64_t)p.L * p.O, kBox, kNT, CU_TENSOR_MAP_SWIZZLE_128B);
+           make_map(&maps[2], p.b, t, 2, p.r, (uint64_t)p.L * p.O, kBox, kNT, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           make_map_pairs(&maps[4], p.b, t, p.r, (uint64_t)p.L * p.O, p.out_type == MOE_F32 ? 4 : 8);
 }
 
-cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[4], float* part, int32_t* err, int max_segs,
+cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[5], float* part, int32_t* err, int max_segs,
                            cudaStream_t st) {
     TcArgs g{};
     g.p = p;
@@ -666,14 +651,11 @@ cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&
                         maps[0], maps[3], maps[1], g)) != cudaSuccess)
         return e;
 
-    // Rows of base and out that are aligned to 16 bytes, in device memory: one block an SM, whose warps
-    // have as many passes in shared memory as fit, up to four.
     const bool f32 = p.out_type == MOE_F32, bf = x_type == MOE_BF16;
-    const bool wide = !p.out_host && p.vec * (f32 ? 4 : 2) >= 16;
-    g.slots = 0;
-    if (wide)
-        for (g.slots = 4; g.slots > 2 && expand_smem(g.N, f32, g.slots) > kMaxSmem; --g.slots) {}
-    g.expand_blocks = wide ? kLoraBlocks / 2 : kLoraBlocks;
+    const int64_t esize = f32 ? 4 : 2;
+    const bool wide = !p.out_host && p.O * esize % 64 == 0 && p.vec * esize >= 16;
+    const size_t expand_bytes = expand_smem(g.N, f32, wide);
+    g.expand_blocks = f32 || expand_bytes > kMaxSmem / 2 ? kLoraBlocks / 2 : kLoraBlocks;
     const dim3 grid((unsigned)std::min<int64_t>(g.expand_blocks, (int64_t)max_segs * ((p.O + kNT - 1) / kNT)));
     auto of_out = [&](auto bf16, auto is_wide) {
         constexpr bool kB = decltype(bf16)::value, kW = decltype(is_wide)::value;
@@ -684,7 +666,7 @@ cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&
     using no = std::false_type;
     auto expand = bf ? (wide ? of_out(yes{}, yes{}) : of_out(yes{}, no{})) : (wide ? of_out(no{}, yes{}) : of_out(no{}, no{}));
     if ((e = configure(expand, 2 + (wide ? 6 : 0) + (bf ? 0 : 3) + p.out_type)) != cudaSuccess) return e;
-    return launch_pdl(expand, grid, dim3(kExpandThreads), expand_smem(g.N, f32, g.slots), st, maps[2], g);
+    return launch_pdl(expand, grid, dim3(kExpandThreads), expand_bytes, st, maps[wide ? 4 : 2], g);
 }
 
 }  // namespace moe
