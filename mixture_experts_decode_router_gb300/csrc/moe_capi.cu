@@ -917,7 +917,7 @@ static moe_status_t check_lora(const moe_lora_config_t* c) {
 
 size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows) {
     if (check_lora(cfg) != MOE_OK || max_rows < 0) return 0;
-    return lora_workspace(max_rows, cfg->num_adapters, cfg->rank);
+    return lora_workspace(max_rows, cfg->num_adapters, cfg->in_features, cfg->out_features, cfg->rank);
 }
 
 moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b, const float* scale, const void* x,
@@ -938,7 +938,7 @@ moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b
     if (!aligned16(x) || x_stride % 8 || begin_of(Y0) % osize || begin_of(Y) % osize || !aligned4(idx) || !aligned16(ws))
         return MOE_ERR_ALIGNMENT;
     if (overlap(X, Y) || (overlap(Y0, Y) && !same_rows(Y0, Y))) return MOE_ERR_ALIAS;
-    if (ws_bytes < lora_workspace(n, cfg->num_adapters, cfg->rank)) return MOE_ERR_WORKSPACE;
+    if (ws_bytes < lora_workspace(n, cfg->num_adapters, K, O, cfg->rank)) return MOE_ERR_WORKSPACE;
     const int at_x = residency(x), at_out = residency(out), at_base = base ? residency(base) : 0;
     if (at_x < 0 || at_out < 0 || at_base < 0) return MOE_ERR_HOST_MEMORY;
     LoraParams p{};

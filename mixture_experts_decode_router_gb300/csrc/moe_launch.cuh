@@ -233,7 +233,7 @@ struct LoraParams {
     const int32_t *segs, *perm;
     const Ctrl* ctrl;
 };
-size_t lora_workspace(int64_t n, int L, int r);
+size_t lora_workspace(int64_t n, int L, int K, int O, int r);
 cudaError_t launch_lora(const LoraParams& p, int x_type, void* ws, int num_sms, cudaStream_t st);
 // Runs of at most 128 rows through the tensor cores' kernels, v's partial sums [splits][n][r] in part.
 constexpr int kLoraTile = 128;

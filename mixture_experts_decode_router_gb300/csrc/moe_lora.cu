@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kRows = 8;           // rows of a cluster (the n of the products)
-constexpr int kScanRows = 512;     // rows whose adapters a block can go through by itself
+constexpr int kScanRows = 512;     // rows whose adapters a cluster goes through for itself, at most
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -68,16 +68,20 @@ __device__ __forceinline__ void copy_row(const LoraParams& p, int64_t row, int p
     }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
+
 // kRT: tiles of 16 of the rank.  kParts: parts of v.
 template <bool kBf16, int kRT, int kParts>
 __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p) {
     constexpr int kR = kRT * 16;
-    __shared__ float s_part[kWarps][kR][kRows];   // then v, [row][rank]
+    constexpr int kPad = kRT == 1 ? 0 : 16;       // (no bank conflicts between rows of parts)
+    __shared__ __align__(16) float s_part[kWarps][kR][kRows];   // then v's parts, [part][row][rank]
     __shared__ float s_mine[kR * kRows];
-    __shared__ int32_t s_idx[kScanRows];
-    __shared__ int s_rows[kRows], s_count;
+    __shared__ int s_rows[kWarps][kRows];         // (every warp finds them for itself)
+    __shared__ uint32_t s_top[kRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int C = (int)cluster_size(), c = (int)cluster_rank(), group = blockIdx.x / C;
+    if (tid < kRows) s_top[tid] = 0;
     pdl_wait();
 
     // The cluster's rows: row `group`, if an adapter's rows before it fill whole clusters, and
@@ -92,48 +96,54 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
             for (int i = 0; p.copy && i < count; ++i) copy_row(p, p.perm[first + i], c, C);
             return;
         }
-        if (tid < count) s_rows[tid] = p.perm[first + tid];
+        if (lane < count) s_rows[warp][lane] = p.perm[first + lane];
     } else {
-        for (int i = tid; i < p.n; i += kThreads) s_idx[i] = p.idx[i];
-        __syncthreads();
-        adapter = s_idx[group];
+        constexpr int kBatch = 4;   // of 32 rows whose loads are in flight
+        adapter = p.idx[group];
+        int before = 0, found = 0;
+        for (int i0 = 0; i0 < p.n && found < kRows; i0 += 32 * kBatch) {
+            int e[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) e[u] = i0 + 32 * u + lane < p.n ? p.idx[i0 + 32 * u + lane] : -1;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int row = i0 + 32 * u + lane;
+                const uint32_t all = __ballot_sync(0xffffffffu, e[u] == adapter && row < p.n), late = __ballot_sync(0xffffffffu, row >= group);
+                before += __popc(all & ~late);
+                const int at = found + __popc(all & late & ((1u << lane) - 1));
+                if ((all & late) >> lane & 1 && at < kRows) s_rows[warp][at] = row;
+                found += __popc(all & late);
+            }
+        }
         if (adapter < 0 || adapter >= p.L) {
             if (p.copy) copy_row(p, group, c, C);
             return;
         }
-        int before = 0;
-        for (int i0 = 0; i0 < group; i0 += kThreads)
-            before += __syncthreads_count(i0 + tid < group && s_idx[i0 + tid] == adapter);
         if (before % kRows) return;
-        if (warp == 0) {
-            int found = 0;
-            for (int i0 = group; i0 < p.n && found < kRows; i0 += 32) {
-                const bool same = i0 + lane < p.n && s_idx[i0 + lane] == adapter;
-                const uint32_t all = __ballot_sync(0xffffffffu, same);
-                const int at = found + __popc(all & ((1u << lane) - 1));
-                if (same && at < kRows) s_rows[at] = i0 + lane;
-                found += __popc(all);
-            }
-            if (lane == 0) s_count = min(found, kRows);
-        }
-        __syncthreads();
-        count = s_count;
+        count = min(found, kRows);
     }
-    __syncthreads();
+    __syncwarp();
 
     // v = A x: lane (g, t) holds elements 8 t .. 8 t + 7 of a step of 32 along K, of the rows g and
     // g + 8 of each tile and of x's row g.  (The products' order of k is any, the same for both.)
     const int K = p.K, r = p.r;
     const uint16_t* A = p.a + (int64_t)adapter * r * K;
-    const uint16_t* x = g < count ? p.x + (int64_t)s_rows[g] * p.x_stride : nullptr;
+    const uint16_t* x = g < count ? p.x + (int64_t)s_rows[warp][g] * p.x_stride : nullptr;
     const int steps = (K + 31) / 32, per = (steps + C - 1) / C, s1 = min(steps, (c + 1) * per);
+    const int O = p.O, units = (O + 31) / 32, uper = (units + C - 1) / C, u1 = min(units, (c + 1) * uper);
+    const uint16_t* Bm = p.b + (int64_t)adapter * O * r;
+    // The block's part of B is asked for before the loads of A, by lines of 128 bytes.
+    {
+        const int64_t b0 = (int64_t)c * uper * 32 * r, b1 = (int64_t)min(O, u1 * 32) * r;
+        for (int64_t e = b0 + tid * 64; e < b1; e += kThreads * 64) prefetch_l2(Bm + e);
+    }
     float acc[kRT][4];
 #pragma unroll
     for (int j = 0; j < kRT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    constexpr int kU = kRT >= 4 ? 1 : 4 / kRT;   // steps in flight
+    constexpr int kU = kRT >= 8 ? 1 : kRT == 4 ? 2 : 4 / kRT;   // steps in flight
     for (int s = c * per + warp; s < s1; s += kU * kWarps) {
         uint4 xv[kU], av[kU][kRT][2];
 #pragma unroll
@@ -169,94 +179,116 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
         for (int w = 0; w < kWarps; ++w) s += (&s_part[w][0][0])[e];
         s_mine[e] = s;
     }
-    cluster_arrive();
-    cluster_wait();
-    float* s_v = &s_part[0][0][0];   // [kRows][kR]
-    const float scale = p.scale ? __ldg(p.scale + adapter) : 1.f;
-    for (int e = tid; e < kR * kRows; e += kThreads) {
-        float s = 0.f;
-        for (int b = 0; b < C; ++b) s += ld_cluster(&s_mine[e], b);
-        // (Rows behind the rank are 0, not what a 0 weight makes of an infinity.)
-        s_v[(e % kRows) * kR + e / kRows] = e / kRows < r ? s * scale : 0.f;
-    }
-    cluster_arrive();   // (the others' sums are read; waited for before the block ends)
-    __syncthreads();
-
-    // out = base + B v: v is the columns' operand, its parts in registers; lane (g, t) holds
-    // elements 4 t .. 4 t + 3 of a step of 16 along the rank.
-    uint32_t vb[kRT][kParts][2];
-    int e = 0;
-    if constexpr (!kBf16) {
-        float most = 0.f;
-        for (int k = t; k < kR; k += 4) most = fmaxf(most, finite_abs(s_v[g * kR + k]));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        e = f16_shift(most);
-    }
-#pragma unroll
-    for (int j = 0; j < kRT; ++j) {
-        uint16_t q[4][kParts];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float v = s_v[g * kR + j * 16 + 4 * t + i];
-            split<kBf16, kParts>(kBf16 ? v : times_exp2(v, e), q[i]);
-        }
-#pragma unroll
-        for (int m = 0; m < kParts; ++m) {
-            vb[j][m][0] = q[0][m] | ((uint32_t)q[1][m] << 16);
-            vb[j][m][1] = q[2][m] | ((uint32_t)q[3][m] << 16);
-        }
-    }
-    // This lane's results are those of rows 2 t and 2 t + 1.
-    const int e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
+    // This lane's results are those of rows 2 t and 2 t + 1; outputs o .. o + 3 of a unit of 32 are rows g
+    // and g + 8 of two tiles.  A unit's loads are made while the one before it is worked on, the first
+    // one's before v is there (with more than 64 of rank there are no registers for that).
     int64_t orow[2];
     bool has[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
         has[m] = 2 * t + m < count;
-        orow[m] = has[m] ? s_rows[2 * t + m] : 0;
+        orow[m] = has[m] ? s_rows[warp][2 * t + m] : 0;
     }
-    const int O = p.O, units = (O + 31) / 32, uper = (units + C - 1) / C, u1 = min(units, (c + 1) * uper);
-    const uint16_t* Bm = p.b + (int64_t)adapter * O * r;
-    for (int u = c * uper + warp; u < u1; u += kWarps) {
-        // Outputs o .. o + 3 of this lane: rows g and g + 8 of two tiles.
-        const int o = u * 32 + 4 * g, left = O - o;
-        const bool vec = p.vec >= 4 && left >= 4;
-        uint2 bv[kRT][2][2];
+    uint2 bv[kRT][2][2];
+    float was[2][4];
+    auto fetch = [&](int u) {
+        const int o = u * 32 + 4 * g, left = u < u1 ? O - o : 0;
+        const uint16_t* at = Bm + (int64_t)o * r + 4 * t;
 #pragma unroll
         for (int j = 0; j < kRT; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool in = i < left && j * 16 + 4 * t < r;
-                bv[j][i >> 1][i & 1] = in ? ld_stream_v2(Bm + (int64_t)(o + i) * r + j * 16 + 4 * t) : make_uint2(0u, 0u);
+                bv[j][i >> 1][i & 1] = in ? ld_stream_v2(at + i * r + j * 16) : make_uint2(0u, 0u);
             }
-        float was[2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) was[m][i] = 0.f;
-            if (p.base && has[m] && left > 0) load4(p.out_type, p.base, orow[m] * p.base_stride + o, left, vec, was[m]);
+            if (p.base && has[m] && left > 0) load4(p.out_type, p.base, orow[m] * p.base_stride + o, left, p.vec >= 4 && left >= 4, was[m]);
         }
+    };
+    constexpr bool kEarly = kRT < 8;
+    if (kEarly) fetch(c * uper + warp);
+    cluster_arrive();
+    cluster_wait();
+    // Each element of v is summed over the blocks in their order, and split, by one thread.
+    const float scale = p.scale ? __ldg(p.scale + adapter) : 1.f;
+    constexpr int kMine = (kR * kRows + kThreads - 1) / kThreads;
+    float v[kMine];
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        const int i = tid + m * kThreads;
+        v[m] = 0.f;
+        if (i < kR * kRows) {
+            float sum = 0.f;
+            for (int b0 = 0; b0 < C; b0 += 8)
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (b0 + b < C) sum += ld_cluster(&s_mine[i], b0 + b);
+            // (Elements behind the rank are 0, not what a 0 weight makes of an infinity.)
+            if (i / kRows < r) v[m] = sum * scale;
+            if (!kBf16) atomicMax(&s_top[i % kRows], __float_as_uint(finite_abs(v[m])));
+        }
+    }
+    cluster_arrive();   // (the others' sums are read; waited for before the block ends)
+    if (!kBf16) __syncthreads();
+    uint16_t* s_v = reinterpret_cast<uint16_t*>(&s_part[0][0][0]);
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        const int i = tid + m * kThreads;
+        if (i < kR * kRows) {
+            uint16_t part[kParts];
+            split<kBf16, kParts>(kBf16 ? v[m] : times_exp2(v[m], f16_shift(__uint_as_float(s_top[i % kRows]))), part);
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) s_v[(q * kRows + i % kRows) * (kR + kPad) + i / kRows] = part[q];
+        }
+    }
+    __syncthreads();
+
+    // out = base + B v: v's parts are the columns' operand; lane (g, t) holds elements 4 t .. 4 t + 3 of a
+    // step of 16 along the rank.
+    uint2 vb[kRT][kParts];
+#pragma unroll
+    for (int j = 0; j < kRT; ++j)
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) vb[j][q] = *reinterpret_cast<const uint2*>(&s_v[(q * kRows + g) * (kR + kPad) + j * 16 + 4 * t]);
+    float back[2][2];   // what takes this lane's results, rows 2 t and 2 t + 1, back to their size
+    if constexpr (!kBf16) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int e = -f16_shift(__uint_as_float(s_top[2 * t + m]));
+            back[m][0] = exp2i(e >> 1);
+            back[m][1] = exp2i(e - (e >> 1));
+        }
+    }
+    // (Not unrolled: every call runs this code for the first time, and its instructions are fetched as it goes:
+    // four units at once took 4.9 us for a row of 2048 that takes 3.7 so.)
+#pragma unroll 1
+    for (int u = c * uper + warp; u < u1; u += kWarps) {
+        const int o = u * 32 + 4 * g, left = O - o;
+        if (!kEarly) fetch(u);
         float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int j = 0; j < kRT; ++j)
 #pragma unroll
-            for (int m = kParts - 1; m >= 0; --m)
+            for (int q = kParts - 1; q >= 0; --q)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    mma<kBf16>(d[h], bv[j][h][0].x, bv[j][h][1].x, bv[j][h][0].y, bv[j][h][1].y, vb[j][m][0], vb[j][m][1]);
+                    mma<kBf16>(d[h], bv[j][h][0].x, bv[j][h][1].x, bv[j][h][0].y, bv[j][h][1].y, vb[j][q].x, vb[j][q].y);
+        float y[2][4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            if (!has[m] || left <= 0) continue;
-            float y[4];
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float v = d[i >> 1][2 * (i & 1) + m];
-                if constexpr (!kBf16) v = times_exp2(v, -(m ? e1 : e0));
-                y[i] = was[m][i] + v;
+                float w = d[i >> 1][2 * (i & 1) + m];
+                if constexpr (!kBf16) w = w * back[m][0] * back[m][1];
+                y[m][i] = was[m][i] + w;
             }
-            store4(p.out_type, p.out, orow[m] * p.out_stride + o, left, vec, y);
-        }
+        if (kEarly && u + kWarps < u1) fetch(u + kWarps);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            if (has[m] && left > 0) store4(p.out_type, p.out, orow[m] * p.out_stride + o, left, p.vec >= 4 && left >= 4, y[m]);
     }
     pdl_trigger();
     cluster_wait();
@@ -375,6 +407,18 @@ lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_
 template <bool kBf16, int kRT, int kParts>
 cudaError_t launch_rows(const LoraParams& p, int groups, int cluster, cudaStream_t st) {
     auto kern = lora_rows_kernel<kBf16, kRT, kParts>;
+    if (cluster > 8) {   // (more than every GPU has to offer: to be asked for)
+        static std::mutex mu;
+        static bool configured[128] = {};
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!configured[dev]) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            configured[dev] = true;
+        }
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)groups * cluster);
     cfg.blockDim = dim3(kThreads);
@@ -404,15 +448,33 @@ cudaError_t launch_all(const LoraParams& p, int x_type, int groups, int cluster,
     return three ? launch_rank<false, 3>(p, groups, cluster, st) : launch_rank<false, 2>(p, groups, cluster, st);
 }
 
+// Bytes of an adapter's matrices.
+int64_t adapter_bytes(int K, int O, int r) { return (int64_t)r * ((int64_t)K + O) * 2; }
+
+// Rows that the clusters take as they come, each going through all of them for its own; more are
+// sorted first.  (500 rows: 131 KB an adapter 12.5 us against 20.9 sorted, 64 adapters of 459 KB
+// 26.5 against 43.8, 8 of 1.8 MB 45.7 against 30.6.)
+bool by_scan(int64_t n, int K, int O, int r) { return n <= 256 || (n <= kScanRows && adapter_bytes(K, O, r) < 1 << 20); }
+
+// Blocks of a cluster.  More share an adapter's bytes among them; but most rows' clusters find that
+// another one has them, and all of them are launched.  (us with 4, 8 and 16 blocks: one row, 131 KB an
+// adapter 4.2, 3.7, 3.8, 459 KB 7.9, 5.5, 4.8; 32 rows 4.9, 4.7, 6.8, 11.6, 8.5, 8.7, 1.8 MB 21.2, 14.5, 12.1;
+// 128 rows 6.9, 7.7, 14.4, 15.4, 12.3, 19.0; 256 rows 8.6, 12.4, 22.7, 17.7, 19.2, 27.6.)
+int cluster_blocks(int n, int64_t bytes) {
+    constexpr int64_t kSmall = 256 << 10, kLarge = 1 << 20;
+    if (n <= 32) return bytes >= kLarge || (n <= 8 && bytes >= kSmall) ? 16 : 8;
+    if (n <= 128) return bytes < kSmall ? 4 : 8;
+    return n > 384 && bytes < kSmall ? 2 : 4;
+}
+
 struct Layout {
     size_t perm, segs, part, total;
-    int64_t max_segs;   // of kLoraTile rows
 };
-Layout layout(int64_t n, int L, int r) {
+Layout layout(int64_t n, int L, int K, int O, int r) {
     Layout l{};
     size_t off = sizeof(Ctrl);
     auto take = [&](size_t bytes) { const size_t o = off; off = align_up(off + bytes, 256); return o; };
-    if (n > kScanRows) {
+    if (!by_scan(n, K, O, r)) {
         l.perm = take(sizeof(int32_t) * n);
         l.segs = take(sizeof(int32_t) * 3 * (n / kRows + std::min<int64_t>(n, L + 1) + 1));
         l.part = take(sizeof(float) * lora_part_rows(n) * r);
@@ -441,7 +503,7 @@ cudaError_t launch_sort(const LoraParams& p, int tile, int32_t* perm, int32_t* s
 
 }  // namespace
 
-size_t lora_workspace(int64_t n, int L, int r) { return layout(n, L, r).total; }
+size_t lora_workspace(int64_t n, int L, int K, int O, int r) { return layout(n, L, K, O, r).total; }
 
 cudaError_t launch_lora(const LoraParams& given, int x_type, void* ws, int num_sms, cudaStream_t st) {
     LoraParams p = given;
@@ -454,11 +516,11 @@ cudaError_t launch_lora(const LoraParams& given, int x_type, void* ws, int num_s
         if (rows_of(v, p.out, p.out_stride) && rows_of(v, p.base, p.base_stride)) p.vec = v;
     p.copy = p.base != p.out;
     cudaError_t e;
-    if (p.n <= kScanRows) {
-        e = launch_all(p, x_type, p.n, 8, st);
+    if (by_scan(p.n, p.K, p.O, p.r)) {
+        e = launch_all(p, x_type, p.n, cluster_blocks(p.n, adapter_bytes(p.K, p.O, p.r)), st);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
-    const Layout l = layout(p.n, p.L, p.r);
+    const Layout l = layout(p.n, p.L, p.K, p.O, p.r);
     uint8_t* w = static_cast<uint8_t*>(ws);
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(w);
     p.ctrl = ctrl;

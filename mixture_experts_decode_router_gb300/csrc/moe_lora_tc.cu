@@ -521,6 +521,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
             } else if (warp == kEpiWarps) {
                 const uint32_t idesc = ptx::idesc_f16(kM, kNT, kBf16);
                 const int steps = g.N / 16;
+                const uint64_t a_desc = ptx::sw128_desc(ptx::smem_u32(sV)), b_desc = ptx::sw128_desc(ptx::smem_u32(sB));
                 for (int i = 0; i < nt; ++i) {
                     const int at = done_tiles + i, s = at % kRing, buf = at & 1;
                     if (!wait_warp(&bfull[s], (at / kRing) & 1, s_abort, g.err, 35)) break;
@@ -528,11 +529,17 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                     ptx::tc_fence_after();
                     if (ptx::elect_one()) {
                         uint32_t more = 0;
+                        const uint64_t b = b_desc + (uint32_t)(s * vbytes >> 4);
                         for (int m = kParts - 1; m >= 0; --m)     // the smallest part first
-                            for (int k = 0; k < steps; ++k) {
-                                ptx::mma_f16(tmem + buf * kNT, ptx::sw128_desc(ptx::smem_u32(sV + m * vbytes + (k / 4) * kBoxBytes)) + 2 * (k % 4),
-                                             ptx::sw128_desc(ptx::smem_u32(sB + s * vbytes + (k / 4) * kBoxBytes)) + 2 * (k % 4), idesc, more);
-                                more = 1;
+                            for (int box = 0; box < boxes; ++box) {
+                                const uint32_t at = (uint32_t)(box * kBoxBytes >> 4);
+                                const uint64_t a = a_desc + (uint32_t)(m * vbytes >> 4) + at;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (4 * box + k < steps) {
+                                        ptx::mma_f16(tmem + buf * kNT, a + 2 * k, b + at + 2 * k, idesc, more);
+                                        more = 1;
+                                    }
                             }
                         ptx::mma_commit(&bempty[s]);
                         ptx::mma_commit(&tfull[buf]);
