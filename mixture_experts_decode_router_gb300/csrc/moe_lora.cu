@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     const int C = (int)cluster_size(), c = (int)cluster_rank(), group = blockIdx.x / C;
     if (tid < kRows) s_top[tid] = 0;
     pdl_wait();
+    pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
 
     // The cluster's rows: row `group`, if an adapter's rows before it fill whole clusters, and
     // the next ones of its adapter; or a run of the rows sorted by adapter.
@@ -290,7 +291,6 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
         for (int m = 0; m < 2; ++m)
             if (has[m] && left > 0) store4(p.out_type, p.out, orow[m] * p.out_stride + o, left, p.vec >= 4 && left >= 4, y[m]);
     }
-    pdl_trigger();
     cluster_wait();
 }
 
@@ -308,6 +308,7 @@ lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_
     for (int i = tid; i < (L + 1) * kSortWarps; i += kSortThreads) cnt[i] = 0;
     __syncthreads();
     pdl_wait();
+    pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
     const int per = (int)(((int64_t)n + kSortThreads - 1) / kSortThreads) * 32;
     const int64_t begin = (int64_t)warp * per, end = min((int64_t)n, begin + per);
     int ev[kBatch];
@@ -401,7 +402,6 @@ lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_
             __syncwarp();
         }
     }
-    pdl_trigger();
 }
 
 template <bool kBf16, int kRT, int kParts>

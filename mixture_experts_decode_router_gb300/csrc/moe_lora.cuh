@@ -94,11 +94,16 @@ __device__ __forceinline__ void store4(int type, void* p, int64_t at, int left, 
 }
 
 // Single elements, and the 16 bytes of four (fp32) or eight.
-template <int kType> __device__ __forceinline__ float load_one(const void* p, int64_t at) {
-    if constexpr (kType == MOE_F32) return reinterpret_cast<const float*>(p)[at];
-    const uint16_t u = reinterpret_cast<const uint16_t*>(p)[at];
-    return kType == MOE_BF16 ? bf16_lo(u) : __half2float(__ushort_as_half(u));
+template <int kType> __device__ __forceinline__ uint32_t load_bits(const void* p, int64_t at) {
+    if constexpr (kType == MOE_F32) return reinterpret_cast<const uint32_t*>(p)[at];
+    else return reinterpret_cast<const uint16_t*>(p)[at];
 }
+template <int kType> __device__ __forceinline__ float of_bits(uint32_t u) {
+    if constexpr (kType == MOE_F32) return __uint_as_float(u);
+    else if constexpr (kType == MOE_BF16) return bf16_lo(u);
+    else return __half2float(__ushort_as_half((uint16_t)u));
+}
+template <int kType> __device__ __forceinline__ float load_one(const void* p, int64_t at) { return of_bits<kType>(load_bits<kType>(p, at)); }
 template <int kType> __device__ __forceinline__ void store_one(void* p, int64_t at, float v) {
     if constexpr (kType == MOE_F32) reinterpret_cast<float*>(p)[at] = v;
     else reinterpret_cast<uint16_t*>(p)[at] = kType == MOE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));

@@ -186,6 +186,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
     ptx::tc_fence_after();
     const uint32_t tmem = *s_tmem;
     pdl_wait();
+    pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
 
     const int runs = p.ctrl->n_active, boxes = (p.K + kBox - 1) / kBox;
     const Pieces ks = pieces(runs, boxes, g.max_splits, kLoraBlocks);
@@ -258,7 +259,6 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
     // After a wait that gave up, copies may be in flight: they end before the block does.
     if (*s_abort && threadIdx.x == 0)
         for (int s = 0; s < g.stages; ++s) ptx::mbar_wait_quiet(&full[s], phase, ptx::kWaitLimitNs / 8);
-    pdl_trigger();
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -319,6 +319,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
     ptx::tc_fence_after();
     const uint32_t tmem = *s_tmem;
     pdl_wait();
+    pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
 
     const int O = p.O, n_tiles = (O + kNT - 1) / kNT, runs = p.ctrl->n_rsegs;
     const Pieces ks = pieces(p.ctrl->n_active, (p.K + kBox - 1) / kBox, g.max_splits, kLoraBlocks);
@@ -551,14 +552,22 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                     epilogue();
                 } else {
                     // Any rows: 64 of the 128 outputs in two passes of 32, through the warp's staging; neighbouring lanes
-                    // at neighbouring elements, eight rows in flight.
+                    // at neighbouring elements, all 32 rows' loads in flight while the products run (eight rows' at a
+                    // time, behind them: 110 us against XX for 6000 rows of 3551 outputs).
                     float* stage = reinterpret_cast<float*>(sStage + warp * kStageBytes);
                     for (int i = 0; i < nt; ++i) {
                         const int buf = (done_tiles + i) & 1;
-                        if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) break;
-                        ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
+                            const int o = (t0 + i) * kNT + half * 64 + h * 32 + lane;
+                            uint32_t was[32];
+#pragma unroll
+                            for (int w = 0; w < 32; ++w)
+                                was[w] = p.base && w < here && o < O ? load_bits<kOut>(p.base, (int64_t)s_rows[32 * q + w] * p.base_stride + o) : 0u;
+                            if (h == 0) {
+                                if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) break;
+                                ptx::tc_fence_after();
+                            }
                             if (here > 0) {
                                 const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * kNT + half * 64 + h * 32;
                                 float d[16];
@@ -574,22 +583,13 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                             if (h == 1) ptx::tc_fence_before();       // the accumulator is read
                             __syncwarp();
                             if (h == 1) ptx::mbar_arrive_elect(&tempty[buf]);
-                            const int o = (t0 + i) * kNT + half * 64 + h * 32 + lane;
-                            for (int b0 = 0; b0 < here; b0 += 8) {
-                                float y[8];
 #pragma unroll
-                                for (int w = 0; w < 8; ++w)
-                                    y[w] = p.base && b0 + w < here && o < O
-                                               ? load_one<kOut>(p.base, (int64_t)s_rows[32 * q + b0 + w] * p.base_stride + o)
-                                               : 0.f;
-#pragma unroll
-                                for (int w = 0; w < 8; ++w) {
-                                    const int r = 32 * q + b0 + w;
-                                    if (b0 + w < here && o < O) {
-                                        float v = stage[(b0 + w) * kStageRow + lane];
-                                        if constexpr (!kBf16) v = times_exp2(v, -s_exp[r]);
-                                        store_one<kOut>(p.out, (int64_t)s_rows[r] * p.out_stride + o, p.base ? y[w] + v : v);
-                                    }
+                            for (int w = 0; w < 32; ++w) {
+                                const int r = 32 * q + w;
+                                if (w < here && o < O) {
+                                    float v = stage[w * kStageRow + lane];
+                                    if constexpr (!kBf16) v = times_exp2(v, -s_exp[r]);
+                                    store_one<kOut>(p.out, (int64_t)s_rows[r] * p.out_stride + o, p.base ? of_bits<kOut>(was[w]) + v : v);
                                 }
                             }
                             __syncwarp();                             // the staging is read
@@ -602,7 +602,6 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
         if (__syncthreads_or(*s_abort)) break;   // (and v and the rows' numbers are read)
     }
     if (kWide) cp_wait<0>();
-    pdl_trigger();
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == kEpiWarps) {

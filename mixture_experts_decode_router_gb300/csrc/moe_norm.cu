@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads, kWide || kR =
 #pragma unroll
     for (int c = 0; c < kCh; ++c) in[c] = live && (c * T + tid) * 8 < p.H;
     pdl_wait();
+    pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
 
     // Every load of the row before the first use; of a thread's only chunk the weight's too.
     Raw8<kX> xr[kCh];
@@ -323,7 +324,6 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads, kWide || kR =
             }
         },
         [&](int c) { return kCh == 1 ? wr : load_w16(c); });
-    pdl_trigger();
 }
 
 // ---------------------------------------------------------------- rows of any alignment
@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kMost) norm_any_kernel(const NormParams p) {
     const uint8_t* res = reinterpret_cast<const uint8_t*>(p.res) + row * p.res_stride * size_of(kRT);
     uint8_t* res_out = reinterpret_cast<uint8_t*>(p.res_out) + row * p.res_out_stride * size_of(kRT);
     pdl_wait();
+    pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
     float2 h[kE / 2];
     float rv[kR < 0 ? 1 : kE];
     auto each = [&](int i) -> float& { return i & 1 ? h[i / 2].y : h[i / 2].x; };
@@ -444,7 +445,6 @@ __global__ void __launch_bounds__(kMost) norm_any_kernel(const NormParams p) {
             p.out8[row * p.out8_stride + at] = (uint8_t)e4m3x2(make_float2(each(i) * reciprocal(s), 0.f));
         }
     }
-    pdl_trigger();
 }
 
 // ---------------------------------------------------------------- launches
