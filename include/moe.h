@@ -521,7 +521,8 @@ size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows);
  *               row to the last
  *   ws          device workspace (16-byte aligned) of at least
  *               moe_lora_workspace_bytes(cfg, n) bytes; it need not be cleared,
- *               and keeps nothing between calls
+ *               and keeps nothing between calls (256 bytes: it is not used, and
+ *               may be any address)
  * base and out are aligned to their element.  fp32 sums; A_e x[t] enters the
  * second product in 16 bits of precision for outputs of 16 bits, in 24 for
  * fp32 outputs; one rounding to out_type, after the addition of base.

@@ -58,13 +58,12 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 
 // out[row] = base[row] (zeros without a base), the block's part `part` of `parts`.
 __device__ __forceinline__ void copy_row(const LoraParams& p, int64_t row, int part, int parts) {
-    const int quads = (p.O + 3) / 4;
-    for (int q = part * kThreads + threadIdx.x; q < quads; q += parts * kThreads) {
+    const int quads = (p.O + 3) / 4, step = p.vec >= 4 ? 1 : kThreads;
+    for (int q0 = part * kThreads; q0 < quads; q0 += parts * kThreads) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-        const int left = p.O - 4 * q;
-        const bool vec = p.vec >= 4 && left >= 4;
-        if (p.base) load4(p.out_type, p.base, row * p.base_stride + 4 * q, left, vec, v);
-        store4(p.out_type, p.out, row * p.out_stride + 4 * q, left, vec, v);
+        const int o = 4 * q0 + (step == 1 ? 4 : 1) * (int)threadIdx.x, left = p.O - o;
+        if (p.base) load4(p.out_type, p.base, row * p.base_stride + o, step, left, v);
+        store4(p.out_type, p.out, row * p.out_stride + o, step, left, v);
     }
 }
 
@@ -138,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
         const int64_t b0 = (int64_t)c * uper * 32 * r, b1 = (int64_t)min(O, u1 * 32) * r;
         for (int64_t e = b0 + tid * 64; e < b1; e += kThreads * 64) prefetch_l2(Bm + e);
     }
+    const float scale = p.scale ? __ldg(p.scale + adapter) : 1.f;   // (long before it is used)
     float acc[kRT][4];
 #pragma unroll
     for (int j = 0; j < kRT; ++j)
@@ -192,21 +192,25 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     }
     uint2 bv[kRT][2][2];
     float was[2][4];
+    // Output i of this lane's four of a unit: neighbouring ones where rows are read and written four at a time,
+    // else 8 apart, so that neighbouring lanes have neighbouring ones.
+    const bool fours = p.vec >= 4;
+    const int ostep = fours ? 1 : 8, ofirst = fours ? 4 * g : g;
     auto fetch = [&](int u) {
-        const int o = u * 32 + 4 * g, left = u < u1 ? O - o : 0;
+        const int o = u * 32 + ofirst, left = u < u1 ? O - o : 0;
         const uint16_t* at = Bm + (int64_t)o * r + 4 * t;
 #pragma unroll
         for (int j = 0; j < kRT; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool in = i < left && j * 16 + 4 * t < r;
-                bv[j][i >> 1][i & 1] = in ? ld_stream_v2(at + i * r + j * 16) : make_uint2(0u, 0u);
+                const bool in = i * ostep < left && j * 16 + 4 * t < r;
+                bv[j][i >> 1][i & 1] = in ? ld_stream_v2(at + i * ostep * r + j * 16) : make_uint2(0u, 0u);
             }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) was[m][i] = 0.f;
-            if (p.base && has[m] && left > 0) load4(p.out_type, p.base, orow[m] * p.base_stride + o, left, p.vec >= 4 && left >= 4, was[m]);
+            if (p.base && has[m]) load4(p.out_type, p.base, orow[m] * p.base_stride + o, ostep, left, was[m]);
         }
     };
     constexpr bool kEarly = kRT < 8;
@@ -214,7 +218,6 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     cluster_arrive();
     cluster_wait();
     // Each element of v is summed over the blocks in their order, and split, by one thread.
-    const float scale = p.scale ? __ldg(p.scale + adapter) : 1.f;
     constexpr int kMine = (kR * kRows + kThreads - 1) / kThreads;
     float v[kMine];
 #pragma unroll
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     // four units at once took 4.9 us for a row of 2048 that takes 3.7 so.)
 #pragma unroll 1
     for (int u = c * uper + warp; u < u1; u += kWarps) {
-        const int o = u * 32 + 4 * g, left = O - o;
+        const int o = u * 32 + ofirst, left = O - o;
         if (!kEarly) fetch(u);
         float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
         if (kEarly && u + kWarps < u1) fetch(u + kWarps);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-            if (has[m] && left > 0) store4(p.out_type, p.out, orow[m] * p.out_stride + o, left, p.vec >= 4 && left >= 4, y[m]);
+            if (has[m]) store4(p.out_type, p.out, orow[m] * p.out_stride + o, ostep, left, y[m]);
     }
     cluster_wait();
 }

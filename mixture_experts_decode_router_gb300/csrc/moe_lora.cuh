@@ -26,74 +26,7 @@ template <bool kBf16, int kParts> __device__ __forceinline__ void split(float v,
     }
 }
 
-// Four consecutive elements of a row of base or out.
-__device__ __forceinline__ void load4(int type, const void* p, int64_t at, int left, bool vec, float (&v)[4]) {
-    if (type == MOE_F32) {
-        const float* f = reinterpret_cast<const float*>(p) + at;
-        if (vec) {
-            const float4 q = *reinterpret_cast<const float4*>(f);
-            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = i < left ? f[i] : 0.f;
-        }
-        return;
-    }
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(p) + at;
-    uint32_t u[2];
-    if (vec) {
-        const uint2 q = *reinterpret_cast<const uint2*>(h);
-        u[0] = q.x; u[1] = q.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) u[i] = (2 * i < left ? h[2 * i] : 0u) | ((2 * i + 1 < left ? (uint32_t)h[2 * i + 1] : 0u) << 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (type == MOE_BF16) {
-            v[2 * i] = bf16_lo(u[i]);
-            v[2 * i + 1] = bf16_hi(u[i]);
-        } else {
-            const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-            v[2 * i] = q.x;
-            v[2 * i + 1] = q.y;
-        }
-    }
-}
-__device__ __forceinline__ void store4(int type, void* p, int64_t at, int left, bool vec, const float (&v)[4]) {
-    if (type == MOE_F32) {
-        float* f = reinterpret_cast<float*>(p) + at;
-        if (vec) {
-            *reinterpret_cast<float4*>(f) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < left) f[i] = v[i];
-        }
-        return;
-    }
-    uint32_t u[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (type == MOE_BF16) {
-            const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&q);
-        } else {
-            const __half2 q = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&q);
-        }
-    }
-    uint16_t* h = reinterpret_cast<uint16_t*>(p) + at;
-    if (vec) {
-        *reinterpret_cast<uint2*>(h) = make_uint2(u[0], u[1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < left) h[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
-    }
-}
-
-// Single elements, and the 16 bytes of four (fp32) or eight.
+// Single elements.
 template <int kType> __device__ __forceinline__ uint32_t load_bits(const void* p, int64_t at) {
     if constexpr (kType == MOE_F32) return reinterpret_cast<const uint32_t*>(p)[at];
     else return reinterpret_cast<const uint16_t*>(p)[at];
@@ -108,6 +41,51 @@ template <int kType> __device__ __forceinline__ void store_one(void* p, int64_t 
     if constexpr (kType == MOE_F32) reinterpret_cast<float*>(p)[at] = v;
     else reinterpret_cast<uint16_t*>(p)[at] = kType == MOE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
+// Four elements of a row of base or out, `step` apart, as far as there are (`left`, counted from the first).
+// Neighbouring ones (step 1) are four elements aligned together.
+template <int kType> __device__ __forceinline__ void load4_of(const void* p, int64_t at, int step, int left, float (&v)[4]) {
+    if (step == 1 && left >= 4) {
+        if constexpr (kType == MOE_F32) {
+            const float4 q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
+            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        } else {
+            const uint2 q = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + at);
+            v[0] = of_bits<kType>(q.x & 0xffffu); v[1] = of_bits<kType>(q.x >> 16);
+            v[2] = of_bits<kType>(q.y & 0xffffu); v[3] = of_bits<kType>(q.y >> 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i * step < left ? load_one<kType>(p, at + i * step) : 0.f;
+    }
+}
+__device__ __forceinline__ void load4(int type, const void* p, int64_t at, int step, int left, float (&v)[4]) {
+    if (type == MOE_F32) load4_of<MOE_F32>(p, at, step, left, v);
+    else if (type == MOE_BF16) load4_of<MOE_BF16>(p, at, step, left, v);
+    else load4_of<MOE_F16>(p, at, step, left, v);
+}
+template <int kType> __device__ __forceinline__ void store4_of(void* p, int64_t at, int step, int left, const float (&v)[4]) {
+    if (step == 1 && left >= 4) {
+        if constexpr (kType == MOE_F32) {
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            uint16_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store_one<kType>(u, i, v[i]);
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + at) = make_uint2(u[0] | (uint32_t)u[1] << 16, u[2] | (uint32_t)u[3] << 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i * step < left) store_one<kType>(p, at + i * step, v[i]);
+    }
+}
+__device__ __forceinline__ void store4(int type, void* p, int64_t at, int step, int left, const float (&v)[4]) {
+    if (type == MOE_F32) store4_of<MOE_F32>(p, at, step, left, v);
+    else if (type == MOE_BF16) store4_of<MOE_BF16>(p, at, step, left, v);
+    else store4_of<MOE_F16>(p, at, step, left, v);
+}
+
+// The 16 bytes of four elements (fp32) or eight.
 template <int kType> __device__ __forceinline__ void add_raw(const uint4& was, float* y) {
     const uint32_t u[4] = {was.x, was.y, was.z, was.w};
 #pragma unroll

@@ -414,10 +414,12 @@ PyObject* lora(PyObject* const* a, Py_ssize_t na) {
         out = matrix(n, O, type, dev, st);
         Y = {out.data_ptr(), O};
     }
-    // The call's own workspace, of its stream's memory: calls on several streams share none.
+    // The call's own workspace, of its stream's memory: calls on several streams share none.  (One of 256
+    // bytes is not used: any address will do.)
     const size_t ws_bytes = g_lora_workspace_bytes(c, (int32_t)n);
-    at::Tensor ws = matrix(1, (int64_t)ws_bytes, at::kByte, dev, st);
-    void* wp = ws.data_ptr();
+    at::Tensor ws;
+    void* wp = const_cast<void*>(wa.data_ptr());
+    if (ws_bytes > 256) wp = (ws = matrix(1, (int64_t)ws_bytes, at::kByte, dev, st)).data_ptr();
     const void *ap = wa.data_ptr(), *bp = wb.data_ptr(), *xp = x.data_ptr();
     const float* sp = scale ? data<const float>(*scale) : nullptr;
     const int32_t* ip = data<const int32_t>(idx);
