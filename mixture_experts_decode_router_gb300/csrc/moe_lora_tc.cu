@@ -468,7 +468,11 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                             __syncwarp();
                             ptx::mbar_arrive_elect(&tempty[buf]);
                         }
-                        if (here <= 16 * u) continue;
+                        if (here <= 16 * u) {                    // (no rows: their groups all the same, so that the waits count right)
+                            cp_commit();
+                            cp_commit();
+                            continue;
+                        }
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
                             const int r = 2 * u + s;

@@ -195,6 +195,25 @@ def test_row_counts(lib, n, L):
 
 
 @gpu
+@pytest.mark.parametrize("y", [BF, F32])
+@pytest.mark.parametrize("O", [1024, 2080, 1003])
+@pytest.mark.parametrize("rest", [1, 3, 8, 15, 16, 17, 31, 32, 33, 48, 49, 80, 97, 113, 127, 128])
+def test_runs_that_end_inside_a_tile(lib, y, O, rest):
+    """Rows of an adapter behind whole tiles of 128, over several tiles of outputs, together in memory and not."""
+    a, b, s = adapters(4, 16, 192, O)
+    op = MoeLora(a, b, s, out_dtype=y)
+    idx = torch.cat([torch.full((m,), e, dtype=torch.int32, device="cuda")
+                     for e, m in enumerate((128 + rest, rest, 256 + rest, 384 + rest))])
+    n = len(idx)
+    x, base = rows(n, 192, seed=rest), rows(n, O, y, seed=8)
+    check(op, x, idx, base, op.forward(x, idx, base))
+    p = torch.randperm(n, generator=torch.Generator().manual_seed(rest)).cuda()
+    check(op, x, idx[p], base, op.forward(x, idx[p], base))
+    got = op.forward(x, idx)
+    check(op, x, idx, None, got)
+
+
+@gpu
 @pytest.mark.parametrize("n", [5, 300, 900])
 def test_indexes_outside(lib, n):
     """-1, the number of adapters, and the ends of int32 are no adapter."""
