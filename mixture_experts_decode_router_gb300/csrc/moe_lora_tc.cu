@@ -631,7 +631,7 @@ cudaError_t configure(Kern kern, int slot) {
 
 bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[5]) {
     // (Coordinates are 32-bit; strides fit 40 bits.)
-    if ((int64_t)p.L * p.O > INT32_MAX || p.x_stride * 2 >= (int64_t)1 << 40) return false;
+    if ((int64_t)p.L * p.O > INT32_MAX - 1024 || p.x_stride * 2 >= (int64_t)1 << 40) return false;
     const CUtensorMapDataType t = x_type == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const uint32_t N = (p.r + 15) / 16 * 16;
     return make_map(&maps[0], p.x, t, 2, p.K, p.n, kBox, 1, CU_TENSOR_MAP_SWIZZLE_128B, p.x_stride) &&

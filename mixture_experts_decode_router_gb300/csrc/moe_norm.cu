@@ -29,23 +29,6 @@ __host__ __device__ constexpr int size_of(int type) { return type == MOE_F32 ? 4
 
 // ---------------------------------------------------------------- pairs of fp32
 
-__device__ __forceinline__ uint64_t bits2(float2 v) { return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x); }
-__device__ __forceinline__ float2 floats2(uint64_t u) { return make_float2(__uint_as_float((uint32_t)u), __uint_as_float((uint32_t)(u >> 32))); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return floats2(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return floats2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-    return floats2(r);
-}
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // Two floats of a 16-bit pair, and back (to nearest even).
@@ -166,7 +149,7 @@ template <int N> __device__ __forceinline__ float row_rstd(float ss, float2 (&h)
     float s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        h[i] = mul2(h[i], both(pre));
+        h[i] = __fmul2_rn(h[i], both(pre));
         s2 += h[i].x * h[i].x + h[i].y * h[i].y;
     }
     return 1.f / sqrtf(row_sum(s2, T, red) * inv_h + (p.eps * pre) * pre);
@@ -196,7 +179,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
                 float2 r[4];
                 floats8<kRT>(rr, r);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) hc[i] = add2(hc[i], r[i]);
+                for (int i = 0; i < 4; ++i) hc[i] = __fadd2_rn(hc[i], r[i]);
                 if constexpr (kR != MOE_F32) {   // the rows that are normalised are those that are stored
                     const uint4 st = make_uint4(pack2<kRT>(hc[0]), pack2<kRT>(hc[1]), pack2<kRT>(hc[2]), pack2<kRT>(hc[3]));
                     if (p.res_out) *reinterpret_cast<uint4*>(res_out + (size_t)(c * T + tid) * 16) = st;
@@ -206,7 +189,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ss = fma2(hc[i], hc[i], ss);
+            for (int i = 0; i < 4; ++i) ss = __ffma2_rn(hc[i], hc[i], ss);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) hc[i] = make_float2(0.f, 0.f);
@@ -235,10 +218,10 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
             }
             if (p.w_offset != 0.f) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = add2(w[i], both(p.w_offset));
+                for (int i = 0; i < 4; ++i) w[i] = __fadd2_rn(w[i], both(p.w_offset));
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(y[i], rstd), w[i]);
+            for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(y[i], rstd), w[i]);
             if (p.out) {
                 uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + r0 * p.out_stride * size_of(p.out_type);
                 if (p.out_type == MOE_BF16) store8<MOE_BF16>(out, at, y);
@@ -259,7 +242,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
                     if ((tid & 15) == 0) p.scale8[row * p.n_scales + at / 128] = s;
                     const float2 inv = both(reciprocal(s));
                     *reinterpret_cast<uint2*>(p.out8 + r0 * p.out8_stride + at) =
-                        make_uint2(e4m3x2(mul2(y[0], inv)) | e4m3x2(mul2(y[1], inv)) << 16, e4m3x2(mul2(y[2], inv)) | e4m3x2(mul2(y[3], inv)) << 16);
+                        make_uint2(e4m3x2(__fmul2_rn(y[0], inv)) | e4m3x2(__fmul2_rn(y[1], inv)) << 16, e4m3x2(__fmul2_rn(y[2], inv)) | e4m3x2(__fmul2_rn(y[3], inv)) << 16);
                 }
             } else {
                 top = max(top, most);
@@ -275,7 +258,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
             const float2* y = &h[4 * c];
             if (in[c])
                 *reinterpret_cast<uint2*>(p.out8 + r0 * p.out8_stride + (c * T + tid) * 8) =
-                    make_uint2(e4m3x2(mul2(y[0], inv)) | e4m3x2(mul2(y[1], inv)) << 16, e4m3x2(mul2(y[2], inv)) | e4m3x2(mul2(y[3], inv)) << 16);
+                    make_uint2(e4m3x2(__fmul2_rn(y[0], inv)) | e4m3x2(__fmul2_rn(y[1], inv)) << 16, e4m3x2(__fmul2_rn(y[2], inv)) | e4m3x2(__fmul2_rn(y[3], inv)) << 16);
         }
     }
 }
