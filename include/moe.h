@@ -372,7 +372,8 @@ moe_status_t moe_static_workspace_check(int32_t* device_error, void** workspace,
  *                       wait of the single-token kernel gave up; 1-5: a bounded
  *                       wait of the grouped tensor-core kernels gave up (8: the
  *                       down kernel's grid barrier before its combine); 6-7:
- *                       one of the tensor-core router's; 20: the workspace
+ *                       one of the tensor-core router's; 31-37: one of
+ *                       moe_lora's, in its workspace; 20: the workspace
  *                       control block was not zeroed before use.  An FP8
  *                       call on the grouped path made while an error is
  *                       pending does not write out (its down kernel, which
@@ -521,8 +522,9 @@ size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows);
  *               row to the last
  *   ws          device workspace (16-byte aligned) of at least
  *               moe_lora_workspace_bytes(cfg, n) bytes; it need not be cleared,
- *               and keeps nothing between calls (256 bytes: it is not used, and
- *               may be any address)
+ *               and keeps nothing between calls but the error word of the last,
+ *               for moe_workspace_check (256 bytes: it is not used, and may be
+ *               any address)
  * base and out are aligned to their element.  fp32 sums; A_e x[t] enters the
  * second product in 16 bits of precision for outputs of 16 bits, in 24 for
  * fp32 outputs; one rounding to out_type, after the addition of base.
