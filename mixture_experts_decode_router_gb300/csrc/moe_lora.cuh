@@ -37,6 +37,10 @@ template <int kType> __device__ __forceinline__ float of_bits(uint32_t u) {
     else return __half2float(__ushort_as_half((uint16_t)u));
 }
 template <int kType> __device__ __forceinline__ float load_one(const void* p, int64_t at) { return of_bits<kType>(load_bits<kType>(p, at)); }
+template <int kType> __device__ __forceinline__ void store_bits(void* p, int64_t at, uint32_t u) {
+    if constexpr (kType == MOE_F32) reinterpret_cast<uint32_t*>(p)[at] = u;
+    else reinterpret_cast<uint16_t*>(p)[at] = (uint16_t)u;
+}
 template <int kType> __device__ __forceinline__ void store_one(void* p, int64_t at, float v) {
     if constexpr (kType == MOE_F32) reinterpret_cast<float*>(p)[at] = v;
     else reinterpret_cast<uint16_t*>(p)[at] = kType == MOE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
@@ -101,6 +105,14 @@ template <int kType> __device__ __forceinline__ void add_raw(const uint4& was, f
             y[2 * i + 1] += q.y;
         }
     }
+}
+// The same from single elements.
+template <int kType> __device__ __forceinline__ uint4 gather_raw(const void* p, int64_t at) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        u[i] = kType == MOE_F32 ? load_bits<kType>(p, at + i) : load_bits<kType>(p, at + 2 * i) | load_bits<kType>(p, at + 2 * i + 1) << 16;
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 template <int kType> __device__ __forceinline__ uint4 pack_raw(const float* y) {
     uint32_t u[4];

@@ -271,8 +271,8 @@ constexpr int kNT = 128;                 // outputs of a tile
 constexpr int kEpiWarps = 8;             // 32 rows and 64 outputs of a tile each
 constexpr int kExpandThreads = 32 * (kEpiWarps + 2);
 constexpr int kRing = 2;                 // tiles of B in flight
-constexpr int kStageRow = 36;            // floats of a row of a warp's staging (32 and 4: no bank conflicts)
-constexpr int kStageBytes = 32 * kStageRow * 4;
+constexpr int kStageRow = 70;            // floats of a row of a warp's staging (64 and 6: fewest bank conflicts of both its sides)
+constexpr int kStageBytes = 16 * kStageRow * 4;
 
 __host__ __device__ constexpr int expand_parts(bool f32) { return f32 ? 3 : 2; }
 constexpr size_t kMaxSmem = 226 * 1024;  // (beside 1 KB of static arrays)
@@ -281,6 +281,42 @@ __host__ __device__ constexpr int ahead_bytes(bool f32) { return 32 * 64 * (f32 
 inline size_t expand_smem(int rank16, bool f32, bool wide) {
     const int boxes = (rank16 + kBox - 1) / kBox;
     return 1024 + (size_t)(expand_parts(f32) + kRing) * boxes * kBoxBytes + kEpiWarps * (wide ? ahead_bytes(f32) : kStageBytes) + 256;
+}
+
+// Outputs o0 .. o1 of a row that has no adapter, by a warp: base's elements as they are (or zeros), 16 bytes at a
+// time where the two rows are aligned alike, and then what is left at both ends; else by elements.
+template <int kOut> __device__ __forceinline__ void copy_row(const LoraParams& p, int64_t row, int o0, int o1, int lane) {
+    constexpr int kSize = kOut == MOE_F32 ? 4 : 2, kV = 16 / kSize, kU = 4;
+    const int64_t from = row * p.base_stride, to = row * p.out_stride;
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(p.base) + from * kSize;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + to * kSize;
+    const uint32_t lag = (uint32_t)(reinterpret_cast<uintptr_t>(dst) + (uintptr_t)o0 * kSize);
+    auto elements = [&](int a, int b) {
+        for (int o = a + lane; o < b; o += 32 * 2 * kU) {
+            uint32_t v[2 * kU];
+#pragma unroll
+            for (int u = 0; u < 2 * kU; ++u) v[u] = p.base && o + 32 * u < b ? load_bits<kOut>(src, o + 32 * u) : 0u;
+#pragma unroll
+            for (int u = 0; u < 2 * kU; ++u)
+                if (o + 32 * u < b) store_bits<kOut>(dst, o + 32 * u, v[u]);
+        }
+    };
+    int a = o0, b = o0;      // whole pieces: a .. b
+    if (!p.base || ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) == 0) {
+        a = min(o1, o0 + (int)((0u - lag) & 15) / kSize);
+        b = a + (o1 - a) / kV * kV;
+        for (int o = a + lane * kV; o < b; o += kU * kV * 32) {
+            uint4 v[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                v[u] = p.base && o + u * 32 * kV < b ? *reinterpret_cast<const uint4*>(src + (size_t)(o + u * 32 * kV) * kSize) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (o + u * 32 * kV < b) *reinterpret_cast<uint4*>(dst + (size_t)(o + u * 32 * kV) * kSize) = v[u];
+        }
+    }
+    elements(o0, a);
+    elements(b, o1);
 }
 
 // kWide: rows of base and out that are aligned to 16 bytes, of a multiple of 32 (fp32: 16) outputs.
@@ -333,31 +369,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
         if (adapter < 0 && p.copy) {
             // Rows without an adapter: base's elements as they are.
             const int o0 = t0 * kNT, o1 = min(O, (t0 + nt) * kNT);
-            constexpr int kU = 4;
-            for (int i = warp; i < count; i += kEpiWarps + 2) {
-                const int64_t row = p.perm[first + i];
-                const uint8_t* from = reinterpret_cast<const uint8_t*>(p.base) + row * p.base_stride * kSize;
-                uint8_t* to = reinterpret_cast<uint8_t*>(p.out) + row * p.out_stride * kSize;
-                int o = o0;
-                if (p.vec >= kV) {
-                    for (; o + kV * 32 <= o1; o += kU * kV * 32) {
-                        uint4 v[kU];
-#pragma unroll
-                        for (int u = 0; u < kU; ++u) {
-                            const int at = o + (u * 32 + lane) * kV;
-                            v[u] = p.base && at + kV <= o1 ? *reinterpret_cast<const uint4*>(from + (size_t)at * kSize) : make_uint4(0u, 0u, 0u, 0u);
-                        }
-#pragma unroll
-                        for (int u = 0; u < kU; ++u) {
-                            const int at = o + (u * 32 + lane) * kV;
-                            if (at + kV <= o1) *reinterpret_cast<uint4*>(to + (size_t)at * kSize) = v[u];
-                        }
-                    }
-                    o = min(o, o0 + (o1 - o0) / kV * kV);
-                }
-                for (o += lane; o < o1; o += 32)
-                    store_one<kOut>(p.out, row * p.out_stride + o, p.base ? load_one<kOut>(p.base, row * p.base_stride + o) : 0.f);
-            }
+            for (int i = warp; i < count; i += kEpiWarps + 2) copy_row<kOut>(p, p.perm[first + i], o0, o1, lane);
         } else if (adapter >= 0) {
             const int q = warp & 3, half = warp >> 2, here = warp < kEpiWarps ? min(32, count - 32 * q) : 0;
             if (warp < 4 && lane < here) s_rows[32 * q + lane] = p.perm[first + 32 * q + lane];
@@ -499,6 +511,98 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                     }
                 }
             };
+            // Any rows: 64 outputs of 16 rows at a time through the warp's staging.  Of each row its aligned pieces of 16
+            // bytes belong to neighbouring lanes, and what is left before and behind them (8 elements of 16 bits, 4 of 32,
+            // where the tile is full) to the same lanes by single elements.  All 32 rows of base are in flight while the
+            // products run.
+            auto any_rows = [&]() {
+                constexpr int kCh = 64 / kV, kAt = 32 / kCh, kIt = 16 / kAt;   // pieces of a row, rows at a time, times of 16 rows
+                float* stage = reinterpret_cast<float*>(sStage + warp * kStageBytes);
+                const int c = lane % kCh, sub = lane / kCh;
+                const bool alike = ((reinterpret_cast<uintptr_t>(p.base) ^ reinterpret_cast<uintptr_t>(p.out)) & 15) == 0 &&
+                                   ((p.base_stride - p.out_stride) * kSize & 15) == 0;
+                const uint32_t lag = (uint32_t)reinterpret_cast<uintptr_t>(p.out) / kSize;   // (in elements)
+                for (int i = 0; i < nt; ++i) {
+                    const int buf = (done_tiles + i) & 1, o0 = (t0 + i) * kNT + half * 64, lim = max(0, min(64, O - o0));
+                    // Of row `w` of the warp's: its number, the outputs before the first whole piece, and the pieces.
+                    auto place = [&](int w, int64_t& row, int& head, int& whole) {
+                        row = s_rows[32 * q + w];
+                        head = (int)((0u - lag - (uint32_t)row * (uint32_t)p.out_stride) & (kV - 1));
+                        whole = max(0, lim - head) / kV;
+                    };
+                    uint4 was[2 * kIt];
+                    uint32_t one[2 * kIt];
+#pragma unroll
+                    for (int t = 0; t < 2 * kIt; ++t) {
+                        was[t] = make_uint4(0u, 0u, 0u, 0u);
+                        one[t] = 0u;
+                        const int w = kAt * t + sub;
+                        if (p.base && w < here) {
+                            int64_t row;
+                            int head, whole;
+                            place(w, row, head, whole);
+                            const int64_t at = row * p.base_stride + o0;
+                            if (c < whole) {
+                                if (alike) was[t] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p.base) + (at + head + kV * c) * kSize);
+                                else was[t] = gather_raw<kOut>(p.base, at + head + kV * c);
+                            }
+                            if (c < lim - kV * whole) one[t] = load_bits<kOut>(p.base, at + (c < head ? c : kV * whole + c));
+                        }
+                    }
+                    if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) return;
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (here > 16 * u) {
+                            float d[32];
+                            tmem_ld_fragments(tmem + ((uint32_t)(32 * q + 16 * u) << 16) + buf * kNT + half * 64, d);
+                            float* to = stage + (lane >> 2) * kStageRow + 2 * (lane & 3);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                *reinterpret_cast<float2*>(to + 8 * j) = make_float2(d[4 * j], d[4 * j + 1]);
+                                *reinterpret_cast<float2*>(to + 8 * kStageRow + 8 * j) = make_float2(d[4 * j + 2], d[4 * j + 3]);
+                            }
+                        }
+                        if (u == 1) ptx::tc_fence_before();       // the accumulator is read
+                        __syncwarp();
+                        if (u == 1) ptx::mbar_arrive_elect(&tempty[buf]);
+#pragma unroll
+                        for (int t = kIt * u; t < kIt * (u + 1); ++t) {
+                            const int w = kAt * t + sub;
+                            if (w < here) {
+                                int64_t row;
+                                int head, whole;
+                                place(w, row, head, whole);
+                                const float* y0 = stage + (w - 16 * u) * kStageRow;
+                                const int64_t at = row * p.out_stride + o0;
+                                const int e = kBf16 ? 0 : -s_exp[32 * q + w];
+                                if (c < whole) {
+                                    float y[kV];
+#pragma unroll
+                                    for (int j = 0; j < kV; ++j) {
+                                        y[j] = y0[head + kV * c + j];
+                                        if constexpr (!kBf16) y[j] = times_exp2(y[j], e);
+                                    }
+                                    if (p.base) add_raw<kOut>(was[t], y);
+                                    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.out) + (at + head + kV * c) * kSize) = pack_raw<kOut>(y);
+                                }
+                                auto single = [&](int k, uint32_t base) {
+                                    float y = y0[k];
+                                    if constexpr (!kBf16) y = times_exp2(y, e);
+                                    store_one<kOut>(p.out, at + k, p.base ? of_bits<kOut>(base) + y : y);
+                                };
+                                const int rest = lim - kV * whole;
+                                if (c < rest) single(c < head ? c : kV * whole + c, one[t]);
+                                if (kV == 8 && c + kCh < rest) {         // (up to 14 at a row's end)
+                                    const int k = c + kCh < head ? c + kCh : kV * whole + c + kCh;
+                                    single(k, p.base ? load_bits<kOut>(p.base, row * p.base_stride + o0 + k) : 0u);
+                                }
+                            }
+                        }
+                        __syncwarp();                             // the staging is read
+                    }
+                }
+            };
             if (warp == kEpiWarps + 1) {
                 int sent = done_tiles;
                 for (int i = 0; i < nt; ++i, ++sent) {
@@ -555,50 +659,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                 if constexpr (kWide) {
                     epilogue();
                 } else {
-                    // Any rows: 64 of the 128 outputs in two passes of 32, through the warp's staging; neighbouring lanes
-                    // at neighbouring elements, all 32 rows' loads in flight while the products run (eight rows' at a
-                    // time, behind them: 110 us against 102 for 6000 rows of 3551 outputs).
-                    float* stage = reinterpret_cast<float*>(sStage + warp * kStageBytes);
-                    for (int i = 0; i < nt; ++i) {
-                        const int buf = (done_tiles + i) & 1;
-#pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
-                            const int o = (t0 + i) * kNT + half * 64 + h * 32 + lane;
-                            uint32_t was[32];
-#pragma unroll
-                            for (int w = 0; w < 32; ++w)
-                                was[w] = p.base && w < here && o < O ? load_bits<kOut>(p.base, (int64_t)s_rows[32 * q + w] * p.base_stride + o) : 0u;
-                            if (h == 0) {
-                                if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) break;
-                                ptx::tc_fence_after();
-                            }
-                            if (here > 0) {
-                                const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * kNT + half * 64 + h * 32;
-                                float d[16];
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    ptx::tmem_ld16(tb + 16 * u, d);
-#pragma unroll
-                                    for (int w = 0; w < 4; ++w)
-                                        *reinterpret_cast<float4*>(stage + lane * kStageRow + 16 * u + 4 * w) =
-                                            make_float4(d[4 * w], d[4 * w + 1], d[4 * w + 2], d[4 * w + 3]);
-                                }
-                            }
-                            if (h == 1) ptx::tc_fence_before();       // the accumulator is read
-                            __syncwarp();
-                            if (h == 1) ptx::mbar_arrive_elect(&tempty[buf]);
-#pragma unroll
-                            for (int w = 0; w < 32; ++w) {
-                                const int r = 32 * q + w;
-                                if (w < here && o < O) {
-                                    float v = stage[w * kStageRow + lane];
-                                    if constexpr (!kBf16) v = times_exp2(v, -s_exp[r]);
-                                    store_one<kOut>(p.out, (int64_t)s_rows[r] * p.out_stride + o, p.base ? of_bits<kOut>(was[w]) + v : v);
-                                }
-                            }
-                            __syncwarp();                             // the staging is read
-                        }
-                    }
+                    any_rows();
                 }
             }
             done_tiles += nt;
