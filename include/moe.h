@@ -475,7 +475,10 @@ typedef struct {
  *                   or NULL; one of out and out8 is given
  * Rows are *_stride >= H elements apart; every pointer is aligned to its
  * element.  Where all of them (and the strides) are multiples of 16 bytes (8 for
- * out8) and H of 8, rows are read and written 16 bytes at a time.
+ * out8) and H of 8, rows are read and written 16 bytes at a time.  Other rows
+ * are read by the aligned 16 bytes around their elements: bytes beside a row
+ * may be read with it (within the 16 that hold its first or last element),
+ * and are never written.
  * Outputs overlap nothing else, from their first row to their last.
  * h^2 may leave fp32's range: such a row is normalised all the same.  A row of
  * zeros with eps = 0 gives zeros.  An infinity in h makes NaN of itself and

@@ -9,13 +9,19 @@
 // instructions an element stay few: products and sums in pairs (f32x2), maxima only for 8-bit
 // outputs.
 //
-// Two kernels.  Rows of whole, aligned 16-byte chunks: a row belongs to T threads, each with
-// kCh chunks of eight consecutive elements, T chunks apart, all of whose loads are in flight
-// before the first is used; rows of at most 32 kCh chunks are one warp's, several of them to a
-// block and no barrier.  The scale of 128 elements is a maximum over 16 neighbouring lanes.
-// Any other rows: the same by single elements, neighbouring threads at neighbouring ones (eight
-// a thread, one after another, took 33.8 us for 3001 x 2047 that take 22.2 so).
+// A row belongs to T threads, each with kCh chunks of eight consecutive elements, T chunks apart, all of
+// whose loads are in flight before the first is used; rows of at most 32 kCh chunks are one warp's,
+// several of them to a block and no barrier.  The scale of 128 elements is a maximum over 16
+// neighbouring lanes.
+//
+// Rows that are not of whole chunks at addresses of whole chunks (kAny): a chunk is cut from the two
+// aligned 16 bytes (fp32: three) that it lies in, each of which holds a byte of the row; outputs go
+// through a warp's staging, from which lanes take the aligned 16 bytes (of codes 8) of the span of its
+// 32 chunks, and what is left before and behind them by elements.  A warp writes its own elements only,
+// so rows may still be overwritten in place.  (By single elements, neighbouring threads at
+// neighbouring ones: 22 us for 3001 x 2047 that take 17.5 so, 250 for 5000 x 7168 that take 76.)
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_launch.cuh"
 
@@ -77,30 +83,129 @@ template <int kType> __device__ __forceinline__ void store8(uint8_t* row, int at
     }
 }
 
+// ---------------------------------------------------------------- the same at any address
+
+// The 16 bytes from byte `at` (even) of two neighbouring ones, and the 8 bytes from any byte of 16.
+__device__ __forceinline__ uint4 cut16(const uint4& a, const uint4& b, int at) {
+    const uint32_t r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t s[7], t[5];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) s[i] = at & 4 ? r[i + 1] : r[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) t[i] = at & 8 ? s[i + 2] : s[i];
+    const int bits = 8 * (at & 3);
+    return make_uint4(__funnelshift_r(t[0], t[1], bits), __funnelshift_r(t[1], t[2], bits), __funnelshift_r(t[2], t[3], bits),
+                      __funnelshift_r(t[3], t[4], bits));
+}
+__device__ __forceinline__ uint2 cut8(const uint2& a, const uint2& b, int at) {
+    const uint32_t r0 = at & 4 ? a.y : a.x, r1 = at & 4 ? b.x : a.y, r2 = at & 4 ? b.y : b.x;
+    const int bits = 8 * (at & 3);
+    return make_uint2(__funnelshift_r(r0, r1, bits), __funnelshift_r(r1, r2, bits));
+}
+// The aligned 16 bytes that eight elements of a row lie in; zeros for those that hold nothing of the row.
+template <int kType> struct Around8 { uint4 v[kType == MOE_F32 ? 3 : 2]; };
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+template <int kType> __device__ __forceinline__ void load_around(Around8<kType>& r, const uint8_t* row, int at, int H) {
+    const uint8_t *a = row + (size_t)at * size_of(kType), *end = row + (size_t)H * size_of(kType);
+    const int off = (int)(reinterpret_cast<uintptr_t>(a) & 15);
+    a -= off;
+    constexpr int kN = size_of(kType) / 2;      // 16 bytes of eight elements
+#pragma unroll
+    for (int i = 0; i <= kN; ++i) r.v[i] = i == 0 || ((i < kN || off) && a + 16 * i < end) ? ld_v4(a + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+}
+template <int kType> __device__ __forceinline__ Raw8<kType> cut_around(const Around8<kType>& r, const uint8_t* row) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+    Raw8<kType> q;
+#pragma unroll
+    for (int i = 0; i < size_of(kType) / 2; ++i) q.v[i] = cut16(r.v[i], r.v[i + 1], off);
+    return q;
+}
+// What a warp's lanes have of `n` elements from `to` on, eight a lane, through its staging of 1 KB.
+// Of 16 bits ...
+__device__ __forceinline__ void put16(uint8_t* to, int n, const uint4& v, uint8_t* stage) {
+    const int lane = threadIdx.x & 31, off = (int)(reinterpret_cast<uintptr_t>(to) & 15);
+    if (off == 0 && n == 256) {
+        reinterpret_cast<uint4*>(to)[lane] = v;
+        return;
+    }
+    uint4* s = reinterpret_cast<uint4*>(stage);
+    s[lane] = v;
+    __syncwarp();
+    const int head = (16 - off & 15) / 2, whole = max(0, n - head) / 8;
+    if (lane < whole) *reinterpret_cast<uint4*>(to + 2 * head + 16 * lane) = cut16(s[lane], s[min(lane + 1, 31)], 2 * head);
+    if (lane < n - 8 * whole) {
+        const int e = lane < head ? lane : 8 * whole + lane;
+        reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(stage)[e];
+    }
+    __syncwarp();
+}
+// ... of 8 ...
+__device__ __forceinline__ void put8(uint8_t* to, int n, const uint2& v, uint8_t* stage) {
+    const int lane = threadIdx.x & 31, off = (int)(reinterpret_cast<uintptr_t>(to) & 7);
+    if (off == 0 && n == 256) {
+        reinterpret_cast<uint2*>(to)[lane] = v;
+        return;
+    }
+    uint2* s = reinterpret_cast<uint2*>(stage);
+    s[lane] = v;
+    __syncwarp();
+    const int head = 8 - off & 7, whole = max(0, n - head) / 8;
+    if (lane < whole) *reinterpret_cast<uint2*>(to + head + 8 * lane) = cut8(s[lane], s[min(lane + 1, 31)], head);
+    if (lane < n - 8 * whole) {
+        const int e = lane < head ? lane : 8 * whole + lane;
+        to[e] = stage[e];
+    }
+    __syncwarp();
+}
+// ... and of 32.
+__device__ __forceinline__ void put32(uint8_t* to, int n, const float2 (&f)[4], uint8_t* stage) {
+    const int lane = threadIdx.x & 31;
+    float4* s = reinterpret_cast<float4*>(stage) + 2 * lane;
+    s[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    s[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (32 * i + lane < n) reinterpret_cast<float*>(to)[32 * i + lane] = reinterpret_cast<const float*>(stage)[32 * i + lane];
+    __syncwarp();
+}
+template <int kType> __device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+    return make_uint4(pack2<kType>(f[0]), pack2<kType>(f[1]), pack2<kType>(f[2]), pack2<kType>(f[3]));
+}
+// Eight elements of which `n` are the row's: zeros for the others.
+__device__ __forceinline__ void first_of8(float2 (&f)[4], int n) {
+    if (n >= 8) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (2 * i >= n) f[i].x = 0.f;
+        if (2 * i + 1 >= n) f[i].y = 0.f;
+    }
+}
+
 // ---------------------------------------------------------------- rows
 
 // Sum and maximum over the T threads of a row (threadIdx.x), the same value in each.  One
-// warp's by shuffles; else by warp through red[32], added in warp order.
+// warp's by shuffles; more than one warp's through red, 32 words that nothing else uses.
 __device__ __forceinline__ float row_sum(float v, int T, float* red) {
     v = warp_sum(v);
     if (T == 32) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = red[0];
-    for (int i = 1; i < T / 32; ++i) s += red[i];
-    return s;
+    return warp_sum(lane < T / 32 ? red[lane] : 0.f);
 }
 __device__ __forceinline__ uint32_t row_max(uint32_t v, int T, float* red) {
     v = __reduce_max_sync(0xffffffffu, v);
     if (T == 32) return v;
     uint32_t* r = reinterpret_cast<uint32_t*>(red);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) r[threadIdx.x >> 5] = v;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
-    __syncthreads();
-    uint32_t m = r[0];
-    for (int i = 1; i < T / 32; ++i) m = max(m, r[i]);
-    return m;
+    return __reduce_max_sync(0xffffffffu, lane < T / 32 ? r[lane] : 0u);
 }
 
 // |v| as an integer of the same order, infinities and NaN above every finite value.
@@ -142,7 +247,7 @@ template <int N> __device__ __forceinline__ float row_rstd(float ss, float2 (&h)
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) m = max(m, max(abs_bits(h[i].x), abs_bits(h[i].y)));
-    m = max(row_max(m, T, red), __float_as_uint(sqrtf(p.eps)));
+    m = max(row_max(m, T, red + 32), __float_as_uint(sqrtf(p.eps)));
     if (m >= kInfBits) return 1.f / sqrtf(mean);   // as the formula: 0 beside an infinity, NaN
     if (m == 0) return 0.f;                        // zeros with eps = 0
     const float pre = exp2i(max(-max((int)(m >> 23) - 127, -126), -126));
@@ -152,24 +257,32 @@ template <int N> __device__ __forceinline__ float row_rstd(float ss, float2 (&h)
         h[i] = __fmul2_rn(h[i], both(pre));
         s2 += h[i].x * h[i].x + h[i].y * h[i].y;
     }
-    return 1.f / sqrtf(row_sum(s2, T, red) * inv_h + (p.eps * pre) * pre);
+    return 1.f / sqrtf(row_sum(s2, T, red + 64) * inv_h + (p.eps * pre) * pre);
 }
 
 // One row from what get(c, xr, rr) gives of chunk c of x and the residual, and weight16(c) of a 16-bit
 // weight.  in[c]: the thread has a chunk c.  live: the row is one (else it only takes part in the
-// reductions).
-template <int kX, int kR, int kCh, typename Get, typename Weight16>
-__device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool live, int T, const bool (&in)[kCh], float* red, Get get,
-                                         Weight16 weight16) {
+// reductions).  stage: kAny's, of the warp.
+template <int kX, int kR, int kCh, bool kAny, typename Get, typename Weight16, typename Weight32>
+__device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool live, int T, const bool (&in)[kCh], float* red, uint8_t* stage,
+                                         Get get, Weight16 weight16, Weight32 weight32) {
     constexpr int kRT = kR < 0 ? kX : kR;
     const int tid = threadIdx.x;
     const int64_t r0 = live ? row : 0;
     uint8_t* res_out = reinterpret_cast<uint8_t*>(p.res_out) + r0 * p.res_out_stride * size_of(kRT);
+
     const bool w16 = p.w && p.w_type != MOE_F32;
+    // kAny: where the warp's chunks c begin, and how many elements they have.
+    auto span = [&](int c) { return (c * T + (tid & ~31)) * 8; };
+    auto within = [&](int c) { return live ? min(256, p.H - span(c)) : 0; };
+    auto codes = [&](const float2* y, float2 inv) {
+        return make_uint2(e4m3x2(__fmul2_rn(y[0], inv)) | e4m3x2(__fmul2_rn(y[1], inv)) << 16, e4m3x2(__fmul2_rn(y[2], inv)) | e4m3x2(__fmul2_rn(y[3], inv)) << 16);
+    };
     float2 h[kCh * 4], ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < kCh; ++c) {
         float2(&hc)[4] = *reinterpret_cast<float2(*)[4]>(&h[4 * c]);
+        uint4 st = make_uint4(0u, 0u, 0u, 0u);
         if (in[c]) {
             Raw8<kX> xr;
             Raw8<kRT> rr;
@@ -181,18 +294,26 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) hc[i] = __fadd2_rn(hc[i], r[i]);
                 if constexpr (kR != MOE_F32) {   // the rows that are normalised are those that are stored
-                    const uint4 st = make_uint4(pack2<kRT>(hc[0]), pack2<kRT>(hc[1]), pack2<kRT>(hc[2]), pack2<kRT>(hc[3]));
-                    if (p.res_out) *reinterpret_cast<uint4*>(res_out + (size_t)(c * T + tid) * 16) = st;
+                    st = pack8<kRT>(hc);
+                    if (!kAny && p.res_out) *reinterpret_cast<uint4*>(res_out + (size_t)(c * T + tid) * 16) = st;
                     floats8<kRT>(Raw8<kRT>{{st}}, hc);
-                } else if (p.res_out) {
+                } else if (!kAny && p.res_out) {
                     store8<MOE_F32>(res_out, (c * T + tid) * 8, hc);
                 }
             }
+            if constexpr (kAny) first_of8(hc, p.H - (c * T + tid) * 8);
 #pragma unroll
             for (int i = 0; i < 4; ++i) ss = __ffma2_rn(hc[i], hc[i], ss);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) hc[i] = make_float2(0.f, 0.f);
+        }
+        if constexpr (kAny && kR >= 0) {
+            if (p.res_out && within(c) > 0) {
+                uint8_t* to = res_out + (size_t)span(c) * size_of(kRT);
+                if constexpr (kR == MOE_F32) put32(to, within(c), hc, stage);
+                else put16(to, within(c), st, stage);
+            }
         }
     }
     const float2 rstd = both(row_rstd(ss.x + ss.y, h, p, T, red));
@@ -209,10 +330,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
                 if (p.w_type == MOE_BF16) floats8<MOE_BF16>(Raw8<MOE_BF16>{{wr}}, w);
                 else floats8<MOE_F16>(Raw8<MOE_F16>{{wr}}, w);
             } else if (p.w) {
-                const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.w) + at);
-                const float4 a = __ldg(f), b = __ldg(f + 1);
-                w[0] = make_float2(a.x, a.y); w[1] = make_float2(a.z, a.w);
-                w[2] = make_float2(b.x, b.y); w[3] = make_float2(b.z, b.w);
+                floats8<MOE_F32>(weight32(c), w);
             } else {
                 w[0] = w[1] = w[2] = w[3] = both(1.f);
             }
@@ -222,12 +340,18 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(y[i], rstd), w[i]);
-            if (p.out) {
+            if constexpr (kAny) first_of8(y, p.H - at);
+            if (!kAny && p.out) {
                 uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + r0 * p.out_stride * size_of(p.out_type);
                 if (p.out_type == MOE_BF16) store8<MOE_BF16>(out, at, y);
                 else if (p.out_type == MOE_F16) store8<MOE_F16>(out, at, y);
                 else store8<MOE_F32>(out, at, y);
             }
+        }
+        if (kAny && p.out && within(c) > 0) {
+            uint8_t* to = reinterpret_cast<uint8_t*>(p.out) + (r0 * p.out_stride + span(c)) * size_of(p.out_type);
+            if (p.out_type == MOE_F32) put32(to, within(c), y, stage);
+            else put16(to, within(c), p.out_type == MOE_BF16 ? pack8<MOE_BF16>(y) : pack8<MOE_F16>(y), stage);
         }
         if (p.out8) {
             float m = 0.f;
@@ -238,11 +362,12 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
 #pragma unroll
                 for (int o = 1; o < 16; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
                 const float s = scale_of(most);
-                if (in[c]) {
-                    if ((tid & 15) == 0) p.scale8[row * p.n_scales + at / 128] = s;
-                    const float2 inv = both(reciprocal(s));
-                    *reinterpret_cast<uint2*>(p.out8 + r0 * p.out8_stride + at) =
-                        make_uint2(e4m3x2(__fmul2_rn(y[0], inv)) | e4m3x2(__fmul2_rn(y[1], inv)) << 16, e4m3x2(__fmul2_rn(y[2], inv)) | e4m3x2(__fmul2_rn(y[3], inv)) << 16);
+                if (in[c] && (tid & 15) == 0) p.scale8[row * p.n_scales + at / 128] = s;
+                const uint2 q = codes(y, both(reciprocal(s)));
+                if constexpr (kAny) {
+                    if (within(c) > 0) put8(p.out8 + r0 * p.out8_stride + span(c), within(c), q, stage);
+                } else if (in[c]) {
+                    *reinterpret_cast<uint2*>(p.out8 + r0 * p.out8_stride + at) = q;
                 }
             } else {
                 top = max(top, most);
@@ -250,26 +375,30 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
         }
     }
     if (p.out8 && !p.group) {
-        const float s = scale_of(row_max(top, T, red));
+        const float s = scale_of(row_max(top, T, red + 96));
         const float2 inv = both(reciprocal(s));
         if (tid == 0 && live) p.scale8[row] = s;
 #pragma unroll
         for (int c = 0; c < kCh; ++c) {
-            const float2* y = &h[4 * c];
-            if (in[c])
-                *reinterpret_cast<uint2*>(p.out8 + r0 * p.out8_stride + (c * T + tid) * 8) =
-                    make_uint2(e4m3x2(__fmul2_rn(y[0], inv)) | e4m3x2(__fmul2_rn(y[1], inv)) << 16, e4m3x2(__fmul2_rn(y[2], inv)) | e4m3x2(__fmul2_rn(y[3], inv)) << 16);
+            const uint2 q = codes(&h[4 * c], inv);
+            if constexpr (kAny) {
+                if (within(c) > 0) put8(p.out8 + r0 * p.out8_stride + span(c), within(c), q, stage);
+            } else if (in[c]) {
+                *reinterpret_cast<uint2*>(p.out8 + r0 * p.out8_stride + (c * T + tid) * 8) = q;
+            }
         }
     }
 }
 
-// kX: type of x.  kR: type of the residual, or -1 for none.  Rows of whole aligned chunks.  kWide:
-// rows so long that their threads have no registers for loads in flight.
-template <int kX, int kR, int kCh, bool kWide>
+// kX: type of x.  kR: type of the residual, or -1 for none.  kWide: rows so long that their threads have
+// no registers for loads in flight.
+template <int kX, int kR, int kCh, bool kWide, bool kAny>
 __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads, kWide || kR == MOE_F32 ? 1 : 2) norm_kernel(const NormParams p) {
-    __shared__ float red[32];
+    __shared__ float red[4 * 32];
+    __shared__ __align__(16) uint8_t staging[kAny ? (kWide ? kWideThreads : kThreads) * 32 : 16];
     constexpr int kRT = kR < 0 ? kX : kR;
     const int T = blockDim.x, tid = threadIdx.x;
+    uint8_t* stage = staging + (kAny ? (threadIdx.y * T + tid) / 32 * 1024 : 0);
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = row < p.n;   // (whole warps: T > 32 means one row a block)
     const int64_t r0 = live ? row : 0;
@@ -282,172 +411,70 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads, kWide || kR =
     pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
 
     // Every load of the row before the first use; of a thread's only chunk the weight's too.
-    Raw8<kX> xr[kCh];
-    Raw8<kRT> rr[kR < 0 ? 1 : kCh];
+    using RawX = std::conditional_t<kAny, Around8<kX>, Raw8<kX>>;
+    using RawR = std::conditional_t<kAny, Around8<kRT>, Raw8<kRT>>;
+    auto load = [&](int c, RawX& a, RawR& b) {
+        const int at = (c * T + tid) * 8;
+        if constexpr (kAny) {
+            load_around<kX>(a, x, at, p.H);
+            if constexpr (kR >= 0) load_around<kRT>(b, res, at, p.H);
+        } else {
+            load8<kX>(a, x, at);
+            if constexpr (kR >= 0) load8<kRT>(b, res, at);
+        }
+    };
+    RawX xr[kCh];
+    RawR rr[kR < 0 ? 1 : kCh];
+    const uint8_t* w = reinterpret_cast<const uint8_t*>(p.w);
+    auto load_w16 = [&](int c) {
+        if constexpr (kAny) {
+            Around8<MOE_BF16> r;
+            load_around<MOE_BF16>(r, w, (c * T + tid) * 8, p.H);
+            return cut_around<MOE_BF16>(r, w).v[0];
+        } else {
+            return __ldg(reinterpret_cast<const uint4*>(w) + (c * T + tid));
+        }
+    };
+    auto load_w32 = [&](int c) {
+        Raw8<MOE_F32> r;
+        if constexpr (kAny) {
+            Around8<MOE_F32> a;
+            load_around<MOE_F32>(a, w, (c * T + tid) * 8, p.H);
+            r = cut_around<MOE_F32>(a, w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) r.v[i] = __ldg(reinterpret_cast<const uint4*>(w) + 2 * (c * T + tid) + i);
+        }
+        return r;
+    };
     uint4 wr = make_uint4(0u, 0u, 0u, 0u);
-    auto load_w16 = [&](int c) { return __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.w) + (c * T + tid) * 8)); };
     if constexpr (!kWide) {
 #pragma unroll
         for (int c = 0; c < kCh; ++c)
-            if (in[c]) {
-                load8<kX>(xr[c], x, (c * T + tid) * 8);
-                if constexpr (kR >= 0) load8<kRT>(rr[c], res, (c * T + tid) * 8);
-            }
+            if (in[c]) load(c, xr[c], rr[kR < 0 ? 0 : c]);
         if (kCh == 1 && in[0] && p.w && p.w_type != MOE_F32) wr = load_w16(0);
     }
-    norm_row<kX, kR, kCh>(
-        p, row, live, T, in, red,
+    norm_row<kX, kR, kCh, kAny>(
+        p, row, live, T, in, red, stage,
         [&](int c, Raw8<kX>& a, Raw8<kRT>& b) {
-            if constexpr (kWide) {
-                load8<kX>(a, x, (c * T + tid) * 8);
-                if constexpr (kR >= 0) load8<kRT>(b, res, (c * T + tid) * 8);
+            if constexpr (kWide) load(c, xr[0], rr[0]);
+            const int i = kWide ? 0 : c;
+            if constexpr (kAny) {
+                a = cut_around<kX>(xr[i], x);
+                if constexpr (kR >= 0) b = cut_around<kRT>(rr[i], res);
             } else {
-                a = xr[c];
-                if constexpr (kR >= 0) b = rr[c];
+                a = xr[i];
+                if constexpr (kR >= 0) b = rr[i];
             }
         },
-        [&](int c) { return kCh == 1 ? wr : load_w16(c); });
-}
-
-// ---------------------------------------------------------------- rows of any alignment
-
-template <int kType> __device__ __forceinline__ float load1(const void* row, int at) {
-    if constexpr (kType == MOE_F32) return reinterpret_cast<const float*>(row)[at];
-    const uint16_t u = reinterpret_cast<const uint16_t*>(row)[at];
-    return unpack2<kType>(u).x;
-}
-// Elements i T + tid of the weight (1 without one), plus its offset.
-template <int kType, int kE> __device__ __forceinline__ void load_weight(const NormParams& p, int T, float (&w)[kE]) {
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-        const int at = i * T + (int)threadIdx.x;
-        if constexpr (kType == MOE_F32) {
-            w[i] = at < p.H ? __ldg(reinterpret_cast<const float*>(p.w) + at) : 0.f;
-        } else {
-            const uint16_t u = at < p.H ? __ldg(reinterpret_cast<const uint16_t*>(p.w) + at) : (uint16_t)0;
-            w[i] = unpack2<kType>(u).x;
-        }
-    }
-}
-template <int kE> __device__ __forceinline__ void load_weight_as(const NormParams& p, int T, float (&w)[kE]) {
-    if (!p.w) {
-#pragma unroll
-        for (int i = 0; i < kE; ++i) w[i] = 1.f;
-    } else if (p.w_type == MOE_F32) load_weight<MOE_F32>(p, T, w);
-    else if (p.w_type == MOE_BF16) load_weight<MOE_BF16>(p, T, w);
-    else load_weight<MOE_F16>(p, T, w);
-#pragma unroll
-    for (int i = 0; i < kE; ++i) w[i] += p.w_offset;
-}
-template <int kType> __device__ __forceinline__ void store1(void* row, int at, float v) {
-    if constexpr (kType == MOE_F32) reinterpret_cast<float*>(row)[at] = v;
-    else reinterpret_cast<uint16_t*>(row)[at] = (uint16_t)pack2<kType>(make_float2(v, 0.f));
-}
-__device__ __forceinline__ void store1_as(int type, void* row, int at, float v) {
-    if (type == MOE_F32) store1<MOE_F32>(row, at, v);
-    else if (type == MOE_BF16) store1<MOE_BF16>(row, at, v);
-    else store1<MOE_F16>(row, at, v);
-}
-
-// A row a block, element i T + tid the thread's i-th of kE (T a multiple of 128: the scale of 128
-// elements is a maximum over four warps).
-template <int kX, int kR, int kE, int kMost>
-__global__ void __launch_bounds__(kMost) norm_any_kernel(const NormParams p) {
-    __shared__ float red[32];
-    __shared__ __align__(16) uint32_t tops[kE * (kMost / 32)];
-    constexpr int kRT = kR < 0 ? kX : kR;
-    const int T = blockDim.x, tid = threadIdx.x, H = p.H;
-    const int64_t row = blockIdx.x;
-    const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x) + row * p.x_stride * size_of(kX);
-    const uint8_t* res = reinterpret_cast<const uint8_t*>(p.res) + row * p.res_stride * size_of(kRT);
-    uint8_t* res_out = reinterpret_cast<uint8_t*>(p.res_out) + row * p.res_out_stride * size_of(kRT);
-    pdl_wait();
-    pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
-    float2 h[kE / 2];
-    float rv[kR < 0 ? 1 : kE];
-    auto each = [&](int i) -> float& { return i & 1 ? h[i / 2].y : h[i / 2].x; };
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-        const int at = i * T + tid;
-        each(i) = at < H ? load1<kX>(x, at) : 0.f;
-        if constexpr (kR >= 0) rv[i] = at < H ? load1<kRT>(res, at) : 0.f;
-    }
-    // The weight before the first store, behind which its loads would wait one by one.
-    float w[kE];
-    constexpr bool kEarly = kE < 32;
-    if (kEarly) load_weight_as(p, T, w);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-        float& v = each(i);
-        if constexpr (kR >= 0) {
-            v += rv[i];
-            if constexpr (kR != MOE_F32) v = unpack2<kRT>(pack2<kRT>(make_float2(v, 0.f))).x;
-            if (p.res_out && i * T + tid < H) store1<kRT>(res_out, i * T + tid, v);
-        }
-        ss = fmaf(v, v, ss);
-    }
-    const float rstd = row_rstd(ss, h, p, T, red);
-    if (!kEarly) load_weight_as(p, T, w);
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-        const int at = i * T + tid;
-        float& y = each(i);
-        if (at < H) {
-            y = (y * rstd) * w[i];
-            if (p.out) store1_as(p.out_type, reinterpret_cast<uint8_t*>(p.out) + row * p.out_stride * size_of(p.out_type), at, y);
-        }
-        if (p.out8) {
-            const uint32_t m = at < H ? abs_bits(y) : 0u;
-            if (p.group) {
-                const uint32_t most = __reduce_max_sync(0xffffffffu, m);
-                if ((tid & 31) == 0) tops[i * (T / 32) + tid / 32] = most;
-            } else {
-                top = max(top, m);
-            }
-        }
-    }
-    if (p.out8) {
-        float s = 0.f;
-        if (p.group) {
-            __syncthreads();
-        } else {
-            s = scale_of(row_max(top, T, red));
-            if (tid == 0) p.scale8[row] = s;
-        }
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-            const int at = i * T + tid;
-            if (at >= H) break;
-            if (p.group) {
-                const uint4 m = *reinterpret_cast<const uint4*>(&tops[i * (T / 32) + tid / 128 * 4]);
-                s = scale_of(max(max(m.x, m.y), max(m.z, m.w)));
-                if (tid % 128 == 0) p.scale8[row * p.n_scales + at / 128] = s;
-            }
-            p.out8[row * p.out8_stride + at] = (uint8_t)e4m3x2(make_float2(each(i) * reciprocal(s), 0.f));
-        }
-    }
+        [&](int c) { return kCh == 1 ? wr : load_w16(c); }, load_w32);
 }
 
 // ---------------------------------------------------------------- launches
 
 template <int kX, int kR>
 cudaError_t launch_types(const NormParams& p, bool chunks, int num_sms, cudaStream_t st) {
-    if (!chunks) {
-        auto go = [&](auto kern, int e) {
-            launch_pdl(kern, dim3((unsigned)p.n), dim3(((p.H + e - 1) / e + 127) / 128 * 128), 0, st, p);
-            return cudaGetLastError();
-        };
-        // Elements of a thread: four while the rows' threads all run at once, else eight, as many
-        // as long rows ask for (2047 elements: 152 rows 3.4 us with 4, 4.1 with 8; 4000 rows 38.7 and 35.2).
-        const int few = (p.H + 3) / 4;
-        if (few <= kThreads && (int64_t)p.n * few <= (int64_t)num_sms * 2048) return go(norm_any_kernel<kX, kR, 4, kThreads>, 4);
-        if (p.H <= 8 * kThreads) return go(norm_any_kernel<kX, kR, 8, kThreads>, 8);
-        if (p.H <= 16 * kThreads) return go(norm_any_kernel<kX, kR, 16, kThreads>, 16);
-        return go(norm_any_kernel<kX, kR, 32, kWideThreads>, 32);
-    }
-    const int n8 = p.H / 8;
+    const int n8 = (p.H + 7) / 8;
     auto threads = [&](int ch) { return ((n8 + ch - 1) / ch + 31) / 32 * 32; };
     auto go = [&](auto kern, int ch) {
         const int T = threads(ch), rows = T == 32 ? std::min(p.n, 8) : 1;
@@ -455,15 +482,23 @@ cudaError_t launch_types(const NormParams& p, bool chunks, int num_sms, cudaStre
         return cudaGetLastError();
     };
     // Chunks of a thread: one while the rows' threads all run at once, else as many as its registers
-    // hold (two of two fp32 rows).
+    // hold (two of two fp32 rows, and where each comes with its neighbours, but without a residual four: 8000 rows
+    // of 1001 11.6 us against 13.9 with two).
     constexpr int kMost = kX == MOE_F32 && kR == MOE_F32 ? 2 : 4;
+    constexpr int kMostAny = kR < 0 && kX != MOE_F32 ? 4 : 2;
+    const int most = chunks ? kMost : kMostAny;
     int ch = 1;
     while (threads(ch) > kThreads) ch *= 2;
-    while (ch < kMost && (int64_t)p.n * threads(ch) > (int64_t)num_sms * 2048) ch *= 2;
-    if (ch > kMost) return go(norm_kernel<kX, kR, 4, true>, 4);
-    if (ch == 1) return go(norm_kernel<kX, kR, 1, false>, 1);
-    if (ch == 2) return go(norm_kernel<kX, kR, 2, false>, 2);
-    if constexpr (kMost == 4) return go(norm_kernel<kX, kR, 4, false>, 4);
+    while (ch < most && (int64_t)p.n * threads(ch) > (int64_t)num_sms * 2048) ch *= 2;
+    if (!chunks) {
+        if (ch > most) return go(norm_kernel<kX, kR, 4, true, true>, 4);
+        if constexpr (kMostAny == 4) if (ch == 4) return go(norm_kernel<kX, kR, 4, false, true>, 4);
+        return ch == 1 ? go(norm_kernel<kX, kR, 1, false, true>, 1) : go(norm_kernel<kX, kR, 2, false, true>, 2);
+    }
+    if (ch > most) return go(norm_kernel<kX, kR, 4, true, false>, 4);
+    if (ch == 1) return go(norm_kernel<kX, kR, 1, false, false>, 1);
+    if (ch == 2) return go(norm_kernel<kX, kR, 2, false, false>, 2);
+    if constexpr (kMost == 4) return go(norm_kernel<kX, kR, 4, false, false>, 4);
     return cudaErrorInvalidValue;
 }
 

@@ -217,6 +217,40 @@ def test_strides_and_offsets(lib, pad, at):
 
 
 @gpu
+@pytest.mark.parametrize("r", [None, BF, F32])
+@pytest.mark.parametrize("out", [HF, F32])
+@pytest.mark.parametrize("H,W,n", [(1, 3, 40), (5, 9, 7), (40, 43, 300), (264, 267, 9), (1001, 1003, 1300), (2040, 2055, 5), (4097, 4099, 1), (8203, 8205, 3)])
+def test_every_alignment(lib, H, W, n, out, r):
+    """Rows of an odd stride begin at every address there is; NaN beside x, residual and weight stays there, what is
+    beside the outputs stays as it was."""
+    def inside(t, fill, dtype, at):
+        b = torch.full((n + 2, W), fill, device="cuda").to(dtype)
+        v = b[1:n + 1, at:at + H]
+        if t is not None:
+            v.copy_(t)
+        return b, v
+
+    nan = float("nan")
+    w = torch.full((H + 8,), nan, device="cuda", dtype=BF)
+    w[3:3 + H] = weights(H)
+    for out8 in ("group", "row"):
+        op = MoeNorm(w[3:3 + H], out_dtype=out, out8=out8)
+        x = inside(rows(n, H), nan, BF, 1)[1]
+        rb, res = inside(rows(n, H, r, seed=2), nan, r, 2) if r else (None, None)
+        ob, y = inside(None, 7.0, out, W - H)
+        qb, q = inside(None, 7.0, torch.float8_e4m3fn, 0)
+        was = None if res is None else res.clone()
+        got = op.forward(x, res, residual_out=res, out=y, out8=q)
+        check(op, x, was, tuple(g if g is None else g.contiguous() for g in got))
+        y.fill_(7.0)
+        q.copy_(torch.full((n, H), 7.0, device="cuda").to(q.dtype))
+        assert bool((ob == 7).all()) and bool((qb.float() == 7).all())
+        if res is not None:
+            res.fill_(nan)
+            assert bool(rb.isnan().all())
+
+
+@gpu
 @pytest.mark.parametrize("H", [100, 2048, 7168])
 def test_in_place(lib, H):
     op = MoeNorm(weights(H))
