@@ -228,6 +228,7 @@ struct LoraParams {
     // Set by launch_lora.
     int vec;                   // elements of base's and out's rows that can be read at once: 8, 4 or 1
     bool copy;                 // rows without an adapter are to be written
+    int groups;                // few rows: clusters that are launched, or 0 for one a row
     // The rows sorted by adapter, or null: runs (adapter, or -1 for none; first position; rows), the
     // runs of adapters before those of none.  ctrl->n_active runs of adapters, n_rsegs in all.
     const int32_t *segs, *perm;

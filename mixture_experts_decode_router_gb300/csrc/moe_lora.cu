@@ -22,8 +22,9 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRows = 8;           // rows of a cluster (the n of the products)
-constexpr int kScanRows = 512;     // rows whose adapters a cluster goes through for itself, at most
+constexpr int kRows = 8;            // rows of a cluster (the n of the products)
+constexpr int kScanRows = 512;      // rows whose adapters a cluster goes through for itself, at most
+constexpr int kGroupAdapters = 255; // adapters whose rows it counts, where fewer clusters than rows are launched
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -67,10 +68,80 @@ __device__ __forceinline__ void copy_row(const LoraParams& p, int64_t row, int p
     }
 }
 
+// Which rows are cluster `group`'s, where fewer clusters than rows are launched: that many groups of kRows of an
+// adapter lie before it.  Row tid + kThreads h's rank among its adapter's rows: those before it in its 32 rows, and
+// the counts of the 32s before, a byte each, 16 an adapter (table: (L + 1) times 16 bytes, the last one's of rows
+// without an adapter).  Of these the cluster copies those of rank `group` and every p.groups-th from there.
+struct Found {
+    int adapter, count, copies;      // count 0: no group is left
+};
+__device__ __forceinline__ Found find_rows(const LoraParams& p, int group, uint8_t* table, int (&s_rows)[kWarps][kRows], int* s_copy) {
+    constexpr int kH = kScanRows / kThreads;
+    __shared__ int s_lead[kScanRows / 32], s_found[3];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i <= p.L; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < 3) s_found[tid] = 0;
+    int e[kH], rank[kH], total[kH];
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+        const int row = tid + h * kThreads;
+        e[h] = row < p.n ? p.idx[row] : -2;
+        if (row < p.n && (e[h] < 0 || e[h] >= p.L)) e[h] = p.L;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+        const uint32_t peers = __match_any_sync(0xffffffffu, e[h]);
+        rank[h] = __popc(peers & ((1u << lane) - 1));
+        if (rank[h] == 0 && e[h] >= 0) table[e[h] * 16 + warp + h * kWarps] = (uint8_t)__popc(peers);
+    }
+    __syncthreads();
+    uint32_t leads[kH];
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+        const uint4 q = reinterpret_cast<const uint4*>(table)[max(e[h], 0)];
+        const uint32_t c[4] = {q.x, q.y, q.z, q.w};
+        const int b = warp + h * kWarps;
+        total[h] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int here = min(max(b - 4 * i, 0), 4);      // bytes of this word that count
+            total[h] = __dp4a(c[i], 0x01010101u, (uint32_t)total[h]);
+            rank[h] = __dp4a(c[i], here == 4 ? 0x01010101u : 0x01010101u & ((1u << 8 * here) - 1), (uint32_t)rank[h]);
+        }
+        leads[h] = __ballot_sync(0xffffffffu, e[h] >= 0 && e[h] < p.L && rank[h] % kRows == 0);
+        if (lane == 0) s_lead[b] = __popc(leads[h]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+        const int b = warp + h * kWarps;
+        int before = 0;
+        for (int i = 0; i < b; ++i) before += s_lead[i];
+        if ((leads[h] >> lane & 1) && before + __popc(leads[h] & ((1u << lane) - 1)) == group) {
+            s_found[0] = e[h];
+            s_found[1] = rank[h];
+            s_found[2] = min(kRows, total[h] - rank[h]);
+        }
+        if (e[h] == p.L && rank[h] % p.groups == group) s_copy[rank[h] / p.groups] = tid + h * kThreads;
+    }
+    __syncthreads();
+    const uint4 q = reinterpret_cast<const uint4*>(table)[p.L];
+    const int none = __dp4a(q.x, 0x01010101u, __dp4a(q.y, 0x01010101u, __dp4a(q.z, 0x01010101u, __dp4a(q.w, 0x01010101u, 0u))));
+    const Found f{s_found[0], s_found[2], p.copy && none > group ? (none - group - 1) / p.groups + 1 : 0};
+#pragma unroll
+    for (int h = 0; h < kH; ++h)
+        if (f.count && e[h] == f.adapter && rank[h] / kRows == s_found[1] / kRows)
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s_rows[w][rank[h] % kRows] = tid + h * kThreads;
+    __syncthreads();
+    return f;
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
 
-// kRT: tiles of 16 of the rank.  kParts: parts of v.
-template <bool kBf16, int kRT, int kParts>
+// kRT: tiles of 16 of the rank.  kParts: parts of v.  kGroups: fewer clusters than rows (find_rows).
+template <bool kBf16, int kRT, int kParts, bool kGroups>
 __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p) {
     constexpr int kR = kRT * 16;
     constexpr int kPad = kRT == 1 ? 0 : 16;       // (no bank conflicts between rows of parts)
@@ -78,6 +149,7 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     __shared__ float s_mine[kR * kRows];
     __shared__ int s_rows[kWarps][kRows];         // (every warp finds them for itself)
     __shared__ uint32_t s_top[kRows];
+    __shared__ int s_copy[kGroups ? kRows + 1 : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int C = (int)cluster_size(), c = (int)cluster_rank(), group = blockIdx.x / C;
     if (tid < kRows) s_top[tid] = 0;
@@ -85,9 +157,20 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
 
     // The cluster's rows: row `group`, if an adapter's rows before it fill whole clusters, and
-    // the next ones of its adapter; or a run of the rows sorted by adapter.
+    // the next ones of its adapter; kGroups: the group-th of these; or a run of the rows sorted by adapter.
     int adapter, count;
-    if (p.segs) {
+    [[maybe_unused]] int copies = 0;
+    if constexpr (kGroups) {
+        static_assert(sizeof(s_part) >= (kGroupAdapters + 1) * 16, "the counts fit");
+        const Found f = find_rows(p, group, reinterpret_cast<uint8_t*>(&s_part[0][0][0]), s_rows, s_copy);
+        adapter = f.adapter;
+        count = f.count;
+        copies = f.copies;
+        if (!count) {
+            for (int i = 0; i < copies; ++i) copy_row(p, s_copy[i], c, C);
+            return;
+        }
+    } else if (p.segs) {
         if (group >= p.ctrl->n_rsegs) return;
         const int first = p.segs[3 * group + 1];
         adapter = p.segs[3 * group];
@@ -216,6 +299,8 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     constexpr bool kEarly = kRT < 8;
     if (kEarly) fetch(c * uper + warp);
     cluster_arrive();
+    if constexpr (kGroups)
+        for (int i = 0; i < copies; ++i) copy_row(p, s_copy[i], c, C);
     cluster_wait();
     // Each element of v is summed over the blocks in their order, and split, by one thread.
     constexpr int kMine = (kR * kRows + kThreads - 1) / kThreads;
@@ -407,9 +492,9 @@ lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_
     }
 }
 
-template <bool kBf16, int kRT, int kParts>
-cudaError_t launch_rows(const LoraParams& p, int groups, int cluster, cudaStream_t st) {
-    auto kern = lora_rows_kernel<kBf16, kRT, kParts>;
+template <bool kBf16, int kRT, int kParts, bool kGroups>
+cudaError_t launch_clusters(const LoraParams& p, int groups, int cluster, cudaStream_t st) {
+    auto kern = lora_rows_kernel<kBf16, kRT, kParts, kGroups>;
     if (cluster > 8) {   // (more than every GPU has to offer: to be asked for)
         static std::mutex mu;
         static bool configured[128] = {};
@@ -437,6 +522,12 @@ cudaError_t launch_rows(const LoraParams& p, int groups, int cluster, cudaStream
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <bool kBf16, int kRT, int kParts>
+cudaError_t launch_rows(const LoraParams& p, int groups, int cluster, cudaStream_t st) {
+    return p.groups ? launch_clusters<kBf16, kRT, kParts, true>(p, groups, cluster, st)
+                    : launch_clusters<kBf16, kRT, kParts, false>(p, groups, cluster, st);
+}
+
 template <bool kBf16, int kParts>
 cudaError_t launch_rank(const LoraParams& p, int groups, int cluster, cudaStream_t st) {
     if (p.r <= 16) return launch_rows<kBf16, 1, kParts>(p, groups, cluster, st);
@@ -454,10 +545,22 @@ cudaError_t launch_all(const LoraParams& p, int x_type, int groups, int cluster,
 // Bytes of an adapter's matrices.
 int64_t adapter_bytes(int K, int O, int r) { return (int64_t)r * ((int64_t)K + O) * 2; }
 
-// Rows that the clusters take as they come, each going through all of them for its own; more are
-// sorted first.  (500 rows: 131 KB an adapter 12.5 us against 20.9 sorted, 64 adapters of 459 KB
-// 26.5 against 43.8, 8 of 1.8 MB 45.7 against 30.6.)
-bool by_scan(int64_t n, int K, int O, int r) { return n <= 256 || (n <= kScanRows && adapter_bytes(K, O, r) < 1 << 20); }
+// Rows that the clusters take as they come, each going through all of them for its own; more are sorted first.
+// (500 rows, us so and sorted: 131 KB an adapter 12.5 and 20.9, 64 adapters of 459 KB 26.5 and 43.8; of rank 64,
+// 4 of 1.8 MB 27.5 and 33.6, 8 of 1 MB 18.1 and 25.4, 20 of 1.8 MB 35.3 and 31.3; 400 rows, 16 of rank 128 45 and 30.)
+bool by_scan(int64_t n, int L, int K, int O, int r) {
+    return n <= 256 || (n <= kScanRows && (adapter_bytes(K, O, r) < 1 << 20 || (L <= 8 && r <= 64)));
+}
+
+// The groups of kRows that L adapters' rows make at most, where so few clusters are launched; 0: one a row.  A
+// cluster then costs the ranking of all rows, and saves the launches of those whose row another one takes.  (us a
+// row each and so: 64 rows, 8 adapters of 131 KB 5.9 and 5.6; 30 rows, 3 of 2 MB 12.6 and 11.5; 200 rows, 20 of
+// 1.1 MB 23.7 and 15.6; 500 rows, 8 of 262 KB 16.0 and 10.2; 8 rows of one adapter 4.1 and 4.9; 256 rows, 100 of
+// 440 KB, 119 groups, 17.1 and 17.6.)
+int group_count(int n, int L) {
+    const int most = (n + 7 * std::min(n, L)) / 8;
+    return n > 16 && L <= kGroupAdapters && most <= n * 7 / 16 ? most : 0;
+}
 
 // Blocks of a cluster.  More share an adapter's bytes among them; but most rows' clusters find that
 // another one has them, and all of them are launched.  (us with 4, 8 and 16 blocks: one row, 131 KB an
@@ -470,6 +573,17 @@ int cluster_blocks(int n, int64_t bytes) {
     return n > 384 && bytes < kSmall ? 2 : 4;
 }
 
+// The same where groups are launched, most of which have rows.  (us with 2, 4, 8 and 16 blocks: 6 groups of 2 MB 32,
+// 20, 12.7, 11.5; 15 of 131 KB 7.7, 6.0, 5.6, 6.3; 15 of 1.1 MB 16.8, 11.0, 8.9, 10.6; 42 of 448 KB, rank 16, 21, 13.3, 11.9,
+// 13.5; 40 of 1 MB, rank 64, 21.6, 16.5, 20.0, 32; 80 of 1.8 MB 48, 35, 50, 81; 118 of 131 KB 10.8, 11.4, 16.2, 27.6;
+// 143 of 378 KB 19.8, 25.5, 37, 82.)
+int group_blocks(int groups, int64_t bytes, int r) {
+    const bool large = bytes >= 256 << 10;
+    if (large && groups * 16 <= 152) return 16;
+    if (groups * 8 <= (large && r <= 32 ? 400 : 240)) return 8;
+    return groups <= 100 ? 4 : 2;
+}
+
 struct Layout {
     size_t perm, segs, part, total;
 };
@@ -477,7 +591,7 @@ Layout layout(int64_t n, int L, int K, int O, int r) {
     Layout l{};
     size_t off = sizeof(Ctrl);
     auto take = [&](size_t bytes) { const size_t o = off; off = align_up(off + bytes, 256); return o; };
-    if (!by_scan(n, K, O, r)) {
+    if (!by_scan(n, L, K, O, r)) {
         l.perm = take(sizeof(int32_t) * n);
         l.segs = take(sizeof(int32_t) * 3 * (n / kRows + std::min<int64_t>(n, L + 1) + 1));
         l.part = take(sizeof(float) * lora_part_rows(n) * r);
@@ -519,8 +633,11 @@ cudaError_t launch_lora(const LoraParams& given, int x_type, void* ws, int num_s
         if (rows_of(v, p.out, p.out_stride) && rows_of(v, p.base, p.base_stride)) p.vec = v;
     p.copy = p.base != p.out;
     cudaError_t e;
-    if (by_scan(p.n, p.K, p.O, p.r)) {
-        e = launch_all(p, x_type, p.n, cluster_blocks(p.n, adapter_bytes(p.K, p.O, p.r)), st);
+    if (by_scan(p.n, p.L, p.K, p.O, p.r)) {
+        const int64_t bytes = adapter_bytes(p.K, p.O, p.r);
+        p.groups = group_count(p.n, p.L);
+        e = p.groups ? launch_all(p, x_type, p.groups, group_blocks(p.groups, bytes, p.r), st)
+                     : launch_all(p, x_type, p.n, cluster_blocks(p.n, bytes), st);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
     const Layout l = layout(p.n, p.L, p.K, p.O, p.r);

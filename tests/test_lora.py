@@ -214,6 +214,36 @@ def test_runs_that_end_inside_a_tile(lib, y, O, rest):
 
 
 @gpu
+@pytest.mark.parametrize("n", [17, 32, 33, 200, 257, 500, 511, 512])
+@pytest.mark.parametrize("L", [1, 7, 219])
+@pytest.mark.parametrize("how", ["one", "none", "skewed", "blocks", "few"])
+def test_how_rows_share_adapters(lib, n, L, how):
+    """Rows of one adapter, of none, most of one, runs of eight and nine, and a few rows between many without."""
+    a, b, s = adapters(L, 16, 96, 131)
+    g, t = torch.Generator(device="cuda").manual_seed(n + L), torch.arange(n, device="cuda")
+    idx = torch.randint(0, L, (n,), generator=g, device="cuda")
+    some = torch.rand(n, generator=g, device="cuda")
+    if how == "one":
+        idx = torch.full_like(idx, L - 1)
+    elif how == "none":
+        idx = torch.where(t % 2 == 0, -1, L)
+    elif how == "skewed":
+        idx = torch.where(some < 0.8, L // 2, idx)
+    elif how == "blocks":
+        idx = t // torch.where(t < n // 2, 8, 9) % (L + 1)
+    else:
+        idx = torch.where(some < 0.9, 1 << 20, idx)
+    idx, x = idx.to(torch.int32), rows(n, 96)
+    op = MoeLora(a, b, s)
+    base = rows(n, 131, seed=8)
+    check(op, x, idx, base, op.forward(x, idx, base))
+    check(op, x, idx, None, op.forward(x, idx))
+    out = base.clone()
+    op.forward(x, idx, out, out=out)
+    check(op, x, idx, base, out)
+
+
+@gpu
 @pytest.mark.parametrize("n", [5, 300, 900])
 def test_indexes_outside(lib, n):
     """-1, the number of adapters, and the ends of int32 are no adapter."""
