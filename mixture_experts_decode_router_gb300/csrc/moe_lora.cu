@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kRows = 8;            // rows of a cluster (the n of the products)
-constexpr int kScanRows = 512;      // rows whose adapters a cluster goes through for itself, at most
+constexpr int kScanRows = 1024;     // rows whose adapters a cluster goes through for itself, at most
 constexpr int kGroupAdapters = 255; // adapters whose rows it counts, where fewer clusters than rows are launched
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -70,44 +70,53 @@ __device__ __forceinline__ void copy_row(const LoraParams& p, int64_t row, int p
 
 // Which rows are cluster `group`'s, where fewer clusters than rows are launched: that many groups of kRows of an
 // adapter lie before it.  Row tid + kThreads h's rank among its adapter's rows: those before it in its 32 rows, and
-// the counts of the 32s before, a byte each, 16 an adapter (table: (L + 1) times 16 bytes, the last one's of rows
+// the counts of the 32s before, a byte each, 32 an adapter (table: (L + 1) times 32 bytes, the last one's of rows
 // without an adapter).  Of these the cluster copies those of rank `group` and every p.groups-th from there.
 struct Found {
     int adapter, count, copies;      // count 0: no group is left
 };
 __device__ __forceinline__ Found find_rows(const LoraParams& p, int group, uint8_t* table, int (&s_rows)[kWarps][kRows], int* s_copy) {
-    constexpr int kH = kScanRows / kThreads;
+    constexpr int kH = kScanRows / kThreads, kWords = kScanRows / 128;
     __shared__ int s_lead[kScanRows / 32], s_found[3];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int i = tid; i <= p.L; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(table);
+    for (int i = tid; i < 2 * (p.L + 1); i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 3) s_found[tid] = 0;
+    if (tid < kScanRows / 32) s_lead[tid] = 0;
+    // (Of the kH times kThreads rows only those that are there are gone through: most calls have few.)
     int e[kH], rank[kH], total[kH];
-#pragma unroll
-    for (int h = 0; h < kH; ++h) {
-        const int row = tid + h * kThreads;
-        e[h] = row < p.n ? p.idx[row] : -2;
-        if (row < p.n && (e[h] < 0 || e[h] >= p.L)) e[h] = p.L;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < kH; ++h) {
-        const uint32_t peers = __match_any_sync(0xffffffffu, e[h]);
-        rank[h] = __popc(peers & ((1u << lane) - 1));
-        if (rank[h] == 0 && e[h] >= 0) table[e[h] * 16 + warp + h * kWarps] = (uint8_t)__popc(peers);
-    }
-    __syncthreads();
     uint32_t leads[kH];
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
-        const uint4 q = reinterpret_cast<const uint4*>(table)[max(e[h], 0)];
-        const uint32_t c[4] = {q.x, q.y, q.z, q.w};
-        const int b = warp + h * kWarps;
-        total[h] = 0;
+        const int row = tid + h * kThreads;
+        e[h] = -2;
+        rank[h] = total[h] = 0;
+        leads[h] = 0;
+        if (row < p.n) {
+            e[h] = p.idx[row];
+            if (e[h] < 0 || e[h] >= p.L) e[h] = p.L;
+        }
+    }
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+    for (int h = 0; h < kH; ++h) {
+        if (h * kThreads >= p.n) continue;
+        const uint32_t peers = __match_any_sync(0xffffffffu, e[h]);
+        rank[h] = __popc(peers & ((1u << lane) - 1));
+        if (rank[h] == 0 && e[h] >= 0) table[e[h] * 4 * kWords + warp + h * kWarps] = (uint8_t)__popc(peers);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+        if (h * kThreads >= p.n) continue;
+        const int b = warp + h * kWarps;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if (128 * i >= p.n) continue;
+            const uint32_t c = words[max(e[h], 0) * kWords + i];
             const int here = min(max(b - 4 * i, 0), 4);      // bytes of this word that count
-            total[h] = __dp4a(c[i], 0x01010101u, (uint32_t)total[h]);
-            rank[h] = __dp4a(c[i], here == 4 ? 0x01010101u : 0x01010101u & ((1u << 8 * here) - 1), (uint32_t)rank[h]);
+            total[h] = __dp4a(c, 0x01010101u, (uint32_t)total[h]);
+            rank[h] = __dp4a(c, here == 4 ? 0x01010101u : 0x01010101u & ((1u << 8 * here) - 1), (uint32_t)rank[h]);
         }
         leads[h] = __ballot_sync(0xffffffffu, e[h] >= 0 && e[h] < p.L && rank[h] % kRows == 0);
         if (lane == 0) s_lead[b] = __popc(leads[h]);
@@ -115,6 +124,7 @@ __device__ __forceinline__ Found find_rows(const LoraParams& p, int group, uint8
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
+        if (h * kThreads >= p.n) continue;
         const int b = warp + h * kWarps;
         int before = 0;
         for (int i = 0; i < b; ++i) before += s_lead[i];
@@ -126,12 +136,13 @@ __device__ __forceinline__ Found find_rows(const LoraParams& p, int group, uint8
         if (e[h] == p.L && rank[h] % p.groups == group) s_copy[rank[h] / p.groups] = tid + h * kThreads;
     }
     __syncthreads();
-    const uint4 q = reinterpret_cast<const uint4*>(table)[p.L];
-    const int none = __dp4a(q.x, 0x01010101u, __dp4a(q.y, 0x01010101u, __dp4a(q.z, 0x01010101u, __dp4a(q.w, 0x01010101u, 0u))));
-    const Found f{s_found[0], s_found[2], p.copy && none > group ? (none - group - 1) / p.groups + 1 : 0};
+    uint32_t none = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) none = __dp4a(words[p.L * kWords + i], 0x01010101u, none);
+    const Found f{s_found[0], s_found[2], p.copy && (int)none > group ? ((int)none - group - 1) / p.groups + 1 : 0};
 #pragma unroll
     for (int h = 0; h < kH; ++h)
-        if (f.count && e[h] == f.adapter && rank[h] / kRows == s_found[1] / kRows)
+        if (h * kThreads < p.n && f.count && e[h] == f.adapter && rank[h] / kRows == s_found[1] / kRows)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) s_rows[w][rank[h] % kRows] = tid + h * kThreads;
     __syncthreads();
@@ -145,7 +156,8 @@ template <bool kBf16, int kRT, int kParts, bool kGroups>
 __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p) {
     constexpr int kR = kRT * 16;
     constexpr int kPad = kRT == 1 ? 0 : 16;       // (no bank conflicts between rows of parts)
-    __shared__ __align__(16) float s_part[kWarps][kR][kRows];   // then v's parts, [part][row][rank]
+    constexpr int kSpan = kGroups && kRT == 1 ? 2 * kWarps : kWarps;
+    __shared__ __align__(16) float s_part[kSpan][kR][kRows];    // (first the counts,) then v's parts, [part][row][rank]
     __shared__ float s_mine[kR * kRows];
     __shared__ int s_rows[kWarps][kRows];         // (every warp finds them for itself)
     __shared__ uint32_t s_top[kRows];
@@ -161,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     int adapter, count;
     [[maybe_unused]] int copies = 0;
     if constexpr (kGroups) {
-        static_assert(sizeof(s_part) >= (kGroupAdapters + 1) * 16, "the counts fit");
+        static_assert(sizeof(s_part) >= (kGroupAdapters + 1) * (kScanRows / 32), "the counts fit");
         const Found f = find_rows(p, group, reinterpret_cast<uint8_t*>(&s_part[0][0][0]), s_rows, s_copy);
         adapter = f.adapter;
         count = f.count;
@@ -545,21 +557,27 @@ cudaError_t launch_all(const LoraParams& p, int x_type, int groups, int cluster,
 // Bytes of an adapter's matrices.
 int64_t adapter_bytes(int K, int O, int r) { return (int64_t)r * ((int64_t)K + O) * 2; }
 
-// Rows that the clusters take as they come, each going through all of them for its own; more are sorted first.
-// (500 rows, us so and sorted: 131 KB an adapter 12.5 and 20.9, 64 adapters of 459 KB 26.5 and 43.8; of rank 64,
-// 4 of 1.8 MB 27.5 and 33.6, 8 of 1 MB 18.1 and 25.4, 20 of 1.8 MB 35.3 and 31.3; 400 rows, 16 of rank 128 45 and 30.)
-bool by_scan(int64_t n, int L, int K, int O, int r) {
-    return n <= 256 || (n <= kScanRows && (adapter_bytes(K, O, r) < 1 << 20 || (L <= 8 && r <= 64)));
-}
-
 // The groups of kRows that L adapters' rows make at most, where so few clusters are launched; 0: one a row.  A
 // cluster then costs the ranking of all rows, and saves the launches of those whose row another one takes.  (us a
 // row each and so: 64 rows, 8 adapters of 131 KB 5.9 and 5.6; 30 rows, 3 of 2 MB 12.6 and 11.5; 200 rows, 20 of
 // 1.1 MB 23.7 and 15.6; 500 rows, 8 of 262 KB 16.0 and 10.2; 8 rows of one adapter 4.1 and 4.9; 256 rows, 100 of
 // 440 KB, 119 groups, 17.1 and 17.6.)
+int most_groups(int n, int L) { return (int)((n + 7LL * std::min(n, L)) / 8); }
 int group_count(int n, int L) {
-    const int most = (n + 7 * std::min(n, L)) / 8;
+    const int most = most_groups(n, L);
     return n > 16 && L <= kGroupAdapters && most <= n * 7 / 16 ? most : 0;
+}
+
+// Rows that the clusters take as they come, each going through all of them for its own; more are sorted first.
+// (us so and sorted: 500 rows, 131 KB an adapter 12.5 and 20.9, 64 adapters of 459 KB 26.5 and 43.8; of rank 64, 4 of
+// 1.8 MB 27.5 and 33.6, 8 of 1 MB 18.1 and 25.4, 20 of 1.8 MB 35.3 and 31.3; 400 rows, 16 of rank 128 45 and 30.  In groups:
+// 700 rows, 96 groups of 393 KB 15.4 and 22.5; 1024 rows, 215 of 131 KB 20.2 and 29.1; 1000 rows, 132 of 262 KB 21.2 and
+// 22.8, 142 of 524 KB 31.2 and 26.4; 600 rows, 82 of 1 MB 33.4 and 26.3.)  What holds for n rows holds for fewer, so
+// that a workspace for many serves few; above 512 rows L <= 182 makes them groups.
+bool by_scan(int64_t n, int L, int K, int O, int r) {
+    const int64_t bytes = adapter_bytes(K, O, r);
+    if (n <= 256 || (n <= 512 && (bytes < 1 << 20 || (L <= 8 && r <= 64)))) return true;
+    return n <= kScanRows && L <= 182 && most_groups((int)n, L) * bytes <= 48 << 20;
 }
 
 // Blocks of a cluster.  More share an adapter's bytes among them; but most rows' clusters find that

@@ -64,6 +64,14 @@ def test_workspace_bytes():
     assert sizes == sorted(sizes) and sizes[0] >= 256 and all(s % 256 == 0 for s in sizes)
 
 
+@pytest.mark.parametrize("L", [1, 7, 8, 9, 100, 182, 183, 255, 256, 1024])
+@pytest.mark.parametrize("inp,feats,rank", [(64, 48, 16), (2048, 2048, 16), (4096, 4096, 32), (7168, 7168, 64), (4096, 4096, 128)])
+def test_a_workspace_for_many_rows_serves_fewer(L, inp, feats, rank):
+    c = _config(inp, feats, rank, L)
+    sizes = [B.moe_lora_workspace_bytes(c, n) for n in range(1100)]
+    assert sizes == sorted(sizes)
+
+
 def test_holder_refusals():
     a, b = torch.zeros(3, 16, 64, dtype=BF), torch.zeros(3, 40, 16, dtype=BF)
     for bad in ((a[0], b), (a, b[:2]), (a, b.half()), (a.float(), b.float()), (a[:, :8], b), (a.transpose(1, 2), b), (a, b, torch.ones(4)),
@@ -214,7 +222,7 @@ def test_runs_that_end_inside_a_tile(lib, y, O, rest):
 
 
 @gpu
-@pytest.mark.parametrize("n", [17, 32, 33, 200, 257, 500, 511, 512])
+@pytest.mark.parametrize("n", [17, 32, 33, 200, 257, 500, 511, 512, 513, 767, 1023, 1024])
 @pytest.mark.parametrize("L", [1, 7, 219])
 @pytest.mark.parametrize("how", ["one", "none", "skewed", "blocks", "few"])
 def test_how_rows_share_adapters(lib, n, L, how):
