@@ -708,7 +708,11 @@ cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&
     g.p = p;
     g.N = (p.r + 15) / 16 * 16;
     g.part = part;
-    g.max_splits = (int)std::min<int64_t>(kLoraMaxSplits, lora_part_rows(p.n) / p.n);
+    // Stretches of K: each is a part of v that every block of the expansion reads and adds.  (us with 8, 6, 4, 3 and 2:
+    // 1000 rows of 1024, rank 128, 36, 32, 28, 26, 24; 600 of 2048, rank 128, 39, 34, 30, 28, 27; 600 of 4096, rank 64, 27.1,
+    // 25.6, 24.7, 25.4, 27.6; 1000 of 7168, rank 64, 38, 39, 42, 47, 57; 3001 of 2048, rank 16, 26, 27, 27, 29, 32.)
+    const int by_rank = std::max(2, 6 * ((p.K + kBox - 1) / kBox) / p.r);
+    g.max_splits = (int)std::min<int64_t>(std::min(kLoraMaxSplits, by_rank), lora_part_rows(p.n) / p.n);
     g.err = err;
     const int stage = kBoxBytes + g.N * kBox * 2;
     g.stages = std::min((p.K + kBox - 1) / kBox, 100 * 1024 / stage);
