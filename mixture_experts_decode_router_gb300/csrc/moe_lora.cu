@@ -2,7 +2,9 @@
 //   out[t] = base[t] + scale[a] B_a (A_a x[t]),  a = idx[t];  out[t] = base[t] where a is no adapter
 //
 // Few rows: bound by the bytes of the adapters that occur and by latency.  One cluster takes up
-// to eight rows that share an adapter, so that the adapter's matrices are read once for them:
+// to eight rows that share an adapter, so that the adapter's matrices are read once for them (one row of
+// 2048 -> 2048, rank 16: 3.8 us; 64 of 7168 -> 2048, rank 64, 8 adapters: 9.3; 256 of 2048 -> 5003 fp32,
+// rank 32, 200 adapters: 15.5):
 // its blocks split K for v = A x (each warp's products m16n8k16 with A as the rows and the
 // eight x as the columns, 16-byte loads straight into the fragments), add their partial v over
 // distributed shared memory, and split the outputs for B v.  No workspace and one launch.
