@@ -7,6 +7,7 @@
 // v = A x (lora_shrink_kernel): a block takes a tile of rows and a stretch of K.  Rows of x are
 // gathered where they lie by TMA (four rows an instruction, 64 elements of each), beside the adapter's
 // rows; M = 128 rows, N = the rank; the fp32 sums in tensor memory are written as that stretch's part.
+// (Of ranks above 16 the parts are then added by lora_sum_kernel.)
 //
 // out = base + B v (lora_expand_kernel): a block takes a tile of rows and a stretch of the outputs,
 // 128 at a time.  v, summed over the stretches in their order, scaled and split into 16-bit parts
@@ -42,6 +43,7 @@ struct TcArgs {
     int stages;       // shrink: ring
     int tmem_cols;    // shrink
     int expand_blocks;
+    bool summed;      // v's parts have been added into the first
     float* part;      // [splits][n][r]
     int32_t* err;
 };
@@ -268,6 +270,29 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
     }
 }
 
+// v's parts added into the first, in their order, four elements a thread: where every block of the expansion would
+// read and add many of them.
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const TcArgs g) {
+    const LoraParams& p = g.p;
+    pdl_wait();
+    pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
+    const int n = pieces(p.ctrl->n_active, (p.K + kBox - 1) / kBox, g.max_splits, kLoraBlocks).n;
+    const int64_t size = (int64_t)p.n * p.r / 4;
+    float4* part = reinterpret_cast<float4*>(g.part);
+    for (int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x; n > 1 && i < size; i += (int64_t)gridDim.x * kSumThreads) {
+        float4 v[kLoraMaxSplits];
+#pragma unroll
+        for (int k = 0; k < kLoraMaxSplits; ++k) v[k] = k < n ? part[i + k * size] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 1; k < kLoraMaxSplits; ++k)
+            if (k < n) {
+                v[0].x += v[k].x; v[0].y += v[k].y; v[0].z += v[k].z; v[0].w += v[k].w;
+            }
+        part[i] = v[0];
+    }
+}
+
 constexpr int kNT = 128;                 // outputs of a tile
 constexpr int kEpiWarps = 8;             // 32 rows and 64 outputs of a tile each
 constexpr int kExpandThreads = 32 * (kEpiWarps + 2);
@@ -359,7 +384,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
     pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
 
     const int O = p.O, n_tiles = (O + kNT - 1) / kNT, runs = p.ctrl->n_rsegs;
-    const Pieces ks = pieces(p.ctrl->n_active, (p.K + kBox - 1) / kBox, g.max_splits, kLoraBlocks);
+    const int parts = g.summed ? 1 : pieces(p.ctrl->n_active, (p.K + kBox - 1) / kBox, g.max_splits, kLoraBlocks).n;
     const Pieces os = pieces(runs, n_tiles, 64, g.expand_blocks);
     int done_tiles = 0;      // of this block, before this unit
     constexpr int kSize = kF32 ? 4 : 2, kV = 16 / kSize;        // elements of 16 bytes
@@ -418,7 +443,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                     if (row < count && c8 * 8 < p.r) {
                         const float* part = g.part + (int64_t)(first + row) * p.r + c8 * 8;
 #pragma unroll 2
-                        for (int s = 0; s < ks.n; ++s, part += (int64_t)p.n * p.r) {
+                        for (int s = 0; s < parts; ++s, part += (int64_t)p.n * p.r) {
                             const float4 a = *reinterpret_cast<const float4*>(part), b = *reinterpret_cast<const float4*>(part + 4);
                             v[u][0] += a.x; v[u][1] += a.y; v[u][2] += a.z; v[u][3] += a.w;
                             v[u][4] += b.x; v[u][5] += b.y; v[u][6] += b.z; v[u][7] += b.w;
@@ -709,11 +734,12 @@ cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&
     g.p = p;
     g.N = (p.r + 15) / 16 * 16;
     g.part = part;
-    // Stretches of K: each is a part of v that every block of the expansion reads and adds.  (us with 8, 6, 4, 3 and 2:
-    // 1000 rows of 1024, rank 128, 36, 32, 28, 26, 24; 600 of 2048, rank 128, 39, 34, 30, 28, 27; 600 of 4096, rank 64, 27.1,
-    // 25.6, 24.7, 25.4, 27.6; 1000 of 7168, rank 64, 38, 39, 42, 47, 57; 3001 of 2048, rank 16, 26, 27, 27, 29, 32.)
-    const int by_rank = std::max(2, 6 * ((p.K + kBox - 1) / kBox) / p.r);
-    g.max_splits = (int)std::min<int64_t>(std::min(kLoraMaxSplits, by_rank), lora_part_rows(p.n) / p.n);
+    // Parts of v, one a stretch of K, that every block of the expansion would read and add are first added by a kernel
+    // of their own, which costs less above a rank of 16 (us without and with it: 1000 rows of 7168, rank 64, 38.7 and 32.9;
+    // 600 of 2048, rank 128, 39.0 and 22.7; 4000 of 4096, rank 64, 42.9 and 37.8; 1000 of 4096, rank 32, 23.7 and 21.5; 3001 of
+    // 2048, rank 16, 26.6 and 28.2).
+    g.summed = p.r > 16;
+    g.max_splits = (int)std::min<int64_t>(kLoraMaxSplits, lora_part_rows(p.n) / p.n);
     g.err = err;
     const int stage = kBoxBytes + g.N * kBox * 2;
     g.stages = std::min((p.K + kBox - 1) / kBox, 100 * 1024 / stage);
@@ -727,6 +753,10 @@ cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&
                         maps[0], maps[3], maps[1], g)) != cudaSuccess)
         return e;
 
+    if (g.summed &&
+        (e = launch_pdl(lora_sum_kernel, dim3((unsigned)std::min<int64_t>(8 * 152, ((int64_t)p.n * p.r / 4 + kSumThreads - 1) / kSumThreads)),
+                        dim3(kSumThreads), 0, st, g)) != cudaSuccess)
+        return e;
     const bool f32 = p.out_type == MOE_F32, bf = x_type == MOE_BF16;
     const int64_t esize = f32 ? 4 : 2;
     const bool wide = !p.out_host && p.O * esize % 64 == 0 && p.vec * esize >= 16;
