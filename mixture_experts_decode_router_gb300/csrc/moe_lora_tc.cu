@@ -15,12 +15,12 @@
 // warps add the base to what they read of tensor memory.  They read it by fragments, of which a lane
 // has column pairs 8 apart; B's rows are put into shared memory so that these are pieces of 16 bytes
 // of neighbouring outputs, four lanes' side by side.  base comes by asynchronous copies, a tile ahead,
-// to where the lane that wants it reads it, and out is written from the registers.  (8192 rows of 7168
-// outputs, rank 64: 43 us, 5.4 TB/s, and the sums of v before it 26 and 5; base loaded into registers a tile
-// ahead: 74, when this form took 49, since waits for anything else waited for those loads too; results through shared memory, 128 bytes along a row: 61 us, bound
-// by its traffic and steps.)  Rows that are not of whole aligned pieces go through shared memory: their
-// aligned 16 bytes, and single elements at the ends (6000 rows of 3551 outputs: 49 us; all by single
-// elements 102).
+// to where the lane that wants it reads it, and out is written from the registers (8192 rows of 7168
+// outputs, rank 64: 43 us, 5.4 TB/s, and the sums of v before it 26 and 5).  Of the other forms, when this
+// one took 49 us: base loaded into registers a tile ahead 74, since waits for anything else waited for
+// those loads too; results through shared memory, 128 bytes along a row, 61, bound by its traffic and
+// steps.  Rows that are not of whole aligned pieces go through shared memory: their aligned 16 bytes, and
+// single elements at the ends (6000 rows of 3551 outputs: 49 us; all by single elements 102).
 #include <mutex>
 #include <type_traits>
 
