@@ -15,6 +15,7 @@
 // times a power of two for each row, which takes its largest element to [2^14, 2^15).
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "moe_launch.cuh"
 #include "moe_lora.cuh"
@@ -26,7 +27,8 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kRows = 8;            // rows of a cluster (the n of the products)
 constexpr int kScanRows = 1024;     // rows whose adapters a cluster goes through for itself, at most
-constexpr int kGroupAdapters = 255; // adapters whose rows it counts, where fewer clusters than rows are launched
+constexpr int kGroupAdapters = 255; // adapters whose rows it counts, where it takes groups of rows
+constexpr int kGroups = 448;        // of kRows at most
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -70,30 +72,30 @@ __device__ __forceinline__ void copy_row(const LoraParams& p, int64_t row, int p
     }
 }
 
-// Which rows are cluster `group`'s, where fewer clusters than rows are launched: that many groups of kRows of an
-// adapter lie before it.  Row tid + kThreads h's rank among its adapter's rows: those before it in its 32 rows, and
-// the counts of the 32s before, a byte each, 32 an adapter (table: (L + 1) times 32 bytes, the last one's of rows
-// without an adapter).  Of these the cluster copies those of rank `group` and every p.groups-th from there.
-struct Found {
-    int adapter, count, copies;      // count 0: no group is left
+// The rows in groups of kRows of an adapter, the adapters one after another, formed by each block for itself.  A
+// row's rank among its adapter's rows: those before it in its 32 rows, and the counts of the 32s before, a byte
+// each, 32 an adapter (table: (L + 1) times 32 bytes, the last one's of rows without an adapter).
+struct Groups {
+    uint16_t rows[kGroups * kRows], none[kScanRows], base[kThreads];
+    uint8_t adapter[kGroups], count[kGroups];
 };
-__device__ __forceinline__ Found find_rows(const LoraParams& p, int group, uint8_t* table, int (&s_rows)[kWarps][kRows], int* s_copy) {
+struct Found {
+    int groups, none;
+};
+__device__ __forceinline__ Found find_groups(const LoraParams& p, uint8_t* table, Groups& out) {
     constexpr int kH = kScanRows / kThreads, kWords = kScanRows / 128;
-    __shared__ int s_lead[kScanRows / 32], s_found[3];
+    static_assert(kGroupAdapters <= kThreads, "an adapter a thread");
+    __shared__ int s_sum[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t* words = reinterpret_cast<const uint32_t*>(table);
     for (int i = tid; i < 2 * (p.L + 1); i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid < 3) s_found[tid] = 0;
-    if (tid < kScanRows / 32) s_lead[tid] = 0;
     // (Of the kH times kThreads rows only those that are there are gone through: most calls have few.)
-    int e[kH], rank[kH], total[kH];
-    uint32_t leads[kH];
+    int e[kH], rank[kH];
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
         const int row = tid + h * kThreads;
         e[h] = -2;
-        rank[h] = total[h] = 0;
-        leads[h] = 0;
+        rank[h] = 0;
         if (row < p.n) {
             e[h] = p.idx[row];
             if (e[h] < 0 || e[h] >= p.L) e[h] = p.L;
@@ -108,62 +110,68 @@ __device__ __forceinline__ Found find_rows(const LoraParams& p, int group, uint8
         if (rank[h] == 0 && e[h] >= 0) table[e[h] * 4 * kWords + warp + h * kWarps] = (uint8_t)__popc(peers);
     }
     __syncthreads();
+    // Each adapter's groups: an adapter a thread.
+    uint32_t total = 0, none = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        if (128 * i >= p.n) continue;
+        if (tid < p.L) total = __dp4a(words[tid * kWords + i], 0x01010101u, total);
+        none = __dp4a(words[p.L * kWords + i], 0x01010101u, none);
+    }
+    const int mine = (int)(total + kRows - 1) / kRows;
+    int before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) s_sum[warp] = before;
+    before -= mine;
+    __syncthreads();
+    int groups = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_sum[w];
+        groups += s_sum[w];
+    }
+    out.base[tid] = (uint16_t)before;
+    for (int j = 0; j < mine; ++j) {
+        out.adapter[before + j] = (uint8_t)tid;
+        out.count[before + j] = (uint8_t)min(kRows, (int)total - j * kRows);
+    }
+    __syncthreads();
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
         if (h * kThreads >= p.n) continue;
         const int b = warp + h * kWarps;
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
-            if (128 * i >= p.n) continue;
+            if (4 * i >= b) continue;
             const uint32_t c = words[max(e[h], 0) * kWords + i];
-            const int here = min(max(b - 4 * i, 0), 4);      // bytes of this word that count
-            total[h] = __dp4a(c, 0x01010101u, (uint32_t)total[h]);
+            const int here = min(b - 4 * i, 4);      // bytes of this word that count
             rank[h] = __dp4a(c, here == 4 ? 0x01010101u : 0x01010101u & ((1u << 8 * here) - 1), (uint32_t)rank[h]);
         }
-        leads[h] = __ballot_sync(0xffffffffu, e[h] >= 0 && e[h] < p.L && rank[h] % kRows == 0);
-        if (lane == 0) s_lead[b] = __popc(leads[h]);
+        const int row = tid + h * kThreads;
+        if (e[h] == p.L) out.none[rank[h]] = (uint16_t)row;
+        else if (e[h] >= 0) out.rows[out.base[e[h]] * kRows + rank[h]] = (uint16_t)row;
     }
     __syncthreads();
-#pragma unroll
-    for (int h = 0; h < kH; ++h) {
-        if (h * kThreads >= p.n) continue;
-        const int b = warp + h * kWarps;
-        int before = 0;
-        for (int i = 0; i < b; ++i) before += s_lead[i];
-        if ((leads[h] >> lane & 1) && before + __popc(leads[h] & ((1u << lane) - 1)) == group) {
-            s_found[0] = e[h];
-            s_found[1] = rank[h];
-            s_found[2] = min(kRows, total[h] - rank[h]);
-        }
-        if (e[h] == p.L && rank[h] % p.groups == group) s_copy[rank[h] / p.groups] = tid + h * kThreads;
-    }
-    __syncthreads();
-    uint32_t none = 0;
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) none = __dp4a(words[p.L * kWords + i], 0x01010101u, none);
-    const Found f{s_found[0], s_found[2], p.copy && (int)none > group ? ((int)none - group - 1) / p.groups + 1 : 0};
-#pragma unroll
-    for (int h = 0; h < kH; ++h)
-        if (h * kThreads < p.n && f.count && e[h] == f.adapter && rank[h] / kRows == s_found[1] / kRows)
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) s_rows[w][rank[h] % kRows] = tid + h * kThreads;
-    __syncthreads();
-    return f;
+    return {groups, (int)none};
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
 
-// kRT: tiles of 16 of the rank.  kParts: parts of v.  kGroups: fewer clusters than rows (find_rows).
-template <bool kBf16, int kRT, int kParts, bool kGroups>
+// kRT: tiles of 16 of the rank.  kParts: parts of v.  kInGroups: a cluster for each group of rows (find_groups).
+template <bool kBf16, int kRT, int kParts, bool kInGroups>
 __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p) {
     constexpr int kR = kRT * 16;
     constexpr int kPad = kRT == 1 ? 0 : 16;       // (no bank conflicts between rows of parts)
-    constexpr int kSpan = kGroups && kRT == 1 ? 2 * kWarps : kWarps;
+    constexpr int kSpan = kInGroups && kRT == 1 ? 2 * kWarps : kWarps;
     __shared__ __align__(16) float s_part[kSpan][kR][kRows];    // (first the counts,) then v's parts, [part][row][rank]
     __shared__ float s_mine[kR * kRows];
     __shared__ int s_rows[kWarps][kRows];         // (every warp finds them for itself)
     __shared__ uint32_t s_top[kRows];
-    __shared__ int s_copy[kGroups ? kRows + 1 : 1];
+    __shared__ std::conditional_t<kInGroups, Groups, int> s_groups;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int C = (int)cluster_size(), c = (int)cluster_rank(), group = blockIdx.x / C;
     if (tid < kRows) s_top[tid] = 0;
@@ -171,19 +179,24 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
 
     // The cluster's rows: row `group`, if an adapter's rows before it fill whole clusters, and
-    // the next ones of its adapter; kGroups: the group-th of these; or a run of the rows sorted by adapter.
+    // the next ones of its adapter; kInGroups: the group-th of these; or a run of the rows sorted by adapter.
     int adapter, count;
-    [[maybe_unused]] int copies = 0;
-    if constexpr (kGroups) {
+    [[maybe_unused]] int none = 0;       // rows without an adapter that are to be written
+    auto copy_none = [&]() {
+        if constexpr (kInGroups)
+            for (int i = group; i < none; i += p.groups) copy_row(p, s_groups.none[i], c, C);
+    };
+    if constexpr (kInGroups) {
         static_assert(sizeof(s_part) >= (kGroupAdapters + 1) * (kScanRows / 32), "the counts fit");
-        const Found f = find_rows(p, group, reinterpret_cast<uint8_t*>(&s_part[0][0][0]), s_rows, s_copy);
-        adapter = f.adapter;
-        count = f.count;
-        copies = f.copies;
-        if (!count) {
-            for (int i = 0; i < copies; ++i) copy_row(p, s_copy[i], c, C);
+        const Found f = find_groups(p, reinterpret_cast<uint8_t*>(&s_part[0][0][0]), s_groups);
+        none = p.copy ? f.none : 0;
+        if (group >= f.groups) {
+            copy_none();
             return;
         }
+        adapter = s_groups.adapter[group];
+        count = s_groups.count[group];
+        if (lane < count) s_rows[warp][lane] = s_groups.rows[group * kRows + lane];
     } else if (p.segs) {
         if (group >= p.ctrl->n_rsegs) return;
         const int first = p.segs[3 * group + 1];
@@ -313,8 +326,7 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
     constexpr bool kEarly = kRT < 8;
     if (kEarly) fetch(c * uper + warp);
     cluster_arrive();
-    if constexpr (kGroups)
-        for (int i = 0; i < copies; ++i) copy_row(p, s_copy[i], c, C);
+    copy_none();
     cluster_wait();
     // Each element of v is summed over the blocks in their order, and split, by one thread.
     constexpr int kMine = (kR * kRows + kThreads - 1) / kThreads;
@@ -506,9 +518,9 @@ lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_
     }
 }
 
-template <bool kBf16, int kRT, int kParts, bool kGroups>
+template <bool kBf16, int kRT, int kParts, bool kInGroups>
 cudaError_t launch_clusters(const LoraParams& p, int groups, int cluster, cudaStream_t st) {
-    auto kern = lora_rows_kernel<kBf16, kRT, kParts, kGroups>;
+    auto kern = lora_rows_kernel<kBf16, kRT, kParts, kInGroups>;
     if (cluster > 8) {   // (more than every GPU has to offer: to be asked for)
         static std::mutex mu;
         static bool configured[128] = {};
@@ -567,7 +579,7 @@ int64_t adapter_bytes(int K, int O, int r) { return (int64_t)r * ((int64_t)K + O
 int most_groups(int n, int L) { return (int)((n + 7LL * std::min(n, L)) / 8); }
 int group_count(int n, int L) {
     const int most = most_groups(n, L);
-    return n > 16 && L <= kGroupAdapters && most <= n * 7 / 16 ? most : 0;
+    return n > 16 && L <= kGroupAdapters && most <= std::min(n * 7 / 16, kGroups) ? most : 0;
 }
 
 // Rows that the clusters take as they come, each going through all of them for its own; more are sorted first.
