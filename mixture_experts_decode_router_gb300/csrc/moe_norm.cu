@@ -218,18 +218,28 @@ __device__ __forceinline__ float max_abs(float m, float v) {
     return r;
 }
 
-// The scale of values whose largest magnitude has the bits `most`: at least 2^-126, so that its
-// reciprocal is finite; an infinity's or NaN's is itself, and the values it scales read as NaN.
+// The scale of values whose largest magnitude has the bits `most`: their 448th part (the quotient: a product with
+// 1 / 448 is another number for half of all magnitudes, and is corrected by what it leaves of m: Markstein, 1990),
+// at least 2^-126, so that its reciprocal is finite; an infinity's or NaN's is itself, and the values it scales read
+// as NaN.
 __device__ __forceinline__ float scale_of(uint32_t most) {
-    const float m = __uint_as_float(most);
-    return most >= kInfBits ? m : fmaxf(m * (1.f / 448.f), 0x1p-126f);
+    const float m = __uint_as_float(most), q = m * (1.f / 448.f);
+    return most >= kInfBits ? m : fmaxf(fmaf(fmaf(q, -448.f, m), 1.f / 448.f, q), 0x1p-126f);
 }
-// 1 / s of a scale (2^-126 to 2^120, or as above), within a step of fp32.
-__device__ __forceinline__ float reciprocal(float s) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-    return r;
-}
+// 1 / s of a scale (2^-126 to 2^120, or as above) as a sum of two fp32, off by some 2^-46 of it: a product with it is
+// the quotient rounded once (but for quotients that near to the middle of two fp32).  One with its first part alone
+// is off by steps of fp32, which take a code that lies at a border to the other side of it (2200 of 8192 x 7168;
+// 69.2 us so and 70.2 with both).
+struct Reciprocal {
+    float2 hi, lo;
+    __device__ __forceinline__ explicit Reciprocal(float s) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+        hi = both(r);
+        lo = both(s < INFINITY ? fmaf(-s, r, 1.f) * r : 0.f);
+    }
+    __device__ __forceinline__ float2 times(float2 v) const { return __ffma2_rn(v, hi, __fmul2_rn(v, lo)); }
+};
 // E4M3 of a pair (x in the low byte), to nearest even; NaN is NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float2 v) {
     uint16_t r;
@@ -275,8 +285,8 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
     // kAny: where the warp's chunks c begin, and how many elements they have.
     auto span = [&](int c) { return (c * T + (tid & ~31)) * 8; };
     auto within = [&](int c) { return live ? min(256, p.H - span(c)) : 0; };
-    auto codes = [&](const float2* y, float2 inv) {
-        return make_uint2(e4m3x2(__fmul2_rn(y[0], inv)) | e4m3x2(__fmul2_rn(y[1], inv)) << 16, e4m3x2(__fmul2_rn(y[2], inv)) | e4m3x2(__fmul2_rn(y[3], inv)) << 16);
+    auto codes = [&](const float2* y, const Reciprocal& r) {
+        return make_uint2(e4m3x2(r.times(y[0])) | e4m3x2(r.times(y[1])) << 16, e4m3x2(r.times(y[2])) | e4m3x2(r.times(y[3])) << 16);
     };
     float2 h[kCh * 4], ss = make_float2(0.f, 0.f);
 #pragma unroll
@@ -363,7 +373,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
                 for (int o = 1; o < 16; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
                 const float s = scale_of(most);
                 if (in[c] && (tid & 15) == 0) p.scale8[row * p.n_scales + at / 128] = s;
-                const uint2 q = codes(y, both(reciprocal(s)));
+                const uint2 q = codes(y, Reciprocal(s));
                 if constexpr (kAny) {
                     if (within(c) > 0) put8(p.out8 + r0 * p.out8_stride + span(c), within(c), q, stage);
                 } else if (in[c]) {
@@ -376,11 +386,11 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
     }
     if (p.out8 && !p.group) {
         const float s = scale_of(row_max(top, T, red + 96));
-        const float2 inv = both(reciprocal(s));
+        const Reciprocal r(s);
         if (tid == 0 && live) p.scale8[row] = s;
 #pragma unroll
         for (int c = 0; c < kCh; ++c) {
-            const uint2 q = codes(&h[4 * c], inv);
+            const uint2 q = codes(&h[4 * c], r);
             if constexpr (kAny) {
                 if (within(c) > 0) put8(p.out8 + r0 * p.out8_stride + span(c), within(c), q, stage);
             } else if (in[c]) {

@@ -308,6 +308,30 @@ def test_rows_of_zeros(lib, eps, H):
 
 
 @gpu
+@pytest.mark.parametrize("x,r", [(BF, BF), (HF, F32), (F32, None)])
+@pytest.mark.parametrize("out8", ["group", "row"])
+@pytest.mark.parametrize("n,H", [(64, 7168), (700, 333), (40, 16392)])
+def test_scales_and_codes_are_quotients(lib, x, r, out8, n, H):
+    """Of y as the fp32 output shows it: scale = max |y| / 448 and code = E4M3(y / scale), both rounded once, at every
+    border (a bf16 row's elements lie on many).  Rows of small scales among them."""
+    for w in (weights(H), torch.ones(H, device="cuda")):
+        op = MoeNorm(w, eps=0.0, out_dtype=F32, out8=out8)
+        by = MoeNorm((w.float() * 2.0 ** -80).to(BF), eps=0.0, out_dtype=F32, out8=out8)
+        xv, rv = rows(n, H, x, seed=H), None if r is None else rows(n, H, r, seed=2, spread=3.0)
+        for o in (op, by):
+            y, _, q, s = o.forward(xv, rv)
+            size = 128 if out8 == "group" else H
+            G = -(-H // size)
+            z = torch.zeros(n, G * size, dtype=torch.float64, device="cuda")
+            z[:, :H] = y
+            # (64 bits hold more than twice 24 and two: rounded to 32 they are the quotient rounded once.)
+            want = (z.view(n, G, size).abs().amax(2) / 448).float().clamp(min=2.0 ** -126)
+            assert torch.equal(s, want)
+            v = (y.double() / s.double().repeat_interleave(size, 1)[:, :H]).float()
+            assert torch.equal(q.view(torch.uint8), v.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+
+
+@gpu
 @pytest.mark.parametrize("H", [96, 2048])
 def test_special_values_stay_in_their_row(lib, H):
     x, r = rows(8, H), rows(8, H, seed=2)
