@@ -405,8 +405,10 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
             uint8_t* to[4];
             const int left = O - (t0 * kNT + half * 64 + kV * (lane & 3));      // outputs from the lane's first one on
             uint8_t* mine = sStage + warp * ahead_bytes(kF32) + lane * 16;      // [row][piece][lane]
+            // (Rows r that the warp has none of get no copies: no wait would stand between those and the next
+            // unit's, which go to the same places.)
             auto fetch = [&](int i, int r) {
-                if (p.base && i < nt) {
+                if (p.base && i < nt && 8 * r < here) {
 #pragma unroll
                     for (int w = 0; w < kPieces; ++w)
                         if (i * kNT + 4 * kV * w < left) cp_async16(mine + (r * kPieces + w) * 512, from[r] + (size_t)i * (kNT * kSize) + 64 * w);
