@@ -373,7 +373,8 @@ moe_status_t moe_static_workspace_check(int32_t* device_error, void** workspace,
  *                       wait of the grouped tensor-core kernels gave up (8: the
  *                       down kernel's grid barrier before its combine); 6-7:
  *                       one of the tensor-core router's; 31-37: one of
- *                       moe_lora's, in its workspace; 20: the workspace
+ *                       moe_lora's, in its workspace, or moe_lora_checked's,
+ *                       in its errors; 20: the workspace
  *                       control block was not zeroed before use.  An FP8
  *                       call on the grouped path made while an error is
  *                       pending does not write out (its down kernel, which
@@ -528,7 +529,8 @@ size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows);
  *               moe_lora_workspace_bytes(cfg, n) bytes; it need not be cleared,
  *               and keeps nothing between calls but the error word of the last,
  *               for moe_workspace_check (256 bytes: it is not used, and may be
- *               any address)
+ *               any address).  Where the products of v gave up, out is not written;
+ *               where those of out did, some of it is
  * base and out are aligned to their element.  fp32 sums; A_e x[t] enters the
  * second product in 16 bits of precision for outputs of 16 bits, in 24 for
  * fp32 outputs; one rounding to out_type, after the addition of base.
@@ -540,6 +542,16 @@ size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows);
 moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b, const float* scale, const void* x,
                       int64_t x_stride, const int32_t* idx, int32_t n, const void* base, int64_t base_stride, void* out,
                       int64_t out_stride, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* moe_lora for a workspace that does not outlive the call: the code of a bounded
+ * wait that gives up goes to `errors` (device, 256 bytes, 16-byte aligned, zeros
+ * before the first call; of any number of calls, on any streams), where it stays
+ * until moe_workspace_check(errors, 256, ...) reads and clears it.  Calls whose
+ * workspace is above 256 bytes do not write out while it is there (the others
+ * have no such waits). */
+moe_status_t moe_lora_checked(const moe_lora_config_t* cfg, const void* a, const void* b, const float* scale, const void* x,
+                              int64_t x_stride, const int32_t* idx, int32_t n, const void* base, int64_t base_stride, void* out,
+                              int64_t out_stride, void* ws, size_t ws_bytes, void* errors, moe_stream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* moe_status_string(moe_status_t status);

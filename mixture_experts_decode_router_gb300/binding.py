@@ -48,7 +48,8 @@ MOE_PATH_GROUPED = 2
 # Every function include/moe.h declares.
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_experts", "moe_forward",
             "moe_forward_timed", "moe_forward_static_ws", "moe_static_workspace_check",
-            "moe_topk", "moe_matvec", "moe_norm", "moe_lora_workspace_bytes", "moe_lora", "moe_workspace_check", "moe_status_string",
+            "moe_topk", "moe_matvec", "moe_norm", "moe_lora_workspace_bytes", "moe_lora", "moe_lora_checked", "moe_workspace_check",
+            "moe_status_string",
             "moe_abi_version")
 
 MOE_STATIC_WORKSPACE_BYTES = 16 << 20
@@ -167,6 +168,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.moe_lora_workspace_bytes.restype = S
     lib.moe_lora.argtypes = [ctypes.POINTER(moe_lora_config_t), P, P, P, P, I64, P, I32, P, I64, P, I64, P, S, P]
     lib.moe_lora.restype = ctypes.c_int
+    lib.moe_lora_checked.argtypes = [*lib.moe_lora.argtypes[:-1], P, P]
+    lib.moe_lora_checked.restype = ctypes.c_int
     lib.moe_status_string.argtypes = [ctypes.c_int]
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_abi_version.argtypes = []
@@ -280,6 +283,11 @@ def moe_lora(cfg, a, b, scale, x, x_stride, idx, n, base, base_stride, out, out_
                            int(base_stride), _ptr(out), int(out_stride), _ptr(ws), int(ws_bytes), _stream(stream))
 
 
+def moe_lora_checked(cfg, a, b, scale, x, x_stride, idx, n, base, base_stride, out, out_stride, ws, ws_bytes, errors, stream=None) -> int:
+    return load().moe_lora_checked(_ref(cfg), _ptr(a), _ptr(b), _ptr(scale), _ptr(x), int(x_stride), _ptr(idx), int(n), _ptr(base),
+                                   int(base_stride), _ptr(out), int(out_stride), _ptr(ws), int(ws_bytes), _ptr(errors), _stream(stream))
+
+
 def moe_workspace_check(ws, ws_bytes, stream=None):
     """(status, device error word); reads and clears the word, syncing the stream."""
     v = ctypes.c_int32(0)
@@ -316,7 +324,7 @@ def tensor_calls():
         ext = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ext)
         addr = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-                for f in ("moe_topk", "moe_matvec", "moe_experts", "moe_forward", "moe_norm", "moe_lora_workspace_bytes", "moe_lora")]
+                for f in ("moe_topk", "moe_matvec", "moe_experts", "moe_forward", "moe_norm", "moe_lora_workspace_bytes", "moe_lora_checked")]
         ext.bind(*addr, check)
         _ext = ext
     return _ext

@@ -920,9 +920,10 @@ size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows) 
     return lora_workspace(max_rows, cfg->num_adapters, cfg->in_features, cfg->out_features, cfg->rank);
 }
 
-moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b, const float* scale, const void* x,
-                      int64_t x_stride, const int32_t* idx, int32_t n, const void* base, int64_t base_stride, void* out,
-                      int64_t out_stride, void* ws, size_t ws_bytes, moe_stream_t stream) {
+// errors: a control block that keeps the code of a wait that gave up, or null for the workspace's own.
+static moe_status_t lora_impl(const moe_lora_config_t* cfg, const void* a, const void* b, const float* scale, const void* x,
+                              int64_t x_stride, const int32_t* idx, int32_t n, const void* base, int64_t base_stride, void* out,
+                              int64_t out_stride, void* ws, size_t ws_bytes, Ctrl* errors, moe_stream_t stream) {
     const moe_status_t s = check_lora(cfg);
     if (s != MOE_OK) return s;
     const int K = cfg->in_features, O = cfg->out_features;
@@ -948,6 +949,7 @@ moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b
     p.x = static_cast<const uint16_t*>(x);
     p.x_host = at_x == 1;
     p.out_host = at_out == 1 || at_base == 1;
+    p.err = errors ? &errors->err : nullptr;
     p.idx = idx;
     p.base = base;
     p.out = out;
@@ -955,6 +957,21 @@ moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b
     p.n = n; p.K = K; p.O = O; p.r = cfg->rank; p.L = cfg->num_adapters; p.out_type = cfg->out_type;
     return launch_lora(p, cfg->x_type, ws, device_sm_count(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b, const float* scale, const void* x,
+                      int64_t x_stride, const int32_t* idx, int32_t n, const void* base, int64_t base_stride, void* out,
+                      int64_t out_stride, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    return lora_impl(cfg, a, b, scale, x, x_stride, idx, n, base, base_stride, out, out_stride, ws, ws_bytes, nullptr, stream);
+}
+
+moe_status_t moe_lora_checked(const moe_lora_config_t* cfg, const void* a, const void* b, const float* scale, const void* x,
+                              int64_t x_stride, const int32_t* idx, int32_t n, const void* base, int64_t base_stride, void* out,
+                              int64_t out_stride, void* ws, size_t ws_bytes, void* errors, moe_stream_t stream) {
+    if (!errors) return MOE_ERR_NULL;
+    if (!aligned16(errors)) return MOE_ERR_ALIGNMENT;
+    return lora_impl(cfg, a, b, scale, x, x_stride, idx, n, base, base_stride, out, out_stride, ws, ws_bytes, static_cast<Ctrl*>(errors),
+                     stream);
 }
 
 moe_status_t moe_workspace_check(void* ws, size_t ws_bytes, int32_t* device_error, moe_stream_t stream) {

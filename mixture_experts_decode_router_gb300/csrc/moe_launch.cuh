@@ -225,6 +225,7 @@ struct LoraParams {
     int64_t x_stride, base_stride, out_stride;
     int n, K, O, r, L, out_type;
     bool x_host, out_host;     // x; base or out: it is pinned host memory
+    int32_t* err;              // where a bounded wait that gives up leaves its code; no output while one is there.  Null: in the workspace
     // Set by launch_lora.
     int vec;                   // elements of base's and out's rows that can be read at once: 8, 4 or 1
     bool copy;                 // rows without an adapter are to be written
@@ -232,7 +233,7 @@ struct LoraParams {
     // The rows sorted by adapter, or null: runs (adapter, or -1 for none; first position; rows), the
     // runs of adapters before those of none.  ctrl->n_active runs of adapters, n_rsegs in all.
     const int32_t *segs, *perm;
-    const Ctrl* ctrl;
+    Ctrl* ctrl;
 };
 size_t lora_workspace(int64_t n, int L, int K, int O, int r);
 cudaError_t launch_lora(const LoraParams& p, int x_type, void* ws, int num_sms, cudaStream_t st);
@@ -246,8 +247,7 @@ inline int64_t lora_part_rows(int64_t n) {   // of splits * n, and of every smal
 // Whether the tensor maps of a call can be made; `maps` receives them (x by
 // single rows, A, B, x by 32 rows, B by pairs of rows).
 bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[5]);
-cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[5], float* part, int32_t* err, int max_segs,
-                           cudaStream_t st);
+cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[5], float* part, int max_segs, cudaStream_t st);
 
 // tile: routes of a segment at most.
 cudaError_t launch_group(const int32_t* idx, int nk, int E, int tile, int e_begin, int e_end, int32_t* counts,

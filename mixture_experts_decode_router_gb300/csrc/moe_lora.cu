@@ -409,10 +409,12 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraParams p)
 }
 
 // The rows sorted by adapter (stable), those of no adapter last, by one block: each warp counts and
-// then places a stretch of the rows, 32 at a time, the equal ones among them found by a match.
+// then places a stretch of the rows, 32 at a time, the equal ones among them found by a match.  No runs for the
+// kernels behind it while `pending` (or null) has an error.
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kBatch = 8;
 __global__ void __launch_bounds__(kSortThreads)
-lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_t* __restrict__ perm, int32_t* __restrict__ segs, Ctrl* ctrl) {
+lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_t* __restrict__ perm, int32_t* __restrict__ segs, Ctrl* ctrl,
+                 const int32_t* pending) {
     // cnt[e][w]: adapter e's rows (e = L: no adapter's) in warp w's stretch, then those before them;
     // total[e]: e's rows; first[e]: their first position.
     extern __shared__ int32_t cnt[];
@@ -423,6 +425,7 @@ lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_
     __syncthreads();
     pdl_wait();
     pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
+    const bool stop = tid == 0 && pending && *pending != 0;
     const int per = (int)(((int64_t)n + kSortThreads - 1) / kSortThreads) * 32;
     const int64_t begin = (int64_t)warp * per, end = min((int64_t)n, begin + per);
     int ev[kBatch];
@@ -495,8 +498,8 @@ lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_
     for (int i = tid; i < runs; i += kSortThreads) write_run(s_all[1] + i, -1, s_all[0] + i * tile, none - i * tile);
     if (tid == 0) {
         first[L] = s_all[0];
-        ctrl->n_active = s_all[1];
-        ctrl->n_rsegs = s_all[1] + runs;
+        ctrl->n_active = stop ? 0 : s_all[1];
+        ctrl->n_rsegs = stop ? 0 : s_all[1] + runs;
         ctrl->err = 0;
     }
     __syncthreads();
@@ -632,7 +635,7 @@ Layout layout(int64_t n, int L, int K, int O, int r) {
     return l;
 }
 
-cudaError_t launch_sort(const LoraParams& p, int tile, int32_t* perm, int32_t* segs, Ctrl* ctrl, cudaStream_t st) {
+cudaError_t launch_sort(const LoraParams& p, int tile, int32_t* perm, int32_t* segs, const int32_t* pending, cudaStream_t st) {
     const size_t smem = sizeof(int32_t) * (p.L + 1) * (kSortWarps + 2);
     static std::mutex mu;
     static bool configured[128] = {};
@@ -647,7 +650,7 @@ cudaError_t launch_sort(const LoraParams& p, int tile, int32_t* perm, int32_t* s
             configured[dev] = true;
         }
     }
-    return launch_pdl(lora_sort_kernel, dim3(1), dim3(kSortThreads), smem, st, p.idx, p.n, p.L, tile, perm, segs, ctrl);
+    return launch_pdl(lora_sort_kernel, dim3(1), dim3(kSortThreads), smem, st, p.idx, p.n, p.L, tile, perm, segs, p.ctrl, pending);
 }
 
 }  // namespace
@@ -676,15 +679,16 @@ cudaError_t launch_lora(const LoraParams& given, int x_type, void* ws, int num_s
     uint8_t* w = static_cast<uint8_t*>(ws);
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(w);
     p.ctrl = ctrl;
+    if (!p.err) p.err = &ctrl->err;
     p.segs = reinterpret_cast<int32_t*>(w + l.segs);
     p.perm = reinterpret_cast<int32_t*>(w + l.perm);
     CUtensorMap maps[5];
     const bool tc = !p.x_host && lora_maps(p, x_type, maps);
     const int tile = tc ? kLoraTile : kRows;
-    if ((e = launch_sort(p, tile, reinterpret_cast<int32_t*>(w + l.perm), reinterpret_cast<int32_t*>(w + l.segs), ctrl, st)) != cudaSuccess)
+    if ((e = launch_sort(p, tile, reinterpret_cast<int32_t*>(w + l.perm), reinterpret_cast<int32_t*>(w + l.segs), given.err, st)) != cudaSuccess)
         return e;
     const int max_segs = (int)(p.n / tile + std::min(p.n, p.L + 1) + 1);
-    e = tc ? launch_lora_tc(p, x_type, maps, reinterpret_cast<float*>(w + l.part), &ctrl->err, max_segs, st)
+    e = tc ? launch_lora_tc(p, x_type, maps, reinterpret_cast<float*>(w + l.part), max_segs, st)
            : launch_all(p, x_type, max_segs, 4, st);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

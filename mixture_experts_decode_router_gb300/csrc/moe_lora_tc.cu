@@ -45,7 +45,6 @@ struct TcArgs {
     int expand_blocks;
     bool summed;      // v's parts have been added into the first
     float* part;      // [splits][n][r]
-    int32_t* err;
 };
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
@@ -210,7 +209,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
         if (warp == 1) {
             const uint32_t idesc = ptx::idesc_f16(kM, g.N, kBf16);
             for (int j = 0; j < nj; ++j, next()) {
-                if (!wait_warp(&full[slot], phase, s_abort, g.err, 32)) break;
+                if (!wait_warp(&full[slot], phase, s_abort, p.err, 32)) break;
                 ptx::tc_fence_after();
                 if (ptx::elect_one()) {
                     const uint64_t a = ptx::sw128_desc(ptx::smem_u32(smem + slot * stage_bytes));
@@ -227,7 +226,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
             if (warp > 1) f.start(p.perm, first, 32 * (warp - 2), count);
             const uint32_t bytes = warp == 0 ? g.N * kBox * 2 : f.bytes();
             for (int j = 0; j < nj; ++j, next()) {
-                if (used && !wait_warp(&empty[slot], phase ^ 1, s_abort, g.err, 31)) break;
+                if (used && !wait_warp(&empty[slot], phase ^ 1, s_abort, p.err, 31)) break;
                 uint8_t* at = smem + slot * stage_bytes;
                 if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(&full[slot], bytes);
@@ -239,7 +238,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
             }
         }
         __syncwarp();
-        if (wait_warp(done, unit_no & 1, s_abort, g.err, 33)) {
+        if (wait_warp(done, unit_no & 1, s_abort, p.err, 33)) {
             ptx::tc_fence_after();
             const int q = warp & 3, row = 32 * q + lane;     // (the quarter of tensor memory that the warp can read)
             float* to = g.part + ((int64_t)piece * p.n + first + row) * p.r;
@@ -260,6 +259,8 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_consta
         ptx::tc_fence_after();
     }
     // After a wait that gave up, copies may be in flight: they end before the block does.
+    // The expansion finds no runs, and so writes nothing of a v that is not there.
+    if (*s_abort && threadIdx.x == 0) p.ctrl->n_rsegs = 0;
     if (*s_abort && threadIdx.x == 0)
         for (int s = 0; s < g.stages; ++s) ptx::mbar_wait_quiet(&full[s], phase, ptx::kWaitLimitNs / 8);
     ptx::tc_fence_before();
@@ -497,7 +498,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                 }
                 for (int i = 0; i < nt; ++i) {
                     const int buf = (done_tiles + i) & 1;
-                    if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) return;
+                    if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, p.err, 37)) return;
                     ptx::tc_fence_after();
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
@@ -577,7 +578,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                             if (c < lim - kV * whole) one[t] = load_bits<kOut>(p.base, at + (c < head ? c : kV * whole + c));
                         }
                     }
-                    if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, g.err, 37)) return;
+                    if (!wait_warp(&tfull[buf], ((done_tiles + i) >> 1) & 1, s_abort, p.err, 37)) return;
                     ptx::tc_fence_after();
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
@@ -635,7 +636,7 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                 int sent = done_tiles;
                 for (int i = 0; i < nt; ++i, ++sent) {
                     const int s = sent % kRing;
-                    if (sent >= kRing && !wait_warp(&bempty[s], (sent / kRing - 1) & 1, s_abort, g.err, 34)) break;
+                    if (sent >= kRing && !wait_warp(&bempty[s], (sent / kRing - 1) & 1, s_abort, p.err, 34)) break;
                     if (lane == 0) {
                         ptx::mbar_arrive_expect_tx(&bfull[s], vbytes);
                         const int row = adapter * O + (t0 + i) * kNT;
@@ -661,8 +662,8 @@ lora_expand_kernel(const __grid_constant__ CUtensorMap bmap, const TcArgs g) {
                 const uint64_t a_desc = ptx::sw128_desc(ptx::smem_u32(sV)), b_desc = ptx::sw128_desc(ptx::smem_u32(sB));
                 for (int i = 0; i < nt; ++i) {
                     const int at = done_tiles + i, s = at % kRing, buf = at & 1;
-                    if (!wait_warp(&bfull[s], (at / kRing) & 1, s_abort, g.err, 35)) break;
-                    if (at >= 2 && !wait_warp(&tempty[buf], (at / 2 - 1) & 1, s_abort, g.err, 36)) break;
+                    if (!wait_warp(&bfull[s], (at / kRing) & 1, s_abort, p.err, 35)) break;
+                    if (at >= 2 && !wait_warp(&tempty[buf], (at / 2 - 1) & 1, s_abort, p.err, 36)) break;
                     ptx::tc_fence_after();
                     if (ptx::elect_one()) {
                         uint32_t more = 0;
@@ -730,8 +731,7 @@ bool lora_maps(const LoraParams& p, int x_type, CUtensorMap (&maps)[5]) {
            make_map_pairs(&maps[4], p.b, t, p.r, (uint64_t)p.L * p.O, p.out_type == MOE_F32 ? 4 : 8);
 }
 
-cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[5], float* part, int32_t* err, int max_segs,
-                           cudaStream_t st) {
+cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&maps)[5], float* part, int max_segs, cudaStream_t st) {
     TcArgs g{};
     g.p = p;
     g.N = (p.r + 15) / 16 * 16;
@@ -742,7 +742,6 @@ cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&
     // 2048, rank 16, 26.6 and 28.2).
     g.summed = p.r > 16;
     g.max_splits = (int)std::min<int64_t>(kLoraMaxSplits, lora_part_rows(p.n) / p.n);
-    g.err = err;
     const int stage = kBoxBytes + g.N * kBox * 2;
     g.stages = std::min((p.K + kBox - 1) / kBox, 100 * 1024 / stage);
     g.tmem_cols = 32;

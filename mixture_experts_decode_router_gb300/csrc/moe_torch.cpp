@@ -26,7 +26,7 @@ decltype(&moe_experts) g_experts;
 decltype(&moe_forward) g_forward;
 decltype(&moe_norm) g_norm;
 decltype(&moe_lora_workspace_bytes) g_lora_workspace_bytes;
-decltype(&moe_lora) g_lora;
+decltype(&moe_lora_checked) g_lora;
 PyObject* g_check;   // raises a status's error
 
 struct Raised {};    // a Python exception is set
@@ -108,7 +108,7 @@ void need(Py_ssize_t got, Py_ssize_t want) {
     if (got != want) raise(PyExc_TypeError, "wrong number of arguments");
 }
 
-// bind(moe_topk, moe_matvec, moe_experts, moe_forward, moe_norm, moe_lora_workspace_bytes, moe_lora, check): the
+// bind(moe_topk, moe_matvec, moe_experts, moe_forward, moe_norm, moe_lora_workspace_bytes, moe_lora_checked, check): the
 // functions' addresses.
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
     need(n, 8);
@@ -375,13 +375,13 @@ PyObject* norm(PyObject* const* a, Py_ssize_t na) {
     return Py_BuildValue("(NNNN)", give(y, a[6]), give(ro, a[5]), give(q, a[7]), give(s, a[8]));
 }
 
-// lora(config address, (a, b, scale or None), the adapters' device, x, idx, base or None, out or None, stream or None) -> out
+// lora(config address, (a, b, scale or None, errors), the adapters' device, x, idx, base or None, out or None, stream or None) -> out
 PyObject* lora(PyObject* const* a, Py_ssize_t na) {
     need(na, 8);
     const moe_lora_config_t* c = address<const moe_lora_config_t>(a[0]);
-    if (!PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[1]) != 3) raise(PyExc_TypeError, "three matrices are expected");
+    if (!PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[1]) != 4) raise(PyExc_TypeError, "four tensors are expected");
     const at::Tensor &wa = some_tensor(PyTuple_GET_ITEM(a[1], 0)), &wb = some_tensor(PyTuple_GET_ITEM(a[1], 1)),
-                     *scale = tensor(PyTuple_GET_ITEM(a[1], 2));
+                     *scale = tensor(PyTuple_GET_ITEM(a[1], 2)), &errors = some_tensor(PyTuple_GET_ITEM(a[1], 3));
     const long long wdev = integer(a[2]);
     const at::Tensor &x = some_tensor(a[3]), &idx = some_tensor(a[4]), *base = tensor(a[5]), *given = tensor(a[6]);
     const int64_t K = c->in_features, O = c->out_features;
@@ -399,7 +399,7 @@ PyObject* lora(PyObject* const* a, Py_ssize_t na) {
         !wa.is_contiguous() || !wb.is_contiguous() ||
         (scale && (scale->scalar_type() != at::kFloat || scale->numel() != L || !scale->is_contiguous())))
         raise(PyExc_ValueError, "the adapters are no longer what the operator was made with");
-    if (wdev != dev || wa.get_device() != dev || wb.get_device() != dev || (scale && scale->get_device() != dev))
+    if (wdev != dev || wa.get_device() != dev || wb.get_device() != dev || (scale && scale->get_device() != dev) || errors.get_device() != dev)
         raise(PyExc_ValueError, "the adapters are not on the current device");
     if (idx.scalar_type() != at::kInt || idx.dim() != 1 || idx.size(0) != n || !idx.is_contiguous() || !idx.is_cuda() ||
         idx.get_device() != dev)
@@ -423,10 +423,11 @@ PyObject* lora(PyObject* const* a, Py_ssize_t na) {
     const void *ap = wa.data_ptr(), *bp = wb.data_ptr(), *xp = x.data_ptr();
     const float* sp = scale ? data<const float>(*scale) : nullptr;
     const int32_t* ip = data<const int32_t>(idx);
+    void* ep = errors.data_ptr();
     const int64_t stride = n > 1 ? x.stride(0) : K;
     moe_status_t s;
     Py_BEGIN_ALLOW_THREADS;
-    s = g_lora(c, ap, bp, sp, xp, stride, ip, (int32_t)n, Y0.p, Y0.stride, Y.p, Y.stride, wp, ws_bytes, st);
+    s = g_lora(c, ap, bp, sp, xp, stride, ip, (int32_t)n, Y0.p, Y0.stride, Y.p, Y.stride, wp, ws_bytes, ep, st);
     Py_END_ALLOW_THREADS;
     check(s);
     return wrap(std::move(out));

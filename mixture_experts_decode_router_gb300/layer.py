@@ -332,6 +332,9 @@ class MoeLora:
     ``x`` ``[n, in]`` is; ``scale`` is fp32 ``[adapters]`` or None (1).  ``idx`` is int32
     ``[n]``.  ``base`` is the projection's ``[n, out]`` of ``out_dtype`` or None (0);
     ``out=base`` adds in place.  Rows may be strided.
+
+    ``device_error()`` says whether a bounded wait of the kernels for many rows gave up since it was
+    last asked (0: none); until then those write no output.
     """
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16):
@@ -348,7 +351,10 @@ class MoeLora:
         c.out_features, c.x_type, c.out_type = b.shape[1], _TYPE[a.dtype], _TYPE[out_dtype]
         if B.moe_lora_workspace_bytes(c, 0) == 0:
             raise B.MoeError("invalid adapters: the rank is a multiple of 8 up to 128, in of 8, and there are at most 1024")
-        self.c_cfg, self._held, self.out_dtype, self._device = c, (a, b, scale), out_dtype, dev
+        errors = torch.zeros(256, dtype=torch.uint8, device=a.device)
+        if a.is_cuda and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(a.device).synchronize()       # zeros for calls on every stream
+        self.c_cfg, self._held, self.out_dtype, self._device = c, (a, b, scale, errors), out_dtype, dev
         self._lora = B.tensor_calls().lora
 
     @property
@@ -362,6 +368,12 @@ class MoeLora:
     @property
     def scale(self) -> Optional[torch.Tensor]:
         return self._held[2]
+
+    def device_error(self, stream=None) -> int:
+        """Reads and clears the word that a wait that gave up leaves its code in (31 to 37; syncs the stream)."""
+        s, v = B.moe_workspace_check(self._held[3], 256, stream)
+        B.check(s)
+        return v
 
     def forward(self, x: torch.Tensor, idx: torch.Tensor, base: Optional[torch.Tensor] = None, out=None, stream=None):
         return self._lora(addressof(self.c_cfg), self._held, self._device, x, idx, base, out,

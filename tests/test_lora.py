@@ -56,6 +56,14 @@ def test_refusals():
         assert _call(**kw) == B.MOE_ERR_HOST_MEMORY, kw
 
 
+def test_refusals_of_the_checked_call():
+    def call(errors, n=3):
+        return B.moe_lora_checked(_config(), FAKE, FAKE + MB, None, FAKE + 2 * MB, 64, FAKE + 3 * MB, n, None, 0, FAKE + 5 * MB, 48, FAKE + 6 * MB,
+                                  1 << 30, errors, 0)
+    assert call(None) == B.MOE_ERR_NULL and call(FAKE + 7 * MB + 8) == B.MOE_ERR_ALIGNMENT
+    assert call(FAKE + 7 * MB) == B.MOE_ERR_HOST_MEMORY and call(FAKE + 7 * MB, 0) == B.MOE_OK and call(FAKE + 7 * MB, -1) == B.MOE_ERR_INVALID_CONFIG
+
+
 def test_workspace_bytes():
     assert ctypes.sizeof(B.moe_lora_config_t) == 24
     assert B.moe_lora_workspace_bytes(None, 1) == 0 and B.moe_lora_workspace_bytes(_config(), -1) == 0
