@@ -488,7 +488,7 @@ cudaError_t launch_types(const NormParams& p, bool chunks, int num_sms, cudaStre
     auto threads = [&](int ch) { return ((n8 + ch - 1) / ch + 31) / 32 * 32; };
     auto go = [&](auto kern, int ch) {
         const int T = threads(ch), rows = T == 32 ? std::min(p.n, 8) : 1;
-        launch_pdl(kern, dim3((unsigned)((p.n + rows - 1) / rows)), dim3(T, rows), 0, st, p);
+        launch_pdl(kern, dim3((unsigned)(((int64_t)p.n + rows - 1) / rows)), dim3(T, rows), 0, st, p);
         return cudaGetLastError();
     };
     // Chunks of a thread: one while the rows' threads all run at once, else as many as its registers

@@ -332,6 +332,22 @@ def test_scales_and_codes_are_quotients(lib, x, r, out8, n, H):
 
 
 @gpu
+def test_as_many_rows_as_there_can_be(lib):
+    """2^31 - 1 rows: the blocks that take eight rows each are still counted right."""
+    n = (1 << 31) - 1
+    try:
+        x = torch.empty(n, 1, dtype=BF, device="cuda").fill_(2.0)
+        out = torch.empty(n, 1, dtype=BF, device="cuda")
+    except torch.OutOfMemoryError:
+        pytest.skip("needs 9 GB")
+    x[-1], x[n // 2], x[0] = -3.0, -0.5, 0.0
+    MoeNorm(torch.full((1,), 4.0, device="cuda")).forward(x, out=out)
+    for at, want in ((-1, -4.0), (n // 2, -4.0), (0, 0.0), (1, 4.0), (-2, 4.0)):
+        assert out[at].item() == want
+    assert all(bool((part[part != -4] == 4).all()) for part in out[1:].split(1 << 28))
+
+
+@gpu
 @pytest.mark.parametrize("H", [96, 2048])
 def test_special_values_stay_in_their_row(lib, H):
     x, r = rows(8, H), rows(8, H, seed=2)
