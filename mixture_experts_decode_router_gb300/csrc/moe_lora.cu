@@ -461,7 +461,7 @@ lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_
     }
     __syncthreads();
     // First position and first run of each adapter (L <= 1024, one a thread).
-    const int c = tid < L ? total[tid] : 0, g = (c + tile - 1) / tile;
+    const int c = tid < L ? total[tid] : 0, g = c / tile + (c % tile != 0);   // (c + tile may pass 2^31)
     int sc = c, sg = g;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
