@@ -523,10 +523,11 @@ size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows);
  *   base        device [n, out_features], rows base_stride elements apart, or
  *               NULL (zeros); may be out itself
  *   out         device [n, out_features] (out), rows out_stride elements apart;
- *               overlaps neither x nor (unless it is base) base, from the first
+ *               overlaps nothing else but base where it is that, from the first
  *               row to the last
  *   ws          device workspace (16-byte aligned) of at least
- *               moe_lora_workspace_bytes(cfg, n) bytes; it need not be cleared,
+ *               moe_lora_workspace_bytes(cfg, n) bytes, of which no other
+ *               argument has any; it need not be cleared,
  *               and keeps nothing between calls but the error word of the last,
  *               for moe_workspace_check (256 bytes: it is not used, and may be
  *               any address).  Where the products of v gave up, out is not written;

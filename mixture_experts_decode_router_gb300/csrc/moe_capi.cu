@@ -938,8 +938,17 @@ static moe_status_t lora_impl(const moe_lora_config_t* cfg, const void* a, const
         if (r->p && (r->stride < r->cols || r->stride > kMaxStride)) return MOE_ERR_INVALID_CONFIG;
     if (!aligned16(x) || x_stride % 8 || begin_of(Y0) % osize || begin_of(Y) % osize || !aligned4(idx) || !aligned16(ws))
         return MOE_ERR_ALIGNMENT;
-    if (overlap(X, Y) || (overlap(Y0, Y) && !same_rows(Y0, Y))) return MOE_ERR_ALIAS;
-    if (ws_bytes < lora_workspace(n, cfg->num_adapters, K, O, cfg->rank)) return MOE_ERR_WORKSPACE;
+    const size_t ws_need = lora_workspace(n, cfg->num_adapters, K, O, cfg->rank);
+    if (ws_bytes < ws_need) return MOE_ERR_WORKSPACE;
+    // What the kernels write, on its own but for out in place of base.  (A workspace of the control block alone is
+    // not written.)
+    const int64_t L = cfg->num_adapters, r = cfg->rank;
+    auto run = [](const void* q, int64_t count, size_t size) { return RowsArg{q, count, 1, count, size}; };
+    const RowsArg W = run(ws_need > sizeof(Ctrl) ? ws : nullptr, (int64_t)ws_need, 1);
+    if (overlap(Y0, Y) && !same_rows(Y0, Y)) return MOE_ERR_ALIAS;
+    if (overlap(Y, W) || overlap(Y0, W)) return MOE_ERR_ALIAS;
+    for (const RowsArg& q : {X, run(a, L * r * K, 2), run(b, L * r * O, 2), run(scale, L, 4), run(idx, n, 4), run(errors, sizeof(Ctrl), 1)})
+        if (overlap(q, Y) || overlap(q, W)) return MOE_ERR_ALIAS;
     const int at_x = residency(x), at_out = residency(out), at_base = base ? residency(base) : 0;
     if (at_x < 0 || at_out < 0 || at_base < 0) return MOE_ERR_HOST_MEMORY;
     LoraParams p{};

@@ -56,6 +56,21 @@ def test_refusals():
         assert _call(**kw) == B.MOE_ERR_HOST_MEMORY, kw
 
 
+def test_outputs_over_other_arguments():
+    """The adapters have 8 and 6 KB, scales 16 bytes, indexes 20000, out 480 KB; the workspace its size."""
+    need = B.moe_lora_workspace_bytes(_config(), 5000)
+    ws = FAKE + 6 * MB
+    for kw in (dict(out=FAKE), dict(out=FAKE + 8190), dict(out=FAKE + MB + 6142), dict(scale=FAKE + 5 * MB), dict(scale=FAKE + 5 * MB + 479996),
+               dict(out=FAKE + 3 * MB), dict(out=FAKE + 3 * MB + 19998), dict(out=ws + need - 2), dict(ws=FAKE + 5 * MB - 16), dict(a=ws), dict(b=ws + 16),
+               dict(scale=ws + need - 4), dict(idx=ws), dict(x=ws), dict(base=ws)):
+        assert _call(**{**dict(n=5000, ws_bytes=need), **kw}) == B.MOE_ERR_ALIAS, kw
+    # A workspace of 256 bytes is not used.
+    for kw in (dict(ws=FAKE), dict(ws=FAKE + 5 * MB), dict(out=FAKE + 8192, ws=FAKE + 8192)):
+        assert _call(**kw) == B.MOE_ERR_HOST_MEMORY, kw
+    for kw in (dict(out=FAKE + 8192), dict(out=FAKE + 3 * MB + 20000), dict(scale=FAKE + 5 * MB + 480000), dict(base=ws + (need + 255) // 256 * 256)):
+        assert _call(**{**dict(n=5000, ws_bytes=need), **kw}) == B.MOE_ERR_HOST_MEMORY, kw
+
+
 def test_refusals_of_the_checked_call():
     def call(errors, n=3):
         return B.moe_lora_checked(_config(), FAKE, FAKE + MB, None, FAKE + 2 * MB, 64, FAKE + 3 * MB, n, None, 0, FAKE + 5 * MB, 48, FAKE + 6 * MB,
