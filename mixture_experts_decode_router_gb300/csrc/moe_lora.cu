@@ -524,30 +524,37 @@ lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_
 template <bool kBf16, int kRT, int kParts, bool kInGroups>
 cudaError_t launch_clusters(const LoraParams& p, int groups, int cluster, cudaStream_t st) {
     auto kern = lora_rows_kernel<kBf16, kRT, kParts, kInGroups>;
-    if (cluster > 8) {   // (more than every GPU has to offer: to be asked for)
-        static std::mutex mu;
-        static bool configured[128] = {};
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
-        std::lock_guard<std::mutex> lock(mu);
-        if (!configured[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return e;
-            configured[dev] = true;
-        }
-    }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)groups * cluster);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    auto blocks = [&](int of) {
+        cfg.gridDim = dim3((unsigned)groups * of);
+        attr[1].val.clusterDim.x = of;
+    };
+    if (cluster > 8) {   // (more than every GPU has to offer: to be asked for; eight blocks where there is no place for them)
+        static std::mutex mu;
+        static int fits[128] = {};   // 0: not known; -1: no; 1: yes
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!fits[dev]) {
+            int at_once = 0;
+            blocks(16);
+            fits[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                                cudaOccupancyMaxActiveClusters(&at_once, kern, &cfg) == cudaSuccess && at_once > 0
+                            ? 1 : -1;
+            if (fits[dev] < 0) cudaGetLastError();   // (no error of the launch)
+        }
+        if (fits[dev] < 0) cluster = 8;
+    }
+    blocks(cluster);
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
