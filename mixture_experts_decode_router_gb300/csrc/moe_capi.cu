@@ -964,7 +964,7 @@ static moe_status_t lora_impl(const moe_lora_config_t* cfg, const void* a, const
     p.out = out;
     p.x_stride = x_stride; p.base_stride = base_stride; p.out_stride = out_stride;
     p.n = n; p.K = K; p.O = O; p.r = cfg->rank; p.L = cfg->num_adapters; p.out_type = cfg->out_type;
-    return launch_lora(p, cfg->x_type, ws, device_sm_count(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch_lora(p, cfg->x_type, ws, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -236,10 +236,12 @@ struct LoraParams {
     Ctrl* ctrl;
 };
 size_t lora_workspace(int64_t n, int L, int K, int O, int r);
-cudaError_t launch_lora(const LoraParams& p, int x_type, void* ws, int num_sms, cudaStream_t st);
+cudaError_t launch_lora(const LoraParams& p, int x_type, void* ws, cudaStream_t st);
 // Runs of at most 128 rows through the tensor cores' kernels, v's partial sums [splits][n][r] in part.
 constexpr int kLoraTile = 128;
-constexpr int kLoraBlocks = 304;      // blocks that a call aims at
+// Blocks that a call aims at: two on each of GB300's 152 SMs.  (A constant, since the size of a workspace follows from it: on a
+// GPU of fewer SMs blocks wait for their turn.)
+constexpr int kLoraBlocks = 304;
 constexpr int kLoraMaxSplits = 8;
 inline int64_t lora_part_rows(int64_t n) {   // of splits * n, and of every smaller n's
     return std::min<int64_t>(kLoraMaxSplits * n, (int64_t)kLoraBlocks * kLoraTile + 2 * n);

@@ -621,7 +621,7 @@ int cluster_blocks(int n, int64_t bytes) {
 // 143 of 378 KB 19.8, 25.5, 37, 82.)
 int group_blocks(int groups, int64_t bytes, int r) {
     const bool large = bytes >= 256 << 10;
-    if (large && groups * 16 <= 152) return 16;
+    if (large && groups * 16 <= kLoraBlocks / 2) return 16;
     if (groups * 8 <= (large && r <= 32 ? 400 : 240)) return 8;
     return groups <= 100 ? 4 : 2;
 }
@@ -664,7 +664,7 @@ cudaError_t launch_sort(const LoraParams& p, int tile, int32_t* perm, int32_t* s
 
 size_t lora_workspace(int64_t n, int L, int K, int O, int r) { return layout(n, L, K, O, r).total; }
 
-cudaError_t launch_lora(const LoraParams& given, int x_type, void* ws, int num_sms, cudaStream_t st) {
+cudaError_t launch_lora(const LoraParams& given, int x_type, void* ws, cudaStream_t st) {
     LoraParams p = given;
     const int size = p.out_type == MOE_F32 ? 4 : 2;
     auto rows_of = [&](int v, const void* a, int64_t stride) {

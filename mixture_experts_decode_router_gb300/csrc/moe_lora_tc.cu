@@ -755,7 +755,7 @@ cudaError_t launch_lora_tc(const LoraParams& p, int x_type, const CUtensorMap (&
         return e;
 
     if (g.summed &&
-        (e = launch_pdl(lora_sum_kernel, dim3((unsigned)std::min<int64_t>(8 * 152, ((int64_t)p.n * p.r / 4 + kSumThreads - 1) / kSumThreads)),
+        (e = launch_pdl(lora_sum_kernel, dim3((unsigned)std::min<int64_t>(4 * kLoraBlocks, ((int64_t)p.n * p.r / 4 + kSumThreads - 1) / kSumThreads)),
                         dim3(kSumThreads), 0, st, g)) != cudaSuccess)
         return e;
     const bool f32 = p.out_type == MOE_F32, bf = x_type == MOE_BF16;
