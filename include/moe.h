@@ -468,7 +468,8 @@ typedef struct {
  *   y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset)      (fp32)
  *   residual_out = h;  out = y, rounded to out_type;
  *   scale8[g] = max(max |y| / 448, 2^-126) over the group g;  out8 = E4M3(y / scale8[g])
- *   (y is what an fp32 out holds, before any rounding to 16 bits; both are quotients of fp32, codes to nearest even)
+ *   (scale8 from y as an fp32 out holds it; codes, to nearest even, from h (weight + weight_offset) and its largest,
+ *   which the root does not enter: of 16-bit h and weights as exact arithmetic has them)
  *   x, residual     device [n, H]; residual may be NULL
  *   weight          device [H], or NULL (1)
  *   residual_out    device [n, H] (out), or NULL; may be residual itself

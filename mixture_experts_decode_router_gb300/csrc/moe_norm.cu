@@ -30,6 +30,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512, kWideThreads = 1024;   // of a row at most
+constexpr int kNoCodes = 0, kRow = 1, kGroups = 2;   // out8's scales: none, of the row, of 128 elements
 
 __host__ __device__ constexpr int size_of(int type) { return type == MOE_F32 ? 4 : 2; }
 
@@ -218,27 +219,32 @@ __device__ __forceinline__ float max_abs(float m, float v) {
     return r;
 }
 
-// The scale of values whose largest magnitude has the bits `most`: their 448th part (the quotient: a product with
-// 1 / 448 is another number for half of all magnitudes, and is corrected by what it leaves of m: Markstein, 1990),
-// at least 2^-126, so that its reciprocal is finite; an infinity's or NaN's is itself, and the values it scales read
-// as NaN.
-__device__ __forceinline__ float scale_of(uint32_t most) {
-    const float m = __uint_as_float(most), q = m * (1.f / 448.f);
-    return most >= kInfBits ? m : fmaxf(fmaf(fmaf(q, -448.f, m), 1.f / 448.f, q), 0x1p-126f);
-}
-// 1 / s of a scale (2^-126 to 2^120, or as above) as a sum of two fp32, off by some 2^-46 of it: a product with it is
-// the quotient rounded once (but for quotients that near to the middle of two fp32).  One with its first part alone
-// is off by steps of fp32, which take a code that lies at a border to the other side of it (2200 of 8192 x 7168;
-// 69.2 us so and 70.2 with both).
-struct Reciprocal {
+// A group's scale, and what takes values to their codes' quotients by it.  y is t times the root's part m in [1, 2), so
+// y / (max |y| / 448) is t times 448 / max |t|, which m does not enter: from t, whose products of 16-bit numbers are
+// exact, a quotient at a border of E4M3 falls as exact arithmetic has it.  (A row of 16-bit elements has many there: from y
+// and the scale, each rounded, some 5400 of 8192 x 7168 codes were the neighbouring ones, and none so.)  The scale is the
+// quotient of y's largest (a product with 1 / 448 is another number for half of all magnitudes, and is corrected by what it
+// leaves: Markstein, 1990); the factor is a sum of two fp32, off by some 2^-46 of it, so that a product with it is
+// rounded once.  (Selects for the rare scales: with branches 8192 x 7168 took 1.5 us more.)
+struct Factor {
+    float scale;
     float2 hi, lo;
-    __device__ __forceinline__ explicit Reciprocal(float s) {
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    __device__ __forceinline__ Factor(float top, float m) {      // top: max |t|
+        const float v = top * m, q = v * (1.f / 448.f), s = fmaf(fmaf(q, -448.f, v), 1.f / 448.f, q);
+        scale = v < INFINITY ? fmaxf(s, 0x1p-126f) : v;
+        float up = 1.f, r;
+        if (scale < 0x1p-100f) up = 0x1p64f;     // (what r is taken of stays above fp32's smallest)
+        top *= up;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(top * (1.f / 448.f)));
+        float rest = fmaf(-top, r, 448.f) * (1.f / 448.f) * r;
+        if (!(top < INFINITY)) rest = 0.f;       // (a number by an infinity is 0)
+        r *= up;
+        rest *= up;
+        if (scale == 0x1p-126f) r = m * 0x1p126f, rest = 0.f;      // the smallest scale there is: y 2^126
         hi = both(r);
-        lo = both(s < INFINITY ? fmaf(-s, r, 1.f) * r : 0.f);
+        lo = both(rest);
     }
-    __device__ __forceinline__ float2 times(float2 v) const { return __ffma2_rn(v, hi, __fmul2_rn(v, lo)); }
+    __device__ __forceinline__ float2 times(float2 t) const { return __ffma2_rn(t, hi, __fmul2_rn(t, lo)); }
 };
 // E4M3 of a pair (x in the low byte), to nearest even; NaN is NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float2 v) {
@@ -273,7 +279,7 @@ template <int N> __device__ __forceinline__ float row_rstd(float ss, float2 (&h)
 // One row from what get(c, xr, rr) gives of chunk c of x and the residual, and weight16(c) of a 16-bit
 // weight.  in[c]: the thread has a chunk c.  live: the row is one (else it only takes part in the
 // reductions).  stage: kAny's, of the warp.
-template <int kX, int kR, int kCh, bool kAny, typename Get, typename Weight16, typename Weight32>
+template <int kX, int kR, int kCh, bool kAny, int kCodes, typename Get, typename Weight16, typename Weight32>
 __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool live, int T, const bool (&in)[kCh], float* red, uint8_t* stage,
                                          Get get, Weight16 weight16, Weight32 weight32) {
     constexpr int kRT = kR < 0 ? kX : kR;
@@ -285,8 +291,8 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
     // kAny: where the warp's chunks c begin, and how many elements they have.
     auto span = [&](int c) { return (c * T + (tid & ~31)) * 8; };
     auto within = [&](int c) { return live ? min(256, p.H - span(c)) : 0; };
-    auto codes = [&](const float2* y, const Reciprocal& r) {
-        return make_uint2(e4m3x2(r.times(y[0])) | e4m3x2(r.times(y[1])) << 16, e4m3x2(r.times(y[2])) | e4m3x2(r.times(y[3])) << 16);
+    auto codes = [&](const float2* t, const Factor& f) {
+        return make_uint2(e4m3x2(f.times(t[0])) | e4m3x2(f.times(t[1])) << 16, e4m3x2(f.times(t[2])) | e4m3x2(f.times(t[3])) << 16);
     };
     float2 h[kCh * 4], ss = make_float2(0.f, 0.f);
 #pragma unroll
@@ -326,7 +332,12 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
             }
         }
     }
-    const float2 rstd = both(row_rstd(ss.x + ss.y, h, p, T, red));
+    // With codes, the root's power of two (exact), and the rest of it, m, only on the way to out and the scales (Factor).
+    const float root = row_rstd(ss.x + ss.y, h, p, T, red);
+    const uint32_t root_bits = __float_as_uint(root);
+    const bool apart = kCodes != kNoCodes && root_bits < kInfBits;
+    const float2 rstd = both(apart ? __uint_as_float(root_bits & kInfBits) : root);
+    const float m = apart ? __uint_as_float((root_bits & ~kInfBits) | 0x3f800000u) : 1.f;
 
     uint32_t top = 0;
 #pragma unroll
@@ -351,29 +362,37 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(y[i], rstd), w[i]);
             if constexpr (kAny) first_of8(y, p.H - at);
-            if (!kAny && p.out) {
+        }
+        if (kCodes == kNoCodes || p.out) {
+            float2 z[4] = {y[0], y[1], y[2], y[3]};
+            if constexpr (kCodes != kNoCodes) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = __fmul2_rn(z[i], both(m));
+            }
+            if constexpr (kAny) {
+                if (within(c) > 0) {
+                    uint8_t* to = reinterpret_cast<uint8_t*>(p.out) + (r0 * p.out_stride + span(c)) * size_of(p.out_type);
+                    if (p.out_type == MOE_F32) put32(to, within(c), z, stage);
+                    else put16(to, within(c), p.out_type == MOE_BF16 ? pack8<MOE_BF16>(z) : pack8<MOE_F16>(z), stage);
+                }
+            } else if (in[c]) {
                 uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + r0 * p.out_stride * size_of(p.out_type);
-                if (p.out_type == MOE_BF16) store8<MOE_BF16>(out, at, y);
-                else if (p.out_type == MOE_F16) store8<MOE_F16>(out, at, y);
-                else store8<MOE_F32>(out, at, y);
+                if (p.out_type == MOE_BF16) store8<MOE_BF16>(out, at, z);
+                else if (p.out_type == MOE_F16) store8<MOE_F16>(out, at, z);
+                else store8<MOE_F32>(out, at, z);
             }
         }
-        if (kAny && p.out && within(c) > 0) {
-            uint8_t* to = reinterpret_cast<uint8_t*>(p.out) + (r0 * p.out_stride + span(c)) * size_of(p.out_type);
-            if (p.out_type == MOE_F32) put32(to, within(c), y, stage);
-            else put16(to, within(c), p.out_type == MOE_BF16 ? pack8<MOE_BF16>(y) : pack8<MOE_F16>(y), stage);
-        }
-        if (p.out8) {
-            float m = 0.f;
+        if constexpr (kCodes != kNoCodes) {
+            float top8 = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = max_abs(max_abs(m, y[i].x), y[i].y);
-            uint32_t most = in[c] ? __float_as_uint(m) : 0u;
-            if (p.group) {
+            for (int i = 0; i < 4; ++i) top8 = max_abs(max_abs(top8, y[i].x), y[i].y);
+            uint32_t most = in[c] ? __float_as_uint(top8) : 0u;
+            if constexpr (kCodes == kGroups) {
 #pragma unroll
                 for (int o = 1; o < 16; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-                const float s = scale_of(most);
-                if (in[c] && (tid & 15) == 0) p.scale8[row * p.n_scales + at / 128] = s;
-                const uint2 q = codes(y, Reciprocal(s));
+                const Factor f(__uint_as_float(most), m);
+                if (in[c] && (tid & 15) == 0) p.scale8[row * p.n_scales + at / 128] = f.scale;
+                const uint2 q = codes(y, f);
                 if constexpr (kAny) {
                     if (within(c) > 0) put8(p.out8 + r0 * p.out8_stride + span(c), within(c), q, stage);
                 } else if (in[c]) {
@@ -384,13 +403,12 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
             }
         }
     }
-    if (p.out8 && !p.group) {
-        const float s = scale_of(row_max(top, T, red + 96));
-        const Reciprocal r(s);
-        if (tid == 0 && live) p.scale8[row] = s;
+    if constexpr (kCodes == kRow) {
+        const Factor f(__uint_as_float(row_max(top, T, red + 96)), m);
+        if (tid == 0 && live) p.scale8[row] = f.scale;
 #pragma unroll
         for (int c = 0; c < kCh; ++c) {
-            const uint2 q = codes(&h[4 * c], r);
+            const uint2 q = codes(&h[4 * c], f);
             if constexpr (kAny) {
                 if (within(c) > 0) put8(p.out8 + r0 * p.out8_stride + span(c), within(c), q, stage);
             } else if (in[c]) {
@@ -400,9 +418,10 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
     }
 }
 
-// kX: type of x.  kR: type of the residual, or -1 for none.  kWide: rows so long that their threads have
+// kX: type of x.  kR: type of the residual, or -1 for none.  kCodes: out8's scales.  (Kernels of their own: with all three
+// in one, 2048 x 7168 without codes took 16.1 us that take 14.6 so, 8192 x 7168 in groups 71.6 that take 68.1.)  kWide: rows so long that their threads have
 // no registers for loads in flight.
-template <int kX, int kR, int kCh, bool kWide, bool kAny>
+template <int kX, int kR, int kCh, bool kWide, bool kAny, int kCodes>
 __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads, kWide || kR == MOE_F32 ? 1 : 2) norm_kernel(const NormParams p) {
     __shared__ float red[4 * 32];
     __shared__ __align__(16) uint8_t staging[kAny ? (kWide ? kWideThreads : kThreads) * 32 : 16];
@@ -464,7 +483,7 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads, kWide || kR =
             if (in[c]) load(c, xr[c], rr[kR < 0 ? 0 : c]);
         if (kCh == 1 && in[0] && p.w && p.w_type != MOE_F32) wr = load_w16(0);
     }
-    norm_row<kX, kR, kCh, kAny>(
+    norm_row<kX, kR, kCh, kAny, kCodes>(
         p, row, live, T, in, red, stage,
         [&](int c, Raw8<kX>& a, Raw8<kRT>& b) {
             if constexpr (kWide) load(c, xr[0], rr[0]);
@@ -482,7 +501,7 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads, kWide || kR =
 
 // ---------------------------------------------------------------- launches
 
-template <int kX, int kR>
+template <int kX, int kR, int kCodes>
 cudaError_t launch_types(const NormParams& p, bool chunks, int num_sms, cudaStream_t st) {
     const int n8 = (p.H + 7) / 8;
     auto threads = [&](int ch) { return ((n8 + ch - 1) / ch + 31) / 32 * 32; };
@@ -501,15 +520,32 @@ cudaError_t launch_types(const NormParams& p, bool chunks, int num_sms, cudaStre
     while (threads(ch) > kThreads) ch *= 2;
     while (ch < most && (int64_t)p.n * threads(ch) > (int64_t)num_sms * 2048) ch *= 2;
     if (!chunks) {
-        if (ch > most) return go(norm_kernel<kX, kR, 4, true, true>, 4);
-        if constexpr (kMostAny == 4) if (ch == 4) return go(norm_kernel<kX, kR, 4, false, true>, 4);
-        return ch == 1 ? go(norm_kernel<kX, kR, 1, false, true>, 1) : go(norm_kernel<kX, kR, 2, false, true>, 2);
+        if (ch > most) return go(norm_kernel<kX, kR, 4, true, true, kCodes>, 4);
+        if constexpr (kMostAny == 4) if (ch == 4) return go(norm_kernel<kX, kR, 4, false, true, kCodes>, 4);
+        return ch == 1 ? go(norm_kernel<kX, kR, 1, false, true, kCodes>, 1) : go(norm_kernel<kX, kR, 2, false, true, kCodes>, 2);
     }
-    if (ch > most) return go(norm_kernel<kX, kR, 4, true, false>, 4);
-    if (ch == 1) return go(norm_kernel<kX, kR, 1, false, false>, 1);
-    if (ch == 2) return go(norm_kernel<kX, kR, 2, false, false>, 2);
-    if constexpr (kMost == 4) return go(norm_kernel<kX, kR, 4, false, false>, 4);
+    if (ch > most) return go(norm_kernel<kX, kR, 4, true, false, kCodes>, 4);
+    if (ch == 1) return go(norm_kernel<kX, kR, 1, false, false, kCodes>, 1);
+    if (ch == 2) return go(norm_kernel<kX, kR, 2, false, false, kCodes>, 2);
+    if constexpr (kMost == 4) return go(norm_kernel<kX, kR, 4, false, false, kCodes>, 4);
     return cudaErrorInvalidValue;
+}
+
+template <int kCodes>
+cudaError_t launch_codes(const NormParams& p, bool chunks, int num_sms, cudaStream_t st) {
+    const bool f32_res = p.res && p.res_type == MOE_F32;
+    switch (p.x_type) {
+        case MOE_F32:
+            return p.res ? launch_types<MOE_F32, MOE_F32, kCodes>(p, chunks, num_sms, st) : launch_types<MOE_F32, -1, kCodes>(p, chunks, num_sms, st);
+        case MOE_BF16:
+            return !p.res ? launch_types<MOE_BF16, -1, kCodes>(p, chunks, num_sms, st)
+                 : f32_res ? launch_types<MOE_BF16, MOE_F32, kCodes>(p, chunks, num_sms, st)
+                           : launch_types<MOE_BF16, MOE_BF16, kCodes>(p, chunks, num_sms, st);
+        default:
+            return !p.res ? launch_types<MOE_F16, -1, kCodes>(p, chunks, num_sms, st)
+                 : f32_res ? launch_types<MOE_F16, MOE_F32, kCodes>(p, chunks, num_sms, st)
+                           : launch_types<MOE_F16, MOE_F16, kCodes>(p, chunks, num_sms, st);
+    }
 }
 
 }  // namespace
@@ -526,19 +562,8 @@ cudaError_t launch_norm(const NormParams& p, int num_sms, cudaStream_t st) {
                         rows16(p.res_out, p.res_out_stride, size_of(p.res_type)) && rows16(p.out, p.out_stride, size_of(p.out_type)) &&
                         rows16(p.w, 0, 0) &&
                         (!p.out8 || (reinterpret_cast<uintptr_t>(p.out8) % 8 == 0 && (p.n == 1 || p.out8_stride % 8 == 0)));
-    const bool f32_res = p.res && p.res_type == MOE_F32;
-    switch (p.x_type) {
-        case MOE_F32:
-            return p.res ? launch_types<MOE_F32, MOE_F32>(p, chunks, num_sms, st) : launch_types<MOE_F32, -1>(p, chunks, num_sms, st);
-        case MOE_BF16:
-            return !p.res ? launch_types<MOE_BF16, -1>(p, chunks, num_sms, st)
-                 : f32_res ? launch_types<MOE_BF16, MOE_F32>(p, chunks, num_sms, st)
-                           : launch_types<MOE_BF16, MOE_BF16>(p, chunks, num_sms, st);
-        default:
-            return !p.res ? launch_types<MOE_F16, -1>(p, chunks, num_sms, st)
-                 : f32_res ? launch_types<MOE_F16, MOE_F32>(p, chunks, num_sms, st)
-                           : launch_types<MOE_F16, MOE_F16>(p, chunks, num_sms, st);
-    }
+    return !p.out8 ? launch_codes<kNoCodes>(p, chunks, num_sms, st)
+         : p.group ? launch_codes<kGroups>(p, chunks, num_sms, st) : launch_codes<kRow>(p, chunks, num_sms, st);
 }
 
 }  // namespace moe

@@ -308,27 +308,45 @@ def test_rows_of_zeros(lib, eps, H):
 
 
 @gpu
-@pytest.mark.parametrize("x,r", [(BF, BF), (HF, F32), (F32, None)])
+@pytest.mark.parametrize("x,r,w", [(BF, BF, BF), (HF, None, BF), (BF, None, HF), (HF, HF, HF), (HF, F32, BF), (F32, None, F32), (BF, BF, F32)])
 @pytest.mark.parametrize("out8", ["group", "row"])
 @pytest.mark.parametrize("n,H", [(64, 7168), (700, 333), (40, 16392)])
-def test_scales_and_codes_are_quotients(lib, x, r, out8, n, H):
-    """Of y as the fp32 output shows it: scale = max |y| / 448 and code = E4M3(y / scale), both rounded once, at every
-    border (a bf16 row's elements lie on many).  Rows of small scales among them."""
-    for w in (weights(H), torch.ones(H, device="cuda")):
-        op = MoeNorm(w, eps=0.0, out_dtype=F32, out8=out8)
-        by = MoeNorm((w.float() * 2.0 ** -80).to(BF), eps=0.0, out_dtype=F32, out8=out8)
-        xv, rv = rows(n, H, x, seed=H), None if r is None else rows(n, H, r, seed=2, spread=3.0)
-        for o in (op, by):
-            y, _, q, s = o.forward(xv, rv)
-            size = 128 if out8 == "group" else H
-            G = -(-H // size)
-            z = torch.zeros(n, G * size, dtype=torch.float64, device="cuda")
-            z[:, :H] = y
-            # (64 bits hold more than twice 24 and two: rounded to 32 they are the quotient rounded once.)
-            want = (z.view(n, G, size).abs().amax(2) / 448).float().clamp(min=2.0 ** -126)
-            assert torch.equal(s, want)
-            v = (y.double() / s.double().repeat_interleave(size, 1)[:, :H]).float()
-            assert torch.equal(q.view(torch.uint8), v.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+def test_scales_and_codes(lib, x, r, w, out8, n, H):
+    """The scale is the quotient max |y| / 448 of y as the fp32 output shows it.  Codes are those of h (w + offset) against its
+    largest in 64 bits: of 16-bit h and weights all of them, whose products are exact (rows of 16 bits have many quotients at the
+    borders of E4M3); else those of a number within 2^-22 (two rounded products, the quotient's rounding and this test's, 2^-24
+    each).  Where weights are so small that products are subnormal (off by 2^-150, scales at least 2^-126), 2^-23 besides; and
+    where the scale is the smallest there is, the row's root counts (REL)."""
+    for wv in (weights(H, w), torch.ones(H, device="cuda", dtype=w)):
+        for f in (0, -80, -117, -118, -119, -120, -121, -133):
+            wf = (wv.float() * 2.0 ** f).to(w)
+            if f < 0 and w == HF:
+                continue
+            for out in (F32, None):
+                op = MoeNorm(wf, eps=0.0, out_dtype=out, out8=out8)
+                xv, rv = rows(n, H, x, seed=H), None if r is None else rows(n, H, r, seed=2, spread=3.0)
+                y, h, q, s = op.forward(xv, rv)
+                h = xv if h is None else h
+                size = 128 if out8 == "group" else H
+                G = -(-H // size)
+                if out is not None:
+                    z = torch.zeros(n, G * size, dtype=torch.float64, device="cuda")
+                    z[:, :H] = y
+                    # (64 bits hold more than twice 24 and two: rounded to 32 they are the quotient rounded once.)
+                    want = (z.view(n, G, size).abs().amax(2) / 448).float().clamp(min=2.0 ** -126)
+                    assert torch.equal(s, want)
+                z = torch.zeros(n, G * size, dtype=torch.float64, device="cuda")
+                z[:, :H] = h.double() * wf.double()
+                z = z / torch.sqrt(h.double().square().mean(1, keepdim=True))
+                z = z.view(n, G, size)
+                v = (z / (z.abs().amax(2, keepdim=True) / 448).clamp(min=2.0 ** -126)).reshape(n, -1)[:, :H]
+                if h.dtype != F32 and w != F32 and f == 0:
+                    assert torch.equal(q.double(), e4m3(v))
+                else:
+                    slack, least = (2.0 ** -22, 0.0) if f > -100 else (REL, 2.0 ** -23)
+                    qa = q.double().abs()
+                    assert bool((e4m3((v.abs() * (1 - slack) - least).clamp(min=0)) <= qa).all())
+                    assert bool((qa <= e4m3(v.abs() * (1 + slack) + least)).all()) and bool((q.double() * v >= 0).all())
 
 
 @gpu
