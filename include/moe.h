@@ -535,7 +535,9 @@ size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows);
  *               where those of out did, some of it is
  * base and out are aligned to their element.  fp32 sums; A_e x[t] enters the
  * second product in 16 bits of precision for outputs of 16 bits, in 24 for
- * fp32 outputs; one rounding to out_type, after the addition of base.
+ * fp32 outputs; one rounding to out_type, after the addition of base.  (As a
+ * sum of 16-bit parts, of which some are 0 or of the other sign: an infinity
+ * in b may come out as NaN where the formula has an infinity.)
  * x, base and out may also be pinned host memory; n == 0 is a no-op.
  * Errors: MOE_ERR_NULL, MOE_ERR_INVALID_CONFIG, MOE_ERR_UNSUPPORTED (a rank
  * over 128, more than 1024 adapters, 2^20 in_features or 2^28 out_features),
@@ -550,7 +552,7 @@ moe_status_t moe_lora(const moe_lora_config_t* cfg, const void* a, const void* b
  * before the first call; of any number of calls, on any streams), where it stays
  * until moe_workspace_check(errors, 256, ...) reads and clears it.  Calls whose
  * workspace is above 256 bytes do not write out while it is there (the others
- * have no such waits). */
+ * have no such waits); what is no such code there is not looked at. */
 moe_status_t moe_lora_checked(const moe_lora_config_t* cfg, const void* a, const void* b, const float* scale, const void* x,
                               int64_t x_stride, const int32_t* idx, int32_t n, const void* base, int64_t base_stride, void* out,
                               int64_t out_stride, void* ws, size_t ws_bytes, void* errors, moe_stream_t stream);

@@ -243,6 +243,7 @@ constexpr int kLoraTile = 128;
 // GPU of fewer SMs blocks wait for their turn.)
 constexpr int kLoraBlocks = 304;
 constexpr int kLoraMaxSplits = 8;
+constexpr int kLoraErrFirst = 31, kLoraErrLast = 37;   // codes of the bounded waits (anything else is memory not cleared yet)
 inline int64_t lora_part_rows(int64_t n) {   // of splits * n, and of every smaller n's
     return std::min<int64_t>(kLoraMaxSplits * n, (int64_t)kLoraBlocks * kLoraTile + 2 * n);
 }

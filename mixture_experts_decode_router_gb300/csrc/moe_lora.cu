@@ -425,7 +425,7 @@ lora_sort_kernel(const int32_t* __restrict__ idx, int n, int L, int tile, int32_
     __syncthreads();
     pdl_wait();
     pdl_trigger();   // (the next kernel's launch overlaps this one; it waits for its end)
-    const bool stop = tid == 0 && pending && *pending != 0;
+    const bool stop = tid == 0 && pending && *pending >= kLoraErrFirst && *pending <= kLoraErrLast;
     const int per = (int)(((int64_t)n + kSortThreads - 1) / kSortThreads) * 32;
     const int64_t begin = (int64_t)warp * per, end = min((int64_t)n, begin + per);
     int ev[kBatch];

@@ -373,7 +373,7 @@ class MoeLora:
         """Reads and clears the word that a wait that gave up leaves its code in (31 to 37; syncs the stream)."""
         s, v = B.moe_workspace_check(self._held[3], 256, stream)
         B.check(s)
-        return v
+        return v if 31 <= v <= 37 else 0            # (made within a capture, the word is cleared by the first replay)
 
     def forward(self, x: torch.Tensor, idx: torch.Tensor, base: Optional[torch.Tensor] = None, out=None, stream=None):
         return self._lora(addressof(self.c_cfg), self._held, self._device, x, idx, base, out,

@@ -59,6 +59,9 @@ def test_nothing_is_written_while_an_error_is_pending(lib, y, O, r):
     assert torch.equal(keep, base)
     assert op.device_error() == 33 and op.device_error() == 0
     assert torch.equal(op.forward(x, idx, base), want)
+    # What is no code of these waits says nothing (a holder that was made within a capture, before its first replay).
+    errors[8:12] = 255
+    assert torch.equal(op.forward(x, idx, base), want) and op.device_error() == 0
     # A workspace's own word is the last call's.
     c, need = op.c_cfg, B.moe_lora_workspace_bytes(op.c_cfg, n)
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
@@ -352,3 +355,20 @@ def test_rows_past_32_bit_offsets(lib, O):
     base.copy_(rows(n, O, seed=8))
     op.forward(x, idx, base, out=y)
     check(op, x.contiguous(), idx, base.contiguous(), y.contiguous())
+
+
+def test_made_within_a_capture(lib):
+    n = 1500
+    a, b, s = adapters(5, 16, 256, WIDE)
+    x, idx, base = rows(n, 256), choose(n, 5), rows(n, WIDE, seed=8)
+    want = holder(n, a, b, s).forward(x, idx, base)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        op = holder(n, a, b, s)
+        held = op.forward(x, idx, base)
+    assert torch.equal(op.forward(x, idx, base), want)      # before the word was ever cleared
+    for _ in range(2):
+        held.fill_(7)
+        g.replay()
+        assert torch.equal(held, want) and op.device_error() == 0
