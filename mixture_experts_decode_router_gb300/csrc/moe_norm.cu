@@ -231,13 +231,15 @@ struct Factor {
     float2 hi, lo;
     __device__ __forceinline__ Factor(float top, float m) {      // top: max |t|
         const float v = top * m, q = v * (1.f / 448.f), s = fmaf(fmaf(q, -448.f, v), 1.f / 448.f, q);
-        scale = v < INFINITY ? fmaxf(s, 0x1p-126f) : v;
+        const bool finite = v < INFINITY;        // (of y: top may still be)
+        scale = finite ? fmaxf(s, 0x1p-126f) : v;
+        top = finite ? top : v;
         float up = 1.f, r;
         if (scale < 0x1p-100f) up = 0x1p64f;     // (what r is taken of stays above fp32's smallest)
         top *= up;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(top * (1.f / 448.f)));
         float rest = fmaf(-top, r, 448.f) * (1.f / 448.f) * r;
-        if (!(top < INFINITY)) rest = 0.f;       // (a number by an infinity is 0)
+        if (!finite) rest = 0.f;                 // (a number by an infinity is 0)
         r *= up;
         rest *= up;
         if (scale == 0x1p-126f) r = m * 0x1p126f, rest = 0.f;      // the smallest scale there is: y 2^126
@@ -418,9 +420,9 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, bool 
     }
 }
 
-// kX: type of x.  kR: type of the residual, or -1 for none.  kCodes: out8's scales.  (Kernels of their own: with all three
-// in one, 2048 x 7168 without codes took 16.1 us that take 14.6 so, 8192 x 7168 in groups 71.6 that take 68.1.)  kWide: rows so long that their threads have
-// no registers for loads in flight.
+// kX: type of x.  kR: type of the residual, or -1 for none.  kWide: rows so long that their threads have
+// no registers for loads in flight.  kCodes: out8's scales.  (Kernels of their own: with all three in one, 2048 x 7168
+// without codes took 16.1 us that take 14.6 so, 8192 x 7168 in groups 71.6 that take 68.1.)
 template <int kX, int kR, int kCh, bool kWide, bool kAny, int kCodes>
 __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads, kWide || kR == MOE_F32 ? 1 : 2) norm_kernel(const NormParams p) {
     __shared__ float red[4 * 32];

@@ -350,6 +350,24 @@ def test_scales_and_codes(lib, x, r, w, out8, n, H):
 
 
 @gpu
+@pytest.mark.parametrize("out8", ["group", "row"])
+@pytest.mark.parametrize("big", [1.5, 3.0, -1.5])
+@pytest.mark.parametrize("out", [F32, None])
+def test_results_past_fp32(lib, out8, big, out):
+    """An element that the weight takes past fp32 makes its group's scale an infinity, and every value that it stands for NaN."""
+    x = torch.ones(3, 300, device="cuda")
+    x[1, 5] = big
+    w = torch.full((300,), 3e38, device="cuda")
+    y, _, q, s = MoeNorm(w, eps=0.0, out_dtype=out, out8=out8).forward(x)
+    if out is not None:
+        assert y[1, 5].item() == float("inf") * big and int(y.isinf().sum()) == 1
+    stands = q.float() * (s.repeat_interleave(128, 1)[:, :300] if out8 == "group" else s)
+    last = 128 if out8 == "group" else 300
+    assert s[1, 0].item() == float("inf") and bool(stands[1, :last].isnan().all())
+    assert bool(stands[1, last:].isfinite().all()) and bool(stands[[0, 2]].isfinite().all())
+
+
+@gpu
 def test_as_many_rows_as_there_can_be(lib):
     """2^31 - 1 rows: the blocks that take eight rows each are still counted right."""
     n = (1 << 31) - 1
