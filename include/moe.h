@@ -468,8 +468,9 @@ typedef struct {
  *   y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset)      (fp32)
  *   residual_out = h;  out = y, rounded to out_type;
  *   scale8[g] = max(max |y| / 448, 2^-126) over the group g;  out8 = E4M3(y / scale8[g])
- *   (scale8 from y as an fp32 out holds it; codes, to nearest even, from h (weight + weight_offset) and its largest,
- *   which the root does not enter: of 16-bit h and weights as exact arithmetic has them)
+ *   (scale8 from y as an fp32 out holds it; codes, to nearest even, from
+ *   h (weight + weight_offset) and its largest, which the root does not enter: of
+ *   16-bit h and weights, weight_offset 0, as exact arithmetic has them)
  *   x, residual     device [n, H]; residual may be NULL
  *   weight          device [H], or NULL (1)
  *   residual_out    device [n, H] (out), or NULL; may be residual itself
@@ -531,8 +532,8 @@ size_t moe_lora_workspace_bytes(const moe_lora_config_t* cfg, int32_t max_rows);
  *               argument has any; it need not be cleared,
  *               and keeps nothing between calls but the error word of the last,
  *               for moe_workspace_check (256 bytes: it is not used, and may be
- *               any address).  Where the products of v gave up, out is not written;
- *               where those of out did, some of it is
+ *               any address).  Where a wait of the product with A gave up, out
+ *               is not written; of the one with B, some of it is
  * base and out are aligned to their element.  fp32 sums; A_e x[t] enters the
  * second product in 16 bits of precision for outputs of 16 bits, in 24 for
  * fp32 outputs; one rounding to out_type, after the addition of base.  (As a
